@@ -6,8 +6,9 @@ persistent TMA + tcgen05 attention kernel that walks those lists.  This package
 is the Python face of that C ABI: ``bsattn_build_meta``, ``bsattn_fwd``,
 ``bsattn_bwd`` and the rest carry the C names and only marshal arguments;
 ``alloc_meta``, ``build_meta``, ``forward`` and ``backward`` add torch
-allocation of the outputs around them.  PyTorch provides
-device memory and streams only.
+allocation of the outputs around them, and so do, for serving, ``alloc_kv_cache``,
+``kv_append``, ``kv_read``, ``decode`` and ``decode_shared_prefix`` (kv_cache.py).
+PyTorch provides device memory and streams only.
 """
 from __future__ import annotations
 
@@ -16,17 +17,26 @@ from typing import Optional
 
 from ._binding import (BSATTN_ERR_CAPACITY, BSATTN_ERR_CUDA, BSATTN_ERR_INVALID_ARG,
                        BSATTN_ERR_UNSUPPORTED, BSATTN_OK, BSATTN_STATIC_SCRATCH_UNITS, FLAG_BAD_COUNT, FLAG_BAD_INDEX, FLAG_BAD_SEQLENS, FLAG_TIMEOUT,
+                       KV_E4M3, KV_INT8,
                        MASK_CAUSAL, MASK_DOCUMENT, MASK_NONE, MASK_PREFIX, MASK_SLIDING_WINDOW,
                        OUT_BF16, OUT_F32,
+                       bsattn_decode, bsattn_decode_shared_prefix, bsattn_decode_workspace_size,
+                       bsattn_kv_append, bsattn_kv_cache, bsattn_kv_read,
                        BsattnError, MaskParams, Meta, bsattn_abi_version, bsattn_build_meta,
                        bsattn_build_meta_bitmask, bsattn_build_meta_blocks, bsattn_build_meta_bsr,
                        bsattn_fwd_proxy, bsattn_kv_summaries, bsattn_bwd, bsattn_bwd_workspace_size,
                        bsattn_fwd, bsattn_fwd_static_scratch, bsattn_fwd_workspace_size,
                        bsattn_testing_set_wait_limit, library, status_string)
 
+from .kv_cache import (KVCache, alloc_decode_workspace, alloc_kv_cache, decode, decode_shared_prefix,
+                       kv_append, kv_read)
+
 TILE = 128
 
-__all__ = ["bsattn_bwd", "bsattn_bwd_workspace_size", "backward", "bsattn_fwd_proxy", "bsattn_kv_summaries", "bsattn_build_meta", "bsattn_build_meta_bitmask", "bsattn_build_meta_blocks", "bsattn_build_meta_bsr", "bsattn_fwd", "bsattn_fwd_static_scratch", "bsattn_fwd_workspace_size", "bsattn_abi_version", "bsattn_testing_set_wait_limit",
+__all__ = ["KVCache", "alloc_kv_cache", "alloc_decode_workspace", "kv_append", "kv_read", "decode",
+           "decode_shared_prefix", "bsattn_kv_append", "bsattn_kv_read", "bsattn_decode",
+           "bsattn_decode_shared_prefix", "bsattn_decode_workspace_size", "bsattn_kv_cache", "KV_E4M3", "KV_INT8",
+           "bsattn_bwd", "bsattn_bwd_workspace_size", "backward", "bsattn_fwd_proxy", "bsattn_kv_summaries", "bsattn_build_meta", "bsattn_build_meta_bitmask", "bsattn_build_meta_blocks", "bsattn_build_meta_bsr", "bsattn_fwd", "bsattn_fwd_static_scratch", "bsattn_fwd_workspace_size", "bsattn_abi_version", "bsattn_testing_set_wait_limit",
            "alloc_meta", "alloc_workspace", "build_meta",
            "forward", "block_sparse_attention", "Meta", "MaskParams", "BsattnError", "status_string", "library", "TILE",
            "OUT_BF16", "OUT_F32", "MASK_NONE", "MASK_CAUSAL", "MASK_SLIDING_WINDOW", "MASK_DOCUMENT", "MASK_PREFIX",

@@ -18,6 +18,7 @@ BSATTN_ERR_CAPACITY = 4
 BSATTN_STATIC_SCRATCH_UNITS = 65536
 MASK_NONE, MASK_CAUSAL, MASK_SLIDING_WINDOW, MASK_DOCUMENT, MASK_PREFIX = 0, 1, 2, 3, 4
 OUT_BF16, OUT_F32 = 0, 1
+KV_E4M3, KV_INT8 = 0, 1
 FLAG_BAD_COUNT, FLAG_BAD_INDEX, FLAG_TIMEOUT, FLAG_BAD_SEQLENS = 0x1, 0x2, 0x4, 0x8
 
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -37,6 +38,13 @@ class bsattn_meta(ctypes.Structure):
                 ("num_m", ctypes.c_int32), ("num_n", ctypes.c_int32),
                 ("total_m_blocks", ctypes.c_int32), ("total_n_blocks", ctypes.c_int32),
                 ("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32)]
+
+
+class bsattn_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class BsattnError(RuntimeError):
@@ -108,6 +116,21 @@ def library() -> ctypes.CDLL:
         lib.bsattn_bwd_workspace_size.argtypes = [ctypes.POINTER(bsattn_meta),
                                                   ctypes.POINTER(ctypes.c_size_t)]
         lib.bsattn_bwd_workspace_size.restype = ctypes.c_int
+        vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        cache = ctypes.POINTER(bsattn_kv_cache)
+        lib.bsattn_kv_append.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp, i32, i32, vp, cache, vp, vp]
+        lib.bsattn_kv_append.restype = ctypes.c_int
+        lib.bsattn_kv_read.argtypes = [cache, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp]
+        lib.bsattn_kv_read.restype = ctypes.c_int
+        lib.bsattn_decode.argtypes = [vp, i64, i32, i32, cache, vp, i32, i32, vp,
+                                      ctypes.POINTER(bsattn_meta), vp, ctypes.c_float, vp,
+                                      ctypes.c_int, vp, vp, ctypes.c_size_t, vp, vp]
+        lib.bsattn_decode.restype = ctypes.c_int
+        lib.bsattn_decode_shared_prefix.argtypes = lib.bsattn_decode.argtypes[:5] + [vp, i32] + \
+            lib.bsattn_decode.argtypes[5:]
+        lib.bsattn_decode_shared_prefix.restype = ctypes.c_int
+        lib.bsattn_decode_workspace_size.argtypes = [cache, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+        lib.bsattn_decode_workspace_size.restype = ctypes.c_int
         lib.bsattn_status_string.argtypes = [ctypes.c_int]
         lib.bsattn_status_string.restype = ctypes.c_char_p
         lib.bsattn_abi_version.argtypes = []
@@ -323,6 +346,62 @@ def bsattn_bwd_workspace_size(meta: Meta) -> int:
     st = library().bsattn_bwd_workspace_size(ctypes.byref(mt), ctypes.byref(n))
     if st != BSATTN_OK:
         raise BsattnError(st, "bsattn_bwd_workspace_size")
+    return int(n.value)
+
+
+def bsattn_kv_append(k, v, k_stride: int, v_stride: int, total: int, B: int, cu_seqlens, page_table,
+                     table_stride: int, table_cols: int, seqlens, cache: bsattn_kv_cache,
+                     err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    return library().bsattn_kv_append(_ptr(k), _ptr(v), k_stride, v_stride, total, B, _ptr(cu_seqlens),
+                                      _ptr(page_table), table_stride, table_cols, _ptr(seqlens), cache,
+                                      _ptr(err_flag), _stream(stream))
+
+
+def bsattn_kv_read(cache: bsattn_kv_cache, page_table, table_stride: int, table_cols: int, B: int,
+                   cu_seqlens, total: int, k, v, err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    return library().bsattn_kv_read(cache, _ptr(page_table), table_stride, table_cols, B,
+                                    _ptr(cu_seqlens), total, _ptr(k), _ptr(v), _ptr(err_flag),
+                                    _stream(stream))
+
+
+def bsattn_decode(q, q_stride: int, B: int, Hq: int, cache: bsattn_kv_cache, page_table,
+                  table_stride: int, table_cols: int, seqlens, meta: Optional[Meta], kv_valid_len,
+                  softmax_scale: float, out, out_dtype: int, lse, workspace, workspace_bytes: int = 0,
+                  err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    mt = meta.to_c() if meta is not None else None
+    if workspace is not None and not isinstance(workspace, int) and workspace_bytes == 0:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return library().bsattn_decode(
+        _ptr(q), q_stride, B, Hq, cache, _ptr(page_table), table_stride, table_cols, _ptr(seqlens),
+        ctypes.byref(mt) if mt is not None else None, _ptr(kv_valid_len), softmax_scale, _ptr(out),
+        out_dtype, _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(err_flag), _stream(stream))
+
+
+def bsattn_decode_shared_prefix(q, q_stride: int, B: int, Hq: int, cache: bsattn_kv_cache,
+                                prefix_table, prefix_len: int, page_table, table_stride: int,
+                                table_cols: int, seqlens, meta: Optional[Meta], kv_valid_len,
+                                softmax_scale: float, out, out_dtype: int, lse, workspace,
+                                workspace_bytes: int = 0, err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    mt = meta.to_c() if meta is not None else None
+    if workspace is not None and not isinstance(workspace, int) and workspace_bytes == 0:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return library().bsattn_decode_shared_prefix(
+        _ptr(q), q_stride, B, Hq, cache, _ptr(prefix_table), prefix_len, _ptr(page_table), table_stride,
+        table_cols, _ptr(seqlens), ctypes.byref(mt) if mt is not None else None, _ptr(kv_valid_len),
+        softmax_scale, _ptr(out), out_dtype, _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(err_flag),
+        _stream(stream))
+
+
+def bsattn_decode_workspace_size(cache: bsattn_kv_cache, B: int, Hq: int, prefix_len: int = 0) -> int:
+    """Bytes of workspace a decode call with these sizes needs."""
+    n = ctypes.c_size_t(0)
+    st = library().bsattn_decode_workspace_size(cache, B, Hq, prefix_len, ctypes.byref(n))
+    if st != BSATTN_OK:
+        raise BsattnError(st, "bsattn_decode_workspace_size")
     return int(n.value)
 
 

@@ -329,6 +329,13 @@ BwdLayout bwd_layout(const bsattn_meta *m) {
 
 }  // namespace
 
+namespace bsattn {
+
+bsattn_status check_meta_desc(const bsattn_meta *m) { return check_meta(m); }
+int current_device_sms() { return num_sms_current_device(); }
+
+}  // namespace bsattn
+
 extern "C" {
 
 const char *bsattn_status_string(bsattn_status s) {

@@ -126,6 +126,69 @@ struct BwdParams {
 cudaError_t launch_bwd(const BwdParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                        const CUtensorMap &tv, const CUtensorMap &tdo, cudaStream_t stream);
 
+// A paged 8-bit K/V cache as the kernels see it (bsattn_kv_cache, checked).
+struct CacheView {
+    uint8_t *k, *v;                // [num_pages, H, page_size, D] codes
+    float *ks, *vs;                // [num_pages, H, page_size] scales
+    int num_pages, page_shift;     // page_size = 1 << page_shift
+    int H, D;
+    int int8;                      // codes: 1 int8, 0 e4m3
+};
+
+struct AppendParams {
+    CacheView c;
+    const uint16_t *k, *v;         // bf16 rows
+    long long k_stride, v_stride;  // elements between tokens
+    int total, B;
+    const int32_t *cu;             // [B + 1], or null: one token per sequence
+    const int32_t *table;
+    int table_stride, table_cols;
+    const int32_t *seqlens;
+    int32_t *err;
+};
+
+struct ReadParams {
+    CacheView c;
+    const int32_t *table;
+    int table_stride, table_cols;
+    int total, B;
+    const int32_t *cu;
+    uint16_t *k, *v;               // bf16 [total, H, D]
+    int32_t *err;
+};
+
+// One query token per sequence over the cache, optionally behind a shared prefix.
+struct DecodeParams {
+    CacheView c;
+    const uint16_t *q;             // bf16 [B, Hq, D], q_stride elements between rows
+    long long q_stride;
+    int B, Hq, G;                  // G = Hq / H query heads per KV head
+    const int32_t *table;
+    int table_stride, table_cols;
+    const int32_t *seqlens;
+    const int32_t *prefix_table;
+    int prefix_len;
+    // lists over 128-key tiles (has_lists), one query row per sequence
+    int has_lists, lists_varlen, list_n, total_n;
+    const int32_t *full_cnt, *full_idx, *mask_cnt, *mask_idx, *cu_off;
+    const int32_t *vl;             // [B, list_n] or null (mask list only)
+    float scale_log2;              // softmax_scale * log2(e)
+    void *out;
+    int out_f32;
+    float *lse;
+    int32_t *err;
+    uint8_t *ws;
+};
+
+cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_read(const ReadParams &p, cudaStream_t stream);
+cudaError_t launch_decode(const DecodeParams &p, cudaStream_t stream);
+size_t decode_workspace_bytes(int B, int H, int G, int D, int prefix_len);
+
+// Shared with the other entry points (bsattn_api.cu).
+bsattn_status check_meta_desc(const bsattn_meta *m);
+int current_device_sms();          // 0 on failure
+
 cudaError_t launch_meta(const MetaParams &p, cudaStream_t stream);
 cudaError_t launch_kv_summary(const void *k, const void *v, int B, int S, int H, int D, void *k_sum,
                               void *v_sum, cudaStream_t stream);

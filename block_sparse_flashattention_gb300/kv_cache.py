@@ -1,0 +1,298 @@
+"""The paged 8-bit K/V cache and the attention of single query tokens over it.
+
+``kv_append`` quantises new K and V rows into a cache's pages, ``kv_read`` reads
+them back as packed bf16 rows (what ``forward`` takes, for a prefill that follows
+cached context), ``decode`` attends one query token per sequence over them, and
+``decode_shared_prefix`` does so for a batch behind one common prefix.  These are
+calls of the C functions of the same names (bsattn_*, include/bsattn.h, where the
+formats and faults are described) with torch checks and allocations around them.
+
+    cache = bsa.alloc_kv_cache(num_pages, H, D)                 # e4m3, pages of 128
+    bsa.kv_append(k, v, cache, page_table, seqlens)             # k, v [B, H, D]: a token each
+    out, lse = bsa.decode(q, cache, page_table, seqlens)        # q [B, Hq, D]
+
+Work is queued on ``stream`` (the current stream of the cache's device when None);
+outputs and workspaces that a call allocates belong to that stream.  Device faults
+(a page outside the cache, lengths that do not fit) set FLAG_* bits in ``err_flag``.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from ._binding import (BSATTN_OK, KV_E4M3, KV_INT8, OUT_BF16, OUT_F32, BsattnError, bsattn_decode,
+                       bsattn_decode_shared_prefix, bsattn_decode_workspace_size, bsattn_kv_append,
+                       bsattn_kv_cache, bsattn_kv_read)
+
+
+def _check(status: int, where: str) -> None:
+    if status != BSATTN_OK:
+        raise BsattnError(status, where)
+
+
+class KVCache:
+    """A paged cache over caller-owned tensors (kept, not copied).
+
+    k, v: torch.float8_e4m3fn or torch.int8 [num_pages, H, page_size, D];
+    k_scale, v_scale: float32 [num_pages, H, page_size]; contiguous, one device."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "H", "page_size", "D", "dtype", "device", "c", "ref")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dtype not in (torch.float8_e4m3fn, torch.int8) or v.dtype != k.dtype:
+            raise ValueError("k and v must both be torch.float8_e4m3fn or torch.int8")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise ValueError("k_scale and v_scale must be torch.float32")
+        if k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+            raise ValueError("k, v must be [num_pages, H, page_size, D] and the scales [num_pages, H, page_size]")
+        for t in (k, v, k_scale, v_scale):
+            if t.device != k.device:
+                raise ValueError("the cache's tensors must be on one device")
+            if not t.is_contiguous():
+                raise ValueError("the cache's tensors must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.H, self.page_size, self.D = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        self.c = bsattn_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                 self.num_pages, self.page_size, self.H, self.D,
+                                 KV_INT8 if k.dtype == torch.int8 else KV_E4M3)
+        self.ref = ctypes.pointer(self.c)
+
+
+def alloc_kv_cache(num_pages: int, H: int, D: int, *, page_size: int = 128, dtype=None, device="cuda") -> KVCache:
+    """A cache of num_pages pages, zero-filled; dtype torch.float8_e4m3fn (default) or torch.int8."""
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    if dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise ValueError("dtype must be torch.float8_e4m3fn or torch.int8")
+    codes = [torch.zeros((num_pages, H, page_size, D), dtype=torch.uint8, device=device).view(dtype) for _ in range(2)]
+    scales = [torch.zeros((num_pages, H, page_size), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(codes[0], codes[1], scales[0], scales[1])
+
+
+class _On:
+    """Makes the cache's device current, and `stream`, if one is given, the current
+    stream, for the allocations and launches inside; costs nothing when both are."""
+
+    __slots__ = ("stack",)
+
+    def __init__(self, device, stream):
+        import contextlib
+
+        import torch
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.stack.enter_context(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.stack.close()
+
+
+def _elsewhere(cache, stream) -> bool:
+    """Whether a call needs _On: another stream than the current one, or another device."""
+    import torch
+    return cache.device.type == "cuda" and (stream is not None or cache.device.index != torch.cuda.current_device())
+
+
+def _ints(t, name, dim, device):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != dim or t.device != device:
+        raise ValueError(f"{name} must be a {dim}-D torch.int32 tensor on the cache's device")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _err(t, device):
+    if t is not None:
+        _ints(t, "err_flag", 1, device)
+        if t.numel() < 1:
+            raise ValueError("err_flag must hold one element")
+
+
+def _table(t, name, B, device):
+    """(row stride, columns) of a page table of B rows."""
+    _ints(t, name, 2, device)
+    rows, cols = t.shape
+    if rows != B:
+        raise ValueError(f"{name} must have one row per sequence")
+    stride = t.stride(0) if rows > 1 else cols
+    if stride < cols:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return stride, cols
+
+
+def _rows(t, name, H, D, device):
+    """Elements from token to token of bf16 rows [tokens, H, D] whose [H, D] part is contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or t.device != device:
+        raise ValueError(f"{name} must be a torch.bfloat16 tensor [tokens, {H}, {D}] on the cache's device")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
+        raise ValueError(f"{name}'s heads and elements must be contiguous")
+    return s0 if t.shape[0] > 1 else H * D
+
+
+def kv_append(k, v, cache: KVCache, page_table, seqlens, *, cu_seqlens=None, err_flag=None, stream=None) -> KVCache:
+    """Quantises k, v (bf16 [total, H, D]; tokens may be any multiple of 8 elements
+    apart) into the cache and returns it.
+
+    cu_seqlens None: one new token per sequence; else int32 [B+1], the rows of each
+    sequence's new tokens.  seqlens int32 [B]: the lengths after the append (0: a
+    padding row); page_table int32 [B, pages]."""
+    if _elsewhere(cache, stream):
+        with _On(cache.device, stream):
+            return kv_append(k, v, cache, page_table, seqlens, cu_seqlens=cu_seqlens, err_flag=err_flag)
+    dev, B = cache.device, page_table.shape[0]
+    ks, vs = _rows(k, "k", cache.H, cache.D, dev), _rows(v, "v", cache.H, cache.D, dev)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must hold the same tokens")
+    stride, cols = _table(page_table, "page_table", B, dev)
+    _ints(seqlens, "seqlens", 1, dev)
+    if seqlens.shape[0] != B:
+        raise ValueError("seqlens must have one entry per sequence")
+    if cu_seqlens is not None:
+        _ints(cu_seqlens, "cu_seqlens", 1, dev)
+        if cu_seqlens.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must have B + 1 entries")
+    _err(err_flag, dev)
+    _check(bsattn_kv_append(k, v, ks, vs, k.shape[0], B, cu_seqlens, page_table, stride, cols, seqlens,
+                            cache.ref, err_flag, None), "bsattn_kv_append")
+    return cache
+
+
+def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=None, err_flag=None, stream=None):
+    """The cached rows of every sequence, packed: (k, v) bf16 [total, H, D], sequence
+    b's positions 0, 1, ... in rows cu_seqlens[b] .. cu_seqlens[b+1] (int32 [B+1]).
+
+    total: rows to allocate when k and v are not given (cu_seqlens[-1], which lives on
+    the device); rows outside every sequence are not written."""
+    import torch
+    if _elsewhere(cache, stream):
+        with _On(cache.device, stream):
+            return kv_read(cache, page_table, cu_seqlens, total=total, k=k, v=v, err_flag=err_flag)
+    dev, B = cache.device, page_table.shape[0]
+    stride, cols = _table(page_table, "page_table", B, dev)
+    _ints(cu_seqlens, "cu_seqlens", 1, dev)
+    if cu_seqlens.shape[0] != B + 1:
+        raise ValueError("cu_seqlens must have B + 1 entries")
+    _err(err_flag, dev)
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    if k is None:
+        if total is None:
+            raise ValueError("total is needed to allocate k and v")
+        k, v = (torch.empty((total, cache.H, cache.D), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    else:
+        for t, name in ((k, "k"), (v, "v")):
+            _rows(t, name, cache.H, cache.D, dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if v.shape[0] != k.shape[0] or (total is not None and total != k.shape[0]):
+            raise ValueError("k, v and total disagree")
+    _check(bsattn_kv_read(cache.ref, page_table, stride, cols, B, cu_seqlens, k.shape[0], k, v, err_flag, None),
+           "bsattn_kv_read")
+    return k, v
+
+
+def alloc_decode_workspace(cache: KVCache, B: int, Hq: int, *, prefix_len: int = 0):
+    """Workspace of a decode call for B sequences and Hq query heads (prefix_len as in
+    ``decode_shared_prefix``).  It can be kept from call to call; two calls that may
+    run at the same time need one each."""
+    import torch
+    return torch.empty(bsattn_decode_workspace_size(cache.ref, B, Hq, prefix_len), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
+            out_dtype, lse, workspace, err_flag):
+    import torch
+    dev = cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    B, Hq = q.shape[0], q.shape[1]
+    qs = _rows(q, "q", Hq, cache.D, dev)
+    stride, cols = _table(page_table, "page_table", B, dev) if page_table is not None else (0, 0)
+    _ints(seqlens, "seqlens", 1, dev)
+    if seqlens.shape[0] != B:
+        raise ValueError("seqlens must have one entry per sequence")
+    if kv_valid_len is not None:
+        if meta is None:
+            raise ValueError("kv_valid_len belongs to the listed tiles of meta")
+        _ints(kv_valid_len, "kv_valid_len", 2, dev)
+        if tuple(kv_valid_len.shape) != (B, meta.num_n) or not kv_valid_len.is_contiguous():
+            raise ValueError("kv_valid_len must be a contiguous [B, meta.num_n] tensor")
+    if prefix_table is not None:
+        _ints(prefix_table, "prefix_table", 1, dev)
+        if prefix_len < 0 or prefix_table.shape[0] * cache.page_size < prefix_len:
+            raise ValueError("prefix_table does not hold prefix_len tokens")
+    _err(err_flag, dev)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    if out is None:
+        out = torch.empty((B, Hq, cache.D), dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [B, Hq, D] tensor of out_dtype on the cache's device")
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or lse.device != dev or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [B, Hq] tensor on the cache's device")
+    if workspace is None:
+        workspace = alloc_decode_workspace(cache, B, Hq, prefix_len=prefix_len)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(cache.D)
+    od = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
+    if prefix_table is None:
+        _check(bsattn_decode(q, qs, B, Hq, cache.ref, page_table, stride, cols, seqlens, meta, kv_valid_len,
+                             softmax_scale, out, od, lse, workspace, 0, err_flag, None), "bsattn_decode")
+    else:
+        _check(bsattn_decode_shared_prefix(q, qs, B, Hq, cache.ref, prefix_table, prefix_len, page_table, stride,
+                                           cols, seqlens, meta, kv_valid_len, softmax_scale, out, od, lse,
+                                           workspace, 0, err_flag, None), "bsattn_decode_shared_prefix")
+    return out, lse
+
+
+def decode(q, cache: KVCache, page_table, seqlens, *, meta=None, kv_valid_len=None, softmax_scale=None, out=None,
+           out_dtype=None, lse=None, workspace=None, err_flag=None, stream=None):
+    """Attention of one query token per sequence, q bf16 [B, Hq, D] (Hq a multiple of
+    the cache's heads; tokens may be any multiple of 8 elements apart), over the
+    seqlens[b] cached keys of each sequence.
+
+    meta: lists of KV tiles to attend instead of all (a Meta with one query row per
+    sequence and H = cache.H: batched with num_m = 1, or varlen with total_m_blocks =
+    B); kv_valid_len int32 [B, meta.num_n] as for ``forward``.  Returns (out [B, Hq, D]
+    bf16 or out_dtype, lse fp32 [B, Hq]); a sequence without keys gets 0 and -inf.
+    workspace: see alloc_decode_workspace; None allocates one for this call."""
+    if _elsewhere(cache, stream):
+        with _On(cache.device, stream):
+            return _decode(q, cache, None, 0, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
+                           out_dtype, lse, workspace, err_flag)
+    return _decode(q, cache, None, 0, page_table, seqlens, meta, kv_valid_len, softmax_scale, out, out_dtype, lse,
+                   workspace, err_flag)
+
+
+def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_table, seqlens, *, meta=None,
+                         kv_valid_len=None, softmax_scale=None, out=None, out_dtype=None, lse=None, workspace=None,
+                         err_flag=None, stream=None):
+    """``decode`` for a batch whose sequences all begin with one prefix of prefix_len
+    cached tokens, in the pages prefix_table (int32 [pages]); page_table and seqlens
+    (and meta, kv_valid_len) describe what each sequence has after it.  page_table may
+    be None when no sequence has keys of its own.  The prefix is read once for all."""
+    if prefix_table is None:
+        raise ValueError("prefix_table is needed (decode attends sequences without a prefix)")
+    if _elsewhere(cache, stream):
+        with _On(cache.device, stream):
+            return _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len,
+                           softmax_scale, out, out_dtype, lse, workspace, err_flag)
+    return _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
+                   out_dtype, lse, workspace, err_flag)

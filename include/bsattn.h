@@ -1,7 +1,9 @@
 /*
  * bsattn -- block-sparse attention for NVIDIA GB300 (sm_103a): metadata from a
  * block map (byte map, bitmask, BSR or coarse blocks), the forward (exact, or
- * with proxy compensation), and the backward of the exact forward.
+ * with proxy compensation), and the backward of the exact forward; for serving, a
+ * paged 8-bit K/V cache (append, read back) and the attention of single query
+ * tokens over it, alone or behind a prefix that the batch shares.
  *
  * C ABI.  Every pointer argument is caller-owned memory; the library allocates
  * nothing and keeps no state between calls.  Device pointers must be CUDA
@@ -434,6 +436,155 @@ bsattn_status bsattn_bwd(const void *q, const void *k, const void *v, const void
  * tile and head); each of the nine regions rounded up to 256 bytes.
  */
 bsattn_status bsattn_bwd_workspace_size(const bsattn_meta *meta, size_t *bytes);
+
+/*
+ * Paged 8-bit K/V cache, for serving: the keys and values of a batch's sequences
+ * in pages of page_size tokens, one byte per element and one fp32 scale per row
+ * (token and head).  It is an engineering addition: the pages describe no cache.
+ *
+ *   k, v              device, [num_pages, H, page_size, D] bytes, 16-byte aligned
+ *   k_scale, v_scale  device fp32, [num_pages, H, page_size], 16-byte aligned
+ * Position p of sequence b is row p % page_size of page page_table[b][p / page_size].
+ * A row's value is code * scale.  A scale is what bsattn_kv_append writes, or any
+ * value >= 0 of the caller's; a NaN scale makes its row NaN.
+ * page_size in {16, 32, 64, 128}; D in {64, 128} (else BSATTN_ERR_UNSUPPORTED);
+ * num_pages * H * page_size < 2^31.
+ */
+typedef enum {
+    BSATTN_KV_E4M3 = 0, /* codes are e4m3 (4 exponent bits, 3 mantissa bits, largest 448) */
+    BSATTN_KV_INT8 = 1  /* codes are integers -127..127                                  */
+} bsattn_kv_dtype;
+
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int32_t num_pages, page_size, H, D;
+    int32_t dtype; /* bsattn_kv_dtype */
+} bsattn_kv_cache;
+
+/*
+ * bsattn_kv_append -- quantises the K and V rows of new tokens into the cache.
+ *
+ * Sequence b's new tokens are the packed rows cu_seqlens[b] .. cu_seqlens[b+1] of
+ * k and v; they become its positions seqlens[b] - n .. seqlens[b] - 1, where n is
+ * their number: seqlens holds the lengths after the append, as bsattn_decode takes
+ * them.  For a row x with largest magnitude a:
+ *   e4m3  scale = 2^max(-126, ceil(log2(a / 448))), code = x / scale rounded to
+ *         nearest even: the scale is a power of two, so x / scale is exact, and the
+ *         code carries the only rounding;
+ *   int8  a' = max(a, 127 * 2^-126), scale = a' / 127, code = rint(x * (127 / a')),
+ *         each operation rounded to fp32.
+ * A row that holds a NaN or an infinity gets the scale NaN and codes 0.
+ *
+ * k, v         device bf16, rows of [H, D] contiguous elements, k_stride / v_stride
+ *              elements from token to token (at least H * D and a multiple of 8, so
+ *              that the K or V part of a fused projection can be given as it is);
+ *              16-byte aligned.
+ * total        packed rows of k and v.
+ * cu_seqlens   device int32 [B+1], or NULL: one new token per sequence (total == B).
+ * page_table   device int32, B rows of table_cols entries, table_stride apart.
+ * seqlens      device int32 [B].  seqlens[b] <= 0: the sequence is padding, its rows
+ *              are not written.
+ * A page outside [0, num_pages): its rows are not written, BSATTN_FLAG_BAD_INDEX.
+ * A sequence whose offsets leave [0, total] or decrease, that has more new tokens
+ * than seqlens[b], or that outgrows its table row: none of its rows is written,
+ * BSATTN_FLAG_BAD_SEQLENS.  Two rows of one call must not have the same place in
+ * the cache (two sequences that share a page write to it): which of them a place
+ * then holds, and whether codes and scale come from the same one, is not defined.
+ * Everything else in the cache is left as it was.
+ */
+bsattn_status bsattn_kv_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                               int32_t total, int32_t B, const int32_t *cu_seqlens,
+                               const int32_t *page_table, int32_t table_stride, int32_t table_cols,
+                               const int32_t *seqlens, const bsattn_kv_cache *cache,
+                               int32_t *err_flag, void *stream);
+
+/*
+ * bsattn_kv_read -- reads cached K and V back as packed bf16 rows, the layout that
+ * bsattn_fwd takes: rows cu_seqlens[b] .. cu_seqlens[b+1] of k and v receive
+ * positions 0, 1, ... of sequence b, each element code * scale in fp32, rounded to
+ * bf16 (to nearest even).  Rows with a power-of-two scale, as e4m3 rows have, are
+ * read back exactly.
+ *
+ * k, v         device bf16 [total, H, D], contiguous, 16-byte aligned (written).
+ * total        rows of k and v; rows outside every sequence's range are left as
+ *              they were.
+ * A page outside [0, num_pages): its rows read as 0, BSATTN_FLAG_BAD_INDEX.  A
+ * sequence whose offsets leave [0, total] or decrease, or that is longer than its
+ * table row: none of its rows is written, BSATTN_FLAG_BAD_SEQLENS.
+ */
+bsattn_status bsattn_kv_read(const bsattn_kv_cache *cache, const int32_t *page_table,
+                             int32_t table_stride, int32_t table_cols, int32_t B,
+                             const int32_t *cu_seqlens, int32_t total, void *k, void *v,
+                             int32_t *err_flag, void *stream);
+
+/*
+ * bsattn_decode -- attention of one query token per sequence over a paged 8-bit
+ * cache.  For sequence b, query head hq and its KV head h = hq / (Hq / H):
+ *   s_j = softmax_scale * q . K_j over the keys j < seqlens[b], or, with meta, over
+ *   those keys of the listed KV tiles only,
+ *   lse = ln(sum_j exp(s_j)),  out = sum_j exp(s_j - lse) V_j;
+ * no key: out = 0, lse = -inf.  K_j, V_j are the cached values (code * scale); all
+ * sums are fp32, and exp(s_j) V_j's weights are rounded to fp16 (11 bits).
+ *
+ * q            device bf16, B rows of [Hq, D] contiguous elements, q_stride apart (at
+ *              least Hq * D, a multiple of 8); 16-byte aligned.
+ * Hq           query heads, a multiple of cache->H with Hq / H <= 128 (else
+ *              BSATTN_ERR_UNSUPPORTED).
+ * page_table, table_stride, table_cols   as for bsattn_kv_append.
+ * seqlens      device int32 [B]; <= 0: no key.  A length past table_cols * page_size
+ *              is cut there, BSATTN_FLAG_BAD_SEQLENS.
+ * meta         NULL: every key.  Else lists over 128-key tiles as bsattn_build_meta
+ *              writes them for one query row per sequence and H = cache->H: batched
+ *              with num_m = 1, or varlen with total_m_blocks = B and the sequences'
+ *              own lengths.  The tiles of both lists are attended (mask_mod has no
+ *              say here: it is for rows of a prefill); a tile is to be listed once.
+ *              A bad index or count is skipped or clamped and flagged as by
+ *              bsattn_fwd.
+ * kv_valid_len optional device int32 [B, meta->num_n], with meta: valid keys at the
+ *              start of each tile, applied to the tiles of the mask list.
+ * A page outside [0, num_pages): its keys are left out, BSATTN_FLAG_BAD_INDEX.
+ * out          device, [B, Hq, D] contiguous, 16-byte aligned, out_dtype.
+ * lse          device fp32 [B, Hq].
+ * workspace    device, 256-byte aligned, at least bsattn_decode_workspace_size bytes;
+ *              needs no zeroing and carries nothing from call to call.  Two calls
+ *              that may run concurrently must not share one.
+ */
+bsattn_status bsattn_decode(const void *q, int64_t q_stride, int32_t B, int32_t Hq,
+                            const bsattn_kv_cache *cache, const int32_t *page_table,
+                            int32_t table_stride, int32_t table_cols, const int32_t *seqlens,
+                            const bsattn_meta *meta, const int32_t *kv_valid_len,
+                            float softmax_scale, void *out, bsattn_out_dtype out_dtype, float *lse,
+                            void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * bsattn_decode_shared_prefix -- bsattn_decode for a batch whose sequences all begin
+ * with the same prefix: sequence b's keys are the prefix_len keys of the prefix, then
+ * the seqlens[b] keys of its own page-table row (which meta and kv_valid_len, if
+ * given, refer to; the prefix is attended whole).  The prefix's K and V are read once
+ * for all sequences.
+ *
+ * prefix_table device int32 [ceil(prefix_len / page_size)]: the prefix's pages.
+ * prefix_len   >= 0 (0: bsattn_decode).  table_cols may be 0: no sequence has keys of
+ *              its own (page_table may then be NULL).
+ * Other arguments as for bsattn_decode.
+ */
+bsattn_status bsattn_decode_shared_prefix(const void *q, int64_t q_stride, int32_t B, int32_t Hq,
+                                          const bsattn_kv_cache *cache, const int32_t *prefix_table,
+                                          int32_t prefix_len, const int32_t *page_table,
+                                          int32_t table_stride, int32_t table_cols,
+                                          const int32_t *seqlens, const bsattn_meta *meta,
+                                          const int32_t *kv_valid_len, float softmax_scale, void *out,
+                                          bsattn_out_dtype out_dtype, float *lse, void *workspace,
+                                          size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * bsattn_decode_workspace_size -- bytes of workspace that bsattn_decode (prefix_len =
+ * 0) or bsattn_decode_shared_prefix needs for B sequences, Hq query heads and a cache
+ * of this shape (its pointers are not looked at).
+ */
+bsattn_status bsattn_decode_workspace_size(const bsattn_kv_cache *cache, int32_t B, int32_t Hq,
+                                           int32_t prefix_len, size_t *bytes);
 
 /*
  * bsattn_testing_set_wait_limit -- testing hook, not for production use; the

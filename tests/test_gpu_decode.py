@@ -1,0 +1,415 @@
+"""decode and decode_shared_prefix against the oracle, at the sizes and masks where they
+can go wrong; tolerances as derived in kv_case.expect."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import block_sparse_flashattention_gb300 as bsa  # noqa: E402
+from oracle import kv_cache as okv  # noqa: E402
+from tests.kv_case import Pool, agree, bf16, expect, f64, lists, pages_for  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def _q(seed, B, Hq, D, size=1.5):
+    return bf16(size * np.random.default_rng(seed).standard_normal((B, Hq, D))).cuda()
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+DECODE = [
+    # dtype, H, G, D, page, lens
+    ("e4m3", 1, 1, 128, 128, [1]),
+    ("int8", 2, 1, 64, 16, [0, 1, 2, 15, 16, 17]),
+    ("e4m3", 3, 4, 128, 64, [127, 128, 129, 0, 640]),
+    ("int8", 2, 5, 128, 32, [300, 31, 33]),
+    ("e4m3", 2, 8, 64, 128, [257, 1000]),
+    ("int8", 1, 9, 128, 16, [513, 70]),
+    ("e4m3", 1, 16, 64, 64, [400]),
+    ("int8", 1, 17, 128, 128, [200, 3]),
+    ("e4m3", 2, 33, 64, 16, [150]),
+    ("int8", 1, 64, 128, 64, [260, 5]),
+    ("e4m3", 1, 128, 128, 128, [300]),
+    ("e4m3", 5, 2, 128, 128, [2500]),
+    ("int8", 4, 1, 64, 64, [5000, 1, 60]),
+    ("e4m3", 1, 1, 128, 16, [9000]),
+]
+
+
+@pytest.mark.parametrize("dtype,H,G,D,page,lens", DECODE)
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_decode(dtype, H, G, D, page, lens, out_dtype):
+    pool = Pool(11, pages_for(lens, page) + 1, H, D, page, dtype)
+    ht, table = pool.tables(lens)
+    q = _q(12, len(lens), H * G, D)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=out_dtype, err_flag=err)
+    assert int(err) == 0
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], range(lens[b]))], 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("kind", ["varlen", "batched"])
+@pytest.mark.parametrize("dtype,H,G,D,page,lens,mask_every,valid", [
+    ("e4m3", 2, 1, 128, 128, [1000, 130, 0, 128], 0, False),
+    ("int8", 3, 4, 64, 16, [700, 700, 1], 2, True),
+    ("e4m3", 1, 12, 128, 32, [1300, 257], 1, True),
+    ("int8", 2, 2, 128, 64, [5000, 4000], 3, False),
+])
+def test_decode_lists(kind, dtype, H, G, D, page, lens, mask_every, valid):
+    pool = Pool(13, pages_for(lens, page) + 1, H, D, page, dtype)
+    ht, table = pool.tables(lens)
+    rng = np.random.default_rng(14)
+    sel = {(b, h): sorted((int(t) for t in np.flatnonzero(rng.random(-(-n // 128)) < 0.6)), reverse=True)
+           for b, n in enumerate(lens) for h in range(H)}
+    sel[0, 0] = []                                                  # a head that attends nothing
+    meta = lists(H, lens, lambda b, h: sel[b, h], kind=kind, mask_every=mask_every)
+    vl = rng.integers(0, 129, (len(lens), meta.num_n)).astype(np.int32) if valid else None
+
+    def keys(b, h):
+        out = []
+        for i, t in enumerate(sel[b, h]):
+            lim = min(128, lens[b] - 128 * t)
+            if valid and mask_every and i % mask_every == 0:
+                lim = min(lim, int(vl[b, t]))
+            out += range(128 * t, 128 * t + max(lim, 0))
+        return [(ht[b], out)]
+    q = _q(15, len(lens), H * G, D)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), meta=meta, err_flag=err, out_dtype=torch.float32,
+                          kv_valid_len=torch.from_numpy(vl).cuda() if valid else None)
+    assert int(err) == 0
+    agree(out, lse, expect(pool, f64(q), G, keys, 1 / math.sqrt(D)))
+
+
+PREFIX = [
+    # dtype, H, G, D, page, prefix, lens
+    ("e4m3", 1, 1, 128, 128, 1, [1]),
+    ("int8", 2, 1, 64, 16, 17, [0, 5, 40]),
+    ("e4m3", 2, 4, 128, 64, 500, [1, 100, 0, 64]),
+    ("int8", 1, 8, 128, 32, 1000, [300, 20, 1, 0, 7]),
+    ("e4m3", 3, 2, 64, 128, 129, [3] * 20),
+    ("int8", 1, 16, 64, 16, 300, [10, 20, 30]),
+    ("e4m3", 2, 3, 128, 128, 700, [2] * 50),
+    ("int8", 1, 4, 128, 64, 257, [1, 2] * 40),
+    ("e4m3", 1, 20, 64, 128, 400, [5] * 9),
+    ("int8", 1, 100, 128, 128, 140, [20, 130]),
+    ("e4m3", 1, 8, 128, 128, 2000, [0] * 4),
+]
+
+
+@pytest.mark.parametrize("dtype,H,G,D,page,prefix,lens", PREFIX)
+def test_shared_prefix(dtype, H, G, D, page, prefix, lens):
+    pool = Pool(21, pages_for(lens + [prefix], page) + 1, H, D, page, dtype)
+    hp = pool.take(-(-prefix // page))
+    ht, table = pool.tables(lens)
+    q = _q(22, len(lens), H * G, D)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    scale = 0.7 / math.sqrt(D)
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), err_flag=err,
+                                        softmax_scale=scale, out_dtype=torch.float32)
+    assert int(err) == 0
+    ref = expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], range(lens[b]))], scale)
+    agree(out, lse, ref)
+    o16, l16 = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), softmax_scale=scale)
+    agree(o16, l16, ref)
+    if not any(lens):
+        o, l = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, None, _i32(lens), softmax_scale=scale,
+                                        out_dtype=torch.float32)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_prefix_equals_private_copies():
+    """A shared prefix gives what the same keys at the head of every sequence's own table give."""
+    H, G, D, page, prefix, lens = 2, 4, 128, 16, 160, [37, 1, 300]
+    pool = Pool(23, pages_for(lens + [prefix], page), H, D, page, "e4m3")
+    hp = pool.take(prefix // page)
+    ht, table = pool.tables(lens)
+    q = _q(24, 3, H * G, D)
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), out_dtype=torch.float32)
+    whole = torch.cat([_i32(hp)[None].expand(3, -1), table], 1).contiguous()
+    o2, l2 = bsa.decode(q, pool.cache, whole, _i32([prefix + n for n in lens]), out_dtype=torch.float32)
+    ref = expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], range(lens[b]))], 1 / math.sqrt(D))
+    agree(out, lse, ref)
+    agree(o2, l2, ref)
+
+
+def test_prefix_with_lists():
+    """Lists choose among a sequence's own tiles; the prefix is attended whole."""
+    H, G, D, page, prefix, lens = 2, 2, 64, 64, 200, [600, 0, 129]
+    pool = Pool(25, pages_for(lens + [prefix], page), H, D, page, "int8")
+    hp = pool.take(-(-prefix // page))
+    ht, table = pool.tables(lens)
+    q = _q(26, 3, H * G, D)
+    sel = lambda b, h: [t for t in range(-(-lens[b] // 128) - 1, -1, -1) if (t + h) % 2 == 0]  # noqa: E731
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens),
+                                        meta=lists(H, lens, sel), out_dtype=torch.float32)
+    keys = lambda b, h: [p for t in sel(b, h) for p in range(128 * t, min(lens[b], 128 * t + 128))]  # noqa: E731
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], keys(b, h))], 1 / math.sqrt(D)))
+
+
+def test_bad_pages_and_lengths():
+    """Keys on a page outside the cache are left out and flagged; a length past the table is cut."""
+    H, G, D, page, lens = 2, 2, 128, 32, [100, 90, 500, -4]
+    pool = Pool(27, pages_for([100, 90, 128], page), H, D, page, "e4m3")
+    ht, table = pool.tables([100, 90, 128, 0])
+    ht[0, 1], ht[0, 3], ht[1, 0] = 10 ** 6, -7, pool.cache.num_pages
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = _q(28, 4, H * G, D)
+    out, lse = bsa.decode(q, pool.cache, torch.from_numpy(ht).cuda(), _i32(lens), err_flag=err, out_dtype=torch.float32)
+    assert int(err) == bsa.FLAG_BAD_INDEX | bsa.FLAG_BAD_SEQLENS
+    ref = expect(pool, f64(q), G, lambda b, h: [(ht[b], range(min(max(lens[b], 0), 128)))], 1 / math.sqrt(D))
+    agree(out, lse, ref)
+    # without an error word the same results
+    o2, l2 = bsa.decode(q, pool.cache, torch.from_numpy(ht).cuda(), _i32(lens), out_dtype=torch.float32)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    # a prefix of bad pages only: nothing to attend there
+    err.zero_()
+    o3, l3 = bsa.decode_shared_prefix(q, pool.cache, _i32([-1, 99]), 40, torch.from_numpy(ht).cuda(), _i32(lens),
+                                      err_flag=err, out_dtype=torch.float32)
+    assert int(err) == bsa.FLAG_BAD_INDEX | bsa.FLAG_BAD_SEQLENS
+    agree(o3, l3, ref)
+
+
+@pytest.mark.parametrize("kind", ["varlen", "batched"])
+def test_bad_lists(kind):
+    H, G, D, page, lens = 1, 2, 64, 128, [600, 300]
+    pool = Pool(29, pages_for(lens, page), H, D, page, "int8")
+    ht, table = pool.tables(lens)
+    q = _q(30, 2, H * G, D)
+    run = lambda meta, err: bsa.decode(q, pool.cache, table, _i32(lens), meta=meta, err_flag=err, out_dtype=torch.float32)  # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    meta = lists(H, lens, lambda b, h: [-(-lens[b] // 128) - 1, 0], kind=kind)
+    flat = meta.full_idx.view(-1)
+    flat[0] = 77                                  # sequence 0 lists tile 77 and tile 0
+    out, lse = run(meta, err)
+    assert int(err) == bsa.FLAG_BAD_INDEX
+    keys = [list(range(128)), list(range(256, 300)) + list(range(128))]
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], keys[b])], 1 / math.sqrt(D)))
+    err.zero_()
+    meta = lists(H, lens, lambda b, h: [0], kind=kind)
+    meta.full_cnt.view(-1)[0], meta.full_cnt.view(-1)[1] = 1000, -3
+    out, lse = run(meta, err)                     # 1000 -> all of the row's entries, the rest of them -1
+    assert int(err) == bsa.FLAG_BAD_INDEX | bsa.FLAG_BAD_COUNT
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], range(128 if b == 0 else 0))], 1 / math.sqrt(D)))
+    if kind == "varlen":
+        err.zero_()
+        meta = lists(H, lens, lambda b, h: [0], kind=kind)
+        meta.cu_block_idx_offsets[1] = 7          # sequence 1's row would leave the index array
+        out, lse = run(meta, err)
+        assert int(err) == bsa.FLAG_BAD_SEQLENS
+        agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], range(128 if b == 0 else 0))], 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("G", [1, 16])
+def test_what_lies_behind_the_last_key_is_not_read_into_the_result(dtype, G):
+    """Codes and scales past a sequence's end, in the same page, may be anything, NaN included."""
+    H, D, page, lens = 2, 128, 128, [5, 77, 128 + 3]
+    pool = Pool(31, pages_for(lens, page) + 1, H, D, page, dtype)
+    ht, table = pool.tables(lens)
+    q = _q(32, 3, H * G, D)
+    for b, n in enumerate(lens):
+        last = int(ht[b, n // page])
+        for t in (pool.cache.k, pool.cache.v):
+            t.view(torch.uint8)[last, :, n % page:] = 0x7F
+        for t in (pool.cache.k_scale, pool.cache.v_scale):
+            t[last, :, n % page:] = float("nan")
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], range(lens[b]))], 1 / math.sqrt(D)))
+    o2, l2 = bsa.decode_shared_prefix(q, pool.cache, table[2].contiguous(), lens[2], table, _i32(lens), out_dtype=torch.float32)
+    agree(o2, l2, expect(pool, f64(q), G, lambda b, h: [(ht[2], range(lens[2])), (ht[b], range(lens[b]))], 1 / math.sqrt(D)))
+
+
+def test_nan_rows_reach_their_own_sequences_only():
+    H, G, D, page, lens = 1, 2, 64, 16, [40, 40]
+    pool = Pool(33, pages_for(lens, page), H, D, page, "e4m3")
+    ht, table = pool.tables(lens)
+    pool.cache.v_scale[int(ht[0, 1]), 0, 3] = float("nan")
+    q = _q(34, 2, H * G, D)
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    assert out[0].isnan().all() and out[1].isfinite().all() and lse.isfinite().all()
+    pool.cache.k_scale[int(ht[0, 1]), 0, 3] = float("nan")
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    assert out[0].isnan().all() and lse[0].isnan().all() and out[1].isfinite().all() and lse[1].isfinite().all()
+
+
+@pytest.mark.parametrize("G", [1, 12])
+def test_scales_of_all_sizes(G):
+    """Rows whose scales differ by 2^40 and more, zero scales, large scores: the weight of a key that
+    matters is never lost to the range of a 16-bit type."""
+    H, D, page, lens = 1, 64, 64, [300, 200]
+    pool = Pool(35, pages_for(lens, page), H, D, page, "e4m3", spread=0.0)
+    ht, table = pool.tables(lens)
+    rng = np.random.default_rng(36)
+    for name in ("k", "v"):
+        e = rng.integers(-30, 12, pool.scales[name].shape) if name == "v" else rng.integers(-6, 3, pool.scales[name].shape)
+        pool.scales[name] = (pool.scales[name] * 2.0 ** e).astype(np.float32)
+        pool.scales[name][..., 5] = 0.0
+        getattr(pool.cache, name + "_scale").copy_(torch.from_numpy(pool.scales[name]))
+    q = _q(37, 2, H * G, D, size=4.0)
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], range(lens[b]))], 1 / math.sqrt(D)))
+    # one key whose values are tiny next to its neighbours' but which takes all of the weight
+    pool.scales["v"][:] = 1.0
+    pool.scales["v"][ht[1, 0], 0, 7] = 2.0 ** -20
+    pool.cache.v_scale.copy_(torch.from_numpy(pool.scales["v"]))
+    meta_q = q.clone()
+    k7 = pool.host("k", ht[1], 0, [7])[0]
+    meta_q[1] = bf16((k7 / np.linalg.norm(k7) * 2000)[None].repeat(G, 0)).cuda()
+    pool.scales["k"][ht[1, 0], 0, 7] = 4.0
+    pool.cache.k_scale.copy_(torch.from_numpy(pool.scales["k"]))
+    out, lse = bsa.decode(meta_q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    agree(out, lse, expect(pool, f64(meta_q), G, lambda b, h: [(ht[b], range(lens[b]))], 1 / math.sqrt(D)))
+
+
+def test_queries_of_all_sizes():
+    """Queries far below and above fp16's range, zeros, strided rows."""
+    H, G, D, page, lens = 1, 6, 128, 128, [200]
+    pool = Pool(38, 2, H, D, page, "int8")
+    ht, table = pool.tables(lens)
+    x = np.random.default_rng(39).standard_normal((1, 2 * G, D))
+    for g, s in enumerate([1e-30, 1e-6, 0.0, 1e5, 1e20, 1.0]):
+        x[:, g] *= s
+    q = bf16(x).cuda()[:, :G]
+    for scale in (1e-20, 0.1):
+        part = q if scale < 1e-10 else torch.cat([q[:, :3], q[:, 5:]], 1)
+        g = part.shape[1]
+        out, lse = bsa.decode(part, pool.cache, table, _i32(lens), softmax_scale=scale, out_dtype=torch.float32)
+        agree(out, lse, expect(pool, f64(part), g, lambda b, h: [(ht[b], range(lens[b]))], float(np.float32(scale))))
+
+
+def test_fused_query_rows_and_given_buffers():
+    H, G, D, page, lens = 2, 3, 64, 32, [70, 10, 0]
+    pool = Pool(40, pages_for(lens, page), H, D, page, "e4m3")
+    _, table = pool.tables(lens)
+    qkv = _q(41, 3, H * G + 2 * H, D)
+    want = bsa.decode(qkv[:, :H * G].contiguous(), pool.cache, table, _i32(lens))
+    ws = bsa.alloc_decode_workspace(pool.cache, 3, H * G)
+    out, lse = torch.full((3, H * G, D), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((3, H * G), 5.0, device="cuda")
+    for _ in range(3):                                   # whatever the workspace held before
+        ws.fill_(255)
+        got = bsa.decode(qkv[:, :H * G], pool.cache, table, _i32(lens), out=out, lse=lse, workspace=ws)
+        assert got[0] is out and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_small_workspace_is_refused():
+    pool = Pool(42, 1, 1, 64, 16, "e4m3")
+    ws = torch.empty(64, dtype=torch.uint8, device="cuda")
+    with pytest.raises(bsa.BsattnError):
+        bsa.decode(_q(1, 1, 1, 64), pool.cache, _i32([[0]]), _i32([3]), workspace=ws)
+
+
+@pytest.mark.parametrize("op", ["decode", "prefix"])
+def test_repeats_are_equal_bit_for_bit(op):
+    H, G, D, page, lens, prefix = 2, 4, 128, 64, [3000, 10, 777, 0], 900
+    pool = Pool(43, pages_for(lens + [prefix], page), H, D, page, "int8")
+    hp = pool.take(-(-prefix // page))
+    _, table = pool.tables(lens)
+    q = _q(44, 4, H * G, D)
+    call = lambda: bsa.decode(q, pool.cache, table, _i32(lens)) if op == "decode" else \
+        bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens))  # noqa: E731
+    a = call()
+    for _ in range(5):
+        b = call()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_captured_steps_share_a_workspace():
+    """Append and decode, captured twice over one workspace, replayed in turn with the lengths advancing on the
+    device: each replay equals the eager calls."""
+    H, G, D, page, B = 2, 4, 128, 16, 3
+    start, steps = [5, 100, 31], 4
+    pool = Pool(45, pages_for([n + steps for n in start], page), H, D, page, "e4m3")
+    _, table = pool.tables([n + steps for n in start])
+    twin = bsa.KVCache(*(t.clone() for t in (pool.cache.k, pool.cache.v, pool.cache.k_scale, pool.cache.v_scale)))
+    n = _i32(start)
+    n2 = n.clone()
+    bufs = [dict(q=_q(50 + i, B, H * G, D), k=_q(60 + i, B, H, D), v=_q(70 + i, B, H, D)) for i in range(2)]
+    ws = bsa.alloc_decode_workspace(pool.cache, B, H * G)
+
+    def step(b, cache, n):
+        n += 1
+        bsa.kv_append(b["k"], b["v"], cache, table, n)
+        return bsa.decode(b["q"], cache, table, n, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(bufs[0], pool.cache, n)                     # first calls outside the capture
+    torch.cuda.current_stream().wait_stream(side)
+    n.copy_(_i32(start))
+    graphs = []
+    for b in bufs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = step(b, pool.cache, n)
+        graphs.append((g, res))
+    for i in range(steps):
+        g, res = graphs[i % 2]
+        g.replay()
+        got = [t.clone() for t in res]
+        want = step(bufs[i % 2], twin, n2)
+        assert torch.equal(n, n2) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_other_streams_have_their_own_allocations():
+    H, G, D, page, lens = 2, 4, 128, 128, [2000, 500]
+    pool = Pool(46, pages_for(lens, page), H, D, page, "e4m3")
+    _, table = pool.tables(lens)
+    q, n = _q(47, 2, H * G, D), _i32(lens)
+    want = bsa.decode(q, pool.cache, table, n)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [bsa.decode(q, pool.cache, table, n, stream=s if i % 2 else s.cuda_stream)
+           for _ in range(4) for i, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+def test_a_serving_run(dtype):
+    """Prompts appended, steps of append + decode, then the cached context read back for the block-sparse forward:
+    the forward's row for the newest token equals decode's, by way of the same lists."""
+    H, D, page, prompts, steps = 4, 128, 64, [100, 260, 1], 3
+    pool = Pool(48, pages_for([n + steps for n in prompts], page), H, D, page, dtype)
+    _, table = pool.tables([n + steps for n in prompts])
+    cache, B = pool.cache, len(prompts)
+    rng = np.random.default_rng(49)
+    x = [[bf16(rng.standard_normal((n + steps, H, D))) for n in prompts] for _ in range(3)]
+    cu = _i32(np.concatenate([[0], np.cumsum(prompts)]).tolist())
+    k, v = (torch.cat([x[j][b][:n] for b, n in enumerate(prompts)]).cuda() for j in (1, 2))
+    bsa.kv_append(k, v, cache, table, _i32(prompts), cu_seqlens=cu)
+    for s in range(steps):
+        lens = [n + s + 1 for n in prompts]
+        q, kn, vn = (torch.stack([x[j][b][n + s] for b, n in enumerate(prompts)]).cuda() for j in range(3))
+        bsa.kv_append(kn, vn, cache, table, _i32(lens))
+        out, lse = bsa.decode(q, cache, table, _i32(lens), out_dtype=torch.float32)
+    # the oracle, from the rows that were appended
+    qs, scale = f64(q), 1 / math.sqrt(D)
+    for b, n in enumerate(lens):
+        kq, vq = (c * s[..., None] for c, s in (okv.quantise(f64(x[j][b]), dtype) for j in (1, 2)))
+        for h in range(H):
+            o, l, spread = okv.attend(qs[b, h], kq[:, h], vq[:, h], scale)
+            assert np.all(np.abs(f64(out[b, h]) - o) <= spread * 2.0 ** -10 + 1e-6)
+            assert abs(float(lse[b, h]) - l) <= 1e-5
+    # the whole context through the framework's forward, one query row a sequence
+    total, cuk = sum(lens), _i32(np.concatenate([[0], np.cumsum(lens)]).tolist())
+    kr, vr = bsa.kv_read(cache, table, cuk, total=total)
+    cuq = _i32(list(range(B + 1)))
+    nn = [-(-n // 128) for n in lens]
+    meta = bsa.alloc_meta(B, H, varlen=True, total_m_blocks=B, total_n_blocks=sum(nn), max_num_n=max(nn))
+    block_map = torch.ones((H, sum(nn)), dtype=torch.uint8, device="cuda")
+    block_map[1, nn[0] + nn[1] - 1] = 0                 # head 1 of sequence 1 skips its last tile
+    bsa.build_meta(block_map, meta, cu_seqlens_q=cuq, cu_seqlens_k=cuk, seqlen_q=B, seqlen_k=total)
+    fo, fl = bsa.forward(q, kr, vr, meta, cu_seqlens_q=cuq, cu_seqlens_k=cuk, out_dtype=torch.float32)
+    do, dl = bsa.decode(q, cache, table, _i32(lens), meta=meta, out_dtype=torch.float32)
+    # the forward rounds its weights to bf16 (2^-8), and int8 rows were rounded to bf16 (2^-8 of scores and values)
+    vmax = float(vr.float().abs().max())
+    assert (fo - do).abs().max() <= 5e-3 + (0 if dtype == "e4m3" else 2.0 ** -7 * vmax)
+    assert (fl.t() - dl).abs().max() <= (1e-4 if dtype == "e4m3" else 3e-2)
+    assert not torch.equal(dl[1, 1], lse[1, 1]) and torch.equal(dl[0], lse[0])

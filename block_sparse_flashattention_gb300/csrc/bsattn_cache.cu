@@ -4,7 +4,7 @@
 //   e4m3  scale = 2^e, e = max(-126, ceil(log2(a / 448))).  a = 1.m 2^k and 448 =
 //         1.75 2^8, so e = k - 8, one more where 1.m > 1.75: integer work on a's bits.
 //         x / scale is exact, so the code is x rounded once.
-//   int8  scale = a / 127, code = rint(x (127 / a)), each operation in fp32.
+//   int8  scale = a (1 / 127), code = rint(x (127 (1 / a))), each operation in fp32.
 // The maximum is taken on the bit patterns without the sign (ordered like the
 // magnitudes, infinities and NaNs above all numbers).
 //
@@ -62,8 +62,8 @@ __device__ __forceinline__ uint2 quantise(uint4 x, float &scale) {
     float f;
     if constexpr (kInt8) {
         const float af = fmaxf(__uint_as_float(a << 16), 127.f * 0x1p-126f);
-        scale = __fdiv_rn(af, 127.f);
-        f = __fdiv_rn(127.f, af);
+        scale = __fmul_rn(af, 1.f / 127.f);
+        f = __fmul_rn(127.f, __frcp_rn(af));
     } else {
         const int e = max(-126, (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0));
         scale = __uint_as_float((uint32_t)(e + 127) << 23);

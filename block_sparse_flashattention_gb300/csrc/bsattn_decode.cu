@@ -1,8 +1,40 @@
-// Attention of one query token per sequence over a paged 8-bit K/V cache.
+// Attention of one query token per sequence over a paged 8-bit K/V cache, alone or
+// behind a prefix that every sequence of the batch shares.
 //
-// One block per (sequence, query head); each of its warps walks the keys with a
-// stride, a lane holding D / 32 elements of the row, with a running maximum and sum
-// of its own; the warps' results are joined at the end.
+// For one KV head, query rows r (the head's G queries of one sequence; for the prefix
+// the queries of every sequence) meet keys j:
+//   z_rj = c_r ks_j (q'_r . kcode_j),  c_r = softmax_scale log2(e) 2^e_r, q' = q 2^-e_r,
+//   l_r = sum_j 2^(z_rj - m_r),  O_r = sum_j 2^(z_rj + log2 vs_j - u_r) vcode_j,
+//   out_r = O_r 2^(u_r - m_r) / l_r,  lse_r = ln 2 (m_r + log2 l_r),
+// with running references m_r and u_r.  Both products run on the tensor cores in fp16
+// with fp32 accumulation: codes (e4m3 or int8) are exact in fp16, and so is q' for every
+// element that matters (2^e_r is the row's largest binary exponent, so q' keeps all 8
+// bits of a bf16 element down to 2^-14 of the largest).  The weight of a key carries
+// its value scale in the exponent, with a reference u_r of its own: what is rounded to
+// fp16 (11 bits) is a number relative to the largest contribution, whatever the scales
+// are, and 2^7 of headroom keeps full precision down to 2^-21 of that.
+//
+// Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.
+//
+// Work split.  A segment is one (sequence, KV head), or one (KV head, 128 query rows)
+// of the prefix; its keys are tiles of 128.  All tiles of all segments form one line,
+// cut into equal pieces, one per CTA (one CTA per SM): every SM reads the same number
+// of bytes whatever the lengths.  A segment that lies within one piece is finished
+// there; the parts of the others (fp32 output and LSE) go to the workspace and a second
+// kernel, a programmatic dependent of the first, joins them.
+//
+// Roles (288 threads): warp 8 looks up lists and pages and keeps a ring of stages full
+// (TMA: codes by rows with the 128-byte or 64-byte swizzle, scales as plain copies);
+// warps 0-7 compute.  Rows come in tiles of 16; R row tiles use 8 / R warps each, which
+// share a tile's eight groups of 16 keys and join their sums at the segment's end.
+//
+// Fragments without a transpose.  In S = Q K^T the contraction index may be permuted
+// alike on both sides, so lane 4g + t takes the D / 4 consecutive codes d = (D / 4) t ..
+// of key g, four per k-step.  In O^T = V^T P^T the rows d may be permuted freely, so the
+// lane takes D / 8 consecutive codes of each of its four keys and interleaves the bytes
+// of two keys before they are widened.  P leaves the first product in the layout the
+// second wants.  With the swizzled rows none of these 16-byte loads meets a bank twice
+// (the 8-byte loads of V at D = 64 do, two ways).
 #include "bsattn_internal.h"
 #include "kv_codes.cuh"
 #include "sm100_ptx.cuh"
@@ -11,128 +43,859 @@ namespace bsattn {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kConsumers = 8;                    // computing warps
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kMaxCtas = 256;                    // pieces the workspace has room for
+constexpr int kRowBlock = 128;                   // query rows of a prefix segment
 
-// D / 32 consecutive codes of a row as fp32.
+constexpr uint32_t kLast = 1u, kComplete = 2u;   // TileMsg flags
+
+// What the producer tells the computing warps about a stage.
+struct TileMsg {
+    int32_t seg;      // -1: no further tiles
+    int32_t lim;      // keys of the tile that count
+    uint32_t groups;  // bit i: the page of keys 16 i .. 16 i + 15 is loaded
+    uint32_t flags;
+};
+
 template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t *row, int lane, bool int8, float (&y)[D / 32]) {
-    uint32_t x;
-    if constexpr (D == 128) x = *reinterpret_cast<const uint32_t *>(row + lane * 4);
-    else x = *reinterpret_cast<const uint16_t *>(row + lane * 2);
-    float f[4];
-    if (int8) unpack_int8(x, f);
-    else unpack_e4m3(x, f);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) y[i] = f[i];
+struct Cfg {
+    // 5 x 33 KB or 8 x 17 KB in flight; what HBM needs at 6.7 TB/s and ~1 us is 44 KB per SM
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr uint32_t kCodes = 128u * D;                 // K or V codes of a tile
+    static constexpr uint32_t kStageBytes = 2u * kCodes;
+    static constexpr uint32_t kScales = kStages * kStageBytes;   // per stage 128 K scales, 128 V scales
+    static constexpr uint32_t kRed = kScales + kStages * 1024u;  // join: 4 warps x (D / 2) x 32 lanes fp32
+    static constexpr uint32_t kStat = kRed + 4u * (D / 2) * 128u;  // [8 warps][16 rows] m, u, l
+    static constexpr uint32_t kMsg = kStat + kConsumers * 16u * 12u;
+    static constexpr uint32_t kBar = kMsg + kStages * (uint32_t)sizeof(TileMsg);
+    static constexpr uint32_t kMisc = kBar + (2u * kStages + 1u) * 8u;  // abort flag, start, scan
+    static constexpr uint32_t kBytes = kMisc + 128u;
+    static constexpr uint32_t kAlloc = kBytes + 1024u;           // slack for 1024-byte alignment
+    static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+
+struct Misc {
+    int32_t abort, start_seg;
+    long long start_off;
+    long long warp_sum[kConsumers + 1];
+};
+static_assert(sizeof(Misc) <= 128, "misc area");
+
+// Segment numbering and the workspace: prefix segments (head-major, row blocks inside),
+// then one per (sequence, KV head).  Part `seg + cta` (of its kind) holds what a CTA
+// computed of a segment: along the line of tiles, from one part to the next either the
+// segment or the CTA advances, so no two parts share a number.
+struct Plan {
+    int row_blocks, sp, ss;       // prefix row blocks per head, prefix and suffix segments
+    int rows_p;                   // rows a prefix part has room for
+    size_t rec, pre_o, pre_l, suf_o, suf_l, total;
+};
+
+__host__ __device__ inline Plan make_plan(int B, int H, int G, int D, int prefix_len) {
+    Plan w;
+    const int rows = B * G;
+    w.row_blocks = prefix_len > 0 ? (rows + kRowBlock - 1) / kRowBlock : 0;
+    w.rows_p = rows < kRowBlock ? rows : kRowBlock;
+    w.sp = H * w.row_blocks;
+    w.ss = B * H;
+    const size_t np = w.sp ? (size_t)(w.sp + kMaxCtas) * w.rows_p : 0, ns = (size_t)(w.ss + kMaxCtas) * G;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255u) & ~(size_t)255u;
+        return here;
+    };
+    w.rec = take((size_t)(w.sp + w.ss) * sizeof(int2));
+    w.pre_o = take(np * D * 4u);
+    w.pre_l = take(np * 4u);
+    w.suf_o = take(ns * D * 4u);
+    w.suf_l = take(ns * 4u);
+    w.total = at;
+    return w;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) bsattn_decode_kernel(const __grid_constant__ DecodeParams p) {
-    constexpr int E = D / 32;
-    const int hq = blockIdx.x, b = blockIdx.y, h = hq / p.G;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        q[i] = __uint_as_float((uint32_t)p.q[b * p.q_stride + (long long)hq * D + lane * E + i] << 16);
-        o[i] = 0.f;
-    }
-    const int ps = 1 << p.c.page_shift;
-    auto visit = [&](const int32_t *table, int j) {
-        const int page = __ldg(table + (j >> p.c.page_shift));
-        if (page < 0 || page >= p.c.num_pages) {
-            if (p.err && lane == 0) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
-            return;
-        }
-        const long long row = (((long long)page * p.c.H + h) << p.c.page_shift) + (j & (ps - 1));
-        float x[E];
-        load_codes<D>(p.c.k + row * D, lane, p.c.int8, x);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s = fmaf(q[i], x[i], s);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= p.c.ks[row] * p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m - base), w = exp2f(s - base);
-        m = mn;
-        l = l * a + w;
-        load_codes<D>(p.c.v + row * D, lane, p.c.int8, x);
-        const float wv = w * p.c.vs[row];
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = o[i] * a + wv * x[i];
-    };
-    for (int j = warp; j < p.prefix_len; j += kWarps) visit(p.prefix_table, j);
-    const int cap = p.table_cols << p.c.page_shift;
-    int n = max(p.seqlens[b], 0);
-    if (n > cap) {
-        n = cap;
-        if (p.err && threadIdx.x == 0) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
-    }
-    const int32_t *table = p.table + (long long)b * p.table_stride;
-    if (!p.has_lists) {
-        for (int j = warp; j < n; j += kWarps) visit(table, j);
+struct Seg {
+    int prefix, h, b, row0, rows;
+};
+
+__device__ __forceinline__ Seg segment(const DecodeParams &p, const Plan &w, int seg) {
+    Seg s;
+    if (seg < w.sp) {
+        s.prefix = 1;
+        s.h = seg / w.row_blocks;
+        s.row0 = (seg - s.h * w.row_blocks) * kRowBlock;
+        s.rows = min(kRowBlock, p.B * p.G - s.row0);
+        s.b = 0;
     } else {
-        const int nn = p.lists_varlen ? (n + kTile - 1) / kTile : p.list_n;
-        const long long cnt_at = p.lists_varlen ? (long long)h * p.B + b : (long long)b * p.c.H + h;
-        long long idx_at = cnt_at * p.list_n;
-        bool ok = true;
-        if (p.lists_varlen) {
-            const int off = p.cu_off[b];
-            idx_at = (long long)h * p.total_n + off;
-            ok = off >= 0 && (long long)off + nn <= p.total_n && !(p.vl && nn > p.list_n);
-            if (!ok && p.err && threadIdx.x == 0) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
-        }
-        for (int list = 0; ok && list < 2; ++list) {
-            int cnt = (list ? p.mask_cnt : p.full_cnt)[cnt_at];
-            if (cnt < 0 || cnt > nn) {
-                cnt = cnt < 0 ? 0 : nn;
-                if (p.err && threadIdx.x == 0) atomicOr(p.err, BSATTN_FLAG_BAD_COUNT);
-            }
-            const int32_t *idx = (list ? p.mask_idx : p.full_idx) + idx_at;
-            for (int i = 0; i < cnt; ++i) {
-                const int t = idx[i];
-                if (t < 0 || t >= nn) {
-                    if (p.err && threadIdx.x == 0) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
-                    continue;
-                }
-                int lim = min(kTile, n - t * kTile);
-                if (list && p.vl) lim = min(lim, p.vl[(long long)b * p.list_n + t]);
-                for (int j = warp; j < lim; j += kWarps) visit(table, t * kTile + j);
-            }
+        s.prefix = 0;
+        s.b = (seg - w.sp) / p.c.H;
+        s.h = seg - w.sp - s.b * p.c.H;
+        s.row0 = 0;
+        s.rows = p.G;
+    }
+    return s;
+}
+
+__device__ __forceinline__ void raise(const DecodeParams &p, int bit) {
+    if (p.err) atomicOr(p.err, bit);
+}
+
+// Keys of sequence b's own part; `check`: flag a length past the page table.
+__device__ __forceinline__ int seq_keys(const DecodeParams &p, int b, bool check) {
+    const int n = max(__ldg(p.seqlens + b), 0), cap = p.table_cols << p.c.page_shift;
+    if (n > cap && check) raise(p, BSATTN_FLAG_BAD_SEQLENS);
+    return min(n, cap);
+}
+
+struct ListRow {
+    int full, mask, nn;  // entries of the two lists, tiles an entry may name
+    long long at;        // first index entry
+};
+
+__device__ __forceinline__ ListRow list_row(const DecodeParams &p, int b, int h, int n, bool check) {
+    ListRow r;
+    r.full = r.mask = 0;
+    r.nn = p.lists_varlen ? (n + kTile - 1) / kTile : p.list_n;
+    const long long cnt_at = p.lists_varlen ? (long long)h * p.B + b : (long long)b * p.c.H + h;
+    r.at = cnt_at * p.list_n;
+    if (p.lists_varlen) {
+        const int off = __ldg(p.cu_off + b);
+        r.at = (long long)h * p.total_n + off;
+        if (off < 0 || (long long)off + r.nn > p.total_n || (p.vl && r.nn > p.list_n)) {
+            if (check) raise(p, BSATTN_FLAG_BAD_SEQLENS);
+            return r;
         }
     }
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
+    const int f = __ldg(p.full_cnt + cnt_at), m = __ldg(p.mask_cnt + cnt_at);
+    r.full = min(max(f, 0), r.nn);
+    r.mask = min(max(m, 0), r.nn);
+    if (check && (r.full != f || r.mask != m)) raise(p, BSATTN_FLAG_BAD_COUNT);
+    return r;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+    return x;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 x;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
+    return x;
+}
+
+// Byte offset in a swizzled tile of D-byte rows: 16-byte piece `c` of row `r`.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+    if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+    else return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Where a finished row goes: the call's output, or a part in the workspace.
+struct RowOut {
+    bool direct;
+    long long row;   // output row (direct), or row of the part arrays
+};
+
+// The computing warps.
+template <int D, bool kInt8, bool kWide>
+struct Consumer {
+    using C = Cfg<D>;
+    static constexpr int kSteps = D / 16;   // k-steps of Q K^T, row tiles of V^T
+    static constexpr int kCols = kWide ? 2 : 1;  // groups of 8 query rows
+    const DecodeParams &p;
+    const Plan &w;
+    uint8_t *smem;
+    uint32_t base;
+    int warp, lane, g, t;
+    uint32_t q[kSteps][kWide ? 4 : 2];
+    float qs[kCols];                         // c_r of rows g, g + 8
+    float m[kCols], u[kCols], l[kCols];
+    float o[kSteps][kCols][4];
+    int row_tile, key_group, key_groups;
+    uint32_t sync_phase;
+
+    __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kBar + 8u * (uint32_t)i; }
+
+    // All computing warps meet.
+    __device__ __forceinline__ bool meet(volatile int *abort) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(2 * C::kStages));
+        const bool ok = mbar_wait(bar(2 * C::kStages), sync_phase, abort, p.err, BSATTN_FLAG_TIMEOUT);
+        sync_phase ^= 1u;
+        return __all_sync(0xffffffffu, ok);
+    }
+
+    __device__ __forceinline__ const uint16_t *query(const Seg &s, int r) const {
+        int b = s.b, gi = r;
+        if (s.prefix) {
+            b = (s.row0 + r) / p.G;
+            gi = s.row0 + r - b * p.G;
+        }
+        return p.q + (long long)b * p.q_stride + (long long)(s.h * p.G + gi) * D;
+    }
+
+    __device__ __forceinline__ void begin(const Seg &s) {
+        const int tiles = (s.rows + 15) / 16;
+        const int R = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+        row_tile = warp % R;
+        key_group = warp / R;
+        key_groups = kConsumers / R;
 #pragma unroll
-    for (int i = 0; i < E; ++i) so[warp][lane * E + i] = o[i];
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm[w]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-    for (int w = 0; w < kWarps; ++w) ll += sl[w] * exp2f(sm[w] - base);
-    const bool empty = ll == 0.f;
-    const long long at = (long long)b * p.Hq + hq;
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x += so[w][d] * exp2f(sm[w] - base);
-        x = empty ? 0.f : x / ll;
-        if (p.out_f32) static_cast<float *>(p.out)[at * D + d] = x;
-        else static_cast<uint16_t *>(p.out)[at * D + d] = (uint16_t)pack_bf16x2(x, 0.f);
+        for (int hf = 0; hf < kCols; ++hf) {
+            const int r = row_tile * 16 + g + 8 * hf;
+            uint32_t x[D / 8];               // D / 4 bf16 elements of the row
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint4 y = make_uint4(0, 0, 0, 0);
+                if (r < s.rows) y = __ldg(reinterpret_cast<const uint4 *>(query(s, r) + t * (D / 4)) + i);
+                x[4 * i] = y.x;
+                x[4 * i + 1] = y.y;
+                x[4 * i + 2] = y.z;
+                x[4 * i + 3] = y.w;
+            }
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, x[i] & 0x7fff7fffu);
+            a = max(a & 0xffffu, a >> 16);
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+            // biased exponent of the largest element; zero rows and rows that are not finite stay as they are
+            const int e = (a == 0 || a >= 0x7f80u) ? 127 : min(max((int)(a >> 7), 1), 253);
+            const float f = __uint_as_float((uint32_t)(254 - e) << 23);
+            qs[hf] = p.scale_log2 * __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t y = pack_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
+                // k-step i / 2: elements 4 s, 4 s + 1 are a0 (a1 for row g + 8), 4 s + 2, 4 s + 3 are a2 (a3)
+                if constexpr (kWide) q[i / 2][2 * (i & 1) + hf] = y;
+                else q[i / 2][i & 1] = y;
+            }
+            m[hf] = u[hf] = -INFINITY;
+            l[hf] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[i][n][x] = 0.f;
     }
-    if (threadIdx.x == 0) p.lse[at] = empty ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
+
+    // 16 keys of a stage (group c), the first nv of which count.
+    __device__ __forceinline__ void keys16(uint32_t sk, uint32_t ssc, int c, int nv) {
+        const uint32_t sv = sk + C::kCodes;
+        float s[2][4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+            const int r = 16 * c + 8 * nb + g;
+            uint32_t x[D / 16];
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 y = lds128(sk + piece_at<D>(r, (D / 64) * t + i));
+                x[4 * i] = y.x;
+                x[4 * i + 1] = y.y;
+                x[4 * i + 2] = y.z;
+                x[4 * i + 3] = y.w;
+            }
+            // two accumulators: half the length of the dependent chain
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                uint32_t b0, b1;
+                codes_to_f16x2<kInt8>(x[i], b0, b1);
+                if constexpr (kWide) mma_f16(acc[i & 1], q[i][0], q[i][1], q[i][2], q[i][3], b0, b1);
+                else mma_f16(acc[i & 1], q[i][0], 0u, q[i][1], 0u, b0, b1);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nb][i] = acc[0][i] + acc[1][i];
+        }
+        // V: D / 8 codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 2 * t + (i & 1) + 8 * (i >> 1), r = 16 * c + j;
+            if constexpr (D == 128) {
+                const uint4 y = lds128(sv + piece_at<D>(r, g));
+                v[i][0] = y.x;
+                v[i][1] = y.y;
+                v[i][2] = y.z;
+                v[i][3] = y.w;
+            } else {
+                const uint2 y = lds64(sv + piece_at<D>(r, g >> 1) + 8u * (g & 1));
+                v[i][0] = y.x;
+                v[i][1] = y.y;
+            }
+            if (nv < 16 && j >= nv) {  // what lies behind the last key may be NaN codes
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) v[i][x] = 0u;
+            }
+        }
+        // scores (in units of log2) and scores with the value scale in the exponent
+        float z[kCols][4], zu[kCols][4];
+        float zm[kCols], um[kCols];
+#pragma unroll
+        for (int hf = 0; hf < kCols; ++hf) zm[hf] = um[hf] = -INFINITY;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+            const uint2 kb = lds64(ssc + 4u * (16 * c + 8 * nb + 2 * t));
+            const uint2 vb = lds64(ssc + 512u + 4u * (16 * c + 8 * nb + 2 * t));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float ks = __uint_as_float(e ? kb.y : kb.x);
+                const float lv = lg2_approx(__uint_as_float(e ? vb.y : vb.x));
+                const bool on = nv >= 16 || 8 * nb + 2 * t + e < nv;
+#pragma unroll
+                for (int hf = 0; hf < kCols; ++hf) {
+                    const float x = s[nb][2 * hf + e] * ks * qs[hf];
+                    z[hf][2 * nb + e] = on ? x : -INFINITY;
+                    zu[hf][2 * nb + e] = on ? x + lv : -INFINITY;
+                    zm[hf] = fmaxf(zm[hf], z[hf][2 * nb + e]);
+                    um[hf] = fmaxf(um[hf], zu[hf][2 * nb + e]);
+                }
+            }
+        }
+        // The references move only when some key is 2^8 above them: l and O stay finite
+        // (weights reach 2^15 in fp16), and the quotient is the same.
+        bool grow = false;
+#pragma unroll
+        for (int hf = 0; hf < kCols; ++hf) grow |= zm[hf] > m[hf] + 8.f || um[hf] > u[hf] + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+            float ao[kCols];
+#pragma unroll
+            for (int hf = 0; hf < kCols; ++hf) {
+                float a = fmaxf(zm[hf], __shfl_xor_sync(0xffffffffu, zm[hf], 1));
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                float b = fmaxf(um[hf], __shfl_xor_sync(0xffffffffu, um[hf], 1));
+                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
+                a = fmaxf(a, m[hf]);
+                b = fmaxf(b, u[hf]);
+                l[hf] *= a == -INFINITY ? 1.f : ex2_approx(m[hf] - a);
+                ao[hf] = b == -INFINITY ? 1.f : ex2_approx(u[hf] - b);
+                m[hf] = a;
+                u[hf] = b;
+            }
+            // O's columns are query rows 2t, 2t + 1 (and 8 above)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+                const float a0 = __shfl_sync(0xffffffffu, ao[n], 8 * t);
+                const float a1 = __shfl_sync(0xffffffffu, ao[n], 8 * t + 4);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    o[i][n][0] *= a0;
+                    o[i][n][1] *= a1;
+                    o[i][n][2] *= a0;
+                    o[i][n][3] *= a1;
+                }
+            }
+        }
+        uint32_t pb[kCols][2];
+#pragma unroll
+        for (int hf = 0; hf < kCols; ++hf) {
+            const float nm = m[hf] == -INFINITY ? 0.f : -m[hf];
+            const float nu = (u[hf] == -INFINITY ? 0.f : -u[hf]) + 7.f;
+            l[hf] += (ex2_approx(z[hf][0] + nm) + ex2_approx(z[hf][1] + nm)) +
+                     (ex2_approx(z[hf][2] + nm) + ex2_approx(z[hf][3] + nm));
+            pb[hf][0] = pack_f16x2(ex2_approx(zu[hf][0] + nu), ex2_approx(zu[hf][1] + nu));
+            pb[hf][1] = pack_f16x2(ex2_approx(zu[hf][2] + nu), ex2_approx(zu[hf][3] + nu));
+        }
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            // bytes d, d + 1 of both keys of a pair side by side, then bytes d + 2, d + 3
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const uint32_t sel = hi ? 0x7362u : 0x5140u;
+                uint32_t a0, a1, a2, a3;
+                codes_to_f16x2<kInt8>(__byte_perm(v[0][x], v[1][x], sel), a0, a1);
+                codes_to_f16x2<kInt8>(__byte_perm(v[2][x], v[3][x], sel), a2, a3);
+#pragma unroll
+                for (int n = 0; n < kCols; ++n) mma_f16(o[2 * x + hi][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            }
+        }
+    }
+
+    // Joins the key groups of each row tile and writes the rows.
+    __device__ __forceinline__ bool finish(const Seg &s, int seg, bool complete, volatile int *abort) {
+        float *stat = reinterpret_cast<float *>(smem + C::kStat);  // [warp][row][m, u, l]
+        float *red = reinterpret_cast<float *>(smem + C::kRed);
+#pragma unroll
+        for (int hf = 0; hf < kCols; ++hf) {
+            l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
+            l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
+            if (t == 0) {
+                float *x = stat + (warp * 16 + g + 8 * hf) * 3;
+                x[0] = m[hf];
+                x[1] = u[hf];
+                x[2] = l[hf];
+            }
+        }
+        if (!meet(abort)) return false;
+        const int R = kConsumers / key_groups;
+        // factors of this lane's output rows 2t, 2t + 1 (+ 8): own sums to the joint references
+        float inv[kCols][2], lse2[kCols][2];
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * n + 2 * t + e;
+                float mm = -INFINITY, uu = -INFINITY, ll = 0.f;
+                for (int k = 0; k < key_groups; ++k) {
+                    const float *x = stat + ((k * R + row_tile) * 16 + r) * 3;
+                    mm = fmaxf(mm, x[0]);
+                    uu = fmaxf(uu, x[1]);
+                }
+                const float bm = mm == -INFINITY ? 0.f : mm, bu = uu == -INFINITY ? 0.f : uu;
+                for (int k = 0; k < key_groups; ++k) {
+                    const float *x = stat + ((k * R + row_tile) * 16 + r) * 3;
+                    ll += x[2] * ex2_approx(x[0] - bm);
+                }
+                const float own = ex2_approx(stat[(warp * 16 + r) * 3 + 1] - bu);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    o[i][n][e] *= own;
+                    o[i][n][2 + e] *= own;
+                }
+                const bool empty = ll == 0.f;
+                // no key with a value scale above 0: O is 0, whatever the quotient of the references
+                inv[n][e] = empty || uu == -INFINITY ? 0.f : ex2_approx(bu - bm - 7.f) / ll;
+                lse2[n][e] = empty ? -INFINITY : bm + lg2_approx(ll);
+            }
+        for (int step = key_groups >> 1; step > 0; step >>= 1) {
+            if (key_group >= step && key_group < 2 * step) {
+                float *x = red + (size_t)(warp - step * R) * (D / 2) * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[((i * kCols + n) * 4 + e) * 32] = o[i][n][e];
+            }
+            if (!meet(abort)) return false;
+            if (key_group < step) {
+                const float *x = red + (size_t)warp * (D / 2) * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][n][e] += x[((i * kCols + n) * 4 + e) * 32];
+            }
+            if (!meet(abort)) return false;
+        }
+        if (key_group == 0) {
+            // lane: D / 8 consecutive elements d = (D / 8) g .. of its rows
+#pragma unroll
+            for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row_tile * 16 + 8 * n + 2 * t + e;
+                    if (r >= s.rows) continue;
+                    float y[D / 8];
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        y[2 * i] = o[i][n][e] * inv[n][e];
+                        y[2 * i + 1] = o[i][n][2 + e] * inv[n][e];
+                    }
+                    store_row(s, seg, complete, r, y, lse2[n][e]);
+                }
+        }
+        // the next segment's sums may overwrite `stat` only when every warp has read it
+        return key_groups > 1 || meet(abort);
+    }
+
+    __device__ __forceinline__ void store_row(const Seg &s, int seg, bool complete, int r, const float (&y)[D / 8],
+                                              float lse2) {
+        if (!s.prefix && complete && w.sp == 0) {
+            const long long row = (long long)s.b * p.Hq + s.h * p.G + r;
+            if (p.out_f32) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D + g * (D / 8));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * D + g * (D / 8));
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                        pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+            }
+            if (g == 0) p.lse[row] = lse2 * 0.69314718055994530942f;
+        } else {
+            const long long part = (seg - (s.prefix ? 0 : w.sp)) + (long long)blockIdx.x;
+            const long long row = s.prefix ? part * w.rows_p + r : part * p.G + r;
+            float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.ws + (s.prefix ? w.pre_o : w.suf_o)) +
+                                                     row * D + g * (D / 8));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            if (g == 0) reinterpret_cast<float *>(p.ws + (s.prefix ? w.pre_l : w.suf_l))[row] = lse2;
+        }
+    }
+
+    __device__ __forceinline__ void run(volatile int *abort) {
+        int cur = -1;
+        Seg s = {};
+        for (uint32_t it = 0;; ++it) {
+            const uint32_t st = it % C::kStages;
+            const bool ok = mbar_wait(bar(st), (it / C::kStages) & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            const TileMsg msg = reinterpret_cast<const TileMsg *>(smem + C::kMsg)[st];
+            if (msg.seg < 0) return;
+            if (msg.seg != cur) {
+                cur = msg.seg;
+                s = segment(p, w, cur);
+                begin(s);
+            }
+            const uint32_t sk = base + st * C::kStageBytes, ssc = base + C::kScales + st * 1024u;
+            for (int c = key_group; c < 8; c += key_groups) {
+                const int nv = min(16, msg.lim - 16 * c);
+                if (nv > 0 && ((msg.groups >> c) & 1u)) keys16(sk, ssc, c, nv);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kStages + st));
+            if (msg.flags & kLast) {
+                if (!finish(s, cur, (msg.flags & kComplete) != 0, abort)) return;
+            }
+        }
+    }
+};
+
+template <int D, bool kInt8, bool kWide>
+__global__ void __launch_bounds__(kThreads, 1)
+    bsattn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w,
+                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    Misc *misc = reinterpret_cast<Misc *>(smem + C::kMisc);
+    volatile int *abort = &misc->abort;
+    auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
+    const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
+    grid_launch_dependents();  // the joining kernel may take its place; it waits for this grid
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar(s), 1);
+            mbar_init(bar(C::kStages + s), kConsumers);
+        }
+        mbar_init(bar(2 * C::kStages), kConsumers);
+        misc->abort = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+
+    // Where this CTA's piece of the line of tiles begins.  Each thread sums the tiles of a
+    // run of sequences (or, with lists, of (sequence, head) pairs); CTA c also writes the
+    // records of every gridDim-th of them: the CTAs its segments' parts lie in.
+    const int nt_pre = w.sp ? (p.prefix_len + kTile - 1) / kTile : 0;
+    const long long tiles_pre = (long long)w.sp * nt_pre;
+    const int units = p.has_lists ? p.B * p.c.H : p.B, per = (units + kThreads - 1) / kThreads;
+    const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
+    auto unit_tiles = [&](int x, bool check) -> int {
+        if (!p.has_lists) return (seq_keys(p, x, check) + kTile - 1) / kTile;
+        const int b = x / p.c.H, h = x - b * p.c.H;
+        const ListRow r = list_row(p, b, h, seq_keys(p, b, check && h == 0), check);
+        return r.full + r.mask;
+    };
+    const int reps = p.has_lists ? 1 : p.c.H;  // segments of a unit, of equal length
+    long long sum = 0;
+    for (int x = u0; x < u1; ++x) sum += (long long)unit_tiles(x, x % (int)gridDim.x == (int)blockIdx.x) * reps;
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) misc->warp_sum[warp] = incl;
+    __syncthreads();
+    long long at = tiles_pre + incl - sum, total = tiles_pre;
+    for (int i = 0; i <= kConsumers; ++i) {
+        if (i < warp) at += misc->warp_sum[i];
+        total += misc->warp_sum[i];
+    }
+    // no CTA's piece is empty while a later one's is not: a segment's parts are consecutive
+    const long long cuts = min((long long)gridDim.x, total), cta = blockIdx.x;
+    const long long lo = cta < cuts ? total * cta / cuts : 0, hi = cta < cuts ? total * (cta + 1) / cuts : 0;
+    auto owner = [&](long long tile) -> int { return (int)(((tile + 1) * cuts - 1) / total); };
+    int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
+    if (tid == 0 && lo < hi && lo < tiles_pre) {
+        misc->start_seg = (int)(lo / nt_pre);
+        misc->start_off = lo % nt_pre;
+    }
+    for (int x = (int)blockIdx.x * kThreads + tid; x < w.sp; x += (int)gridDim.x * kThreads)
+        rec[x] = make_int2(owner((long long)x * nt_pre), owner((long long)(x + 1) * nt_pre - 1));
+    for (int x = u0; x < u1; ++x) {
+        const bool mine = x % (int)gridDim.x == (int)blockIdx.x;
+        const int n = unit_tiles(x, false);
+        const long long end = at + (long long)n * reps;
+        if (lo < hi && lo >= at && lo < end) {
+            misc->start_seg = w.sp + x * reps + (int)((lo - at) / n);
+            misc->start_off = (lo - at) % n;
+        }
+        if (mine)
+            for (int r = 0; r < reps; ++r) {
+                const long long a = at + (long long)r * n;
+                rec[w.sp + x * reps + r] = n ? make_int2(owner(a), owner(a + n - 1)) : make_int2(0, -1);
+            }
+        at = end;
+    }
+    __syncthreads();
+    if (lo >= hi) return;
+
+    if (warp == kConsumers) {
+        // ------------------------------------------------------- producer --
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+        const int ps_shift = p.c.page_shift, ps = 1 << ps_shift;
+        const int ppt = kTile >> ps_shift, batch = 32 / ppt;   // pages per tile, tiles looked up at once
+        const int mine = lane / ppt, sub = lane - mine * ppt;
+        const uint32_t page_bytes = (uint32_t)ps * (2u * D + 8u);
+        TileMsg *msgs = reinterpret_cast<TileMsg *>(smem + C::kMsg);
+        uint32_t it = 0;
+        long long left = hi - lo;
+        int seg = misc->start_seg, off = (int)misc->start_off;
+        bool ok = true;
+        while (ok && left > 0) {
+            const Seg s = segment(p, w, seg);
+            const int n = s.prefix ? p.prefix_len : seq_keys(p, s.b, false);
+            const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
+            ListRow r = {};
+            int nt = (n + kTile - 1) / kTile;
+            const bool listed = !s.prefix && p.has_lists;
+            if (listed) {
+                r = list_row(p, s.b, s.h, n, false);
+                nt = r.full + r.mask;
+            }
+            const int begin = off, m = (int)min((long long)(nt - off), left);
+            for (int i0 = 0; ok && i0 < m; i0 += batch) {
+                const int i = begin + i0 + mine;
+                int tile = -1, lim = 0, page = -1;
+                if (i0 + mine < m) {
+                    tile = i;
+                    if (listed) {
+                        const bool masked = i >= r.full;
+                        tile = __ldg((masked ? p.mask_idx + (i - r.full) : p.full_idx + i) + r.at);
+                        if (tile < 0 || tile >= r.nn) {
+                            if (sub == 0) raise(p, BSATTN_FLAG_BAD_INDEX);
+                            tile = -1;
+                        } else if (masked && p.vl) {
+                            lim = __ldg(p.vl + (long long)s.b * p.list_n + tile);
+                        } else {
+                            lim = kTile;
+                        }
+                    } else {
+                        lim = kTile;
+                    }
+                    if (tile >= 0) lim = min(min(lim, kTile), n - min(tile, (n + kTile - 1) / kTile) * kTile);
+                    if (tile >= 0 && (sub << ps_shift) < lim) {
+                        page = __ldg(table + ((tile * kTile + (sub << ps_shift)) >> ps_shift));
+                        if (page < 0 || page >= p.c.num_pages) {
+                            raise(p, BSATTN_FLAG_BAD_INDEX);
+                            page = -1;
+                        }
+                    }
+                }
+                for (int j = 0; j < batch && i0 + j < m; ++j, ++it) {
+                    const uint32_t st = it % C::kStages;
+                    ok = mbar_wait(bar(C::kStages + st), ((it / C::kStages) & 1u) ^ 1u, abort, p.err,
+                                   BSATTN_FLAG_TIMEOUT);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const bool load = mine == j && page >= 0;
+                    const uint32_t loads = __ballot_sync(0xffffffffu, load);
+                    const uint32_t groups = __reduce_or_sync(
+                        0xffffffffu, load ? ((1u << (ps >> 4)) - 1u) << (sub * (ps >> 4)) : 0u);
+                    const int tlim = __shfl_sync(0xffffffffu, lim, j * ppt);
+                    if (lane == 0) {
+                        uint32_t fl = 0u;
+                        if (i0 + j == m - 1) fl = kLast | (begin == 0 && m == nt ? kComplete : 0u);
+                        msgs[st] = TileMsg{seg, tlim, groups, fl};
+                        if (loads) mbar_arrive_expect_tx(bar(st), (uint32_t)__popc(loads) * page_bytes);
+                        else mbar_arrive(bar(st));
+                    }
+                    __syncwarp();
+                    if (load) {
+                        const int row = ((page * p.c.H + s.h) << ps_shift), in = sub << ps_shift;
+                        const uint32_t dst = base + st * C::kStageBytes + (uint32_t)in * D;
+                        const uint32_t sc = base + C::kScales + st * 1024u + 4u * (uint32_t)in;
+                        tma_load_2d(dst, &tk, bar(st), 0, row);
+                        tma_load_2d(dst + C::kCodes, &tv, bar(st), 0, row);
+                        bulk_g2s_lead(1u, sc, p.c.ks + row, 4u * (uint32_t)ps, bar(st));
+                        bulk_g2s_lead(1u, sc + 512u, p.c.vs + row, 4u * (uint32_t)ps, bar(st));
+                    }
+                }
+            }
+            left -= m;
+            ++seg;
+            off = 0;
+        }
+        if (ok) {
+            const uint32_t st = it % C::kStages;
+            ok = mbar_wait(bar(C::kStages + st), ((it / C::kStages) & 1u) ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
+            if (__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) {
+                    msgs[st] = TileMsg{-1, 0, 0u, 0u};
+                    mbar_arrive(bar(st));
+                }
+                ++it;
+            }
+        }
+        // no copy into this CTA's shared memory may be in flight when it ends
+        for (uint32_t s = 0; s < (uint32_t)C::kStages; ++s)
+            if (it > s) mbar_wait_drain(bar((int)((it - 1 - s) % C::kStages)), ((it - 1 - s) / C::kStages) & 1u);
+    } else {
+        Consumer<D, kInt8, kWide> c{p, w, smem, base, warp, lane, lane >> 2, lane & 3};
+        c.sync_phase = 0u;
+        c.run(abort);
+    }
+}
+
+// Joins the parts of one output row: out = sum_i o_i 2^(L_i - L), L = log2 sum_i 2^L_i.
+// One warp per row; a row that the first kernel finished is left alone.
+template <int D>
+__global__ void __launch_bounds__(128) bsattn_decode_join_kernel(const __grid_constant__ DecodeParams p,
+                                                                const __grid_constant__ Plan w) {
+    grid_dependency_wait();
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (long long)p.B * p.Hq) return;
+    const int b = (int)(row / p.Hq), hq = (int)(row - (long long)b * p.Hq), h = hq / p.G, gi = hq - h * p.G;
+    const int2 *rec = reinterpret_cast<const int2 *>(p.ws + w.rec);
+    const int2 rs = rec[w.sp + b * p.c.H + h];
+    int2 rp = make_int2(0, -1);
+    long long pre_row = 0;
+    if (w.sp) {
+        const int r = b * p.G + gi, sp = h * w.row_blocks + r / kRowBlock;
+        rp = rec[sp];
+        pre_row = (long long)(sp + rp.x) * w.rows_p + r % kRowBlock;
+    } else if (rs.x == rs.y) {
+        return;
+    }
+    const int np = rp.y - rp.x + 1, n = np + rs.y - rs.x + 1;
+    const long long suf_row = (long long)(b * p.c.H + h + rs.x) * p.G + gi;
+    const float *pre_o = reinterpret_cast<const float *>(p.ws + w.pre_o), *pre_l = reinterpret_cast<const float *>(p.ws + w.pre_l);
+    const float *suf_o = reinterpret_cast<const float *>(p.ws + w.suf_o), *suf_l = reinterpret_cast<const float *>(p.ws + w.suf_l);
+    auto at = [&](int i) -> long long { return i < np ? pre_row + (long long)i * w.rows_p : suf_row + (long long)(i - np) * p.G; };
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int i = lane; i < n; i += 32) {
+        const float x = (i < np ? pre_l : suf_l)[at(i)];
+        mx = fmaxf(mx, x);
+        nan |= x != x;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    nan = __any_sync(0xffffffffu, nan);
+    float o[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const long long r = at(i);
+        const float x = ex2_approx((i < np ? pre_l : suf_l)[r] - base);
+        const float *src = (i < np ? pre_o : suf_o) + r * D + lane * E;
+        l += x;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x, src[e], o[e]);
+    }
+    const bool empty = l == 0.f;
+    const float inv = empty ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        o[e] *= inv;
+        if (p.out_f32) static_cast<float *>(p.out)[row * D + lane * E + e] = o[e];
+    }
+    if (!p.out_f32) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + row * D + lane * E + e) = pack_bf16x2(o[e], o[e + 1]);
+    }
+    if (lane == 0)
+        p.lse[row] = nan ? __uint_as_float(0x7fc00000u)
+                         : empty ? -INFINITY : (base + lg2_approx(l)) * 0.69314718055994530942f;
+}
+
+template <int D, bool kInt8, bool kWide>
+cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
+                   cudaStream_t stream) {
+    using C = Cfg<D>;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        e = cudaFuncSetAttribute(bsattn_decode_kernel<D, kInt8, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::kAlloc);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    bsattn_decode_kernel<D, kInt8, kWide><<<grid, kThreads, C::kAlloc, stream>>>(p, w, tk, tv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.Hq + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D>, p, w);
+}
+
+template <int D, bool kInt8>
+cudaError_t launch_rows(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
+                        cudaStream_t stream) {
+    // 8 query rows fill one group of columns; more take the build with two
+    const int rows = w.sp ? w.rows_p : 0;
+    if (max(rows, p.G) <= 8) return launch<D, kInt8, false>(p, w, tk, tv, grid, stream);
+    return launch<D, kInt8, true>(p, w, tk, tv, grid, stream);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int, int, int, int, int) { return 256; }
+size_t decode_workspace_bytes(int B, int H, int G, int D, int prefix_len) {
+    return make_plan(B, H, G, D, prefix_len).total;
+}
 
 cudaError_t launch_decode(const DecodeParams &p, cudaStream_t stream) {
-    const dim3 g((unsigned)p.Hq, (unsigned)p.B);
-    if (p.c.D == 128) bsattn_decode_kernel<128><<<g, kWarps * 32, 0, stream>>>(p);
-    else bsattn_decode_kernel<64><<<g, kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    const Plan w = make_plan(p.B, p.c.H, p.G, p.c.D, p.prefix_len);
+    const int sms = current_device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+    CUtensorMap tk, tv;
+    const long long rows = ((long long)(p.c.num_pages > 0 ? p.c.num_pages : 1) * p.c.H) << p.c.page_shift;
+    if (!encode_code_rows(&tk, p.c.k, rows, p.c.D, 1 << p.c.page_shift) ||
+        !encode_code_rows(&tv, p.c.v, rows, p.c.D, 1 << p.c.page_shift))
+        return cudaErrorInvalidValue;
+    if (p.c.D == 128)
+        return p.c.int8 ? launch_rows<128, true>(p, w, tk, tv, grid, stream)
+                        : launch_rows<128, false>(p, w, tk, tv, grid, stream);
+    return p.c.int8 ? launch_rows<64, true>(p, w, tk, tv, grid, stream)
+                    : launch_rows<64, false>(p, w, tk, tv, grid, stream);
 }
 
 }  // namespace bsattn

@@ -188,6 +188,8 @@ size_t decode_workspace_bytes(int B, int H, int G, int D, int prefix_len);
 // Shared with the other entry points (bsattn_api.cu).
 bsattn_status check_meta_desc(const bsattn_meta *m);
 int current_device_sms();          // 0 on failure
+// Tensor map of [rows, D] codes, box_rows x D per copy (128- or 64-byte swizzle).
+bool encode_code_rows(CUtensorMap *map, const void *ptr, long long rows, int D, int box_rows);
 
 cudaError_t launch_meta(const MetaParams &p, cudaStream_t stream);
 cudaError_t launch_kv_summary(const void *k, const void *v, int B, int S, int H, int D, void *k_sum,

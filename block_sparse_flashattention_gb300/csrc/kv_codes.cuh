@@ -45,4 +45,20 @@ __device__ __forceinline__ void unpack_int8(uint32_t x, float (&y)[4]) {
     for (int i = 0; i < 4; ++i) y[i] = (float)(int8_t)(x >> (8 * i));
 }
 
+// Four codes as two fp16 pairs (codes 0, 1 and codes 2, 3); exact.  An int8 code c is
+// 1152 below the fp16 number whose bits are 0x6400 + (c + 128).
+template <bool kInt8>
+__device__ __forceinline__ void codes_to_f16x2(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    if constexpr (kInt8) {
+        const uint32_t u = x ^ 0x80808080u;
+        lo = __byte_perm(u, 0x64646464u, 0x4140);
+        hi = __byte_perm(u, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+    } else {
+        lo = e4m3x2_to_f16x2(x & 0xffffu);
+        hi = e4m3x2_to_f16x2(x >> 16);
+    }
+}
+
 }  // namespace bsattn

@@ -472,8 +472,8 @@ typedef struct {
  *   e4m3  scale = 2^max(-126, ceil(log2(a / 448))), code = x / scale rounded to
  *         nearest even: the scale is a power of two, so x / scale is exact, and the
  *         code carries the only rounding;
- *   int8  a' = max(a, 127 * 2^-126), scale = a' / 127, code = rint(x * (127 / a')),
- *         each operation rounded to fp32.
+ *   int8  a' = max(a, 127 * 2^-126), scale = a' * (1 / 127), code =
+ *         rint(x * (127 * (1 / a'))), each operation rounded to fp32.
  * A row that holds a NaN or an infinity gets the scale NaN and codes 0.
  *
  * k, v         device bf16, rows of [H, D] contiguous elements, k_stride / v_stride

@@ -3,7 +3,8 @@ numpy, in 64 bits, one row or one query at a time, written from the definitions.
 
 The formats: a row's e4m3 scale is 2^max(-126, ceil(log2(a / 448))) for its largest
 magnitude a, its code x / scale rounded to nearest even; an int8 row's scale is
-fl32(a' / 127) with a' = max(a, 127 * 2^-126), its code rint(fl32(x * fl32(127 / a'))).
+a' * (1 / 127) with a' = max(a, 127 * 2^-126), its code rint(x * (127 * (1 / a'))),
+where each operation is rounded to 32 bits.
 """
 from __future__ import annotations
 
@@ -51,8 +52,8 @@ def quantise(x: np.ndarray, dtype: str):
     else:
         f = np.float32
         a32 = np.maximum(a.astype(f), f(127) * f(2.0) ** f(-126))
-        scale = (a32 / f(127)).astype(np.float64)
-        codes = np.rint(x.astype(f) * (f(127) / a32)[..., None]).astype(np.float64)
+        scale = (a32 * (f(1) / f(127))).astype(np.float64)
+        codes = np.rint(x.astype(f) * (f(127) * (f(1) / a32))[..., None]).astype(np.float64)
     return codes, np.where(bad, np.nan, scale)
 
 

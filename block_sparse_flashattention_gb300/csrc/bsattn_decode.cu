@@ -18,8 +18,8 @@
 //
 // Work split.  A segment is one (sequence, KV head), or one (KV head, 128 query rows)
 // of the prefix; its keys are tiles of 128.  All tiles of all segments form one line,
-// cut into equal pieces, one per CTA (one CTA per SM): every SM reads the same number
-// of bytes whatever the lengths.  A segment that lies within one piece is finished
+// cut into equal pieces, one per CTA (one or two CTAs per SM): every SM reads the same
+// number of bytes whatever the lengths.  A segment that lies within one piece is finished
 // there; the parts of the others (fp32 output and LSE) go to the workspace and a second
 // kernel, a programmatic dependent of the first, joins them.
 //
@@ -45,10 +45,11 @@ namespace {
 
 constexpr int kConsumers = 8;                    // computing warps
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kMaxCtas = 256;                    // pieces the workspace has room for
+constexpr int kMaxCtas = 320;                    // pieces the workspace has room for
 constexpr int kRowBlock = 128;                   // query rows of a prefix segment
 
-constexpr uint32_t kLast = 1u, kComplete = 2u;   // TileMsg flags
+// TileMsg flags: a segment's first / last tile in this CTA, its whole line lies here.
+constexpr uint32_t kFirst = 1u, kLast = 2u, kComplete = 4u;
 
 // What the producer tells the computing warps about a stage.
 struct TileMsg {
@@ -58,22 +59,31 @@ struct TileMsg {
     uint32_t flags;
 };
 
-template <int D>
+template <int D, bool kWide>
 struct Cfg {
-    // 5 x 33 KB or 8 x 17 KB in flight; what HBM needs at 6.7 TB/s and ~1 us is 44 KB per SM
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kCtas = kWide ? 1 : 2;                  // per SM
+    // 4 x 33 KB or 8 x 17 KB in flight per SM; what HBM needs at 6.7 TB/s and ~1 us is 44 KB
+    static constexpr int kStages = (D == 128 ? 4 : 8) / kCtas;
+    static constexpr int kQRows = kWide ? 16 : 8;                // query rows that come with a segment's first tile
     static constexpr uint32_t kCodes = 128u * D;                 // K or V codes of a tile
     static constexpr uint32_t kStageBytes = 2u * kCodes;
     static constexpr uint32_t kScales = kStages * kStageBytes;   // per stage 128 K scales, 128 V scales
-    static constexpr uint32_t kRed = kScales + kStages * 1024u;  // join: 4 warps x (D / 2) x 32 lanes fp32
-    static constexpr uint32_t kStat = kRed + 4u * (D / 2) * 128u;  // [8 warps][16 rows] m, u, l
-    static constexpr uint32_t kMsg = kStat + kConsumers * 16u * 12u;
+    static constexpr uint32_t kQ = kScales + kStages * 1024u;    // per stage kQRows query rows
+    static constexpr uint32_t kQBytes = kQRows * D * 2u;
+    static constexpr uint32_t kRed = kQ + kStages * kQBytes;     // join: 8 warps x (D / 2) x 32 lanes fp32
+    static constexpr uint32_t kRedBytes = kConsumers * (kWide ? D / 2 : D / 4) * 128u;
+    static constexpr uint32_t kStat = kRed + kRedBytes;          // [8 x 16 rows] (m, u, l, -)
+    static constexpr uint32_t kMsg = kStat + kConsumers * 16u * 16u;
     static constexpr uint32_t kBar = kMsg + kStages * (uint32_t)sizeof(TileMsg);
     static constexpr uint32_t kMisc = kBar + (2u * kStages + 1u) * 8u;  // abort flag, start, scan
     static constexpr uint32_t kBytes = kMisc + 128u;
     static constexpr uint32_t kAlloc = kBytes + 1024u;           // slack for 1024-byte alignment
-    static_assert(kAlloc <= 227u * 1024u, "shared memory");
+    static_assert(kCtas * (kAlloc + 1024u) <= 228u * 1024u, "shared memory");
 };
+
+// References before the first key: far below any score, yet finite, so that a difference
+// with it is never NaN.
+constexpr float kNoKey = -0x1p100f;
 
 struct Misc {
     int32_t abort, start_seg;
@@ -136,6 +146,10 @@ __device__ __forceinline__ Seg segment(const DecodeParams &p, const Plan &w, int
     }
     return s;
 }
+
+// Whether a segment's query rows are copied with its first tile (few whole sequences').
+template <class C>
+__device__ __forceinline__ bool rows_come_along(const Seg &s) { return s.rows <= C::kQRows && s.row0 == 0; }
 
 __device__ __forceinline__ void raise(const DecodeParams &p, int bit) {
     if (p.err) atomicOr(p.err, bit);
@@ -215,14 +229,14 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
 
 // Where a finished row goes: the call's output, or a part in the workspace.
 struct RowOut {
-    bool direct;
-    long long row;   // output row (direct), or row of the part arrays
+    int kind;        // 0 the output, 1 a prefix part, 2 a part of a sequence's own keys
+    long long row;
 };
 
 // The computing warps.
 template <int D, bool kInt8, bool kWide>
 struct Consumer {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWide>;
     static constexpr int kSteps = D / 16;   // k-steps of Q K^T, row tiles of V^T
     static constexpr int kCols = kWide ? 2 : 1;  // groups of 8 query rows
     const DecodeParams &p;
@@ -257,7 +271,8 @@ struct Consumer {
         return p.q + (long long)b * p.q_stride + (long long)(s.h * p.G + gi) * D;
     }
 
-    __device__ __forceinline__ void begin(const Seg &s) {
+    // Starts a segment; its query rows came with the stage (sq) when they are few.
+    __device__ __forceinline__ void begin(const Seg &s, const uint8_t *sq) {
         const int tiles = (s.rows + 15) / 16;
         const int R = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
         row_tile = warp % R;
@@ -270,7 +285,9 @@ struct Consumer {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint4 y = make_uint4(0, 0, 0, 0);
-                if (r < s.rows) y = __ldg(reinterpret_cast<const uint4 *>(query(s, r) + t * (D / 4)) + i);
+                if (r < s.rows)
+                    y = rows_come_along<C>(s) ? *(reinterpret_cast<const uint4 *>(sq + r * (2 * D) + t * (D / 2)) + i)
+                                         : __ldg(reinterpret_cast<const uint4 *>(query(s, r) + t * (D / 4)) + i);
                 x[4 * i] = y.x;
                 x[4 * i + 1] = y.y;
                 x[4 * i + 2] = y.z;
@@ -285,7 +302,8 @@ struct Consumer {
             // biased exponent of the largest element; zero rows and rows that are not finite stay as they are
             const int e = (a == 0 || a >= 0x7f80u) ? 127 : min(max((int)(a >> 7), 1), 253);
             const float f = __uint_as_float((uint32_t)(254 - e) << 23);
-            qs[hf] = p.scale_log2 * __uint_as_float((uint32_t)e << 23);
+            // above 0: a masked key's score, -inf, stays -inf
+            qs[hf] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)e << 23), 0x1p-126f);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 const uint32_t y = pack_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
@@ -293,7 +311,7 @@ struct Consumer {
                 if constexpr (kWide) q[i / 2][2 * (i & 1) + hf] = y;
                 else q[i / 2][i & 1] = y;
             }
-            m[hf] = u[hf] = -INFINITY;
+            m[hf] = u[hf] = kNoKey;
             l[hf] = 0.f;
         }
 #pragma unroll
@@ -304,7 +322,8 @@ struct Consumer {
                 for (int x = 0; x < 4; ++x) o[i][n][x] = 0.f;
     }
 
-    // 16 keys of a stage (group c), the first nv of which count.
+    // 16 keys of a stage (group c), the first nv of which count (all of them: kFull).
+    template <bool kFull>
     __device__ __forceinline__ void keys16(uint32_t sk, uint32_t ssc, int c, int nv) {
         const uint32_t sv = sk + C::kCodes;
         float s[2][4];
@@ -348,54 +367,68 @@ struct Consumer {
                 v[i][0] = y.x;
                 v[i][1] = y.y;
             }
-            if (nv < 16 && j >= nv) {  // what lies behind the last key may be NaN codes
+            if (!kFull && j >= nv) {  // what lies behind the last key may be NaN codes
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) v[i][x] = 0u;
             }
         }
-        // scores (in units of log2) and scores with the value scale in the exponent
-        float z[kCols][4], zu[kCols][4];
-        float zm[kCols], um[kCols];
-#pragma unroll
-        for (int hf = 0; hf < kCols; ++hf) zm[hf] = um[hf] = -INFINITY;
+        // x = z - m and y = z + log2 vs - u + 7 of this lane's keys 2t, 2t + 1, 2t + 8, 2t + 9
+        float sc[kCols][4], lv[4], x[kCols][4], y[kCols][4];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
             const uint2 kb = lds64(ssc + 4u * (16 * c + 8 * nb + 2 * t));
             const uint2 vb = lds64(ssc + 512u + 4u * (16 * c + 8 * nb + 2 * t));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float ks = __uint_as_float(e ? kb.y : kb.x);
-                const float lv = lg2_approx(__uint_as_float(e ? vb.y : vb.x));
-                const bool on = nv >= 16 || 8 * nb + 2 * t + e < nv;
+                const bool on = kFull || 8 * nb + 2 * t + e < nv;
+                lv[2 * nb + e] = lg2_approx(__uint_as_float(e ? vb.y : vb.x));
+                if (!on) lv[2 * nb + e] = -INFINITY;
 #pragma unroll
                 for (int hf = 0; hf < kCols; ++hf) {
-                    const float x = s[nb][2 * hf + e] * ks * qs[hf];
-                    z[hf][2 * nb + e] = on ? x : -INFINITY;
-                    zu[hf][2 * nb + e] = on ? x + lv : -INFINITY;
-                    zm[hf] = fmaxf(zm[hf], z[hf][2 * nb + e]);
-                    um[hf] = fmaxf(um[hf], zu[hf][2 * nb + e]);
+                    sc[hf][2 * nb + e] = s[nb][2 * hf + e] * __uint_as_float(e ? kb.y : kb.x);
+                    if (!on) sc[hf][2 * nb + e] = -INFINITY;
                 }
             }
         }
-        // The references move only when some key is 2^8 above them: l and O stay finite
-        // (weights reach 2^15 in fp16), and the quotient is the same.
+        float top[kCols];
+        auto relative = [&](int hf) {
+            const float mu = m[hf] - u[hf] + 7.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[hf][i] = fmaf(sc[hf][i], qs[hf], -m[hf]);
+                y[hf][i] = x[hf][i] + (lv[i] + mu);
+            }
+            top[hf] = fmaxf(fmax3(x[hf][0], x[hf][1], x[hf][2]), x[hf][3]);
+            top[hf] = fmaxf(top[hf], fmaxf(fmax3(y[hf][0], y[hf][1], y[hf][2]), y[hf][3]) - 7.f);
+        };
         bool grow = false;
 #pragma unroll
-        for (int hf = 0; hf < kCols; ++hf) grow |= zm[hf] > m[hf] + 8.f || um[hf] > u[hf] + 8.f;
+        for (int hf = 0; hf < kCols; ++hf) {
+            relative(hf);
+            grow |= top[hf] > 8.f;
+        }
+        // The references move only when some key is 2^8 above them: l and O stay finite
+        // (weights reach 2^15 in fp16), and the quotient is the same.
         if (__any_sync(0xffffffffu, grow)) {
             float ao[kCols];
 #pragma unroll
             for (int hf = 0; hf < kCols; ++hf) {
-                float a = fmaxf(zm[hf], __shfl_xor_sync(0xffffffffu, zm[hf], 1));
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                float b = fmaxf(um[hf], __shfl_xor_sync(0xffffffffu, um[hf], 1));
-                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2));
-                a = fmaxf(a, m[hf]);
-                b = fmaxf(b, u[hf]);
-                l[hf] *= a == -INFINITY ? 1.f : ex2_approx(m[hf] - a);
-                ao[hf] = b == -INFINITY ? 1.f : ex2_approx(u[hf] - b);
+                float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float z = sc[hf][i] * qs[hf];
+                    a = fmaxf(a, z);
+                    b = fmaxf(b, z + lv[i]);
+                }
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 1));
+                a = fmaxf(m[hf], fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2)));
+                b = fmaxf(u[hf], fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 2)));
+                l[hf] *= ex2_approx(m[hf] - a);
+                ao[hf] = ex2_approx(u[hf] - b);
                 m[hf] = a;
                 u[hf] = b;
+                relative(hf);
             }
             // O's columns are query rows 2t, 2t + 1 (and 8 above)
 #pragma unroll
@@ -414,146 +447,106 @@ struct Consumer {
         uint32_t pb[kCols][2];
 #pragma unroll
         for (int hf = 0; hf < kCols; ++hf) {
-            const float nm = m[hf] == -INFINITY ? 0.f : -m[hf];
-            const float nu = (u[hf] == -INFINITY ? 0.f : -u[hf]) + 7.f;
-            l[hf] += (ex2_approx(z[hf][0] + nm) + ex2_approx(z[hf][1] + nm)) +
-                     (ex2_approx(z[hf][2] + nm) + ex2_approx(z[hf][3] + nm));
-            pb[hf][0] = pack_f16x2(ex2_approx(zu[hf][0] + nu), ex2_approx(zu[hf][1] + nu));
-            pb[hf][1] = pack_f16x2(ex2_approx(zu[hf][2] + nu), ex2_approx(zu[hf][3] + nu));
+            l[hf] += (ex2_approx(x[hf][0]) + ex2_approx(x[hf][1])) + (ex2_approx(x[hf][2]) + ex2_approx(x[hf][3]));
+            pb[hf][0] = pack_f16x2(ex2_approx(y[hf][0]), ex2_approx(y[hf][1]));
+            pb[hf][1] = pack_f16x2(ex2_approx(y[hf][2]), ex2_approx(y[hf][3]));
         }
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
+        for (int w = 0; w < D / 32; ++w) {
             // bytes d, d + 1 of both keys of a pair side by side, then bytes d + 2, d + 3
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
                 const uint32_t sel = hi ? 0x7362u : 0x5140u;
                 uint32_t a0, a1, a2, a3;
-                codes_to_f16x2<kInt8>(__byte_perm(v[0][x], v[1][x], sel), a0, a1);
-                codes_to_f16x2<kInt8>(__byte_perm(v[2][x], v[3][x], sel), a2, a3);
+                codes_to_f16x2<kInt8>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
+                codes_to_f16x2<kInt8>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
 #pragma unroll
-                for (int n = 0; n < kCols; ++n) mma_f16(o[2 * x + hi][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                for (int n = 0; n < kCols; ++n) mma_f16(o[2 * w + hi][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
             }
         }
     }
 
-    // Joins the key groups of each row tile and writes the rows.
+    // Joins the key groups of each row tile and writes the rows: every warp leaves its
+    // sums and references in shared memory, all meet, and the warps of a row tile share
+    // out its columns; they meet again before the next segment's sums are left there.
     __device__ __forceinline__ bool finish(const Seg &s, int seg, bool complete, volatile int *abort) {
-        float *stat = reinterpret_cast<float *>(smem + C::kStat);  // [warp][row][m, u, l]
+        float4 *stat = reinterpret_cast<float4 *>(smem + C::kStat);
         float *red = reinterpret_cast<float *>(smem + C::kRed);
+        constexpr int kRegs = kSteps * kCols * 4;
 #pragma unroll
         for (int hf = 0; hf < kCols; ++hf) {
             l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
             l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-            if (t == 0) {
-                float *x = stat + (warp * 16 + g + 8 * hf) * 3;
-                x[0] = m[hf];
-                x[1] = u[hf];
-                x[2] = l[hf];
-            }
+            if (t == 0)
+                stat[(row_tile * 16 + g + 8 * hf) * key_groups + key_group] = make_float4(m[hf], u[hf], l[hf], 0.f);
+        }
+        {
+            float *x = red + warp * kRegs * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int n = 0; n < kCols; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[((i * kCols + n) * 4 + e) * 32] = o[i][n][e];
         }
         if (!meet(abort)) return false;
         const int R = kConsumers / key_groups;
-        // factors of this lane's output rows 2t, 2t + 1 (+ 8): own sums to the joint references
-        float inv[kCols][2], lse2[kCols][2];
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * n + 2 * t + e;
-                float mm = -INFINITY, uu = -INFINITY, ll = 0.f;
+                const int r = 8 * n + 2 * t + e;  // a row of this lane's columns
+                const float4 *st = stat + (row_tile * 16 + r) * key_groups;
+                float bm = kNoKey, bu = kNoKey, ll = 0.f;
                 for (int k = 0; k < key_groups; ++k) {
-                    const float *x = stat + ((k * R + row_tile) * 16 + r) * 3;
-                    mm = fmaxf(mm, x[0]);
-                    uu = fmaxf(uu, x[1]);
+                    bm = fmaxf(bm, st[k].x);
+                    bu = fmaxf(bu, st[k].y);
                 }
-                const float bm = mm == -INFINITY ? 0.f : mm, bu = uu == -INFINITY ? 0.f : uu;
-                for (int k = 0; k < key_groups; ++k) {
-                    const float *x = stat + ((k * R + row_tile) * 16 + r) * 3;
-                    ll += x[2] * ex2_approx(x[0] - bm);
-                }
-                const float own = ex2_approx(stat[(warp * 16 + r) * 3 + 1] - bu);
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    o[i][n][e] *= own;
-                    o[i][n][2 + e] *= own;
-                }
+                for (int k = 0; k < key_groups; ++k) ll += st[k].z * ex2_approx(st[k].x - bm);
                 const bool empty = ll == 0.f;
                 // no key with a value scale above 0: O is 0, whatever the quotient of the references
-                inv[n][e] = empty || uu == -INFINITY ? 0.f : ex2_approx(bu - bm - 7.f) / ll;
-                lse2[n][e] = empty ? -INFINITY : bm + lg2_approx(ll);
-            }
-        for (int step = key_groups >> 1; step > 0; step >>= 1) {
-            if (key_group >= step && key_group < 2 * step) {
-                float *x = red + (size_t)(warp - step * R) * (D / 2) * 32 + lane;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                    for (int n = 0; n < kCols; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[((i * kCols + n) * 4 + e) * 32] = o[i][n][e];
-            }
-            if (!meet(abort)) return false;
-            if (key_group < step) {
-                const float *x = red + (size_t)warp * (D / 2) * 32 + lane;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                    for (int n = 0; n < kCols; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][n][e] += x[((i * kCols + n) * 4 + e) * 32];
-            }
-            if (!meet(abort)) return false;
-        }
-        if (key_group == 0) {
-            // lane: D / 8 consecutive elements d = (D / 8) g .. of its rows
-#pragma unroll
-            for (int n = 0; n < kCols; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = row_tile * 16 + 8 * n + 2 * t + e;
-                    if (r >= s.rows) continue;
-                    float y[D / 8];
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        y[2 * i] = o[i][n][e] * inv[n][e];
-                        y[2 * i + 1] = o[i][n][2 + e] * inv[n][e];
+                const float inv = empty || bu == kNoKey ? 0.f : ex2_approx(bu - bm - 7.f) / ll;
+                const float lse2 = empty ? -INFINITY : bm + lg2_approx(ll);
+                if (row_tile * 16 + r < s.rows) {
+                    const RowOut at = row_out(s, seg, complete, row_tile * 16 + r);
+                    for (int i = key_group; i < kSteps; i += key_groups) {
+                        float y0 = 0.f, y1 = 0.f;
+                        for (int k = 0; k < key_groups; ++k) {
+                            const float f = ex2_approx(st[k].y - bu);
+                            const float *x = red + (k * R + row_tile) * kRegs * 32 + ((i * kCols + n) * 4 + e) * 32 + lane;
+                            y0 = fmaf(f, x[0], y0);
+                            y1 = fmaf(f, x[64], y1);
+                        }
+                        store_pair(at, g * (D / 8) + 2 * i, y0 * inv, y1 * inv);
                     }
-                    store_row(s, seg, complete, r, y, lse2[n][e]);
+                    if (key_group == 0 && g == 0) store_lse(at, lse2);
                 }
-        }
-        // the next segment's sums may overwrite `stat` only when every warp has read it
-        return key_groups > 1 || meet(abort);
+            }
+        return meet(abort);
     }
 
-    __device__ __forceinline__ void store_row(const Seg &s, int seg, bool complete, int r, const float (&y)[D / 8],
-                                              float lse2) {
-        if (!s.prefix && complete && w.sp == 0) {
-            const long long row = (long long)s.b * p.Hq + s.h * p.G + r;
-            if (p.out_f32) {
-                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D + g * (D / 8));
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * D + g * (D / 8));
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i)
-                    dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                        pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
-            }
-            if (g == 0) p.lse[row] = lse2 * 0.69314718055994530942f;
+    __device__ __forceinline__ RowOut row_out(const Seg &s, int seg, bool complete, int r) const {
+        if (!s.prefix && complete && w.sp == 0) return RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
+        const long long part = (seg - (s.prefix ? 0 : w.sp)) + (long long)blockIdx.x;
+        return s.prefix ? RowOut{1, part * w.rows_p + r} : RowOut{2, part * p.G + r};
+    }
+
+    __device__ __forceinline__ void store_pair(const RowOut &at, int d, float x, float y) const {
+        if (at.kind == 0 && !p.out_f32) {
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at.row * D + d) = pack_bf16x2(x, y);
         } else {
-            const long long part = (seg - (s.prefix ? 0 : w.sp)) + (long long)blockIdx.x;
-            const long long row = s.prefix ? part * w.rows_p + r : part * p.G + r;
-            float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p.ws + (s.prefix ? w.pre_o : w.suf_o)) +
-                                                     row * D + g * (D / 8));
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            if (g == 0) reinterpret_cast<float *>(p.ws + (s.prefix ? w.pre_l : w.suf_l))[row] = lse2;
+            float *o = at.kind == 0 ? static_cast<float *>(p.out)
+                                    : reinterpret_cast<float *>(p.ws + (at.kind == 1 ? w.pre_o : w.suf_o));
+            *reinterpret_cast<float2 *>(o + at.row * D + d) = make_float2(x, y);
         }
+    }
+
+    __device__ __forceinline__ void store_lse(const RowOut &at, float lse2) const {
+        if (at.kind == 0) p.lse[at.row] = lse2 * 0.69314718055994530942f;
+        else reinterpret_cast<float *>(p.ws + (at.kind == 1 ? w.pre_l : w.suf_l))[at.row] = lse2;
     }
 
     __device__ __forceinline__ void run(volatile int *abort) {
-        int cur = -1;
         Seg s = {};
         for (uint32_t it = 0;; ++it) {
             const uint32_t st = it % C::kStages;
@@ -561,30 +554,31 @@ struct Consumer {
             if (!__all_sync(0xffffffffu, ok)) return;
             const TileMsg msg = reinterpret_cast<const TileMsg *>(smem + C::kMsg)[st];
             if (msg.seg < 0) return;
-            if (msg.seg != cur) {
-                cur = msg.seg;
-                s = segment(p, w, cur);
-                begin(s);
+            if (msg.flags & kFirst) {
+                s = segment(p, w, msg.seg);
+                begin(s, smem + C::kQ + st * C::kQBytes);
             }
             const uint32_t sk = base + st * C::kStageBytes, ssc = base + C::kScales + st * 1024u;
             for (int c = key_group; c < 8; c += key_groups) {
                 const int nv = min(16, msg.lim - 16 * c);
-                if (nv > 0 && ((msg.groups >> c) & 1u)) keys16(sk, ssc, c, nv);
+                if (nv <= 0 || !((msg.groups >> c) & 1u)) continue;
+                if (nv == 16) keys16<true>(sk, ssc, c, nv);
+                else keys16<false>(sk, ssc, c, nv);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kStages + st));
             if (msg.flags & kLast) {
-                if (!finish(s, cur, (msg.flags & kComplete) != 0, abort)) return;
+                if (!finish(s, msg.seg, (msg.flags & kComplete) != 0, abort)) return;
             }
         }
     }
 };
 
 template <int D, bool kInt8, bool kWide>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Cfg<D, kWide>::kCtas)
     bsattn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWide>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -673,50 +667,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t page_bytes = (uint32_t)ps * (2u * D + 8u);
         TileMsg *msgs = reinterpret_cast<TileMsg *>(smem + C::kMsg);
         uint32_t it = 0;
-        long long left = hi - lo;
-        int seg = misc->start_seg, off = (int)misc->start_off;
         bool ok = true;
-        while (ok && left > 0) {
-            const Seg s = segment(p, w, seg);
-            const int n = s.prefix ? p.prefix_len : seq_keys(p, s.b, false);
-            const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
+        // A window of 32 segments, one per lane; x counts tiles from the window's first.
+        int seg0 = misc->start_seg;
+        long long x = misc->start_off, pos = lo;
+        while (ok && pos < hi) {
+            const int ws = seg0 + lane;
+            int n = 0, nt = 0;
             ListRow r = {};
-            int nt = (n + kTile - 1) / kTile;
-            const bool listed = !s.prefix && p.has_lists;
-            if (listed) {
-                r = list_row(p, s.b, s.h, n, false);
-                nt = r.full + r.mask;
+            if (ws < w.sp) {
+                n = p.prefix_len;
+                nt = nt_pre;
+            } else if (ws < w.sp + w.ss) {
+                const int b = (ws - w.sp) / p.c.H;
+                n = seq_keys(p, b, false);
+                nt = (n + kTile - 1) / kTile;
+                if (p.has_lists) {
+                    r = list_row(p, b, ws - w.sp - b * p.c.H, n, false);
+                    nt = r.full + r.mask;
+                }
             }
-            const int begin = off, m = (int)min((long long)(nt - off), left);
-            for (int i0 = 0; ok && i0 < m; i0 += batch) {
-                const int i = begin + i0 + mine;
-                int tile = -1, lim = 0, page = -1;
-                if (i0 + mine < m) {
-                    tile = i;
-                    if (listed) {
-                        const bool masked = i >= r.full;
-                        tile = __ldg((masked ? p.mask_idx + (i - r.full) : p.full_idx + i) + r.at);
-                        if (tile < 0 || tile >= r.nn) {
-                            if (sub == 0) raise(p, BSATTN_FLAG_BAD_INDEX);
-                            tile = -1;
-                        } else if (masked && p.vl) {
-                            lim = __ldg(p.vl + (long long)s.b * p.list_n + tile);
-                        } else {
-                            lim = kTile;
-                        }
-                    } else {
-                        lim = kTile;
-                    }
-                    if (tile >= 0) lim = min(min(lim, kTile), n - min(tile, (n + kTile - 1) / kTile) * kTile);
-                    if (tile >= 0 && (sub << ps_shift) < lim) {
-                        page = __ldg(table + ((tile * kTile + (sub << ps_shift)) >> ps_shift));
-                        if (page < 0 || page >= p.c.num_pages) {
-                            raise(p, BSATTN_FLAG_BAD_INDEX);
-                            page = -1;
-                        }
+            int incl = nt;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += y;
+            }
+            const int in_window = __shfl_sync(0xffffffffu, incl, 31);
+            const int end = (int)min((long long)in_window, x + (hi - pos));
+            for (int x0 = (int)x; ok && x0 < end; x0 += batch) {
+                // lane: page `sub` of tile x0 + mine; the segment is the first whose end lies behind it
+                const int xt = min(x0 + mine, end - 1);
+                int at = 0;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    if (__shfl_sync(0xffffffffu, incl, at + d - 1) <= xt) at += d;
+                const int seg = seg0 + at;
+                const int sn = __shfl_sync(0xffffffffu, n, at), snt = __shfl_sync(0xffffffffu, nt, at);
+                const int start = __shfl_sync(0xffffffffu, incl, at) - snt, i = xt - start;
+                const int full = __shfl_sync(0xffffffffu, r.full, at), nn = __shfl_sync(0xffffffffu, r.nn, at);
+                const long long list_at = __shfl_sync(0xffffffffu, r.at, at);
+                const Seg s = segment(p, w, seg);
+                int tile = i, lim = kTile, page = -1;
+                if (p.has_lists && !s.prefix) {
+                    const bool masked = i >= full;
+                    tile = __ldg((masked ? p.mask_idx + (i - full) : p.full_idx + i) + list_at);
+                    if (tile < 0 || tile >= nn) {
+                        if (sub == 0) raise(p, BSATTN_FLAG_BAD_INDEX);
+                        tile = -1;
+                    } else if (masked && p.vl) {
+                        lim = min(kTile, __ldg(p.vl + (long long)s.b * p.list_n + tile));
                     }
                 }
-                for (int j = 0; j < batch && i0 + j < m; ++j, ++it) {
+                lim = tile < 0 || tile * (long long)kTile >= sn ? 0 : min(lim, sn - tile * kTile);
+                if ((sub << ps_shift) < lim) {
+                    const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
+                    page = __ldg(table + ((tile * kTile) >> ps_shift) + sub);
+                    if (page < 0 || page >= p.c.num_pages) {
+                        raise(p, BSATTN_FLAG_BAD_INDEX);
+                        page = -1;
+                    }
+                }
+                // the CTA's piece begins at x (of this window) and ends hi - pos tiles behind it
+                uint32_t fl = xt == max(start, (int)x) ? kFirst : 0u;
+                if (i == snt - 1 || xt + 1 == x + (hi - pos)) fl |= kLast;
+                if (start >= (int)x && i == snt - 1) fl |= kComplete;
+                const bool q_rows = (fl & kFirst) && rows_come_along<C>(s);
+                for (int j = 0; j < batch && x0 + j < end; ++j, ++it) {
                     const uint32_t st = it % C::kStages;
                     ok = mbar_wait(bar(C::kStages + st), ((it / C::kStages) & 1u) ^ 1u, abort, p.err,
                                    BSATTN_FLAG_TIMEOUT);
@@ -725,13 +742,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t loads = __ballot_sync(0xffffffffu, load);
                     const uint32_t groups = __reduce_or_sync(
                         0xffffffffu, load ? ((1u << (ps >> 4)) - 1u) << (sub * (ps >> 4)) : 0u);
-                    const int tlim = __shfl_sync(0xffffffffu, lim, j * ppt);
-                    if (lane == 0) {
-                        uint32_t fl = 0u;
-                        if (i0 + j == m - 1) fl = kLast | (begin == 0 && m == nt ? kComplete : 0u);
-                        msgs[st] = TileMsg{seg, tlim, groups, fl};
-                        if (loads) mbar_arrive_expect_tx(bar(st), (uint32_t)__popc(loads) * page_bytes);
+                    if (mine == j && sub == 0) {
+                        msgs[st] = TileMsg{seg, lim, groups, fl};
+                        const uint32_t bytes = (uint32_t)__popc(loads) * page_bytes + (q_rows ? s.rows * 2u * D : 0u);
+                        if (bytes) mbar_arrive_expect_tx(bar(st), bytes);
                         else mbar_arrive(bar(st));
+                        if (q_rows) {
+                            const uint32_t dst = base + C::kQ + st * C::kQBytes;
+                            const int seqs = s.prefix ? s.rows / p.G : 1;
+                            for (int b = 0; b < seqs; ++b)
+                                bulk_g2s_lead(1u, dst + (uint32_t)b * p.G * 2u * D,
+                                              p.q + (long long)(s.b + b) * p.q_stride + (long long)s.h * p.G * D,
+                                              (uint32_t)p.G * 2u * D, bar(st));
+                        }
                     }
                     __syncwarp();
                     if (load) {
@@ -745,9 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            left -= m;
-            ++seg;
-            off = 0;
+            pos += end - x;
+            x = 0;
+            seg0 += 32;
         }
         if (ok) {
             const uint32_t st = it % C::kStages;
@@ -838,9 +861,9 @@ __global__ void __launch_bounds__(128) bsattn_decode_join_kernel(const __grid_co
 }
 
 template <int D, bool kInt8, bool kWide>
-cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
+cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int sms,
                    cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWide>;
     static int attr_set_for_device[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -852,6 +875,7 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, 
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
+    const int grid = min(sms * C::kCtas, kMaxCtas);
     bsattn_decode_kernel<D, kInt8, kWide><<<grid, kThreads, C::kAlloc, stream>>>(p, w, tk, tv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -867,12 +891,12 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, 
 }
 
 template <int D, bool kInt8>
-cudaError_t launch_rows(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
+cudaError_t launch_rows(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int sms,
                         cudaStream_t stream) {
     // 8 query rows fill one group of columns; more take the build with two
     const int rows = w.sp ? w.rows_p : 0;
-    if (max(rows, p.G) <= 8) return launch<D, kInt8, false>(p, w, tk, tv, grid, stream);
-    return launch<D, kInt8, true>(p, w, tk, tv, grid, stream);
+    if (max(rows, p.G) <= 8) return launch<D, kInt8, false>(p, w, tk, tv, sms, stream);
+    return launch<D, kInt8, true>(p, w, tk, tv, sms, stream);
 }
 
 }  // namespace
@@ -885,17 +909,16 @@ cudaError_t launch_decode(const DecodeParams &p, cudaStream_t stream) {
     const Plan w = make_plan(p.B, p.c.H, p.G, p.c.D, p.prefix_len);
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     CUtensorMap tk, tv;
     const long long rows = ((long long)(p.c.num_pages > 0 ? p.c.num_pages : 1) * p.c.H) << p.c.page_shift;
     if (!encode_code_rows(&tk, p.c.k, rows, p.c.D, 1 << p.c.page_shift) ||
         !encode_code_rows(&tv, p.c.v, rows, p.c.D, 1 << p.c.page_shift))
         return cudaErrorInvalidValue;
     if (p.c.D == 128)
-        return p.c.int8 ? launch_rows<128, true>(p, w, tk, tv, grid, stream)
-                        : launch_rows<128, false>(p, w, tk, tv, grid, stream);
-    return p.c.int8 ? launch_rows<64, true>(p, w, tk, tv, grid, stream)
-                    : launch_rows<64, false>(p, w, tk, tv, grid, stream);
+        return p.c.int8 ? launch_rows<128, true>(p, w, tk, tv, sms, stream)
+                        : launch_rows<128, false>(p, w, tk, tv, sms, stream);
+    return p.c.int8 ? launch_rows<64, true>(p, w, tk, tv, sms, stream)
+                    : launch_rows<64, false>(p, w, tk, tv, sms, stream);
 }
 
 }  // namespace bsattn

@@ -20,14 +20,29 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import (BSATTN_OK, KV_E4M3, KV_INT8, OUT_BF16, OUT_F32, BsattnError, bsattn_decode,
-                       bsattn_decode_shared_prefix, bsattn_decode_workspace_size, bsattn_kv_append,
-                       bsattn_kv_cache, bsattn_kv_read)
+from ._binding import (BSATTN_OK, KV_E4M3, KV_INT8, OUT_BF16, OUT_F32, BsattnError, bsattn_decode_workspace_size,
+                       bsattn_kv_cache, library)
 
 
 def _check(status: int, where: str) -> None:
     if status != BSATTN_OK:
         raise BsattnError(status, where)
+
+
+# Bound by the first KVCache, so that importing the package does not import torch.
+torch = BF16 = F32 = I32 = _lib = _raw_stream = _current_device = None
+
+
+def _bind() -> None:
+    global torch, BF16, F32, I32, _lib, _raw_stream, _current_device
+    import torch as t
+    BF16, F32, I32 = t.bfloat16, t.float32, t.int32
+    # The current stream's handle: the raw form saves the stream object that the public
+    # call makes (2.9 us of a decode call's host time).
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    _lib = library()
+    torch = t
 
 
 class KVCache:
@@ -36,10 +51,12 @@ class KVCache:
     k, v: torch.float8_e4m3fn or torch.int8 [num_pages, H, page_size, D];
     k_scale, v_scale: float32 [num_pages, H, page_size]; contiguous, one device."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "H", "page_size", "D", "dtype", "device", "c", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "H", "page_size", "D", "dtype", "device", "index", "c", "ref",
+                 "scale")
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
+        if torch is None:
+            _bind()
         if k.dtype not in (torch.float8_e4m3fn, torch.int8) or v.dtype != k.dtype:
             raise ValueError("k and v must both be torch.float8_e4m3fn or torch.int8")
         if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
@@ -53,7 +70,8 @@ class KVCache:
                 raise ValueError("the cache's tensors must be contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.H, self.page_size, self.D = k.shape
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()   # -1: not on a GPU
+        self.scale = 1.0 / math.sqrt(max(self.D, 1))
         self.c = bsattn_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                  self.num_pages, self.page_size, self.H, self.D,
                                  KV_INT8 if k.dtype == torch.int8 else KV_E4M3)
@@ -62,7 +80,8 @@ class KVCache:
 
 def alloc_kv_cache(num_pages: int, H: int, D: int, *, page_size: int = 128, dtype=None, device="cuda") -> KVCache:
     """A cache of num_pages pages, zero-filled; dtype torch.float8_e4m3fn (default) or torch.int8."""
-    import torch
+    if torch is None:
+        _bind()
     dtype = torch.float8_e4m3fn if dtype is None else dtype
     if dtype not in (torch.float8_e4m3fn, torch.int8):
         raise ValueError("dtype must be torch.float8_e4m3fn or torch.int8")
@@ -71,38 +90,29 @@ def alloc_kv_cache(num_pages: int, H: int, D: int, *, page_size: int = 128, dtyp
     return KVCache(codes[0], codes[1], scales[0], scales[1])
 
 
-class _On:
-    """Makes the cache's device current, and `stream`, if one is given, the current
-    stream, for the allocations and launches inside; costs nothing when both are."""
-
-    __slots__ = ("stack",)
-
-    def __init__(self, device, stream):
-        import contextlib
-
-        import torch
-        self.stack = contextlib.ExitStack()
-        self.stack.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.stack.enter_context(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        self.stack.close()
+def _elsewhere(cache, stream, call):
+    """Runs call() with the cache's device current and, if a stream is given, that
+    stream current, so that allocations and launches inside belong to them."""
+    if cache.index < 0:
+        return call()
+    with torch.cuda.device(cache.device):
+        if stream is None:
+            return call()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=cache.device)
+        with torch.cuda.stream(stream):
+            return call()
 
 
-def _elsewhere(cache, stream) -> bool:
-    """Whether a call needs _On: another stream than the current one, or another device."""
-    import torch
-    return cache.device.type == "cuda" and (stream is not None or cache.device.index != torch.cuda.current_device())
+def _on_gpu(cache):
+    if cache.index < 0:
+        raise ValueError("the cache is not on a CUDA device")
 
+
+# Full checks, with the reason in the error.  The calls below first test in one
+# expression what an ordinary call satisfies and come here only if that fails.
 
 def _ints(t, name, dim, device):
-    import torch
     if t.dtype != torch.int32 or t.dim() != dim or t.device != device:
         raise ValueError(f"{name} must be a {dim}-D torch.int32 tensor on the cache's device")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
@@ -130,7 +140,6 @@ def _table(t, name, B, device):
 
 def _rows(t, name, H, D, device):
     """Elements from token to token of bf16 rows [tokens, H, D] whose [H, D] part is contiguous."""
-    import torch
     if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or t.device != device:
         raise ValueError(f"{name} must be a torch.bfloat16 tensor [tokens, {H}, {D}] on the cache's device")
     s0, s1, s2 = t.stride()
@@ -146,12 +155,13 @@ def kv_append(k, v, cache: KVCache, page_table, seqlens, *, cu_seqlens=None, err
     cu_seqlens None: one new token per sequence; else int32 [B+1], the rows of each
     sequence's new tokens.  seqlens int32 [B]: the lengths after the append (0: a
     padding row); page_table int32 [B, pages]."""
-    if _elsewhere(cache, stream):
-        with _On(cache.device, stream):
-            return kv_append(k, v, cache, page_table, seqlens, cu_seqlens=cu_seqlens, err_flag=err_flag)
+    if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
+        return _elsewhere(cache, stream, lambda: kv_append(k, v, cache, page_table, seqlens, cu_seqlens=cu_seqlens,
+                                                           err_flag=err_flag))
     dev, B = cache.device, page_table.shape[0]
     ks, vs = _rows(k, "k", cache.H, cache.D, dev), _rows(v, "v", cache.H, cache.D, dev)
-    if v.shape[0] != k.shape[0]:
+    total = k.shape[0]
+    if v.shape[0] != total:
         raise ValueError("k and v must hold the same tokens")
     stride, cols = _table(page_table, "page_table", B, dev)
     _ints(seqlens, "seqlens", 1, dev)
@@ -162,8 +172,12 @@ def kv_append(k, v, cache: KVCache, page_table, seqlens, *, cu_seqlens=None, err
         if cu_seqlens.shape[0] != B + 1:
             raise ValueError("cu_seqlens must have B + 1 entries")
     _err(err_flag, dev)
-    _check(bsattn_kv_append(k, v, ks, vs, k.shape[0], B, cu_seqlens, page_table, stride, cols, seqlens,
-                            cache.ref, err_flag, None), "bsattn_kv_append")
+    _on_gpu(cache)
+    _check(_lib.bsattn_kv_append(k.data_ptr(), v.data_ptr(), ks, vs, total, B,
+                                 None if cu_seqlens is None else cu_seqlens.data_ptr(), page_table.data_ptr(),
+                                 stride, cols, seqlens.data_ptr(), cache.ref,
+                                 None if err_flag is None else err_flag.data_ptr(), _raw_stream(cache.index)),
+           "bsattn_kv_append")
     return cache
 
 
@@ -173,10 +187,9 @@ def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=Non
 
     total: rows to allocate when k and v are not given (cu_seqlens[-1], which lives on
     the device); rows outside every sequence are not written."""
-    import torch
-    if _elsewhere(cache, stream):
-        with _On(cache.device, stream):
-            return kv_read(cache, page_table, cu_seqlens, total=total, k=k, v=v, err_flag=err_flag)
+    if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
+        return _elsewhere(cache, stream, lambda: kv_read(cache, page_table, cu_seqlens, total=total, k=k, v=v,
+                                                         err_flag=err_flag))
     dev, B = cache.device, page_table.shape[0]
     stride, cols = _table(page_table, "page_table", B, dev)
     _ints(cu_seqlens, "cu_seqlens", 1, dev)
@@ -188,7 +201,8 @@ def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=Non
     if k is None:
         if total is None:
             raise ValueError("total is needed to allocate k and v")
-        k, v = (torch.empty((total, cache.H, cache.D), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        shape = (total, cache.H, cache.D)
+        k, v = torch.empty(shape, dtype=BF16, device=dev), torch.empty(shape, dtype=BF16, device=dev)
     else:
         for t, name in ((k, "k"), (v, "v")):
             _rows(t, name, cache.H, cache.D, dev)
@@ -196,8 +210,10 @@ def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=Non
                 raise ValueError(f"{name} must be contiguous")
         if v.shape[0] != k.shape[0] or (total is not None and total != k.shape[0]):
             raise ValueError("k, v and total disagree")
-    _check(bsattn_kv_read(cache.ref, page_table, stride, cols, B, cu_seqlens, k.shape[0], k, v, err_flag, None),
-           "bsattn_kv_read")
+    _on_gpu(cache)
+    _check(_lib.bsattn_kv_read(cache.ref, page_table.data_ptr(), stride, cols, B, cu_seqlens.data_ptr(), k.shape[0],
+                               k.data_ptr(), v.data_ptr(), None if err_flag is None else err_flag.data_ptr(),
+                               _raw_stream(cache.index)), "bsattn_kv_read")
     return k, v
 
 
@@ -205,23 +221,29 @@ def alloc_decode_workspace(cache: KVCache, B: int, Hq: int, *, prefix_len: int =
     """Workspace of a decode call for B sequences and Hq query heads (prefix_len as in
     ``decode_shared_prefix``).  It can be kept from call to call; two calls that may
     run at the same time need one each."""
-    import torch
     return torch.empty(bsattn_decode_workspace_size(cache.ref, B, Hq, prefix_len), dtype=torch.uint8,
                        device=cache.device)
 
 
-def _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
-            out_dtype, lse, workspace, err_flag):
-    import torch
+def _decode_checks(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, out, out_dtype, lse,
+                   workspace, err_flag):
     dev = cache.device
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
     B, Hq = q.shape[0], q.shape[1]
-    qs = _rows(q, "q", Hq, cache.D, dev)
-    stride, cols = _table(page_table, "page_table", B, dev) if page_table is not None else (0, 0)
+    _rows(q, "q", Hq, cache.D, dev)
+    if page_table is not None:
+        _table(page_table, "page_table", B, dev)
+    elif prefix_table is None:
+        raise ValueError("page_table is needed")
     _ints(seqlens, "seqlens", 1, dev)
     if seqlens.shape[0] != B:
         raise ValueError("seqlens must have one entry per sequence")
+    if meta is not None:
+        for name in ("full_cnt", "full_idx", "mask_cnt", "mask_idx", "cu_block_idx_offsets"):
+            t = getattr(meta, name)
+            if t is not None and not isinstance(t, int) and (t.device != dev or t.dtype != I32 or not t.is_contiguous()):
+                raise ValueError(f"meta.{name} must be a contiguous torch.int32 tensor on the cache's device")
     if kv_valid_len is not None:
         if meta is None:
             raise ValueError("kv_valid_len belongs to the listed tiles of meta")
@@ -233,32 +255,64 @@ def _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_va
         if prefix_len < 0 or prefix_table.shape[0] * cache.page_size < prefix_len:
             raise ValueError("prefix_table does not hold prefix_len tokens")
     _err(err_flag, dev)
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype not in (None, BF16, F32):
         raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-    if out is None:
-        out = torch.empty((B, Hq, cache.D), dtype=out_dtype, device=dev)
-    elif out.dtype != out_dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+    if out is not None and (out.dtype not in (BF16, F32) or (out_dtype is not None and out.dtype != out_dtype) or
+                            out.shape != q.shape or out.device != dev or not out.is_contiguous()):
         raise ValueError("out must be a contiguous [B, Hq, D] tensor of out_dtype on the cache's device")
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or lse.device != dev or not lse.is_contiguous():
+    if lse is not None and (lse.dtype != F32 or tuple(lse.shape) != (B, Hq) or lse.device != dev or
+                            not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [B, Hq] tensor on the cache's device")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _on_gpu(cache)
+
+
+def _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
+            out_dtype, lse, workspace, err_flag, stream):
+    if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
+        return _elsewhere(cache, stream, lambda: _decode(q, cache, prefix_table, prefix_len, page_table, seqlens,
+                                                         meta, kv_valid_len, softmax_scale, out, out_dtype, lse,
+                                                         workspace, err_flag, None))
+    index, shape = cache.index, q.shape
+    # what a step of a serving loop passes: contiguous tensors of one device, no lists, no
+    # error word, outputs allocated here; anything else takes the full checks
+    if not (len(shape) == 3 and q.dtype is BF16 and shape[2] == cache.D and q.is_contiguous() and
+            q.get_device() == index >= 0 and seqlens.dtype is I32 and seqlens.is_contiguous() and
+            seqlens.shape == shape[:1] and seqlens.get_device() == index and page_table is not None and
+            page_table.dtype is I32 and page_table.is_contiguous() and page_table.dim() == 2 and
+            page_table.shape[0] == shape[0] and page_table.get_device() == index and meta is None and
+            kv_valid_len is None and out is None and lse is None and err_flag is None and out_dtype is None and
+            (workspace is None or (workspace.get_device() == index and workspace.is_contiguous())) and
+            (prefix_table is None or (prefix_table.dtype is I32 and prefix_table.dim() == 1 and
+                                      prefix_table.is_contiguous() and prefix_table.get_device() == index and
+                                      0 <= prefix_len <= prefix_table.shape[0] * cache.page_size))):
+        _decode_checks(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, out, out_dtype,
+                       lse, workspace, err_flag)
+    B, Hq, D = shape
+    qs = q.stride(0) if B > 1 else Hq * D
+    if page_table is not None:
+        cols = page_table.shape[1]
+        table, stride = page_table.data_ptr(), page_table.stride(0) if B > 1 else cols
+    else:
+        table = None
+        stride = cols = 0
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or BF16, device=cache.device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=F32, device=cache.device)
     if workspace is None:
         workspace = alloc_decode_workspace(cache, B, Hq, prefix_len=prefix_len)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(cache.D)
-    od = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
+    rest = (table, stride, cols, seqlens.data_ptr(), None if meta is None else ctypes.byref(meta.to_c()),
+            None if kv_valid_len is None else kv_valid_len.data_ptr(),
+            cache.scale if softmax_scale is None else softmax_scale, out.data_ptr(),
+            OUT_BF16 if out.dtype is BF16 else OUT_F32, lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+            None if err_flag is None else err_flag.data_ptr(), _raw_stream(index))
     if prefix_table is None:
-        _check(bsattn_decode(q, qs, B, Hq, cache.ref, page_table, stride, cols, seqlens, meta, kv_valid_len,
-                             softmax_scale, out, od, lse, workspace, 0, err_flag, None), "bsattn_decode")
+        _check(_lib.bsattn_decode(q.data_ptr(), qs, B, Hq, cache.ref, *rest), "bsattn_decode")
     else:
-        _check(bsattn_decode_shared_prefix(q, qs, B, Hq, cache.ref, prefix_table, prefix_len, page_table, stride,
-                                           cols, seqlens, meta, kv_valid_len, softmax_scale, out, od, lse,
-                                           workspace, 0, err_flag, None), "bsattn_decode_shared_prefix")
+        _check(_lib.bsattn_decode_shared_prefix(q.data_ptr(), qs, B, Hq, cache.ref, prefix_table.data_ptr(),
+                                                prefix_len, *rest), "bsattn_decode_shared_prefix")
     return out, lse
 
 
@@ -273,12 +327,8 @@ def decode(q, cache: KVCache, page_table, seqlens, *, meta=None, kv_valid_len=No
     B); kv_valid_len int32 [B, meta.num_n] as for ``forward``.  Returns (out [B, Hq, D]
     bf16 or out_dtype, lse fp32 [B, Hq]); a sequence without keys gets 0 and -inf.
     workspace: see alloc_decode_workspace; None allocates one for this call."""
-    if _elsewhere(cache, stream):
-        with _On(cache.device, stream):
-            return _decode(q, cache, None, 0, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
-                           out_dtype, lse, workspace, err_flag)
     return _decode(q, cache, None, 0, page_table, seqlens, meta, kv_valid_len, softmax_scale, out, out_dtype, lse,
-                   workspace, err_flag)
+                   workspace, err_flag, stream)
 
 
 def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_table, seqlens, *, meta=None,
@@ -290,9 +340,5 @@ def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_
     be None when no sequence has keys of its own.  The prefix is read once for all."""
     if prefix_table is None:
         raise ValueError("prefix_table is needed (decode attends sequences without a prefix)")
-    if _elsewhere(cache, stream):
-        with _On(cache.device, stream):
-            return _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len,
-                           softmax_scale, out, out_dtype, lse, workspace, err_flag)
     return _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
-                   out_dtype, lse, workspace, err_flag)
+                   out_dtype, lse, workspace, err_flag, stream)

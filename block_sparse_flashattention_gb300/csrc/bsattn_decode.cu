@@ -16,12 +16,13 @@
 //
 // Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.
 //
-// Work split.  A segment is one (sequence, KV head), or one (KV head, 128 query rows)
-// of the prefix; its keys are tiles of 128.  All tiles of all segments form one line,
-// cut into equal pieces, one per CTA (one or two CTAs per SM): every SM reads the same
-// number of bytes whatever the lengths.  A segment that lies within one piece is finished
-// there; the parts of the others (fp32 output and LSE) go to the workspace and a second
-// kernel, a programmatic dependent of the first, joins them.
+// Work split.  A segment is one (sequence, KV head), or one KV head of the prefix while
+// at most 16 query rows a head meet it (more take bsattn_prefix.cu); its keys are tiles
+// of 128.  All tiles of all segments form one line, cut into equal pieces, one per CTA
+// (one or two CTAs per SM): every SM reads the same number of bytes whatever the lengths.
+// A segment that lies within one piece is finished there; the parts of the others (fp32
+// output and LSE) go to the workspace and a second kernel, a programmatic dependent of
+// the first, joins them.
 //
 // Roles (288 threads): warp 8 looks up lists and pages and keeps a ring of stages full
 // (TMA: codes by rows with the 128-byte or 64-byte swizzle, scales as plain copies);
@@ -36,6 +37,7 @@
 // second wants.  With the swizzled rows none of these 16-byte loads meets a bank twice
 // (the 8-byte loads of V at D = 64 do, two ways).
 #include "bsattn_internal.h"
+#include "decode_plan.cuh"
 #include "kv_codes.cuh"
 #include "sm100_ptx.cuh"
 
@@ -45,8 +47,6 @@ namespace {
 
 constexpr int kConsumers = 8;                    // computing warps
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kMaxCtas = 320;                    // pieces the workspace has room for
-constexpr int kRowBlock = 128;                   // query rows of a prefix segment
 
 // TileMsg flags: a segment's first / last tile in this CTA, its whole line lies here.
 constexpr uint32_t kFirst = 1u, kLast = 2u, kComplete = 4u;
@@ -92,39 +92,6 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 128, "misc area");
 
-// Segment numbering and the workspace: prefix segments (head-major, row blocks inside),
-// then one per (sequence, KV head).  Part `seg + cta` (of its kind) holds what a CTA
-// computed of a segment: along the line of tiles, from one part to the next either the
-// segment or the CTA advances, so no two parts share a number.
-struct Plan {
-    int row_blocks, sp, ss;       // prefix row blocks per head, prefix and suffix segments
-    int rows_p;                   // rows a prefix part has room for
-    size_t rec, pre_o, pre_l, suf_o, suf_l, total;
-};
-
-__host__ __device__ inline Plan make_plan(int B, int H, int G, int D, int prefix_len) {
-    Plan w;
-    const int rows = B * G;
-    w.row_blocks = prefix_len > 0 ? (rows + kRowBlock - 1) / kRowBlock : 0;
-    w.rows_p = rows < kRowBlock ? rows : kRowBlock;
-    w.sp = H * w.row_blocks;
-    w.ss = B * H;
-    const size_t np = w.sp ? (size_t)(w.sp + kMaxCtas) * w.rows_p : 0, ns = (size_t)(w.ss + kMaxCtas) * G;
-    size_t at = 0;
-    auto take = [&](size_t n) {
-        const size_t here = at;
-        at += (n + 255u) & ~(size_t)255u;
-        return here;
-    };
-    w.rec = take((size_t)(w.sp + w.ss) * sizeof(int2));
-    w.pre_o = take(np * D * 4u);
-    w.pre_l = take(np * 4u);
-    w.suf_o = take(ns * D * 4u);
-    w.suf_l = take(ns * 4u);
-    w.total = at;
-    return w;
-}
-
 struct Seg {
     int prefix, h, b, row0, rows;
 };
@@ -134,8 +101,8 @@ __device__ __forceinline__ Seg segment(const DecodeParams &p, const Plan &w, int
     if (seg < w.sp) {
         s.prefix = 1;
         s.h = seg / w.row_blocks;
-        s.row0 = (seg - s.h * w.row_blocks) * kRowBlock;
-        s.rows = min(kRowBlock, p.B * p.G - s.row0);
+        s.row0 = (seg - s.h * w.row_blocks) * kLineRows;
+        s.rows = min(kLineRows, p.B * p.G - s.row0);
         s.b = 0;
     } else {
         s.prefix = 0;
@@ -192,12 +159,6 @@ __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -526,7 +487,7 @@ struct Consumer {
     }
 
     __device__ __forceinline__ RowOut row_out(const Seg &s, int seg, bool complete, int r) const {
-        if (!s.prefix && complete && w.sp == 0) return RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
+        if (!s.prefix && complete && w.mode == kNoPrefix) return RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
         const long long part = (seg - (s.prefix ? 0 : w.sp)) + (long long)blockIdx.x;
         return s.prefix ? RowOut{1, part * w.rows_p + r} : RowOut{2, part * p.G + r};
     }
@@ -655,7 +616,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kWide>::kCtas)
         at = end;
     }
     __syncthreads();
-    if (lo >= hi) return;
+    if (lo >= hi) {
+        if (w.mode == kOwnKernel) grid_dependency_wait();
+        return;
+    }
 
     if (warp == kConsumers) {
         // ------------------------------------------------------- producer --
@@ -786,6 +750,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kWide>::kCtas)
         // no copy into this CTA's shared memory may be in flight when it ends
         for (uint32_t s = 0; s < (uint32_t)C::kStages; ++s)
             if (it > s) mbar_wait_drain(bar((int)((it - 1 - s) % C::kStages)), ((it - 1 - s) / C::kStages) & 1u);
+        // Launched beside the prefix kernel: this grid must not end before that one, since
+        // the join waits for this grid alone.
+        if (w.mode == kOwnKernel) grid_dependency_wait();
     } else {
         Consumer<D, kInt8, kWide> c{p, w, smem, base, warp, lane, lane >> 2, lane & 3};
         c.sync_phase = 0u;
@@ -806,20 +773,33 @@ __global__ void __launch_bounds__(128) bsattn_decode_join_kernel(const __grid_co
     const int b = (int)(row / p.Hq), hq = (int)(row - (long long)b * p.Hq), h = hq / p.G, gi = hq - h * p.G;
     const int2 *rec = reinterpret_cast<const int2 *>(p.ws + w.rec);
     const int2 rs = rec[w.sp + b * p.c.H + h];
-    int2 rp = make_int2(0, -1);
-    long long pre_row = 0;
-    if (w.sp) {
-        const int r = b * p.G + gi, sp = h * w.row_blocks + r / kRowBlock;
-        rp = rec[sp];
-        pre_row = (long long)(sp + rp.x) * w.rows_p + r % kRowBlock;
+    // the prefix's parts of this row: np of them, pre_step rows apart
+    int np = 0;
+    long long pre_row = 0, pre_step = w.rows_p;
+    if (w.mode) {
+        const int r = b * p.G + gi, blk = r / w.block_rows, rb = r - blk * w.block_rows, sp = h * w.row_blocks + blk;
+        if (w.mode == kInLine) {
+            const int2 rp = rec[sp];
+            np = rp.y - rp.x + 1;
+            pre_row = (long long)(sp + rp.x) * w.rows_p + rb;
+        } else {
+            const int nt = (p.prefix_len + kTile - 1) / kTile;
+            const int c0 = w.pre_owner((long long)sp * nt, nt), c1 = w.pre_owner((long long)(sp + 1) * nt - 1, nt);
+            np = c1 - c0 + 1;
+            pre_row = (long long)(sp + c0) * w.rows_p + rb;
+            if (p.B * p.G - blk * kBlockRows <= kTile) {  // both slots hold parts of the row
+                np *= 2;
+                pre_step = kTile;
+            }
+        }
     } else if (rs.x == rs.y) {
         return;
     }
-    const int np = rp.y - rp.x + 1, n = np + rs.y - rs.x + 1;
+    const int n = np + rs.y - rs.x + 1;
     const long long suf_row = (long long)(b * p.c.H + h + rs.x) * p.G + gi;
     const float *pre_o = reinterpret_cast<const float *>(p.ws + w.pre_o), *pre_l = reinterpret_cast<const float *>(p.ws + w.pre_l);
     const float *suf_o = reinterpret_cast<const float *>(p.ws + w.suf_o), *suf_l = reinterpret_cast<const float *>(p.ws + w.suf_l);
-    auto at = [&](int i) -> long long { return i < np ? pre_row + (long long)i * w.rows_p : suf_row + (long long)(i - np) * p.G; };
+    auto at = [&](int i) -> long long { return i < np ? pre_row + i * pre_step : suf_row + (long long)(i - np) * p.G; };
     float mx = -INFINITY;
     bool nan = false;
     for (int i = lane; i < n; i += 32) {
@@ -876,16 +856,22 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, 
         attr_set_for_device[dev] = 1;
     }
     const int grid = min(sms * C::kCtas, kMaxCtas);
-    bsattn_decode_kernel<D, kInt8, kWide><<<grid, kThreads, C::kAlloc, stream>>>(p, w, tk, tv);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.Hq + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    cfg.stream = stream;
+    // beside the prefix kernel, whose results it does not need; else after what came before
+    cfg.numAttrs = w.mode == kOwnKernel ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kAlloc;
+    e = cudaLaunchKernelEx(&cfg, bsattn_decode_kernel<D, kInt8, kWide>, p, w, tk, tv);
+    if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.Hq + 3) / 4));
+    cfg.blockDim = dim3(128);
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D>, p, w);
 }
@@ -894,7 +880,7 @@ template <int D, bool kInt8>
 cudaError_t launch_rows(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int sms,
                         cudaStream_t stream) {
     // 8 query rows fill one group of columns; more take the build with two
-    const int rows = w.sp ? w.rows_p : 0;
+    const int rows = w.mode == kInLine ? w.rows_p : 0;
     if (max(rows, p.G) <= 8) return launch<D, kInt8, false>(p, w, tk, tv, sms, stream);
     return launch<D, kInt8, true>(p, w, tk, tv, sms, stream);
 }
@@ -902,18 +888,22 @@ cudaError_t launch_rows(const DecodeParams &p, const Plan &w, const CUtensorMap 
 }  // namespace
 
 size_t decode_workspace_bytes(int B, int H, int G, int D, int prefix_len) {
-    return make_plan(B, H, G, D, prefix_len).total;
+    return make_plan(B, H, G, D, prefix_len, 0).total;
 }
 
 cudaError_t launch_decode(const DecodeParams &p, cudaStream_t stream) {
-    const Plan w = make_plan(p.B, p.c.H, p.G, p.c.D, p.prefix_len);
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
+    const Plan w = make_plan(p.B, p.c.H, p.G, p.c.D, p.prefix_len, sms);
     CUtensorMap tk, tv;
     const long long rows = ((long long)(p.c.num_pages > 0 ? p.c.num_pages : 1) * p.c.H) << p.c.page_shift;
     if (!encode_code_rows(&tk, p.c.k, rows, p.c.D, 1 << p.c.page_shift) ||
         !encode_code_rows(&tv, p.c.v, rows, p.c.D, 1 << p.c.page_shift))
         return cudaErrorInvalidValue;
+    if (w.mode == kOwnKernel) {
+        const cudaError_t e = launch_prefix(p, w, stream);
+        if (e != cudaSuccess) return e;
+    }
     if (p.c.D == 128)
         return p.c.int8 ? launch_rows<128, true>(p, w, tk, tv, sms, stream)
                         : launch_rows<128, false>(p, w, tk, tv, sms, stream);

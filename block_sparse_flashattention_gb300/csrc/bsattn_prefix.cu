@@ -1,0 +1,670 @@
+// The shared prefix of a decoding batch, when many query rows meet it: tcgen05 kernel.
+//
+// For one KV head, the queries of every sequence are rows of one attention over the
+// prefix's keys, 4 D flop per row and key against 2 (D + 4) bytes per key: from about
+// 150 rows on the products bound it, not HBM.  The 8-bit codes are widened once per 256
+// rows, in shared memory:
+//   K' = fp16(code), exact; the key's scale multiplies its scores in fp32;
+//   V' = fp16(code) fp16(vs 2^(6 - E)), E the largest binary exponent of a value scale
+//        so far (O is rescaled when it grows): exact for power-of-two scales, otherwise
+//        off by two roundings to 11 bits; a row keeps 10 bits down to 2^-30 of the largest;
+//   Q' = fp16(q 2^-e), e the row's largest binary exponent (as in bsattn_decode.cu).
+// With t_j = S_j ks_j and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 6) is rounded
+// to fp16 for P V', l sums it in fp32; out = O 2^(E - 6) / l, log2-LSE = m - 6 + log2 l.
+//
+// A segment is (KV head, 256 query rows): two 128-row tiles ("slots") that share each
+// K/V tile.  With 128 rows or fewer both slots hold the same rows and take the key tiles
+// in turn, each with sums of its own: the softmax of one slot always runs beside the
+// products of the other.  The line of all segments' 128-key tiles is cut evenly over the
+// SMs; each part (fp32 output and LSE per slot row) goes to the workspace for the join.
+//
+// Roles (512 threads, one CTA per SM, all of TMEM):
+//   warp 0        issues the MMAs: S_t = Q_t K'^T into TMEM, O_t += P_t V' with P in TMEM
+//   warp 1        owns the TMEM allocation
+//   warps 4-7, 8-11   slot 0, slot 1: load the query rows, softmax, O rescale, part
+//   warps 12-15   load codes and scales (the next tile's codes wait in registers), widen
+//                 them into the K and V stages (128-byte swizzle; V as it lies, MN-major)
+// TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P_t over S_t.
+#include "bsattn_internal.h"
+#include "decode_plan.cuh"
+#include "kv_codes.cuh"
+#include "sm100_ptx.cuh"
+
+namespace bsattn {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+// 128 registers per thread at launch; the control warpgroup's surplus goes to the
+// softmax: 128 * 56 + 2 * 128 * 176 + 128 * 96 = 64512 <= 512 * 128.
+constexpr int kLaunchRegs = 128;
+constexpr uint32_t kCtrlRegs = 56, kSoftmaxRegs = 176, kWidenRegs = 96;
+static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs + 128 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr uint32_t kSub = kTile * 64 * 2;  // 128 rows x 64 fp16: one 128-byte swizzle span
+constexpr int kMsgs = 4;                   // tiles whose key scales and masks are kept
+
+struct KeyMsg {
+    uint32_t keep[4];  // keys that count, one bit each
+    int32_t exp;       // E (biased) of the value factors
+    int32_t pad[3];
+};
+
+template <int D>
+struct Cfg {
+    static constexpr uint32_t kTileBytes = kTile * D * 2;
+    static constexpr uint32_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + 2 * kTileBytes;
+    static constexpr uint32_t kScale = kV + 2 * kTileBytes;          // kMsgs x 128 key scales
+    static constexpr uint32_t kMsg = kScale + kMsgs * 512u;
+    static constexpr uint32_t kBar = kMsg + kMsgs * (uint32_t)sizeof(KeyMsg);
+    // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete
+    static constexpr int bKF = 0, bKE = 2, bVF = 4, bVE = 6, bQF = 8, bSR = 10, bPR = 12, bOD = 16, bDrain = 18,
+                         kNumBars = 19;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
+    static constexpr uint32_t kBytes = kMisc + 16;
+    static constexpr uint32_t kAlloc = kBytes + 1024;                // slack for 1024-byte alignment
+    static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+
+// This CTA's pieces of the line, one segment at a time; every role walks them alike.
+struct Walk {
+    long long pos, end;
+    int nt;
+    int seg, off, n;  // segment, its first tile here, tiles here
+    __device__ __forceinline__ bool next() {
+        if (pos >= end) return false;
+        seg = (int)(pos / nt);
+        off = (int)(pos - (long long)seg * nt);
+        n = (int)min((long long)(nt - off), end - pos);
+        pos += n;
+        return true;
+    }
+};
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Instruction descriptor, kind::f16 with fp16 A and B, fp32 D (see idesc_bf16_f32).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// One slot: warps 4-7 (t = 0) or 8-11 (t = 1), one row per thread.
+template <int D>
+__device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &w, Walk walk, uint32_t tmem, int t,
+                                             uint32_t warp, uint32_t lane, uint32_t base, uint8_t *smem,
+                                             volatile int *abort) {
+    using C = Cfg<D>;
+    auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
+    const uint32_t quarter = warp & 3u;
+    const int r = (int)(quarter * 32 + lane);
+    const uint32_t lane_addr = tmem + ((quarter * 32u) << 16);
+    const uint32_t s_col = (uint32_t)t * 128u, o_col = 256u + (uint32_t)t * D;
+    const int rows_total = p.B * p.G;
+    uint32_t sc = 0, od = 0;   // phases of S ready and O complete
+    uint32_t tile0 = 0;        // tiles of earlier segments (they number the K stages and messages)
+    bool ok = true;
+    while (ok && walk.next()) {
+        const int h = walk.seg / w.row_blocks, row0 = (walk.seg - h * w.row_blocks) * kBlockRows;
+        const int rows = min(kBlockRows, rows_total - row0);
+        const bool split = rows <= kTile;
+        const int row = split ? r : t * kTile + r;   // of the segment
+        const bool row_ok = row < rows;
+        // ---- the query row: fp16 of q 2^-e into the slot's tile (K-major, swizzled)
+        float c;
+        {
+            uint32_t x[D / 2];
+            const int m = row0 + row, b = row_ok ? m / p.G : 0;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + (long long)b * p.q_stride + (long long)(h * p.G + (row_ok ? m - b * p.G : 0)) * D);
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 y = row_ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                x[4 * i] = y.x;
+                x[4 * i + 1] = y.y;
+                x[4 * i + 2] = y.z;
+                x[4 * i + 3] = y.w;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) a = __vmaxu2(a, x[i] & 0x7fff7fffu);
+            a = max(a & 0xffffu, a >> 16);
+            const int e = (a == 0 || a >= 0x7f80u) ? 127 : min(max((int)(a >> 7), 1), 253);
+            const float f = __uint_as_float((uint32_t)(254 - e) << 23);
+            c = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)e << 23), 0x1p-126f);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[k] = pack_f16x2(__uint_as_float(x[4 * i + k] << 16) * f,
+                                      __uint_as_float(x[4 * i + k] & 0xffff0000u) * f);
+                const uint32_t at = C::kQ + (uint32_t)t * C::kTileBytes + (uint32_t)(i >> 3) * kSub +
+                                    (uint32_t)r * 128u + (uint32_t)(((i & 7) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4 *>(smem + at) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::bQF + t));
+        // ---- the slot's tiles
+        float m_run = -INFINITY, l_run = 0.f;
+        int exp_run = 0, done = 0;
+        for (int k = split ? t : 0; ok && k < walk.n; k += split ? 2 : 1) {
+            ok = mbar_wait(bar(C::bSR + t), sc & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            ++sc;
+            tc_fence_after();
+            const uint32_t slot = (tile0 + (uint32_t)k) % kMsgs;
+            const KeyMsg *msg = reinterpret_cast<const KeyMsg *>(smem + C::kMsg) + slot;
+            const float4 *ks = reinterpret_cast<const float4 *>(smem + C::kScale + slot * 512u);
+            float s[128];
+            {
+                uint32_t v0[32], v1[32], v2[32], v3[32];
+                tmem_ld32(lane_addr + s_col + 0, v0);
+                tmem_ld32(lane_addr + s_col + 32, v1);
+                tmem_ld32(lane_addr + s_col + 64, v2);
+                tmem_ld32(lane_addr + s_col + 96, v3);
+                tmem_wait_ld();
+                reg_fence(v0);
+                reg_fence(v1);
+                reg_fence(v2);
+                reg_fence(v3);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    s[x] = __uint_as_float(v0[x]);
+                    s[32 + x] = __uint_as_float(v1[x]);
+                    s[64 + x] = __uint_as_float(v2[x]);
+                    s[96 + x] = __uint_as_float(v3[x]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                const float4 f = ks[x];
+                fmul2(s[4 * x], s[4 * x + 1], s[4 * x], s[4 * x + 1], f.x, f.y);
+                fmul2(s[4 * x + 2], s[4 * x + 3], s[4 * x + 2], s[4 * x + 3], f.z, f.w);
+            }
+            const uint4 kw = *reinterpret_cast<const uint4 *>(msg->keep);
+            if ((kw.x & kw.y & kw.z & kw.w) != 0xffffffffu) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t keep = q == 0 ? kw.x : q == 1 ? kw.y : q == 2 ? kw.z : kw.w;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (!((keep >> x) & 1u)) s[32 * q + x] = -INFINITY;
+                }
+            }
+            float g[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                g[q] = fmax3(s[32 * q], s[32 * q + 1], s[32 * q + 2]);
+#pragma unroll
+                for (int x = 3; x < 31; x += 2) g[q] = fmax3(g[q], s[32 * q + x], s[32 * q + x + 1]);
+                g[q] = fmaxf(g[q], s[32 * q + 31]);
+            }
+            const float m_new = fmaxf(m_run, fmax3(g[0], g[1], fmaxf(g[2], g[3])) * c);
+            const int exp_new = msg->exp;
+            // O is rescaled when some row's maximum grew by more than 2^8 or E grew; otherwise
+            // the stale references serve (P stays below 2^14)
+            const bool grew = __any_sync(0xffffffffu, (m_new - m_run) > 8.0f);
+            const bool rescale = done > 0 && (grew || exp_new != exp_run);
+            float alpha = 1.f, alpha_o = 1.f;
+            if (done == 0) {
+                m_run = m_new;
+                exp_run = exp_new;
+            } else if (rescale) {
+                if (grew) {
+                    if (m_new != -INFINITY) alpha = ex2_approx(m_run - m_new);
+                    m_run = m_new;
+                }
+                alpha_o = alpha * ex2_approx((float)(exp_run - exp_new));
+                exp_run = exp_new;
+            }
+            const float nm = (m_run == -INFINITY ? 0.f : -m_run) + 6.f;
+            float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
+            auto p_half = [&](int q) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    float x0, x1;
+                    ffma2(x0, x1, s[q * 64 + 2 * x], s[q * 64 + 2 * x + 1], c, c, nm, nm);
+                    const float p0 = ex2_approx(x0);
+                    const float p1 = ex2_approx(x1);
+                    if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
+                    else fadd2(la0, la1, la0, la1, p0, p1);
+                    pk[x] = pack_f16x2(p0, p1);
+                }
+                tmem_st32(lane_addr + s_col + q * 32, pk);
+            };
+            auto publish = [&](int half) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bPR + 2 * t + half));
+            };
+            p_half(0);
+            if (rescale) {
+                // S of this tile was issued after the slot's previous P V: O is up to date
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + o_col + q * 32, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * alpha_o);
+                    tmem_st32(lane_addr + o_col + q * 32, v);
+                }
+            }
+            publish(0);
+            p_half(1);
+            publish(1);
+            l_run = l_run * alpha + ((la0 + lb0) + (la1 + lb1));
+            ++done;
+        }
+        if (!ok) break;
+        tile0 += (uint32_t)walk.n;
+        // ---- the part: rows of 128-byte blocks go through the slot's query tile (no S of
+        // this segment is outstanding), so that every store writes whole row pieces
+        if (done > 0) {
+            ok = mbar_wait(bar(C::bOD + t), od & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            ++od;
+            tc_fence_after();
+        }
+        const bool empty = done == 0 || l_run == 0.f;   // NaN is not empty
+        const float inv = empty ? 0.f : ex2_approx((float)(exp_run - 127 - 6)) / l_run;
+        const long long part_row = ((long long)walk.seg + blockIdx.x) * w.rows_p + t * kTile;
+        float *po = reinterpret_cast<float *>(p.ws + w.pre_o) + part_row * D;
+        uint4 *scr = reinterpret_cast<uint4 *>(smem + C::kQ + (uint32_t)t * C::kTileBytes + quarter * 4096u);
+        const int first = (int)(quarter * 32u) + 8 * (int)(lane >> 3);   // rows this lane stores
+        const int limit = split ? rows : rows - t * kTile;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            if (done > 0) {
+                tmem_ld32(lane_addr + o_col + q * 32, v);
+                tmem_wait_ld();
+                reg_fence(v);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) v[x] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                scr[lane * 8u + ((uint32_t)i ^ (lane & 7u))] =
+                    make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * inv),
+                               __float_as_uint(__uint_as_float(v[4 * i + 1]) * inv),
+                               __float_as_uint(__uint_as_float(v[4 * i + 2]) * inv),
+                               __float_as_uint(__uint_as_float(v[4 * i + 3]) * inv));
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint4 x = scr[(lane >> 3) * 64u + (uint32_t)k * 8u + ((lane & 7u) ^ (uint32_t)k)];
+                if (first + k < limit)
+                    *reinterpret_cast<uint4 *>(po + (long long)(first + k) * D + q * 32 + 4 * (lane & 7u)) = x;
+            }
+            __syncwarp();
+        }
+        if (row_ok)
+            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - 6.f + lg2(l_run);
+        tc_fence_before();
+    }
+}
+
+// Codes and scales of a tile, loaded ahead: this thread's pieces of 16 codes (8 rows
+// of the warp's 32 at D = 128, 4 at D = 64), and scales of four keys (of the tile) and
+// of one (of the warp's 32).
+template <int D>
+struct Raw {
+    static constexpr int kPieces = D / 16;       // 16-byte pieces of a row
+    static constexpr int kRowsPerStep = 32 / kPieces, kSteps = 32 / kRowsPerStep;
+    uint4 x[kSteps];
+};
+
+template <int D, bool kInt8>
+__device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w, Walk walk, int warp, int lane,
+                                           uint32_t base, uint8_t *smem, volatile int *abort) {
+    using C = Cfg<D>;
+    using R = Raw<D>;
+    auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
+    const int piece = lane % R::kPieces, sub_row = lane / R::kPieces;
+    const int ps_shift = p.c.page_shift, n_keys = p.prefix_len;
+    // Row of the caches (of page rows) that holds key `key` of head h, or -1.
+    auto cache_row = [&](int key, int h) -> int {
+        if (key >= n_keys) return -1;
+        const int page = __ldg(p.prefix_table + (key >> ps_shift));
+        if (page < 0 || page >= p.c.num_pages) {
+            if (lane == 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+            return -1;
+        }
+        return ((page * p.c.H + h) << ps_shift) + (key & ((1 << ps_shift) - 1));
+    };
+    // This warp's 32 keys are two runs of 16, each inside one page.
+    struct Rows {
+        int run[2];
+    };
+    auto rows_of = [&](int tile, int h) -> Rows {
+        const int k0 = tile * kTile + warp * 32;
+        return Rows{{cache_row(k0, h), cache_row(k0 + 16, h)}};
+    };
+    auto load = [&](R &raw, const uint8_t *codes, const Rows &rw, int tile) {
+#pragma unroll
+        for (int i = 0; i < R::kSteps; ++i) {
+            const int k = i * R::kRowsPerStep + sub_row;   // of the warp's 32
+            const int row = rw.run[k >> 4];
+            const bool on = row >= 0 && tile * kTile + warp * 32 + k < n_keys;
+            raw.x[i] = on ? __ldg(reinterpret_cast<const uint4 *>(codes + ((long long)row + (k & 15)) * D + piece * 16))
+                          : make_uint4(0, 0, 0, 0);
+        }
+    };
+    // 16 codes as 32 bytes of fp16 into the swizzled tile; lanes of the second 64-column
+    // span store their two halves in the other order, which keeps the banks apart
+    auto store = [&](uint32_t tile_at, int k, uint4 x, uint32_t f) {
+        const bool swap = D == 128 && piece >= 4;
+        const uint32_t y[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
+        const int row = warp * 32 + k;
+        const uint32_t at = tile_at + (uint32_t)(piece >> 2) * kSub + (uint32_t)row * 128u;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            uint32_t o[4];
+            codes_to_f16x2<kInt8>(y[2 * hf], o[0], o[1]);
+            codes_to_f16x2<kInt8>(y[2 * hf + 1], o[2], o[3]);
+            if (f != 0u) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(f));
+            }
+            const uint32_t chunk = (uint32_t)((piece & 3) * 2 + (hf ^ (swap ? 1 : 0)));
+            *reinterpret_cast<uint4 *>(smem + at + ((chunk ^ (uint32_t)(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    };
+    uint32_t it = 0;
+    int exp_run = 1;
+    Walk ahead = walk;          // the tile after the current one
+    R kr, vr;
+    Rows rw = {};
+    int h = 0;
+    bool more = ahead.next();
+    int ak = 0;
+    if (more) {
+        h = ahead.seg / w.row_blocks;
+        rw = rows_of(ahead.off, h);
+        load(kr, p.c.k, rw, ahead.off);
+        load(vr, p.c.v, rw, ahead.off);
+    }
+    while (walk.next()) {
+        exp_run = 1;            // E starts anew with a segment's sums
+        for (int k = 0; k < walk.n; ++k, ++it) {
+            const int tile = walk.off + k;
+            const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
+            // scales: of the warp's own 32 keys, one per lane, and the largest value scale of the tile
+            const int kr_row = rw.run[lane >> 4];
+            const bool on = kr_row >= 0 && tile * kTile + warp * 32 + lane < n_keys;
+            const float ksc = on ? __ldg(p.c.ks + (long long)kr_row + (lane & 15)) : 0.f;
+            const float vsc = on ? __ldg(p.c.vs + (long long)kr_row + (lane & 15)) : 0.f;
+            uint32_t top = 0;
+            {
+                const int key = tile * kTile + 4 * lane;
+                const int page = key < n_keys ? __ldg(p.prefix_table + (key >> ps_shift)) : -1;
+                if (page >= 0 && page < p.c.num_pages) {
+                    const long long row = (((long long)page * p.c.H + h) << ps_shift) + (key & ((1 << ps_shift) - 1));
+                    const float4 y = __ldg(reinterpret_cast<const float4 *>(p.c.vs + row));
+                    const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bits = __float_as_uint(z[i]);
+                        if (key + i < n_keys && bits < 0x7f800000u) top = max(top, bits);
+                    }
+                }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            exp_run = max(exp_run, (int)(top >> 23));
+            const uint32_t keep = __ballot_sync(0xffffffffu, on);
+            // where the next tile lies
+            int ntile = 0, nh = h;
+            Rows nrw = {};
+            bool nmore = more;
+            if (more && ++ak >= ahead.n) {
+                ak = 0;
+                nmore = ahead.next();
+                nh = nmore ? ahead.seg / w.row_blocks : 0;
+            }
+            if (nmore) {
+                ntile = ahead.off + ak;
+                nrw = rows_of(ntile, nh);
+            }
+            // K
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(C::bKE + st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
+                return;
+#pragma unroll
+            for (int i = 0; i < R::kSteps; ++i)
+                store(C::kK + st * C::kTileBytes, i * R::kRowsPerStep + sub_row, kr.x[i], 0u);
+            reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = ksc;
+            KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
+            if (lane == 0) {
+                msg->keep[warp] = keep;
+                if (warp == 0) msg->exp = exp_run;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bKF + st));
+            if (nmore) load(kr, p.c.k, nrw, ntile);
+            // V
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(C::bVE + st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
+                return;
+            const float to = __uint_as_float((uint32_t)min(254, 260 - exp_run) << 23);   // 2^(6 - E)
+            const uint32_t fv = pack_f16x2(vsc * to, vsc * to);
+#pragma unroll
+            for (int i = 0; i < R::kSteps; ++i) {
+                const int kk = i * R::kRowsPerStep + sub_row;
+                const uint32_t f = __shfl_sync(0xffffffffu, fv, kk);
+                uint4 x = vr.x[i];
+                if (f == 0u) x = make_uint4(0, 0, 0, 0);
+                store(C::kV + st * C::kTileBytes, kk, x, f);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bVF + st));
+            if (nmore) load(vr, p.c.v, nrw, ntile);
+            rw = nrw;
+            h = nh;
+            more = nmore;
+        }
+    }
+}
+
+template <int D, bool kInt8>
+__global__ void __launch_bounds__(kThreads, 1)
+    bsattn_prefix_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    volatile int *abort = reinterpret_cast<volatile int *>(misc + 1);
+    auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
+    const uint32_t warp = warp_id(), lane = lane_id();
+    grid_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(C::bKF + s), 4);       // one arrival per widening warp
+            mbar_init(bar(C::bKE + s), 1);
+            mbar_init(bar(C::bVF + s), 4);
+            mbar_init(bar(C::bVE + s), 1);
+            mbar_init(bar(C::bQF + s), 4);       // one per softmax warp of the slot
+            mbar_init(bar(C::bSR + s), 2);
+            mbar_init(bar(C::bPR + 2 * s), 4);
+            mbar_init(bar(C::bPR + 2 * s + 1), 4);
+            mbar_init(bar(C::bOD + s), 1);
+        }
+        mbar_init(bar(C::bDrain), 1);
+        misc[1] = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(base + C::kMisc, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    Walk walk;
+    walk.nt = (p.prefix_len + kTile - 1) / kTile;
+    walk.pos = w.pre_first((int)blockIdx.x, walk.nt);
+    walk.end = w.pre_first((int)blockIdx.x + 1, walk.nt);
+
+    if (warp == 0) {
+        regs_release<kCtrlRegs>();
+        // ---------------------------------------------------- MMA issuer --
+        // The whole warp runs in step; lane 0 issues.
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, false);
+        constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
+        const uint64_t desc_q = smem_desc_sw128(base + C::kQ, 16, 1024);
+        const uint64_t desc_k = smem_desc_sw128(base + C::kK, 16, 1024);
+        const uint64_t desc_v = smem_desc_sw128(base + C::kV, kSub, 1024);
+        constexpr uint64_t kTileUnits = C::kTileBytes >> 4, kSubUnits = kSub >> 4;
+        uint32_t it = 0, seg = 0;          // tiles, segments so far
+        uint32_t pc[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](int b, uint32_t phase) -> bool {
+            ok = ok && mbar_wait(bar(b), phase, abort, p.err, BSATTN_FLAG_TIMEOUT);
+            return ok;
+        };
+        auto score = [&](int t, uint32_t tile) {
+            const uint64_t qd = desc_q + (uint64_t)t * kTileUnits, kd = desc_k + (uint64_t)(tile & 1u) * kTileUnits;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)((kk >> 2) * kSubUnits + (kk & 3) * 2);
+                mma_ss_lead(lead, tmem + t * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_lead(lead, bar(C::bSR + t));
+            mbar_arrive_lead(lead, bar(C::bSR + t));
+        };
+        auto output = [&](int t, uint32_t tile, bool first) -> bool {
+            if (!wait(C::bVF + (int)(tile & 1u), (tile >> 1) & 1u)) return false;
+            const uint64_t vd = desc_v + (uint64_t)(tile & 1u) * kTileUnits;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!wait(C::bPR + 2 * t + half, pc[t] & 1u)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                    mma_ts_lead(lead, tmem + 256 + t * D, tmem + t * 128 + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)),
+                                idesc_pv, kk > 0 || !first ? 1u : 0u);
+            }
+            ++pc[t];
+            return true;
+        };
+        while (ok && walk.next()) {
+            const int h = walk.seg / w.row_blocks, row0 = (walk.seg - h * w.row_blocks) * kBlockRows;
+            const bool split = p.B * p.G - row0 <= kTile;
+            if (!wait(C::bQF, seg & 1u) || !wait(C::bQF + 1, seg & 1u)) break;
+            tc_fence_after();
+            for (int k = 0; ok && k < walk.n; ++k) {
+                const uint32_t tile = it + (uint32_t)k;
+                if (!wait(C::bKF + (int)(tile & 1u), (tile >> 1) & 1u)) break;
+                tc_fence_after();
+                if (split) {
+                    const int t = k & 1;
+                    if (k >= 2) {
+                        if (!output(t, tile - 2, k < 4)) break;
+                        mma_commit_lead(lead, bar(C::bVE + (int)(tile & 1u)));
+                    }
+                    score(t, tile);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (k > 0 && !output(t, tile - 1, k == 1)) break;
+                        score(t, tile);
+                    }
+                    if (!ok) break;
+                    if (k > 0) mma_commit_lead(lead, bar(C::bVE + (int)((tile - 1) & 1u)));
+                }
+                mma_commit_lead(lead, bar(C::bKE + (int)(tile & 1u)));
+            }
+            if (!ok) break;
+            const uint32_t last = it + (uint32_t)walk.n - 1;
+            if (split) {
+                if (walk.n >= 2) {
+                    const int t = (walk.n - 2) & 1;
+                    if (!output(t, last - 1, walk.n - 2 < 2)) break;
+                    mma_commit_lead(lead, bar(C::bVE + (int)((last - 1) & 1u)));
+                    mma_commit_lead(lead, bar(C::bOD + t));
+                }
+                const int t = (walk.n - 1) & 1;
+                if (!output(t, last, walk.n - 1 < 2)) break;
+                mma_commit_lead(lead, bar(C::bVE + (int)(last & 1u)));
+                mma_commit_lead(lead, bar(C::bOD + t));
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!output(t, last, walk.n == 1)) break;
+                    mma_commit_lead(lead, bar(C::bOD + t));
+                }
+                if (!ok) break;
+                mma_commit_lead(lead, bar(C::bVE + (int)(last & 1u)));
+            }
+            it += (uint32_t)walk.n;
+            ++seg;
+        }
+        // Wait until every tcgen05 operation issued above has completed.
+        mma_commit_lead(lead, bar(C::bDrain));
+        mbar_wait_drain(bar(C::bDrain), 0);
+    } else if (warp < 4) {
+        regs_release<kCtrlRegs>();
+    } else if (warp < 12) {
+        regs_claim<kSoftmaxRegs>();
+        softmax_role<D>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);
+    } else {
+        regs_release<kWidenRegs>();
+        widen_role<D, kInt8>(p, w, walk, (int)warp - 12, (int)lane, base, smem, abort);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool kInt8>
+cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
+    using C = Cfg<D>;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, bsattn_prefix_kernel<D, kInt8>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(bsattn_prefix_kernel<D, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::kAlloc);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    bsattn_prefix_kernel<D, kInt8><<<w.pre_cuts, kThreads, C::kAlloc, stream>>>(p, w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefix(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
+    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, w, stream) : launch<128, false>(p, w, stream);
+    return p.c.int8 ? launch<64, true>(p, w, stream) : launch<64, false>(p, w, stream);
+}
+
+}  // namespace bsattn

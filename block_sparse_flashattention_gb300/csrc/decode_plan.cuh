@@ -1,0 +1,73 @@
+// How a decode call's work is numbered and where its parts lie in the workspace; shared
+// by the decode kernel (bsattn_decode.cu) and the prefix kernel (bsattn_prefix.cu).
+#pragma once
+
+#include "bsattn_internal.h"
+
+namespace bsattn {
+
+constexpr int kMaxCtas = 320;     // CTAs whose parts the workspace has room for
+constexpr int kLineRows = 128;    // query rows of a prefix segment in the decode kernel's line
+constexpr int kBlockRows = 256;   // and in the prefix kernel
+
+// Up to 16 query rows a KV head meet the prefix inside the decode kernel's line (kInLine);
+// more run in a kernel of their own (kOwnKernel).
+enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2 };
+
+// Segments: of the prefix, (KV head, block of query rows), head-major; of the sequences'
+// own keys, (sequence, KV head).  A line of tiles is cut over CTAs, and part `segment +
+// cta` holds what a CTA computed of a segment: from one part of the line to the next
+// either the segment or the CTA advances, so no two parts share a number.
+struct Plan {
+    int mode;
+    int row_blocks, pre_segs, block_rows;  // prefix: blocks per head, segments, rows of a block
+    int rows_p;                            // rows a prefix part has room for
+    int sp, ss;                            // prefix and own segments of the decode kernel's line
+    int pre_cuts;                          // CTAs of the prefix kernel
+    size_t rec, pre_o, pre_l, suf_o, suf_l, total;  // byte offsets: records, parts, size
+
+    // First tile of CTA `cta`'s piece of the prefix kernel's line.
+    __host__ __device__ long long pre_first(int cta, int nt) const {
+        return (long long)pre_segs * nt * cta / pre_cuts;
+    }
+    // The CTA whose piece holds tile `tile` of that line.
+    __host__ __device__ int pre_owner(long long tile, int nt) const {
+        return (int)(((tile + 1) * pre_cuts - 1) / ((long long)pre_segs * nt));
+    }
+};
+
+// sms: SMs of the device (0: only the workspace's layout is wanted).
+inline Plan make_plan(int B, int H, int G, int D, int prefix_len, int sms) {
+    Plan w = {};
+    const int rows = B * G;
+    w.mode = prefix_len <= 0 ? kNoPrefix : rows <= 16 ? kInLine : kOwnKernel;
+    w.block_rows = w.mode == kOwnKernel ? kBlockRows : kLineRows;
+    w.row_blocks = w.mode ? (rows + w.block_rows - 1) / w.block_rows : 0;
+    w.pre_segs = H * w.row_blocks;
+    // the prefix kernel's parts hold both slots of 128 rows
+    w.rows_p = w.mode == kOwnKernel ? kBlockRows : rows < kLineRows ? rows : kLineRows;
+    w.sp = w.mode == kInLine ? w.pre_segs : 0;
+    w.ss = B * H;
+    const long long tiles = (long long)w.pre_segs * ((prefix_len + kTile - 1) / kTile);
+    const int most = sms < kMaxCtas ? sms : kMaxCtas;
+    w.pre_cuts = (int)(tiles < most ? tiles : most);
+    const size_t np = w.mode ? (size_t)(w.pre_segs + kMaxCtas) * w.rows_p : 0;
+    const size_t ns = (size_t)(w.ss + kMaxCtas) * G;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255u) & ~(size_t)255u;
+        return here;
+    };
+    w.rec = take((size_t)(w.sp + w.ss) * sizeof(int2));
+    w.pre_o = take(np * D * 4u);
+    w.pre_l = take(np * 4u);
+    w.suf_o = take(ns * D * 4u);
+    w.suf_l = take(ns * 4u);
+    w.total = at;
+    return w;
+}
+
+cudaError_t launch_prefix(const DecodeParams &p, const Plan &w, cudaStream_t stream);
+
+}  // namespace bsattn

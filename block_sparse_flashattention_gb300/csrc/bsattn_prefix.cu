@@ -37,9 +37,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
 // 128 registers per thread at launch; the control warpgroup's surplus goes to the
-// softmax: 128 * 56 + 2 * 128 * 176 + 128 * 96 = 64512 <= 512 * 128.
+// softmax: 128 * 48 + 2 * 128 * 176 + 128 * 112 = 65536 = 512 * 128.
 constexpr int kLaunchRegs = 128;
-constexpr uint32_t kCtrlRegs = 56, kSoftmaxRegs = 176, kWidenRegs = 96;
+constexpr uint32_t kCtrlRegs = 48, kSoftmaxRegs = 176, kWidenRegs = 112;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs + 128 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;  // 128 rows x 64 fp16: one 128-byte swizzle span
@@ -336,30 +336,40 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
     const int piece = lane % R::kPieces, sub_row = lane / R::kPieces;
     const int ps_shift = p.c.page_shift, n_keys = p.prefix_len;
-    // Row of the caches (of page rows) that holds key `key` of head h, or -1.
-    auto cache_row = [&](int key, int h) -> int {
+    // Cache row of this lane's keys 4 lane .. 4 lane + 3 of a tile (one page), or -1.
+    auto look_up = [&](int tile, int h) -> int {
+        const int key = tile * kTile + 4 * lane;
         if (key >= n_keys) return -1;
         const int page = __ldg(p.prefix_table + (key >> ps_shift));
         if (page < 0 || page >= p.c.num_pages) {
-            if (lane == 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+            if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
             return -1;
         }
         return ((page * p.c.H + h) << ps_shift) + (key & ((1 << ps_shift) - 1));
     };
-    // This warp's 32 keys are two runs of 16, each inside one page.
-    struct Rows {
-        int run[2];
+    // What is loaded of a tile one tile ahead.
+    struct Ahead {
+        int run0, run1;  // cache rows of the warp's keys 0 .. 15 and 16 .. 31, or -1
+        int n;           // keys of the tile
+        float ks, vs;    // scales of the warp's key `lane`
+        uint4 vs4;       // value scales of the tile's keys 4 lane ..
     };
-    auto rows_of = [&](int tile, int h) -> Rows {
-        const int k0 = tile * kTile + warp * 32;
-        return Rows{{cache_row(k0, h), cache_row(k0 + 16, h)}};
+    auto load_scales = [&](Ahead &a, int row4, int tile) {
+        a.run0 = __shfl_sync(0xffffffffu, row4, warp * 8);
+        a.run1 = __shfl_sync(0xffffffffu, row4, warp * 8 + 4);
+        a.n = min(kTile, n_keys - tile * kTile);
+        const int row = lane < 16 ? a.run0 : a.run1;
+        const bool on = row >= 0 && warp * 32 + lane < a.n;
+        a.ks = on ? __ldg(p.c.ks + (long long)row + (lane & 15)) : 0.f;
+        a.vs = on ? __ldg(p.c.vs + (long long)row + (lane & 15)) : 0.f;
+        a.vs4 = row4 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
     };
-    auto load = [&](R &raw, const uint8_t *codes, const Rows &rw, int tile) {
+    auto load = [&](R &raw, const uint8_t *codes, const Ahead &a) {
 #pragma unroll
         for (int i = 0; i < R::kSteps; ++i) {
             const int k = i * R::kRowsPerStep + sub_row;   // of the warp's 32
-            const int row = rw.run[k >> 4];
-            const bool on = row >= 0 && tile * kTile + warp * 32 + k < n_keys;
+            const int row = i * R::kRowsPerStep < 16 ? a.run0 : a.run1;
+            const bool on = row >= 0 && warp * 32 + k < a.n;
             raw.x[i] = on ? __ldg(reinterpret_cast<const uint4 *>(codes + ((long long)row + (k & 15)) * D + piece * 16))
                           : make_uint4(0, 0, 0, 0);
         }
@@ -384,82 +394,73 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             *reinterpret_cast<uint4 *>(smem + at + ((chunk ^ (uint32_t)(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     };
-    uint32_t it = 0;
-    int exp_run = 1;
-    Walk ahead = walk;          // the tile after the current one
+    // `ahead` walks two tiles in front: its tile's page is being looked up while the tile
+    // before it is loaded and the one before that is widened.
+    Walk ahead = walk;
+    int ak = 0, tile2 = 0, h2 = 0;
+    bool more2 = ahead.next();
+    auto step = [&] {
+        if (more2 && ++ak >= ahead.n) {
+            ak = 0;
+            more2 = ahead.next();
+        }
+        tile2 = ahead.off + ak;
+        h2 = ahead.seg / w.row_blocks;
+    };
+    if (!more2) return;
+    tile2 = ahead.off;
+    h2 = ahead.seg / w.row_blocks;
+    Ahead cur;
     R kr, vr;
-    Rows rw = {};
-    int h = 0;
-    bool more = ahead.next();
-    int ak = 0;
-    if (more) {
-        h = ahead.seg / w.row_blocks;
-        rw = rows_of(ahead.off, h);
-        load(kr, p.c.k, rw, ahead.off);
-        load(vr, p.c.v, rw, ahead.off);
-    }
+    load_scales(cur, look_up(tile2, h2), tile2);
+    load(kr, p.c.k, cur);
+    load(vr, p.c.v, cur);
+    step();
+    bool more1 = more2;
+    int tile1 = tile2;
+    int row4 = more1 ? look_up(tile2, h2) : -1;
+    uint32_t it = 0;
     while (walk.next()) {
-        exp_run = 1;            // E starts anew with a segment's sums
+        int exp_run = 1;            // E starts anew with a segment's sums
         for (int k = 0; k < walk.n; ++k, ++it) {
-            const int tile = walk.off + k;
             const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
-            // scales: of the warp's own 32 keys, one per lane, and the largest value scale of the tile
-            const int kr_row = rw.run[lane >> 4];
-            const bool on = kr_row >= 0 && tile * kTile + warp * 32 + lane < n_keys;
-            const float ksc = on ? __ldg(p.c.ks + (long long)kr_row + (lane & 15)) : 0.f;
-            const float vsc = on ? __ldg(p.c.vs + (long long)kr_row + (lane & 15)) : 0.f;
+            // the largest value scale of the tile (its bits; NaN and infinity do not count)
             uint32_t top = 0;
-            {
-                const int key = tile * kTile + 4 * lane;
-                const int page = key < n_keys ? __ldg(p.prefix_table + (key >> ps_shift)) : -1;
-                if (page >= 0 && page < p.c.num_pages) {
-                    const long long row = (((long long)page * p.c.H + h) << ps_shift) + (key & ((1 << ps_shift) - 1));
-                    const float4 y = __ldg(reinterpret_cast<const float4 *>(p.c.vs + row));
-                    const float z[4] = {y.x, y.y, y.z, y.w};
+            const uint32_t v4[4] = {cur.vs4.x, cur.vs4.y, cur.vs4.z, cur.vs4.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t bits = __float_as_uint(z[i]);
-                        if (key + i < n_keys && bits < 0x7f800000u) top = max(top, bits);
-                    }
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                if (v4[i] < 0x7f800000u && 4 * lane + i < cur.n) top = max(top, v4[i]);
             top = __reduce_max_sync(0xffffffffu, top);
             exp_run = max(exp_run, (int)(top >> 23));
-            const uint32_t keep = __ballot_sync(0xffffffffu, on);
-            // where the next tile lies
-            int ntile = 0, nh = h;
-            Rows nrw = {};
-            bool nmore = more;
-            if (more && ++ak >= ahead.n) {
-                ak = 0;
-                nmore = ahead.next();
-                nh = nmore ? ahead.seg / w.row_blocks : 0;
-            }
-            if (nmore) {
-                ntile = ahead.off + ak;
-                nrw = rows_of(ntile, nh);
-            }
+            const uint32_t keep = __ballot_sync(0xffffffffu, (lane < 16 ? cur.run0 : cur.run1) >= 0 && warp * 32 + lane < cur.n);
+            // look up the tile after the next
+            step();
+            const int row4_2 = more2 ? look_up(tile2, h2) : -1;
             // K
             if (!__all_sync(0xffffffffu, mbar_wait(bar(C::bKE + st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
                 return;
 #pragma unroll
             for (int i = 0; i < R::kSteps; ++i)
                 store(C::kK + st * C::kTileBytes, i * R::kRowsPerStep + sub_row, kr.x[i], 0u);
-            reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = ksc;
-            KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
+            reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = cur.ks;
             if (lane == 0) {
+                KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
                 msg->keep[warp] = keep;
                 if (warp == 0) msg->exp = exp_run;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bKF + st));
-            if (nmore) load(kr, p.c.k, nrw, ntile);
+            const float vs = cur.vs;
+            if (more1) {
+                load_scales(cur, row4, tile1);
+                load(kr, p.c.k, cur);
+            }
             // V
             if (!__all_sync(0xffffffffu, mbar_wait(bar(C::bVE + st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
                 return;
             const float to = __uint_as_float((uint32_t)min(254, 260 - exp_run) << 23);   // 2^(6 - E)
-            const uint32_t fv = pack_f16x2(vsc * to, vsc * to);
+            const uint32_t fv = pack_f16x2(vs * to, vs * to);
 #pragma unroll
             for (int i = 0; i < R::kSteps; ++i) {
                 const int kk = i * R::kRowsPerStep + sub_row;
@@ -471,10 +472,10 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bVF + st));
-            if (nmore) load(vr, p.c.v, nrw, ntile);
-            rw = nrw;
-            h = nh;
-            more = nmore;
+            if (more1) load(vr, p.c.v, cur);
+            row4 = row4_2;
+            more1 = more2;
+            tile1 = tile2;
         }
     }
 }

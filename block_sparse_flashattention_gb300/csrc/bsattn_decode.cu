@@ -1,5 +1,6 @@
 // Attention of one query token per sequence over a paged 8-bit K/V cache, alone or
-// behind a prefix that every sequence of the batch shares.
+// behind a prefix that every sequence of the batch shares: up to 16 query heads per KV
+// head (more: bsattn_decode_rows.cu), and the kernel that joins parts.
 //
 // For one KV head, query rows r (the head's G queries of one sequence; for the prefix
 // the queries of every sequence) meet keys j:
@@ -16,262 +17,90 @@
 //
 // Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.
 //
-// Work split.  A segment is one (sequence, KV head), or one KV head of the prefix while
-// at most 16 query rows a head meet it (more take bsattn_prefix.cu); its keys are tiles
-// of 128.  All tiles of all segments form one line, cut into equal pieces, one per CTA
-// (one or two CTAs per SM): every SM reads the same number of bytes whatever the lengths.
-// A segment that lies within one piece is finished there; the parts of the others (fp32
-// output and LSE) go to the workspace and a second kernel, a programmatic dependent of
-// the first, joins them.
+// Work split.  Every warp is a worker of its own.  A segment is one (sequence, KV head),
+// or one KV head of the prefix while at most 16 query rows a head meet it (more take
+// bsattn_prefix.cu); its keys are groups of 16.  The groups of all segments form one
+// line, where a segment also counts kSegCost groups for what it costs to start and end
+// one, and the line is cut evenly over the warps of the device: every warp streams the
+// same number of bytes whatever the lengths.  A warp holds the query rows, the sums and
+// the next group's codes in registers; nothing in its loop waits for another warp.  A
+// segment within one warp's piece is finished there; the parts of the others (fp32 output
+// and LSE) go to the workspace, and a second kernel, a programmatic dependent of the
+// first, joins them.
 //
-// Roles (288 threads): warp 8 looks up lists and pages and keeps a ring of stages full
-// (TMA: codes by rows with the 128-byte or 64-byte swizzle, scales as plain copies);
-// warps 0-7 compute.  Rows come in tiles of 16; R row tiles use 8 / R warps each, which
-// share a tile's eight groups of 16 keys and join their sums at the segment's end.
-//
-// Fragments without a transpose.  In S = Q K^T the contraction index may be permuted
-// alike on both sides, so lane 4g + t takes the D / 4 consecutive codes d = (D / 4) t ..
-// of key g, four per k-step.  In O^T = V^T P^T the rows d may be permuted freely, so the
-// lane takes D / 8 consecutive codes of each of its four keys and interleaves the bytes
-// of two keys before they are widened.  P leaves the first product in the layout the
-// second wants.  With the swizzled rows none of these 16-byte loads meets a bank twice
-// (the 8-byte loads of V at D = 64 do, two ways).
+// Fragments straight from global memory.  In S = Q K^T (m16n8k16) the contraction index
+// may be permuted alike on both sides, so lane 4g + t takes 16-byte pieces t (and t + 4)
+// of key g's row, four codes per k-step.  In O^T = V^T P^T the rows d may be permuted
+// freely, so the lane takes D / 8 consecutive codes of each of its four keys and
+// interleaves the bytes of two keys before they are widened.  P leaves the first product
+// in the layout the second wants.  Every load covers whole 64- or 128-byte pieces of rows.
 #include "bsattn_internal.h"
-#include "decode_plan.cuh"
+#include "decode_common.cuh"
 #include "kv_codes.cuh"
-#include "sm100_ptx.cuh"
 
 namespace bsattn {
 
 namespace {
 
-constexpr int kConsumers = 8;                    // computing warps
-constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kSegCost = 2;  // groups of 16 keys that starting and ending a segment costs
 
-// TileMsg flags: a segment's first / last tile in this CTA, its whole line lies here.
-constexpr uint32_t kFirst = 1u, kLast = 2u, kComplete = 4u;
-
-// What the producer tells the computing warps about a stage.
-struct TileMsg {
-    int32_t seg;      // -1: no further tiles
-    int32_t lim;      // keys of the tile that count
-    uint32_t groups;  // bit i: the page of keys 16 i .. 16 i + 15 is loaded
-    uint32_t flags;
-};
-
-template <int D, bool kWide>
-struct Cfg {
-    static constexpr int kCtas = kWide ? 1 : 2;                  // per SM
-    // 4 x 33 KB or 8 x 17 KB in flight per SM; what HBM needs at 6.7 TB/s and ~1 us is 44 KB
-    static constexpr int kStages = (D == 128 ? 4 : 8) / kCtas;
-    static constexpr int kQRows = kWide ? 16 : 8;                // query rows that come with a segment's first tile
-    static constexpr uint32_t kCodes = 128u * D;                 // K or V codes of a tile
-    static constexpr uint32_t kStageBytes = 2u * kCodes;
-    static constexpr uint32_t kScales = kStages * kStageBytes;   // per stage 128 K scales, 128 V scales
-    static constexpr uint32_t kQ = kScales + kStages * 1024u;    // per stage kQRows query rows
-    static constexpr uint32_t kQBytes = kQRows * D * 2u;
-    static constexpr uint32_t kRed = kQ + kStages * kQBytes;     // join: 8 warps x (D / 2) x 32 lanes fp32
-    static constexpr uint32_t kRedBytes = kConsumers * (kWide ? D / 2 : D / 4) * 128u;
-    static constexpr uint32_t kStat = kRed + kRedBytes;          // [8 x 16 rows] (m, u, l, -)
-    static constexpr uint32_t kMsg = kStat + kConsumers * 16u * 16u;
-    static constexpr uint32_t kBar = kMsg + kStages * (uint32_t)sizeof(TileMsg);
-    static constexpr uint32_t kMisc = kBar + (2u * kStages + 1u) * 8u;  // abort flag, start, scan
-    static constexpr uint32_t kBytes = kMisc + 128u;
-    static constexpr uint32_t kAlloc = kBytes + 1024u;           // slack for 1024-byte alignment
-    static_assert(kCtas * (kAlloc + 1024u) <= 228u * 1024u, "shared memory");
-};
-
-// References before the first key: far below any score, yet finite, so that a difference
-// with it is never NaN.
-constexpr float kNoKey = -0x1p100f;
-
-struct Misc {
-    int32_t abort, start_seg;
-    long long start_off;
-    long long warp_sum[kConsumers + 1];
-};
-static_assert(sizeof(Misc) <= 128, "misc area");
-
-struct Seg {
-    int prefix, h, b, row0, rows;
-};
-
-__device__ __forceinline__ Seg segment(const DecodeParams &p, const Plan &w, int seg) {
-    Seg s;
-    if (seg < w.sp) {
-        s.prefix = 1;
-        s.h = seg / w.row_blocks;
-        s.row0 = (seg - s.h * w.row_blocks) * kLineRows;
-        s.rows = min(kLineRows, p.B * p.G - s.row0);
-        s.b = 0;
-    } else {
-        s.prefix = 0;
-        s.b = (seg - w.sp) / p.c.H;
-        s.h = seg - w.sp - s.b * p.c.H;
-        s.row0 = 0;
-        s.rows = p.G;
-    }
-    return s;
-}
-
-// Whether a segment's query rows are copied with its first tile (few whole sequences').
-template <class C>
-__device__ __forceinline__ bool rows_come_along(const Seg &s) { return s.rows <= C::kQRows && s.row0 == 0; }
-
-__device__ __forceinline__ void raise(const DecodeParams &p, int bit) {
-    if (p.err) atomicOr(p.err, bit);
-}
-
-// Keys of sequence b's own part; `check`: flag a length past the page table.
-__device__ __forceinline__ int seq_keys(const DecodeParams &p, int b, bool check) {
-    const int n = max(__ldg(p.seqlens + b), 0), cap = p.table_cols << p.c.page_shift;
-    if (n > cap && check) raise(p, BSATTN_FLAG_BAD_SEQLENS);
-    return min(n, cap);
-}
-
-struct ListRow {
-    int full, mask, nn;  // entries of the two lists, tiles an entry may name
-    long long at;        // first index entry
-};
-
-__device__ __forceinline__ ListRow list_row(const DecodeParams &p, int b, int h, int n, bool check) {
-    ListRow r;
-    r.full = r.mask = 0;
-    r.nn = p.lists_varlen ? (n + kTile - 1) / kTile : p.list_n;
-    const long long cnt_at = p.lists_varlen ? (long long)h * p.B + b : (long long)b * p.c.H + h;
-    r.at = cnt_at * p.list_n;
-    if (p.lists_varlen) {
-        const int off = __ldg(p.cu_off + b);
-        r.at = (long long)h * p.total_n + off;
-        if (off < 0 || (long long)off + r.nn > p.total_n || (p.vl && r.nn > p.list_n)) {
-            if (check) raise(p, BSATTN_FLAG_BAD_SEQLENS);
-            return r;
-        }
-    }
-    const int f = __ldg(p.full_cnt + cnt_at), m = __ldg(p.mask_cnt + cnt_at);
-    r.full = min(max(f, 0), r.nn);
-    r.mask = min(max(m, 0), r.nn);
-    if (check && (r.full != f || r.mask != m)) raise(p, BSATTN_FLAG_BAD_COUNT);
-    return r;
-}
-
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
+// Codes that are read once: 16 bytes past L1.
+__device__ __forceinline__ uint4 ld_codes16(const uint8_t *p) {
     uint4 x;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
     return x;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
+__device__ __forceinline__ uint2 ld_codes8(const uint8_t *p) {
     uint2 x;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
     return x;
 }
 
-// Byte offset in a swizzled tile of D-byte rows: 16-byte piece `c` of row `r`.
-template <int D>
-__device__ __forceinline__ uint32_t piece_at(int r, int c) {
-    if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
-    else return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
-
-// Where a finished row goes: the call's output, or a part in the workspace.
-struct RowOut {
-    int kind;        // 0 the output, 1 a prefix part, 2 a part of a sequence's own keys
-    long long row;
-};
-
-// The computing warps.
-template <int D, bool kInt8, bool kWide>
-struct Consumer {
-    using C = Cfg<D, kWide>;
-    static constexpr int kSteps = D / 16;   // k-steps of Q K^T, row tiles of V^T
-    static constexpr int kCols = kWide ? 2 : 1;  // groups of 8 query rows
+// One warp's state: kCols groups of 8 query rows.
+template <int D, bool kInt8, int kCols>
+struct Worker {
+    static constexpr int kSteps = D / 16;        // k-steps of Q K^T, row tiles of V^T
     const DecodeParams &p;
-    const Plan &w;
-    uint8_t *smem;
-    uint32_t base;
-    int warp, lane, g, t;
-    uint32_t q[kSteps][kWide ? 4 : 2];
-    float qs[kCols];                         // c_r of rows g, g + 8
+    int lane, g, t;
+    uint32_t q[kSteps][2 * kCols];
+    float qs[kCols];                             // c_r of rows g, g + 8
     float m[kCols], u[kCols], l[kCols];
     float o[kSteps][kCols][4];
-    int row_tile, key_group, key_groups;
-    uint32_t sync_phase;
+    // the group to come
+    uint32_t kx[2][D / 16], vx[4][D / 32];
+    float2 ksx[2], vsx[2];
 
-    __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kBar + 8u * (uint32_t)i; }
-
-    // All computing warps meet.
-    __device__ __forceinline__ bool meet(volatile int *abort) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(2 * C::kStages));
-        const bool ok = mbar_wait(bar(2 * C::kStages), sync_phase, abort, p.err, BSATTN_FLAG_TIMEOUT);
-        sync_phase ^= 1u;
-        return __all_sync(0xffffffffu, ok);
-    }
-
-    __device__ __forceinline__ const uint16_t *query(const Seg &s, int r) const {
-        int b = s.b, gi = r;
-        if (s.prefix) {
-            b = (s.row0 + r) / p.G;
-            gi = s.row0 + r - b * p.G;
-        }
-        return p.q + (long long)b * p.q_stride + (long long)(s.h * p.G + gi) * D;
-    }
-
-    // Starts a segment; its query rows came with the stage (sq) when they are few.
-    __device__ __forceinline__ void begin(const Seg &s, const uint8_t *sq) {
-        const int tiles = (s.rows + 15) / 16;
-        const int R = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
-        row_tile = warp % R;
-        key_group = warp / R;
-        key_groups = kConsumers / R;
+    __device__ __forceinline__ void begin(const Seg &s) {
 #pragma unroll
         for (int hf = 0; hf < kCols; ++hf) {
-            const int r = row_tile * 16 + g + 8 * hf;
-            uint32_t x[D / 8];               // D / 4 bf16 elements of the row
+            const int r = g + 8 * hf;
+            const int b = s.prefix ? r / p.G : s.b, gi = s.prefix ? r - b * p.G : r;
+            const uint16_t *row = p.q + (long long)b * p.q_stride + (long long)(s.h * p.G + gi) * D;
+            uint32_t x[D / 8], a = 0;            // D / 4 bf16 elements of the row
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint4 y = make_uint4(0, 0, 0, 0);
-                if (r < s.rows)
-                    y = rows_come_along<C>(s) ? *(reinterpret_cast<const uint4 *>(sq + r * (2 * D) + t * (D / 2)) + i)
-                                         : __ldg(reinterpret_cast<const uint4 *>(query(s, r) + t * (D / 4)) + i);
+                // pieces of 16 elements: t, t + 4
+                if (r < s.rows) y = __ldg(reinterpret_cast<const uint4 *>(row + (t + 4 * (i >> 1)) * 16) + (i & 1));
                 x[4 * i] = y.x;
                 x[4 * i + 1] = y.y;
                 x[4 * i + 2] = y.z;
                 x[4 * i + 3] = y.w;
             }
-            uint32_t a = 0;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, x[i] & 0x7fff7fffu);
             a = max(a & 0xffffu, a >> 16);
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            // biased exponent of the largest element; zero rows and rows that are not finite stay as they are
-            const int e = (a == 0 || a >= 0x7f80u) ? 127 : min(max((int)(a >> 7), 1), 253);
-            const float f = __uint_as_float((uint32_t)(254 - e) << 23);
-            // above 0: a masked key's score, -inf, stays -inf
-            qs[hf] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)e << 23), 0x1p-126f);
+            float f;
+            row_scale(a, p.scale_log2, f, qs[hf]);
+            // k-step i / 2: a piece's elements 4 s, 4 s + 1 are a0 (a1 for row g + 8), 4 s + 2, 4 s + 3 are a2 (a3)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t y = pack_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
-                // k-step i / 2: elements 4 s, 4 s + 1 are a0 (a1 for row g + 8), 4 s + 2, 4 s + 3 are a2 (a3)
-                if constexpr (kWide) q[i / 2][2 * (i & 1) + hf] = y;
-                else q[i / 2][i & 1] = y;
-            }
+            for (int i = 0; i < D / 8; ++i)
+                q[i / 2][kCols * (i & 1) + hf] =
+                    pack_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
             m[hf] = u[hf] = kNoKey;
             l[hf] = 0.f;
         }
@@ -283,74 +112,86 @@ struct Consumer {
                 for (int x = 0; x < 4; ++x) o[i][n][x] = 0.f;
     }
 
-    // 16 keys of a stage (group c), the first nv of which count (all of them: kFull).
+    // Loads of the group whose first key is row `row` of the cache.
+    __device__ __forceinline__ void load_k(int row) {
+        const uint8_t *src = p.c.k + (long long)row * D + g * D + t * 16;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 y = ld_codes16(src + nb * 8 * D + i * 64);
+                kx[nb][4 * i] = y.x;
+                kx[nb][4 * i + 1] = y.y;
+                kx[nb][4 * i + 2] = y.z;
+                kx[nb][4 * i + 3] = y.w;
+            }
+    }
+    __device__ __forceinline__ void load_scales(int row) {
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+            ksx[nb] = __ldg(reinterpret_cast<const float2 *>(p.c.ks + row + 8 * nb + 2 * t));
+            vsx[nb] = __ldg(reinterpret_cast<const float2 *>(p.c.vs + row + 8 * nb + 2 * t));
+        }
+    }
+    __device__ __forceinline__ void load_v(int row) {
+        const uint8_t *src = p.c.v + (long long)row * D + 2 * t * D + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+            const uint8_t *at = src + ((i & 1) + 8 * (i >> 1)) * D;
+            if constexpr (D == 128) {
+                const uint4 y = ld_codes16(at);
+                vx[i][0] = y.x;
+                vx[i][1] = y.y;
+                vx[i][2] = y.z;
+                vx[i][3] = y.w;
+            } else {
+                const uint2 y = ld_codes8(at);
+                vx[i][0] = y.x;
+                vx[i][1] = y.y;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void mma_q(float (&c)[4], int i, uint32_t b0, uint32_t b1) const {
+        if constexpr (kCols == 2) mma_f16(c, q[i][0], q[i][1], q[i][2], q[i][3], b0, b1);
+        else mma_f16(c, q[i][0], 0u, q[i][1], 0u, b0, b1);
+    }
+
+    // The loaded group, the first nv keys of which count (all 16: kFull); the next one,
+    // at row `next` (< 0: none), is loaded as registers come free.
     template <bool kFull>
-    __device__ __forceinline__ void keys16(uint32_t sk, uint32_t ssc, int c, int nv) {
-        const uint32_t sv = sk + C::kCodes;
+    __device__ __forceinline__ void keys16(int nv, int next) {
         float s[2][4];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
-            const int r = 16 * c + 8 * nb + g;
-            uint32_t x[D / 16];
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 y = lds128(sk + piece_at<D>(r, (D / 64) * t + i));
-                x[4 * i] = y.x;
-                x[4 * i + 1] = y.y;
-                x[4 * i + 2] = y.z;
-                x[4 * i + 3] = y.w;
-            }
             // two accumulators: half the length of the dependent chain
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 uint32_t b0, b1;
-                codes_to_f16x2<kInt8>(x[i], b0, b1);
-                if constexpr (kWide) mma_f16(acc[i & 1], q[i][0], q[i][1], q[i][2], q[i][3], b0, b1);
-                else mma_f16(acc[i & 1], q[i][0], 0u, q[i][1], 0u, b0, b1);
+                codes_to_f16x2<kInt8>(kx[nb][i], b0, b1);
+                mma_q(acc[i & 1], i, b0, b1);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nb][i] = acc[0][i] + acc[1][i];
+            for (int i = 0; i < 2 * kCols; ++i) s[nb][i] = acc[0][i] + acc[1][i];
         }
-        // V: D / 8 codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
-        uint32_t v[4][D / 32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = 2 * t + (i & 1) + 8 * (i >> 1), r = 16 * c + j;
-            if constexpr (D == 128) {
-                const uint4 y = lds128(sv + piece_at<D>(r, g));
-                v[i][0] = y.x;
-                v[i][1] = y.y;
-                v[i][2] = y.z;
-                v[i][3] = y.w;
-            } else {
-                const uint2 y = lds64(sv + piece_at<D>(r, g >> 1) + 8u * (g & 1));
-                v[i][0] = y.x;
-                v[i][1] = y.y;
-            }
-            if (!kFull && j >= nv) {  // what lies behind the last key may be NaN codes
-#pragma unroll
-                for (int x = 0; x < D / 32; ++x) v[i][x] = 0u;
-            }
-        }
+        if (next >= 0) load_k(next);
         // x = z - m and y = z + log2 vs - u + 7 of this lane's keys 2t, 2t + 1, 2t + 8, 2t + 9
         float sc[kCols][4], lv[4], x[kCols][4], y[kCols][4];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-            const uint2 kb = lds64(ssc + 4u * (16 * c + 8 * nb + 2 * t));
-            const uint2 vb = lds64(ssc + 512u + 4u * (16 * c + 8 * nb + 2 * t));
+        for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool on = kFull || 8 * nb + 2 * t + e < nv;
-                lv[2 * nb + e] = lg2_approx(__uint_as_float(e ? vb.y : vb.x));
+                lv[2 * nb + e] = lg2_approx(e ? vsx[nb].y : vsx[nb].x);
                 if (!on) lv[2 * nb + e] = -INFINITY;
 #pragma unroll
                 for (int hf = 0; hf < kCols; ++hf) {
-                    sc[hf][2 * nb + e] = s[nb][2 * hf + e] * __uint_as_float(e ? kb.y : kb.x);
+                    sc[hf][2 * nb + e] = s[nb][2 * hf + e] * (e ? ksx[nb].y : ksx[nb].x);
                     if (!on) sc[hf][2 * nb + e] = -INFINITY;
                 }
             }
-        }
+        if (next >= 0) load_scales(next);
         float top[kCols];
         auto relative = [&](int hf) {
             const float mu = m[hf] - u[hf] + 7.f;
@@ -412,6 +253,15 @@ struct Consumer {
             pb[hf][0] = pack_f16x2(ex2_approx(y[hf][0]), ex2_approx(y[hf][1]));
             pb[hf][1] = pack_f16x2(ex2_approx(y[hf][2]), ex2_approx(y[hf][3]));
         }
+        if (!kFull) {
+            // what lies behind the last key may be NaN codes
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (2 * t + (i & 1) + 8 * (i >> 1) >= nv) {
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) vx[i][w] = 0u;
+                }
+        }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
             // bytes d, d + 1 of both keys of a pair side by side, then bytes d + 2, d + 3
@@ -419,378 +269,269 @@ struct Consumer {
             for (int hi = 0; hi < 2; ++hi) {
                 const uint32_t sel = hi ? 0x7362u : 0x5140u;
                 uint32_t a0, a1, a2, a3;
-                codes_to_f16x2<kInt8>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
-                codes_to_f16x2<kInt8>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
+                codes_to_f16x2<kInt8>(__byte_perm(vx[0][w], vx[1][w], sel), a0, a1);
+                codes_to_f16x2<kInt8>(__byte_perm(vx[2][w], vx[3][w], sel), a2, a3);
 #pragma unroll
                 for (int n = 0; n < kCols; ++n) mma_f16(o[2 * w + hi][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
             }
         }
+        if (next >= 0) load_v(next);
     }
 
-    // Joins the key groups of each row tile and writes the rows: every warp leaves its
-    // sums and references in shared memory, all meet, and the warps of a row tile share
-    // out its columns; they meet again before the next segment's sums are left there.
-    __device__ __forceinline__ bool finish(const Seg &s, int seg, bool complete, volatile int *abort) {
-        float4 *stat = reinterpret_cast<float4 *>(smem + C::kStat);
-        float *red = reinterpret_cast<float *>(smem + C::kRed);
-        constexpr int kRegs = kSteps * kCols * 4;
-#pragma unroll
-        for (int hf = 0; hf < kCols; ++hf) {
-            l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-            l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-            if (t == 0)
-                stat[(row_tile * 16 + g + 8 * hf) * key_groups + key_group] = make_float4(m[hf], u[hf], l[hf], 0.f);
+    // Groups t0 .. t1 of a segment of n keys.
+    __device__ __forceinline__ void groups(const Seg &s, int n, const ListRow &lr, int t0, int t1) {
+        const bool listed = p.has_lists && !s.prefix;
+        const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
+        // cache row of group i's first key (-1: nothing to read) and how many of its keys count, one group per lane
+        auto look_up = [&](int i, int &row, int &nv) {
+            row = -1;
+            nv = 0;
+            if (i >= t1) return;
+            int key = i * 16, lim = 16;
+            if (listed) {
+                const int e = i >> 3;
+                const bool masked = e >= lr.full;
+                const int tile = __ldg((masked ? p.mask_idx + (e - lr.full) : p.full_idx + e) + lr.at);
+                if (tile < 0 || tile >= lr.nn) {
+                    if ((i & 7) == 0 || i == t0) raise(p, BSATTN_FLAG_BAD_INDEX);
+                    return;
+                }
+                if (tile >= (n + kTile - 1) / kTile) return;
+                key = tile * kTile + (i & 7) * 16;
+                if (masked && p.vl) lim = __ldg(p.vl + (long long)s.b * p.list_n + tile) - (i & 7) * 16;
+            }
+            nv = min(min(lim, 16), n - key);
+            if (nv <= 0) return;
+            const int page = __ldg(table + (key >> p.c.page_shift));
+            if (page < 0 || page >= p.c.num_pages) {
+                raise(p, BSATTN_FLAG_BAD_INDEX);
+                return;
+            }
+            row = ((page * p.c.H + s.h) << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1));
+        };
+        int row0, nv0, row1 = -1, nv1 = 0;
+        look_up(t0 + lane, row0, nv0);
+        int cur = __shfl_sync(0xffffffffu, row0, 0);
+        if (cur >= 0) {
+            load_k(cur);
+            load_scales(cur);
+            load_v(cur);
         }
-        {
-            float *x = red + warp * kRegs * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                for (int n = 0; n < kCols; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[((i * kCols + n) * 4 + e) * 32] = o[i][n][e];
+        for (int i = t0; i < t1; ++i) {
+            const int j = (i - t0) & 31;
+            if (j == 0) look_up(i + 32 + lane, row1, nv1);
+            const int nv = __shfl_sync(0xffffffffu, nv0, j);
+            const int next = __shfl_sync(0xffffffffu, j < 31 ? row0 : row1, (j + 1) & 31);
+            if (cur < 0) {
+                if (next >= 0) {
+                    load_k(next);
+                    load_scales(next);
+                    load_v(next);
+                }
+            } else if (nv == 16) {
+                keys16<true>(nv, next);
+            } else {
+                keys16<false>(nv, next);
+            }
+            cur = next;
+            if (j == 31) {
+                row0 = row1;
+                nv0 = nv1;
+            }
         }
-        if (!meet(abort)) return false;
-        const int R = kConsumers / key_groups;
+    }
+
+    // Writes the rows of a segment (or of the part of it that this worker has).
+    __device__ __forceinline__ void finish(const Plan &w, const Seg &s, int seg, int worker, bool complete) {
 #pragma unroll
-        for (int n = 0; n < kCols; ++n)
+        for (int n = 0; n < kCols; ++n) {
+            l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+            l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+            const bool empty = l[n] == 0.f;
+            // no key with a value scale above 0: O is 0, whatever the quotient of the references
+            const float own_inv = empty || u[n] == kNoKey ? 0.f : ex2_approx(u[n] - m[n] - 7.f) / l[n];
+            const float own_lse = empty ? -INFINITY : m[n] + lg2_approx(l[n]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * n + 2 * t + e;  // a row of this lane's columns
-                const float4 *st = stat + (row_tile * 16 + r) * key_groups;
-                float bm = kNoKey, bu = kNoKey, ll = 0.f;
-                for (int k = 0; k < key_groups; ++k) {
-                    bm = fmaxf(bm, st[k].x);
-                    bu = fmaxf(bu, st[k].y);
+                const float inv = __shfl_sync(0xffffffffu, own_inv, 8 * t + 4 * e);
+                const float lse2 = __shfl_sync(0xffffffffu, own_lse, 8 * t + 4 * e);
+                const int r = 8 * n + 2 * t + e;
+                if (r >= s.rows) continue;
+                float y[D / 8];                  // elements (D / 8) g ..
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    y[2 * i] = o[i][n][e] * inv;
+                    y[2 * i + 1] = o[i][n][2 + e] * inv;
                 }
-                for (int k = 0; k < key_groups; ++k) ll += st[k].z * ex2_approx(st[k].x - bm);
-                const bool empty = ll == 0.f;
-                // no key with a value scale above 0: O is 0, whatever the quotient of the references
-                const float inv = empty || bu == kNoKey ? 0.f : ex2_approx(bu - bm - 7.f) / ll;
-                const float lse2 = empty ? -INFINITY : bm + lg2_approx(ll);
-                if (row_tile * 16 + r < s.rows) {
-                    const RowOut at = row_out(s, seg, complete, row_tile * 16 + r);
-                    for (int i = key_group; i < kSteps; i += key_groups) {
-                        float y0 = 0.f, y1 = 0.f;
-                        for (int k = 0; k < key_groups; ++k) {
-                            const float f = ex2_approx(st[k].y - bu);
-                            const float *x = red + (k * R + row_tile) * kRegs * 32 + ((i * kCols + n) * 4 + e) * 32 + lane;
-                            y0 = fmaf(f, x[0], y0);
-                            y1 = fmaf(f, x[64], y1);
-                        }
-                        store_pair(at, g * (D / 8) + 2 * i, y0 * inv, y1 * inv);
-                    }
-                    if (key_group == 0 && g == 0) store_lse(at, lse2);
+                RowOut at;
+                if (!s.prefix && complete && w.mode == kNoPrefix) at = RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
+                else if (s.prefix) at = RowOut{1, ((long long)seg + worker) * w.rows_p + r};
+                else at = RowOut{2, ((long long)(seg - w.sp) + worker) * p.G + r};
+                if (at.kind == 0 && !p.out_f32) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at.row * D + g * (D / 8));
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                            pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+                } else {
+                    float *dst = at.kind == 0 ? static_cast<float *>(p.out)
+                                              : reinterpret_cast<float *>(p.ws + (at.kind == 1 ? w.pre_o : w.suf_o));
+                    dst += at.row * D + g * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        reinterpret_cast<float4 *>(dst)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 }
-            }
-        return meet(abort);
-    }
-
-    __device__ __forceinline__ RowOut row_out(const Seg &s, int seg, bool complete, int r) const {
-        if (!s.prefix && complete && w.mode == kNoPrefix) return RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
-        const long long part = (seg - (s.prefix ? 0 : w.sp)) + (long long)blockIdx.x;
-        return s.prefix ? RowOut{1, part * w.rows_p + r} : RowOut{2, part * p.G + r};
-    }
-
-    __device__ __forceinline__ void store_pair(const RowOut &at, int d, float x, float y) const {
-        if (at.kind == 0 && !p.out_f32) {
-            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at.row * D + d) = pack_bf16x2(x, y);
-        } else {
-            float *o = at.kind == 0 ? static_cast<float *>(p.out)
-                                    : reinterpret_cast<float *>(p.ws + (at.kind == 1 ? w.pre_o : w.suf_o));
-            *reinterpret_cast<float2 *>(o + at.row * D + d) = make_float2(x, y);
-        }
-    }
-
-    __device__ __forceinline__ void store_lse(const RowOut &at, float lse2) const {
-        if (at.kind == 0) p.lse[at.row] = lse2 * 0.69314718055994530942f;
-        else reinterpret_cast<float *>(p.ws + (at.kind == 1 ? w.pre_l : w.suf_l))[at.row] = lse2;
-    }
-
-    __device__ __forceinline__ void run(volatile int *abort) {
-        Seg s = {};
-        for (uint32_t it = 0;; ++it) {
-            const uint32_t st = it % C::kStages;
-            const bool ok = mbar_wait(bar(st), (it / C::kStages) & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
-            if (!__all_sync(0xffffffffu, ok)) return;
-            const TileMsg msg = reinterpret_cast<const TileMsg *>(smem + C::kMsg)[st];
-            if (msg.seg < 0) return;
-            if (msg.flags & kFirst) {
-                s = segment(p, w, msg.seg);
-                begin(s, smem + C::kQ + st * C::kQBytes);
-            }
-            const uint32_t sk = base + st * C::kStageBytes, ssc = base + C::kScales + st * 1024u;
-            for (int c = key_group; c < 8; c += key_groups) {
-                const int nv = min(16, msg.lim - 16 * c);
-                if (nv <= 0 || !((msg.groups >> c) & 1u)) continue;
-                if (nv == 16) keys16<true>(sk, ssc, c, nv);
-                else keys16<false>(sk, ssc, c, nv);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::kStages + st));
-            if (msg.flags & kLast) {
-                if (!finish(s, msg.seg, (msg.flags & kComplete) != 0, abort)) return;
+                if (g == 0) store_lse(p, w, at, lse2);
             }
         }
     }
 };
 
-template <int D, bool kInt8, bool kWide>
-__global__ void __launch_bounds__(kThreads, Cfg<D, kWide>::kCtas)
-    bsattn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w,
-                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-    using C = Cfg<D, kWide>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (base - raw);
-    Misc *misc = reinterpret_cast<Misc *>(smem + C::kMisc);
-    volatile int *abort = &misc->abort;
-    auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
+// CTAs per SM: with one group of columns 128 registers a thread suffice for two; two
+// groups take 168 and leave room for three quarters of that.
+template <int kCols>
+constexpr int kCtasPerSm = kCols == 1 ? 2 : 1;
+template <int kCols>
+constexpr int kWarps = kCols == 1 ? kStreamWarps : 12;
+
+template <int D, bool kInt8, int kCols>
+__global__ void __launch_bounds__(kWarps<kCols> * 32, kCtasPerSm<kCols>)
+    bsattn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w) {
+    constexpr int kW = kWarps<kCols>, kThreads = kW * 32;
+    __shared__ long long warp_sum[kW], start_at[kW];
+    __shared__ int start_seg[kW];
     const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
     grid_launch_dependents();  // the joining kernel may take its place; it waits for this grid
-    if (tid == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(s), 1);
-            mbar_init(bar(C::kStages + s), kConsumers);
-        }
-        mbar_init(bar(2 * C::kStages), kConsumers);
-        misc->abort = 0;
-        fence_barrier_init();
-        fence_proxy_async_smem();
-    }
 
-    // Where this CTA's piece of the line of tiles begins.  Each thread sums the tiles of a
-    // run of sequences (or, with lists, of (sequence, head) pairs); CTA c also writes the
-    // records of every gridDim-th of them: the CTAs its segments' parts lie in.
-    const int nt_pre = w.sp ? (p.prefix_len + kTile - 1) / kTile : 0;
-    const long long tiles_pre = (long long)w.sp * nt_pre;
+    // Where each worker's piece of the line begins.  Each thread sums the cost of a run
+    // of sequences (or, with lists, of (sequence, head) pairs); CTA c also writes the
+    // records of every gridDim-th of them: the workers its segments' parts lie with.
+    const int g_pre = w.sp ? (p.prefix_len + 15) / 16 : 0;
+    const long long line_pre = (long long)w.sp * (g_pre + kSegCost);
     const int units = p.has_lists ? p.B * p.c.H : p.B, per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
-    auto unit_tiles = [&](int x, bool check) -> int {
-        if (!p.has_lists) return (seq_keys(p, x, check) + kTile - 1) / kTile;
+    auto unit_groups = [&](int x, bool check) -> int {
+        if (!p.has_lists) return (seq_keys(p, x, check) + 15) / 16;
         const int b = x / p.c.H, h = x - b * p.c.H;
         const ListRow r = list_row(p, b, h, seq_keys(p, b, check && h == 0), check);
-        return r.full + r.mask;
+        return 8 * (r.full + r.mask);
     };
     const int reps = p.has_lists ? 1 : p.c.H;  // segments of a unit, of equal length
     long long sum = 0;
-    for (int x = u0; x < u1; ++x) sum += (long long)unit_tiles(x, x % (int)gridDim.x == (int)blockIdx.x) * reps;
+    for (int x = u0; x < u1; ++x) {
+        const int n = unit_groups(x, x % (int)gridDim.x == (int)blockIdx.x);
+        sum += n ? (long long)(n + kSegCost) * reps : 0;
+    }
     long long incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += y;
     }
-    if (lane == 31) misc->warp_sum[warp] = incl;
+    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    long long at = tiles_pre + incl - sum, total = tiles_pre;
-    for (int i = 0; i <= kConsumers; ++i) {
-        if (i < warp) at += misc->warp_sum[i];
-        total += misc->warp_sum[i];
+    long long at = line_pre + incl - sum, total = line_pre;
+    for (int i = 0; i < kW; ++i) {
+        if (i < warp) at += warp_sum[i];
+        total += warp_sum[i];
     }
-    // no CTA's piece is empty while a later one's is not: a segment's parts are consecutive
-    const long long cuts = min((long long)gridDim.x, total), cta = blockIdx.x;
-    const long long lo = cta < cuts ? total * cta / cuts : 0, hi = cta < cuts ? total * (cta + 1) / cuts : 0;
-    auto owner = [&](long long tile) -> int { return (int)(((tile + 1) * cuts - 1) / total); };
-    int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
-    if (tid == 0 && lo < hi && lo < tiles_pre) {
-        misc->start_seg = (int)(lo / nt_pre);
-        misc->start_off = lo % nt_pre;
-    }
-    for (int x = (int)blockIdx.x * kThreads + tid; x < w.sp; x += (int)gridDim.x * kThreads)
-        rec[x] = make_int2(owner((long long)x * nt_pre), owner((long long)(x + 1) * nt_pre - 1));
-    for (int x = u0; x < u1; ++x) {
-        const bool mine = x % (int)gridDim.x == (int)blockIdx.x;
-        const int n = unit_tiles(x, false);
-        const long long end = at + (long long)n * reps;
-        if (lo < hi && lo >= at && lo < end) {
-            misc->start_seg = w.sp + x * reps + (int)((lo - at) / n);
-            misc->start_off = (lo - at) % n;
+    // pieces of at least one place each: a segment's parts lie with consecutive workers
+    const long long cuts = min((long long)gridDim.x * kW, total);
+    auto first_of = [&](long long worker) -> long long { return total * worker / cuts; };
+    auto owner = [&](long long place) -> int { return (int)(((place + 1) * cuts - 1) / total); };
+    auto begins_at = [&](long long begin, long long len, int seg, long long seg_len) {
+        // workers of this CTA whose pieces begin within [begin, begin + len): segments seg, seg + 1, ... of seg_len
+        for (int x = 0; x < kW; ++x) {
+            const long long worker = (long long)blockIdx.x * kW + x;
+            if (worker >= cuts) return;
+            const long long lo = first_of(worker);
+            if (lo >= begin && lo < begin + len) {
+                const long long k = (lo - begin) / seg_len;
+                start_seg[x] = seg + (int)k;
+                start_at[x] = begin + k * seg_len;
+            }
         }
-        if (mine)
+    };
+    int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
+    if (w.sp && tid == 0) begins_at(0, line_pre, 0, g_pre + kSegCost);
+    for (int x = (int)blockIdx.x * kThreads + tid; x < w.sp; x += (int)gridDim.x * kThreads) {
+        const long long a = (long long)x * (g_pre + kSegCost) + kSegCost;
+        rec[x] = make_int2(owner(a), owner(a + g_pre - 1));
+    }
+    for (int x = u0; x < u1; ++x) {
+        const int n = unit_groups(x, false);
+        const long long len = n ? (long long)(n + kSegCost) * reps : 0;
+        if (len) begins_at(at, len, w.sp + x * reps, n + kSegCost);
+        if (x % (int)gridDim.x == (int)blockIdx.x)
             for (int r = 0; r < reps; ++r) {
-                const long long a = at + (long long)r * n;
+                const long long a = at + (long long)r * (n + kSegCost) + kSegCost;
                 rec[w.sp + x * reps + r] = n ? make_int2(owner(a), owner(a + n - 1)) : make_int2(0, -1);
             }
-        at = end;
+        at += len;
     }
     __syncthreads();
-    if (lo >= hi) {
-        if (w.mode == kOwnKernel) grid_dependency_wait();
-        return;
-    }
-
-    if (warp == kConsumers) {
-        // ------------------------------------------------------- producer --
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
-        const int ps_shift = p.c.page_shift, ps = 1 << ps_shift;
-        const int ppt = kTile >> ps_shift, batch = 32 / ppt;   // pages per tile, tiles looked up at once
-        const int mine = lane / ppt, sub = lane - mine * ppt;
-        const uint32_t page_bytes = (uint32_t)ps * (2u * D + 8u);
-        TileMsg *msgs = reinterpret_cast<TileMsg *>(smem + C::kMsg);
-        uint32_t it = 0;
-        bool ok = true;
-        // A window of 32 segments, one per lane; x counts tiles from the window's first.
-        int seg0 = misc->start_seg;
-        long long x = misc->start_off, pos = lo;
-        while (ok && pos < hi) {
-            const int ws = seg0 + lane;
-            int n = 0, nt = 0;
-            ListRow r = {};
-            if (ws < w.sp) {
-                n = p.prefix_len;
-                nt = nt_pre;
-            } else if (ws < w.sp + w.ss) {
-                const int b = (ws - w.sp) / p.c.H;
-                n = seq_keys(p, b, false);
-                nt = (n + kTile - 1) / kTile;
-                if (p.has_lists) {
-                    r = list_row(p, b, ws - w.sp - b * p.c.H, n, false);
-                    nt = r.full + r.mask;
-                }
+    const long long worker = (long long)blockIdx.x * kW + warp;
+    if (worker < cuts) {
+        const long long lo = first_of(worker), hi = first_of(worker + 1);
+        Worker<D, kInt8, kCols> k{p, lane, lane >> 2, lane & 3};
+        int seg = start_seg[warp];
+        for (long long begin = start_at[warp]; begin < hi; ++seg) {
+            const Seg s = segment(p, w, seg);
+            const int n = s.prefix ? p.prefix_len : seq_keys(p, s.b, false);
+            ListRow lr = {};
+            int g = (n + 15) / 16;
+            if (p.has_lists && !s.prefix) {
+                lr = list_row(p, s.b, s.h, n, false);
+                g = 8 * (lr.full + lr.mask);
             }
-            int incl = nt;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += y;
+            if (g == 0) continue;
+            const long long first = begin + kSegCost;
+            const int t0 = (int)max(0ll, min((long long)g, lo - first)), t1 = (int)max(0ll, min((long long)g, hi - first));
+            if (t0 < t1) {
+                k.begin(s);
+                k.groups(s, n, lr, t0, t1);
+                k.finish(w, s, seg, (int)worker, t0 == 0 && t1 == g);
             }
-            const int in_window = __shfl_sync(0xffffffffu, incl, 31);
-            const int end = (int)min((long long)in_window, x + (hi - pos));
-            for (int x0 = (int)x; ok && x0 < end; x0 += batch) {
-                // lane: page `sub` of tile x0 + mine; the segment is the first whose end lies behind it
-                const int xt = min(x0 + mine, end - 1);
-                int at = 0;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    if (__shfl_sync(0xffffffffu, incl, at + d - 1) <= xt) at += d;
-                const int seg = seg0 + at;
-                const int sn = __shfl_sync(0xffffffffu, n, at), snt = __shfl_sync(0xffffffffu, nt, at);
-                const int start = __shfl_sync(0xffffffffu, incl, at) - snt, i = xt - start;
-                const int full = __shfl_sync(0xffffffffu, r.full, at), nn = __shfl_sync(0xffffffffu, r.nn, at);
-                const long long list_at = __shfl_sync(0xffffffffu, r.at, at);
-                const Seg s = segment(p, w, seg);
-                int tile = i, lim = kTile, page = -1;
-                if (p.has_lists && !s.prefix) {
-                    const bool masked = i >= full;
-                    tile = __ldg((masked ? p.mask_idx + (i - full) : p.full_idx + i) + list_at);
-                    if (tile < 0 || tile >= nn) {
-                        if (sub == 0) raise(p, BSATTN_FLAG_BAD_INDEX);
-                        tile = -1;
-                    } else if (masked && p.vl) {
-                        lim = min(kTile, __ldg(p.vl + (long long)s.b * p.list_n + tile));
-                    }
-                }
-                lim = tile < 0 || tile * (long long)kTile >= sn ? 0 : min(lim, sn - tile * kTile);
-                if ((sub << ps_shift) < lim) {
-                    const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
-                    page = __ldg(table + ((tile * kTile) >> ps_shift) + sub);
-                    if (page < 0 || page >= p.c.num_pages) {
-                        raise(p, BSATTN_FLAG_BAD_INDEX);
-                        page = -1;
-                    }
-                }
-                // the CTA's piece begins at x (of this window) and ends hi - pos tiles behind it
-                uint32_t fl = xt == max(start, (int)x) ? kFirst : 0u;
-                if (i == snt - 1 || xt + 1 == x + (hi - pos)) fl |= kLast;
-                if (start >= (int)x && i == snt - 1) fl |= kComplete;
-                const bool q_rows = (fl & kFirst) && rows_come_along<C>(s);
-                for (int j = 0; j < batch && x0 + j < end; ++j, ++it) {
-                    const uint32_t st = it % C::kStages;
-                    ok = mbar_wait(bar(C::kStages + st), ((it / C::kStages) & 1u) ^ 1u, abort, p.err,
-                                   BSATTN_FLAG_TIMEOUT);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    const bool load = mine == j && page >= 0;
-                    const uint32_t loads = __ballot_sync(0xffffffffu, load);
-                    const uint32_t groups = __reduce_or_sync(
-                        0xffffffffu, load ? ((1u << (ps >> 4)) - 1u) << (sub * (ps >> 4)) : 0u);
-                    if (mine == j && sub == 0) {
-                        msgs[st] = TileMsg{seg, lim, groups, fl};
-                        const uint32_t bytes = (uint32_t)__popc(loads) * page_bytes + (q_rows ? s.rows * 2u * D : 0u);
-                        if (bytes) mbar_arrive_expect_tx(bar(st), bytes);
-                        else mbar_arrive(bar(st));
-                        if (q_rows) {
-                            const uint32_t dst = base + C::kQ + st * C::kQBytes;
-                            const int seqs = s.prefix ? s.rows / p.G : 1;
-                            for (int b = 0; b < seqs; ++b)
-                                bulk_g2s_lead(1u, dst + (uint32_t)b * p.G * 2u * D,
-                                              p.q + (long long)(s.b + b) * p.q_stride + (long long)s.h * p.G * D,
-                                              (uint32_t)p.G * 2u * D, bar(st));
-                        }
-                    }
-                    __syncwarp();
-                    if (load) {
-                        const int row = ((page * p.c.H + s.h) << ps_shift), in = sub << ps_shift;
-                        const uint32_t dst = base + st * C::kStageBytes + (uint32_t)in * D;
-                        const uint32_t sc = base + C::kScales + st * 1024u + 4u * (uint32_t)in;
-                        tma_load_2d(dst, &tk, bar(st), 0, row);
-                        tma_load_2d(dst + C::kCodes, &tv, bar(st), 0, row);
-                        bulk_g2s_lead(1u, sc, p.c.ks + row, 4u * (uint32_t)ps, bar(st));
-                        bulk_g2s_lead(1u, sc + 512u, p.c.vs + row, 4u * (uint32_t)ps, bar(st));
-                    }
-                }
-            }
-            pos += end - x;
-            x = 0;
-            seg0 += 32;
+            begin = first + g;
         }
-        if (ok) {
-            const uint32_t st = it % C::kStages;
-            ok = mbar_wait(bar(C::kStages + st), ((it / C::kStages) & 1u) ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
-            if (__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) {
-                    msgs[st] = TileMsg{-1, 0, 0u, 0u};
-                    mbar_arrive(bar(st));
-                }
-                ++it;
-            }
-        }
-        // no copy into this CTA's shared memory may be in flight when it ends
-        for (uint32_t s = 0; s < (uint32_t)C::kStages; ++s)
-            if (it > s) mbar_wait_drain(bar((int)((it - 1 - s) % C::kStages)), ((it - 1 - s) / C::kStages) & 1u);
-        // Launched beside the prefix kernel: this grid must not end before that one, since
-        // the join waits for this grid alone.
-        if (w.mode == kOwnKernel) grid_dependency_wait();
-    } else {
-        Consumer<D, kInt8, kWide> c{p, w, smem, base, warp, lane, lane >> 2, lane & 3};
-        c.sync_phase = 0u;
-        c.run(abort);
     }
+    // Launched beside the prefix kernel: this grid must not end before that one, since the
+    // join waits for this grid alone.
+    if (w.mode == kOwnKernel) grid_dependency_wait();
 }
 
 // Joins the parts of one output row: out = sum_i o_i 2^(L_i - L), L = log2 sum_i 2^L_i.
-// One warp per row; a row that the first kernel finished is left alone.
+// One block per row, its warps share the parts; a row that the first kernel finished is
+// left alone.
+constexpr int kJoinWarps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(128) bsattn_decode_join_kernel(const __grid_constant__ DecodeParams p,
-                                                                const __grid_constant__ Plan w) {
+__global__ void __launch_bounds__(kJoinWarps * 32) bsattn_decode_join_kernel(const __grid_constant__ DecodeParams p,
+                                                                            const __grid_constant__ Plan w) {
     grid_dependency_wait();
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (long long)p.B * p.Hq) return;
-    const int b = (int)(row / p.Hq), hq = (int)(row - (long long)b * p.Hq), h = hq / p.G, gi = hq - h * p.G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = (int)blockIdx.x;
+    const int b = row / p.Hq, hq = row - b * p.Hq, h = hq / p.G, gi = hq - h * p.G;
     const int2 *rec = reinterpret_cast<const int2 *>(p.ws + w.rec);
     const int2 rs = rec[w.sp + b * p.c.H + h];
     // the prefix's parts of this row: np of them, pre_step rows apart
     int np = 0;
     long long pre_row = 0, pre_step = w.rows_p;
-    if (w.mode) {
-        const int r = b * p.G + gi, blk = r / w.block_rows, rb = r - blk * w.block_rows, sp = h * w.row_blocks + blk;
-        if (w.mode == kInLine) {
-            const int2 rp = rec[sp];
-            np = rp.y - rp.x + 1;
-            pre_row = (long long)(sp + rp.x) * w.rows_p + rb;
-        } else {
-            const int nt = (p.prefix_len + kTile - 1) / kTile;
-            const int c0 = w.pre_owner((long long)sp * nt, nt), c1 = w.pre_owner((long long)(sp + 1) * nt - 1, nt);
-            np = c1 - c0 + 1;
-            pre_row = (long long)(sp + c0) * w.rows_p + rb;
-            if (p.B * p.G - blk * kBlockRows <= kTile) {  // both slots hold parts of the row
-                np *= 2;
-                pre_step = kTile;
-            }
+    const int r = b * p.G + gi;
+    if (w.mode == kInLine) {
+        const int2 rp = rec[h];
+        np = rp.y - rp.x + 1;
+        pre_row = (long long)(h + rp.x) * w.rows_p + r;
+    } else if (w.mode == kOwnKernel) {
+        const int blk = r / kBlockRows, sp = h * w.row_blocks + blk;
+        const int nt = (p.prefix_len + kTile - 1) / kTile;
+        const int c0 = w.pre_owner((long long)sp * nt, nt), c1 = w.pre_owner((long long)(sp + 1) * nt - 1, nt);
+        np = c1 - c0 + 1;
+        pre_row = (long long)(sp + c0) * w.rows_p + (r - blk * kBlockRows);
+        if (p.B * p.G - blk * kBlockRows <= kTile) {  // both slots hold parts of the row
+            np *= 2;
+            pre_step = kTile;
         }
     } else if (rs.x == rs.y) {
         return;
@@ -800,62 +541,54 @@ __global__ void __launch_bounds__(128) bsattn_decode_join_kernel(const __grid_co
     const float *pre_o = reinterpret_cast<const float *>(p.ws + w.pre_o), *pre_l = reinterpret_cast<const float *>(p.ws + w.pre_l);
     const float *suf_o = reinterpret_cast<const float *>(p.ws + w.suf_o), *suf_l = reinterpret_cast<const float *>(p.ws + w.suf_l);
     auto at = [&](int i) -> long long { return i < np ? pre_row + i * pre_step : suf_row + (long long)(i - np) * p.G; };
+    // every warp finds the largest LSE; a NaN is carried by the weights
     float mx = -INFINITY;
-    bool nan = false;
-    for (int i = lane; i < n; i += 32) {
-        const float x = (i < np ? pre_l : suf_l)[at(i)];
-        mx = fmaxf(mx, x);
-        nan |= x != x;
-    }
+    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, (i < np ? pre_l : suf_l)[at(i)]);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    nan = __any_sync(0xffffffffu, nan);
+    const float base = mx == -INFINITY ? 0.f : mx;
     float o[E], l = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const long long r = at(i);
-        const float x = ex2_approx((i < np ? pre_l : suf_l)[r] - base);
-        const float *src = (i < np ? pre_o : suf_o) + r * D + lane * E;
+    for (int i = warp; i < n; i += kJoinWarps) {
+        const long long at_i = at(i);
+        const float x = ex2_approx((i < np ? pre_l : suf_l)[at_i] - base);
+        const float *src = (i < np ? pre_o : suf_o) + at_i * D + lane * E;
         l += x;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(x, src[e], o[e]);
     }
-    const bool empty = l == 0.f;
+    __shared__ float so[kJoinWarps][D], sl[kJoinWarps];
+    if (n > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+        if (lane == 0) sl[warp] = l;
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) {
+            l += sl[k];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += so[k][lane * E + e];
+        }
+    } else if (warp > 0) {
+        return;
+    }
+    const bool empty = l == 0.f;   // NaN is not empty
     const float inv = empty ? 0.f : 1.f / l;
+    const long long dst = (long long)row * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        o[e] *= inv;
-        if (p.out_f32) static_cast<float *>(p.out)[row * D + lane * E + e] = o[e];
+    for (int e = 0; e < E; e += 2) {
+        const float y0 = o[e] * inv, y1 = o[e + 1] * inv;
+        if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + dst + e) = make_float2(y0, y1);
+        else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + dst + e) = pack_bf16x2(y0, y1);
     }
-    if (!p.out_f32) {
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + row * D + lane * E + e) = pack_bf16x2(o[e], o[e + 1]);
-    }
-    if (lane == 0)
-        p.lse[row] = nan ? __uint_as_float(0x7fc00000u)
-                         : empty ? -INFINITY : (base + lg2_approx(l)) * 0.69314718055994530942f;
+    if (lane == 0) p.lse[row] = empty ? -INFINITY : (base + lg2_approx(l)) * 0.69314718055994530942f;
 }
 
-template <int D, bool kInt8, bool kWide>
-cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int sms,
-                   cudaStream_t stream) {
-    using C = Cfg<D, kWide>;
-    static int attr_set_for_device[64] = {0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set_for_device[dev]) {
-        e = cudaFuncSetAttribute(bsattn_decode_kernel<D, kInt8, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)C::kAlloc);
-        if (e != cudaSuccess) return e;
-        attr_set_for_device[dev] = 1;
-    }
-    const int grid = min(sms * C::kCtas, kMaxCtas);
+template <int D, bool kInt8, int kCols>
+cudaError_t launch(const DecodeParams &p, const Plan &w, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -864,25 +597,34 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, 
     cfg.stream = stream;
     // beside the prefix kernel, whose results it does not need; else after what came before
     cfg.numAttrs = w.mode == kOwnKernel ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kAlloc;
-    e = cudaLaunchKernelEx(&cfg, bsattn_decode_kernel<D, kInt8, kWide>, p, w, tk, tv);
-    if (e != cudaSuccess) return e;
-    cfg.dynamicSmemBytes = 0;
-    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.Hq + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D>, p, w);
+    const int most = kMaxCtas * kStreamWarps / kWarps<kCols>;
+    const int grid = sms * kCtasPerSm<kCols>;
+    cfg.gridDim = dim3((unsigned)(grid < most ? grid : most));
+    cfg.blockDim = dim3(kWarps<kCols> * 32);
+    return cudaLaunchKernelEx(&cfg, bsattn_decode_kernel<D, kInt8, kCols>, p, w);
 }
 
-template <int D, bool kInt8>
-cudaError_t launch_rows(const DecodeParams &p, const Plan &w, const CUtensorMap &tk, const CUtensorMap &tv, int sms,
-                        cudaStream_t stream) {
-    // 8 query rows fill one group of columns; more take the build with two
-    const int rows = w.mode == kInLine ? w.rows_p : 0;
-    if (max(rows, p.G) <= 8) return launch<D, kInt8, false>(p, w, tk, tv, sms, stream);
-    return launch<D, kInt8, true>(p, w, tk, tv, sms, stream);
+template <int D>
+cudaError_t launch_d(const DecodeParams &p, const Plan &w, int sms, cudaStream_t stream) {
+    cudaError_t e;
+    if (!w.streaming) {
+        e = launch_decode_rows(p, w, sms, stream);
+    } else if (p.G <= 8 && (w.mode != kInLine || p.B * p.G <= 8)) {
+        e = p.c.int8 ? launch<D, true, 1>(p, w, sms, stream) : launch<D, false, 1>(p, w, sms, stream);
+    } else {
+        e = p.c.int8 ? launch<D, true, 2>(p, w, sms, stream) : launch<D, false, 2>(p, w, sms, stream);
+    }
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hq));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D>, p, w);
 }
 
 }  // namespace
@@ -895,20 +637,11 @@ cudaError_t launch_decode(const DecodeParams &p, cudaStream_t stream) {
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const Plan w = make_plan(p.B, p.c.H, p.G, p.c.D, p.prefix_len, sms);
-    CUtensorMap tk, tv;
-    const long long rows = ((long long)(p.c.num_pages > 0 ? p.c.num_pages : 1) * p.c.H) << p.c.page_shift;
-    if (!encode_code_rows(&tk, p.c.k, rows, p.c.D, 1 << p.c.page_shift) ||
-        !encode_code_rows(&tv, p.c.v, rows, p.c.D, 1 << p.c.page_shift))
-        return cudaErrorInvalidValue;
     if (w.mode == kOwnKernel) {
         const cudaError_t e = launch_prefix(p, w, stream);
         if (e != cudaSuccess) return e;
     }
-    if (p.c.D == 128)
-        return p.c.int8 ? launch_rows<128, true>(p, w, tk, tv, sms, stream)
-                        : launch_rows<128, false>(p, w, tk, tv, sms, stream);
-    return p.c.int8 ? launch_rows<64, true>(p, w, tk, tv, sms, stream)
-                    : launch_rows<64, false>(p, w, tk, tv, sms, stream);
+    return p.c.D == 128 ? launch_d<128>(p, w, sms, stream) : launch_d<64>(p, w, sms, stream);
 }
 
 }  // namespace bsattn

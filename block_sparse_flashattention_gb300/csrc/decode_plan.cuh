@@ -1,26 +1,30 @@
 // How a decode call's work is numbered and where its parts lie in the workspace; shared
-// by the decode kernel (bsattn_decode.cu) and the prefix kernel (bsattn_prefix.cu).
+// by the decode kernels (bsattn_decode.cu, bsattn_decode_rows.cu) and the prefix kernel
+// (bsattn_prefix.cu).
 #pragma once
 
 #include "bsattn_internal.h"
 
 namespace bsattn {
 
-constexpr int kMaxCtas = 320;     // CTAs whose parts the workspace has room for
-constexpr int kLineRows = 128;    // query rows of a prefix segment in the decode kernel's line
-constexpr int kBlockRows = 256;   // and in the prefix kernel
+constexpr int kMaxCtas = 320;      // CTAs whose parts the workspace has room for
+constexpr int kStreamWarps = 8;    // warps of a streaming CTA, each a worker of its own
+constexpr int kStreamRows = 16;    // query rows a streaming worker holds
+constexpr int kBlockRows = 256;    // query rows of a segment in the prefix kernel
 
-// Up to 16 query rows a KV head meet the prefix inside the decode kernel's line (kInLine);
-// more run in a kernel of their own (kOwnKernel).
+// Up to 16 query rows a KV head meet the prefix inside the streaming kernel's line
+// (kInLine); more run in a kernel of their own (kOwnKernel).
 enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2 };
 
-// Segments: of the prefix, (KV head, block of query rows), head-major; of the sequences'
-// own keys, (sequence, KV head).  A line of tiles is cut over CTAs, and part `segment +
-// cta` holds what a CTA computed of a segment: from one part of the line to the next
-// either the segment or the CTA advances, so no two parts share a number.
+// Segments: of the prefix, one per KV head (kInLine) or (KV head, block of 256 query
+// rows); of the sequences' own keys, (sequence, KV head).  A line of keys is cut over
+// workers (warps or CTAs), and part `segment + worker` holds what a worker computed of a
+// segment: from one part of the line to the next either the segment or the worker
+// advances, so no two parts share a number.
 struct Plan {
     int mode;
-    int row_blocks, pre_segs, block_rows;  // prefix: blocks per head, segments, rows of a block
+    int streaming;                         // G <= 16: bsattn_decode.cu, else bsattn_decode_rows.cu
+    int row_blocks, pre_segs;              // prefix kernel: blocks per head, segments
     int rows_p;                            // rows a prefix part has room for
     int sp, ss;                            // prefix and own segments of the decode kernel's line
     int pre_cuts;                          // CTAs of the prefix kernel
@@ -40,19 +44,21 @@ struct Plan {
 inline Plan make_plan(int B, int H, int G, int D, int prefix_len, int sms) {
     Plan w = {};
     const int rows = B * G;
-    w.mode = prefix_len <= 0 ? kNoPrefix : rows <= 16 ? kInLine : kOwnKernel;
-    w.block_rows = w.mode == kOwnKernel ? kBlockRows : kLineRows;
-    w.row_blocks = w.mode ? (rows + w.block_rows - 1) / w.block_rows : 0;
+    w.mode = prefix_len <= 0 ? kNoPrefix : rows <= kStreamRows ? kInLine : kOwnKernel;
+    w.streaming = G <= kStreamRows ? 1 : 0;
+    w.row_blocks = w.mode == kOwnKernel ? (rows + kBlockRows - 1) / kBlockRows : 0;
     w.pre_segs = H * w.row_blocks;
     // the prefix kernel's parts hold both slots of 128 rows
-    w.rows_p = w.mode == kOwnKernel ? kBlockRows : rows < kLineRows ? rows : kLineRows;
-    w.sp = w.mode == kInLine ? w.pre_segs : 0;
+    w.rows_p = w.mode == kOwnKernel ? kBlockRows : rows;
+    w.sp = w.mode == kInLine ? H : 0;
     w.ss = B * H;
     const long long tiles = (long long)w.pre_segs * ((prefix_len + kTile - 1) / kTile);
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
     w.pre_cuts = (int)(tiles < most ? tiles : most);
-    const size_t np = w.mode ? (size_t)(w.pre_segs + kMaxCtas) * w.rows_p : 0;
-    const size_t ns = (size_t)(w.ss + kMaxCtas) * G;
+    const size_t workers = w.streaming ? kMaxCtas * kStreamWarps : kMaxCtas;
+    const size_t np = w.mode == kOwnKernel ? (size_t)(w.pre_segs + kMaxCtas) * w.rows_p
+                    : w.mode == kInLine    ? ((size_t)w.sp + workers) * w.rows_p : 0;
+    const size_t ns = (w.ss + workers) * G;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -69,5 +75,6 @@ inline Plan make_plan(int B, int H, int G, int D, int prefix_len, int sms) {
 }
 
 cudaError_t launch_prefix(const DecodeParams &p, const Plan &w, cudaStream_t stream);
+cudaError_t launch_decode_rows(const DecodeParams &p, const Plan &w, int sms, cudaStream_t stream);
 
 }  // namespace bsattn

@@ -22,18 +22,20 @@
 // bsattn_prefix.cu); its keys are groups of 16.  The groups of all segments form one
 // line, where a segment also counts kSegCost groups for what it costs to start and end
 // one, and the line is cut evenly over the warps of the device: every warp streams the
-// same number of bytes whatever the lengths.  A warp holds the query rows, the sums and
-// the next group's codes in registers; nothing in its loop waits for another warp.  A
-// segment within one warp's piece is finished there; the parts of the others (fp32 output
+// same number of bytes whatever the lengths.  A warp holds the query rows and the sums in
+// registers and keeps a ring of its own in shared memory full with asynchronous copies;
+// nothing in its loop waits for another warp.  A segment within one warp's piece is finished there; the parts of the others (fp32 output
 // and LSE) go to the workspace, and a second kernel, a programmatic dependent of the
 // first, joins them.
 //
-// Fragments straight from global memory.  In S = Q K^T (m16n8k16) the contraction index
-// may be permuted alike on both sides, so lane 4g + t takes 16-byte pieces t (and t + 4)
-// of key g's row, four codes per k-step.  In O^T = V^T P^T the rows d may be permuted
+// Fragments without a transpose.  In S = Q K^T (m16n8k16) the contraction index may be
+// permuted alike on both sides, so lane 4g + t takes the D / 4 consecutive codes d =
+// (D / 4) t .. of key g, four per k-step.  In O^T = V^T P^T the rows d may be permuted
 // freely, so the lane takes D / 8 consecutive codes of each of its four keys and
 // interleaves the bytes of two keys before they are widened.  P leaves the first product
-// in the layout the second wants.  Every load covers whole 64- or 128-byte pieces of rows.
+// in the layout the second wants.  16-byte pieces lie at piece ^ (row mod 8) (D = 64:
+// piece ^ (row / 2 mod 4)): no 16-byte load meets a bank twice (the 8-byte loads of V at
+// D = 64 do, two ways).
 #include "bsattn_internal.h"
 #include "decode_common.cuh"
 #include "kv_codes.cuh"
@@ -44,19 +46,43 @@ namespace {
 
 constexpr int kSegCost = 2;  // groups of 16 keys that starting and ending a segment costs
 
-// Codes that are read once: 16 bytes past L1.
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t *p) {
+// 16 bytes from global to shared memory, past L1; counted by the thread's copy groups.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 x;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
     return x;
 }
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t *p) {
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 x;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
     return x;
 }
+
+// Byte offset of 16-byte piece `c` of row `r` in a group's codes.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+    if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+    else return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// A warp's ring: per stage the codes of 16 keys (K, then V) and their scales (K, then V).
+template <int D, int kCols>
+struct Ring {
+    static constexpr int kWarps = kCols == 1 ? kStreamWarps : 12;      // per CTA
+    static constexpr int kCtas = kCols == 1 ? 2 : 1;                   // per SM
+    static constexpr uint32_t kCodes = 16u * D;
+    static constexpr uint32_t kStage = 2u * kCodes + 128u;
+    // ~200 KB in flight per SM (HBM needs 44 KB at 6.7 TB/s and ~1 us)
+    static constexpr int kStages = (int)(101376u * (2 / kCtas) / (kWarps * kStage));
+    static constexpr uint32_t kBytes = kWarps * kStages * kStage;
+};
 
 // One warp's state: kCols groups of 8 query rows.
 template <int D, bool kInt8, int kCols>
@@ -68,9 +94,9 @@ struct Worker {
     float qs[kCols];                             // c_r of rows g, g + 8
     float m[kCols], u[kCols], l[kCols];
     float o[kSteps][kCols][4];
-    // the group to come
-    uint32_t kx[2][D / 16], vx[4][D / 32];
-    float2 ksx[2], vsx[2];
+    uint32_t ring;                               // shared address of the warp's ring
+
+    using R = Ring<D, kCols>;
 
     __device__ __forceinline__ void begin(const Seg &s) {
 #pragma unroll
@@ -82,8 +108,7 @@ struct Worker {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint4 y = make_uint4(0, 0, 0, 0);
-                // pieces of 16 elements: t, t + 4
-                if (r < s.rows) y = __ldg(reinterpret_cast<const uint4 *>(row + (t + 4 * (i >> 1)) * 16) + (i & 1));
+                if (r < s.rows) y = __ldg(reinterpret_cast<const uint4 *>(row + t * (D / 4)) + i);
                 x[4 * i] = y.x;
                 x[4 * i + 1] = y.y;
                 x[4 * i + 2] = y.z;
@@ -96,7 +121,7 @@ struct Worker {
             a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
             float f;
             row_scale(a, p.scale_log2, f, qs[hf]);
-            // k-step i / 2: a piece's elements 4 s, 4 s + 1 are a0 (a1 for row g + 8), 4 s + 2, 4 s + 3 are a2 (a3)
+            // k-step i / 2: elements 4 s, 4 s + 1 are a0 (a1 for row g + 8), 4 s + 2, 4 s + 3 are a2 (a3)
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
                 q[i / 2][kCols * (i & 1) + hf] =
@@ -112,44 +137,19 @@ struct Worker {
                 for (int x = 0; x < 4; ++x) o[i][n][x] = 0.f;
     }
 
-    // Loads of the group whose first key is row `row` of the cache.
-    __device__ __forceinline__ void load_k(int row) {
-        const uint8_t *src = p.c.k + (long long)row * D + g * D + t * 16;
+    // Starts the copies of the group whose first key is row `row` of the cache.
+    __device__ __forceinline__ void fetch(uint32_t stage, int row) {
+        constexpr int kPieces = D / 16, kRowsPerStep = 32 / kPieces;
+        const int r0 = lane / kPieces, c = lane % kPieces;
+        const long long at = (long long)row * D + lane * 16;
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 y = ld_codes16(src + nb * 8 * D + i * 64);
-                kx[nb][4 * i] = y.x;
-                kx[nb][4 * i + 1] = y.y;
-                kx[nb][4 * i + 2] = y.z;
-                kx[nb][4 * i + 3] = y.w;
-            }
-    }
-    __device__ __forceinline__ void load_scales(int row) {
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-            ksx[nb] = __ldg(reinterpret_cast<const float2 *>(p.c.ks + row + 8 * nb + 2 * t));
-            vsx[nb] = __ldg(reinterpret_cast<const float2 *>(p.c.vs + row + 8 * nb + 2 * t));
+        for (int i = 0; i < 16 / kRowsPerStep; ++i) {
+            const uint32_t dst = stage + piece_at<D>(r0 + i * kRowsPerStep, c);
+            copy16(dst, p.c.k + at + i * 512);
+            copy16(dst + R::kCodes, p.c.v + at + i * 512);
         }
-    }
-    __device__ __forceinline__ void load_v(int row) {
-        const uint8_t *src = p.c.v + (long long)row * D + 2 * t * D + g * (D / 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-            const uint8_t *at = src + ((i & 1) + 8 * (i >> 1)) * D;
-            if constexpr (D == 128) {
-                const uint4 y = ld_codes16(at);
-                vx[i][0] = y.x;
-                vx[i][1] = y.y;
-                vx[i][2] = y.z;
-                vx[i][3] = y.w;
-            } else {
-                const uint2 y = ld_codes8(at);
-                vx[i][0] = y.x;
-                vx[i][1] = y.y;
-            }
-        }
+        if (lane < 8)
+            copy16(stage + 2 * R::kCodes + lane * 16, (lane < 4 ? p.c.ks : p.c.vs) + row + (lane & 3) * 4);
     }
 
     __device__ __forceinline__ void mma_q(float (&c)[4], int i, uint32_t b0, uint32_t b1) const {
@@ -157,41 +157,50 @@ struct Worker {
         else mma_f16(c, q[i][0], 0u, q[i][1], 0u, b0, b1);
     }
 
-    // The loaded group, the first nv keys of which count (all 16: kFull); the next one,
-    // at row `next` (< 0: none), is loaded as registers come free.
+    // The group in `stage`, the first nv keys of which count (all 16: kFull).
     template <bool kFull>
-    __device__ __forceinline__ void keys16(int nv, int next) {
+    __device__ __forceinline__ void keys16(uint32_t stage, int nv) {
         float s[2][4];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
+            uint32_t kx[D / 16];
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 y = lds128(stage + piece_at<D>(8 * nb + g, (D / 64) * t + i));
+                kx[4 * i] = y.x;
+                kx[4 * i + 1] = y.y;
+                kx[4 * i + 2] = y.z;
+                kx[4 * i + 3] = y.w;
+            }
             // two accumulators: half the length of the dependent chain
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 uint32_t b0, b1;
-                codes_to_f16x2<kInt8>(kx[nb][i], b0, b1);
+                codes_to_f16x2<kInt8>(kx[i], b0, b1);
                 mma_q(acc[i & 1], i, b0, b1);
             }
 #pragma unroll
             for (int i = 0; i < 2 * kCols; ++i) s[nb][i] = acc[0][i] + acc[1][i];
         }
-        if (next >= 0) load_k(next);
         // x = z - m and y = z + log2 vs - u + 7 of this lane's keys 2t, 2t + 1, 2t + 8, 2t + 9
         float sc[kCols][4], lv[4], x[kCols][4], y[kCols][4];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int nb = 0; nb < 2; ++nb) {
+            const uint2 kb = lds64(stage + 2 * R::kCodes + 4u * (8 * nb + 2 * t));
+            const uint2 vb = lds64(stage + 2 * R::kCodes + 64u + 4u * (8 * nb + 2 * t));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool on = kFull || 8 * nb + 2 * t + e < nv;
-                lv[2 * nb + e] = lg2_approx(e ? vsx[nb].y : vsx[nb].x);
+                lv[2 * nb + e] = lg2_approx(__uint_as_float(e ? vb.y : vb.x));
                 if (!on) lv[2 * nb + e] = -INFINITY;
 #pragma unroll
                 for (int hf = 0; hf < kCols; ++hf) {
-                    sc[hf][2 * nb + e] = s[nb][2 * hf + e] * (e ? ksx[nb].y : ksx[nb].x);
+                    sc[hf][2 * nb + e] = s[nb][2 * hf + e] * __uint_as_float(e ? kb.y : kb.x);
                     if (!on) sc[hf][2 * nb + e] = -INFINITY;
                 }
             }
-        if (next >= 0) load_scales(next);
+        }
         float top[kCols];
         auto relative = [&](int hf) {
             const float mu = m[hf] - u[hf] + 7.f;
@@ -253,14 +262,26 @@ struct Worker {
             pb[hf][0] = pack_f16x2(ex2_approx(y[hf][0]), ex2_approx(y[hf][1]));
             pb[hf][1] = pack_f16x2(ex2_approx(y[hf][2]), ex2_approx(y[hf][3]));
         }
-        if (!kFull) {
-            // what lies behind the last key may be NaN codes
+        // V: D / 8 codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
+        uint32_t vx[4][D / 32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (2 * t + (i & 1) + 8 * (i >> 1) >= nv) {
+        for (int i = 0; i < 4; ++i) {
+            const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+            if constexpr (D == 128) {
+                const uint4 y = lds128(stage + R::kCodes + piece_at<D>(r, g));
+                vx[i][0] = y.x;
+                vx[i][1] = y.y;
+                vx[i][2] = y.z;
+                vx[i][3] = y.w;
+            } else {
+                const uint2 y = lds64(stage + R::kCodes + piece_at<D>(r, g >> 1) + 8u * (g & 1));
+                vx[i][0] = y.x;
+                vx[i][1] = y.y;
+            }
+            if (!kFull && r >= nv) {  // what lies behind the last key may be NaN codes
 #pragma unroll
-                    for (int w = 0; w < D / 32; ++w) vx[i][w] = 0u;
-                }
+                for (int w = 0; w < D / 32; ++w) vx[i][w] = 0u;
+            }
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
@@ -275,7 +296,6 @@ struct Worker {
                 for (int n = 0; n < kCols; ++n) mma_f16(o[2 * w + hi][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
             }
         }
-        if (next >= 0) load_v(next);
     }
 
     // Groups t0 .. t1 of a segment of n keys.
@@ -311,34 +331,40 @@ struct Worker {
         };
         int row0, nv0, row1 = -1, nv1 = 0;
         look_up(t0 + lane, row0, nv0);
-        int cur = __shfl_sync(0xffffffffu, row0, 0);
-        if (cur >= 0) {
-            load_k(cur);
-            load_scales(cur);
-            load_v(cur);
+        // kStages - 1 groups are on their way while one is worked on; a group without keys
+        // takes its turn as an empty copy group
+        constexpr int kLead = R::kStages - 1;
+#pragma unroll
+        for (int k = 0; k < kLead; ++k) {
+            const int row = __shfl_sync(0xffffffffu, row0, k);
+            if (row >= 0) fetch(ring + k * R::kStage, row);
+            copy_commit();
         }
+        uint32_t cur = ring, ahead = ring + kLead * R::kStage;
+        constexpr uint32_t kWrap = R::kStages * R::kStage;
         for (int i = t0; i < t1; ++i) {
             const int j = (i - t0) & 31;
             if (j == 0) look_up(i + 32 + lane, row1, nv1);
-            const int nv = __shfl_sync(0xffffffffu, nv0, j);
-            const int next = __shfl_sync(0xffffffffu, j < 31 ? row0 : row1, (j + 1) & 31);
-            if (cur < 0) {
-                if (next >= 0) {
-                    load_k(next);
-                    load_scales(next);
-                    load_v(next);
-                }
-            } else if (nv == 16) {
-                keys16<true>(nv, next);
-            } else {
-                keys16<false>(nv, next);
+            const int far = __shfl_sync(0xffffffffu, j + kLead < 32 ? row0 : row1, (j + kLead) & 31);
+            if (far >= 0) fetch(ahead, far);   // the stage that every lane left in the round before
+            copy_commit();
+            const int row = __shfl_sync(0xffffffffu, row0, j), nv = __shfl_sync(0xffffffffu, nv0, j);
+            copy_wait<kLead>();
+            __syncwarp();
+            if (row >= 0) {
+                if (nv == 16) keys16<true>(cur, nv);
+                else keys16<false>(cur, nv);
             }
-            cur = next;
+            __syncwarp();
+            cur = cur + R::kStage == ring + kWrap ? ring : cur + R::kStage;
+            ahead = ahead + R::kStage == ring + kWrap ? ring : ahead + R::kStage;
             if (j == 31) {
                 row0 = row1;
                 nv0 = nv1;
             }
         }
+        copy_wait<0>();  // only empty groups are left
+        __syncwarp();
     }
 
     // Writes the rows of a segment (or of the part of it that this worker has).
@@ -387,17 +413,14 @@ struct Worker {
     }
 };
 
-// CTAs per SM: with one group of columns 128 registers a thread suffice for two; two
-// groups take 168 and leave room for three quarters of that.
-template <int kCols>
-constexpr int kCtasPerSm = kCols == 1 ? 2 : 1;
-template <int kCols>
-constexpr int kWarps = kCols == 1 ? kStreamWarps : 12;
-
+// One group of columns takes two CTAs of 8 warps per SM at 128 registers a thread; two
+// groups take 12 warps at 168.
 template <int D, bool kInt8, int kCols>
-__global__ void __launch_bounds__(kWarps<kCols> * 32, kCtasPerSm<kCols>)
+__global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::kCtas)
     bsattn_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w) {
-    constexpr int kW = kWarps<kCols>, kThreads = kW * 32;
+    using R = Ring<D, kCols>;
+    constexpr int kW = R::kWarps, kThreads = kW * 32;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long warp_sum[kW], start_at[kW];
     __shared__ int start_seg[kW];
     const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
@@ -474,6 +497,7 @@ __global__ void __launch_bounds__(kWarps<kCols> * 32, kCtasPerSm<kCols>)
     if (worker < cuts) {
         const long long lo = first_of(worker), hi = first_of(worker + 1);
         Worker<D, kInt8, kCols> k{p, lane, lane >> 2, lane & 3};
+        k.ring = smem_u32(smem) + (uint32_t)warp * R::kStages * R::kStage;
         int seg = start_seg[warp];
         for (long long begin = start_at[warp]; begin < hi; ++seg) {
             const Seg s = segment(p, w, seg);
@@ -589,6 +613,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) bsattn_decode_join_kernel(con
 
 template <int D, bool kInt8, int kCols>
 cudaError_t launch(const DecodeParams &p, const Plan &w, int sms, cudaStream_t stream) {
+    using R = Ring<D, kCols>;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        e = cudaFuncSetAttribute(bsattn_decode_kernel<D, kInt8, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)R::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -597,10 +633,11 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, int sms, cudaStream_t s
     cfg.stream = stream;
     // beside the prefix kernel, whose results it does not need; else after what came before
     cfg.numAttrs = w.mode == kOwnKernel ? 1 : 0;
-    const int most = kMaxCtas * kStreamWarps / kWarps<kCols>;
-    const int grid = sms * kCtasPerSm<kCols>;
+    const int most = kMaxCtas * kStreamWarps / R::kWarps;
+    const int grid = sms * R::kCtas;
     cfg.gridDim = dim3((unsigned)(grid < most ? grid : most));
-    cfg.blockDim = dim3(kWarps<kCols> * 32);
+    cfg.blockDim = dim3(R::kWarps * 32);
+    cfg.dynamicSmemBytes = R::kBytes;
     return cudaLaunchKernelEx(&cfg, bsattn_decode_kernel<D, kInt8, kCols>, p, w);
 }
 

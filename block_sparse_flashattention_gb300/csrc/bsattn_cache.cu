@@ -94,6 +94,8 @@ struct SeqRows {
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(kWarps * 32) bsattn_kv_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = kHeadsPerWarp / kRows;
+    grid_launch_dependents();  // a dependent waits for this grid's end, as this one for what came before
+    grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int cap = p.table_cols << p.c.page_shift;  // tokens of a table row (checked < 2^31 below)
@@ -148,6 +150,8 @@ __global__ void __launch_bounds__(kWarps * 32) bsattn_kv_append_kernel(const __g
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(kWarps * 32) bsattn_kv_read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = kHeadsPerWarp / kRows;
+    grid_launch_dependents();  // a dependent waits for this grid's end, as this one for what came before
+    grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const long long gw = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int cap = p.table_cols << p.c.page_shift;
@@ -210,32 +214,32 @@ unsigned blocks_for(long long total, int H) {
     return (unsigned)((warps + kWarps - 1) / kWarps);
 }
 
+// Launches as a programmatic dependent of what precedes on the stream: the launch
+// overlaps the end of the kernel before.
+template <class P>
+cudaError_t launch(void (*kernel)(P), const P &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(blocks_for(p.total, p.c.H));
+    cfg.blockDim = dim3(kWarps * 32);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream) {
-    const unsigned g = blocks_for(p.total, p.c.H);
-    const int t = kWarps * 32;
-    if (p.c.D == 128) {
-        if (p.c.int8) bsattn_kv_append_kernel<128, true><<<g, t, 0, stream>>>(p);
-        else bsattn_kv_append_kernel<128, false><<<g, t, 0, stream>>>(p);
-    } else {
-        if (p.c.int8) bsattn_kv_append_kernel<64, true><<<g, t, 0, stream>>>(p);
-        else bsattn_kv_append_kernel<64, false><<<g, t, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    if (p.c.D == 128) return launch(p.c.int8 ? bsattn_kv_append_kernel<128, true> : bsattn_kv_append_kernel<128, false>, p, stream);
+    return launch(p.c.int8 ? bsattn_kv_append_kernel<64, true> : bsattn_kv_append_kernel<64, false>, p, stream);
 }
 
 cudaError_t launch_read(const ReadParams &p, cudaStream_t stream) {
-    const unsigned g = blocks_for(p.total, p.c.H);
-    const int t = kWarps * 32;
-    if (p.c.D == 128) {
-        if (p.c.int8) bsattn_kv_read_kernel<128, true><<<g, t, 0, stream>>>(p);
-        else bsattn_kv_read_kernel<128, false><<<g, t, 0, stream>>>(p);
-    } else {
-        if (p.c.int8) bsattn_kv_read_kernel<64, true><<<g, t, 0, stream>>>(p);
-        else bsattn_kv_read_kernel<64, false><<<g, t, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    if (p.c.D == 128) return launch(p.c.int8 ? bsattn_kv_read_kernel<128, true> : bsattn_kv_read_kernel<128, false>, p, stream);
+    return launch(p.c.int8 ? bsattn_kv_read_kernel<64, true> : bsattn_kv_read_kernel<64, false>, p, stream);
 }
 
 }  // namespace bsattn

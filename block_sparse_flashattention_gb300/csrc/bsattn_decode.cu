@@ -54,6 +54,13 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// Loads that stay where they are written (the query rows go out before the look-ups).
+__device__ __forceinline__ uint4 ld_row16(const uint16_t *p) {
+    uint4 x;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+    return x;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 x;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
@@ -98,21 +105,34 @@ struct Worker {
 
     using R = Ring<D, kCols>;
 
-    __device__ __forceinline__ void begin(const Seg &s) {
+    // The segment's query rows, as they lie: D / 4 bf16 elements of rows g, g + 8.
+    struct RawRows {
+        uint4 x[kCols][D / 32];
+    };
+    __device__ __forceinline__ void load_rows(const Seg &s, RawRows &raw) const {
 #pragma unroll
         for (int hf = 0; hf < kCols; ++hf) {
             const int r = g + 8 * hf;
             const int b = s.prefix ? r / p.G : s.b, gi = s.prefix ? r - b * p.G : r;
-            const uint16_t *row = p.q + (long long)b * p.q_stride + (long long)(s.h * p.G + gi) * D;
-            uint32_t x[D / 8], a = 0;            // D / 4 bf16 elements of the row
+            const uint16_t *row = p.q + (long long)b * p.q_stride + (long long)(s.h * p.G + gi) * D + t * (D / 4);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (r < s.rows) y = __ldg(reinterpret_cast<const uint4 *>(row + t * (D / 4)) + i);
-                x[4 * i] = y.x;
-                x[4 * i + 1] = y.y;
-                x[4 * i + 2] = y.z;
-                x[4 * i + 3] = y.w;
+                raw.x[hf][i] = make_uint4(0, 0, 0, 0);
+                if (r < s.rows) raw.x[hf][i] = ld_row16(row + 8 * i);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void begin(const RawRows &raw) {
+#pragma unroll
+        for (int hf = 0; hf < kCols; ++hf) {
+            uint32_t x[D / 8], a = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                x[4 * i] = raw.x[hf][i].x;
+                x[4 * i + 1] = raw.x[hf][i].y;
+                x[4 * i + 2] = raw.x[hf][i].z;
+                x[4 * i + 3] = raw.x[hf][i].w;
             }
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) a = __vmaxu2(a, x[i] & 0x7fff7fffu);
@@ -298,7 +318,7 @@ struct Worker {
         }
     }
 
-    // Groups t0 .. t1 of a segment of n keys.
+    // Starts a segment of n keys and works on its groups t0 .. t1.
     __device__ __forceinline__ void groups(const Seg &s, int n, const ListRow &lr, int t0, int t1) {
         const bool listed = p.has_lists && !s.prefix;
         const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
@@ -330,6 +350,8 @@ struct Worker {
             row = ((page * p.c.H + s.h) << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1));
         };
         int row0, nv0, row1 = -1, nv1 = 0;
+        RawRows raw;
+        load_rows(s, raw);
         look_up(t0 + lane, row0, nv0);
         // kStages - 1 groups are on their way while one is worked on; a group without keys
         // takes its turn as an empty copy group
@@ -340,6 +362,7 @@ struct Worker {
             if (row >= 0) fetch(ring + k * R::kStage, row);
             copy_commit();
         }
+        begin(raw);
         uint32_t cur = ring, ahead = ring + kLead * R::kStage;
         constexpr uint32_t kWrap = R::kStages * R::kStage;
         for (int i = t0; i < t1; ++i) {
@@ -421,10 +444,12 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     using R = Ring<D, kCols>;
     constexpr int kW = R::kWarps, kThreads = kW * 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long warp_sum[kW], start_at[kW];
+    __shared__ long long warp_sum[kW], piece_at[kW + 1], start_at[kW];
     __shared__ int start_seg[kW];
     const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
     grid_launch_dependents();  // the joining kernel may take its place; it waits for this grid
+    // Beside the prefix kernel (which has waited) this one needs nothing that it writes.
+    if (w.mode != kOwnKernel) grid_dependency_wait();
 
     // Where each worker's piece of the line begins.  Each thread sums the cost of a run
     // of sequences (or, with lists, of (sequence, head) pairs); CTA c also writes the
@@ -460,20 +485,21 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     }
     // pieces of at least one place each: a segment's parts lie with consecutive workers
     const long long cuts = min((long long)gridDim.x * kW, total);
-    auto first_of = [&](long long worker) -> long long { return total * worker / cuts; };
+    if (tid <= kW) {  // where the pieces of this CTA's workers begin
+        const long long worker = min((long long)blockIdx.x * kW + tid, cuts);
+        piece_at[tid] = cuts ? total * worker / cuts : 0;
+    }
+    __syncthreads();
     auto owner = [&](long long place) -> int { return (int)(((place + 1) * cuts - 1) / total); };
     auto begins_at = [&](long long begin, long long len, int seg, long long seg_len) {
         // workers of this CTA whose pieces begin within [begin, begin + len): segments seg, seg + 1, ... of seg_len
-        for (int x = 0; x < kW; ++x) {
-            const long long worker = (long long)blockIdx.x * kW + x;
-            if (worker >= cuts) return;
-            const long long lo = first_of(worker);
-            if (lo >= begin && lo < begin + len) {
-                const long long k = (lo - begin) / seg_len;
-                start_seg[x] = seg + (int)k;
+        if (piece_at[kW] <= begin || piece_at[0] >= begin + len) return;
+        for (int x = 0; x < kW; ++x)
+            if (piece_at[x] >= begin && piece_at[x] < begin + len) {
+                const int k = (int)((piece_at[x] - begin) / seg_len);
+                start_seg[x] = seg + k;
                 start_at[x] = begin + k * seg_len;
             }
-        }
     };
     int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
     if (w.sp && tid == 0) begins_at(0, line_pre, 0, g_pre + kSegCost);
@@ -495,7 +521,7 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     __syncthreads();
     const long long worker = (long long)blockIdx.x * kW + warp;
     if (worker < cuts) {
-        const long long lo = first_of(worker), hi = first_of(worker + 1);
+        const long long lo = piece_at[warp], hi = piece_at[warp + 1];
         Worker<D, kInt8, kCols> k{p, lane, lane >> 2, lane & 3};
         k.ring = smem_u32(smem) + (uint32_t)warp * R::kStages * R::kStage;
         int seg = start_seg[warp];
@@ -512,7 +538,6 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
             const long long first = begin + kSegCost;
             const int t0 = (int)max(0ll, min((long long)g, lo - first)), t1 = (int)max(0ll, min((long long)g, hi - first));
             if (t0 < t1) {
-                k.begin(s);
                 k.groups(s, n, lr, t0, t1);
                 k.finish(w, s, seg, (int)worker, t0 == 0 && t1 == g);
             }
@@ -532,6 +557,7 @@ constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) bsattn_decode_join_kernel(const __grid_constant__ DecodeParams p,
                                                                             const __grid_constant__ Plan w) {
+    grid_launch_dependents();
     grid_dependency_wait();
     constexpr int E = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -565,37 +591,69 @@ __global__ void __launch_bounds__(kJoinWarps * 32) bsattn_decode_join_kernel(con
     const float *pre_o = reinterpret_cast<const float *>(p.ws + w.pre_o), *pre_l = reinterpret_cast<const float *>(p.ws + w.pre_l);
     const float *suf_o = reinterpret_cast<const float *>(p.ws + w.suf_o), *suf_l = reinterpret_cast<const float *>(p.ws + w.suf_l);
     auto at = [&](int i) -> long long { return i < np ? pre_row + i * pre_step : suf_row + (long long)(i - np) * p.G; };
-    // every warp finds the largest LSE; a NaN is carried by the weights
-    float mx = -INFINITY;
-    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, (i < np ? pre_l : suf_l)[at(i)]);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float o[E], l = 0.f;
+    // A warp's parts in rounds of kRound, whose loads go out together; a NaN is carried by the weights.
+    constexpr int kRound = 4;
+    float o[E], l = 0.f, base = kNoKey;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += kJoinWarps) {
-        const long long at_i = at(i);
-        const float x = ex2_approx((i < np ? pre_l : suf_l)[at_i] - base);
-        const float *src = (i < np ? pre_o : suf_o) + at_i * D + lane * E;
-        l += x;
+    for (int i0 = warp; i0 < n; i0 += kJoinWarps * kRound) {
+        float x[kRound], y[kRound][E], top = base;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(x, src[e], o[e]);
+        for (int k = 0; k < kRound; ++k) {
+            const int i = i0 + k * kJoinWarps;
+            x[k] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[k][e] = 0.f;
+            if (i < n) {
+                const long long at_i = at(i);
+                const float *src = (i < np ? pre_o : suf_o) + at_i * D + lane * E;
+                x[k] = (i < np ? pre_l : suf_l)[at_i];
+                if constexpr (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(src);
+                    y[k][0] = f.x, y[k][1] = f.y, y[k][2] = f.z, y[k][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2 *>(src);
+                    y[k][0] = f.x, y[k][1] = f.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) top = fmaxf(top, x[k]);
+        const float a = ex2_approx(base - top);
+        base = top;
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= a;
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) {
+            const float f = ex2_approx(x[k] - base);
+            l += f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(f, y[k][e], o[e]);
+        }
     }
-    __shared__ float so[kJoinWarps][D], sl[kJoinWarps];
+    __shared__ float so[kJoinWarps][D], sl[kJoinWarps], sb[kJoinWarps];
     if (n > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-        if (lane == 0) sl[warp] = l;
+        if (lane == 0) sl[warp] = l, sb[warp] = base;
         __syncthreads();
         if (warp > 0) return;
+        float top = base;
+#pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, sb[k]);
+        float a = ex2_approx(base - top);
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= a;
 #pragma unroll
         for (int k = 1; k < kJoinWarps; ++k) {
-            l += sl[k];
+            a = ex2_approx(sb[k] - top);
+            l = fmaf(sl[k], a, l);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += so[k][lane * E + e];
+            for (int e = 0; e < E; ++e) o[e] = fmaf(so[k][lane * E + e], a, o[e]);
         }
+        base = top;
     } else if (warp > 0) {
         return;
     }
@@ -631,8 +689,7 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, int sms, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.stream = stream;
-    // beside the prefix kernel, whose results it does not need; else after what came before
-    cfg.numAttrs = w.mode == kOwnKernel ? 1 : 0;
+    cfg.numAttrs = 1;
     const int most = kMaxCtas * kStreamWarps / R::kWarps;
     const int grid = sms * R::kCtas;
     cfg.gridDim = dim3((unsigned)(grid < most ? grid : most));

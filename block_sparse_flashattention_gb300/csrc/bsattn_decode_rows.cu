@@ -408,6 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
     const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
     grid_launch_dependents();  // the joining kernel may take its place; it waits for this grid
+    // Beside the prefix kernel (which has waited) this one needs nothing that it writes.
+    if (w.mode != kOwnKernel) grid_dependency_wait();
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(s), 1);
@@ -623,8 +625,7 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, int sms, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.stream = stream;
-    // beside the prefix kernel, whose results it does not need; else after what came before
-    cfg.numAttrs = w.mode == kOwnKernel ? 1 : 0;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3((unsigned)(sms < kMaxCtas ? sms : kMaxCtas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kAlloc;

@@ -492,7 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(misc + 1);
     auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
     const uint32_t warp = warp_id(), lane = lane_id();
-    grid_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(C::bKF + s), 4);       // one arrival per widening warp
@@ -518,6 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
+    // Launched as a dependent of whatever preceded it on the stream; the decode kernel, which
+    // does not wait for what this grid writes, may start once that has completed.
+    grid_dependency_wait();
+    grid_launch_dependents();
     Walk walk;
     walk.nt = (p.prefix_len + kTile - 1) / kTile;
     walk.pos = w.pre_first((int)blockIdx.x, walk.nt);
@@ -657,8 +660,17 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
-    bsattn_prefix_kernel<D, kInt8><<<w.pre_cuts, kThreads, C::kAlloc, stream>>>(p, w);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)w.pre_cuts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kAlloc;
+    return cudaLaunchKernelEx(&cfg, bsattn_prefix_kernel<D, kInt8>, p, w);
 }
 
 }  // namespace

@@ -18,29 +18,30 @@
 // products of the other.  The line of all segments' 128-key tiles is cut evenly over the
 // SMs; each part (fp32 output and LSE per slot row) goes to the workspace for the join.
 //
-// Roles (512 threads, one CTA per SM, all of TMEM):
+// Roles (640 threads, one CTA per SM, all of TMEM):
 //   warp 0        issues the MMAs: S_t = Q_t K'^T into TMEM, O_t += P_t V' with P in TMEM
 //   warp 1        owns the TMEM allocation
 //   warps 4-7, 8-11   slot 0, slot 1: load the query rows, softmax, O rescale, part
-//   warps 12-15   load codes and scales (the next tile's codes wait in registers), widen
-//                 them into the K and V stages (128-byte swizzle; V as it lies, MN-major)
+//   warps 12-15   load codes and scales of keys (the next tile's wait in registers) and
+//                 widen them into the K stages (128-byte swizzle)
+//   warps 16-19   the same for values, as they lie (MN-major)
 // TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P_t over S_t.
 #include "bsattn_internal.h"
-#include "decode_plan.cuh"
+#include "decode_common.cuh"
 #include "kv_codes.cuh"
-#include "sm100_ptx.cuh"
 
 namespace bsattn {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
-// 128 registers per thread at launch; the control warpgroup's surplus goes to the
-// softmax: 128 * 48 + 2 * 128 * 176 + 128 * 112 = 65536 = 512 * 128.
-constexpr int kLaunchRegs = 128;
-constexpr uint32_t kCtrlRegs = 48, kSoftmaxRegs = 176, kWidenRegs = 112;
-static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs + 128 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+// 96 registers per thread at launch; the control warpgroup's surplus and some of the
+// widening ones' go to the softmax: 128 * 32 + 2 * 128 * 144 + 2 * 128 * 80 = 61440 =
+// 640 * 96.
+constexpr int kLaunchRegs = 96;
+constexpr uint32_t kCtrlRegs = 32, kSoftmaxRegs = 144, kWidenRegs = 80;
+static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;  // 128 rows x 64 fp16: one 128-byte swizzle span
 constexpr int kMsgs = 4;                   // tiles whose key scales and masks are kept
@@ -81,12 +82,6 @@ struct Walk {
         return true;
     }
 };
-
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Instruction descriptor, kind::f16 with fp16 A and B, fp32 D (see idesc_bf16_f32).
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -134,9 +129,8 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) a = __vmaxu2(a, x[i] & 0x7fff7fffu);
             a = max(a & 0xffffu, a >> 16);
-            const int e = (a == 0 || a >= 0x7f80u) ? 127 : min(max((int)(a >> 7), 1), 253);
-            const float f = __uint_as_float((uint32_t)(254 - e) << 23);
-            c = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)e << 23), 0x1p-126f);
+            float f;
+            row_scale(a, p.scale_log2, f, c);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 uint32_t y[4];
@@ -154,7 +148,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::bQF + t));
         // ---- the slot's tiles
-        float m_run = -INFINITY, l_run = 0.f;
+        float m_run = kNoKey, l_run = 0.f;
         int exp_run = 0, done = 0;
         for (int k = split ? t : 0; ok && k < walk.n; k += split ? 2 : 1) {
             ok = mbar_wait(bar(C::bSR + t), sc & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
@@ -164,94 +158,58 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             const uint32_t slot = (tile0 + (uint32_t)k) % kMsgs;
             const KeyMsg *msg = reinterpret_cast<const KeyMsg *>(smem + C::kMsg) + slot;
             const float4 *ks = reinterpret_cast<const float4 *>(smem + C::kScale + slot * 512u);
-            float s[128];
-            {
-                uint32_t v0[32], v1[32], v2[32], v3[32];
-                tmem_ld32(lane_addr + s_col + 0, v0);
-                tmem_ld32(lane_addr + s_col + 32, v1);
-                tmem_ld32(lane_addr + s_col + 64, v2);
-                tmem_ld32(lane_addr + s_col + 96, v3);
-                tmem_wait_ld();
-                reg_fence(v0);
-                reg_fence(v1);
-                reg_fence(v2);
-                reg_fence(v3);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    s[x] = __uint_as_float(v0[x]);
-                    s[32 + x] = __uint_as_float(v1[x]);
-                    s[64 + x] = __uint_as_float(v2[x]);
-                    s[96 + x] = __uint_as_float(v3[x]);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-                const float4 f = ks[x];
-                fmul2(s[4 * x], s[4 * x + 1], s[4 * x], s[4 * x + 1], f.x, f.y);
-                fmul2(s[4 * x + 2], s[4 * x + 3], s[4 * x + 2], s[4 * x + 3], f.z, f.w);
-            }
             const uint4 kw = *reinterpret_cast<const uint4 *>(msg->keep);
-            if ((kw.x & kw.y & kw.z & kw.w) != 0xffffffffu) {
+            const bool masked = (kw.x & kw.y & kw.z & kw.w) != 0xffffffffu;
+            const int exp_new = msg->exp;
+            // 32 scores from column 32 q on, times their keys' scales; -inf where a key does not count
+            auto scores = [&](int q, float (&s)[32]) {
+                uint32_t v[32];
+                tmem_ld32(lane_addr + s_col + 32u * q, v);
+                tmem_wait_ld();
+                reg_fence(v);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int x = 0; x < 8; ++x) {
+                    const float4 f = ks[8 * q + x];
+                    fmul2(s[4 * x], s[4 * x + 1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                    fmul2(s[4 * x + 2], s[4 * x + 3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
+                }
+                if (masked) {
                     const uint32_t keep = q == 0 ? kw.x : q == 1 ? kw.y : q == 2 ? kw.z : kw.w;
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
-                        if (!((keep >> x) & 1u)) s[32 * q + x] = -INFINITY;
+                        if (!((keep >> x) & 1u)) s[x] = -INFINITY;
                 }
-            }
-            float g[4];
+            };
+            auto largest = [](const float (&s)[32]) {
+                float g0 = fmax3(s[0], s[1], s[2]), g1 = fmax3(s[3], s[4], s[5]);
 #pragma unroll
+                for (int x = 6; x < 30; x += 4) {
+                    g0 = fmax3(g0, s[x], s[x + 1]);
+                    g1 = fmax3(g1, s[x + 2], s[x + 3]);
+                }
+                return fmax3(g0, fmaxf(s[30], s[31]), g1);
+            };
+            // Two rolled passes, the maximum and then P, each re-reading S from tensor memory: the
+            // roles' loops have to share the instruction caches (see the header).
+            float m_new = m_run;
+#pragma unroll 1
             for (int q = 0; q < 4; ++q) {
-                g[q] = fmax3(s[32 * q], s[32 * q + 1], s[32 * q + 2]);
-#pragma unroll
-                for (int x = 3; x < 31; x += 2) g[q] = fmax3(g[q], s[32 * q + x], s[32 * q + x + 1]);
-                g[q] = fmaxf(g[q], s[32 * q + 31]);
+                float s[32];
+                scores(q, s);
+                m_new = fmaxf(m_new, largest(s) * c);
             }
-            const float m_new = fmaxf(m_run, fmax3(g[0], g[1], fmaxf(g[2], g[3])) * c);
-            const int exp_new = msg->exp;
             // O is rescaled when some row's maximum grew by more than 2^8 or E grew; otherwise
             // the stale references serve (P stays below 2^14)
-            const bool grew = __any_sync(0xffffffffu, (m_new - m_run) > 8.0f);
-            const bool rescale = done > 0 && (grew || exp_new != exp_run);
-            float alpha = 1.f, alpha_o = 1.f;
-            if (done == 0) {
+            const bool grew = __any_sync(0xffffffffu, m_new - m_run > 8.f);
+            float alpha = 1.f;
+            if (grew) {
+                alpha = ex2_approx(m_run - m_new);
                 m_run = m_new;
-                exp_run = exp_new;
-            } else if (rescale) {
-                if (grew) {
-                    if (m_new != -INFINITY) alpha = ex2_approx(m_run - m_new);
-                    m_run = m_new;
-                }
-                alpha_o = alpha * ex2_approx((float)(exp_run - exp_new));
-                exp_run = exp_new;
             }
-            const float nm = (m_run == -INFINITY ? 0.f : -m_run) + 6.f;
-            float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
-            auto p_half = [&](int q) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float x0, x1;
-                    ffma2(x0, x1, s[q * 64 + 2 * x], s[q * 64 + 2 * x + 1], c, c, nm, nm);
-                    const float p0 = ex2_approx(x0);
-                    const float p1 = ex2_approx(x1);
-                    if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
-                    else fadd2(la0, la1, la0, la1, p0, p1);
-                    pk[x] = pack_f16x2(p0, p1);
-                }
-                tmem_st32(lane_addr + s_col + q * 32, pk);
-            };
-            auto publish = [&](int half) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::bPR + 2 * t + half));
-            };
-            p_half(0);
-            if (rescale) {
+            if (done > 0 && (grew || exp_new != exp_run)) {
                 // S of this tile was issued after the slot's previous P V: O is up to date
-#pragma unroll
+                const float alpha_o = alpha * ex2_approx((float)(exp_run - exp_new));
+#pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
                     tmem_ld32(lane_addr + o_col + q * 32, v);
@@ -262,10 +220,33 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                     tmem_st32(lane_addr + o_col + q * 32, v);
                 }
             }
-            publish(0);
-            p_half(1);
-            publish(1);
-            l_run = l_run * alpha + ((la0 + lb0) + (la1 + lb1));
+            exp_run = exp_new;
+            const float nm = 6.f - m_run;
+            float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                float s[32];
+                scores(q, s);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) ffma2(s[2 * x], s[2 * x + 1], s[2 * x], s[2 * x + 1], c, c, nm, nm);
+                uint32_t pk[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float p0 = ex2_approx(s[2 * x]), p1 = ex2_approx(s[2 * x + 1]);
+                    if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
+                    else fadd2(la0, la1, la0, la1, p0, p1);
+                    pk[x] = pack_f16x2(p0, p1);
+                }
+                tmem_st16(lane_addr + s_col + 16u * q, pk);   // over scores that have been read
+                if (q & 1) {                                   // 64 keys more are ready for P V
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::bPR + 2 * t + (q >> 1)));
+                }
+            }
+            const float l_tile = (la0 + lb0) + (la1 + lb1);
+            l_run = l_run * alpha + l_tile;
             ++done;
         }
         if (!ok) break;
@@ -313,29 +294,27 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             __syncwarp();
         }
         if (row_ok)
-            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - 6.f + lg2(l_run);
+            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - 6.f + lg2_approx(l_run);
         tc_fence_before();
     }
 }
 
-// Codes and scales of a tile, loaded ahead: this thread's pieces of 16 codes (8 rows
-// of the warp's 32 at D = 128, 4 at D = 64), and scales of four keys (of the tile) and
-// of one (of the warp's 32).
-template <int D>
-struct Raw {
-    static constexpr int kPieces = D / 16;       // 16-byte pieces of a row
-    static constexpr int kRowsPerStep = 32 / kPieces, kSteps = 32 / kRowsPerStep;
-    uint4 x[kSteps];
-};
-
+// Widens the codes of K tiles (four warps, 32 keys each) or V tiles (four more); one code
+// for both, K with factors of 1, so that the warps share the instruction caches.
+//
+// Lane: 8 codes of a row (16 bytes of fp16, one swizzle piece), D / 8 lanes to a row; a
+// tile's codes are loaded while the tile before it is widened.
 template <int D, bool kInt8>
-__device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w, Walk walk, int warp, int lane,
-                                           uint32_t base, uint8_t *smem, volatile int *abort) {
+__device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w, Walk walk, bool values, int warp,
+                                           int lane, uint32_t base, uint8_t *smem, volatile int *abort) {
     using C = Cfg<D>;
-    using R = Raw<D>;
+    // row of a load instruction: 8 lanes with 8 codes each; a row of 128 codes takes two
+    constexpr int kSpans = D / 64, kSteps = 32 / 4;
     auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
-    const int piece = lane % R::kPieces, sub_row = lane / R::kPieces;
+    const int piece = lane & 7, sub_row = lane >> 3;
     const int ps_shift = p.c.page_shift, n_keys = p.prefix_len;
+    const uint8_t *codes = values ? p.c.v : p.c.k;
+    const float *scales = values ? p.c.vs : p.c.ks;
     // Cache row of this lane's keys 4 lane .. 4 lane + 3 of a tile (one page), or -1.
     auto look_up = [&](int tile, int h) -> int {
         const int key = tile * kTile + 4 * lane;
@@ -348,77 +327,45 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         return ((page * p.c.H + h) << ps_shift) + (key & ((1 << ps_shift) - 1));
     };
     // What is loaded of a tile one tile ahead.
-    struct Ahead {
-        int run0, run1;  // cache rows of the warp's keys 0 .. 15 and 16 .. 31, or -1
-        int n;           // keys of the tile
-        float ks, vs;    // scales of the warp's key `lane`
-        uint4 vs4;       // value scales of the tile's keys 4 lane ..
-    };
-    auto load_scales = [&](Ahead &a, int row4, int tile) {
-        a.run0 = __shfl_sync(0xffffffffu, row4, warp * 8);
-        a.run1 = __shfl_sync(0xffffffffu, row4, warp * 8 + 4);
-        a.n = min(kTile, n_keys - tile * kTile);
-        const int row = lane < 16 ? a.run0 : a.run1;
-        const bool on = row >= 0 && warp * 32 + lane < a.n;
-        a.ks = on ? __ldg(p.c.ks + (long long)row + (lane & 15)) : 0.f;
-        a.vs = on ? __ldg(p.c.vs + (long long)row + (lane & 15)) : 0.f;
-        a.vs4 = row4 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
-    };
-    auto load = [&](R &raw, const uint8_t *codes, const Ahead &a) {
+    int run0, run1, n;  // cache rows of the warp's keys 0 .. 15 and 16 .. 31 (or -1), keys of the tile
+    float scale;        // of the warp's key `lane`
+    uint4 vs4;          // value scales of the tile's keys 4 lane ..
+    uint2 raw[kSteps][kSpans];
+    auto load = [&](int row4, int tile) {
+        run0 = __shfl_sync(0xffffffffu, row4, warp * 8);
+        run1 = __shfl_sync(0xffffffffu, row4, warp * 8 + 4);
+        n = min(kTile, n_keys - tile * kTile);
+        const int row = lane < 16 ? run0 : run1;
+        scale = row >= 0 && warp * 32 + lane < n ? __ldg(scales + (long long)row + (lane & 15)) : 0.f;
+        vs4 = row4 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
+        const uint8_t *a0 = codes + ((long long)run0 + sub_row) * D + piece * 8;
+        const uint8_t *a1 = codes + ((long long)run1 + sub_row) * D + piece * 8;
 #pragma unroll
-        for (int i = 0; i < R::kSteps; ++i) {
-            const int k = i * R::kRowsPerStep + sub_row;   // of the warp's 32
-            const int row = i * R::kRowsPerStep < 16 ? a.run0 : a.run1;
-            const bool on = row >= 0 && warp * 32 + k < a.n;
-            raw.x[i] = on ? __ldg(reinterpret_cast<const uint4 *>(codes + ((long long)row + (k & 15)) * D + piece * 16))
-                          : make_uint4(0, 0, 0, 0);
-        }
-    };
-    // 16 codes as 32 bytes of fp16 into the swizzled tile; lanes of the second 64-column
-    // span store their two halves in the other order, which keeps the banks apart
-    auto store = [&](uint32_t tile_at, int k, uint4 x, uint32_t f) {
-        const bool swap = D == 128 && piece >= 4;
-        const uint32_t y[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
-        const int row = warp * 32 + k;
-        const uint32_t at = tile_at + (uint32_t)(piece >> 2) * kSub + (uint32_t)row * 128u;
+        for (int i = 0; i < kSteps; ++i) {
+            const uint8_t *at = (i < 4 ? a0 : a1) + (i & 3) * 4 * D;
+            const bool on = (i < 4 ? run0 : run1) >= 0 && warp * 32 + i * 4 + sub_row < n;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            uint32_t o[4];
-            codes_to_f16x2<kInt8>(y[2 * hf], o[0], o[1]);
-            codes_to_f16x2<kInt8>(y[2 * hf + 1], o[2], o[3]);
-            if (f != 0u) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(f));
-            }
-            const uint32_t chunk = (uint32_t)((piece & 3) * 2 + (hf ^ (swap ? 1 : 0)));
-            *reinterpret_cast<uint4 *>(smem + at + ((chunk ^ (uint32_t)(row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int x = 0; x < kSpans; ++x)
+                raw[i][x] = on ? __ldg(reinterpret_cast<const uint2 *>(at + x * 64)) : make_uint2(0, 0);
         }
     };
     // `ahead` walks two tiles in front: its tile's page is being looked up while the tile
     // before it is loaded and the one before that is widened.
     Walk ahead = walk;
-    int ak = 0, tile2 = 0, h2 = 0;
+    int ak = 0;
     bool more2 = ahead.next();
+    if (!more2) return;
     auto step = [&] {
         if (more2 && ++ak >= ahead.n) {
             ak = 0;
             more2 = ahead.next();
         }
-        tile2 = ahead.off + ak;
-        h2 = ahead.seg / w.row_blocks;
     };
-    if (!more2) return;
-    tile2 = ahead.off;
-    h2 = ahead.seg / w.row_blocks;
-    Ahead cur;
-    R kr, vr;
-    load_scales(cur, look_up(tile2, h2), tile2);
-    load(kr, p.c.k, cur);
-    load(vr, p.c.v, cur);
+    auto look_ahead = [&]() -> int { return more2 ? look_up(ahead.off + ak, ahead.seg / w.row_blocks) : -1; };
+    load(look_ahead(), ahead.off);
     step();
     bool more1 = more2;
-    int tile1 = tile2;
-    int row4 = more1 ? look_up(tile2, h2) : -1;
+    int tile1 = ahead.off + ak, row4 = look_ahead();
     uint32_t it = 0;
     while (walk.next()) {
         int exp_run = 1;            // E starts anew with a segment's sums
@@ -426,56 +373,51 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
             // the largest value scale of the tile (its bits; NaN and infinity do not count)
             uint32_t top = 0;
-            const uint32_t v4[4] = {cur.vs4.x, cur.vs4.y, cur.vs4.z, cur.vs4.w};
+            const uint32_t v4[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (v4[i] < 0x7f800000u && 4 * lane + i < cur.n) top = max(top, v4[i]);
+                if (v4[i] < 0x7f800000u && 4 * lane + i < n) top = max(top, v4[i]);
             top = __reduce_max_sync(0xffffffffu, top);
             exp_run = max(exp_run, (int)(top >> 23));
-            const uint32_t keep = __ballot_sync(0xffffffffu, (lane < 16 ? cur.run0 : cur.run1) >= 0 && warp * 32 + lane < cur.n);
-            // look up the tile after the next
             step();
-            const int row4_2 = more2 ? look_up(tile2, h2) : -1;
-            // K
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(C::bKE + st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
+            const int row4_2 = look_ahead();
+            float f32 = 1.f;
+            if (values) f32 = scale * __uint_as_float((uint32_t)min(254, 260 - exp_run) << 23);   // vs 2^(6 - E)
+            const uint32_t factor = pack_f16x2(f32, f32);
+            const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(empty + (int)st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
                 return;
+            uint8_t *tile = smem + (values ? C::kV : C::kK) + st * C::kTileBytes + (warp * 32 + sub_row) * 128;
+            const uint32_t swz[2] = {(uint32_t)((piece ^ sub_row) << 4), (uint32_t)((piece ^ (sub_row + 4)) << 4)};
 #pragma unroll
-            for (int i = 0; i < R::kSteps; ++i)
-                store(C::kK + st * C::kTileBytes, i * R::kRowsPerStep + sub_row, kr.x[i], 0u);
-            reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = cur.ks;
-            if (lane == 0) {
-                KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
-                msg->keep[warp] = keep;
-                if (warp == 0) msg->exp = exp_run;
+            for (int i = 0; i < kSteps; ++i) {
+                const uint32_t f = __shfl_sync(0xffffffffu, factor, i * 4 + sub_row);
+#pragma unroll
+                for (int x = 0; x < kSpans; ++x) {
+                    uint32_t o[4];
+                    codes_to_f16x2<kInt8>(raw[i][x].x, o[0], o[1]);
+                    codes_to_f16x2<kInt8>(raw[i][x].y, o[2], o[3]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(f));
+                    *reinterpret_cast<uint4 *>(tile + x * kSub + i * 512 + swz[i & 1]) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            if (!values) {
+                const uint32_t keep = __ballot_sync(0xffffffffu, (lane < 16 ? run0 : run1) >= 0 && warp * 32 + lane < n);
+                reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = scale;
+                if (lane == 0) {
+                    KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
+                    msg->keep[warp] = keep;
+                    if (warp == 0) msg->exp = exp_run;
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::bKF + st));
-            const float vs = cur.vs;
-            if (more1) {
-                load_scales(cur, row4, tile1);
-                load(kr, p.c.k, cur);
-            }
-            // V
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(C::bVE + st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
-                return;
-            const float to = __uint_as_float((uint32_t)min(254, 260 - exp_run) << 23);   // 2^(6 - E)
-            const uint32_t fv = pack_f16x2(vs * to, vs * to);
-#pragma unroll
-            for (int i = 0; i < R::kSteps; ++i) {
-                const int kk = i * R::kRowsPerStep + sub_row;
-                const uint32_t f = __shfl_sync(0xffffffffu, fv, kk);
-                uint4 x = vr.x[i];
-                if (f == 0u) x = make_uint4(0, 0, 0, 0);
-                store(C::kV + st * C::kTileBytes, kk, x, f);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::bVF + st));
-            if (more1) load(vr, p.c.v, cur);
+            if (lane == 0) mbar_arrive(bar(full + (int)st));
+            if (more1) load(row4, tile1);
             row4 = row4_2;
             more1 = more2;
-            tile1 = tile2;
+            tile1 = ahead.off + ak;
         }
     }
 }
@@ -631,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_role<D>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);
     } else {
         regs_release<kWidenRegs>();
-        widen_role<D, kInt8>(p, w, walk, (int)warp - 12, (int)lane, base, smem, abort);
+        widen_role<D, kInt8>(p, w, walk, warp >= 16, (int)(warp & 3u), (int)lane, base, smem, abort);
     }
     tc_fence_before();
     __syncthreads();

@@ -4,12 +4,16 @@
 // prefix's keys, 4 D flop per row and key against 2 (D + 4) bytes per key: from about
 // 150 rows on the products bound it, not HBM.  The 8-bit codes are widened once per 256
 // rows, in shared memory:
-//   K' = fp16(code), exact; the key's scale multiplies its scores in fp32;
+//   K' = fp16(code) fp16(ks 2^(6 - F)), F the largest binary exponent of a key scale in the
+//        tile: exact for power-of-two scales, otherwise off by two roundings to 11 bits.
+//        That is too coarse for the LSE of few keys, so int8 caches (whose scales are not
+//        powers of two) with prefixes below kFoldKeys take K' = fp16(code), exact, and the
+//        key's scale multiplies its scores in fp32 (kFold false; 1.6x the softmax's work);
 //   V' = fp16(code) fp16(vs 2^(6 - E)), E the largest binary exponent of a value scale
 //        so far (O is rescaled when it grows): exact for power-of-two scales, otherwise
 //        off by two roundings to 11 bits; a row keeps 10 bits down to 2^-30 of the largest;
 //   Q' = fp16(q 2^-e), e the row's largest binary exponent (as in bsattn_decode.cu).
-// With t_j = S_j ks_j and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 6) is rounded
+// With t_j the scores in true units and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 6) is rounded
 // to fp16 for P V', l sums it in fp32; out = O 2^(E - 6) / l, log2-LSE = m - 6 + log2 l.
 //
 // A segment is (KV head, 256 query rows): two 128-row tiles ("slots") that share each
@@ -44,12 +48,16 @@ constexpr uint32_t kCtrlRegs = 32, kSoftmaxRegs = 144, kWidenRegs = 80;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;  // 128 rows x 64 fp16: one 128-byte swizzle span
+// int8 prefixes from here on put key scales into K': the error of a score, 2^-11 of it
+// at most, averages out over the keys that the LSE sums.
+constexpr int kFoldKeys = 4096;
 constexpr int kMsgs = 4;                   // tiles whose key scales and masks are kept
 
 struct KeyMsg {
     uint32_t keep[4];  // keys that count, one bit each
     int32_t exp;       // E (biased) of the value factors
-    int32_t pad[3];
+    int32_t key_exp;   // F (biased) of the key factors
+    int32_t pad[2];
 };
 
 template <int D>
@@ -90,7 +98,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
 }
 
 // One slot: warps 4-7 (t = 0) or 8-11 (t = 1), one row per thread.
-template <int D>
+template <int D, bool kFold>
 __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &w, Walk walk, uint32_t tmem, int t,
                                              uint32_t warp, uint32_t lane, uint32_t base, uint8_t *smem,
                                              volatile int *abort) {
@@ -161,17 +169,22 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             const uint4 kw = *reinterpret_cast<const uint4 *>(msg->keep);
             const bool masked = (kw.x & kw.y & kw.z & kw.w) != 0xffffffffu;
             const int exp_new = msg->exp;
-            // 32 scores from column 32 q on, times their keys' scales; -inf where a key does not count
-            auto scores = [&](int q, float (&s)[32]) {
-                uint32_t v[32];
-                tmem_ld32(lane_addr + s_col + 32u * q, v);
-                tmem_wait_ld();
-                reg_fence(v);
+            // what a score of S is worth in units of log2
+            const float ct = kFold ? c * ex2_approx((float)(msg->key_exp - 127 - 6)) : c;
+            // 32 loaded scores of columns 32 q .. (times their keys' scales, if those are not in
+            // K'), -inf where a key does not count
+            auto scores = [&](int q, const uint32_t (&v)[32], float (&s)[32]) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const float4 f = ks[8 * q + x];
-                    fmul2(s[4 * x], s[4 * x + 1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
-                    fmul2(s[4 * x + 2], s[4 * x + 3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
+                    if constexpr (kFold) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) s[4 * x + y] = __uint_as_float(v[4 * x + y]);
+                    } else {
+                        const float4 f = ks[8 * q + x];
+                        fmul2(s[4 * x], s[4 * x + 1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                        fmul2(s[4 * x + 2], s[4 * x + 3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]),
+                              f.z, f.w);
+                    }
                 }
                 if (masked) {
                     const uint32_t keep = q == 0 ? kw.x : q == 1 ? kw.y : q == 2 ? kw.z : kw.w;
@@ -180,23 +193,37 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                         if (!((keep >> x) & 1u)) s[x] = -INFINITY;
                 }
             };
-            auto largest = [](const float (&s)[32]) {
-                float g0 = fmax3(s[0], s[1], s[2]), g1 = fmax3(s[3], s[4], s[5]);
-#pragma unroll
-                for (int x = 6; x < 30; x += 4) {
-                    g0 = fmax3(g0, s[x], s[x + 1]);
-                    g1 = fmax3(g1, s[x + 2], s[x + 3]);
-                }
-                return fmax3(g0, fmaxf(s[30], s[31]), g1);
-            };
-            // Two rolled passes, the maximum and then P, each re-reading S from tensor memory: the
-            // roles' loops have to share the instruction caches (see the header).
+            // Two passes over S, the maximum and then P.  Where scores need no factor and no
+            // mask the first is the load's own reduction.
             float m_new = m_run;
+            if (kFold && !masked) {
+                float hm[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[32];
+                    tmem_ld32_max(lane_addr + s_col + 32u * q, v, hm[q]);
+                }
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) reg_fence(hm[q]);
+                m_new = fmaxf(m_new, fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3])) * ct);
+            } else {
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                float s[32];
-                scores(q, s);
-                m_new = fmaxf(m_new, largest(s) * c);
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + s_col + 32u * q, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+                    float s[32];
+                    scores(q, v, s);
+                    float g0 = fmax3(s[0], s[1], s[2]), g1 = fmax3(s[3], s[4], s[5]);
+#pragma unroll
+                    for (int x = 6; x < 30; x += 4) {
+                        g0 = fmax3(g0, s[x], s[x + 1]);
+                        g1 = fmax3(g1, s[x + 2], s[x + 3]);
+                    }
+                    m_new = fmaxf(m_new, fmax3(g0, fmaxf(s[30], s[31]), g1) * ct);
+                }
             }
             // O is rescaled when some row's maximum grew by more than 2^8 or E grew; otherwise
             // the stale references serve (P stays below 2^14)
@@ -223,12 +250,20 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             exp_run = exp_new;
             const float nm = 6.f - m_run;
             float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            // 32 columns at a time, the next ones on their way; P over scores that have been
+            // read.  The first 64 keys are handed over while the third part is worked on.
+            auto hand_over = [&](int half) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bPR + 2 * t + half));
+            };
+            uint32_t va[32], vb[32];
+            auto part = [&](int q, uint32_t (&v)[32]) {
                 float s[32];
-                scores(q, s);
+                scores(q, v, s);
 #pragma unroll
-                for (int x = 0; x < 16; ++x) ffma2(s[2 * x], s[2 * x + 1], s[2 * x], s[2 * x + 1], c, c, nm, nm);
+                for (int x = 0; x < 16; ++x) ffma2(s[2 * x], s[2 * x + 1], s[2 * x], s[2 * x + 1], ct, ct, nm, nm);
                 uint32_t pk[16];
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
@@ -237,14 +272,26 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                     else fadd2(la0, la1, la0, la1, p0, p1);
                     pk[x] = pack_f16x2(p0, p1);
                 }
-                tmem_st16(lane_addr + s_col + 16u * q, pk);   // over scores that have been read
-                if (q & 1) {                                   // 64 keys more are ready for P V
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::bPR + 2 * t + (q >> 1)));
-                }
-            }
+                tmem_st16(lane_addr + s_col + 16u * q, pk);
+            };
+            tmem_ld32(lane_addr + s_col, va);
+            tmem_wait_ld();
+            reg_fence(va);
+            tmem_ld32(lane_addr + s_col + 32u, vb);
+            part(0, va);
+            tmem_wait_ld();
+            reg_fence(vb);
+            tmem_ld32(lane_addr + s_col + 64u, va);
+            part(1, vb);
+            tmem_wait_ld();
+            reg_fence(va);
+            tmem_ld32(lane_addr + s_col + 96u, vb);
+            part(2, va);
+            hand_over(0);
+            tmem_wait_ld();
+            reg_fence(vb);
+            part(3, vb);
+            hand_over(1);
             const float l_tile = (la0 + lb0) + (la1 + lb1);
             l_run = l_run * alpha + l_tile;
             ++done;
@@ -300,11 +347,11 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
 }
 
 // Widens the codes of K tiles (four warps, 32 keys each) or V tiles (four more); one code
-// for both, K with factors of 1, so that the warps share the instruction caches.
+// for both, so that the warps share the instruction caches.
 //
 // Lane: 8 codes of a row (16 bytes of fp16, one swizzle piece), D / 8 lanes to a row; a
 // tile's codes are loaded while the tile before it is widened.
-template <int D, bool kInt8>
+template <int D, bool kInt8, bool kFold>
 __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w, Walk walk, bool values, int warp,
                                            int lane, uint32_t base, uint8_t *smem, volatile int *abort) {
     using C = Cfg<D>;
@@ -329,7 +376,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     // What is loaded of a tile one tile ahead.
     int run0, run1, n;  // cache rows of the warp's keys 0 .. 15 and 16 .. 31 (or -1), keys of the tile
     float scale;        // of the warp's key `lane`
-    uint4 vs4;          // value scales of the tile's keys 4 lane ..
+    uint4 ks4, vs4;     // scales of the tile's keys 4 lane ..
     uint2 raw[kSteps][kSpans];
     auto load = [&](int row4, int tile) {
         run0 = __shfl_sync(0xffffffffu, row4, warp * 8);
@@ -337,17 +384,37 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         n = min(kTile, n_keys - tile * kTile);
         const int row = lane < 16 ? run0 : run1;
         scale = row >= 0 && warp * 32 + lane < n ? __ldg(scales + (long long)row + (lane & 15)) : 0.f;
-        vs4 = row4 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
+        const bool on4 = row4 >= 0;
+        ks4 = on4 && kFold && !values ? __ldg(reinterpret_cast<const uint4 *>(p.c.ks + row4)) : make_uint4(0, 0, 0, 0);
+        vs4 = on4 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
         const uint8_t *a0 = codes + ((long long)run0 + sub_row) * D + piece * 8;
         const uint8_t *a1 = codes + ((long long)run1 + sub_row) * D + piece * 8;
+        if (run0 >= 0 && run1 >= 0 && warp * 32 + 32 <= n) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const uint8_t *at = (i < 4 ? a0 : a1) + (i & 3) * 4 * D;
-            const bool on = (i < 4 ? run0 : run1) >= 0 && warp * 32 + i * 4 + sub_row < n;
+            for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-            for (int x = 0; x < kSpans; ++x)
-                raw[i][x] = on ? __ldg(reinterpret_cast<const uint2 *>(at + x * 64)) : make_uint2(0, 0);
+                for (int x = 0; x < kSpans; ++x)
+                    raw[i][x] = __ldg(reinterpret_cast<const uint2 *>((i < 4 ? a0 : a1) + (i & 3) * 4 * D + x * 64));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const bool on = (i < 4 ? run0 : run1) >= 0 && warp * 32 + i * 4 + sub_row < n;
+#pragma unroll
+                for (int x = 0; x < kSpans; ++x) {
+                    raw[i][x] = make_uint2(0, 0);
+                    if (on) raw[i][x] = __ldg(reinterpret_cast<const uint2 *>((i < 4 ? a0 : a1) + (i & 3) * 4 * D + x * 64));
+                }
+            }
         }
+    };
+    // Largest binary exponent (biased, at least 1) of a tile's scales; NaN and infinity do not count.
+    auto largest_exp = [&](uint4 x) -> int {
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        uint32_t top = 1u << 23;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (v[i] < 0x7f800000u && 4 * lane + i < n) top = max(top, v[i]);
+        return (int)(__reduce_max_sync(0xffffffffu, top) >> 23);
     };
     // `ahead` walks two tiles in front: its tile's page is being looked up while the tile
     // before it is loaded and the one before that is widened.
@@ -371,18 +438,12 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         int exp_run = 1;            // E starts anew with a segment's sums
         for (int k = 0; k < walk.n; ++k, ++it) {
             const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
-            // the largest value scale of the tile (its bits; NaN and infinity do not count)
-            uint32_t top = 0;
-            const uint32_t v4[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (v4[i] < 0x7f800000u && 4 * lane + i < n) top = max(top, v4[i]);
-            top = __reduce_max_sync(0xffffffffu, top);
-            exp_run = max(exp_run, (int)(top >> 23));
+            exp_run = max(exp_run, largest_exp(vs4));
+            const int exp = kFold && !values ? largest_exp(ks4) : exp_run;
             step();
             const int row4_2 = look_ahead();
-            float f32 = 1.f;
-            if (values) f32 = scale * __uint_as_float((uint32_t)min(254, 260 - exp_run) << 23);   // vs 2^(6 - E)
+            float f32 = 1.f;   // scale 2^(6 - E), or 2^(6 - F)
+            if (kFold || values) f32 = scale * __uint_as_float((uint32_t)min(254, 260 - exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
             const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF;
             if (!__all_sync(0xffffffffu, mbar_wait(bar(empty + (int)st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
@@ -404,11 +465,14 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             }
             if (!values) {
                 const uint32_t keep = __ballot_sync(0xffffffffu, (lane < 16 ? run0 : run1) >= 0 && warp * 32 + lane < n);
-                reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = scale;
+                if (!kFold) reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = scale;
                 if (lane == 0) {
                     KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
                     msg->keep[warp] = keep;
-                    if (warp == 0) msg->exp = exp_run;
+                    if (warp == 0) {
+                        msg->exp = exp_run;
+                        msg->key_exp = exp;
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -422,7 +486,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     }
 }
 
-template <int D, bool kInt8>
+template <int D, bool kInt8, bool kFold>
 __global__ void __launch_bounds__(kThreads, 1)
     bsattn_prefix_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w) {
     using C = Cfg<D>;
@@ -570,10 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_release<kCtrlRegs>();
     } else if (warp < 12) {
         regs_claim<kSoftmaxRegs>();
-        softmax_role<D>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);
+        softmax_role<D, kFold>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);
     } else {
         regs_release<kWidenRegs>();
-        widen_role<D, kInt8>(p, w, walk, warp >= 16, (int)(warp & 3u), (int)lane, base, smem, abort);
+        widen_role<D, kInt8, kFold>(p, w, walk, warp >= 16, (int)(warp & 3u), (int)lane, base, smem, abort);
     }
     tc_fence_before();
     __syncthreads();
@@ -583,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool kInt8>
+template <int D, bool kInt8, bool kFold>
 cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
     using C = Cfg<D>;
     static int attr_set_for_device[64] = {0};
@@ -594,10 +658,10 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
     if (!attr_set_for_device[dev]) {
         // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, bsattn_prefix_kernel<D, kInt8>);
+        e = cudaFuncGetAttributes(&fa, bsattn_prefix_kernel<D, kInt8, kFold>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-        e = cudaFuncSetAttribute(bsattn_prefix_kernel<D, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(bsattn_prefix_kernel<D, kInt8, kFold>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)C::kAlloc);
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
@@ -612,14 +676,19 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)w.pre_cuts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kAlloc;
-    return cudaLaunchKernelEx(&cfg, bsattn_prefix_kernel<D, kInt8>, p, w);
+    return cudaLaunchKernelEx(&cfg, bsattn_prefix_kernel<D, kInt8, kFold>, p, w);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
-    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, w, stream) : launch<128, false>(p, w, stream);
-    return p.c.int8 ? launch<64, true>(p, w, stream) : launch<64, false>(p, w, stream);
+    const bool fold = !p.c.int8 || p.prefix_len >= kFoldKeys;
+    if (p.c.D == 128) {
+        if (!p.c.int8) return launch<128, false, true>(p, w, stream);
+        return fold ? launch<128, true, true>(p, w, stream) : launch<128, true, false>(p, w, stream);
+    }
+    if (!p.c.int8) return launch<64, false, true>(p, w, stream);
+    return fold ? launch<64, true, true>(p, w, stream) : launch<64, true, false>(p, w, stream);
 }
 
 }  // namespace bsattn

@@ -44,7 +44,9 @@ namespace bsattn {
 
 namespace {
 
-constexpr int kSegCost = 2;  // groups of 16 keys that starting and ending a segment costs
+constexpr int kSegCost = 2;   // groups of 16 keys that starting and ending a segment costs
+constexpr int kMinPiece = 2;  // places that make a worker of their own worth its part in the join (1, 4, 8 measured
+                              // slower on short calls)
 
 // 16 bytes from global to shared memory, past L1; counted by the thread's copy groups.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
@@ -318,29 +320,38 @@ struct Worker {
         }
     }
 
-    // Starts a segment of n keys and works on its groups t0 .. t1.
-    __device__ __forceinline__ void groups(const Seg &s, int n, const ListRow &lr, int t0, int t1) {
+    // Starts a segment of n keys, behind `lead` groups of the shared prefix, and works on
+    // its groups t0 .. t1.
+    __device__ __forceinline__ void groups(const Seg &s, int lead, int n, const ListRow &lr, int t0, int t1) {
         const bool listed = p.has_lists && !s.prefix;
-        const int32_t *table = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
+        const int32_t *own = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
         // cache row of group i's first key (-1: nothing to read) and how many of its keys count, one group per lane
         auto look_up = [&](int i, int &row, int &nv) {
             row = -1;
             nv = 0;
             if (i >= t1) return;
-            int key = i * 16, lim = 16;
-            if (listed) {
+            const int32_t *table = own;
+            int keys = n, lim = 16;
+            if (i < lead) {                      // the shared prefix's groups
+                table = p.prefix_table;
+                keys = p.prefix_len;
+            } else {
+                i -= lead;
+            }
+            int key = i * 16;
+            if (listed && table == own) {
                 const int e = i >> 3;
                 const bool masked = e >= lr.full;
                 const int tile = __ldg((masked ? p.mask_idx + (e - lr.full) : p.full_idx + e) + lr.at);
                 if (tile < 0 || tile >= lr.nn) {
-                    if ((i & 7) == 0 || i == t0) raise(p, BSATTN_FLAG_BAD_INDEX);
+                    if ((i & 7) == 0 || i + lead == t0) raise(p, BSATTN_FLAG_BAD_INDEX);
                     return;
                 }
                 if (tile >= (n + kTile - 1) / kTile) return;
                 key = tile * kTile + (i & 7) * 16;
                 if (masked && p.vl) lim = __ldg(p.vl + (long long)s.b * p.list_n + tile) - (i & 7) * 16;
             }
-            nv = min(min(lim, 16), n - key);
+            nv = min(min(lim, 16), keys - key);
             if (nv <= 0) return;
             const int page = __ldg(table + (key >> p.c.page_shift));
             if (page < 0 || page >= p.c.num_pages) {
@@ -413,7 +424,7 @@ struct Worker {
                     y[2 * i + 1] = o[i][n][2 + e] * inv;
                 }
                 RowOut at;
-                if (!s.prefix && complete && w.mode == kNoPrefix) at = RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
+                if (!s.prefix && complete && w.direct) at = RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
                 else if (s.prefix) at = RowOut{1, ((long long)seg + worker) * w.rows_p + r};
                 else at = RowOut{2, ((long long)(seg - w.sp) + worker) * p.G + r};
                 if (at.kind == 0 && !p.out_f32) {
@@ -454,15 +465,15 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     // Where each worker's piece of the line begins.  Each thread sums the cost of a run
     // of sequences (or, with lists, of (sequence, head) pairs); CTA c also writes the
     // records of every gridDim-th of them: the workers its segments' parts lie with.
-    const int g_pre = w.sp ? (p.prefix_len + 15) / 16 : 0;
+    const int g_pre = w.sp ? (p.prefix_len + 15) / 16 : 0, lead = w.mode == kEach ? (p.prefix_len + 15) / 16 : 0;
     const long long line_pre = (long long)w.sp * (g_pre + kSegCost);
     const int units = p.has_lists ? p.B * p.c.H : p.B, per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     auto unit_groups = [&](int x, bool check) -> int {
-        if (!p.has_lists) return (seq_keys(p, x, check) + 15) / 16;
+        if (!p.has_lists) return lead + (seq_keys(p, x, check) + 15) / 16;
         const int b = x / p.c.H, h = x - b * p.c.H;
         const ListRow r = list_row(p, b, h, seq_keys(p, b, check && h == 0), check);
-        return 8 * (r.full + r.mask);
+        return lead + 8 * (r.full + r.mask);
     };
     const int reps = p.has_lists ? 1 : p.c.H;  // segments of a unit, of equal length
     long long sum = 0;
@@ -483,8 +494,8 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
         if (i < warp) at += warp_sum[i];
         total += warp_sum[i];
     }
-    // pieces of at least one place each: a segment's parts lie with consecutive workers
-    const long long cuts = min((long long)gridDim.x * kW, total);
+    // pieces of kMinPiece places or a few less: a segment's parts lie with consecutive workers
+    const long long cuts = min((long long)gridDim.x * kW, (total + kMinPiece - 1) / kMinPiece);
     if (tid <= kW) {  // where the pieces of this CTA's workers begin
         const long long worker = min((long long)blockIdx.x * kW + tid, cuts);
         piece_at[tid] = cuts ? total * worker / cuts : 0;
@@ -534,11 +545,12 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
                 lr = list_row(p, s.b, s.h, n, false);
                 g = 8 * (lr.full + lr.mask);
             }
+            if (!s.prefix) g += lead;
             if (g == 0) continue;
             const long long first = begin + kSegCost;
             const int t0 = (int)max(0ll, min((long long)g, lo - first)), t1 = (int)max(0ll, min((long long)g, hi - first));
             if (t0 < t1) {
-                k.groups(s, n, lr, t0, t1);
+                k.groups(s, lead, n, lr, t0, t1);
                 k.finish(w, s, seg, (int)worker, t0 == 0 && t1 == g);
             }
             begin = first + g;

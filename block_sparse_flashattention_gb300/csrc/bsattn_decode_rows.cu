@@ -352,7 +352,7 @@ struct Consumer {
     }
 
     __device__ __forceinline__ RowOut row_out(const Seg &s, int seg, bool complete, int r) const {
-        if (complete && w.mode == kNoPrefix) return RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
+        if (complete && w.direct) return RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};
         return RowOut{2, ((long long)seg + blockIdx.x) * p.G + r};
     }
 

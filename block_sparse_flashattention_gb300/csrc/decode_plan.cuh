@@ -12,9 +12,16 @@ constexpr int kStreamWarps = 8;    // warps of a streaming CTA, each a worker of
 constexpr int kStreamRows = 16;    // query rows a streaming worker holds
 constexpr int kBlockRows = 256;    // query rows of a segment in the prefix kernel
 
-// Up to 16 query rows a KV head meet the prefix inside the streaming kernel's line
-// (kInLine); more run in a kernel of their own (kOwnKernel).
-enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2 };
+// How the keys of a shared prefix are met.  kEach: they are the first keys of every
+// sequence's own segment, read (from L2) once per sequence: no kernel and no parts more
+// than without a prefix.  kInLine: up to 16 query rows a KV head, as segments of the
+// streaming kernel's line.  kOwnKernel: in the prefix kernel.
+enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2, kEach = 3 };
+
+// Cache bytes that all sequences together may read of the prefix under kEach.  Measured
+// (e4m3, D = 128, own keys of 1 to 200, us a call, kEach against the prefix kernel): 17 MB
+// 14.2 : 18.9, 41 MB 18.2 : 20.1, 68 MB 17.9 : 18.8, 135 MB 28.7 : 20.4, 270 MB 42 : 31.
+constexpr long long kEachBytes = 76ll << 20;
 
 // Segments: of the prefix, one per KV head (kInLine) or (KV head, block of 256 query
 // rows); of the sequences' own keys, (sequence, KV head).  A line of keys is cut over
@@ -23,6 +30,7 @@ enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2 };
 // advances, so no two parts share a number.
 struct Plan {
     int mode;
+    int direct;                            // a segment of the line holds all of its rows' keys
     int streaming;                         // G <= 16: bsattn_decode.cu, else bsattn_decode_rows.cu
     int row_blocks, pre_segs;              // prefix kernel: blocks per head, segments
     int rows_p;                            // rows a prefix part has room for
@@ -44,8 +52,10 @@ struct Plan {
 inline Plan make_plan(int B, int H, int G, int D, int prefix_len, int sms) {
     Plan w = {};
     const int rows = B * G;
-    w.mode = prefix_len <= 0 ? kNoPrefix : rows <= kStreamRows ? kInLine : kOwnKernel;
     w.streaming = G <= kStreamRows ? 1 : 0;
+    const bool each = w.streaming && (long long)B * H * prefix_len * 2 * (D + 4) <= kEachBytes;
+    w.mode = prefix_len <= 0 ? kNoPrefix : each ? kEach : rows <= kStreamRows ? kInLine : kOwnKernel;
+    w.direct = w.mode == kNoPrefix || w.mode == kEach;
     w.row_blocks = w.mode == kOwnKernel ? (rows + kBlockRows - 1) / kBlockRows : 0;
     w.pre_segs = H * w.row_blocks;
     // the prefix kernel's parts hold both slots of 128 rows

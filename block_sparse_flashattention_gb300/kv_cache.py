@@ -225,6 +225,15 @@ def alloc_decode_workspace(cache: KVCache, B: int, Hq: int, *, prefix_len: int =
                        device=cache.device)
 
 
+def _meta_fits(meta, index):
+    """Whether a Meta's tensors are contiguous int32 tensors of device `index` (addresses are taken as given)."""
+    for t in (meta.full_cnt, meta.full_idx, meta.mask_cnt, meta.mask_idx, meta.cu_block_idx_offsets):
+        if t is not None and not isinstance(t, int) and not (t.dtype is I32 and t.get_device() == index and
+                                                             t.is_contiguous()):
+            return False
+    return True
+
+
 def _decode_checks(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, out, out_dtype, lse,
                    workspace, err_flag):
     dev = cache.device
@@ -239,11 +248,8 @@ def _decode_checks(q, cache, prefix_table, prefix_len, page_table, seqlens, meta
     _ints(seqlens, "seqlens", 1, dev)
     if seqlens.shape[0] != B:
         raise ValueError("seqlens must have one entry per sequence")
-    if meta is not None:
-        for name in ("full_cnt", "full_idx", "mask_cnt", "mask_idx", "cu_block_idx_offsets"):
-            t = getattr(meta, name)
-            if t is not None and not isinstance(t, int) and (t.device != dev or t.dtype != I32 or not t.is_contiguous()):
-                raise ValueError(f"meta.{name} must be a contiguous torch.int32 tensor on the cache's device")
+    if meta is not None and not _meta_fits(meta, cache.index):
+        raise ValueError("meta's tensors must be contiguous torch.int32 tensors on the cache's device")
     if kv_valid_len is not None:
         if meta is None:
             raise ValueError("kv_valid_len belongs to the listed tiles of meta")
@@ -275,14 +281,14 @@ def _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_va
                                                          meta, kv_valid_len, softmax_scale, out, out_dtype, lse,
                                                          workspace, err_flag, None))
     index, shape = cache.index, q.shape
-    # what a step of a serving loop passes: contiguous tensors of one device, no lists, no
-    # error word, outputs allocated here; anything else takes the full checks
+    # what a step of a serving loop passes: contiguous tensors of one device, no error word,
+    # outputs allocated here; anything else takes the full checks
     if not (len(shape) == 3 and q.dtype is BF16 and shape[2] == cache.D and q.is_contiguous() and
             q.get_device() == index >= 0 and seqlens.dtype is I32 and seqlens.is_contiguous() and
             seqlens.shape == shape[:1] and seqlens.get_device() == index and page_table is not None and
             page_table.dtype is I32 and page_table.is_contiguous() and page_table.dim() == 2 and
-            page_table.shape[0] == shape[0] and page_table.get_device() == index and meta is None and
-            kv_valid_len is None and out is None and lse is None and err_flag is None and out_dtype is None and
+            page_table.shape[0] == shape[0] and page_table.get_device() == index and
+            (meta is None or _meta_fits(meta, index)) and kv_valid_len is None and out is None and lse is None and err_flag is None and out_dtype is None and
             (workspace is None or (workspace.get_device() == index and workspace.is_contiguous())) and
             (prefix_table is None or (prefix_table.dtype is I32 and prefix_table.dim() == 1 and
                                       prefix_table.is_contiguous() and prefix_table.get_device() == index and

@@ -524,8 +524,9 @@ bsattn_status bsattn_kv_read(const bsattn_kv_cache *cache, const int32_t *page_t
  *   s_j = softmax_scale * q . K_j over the keys j < seqlens[b], or, with meta, over
  *   those keys of the listed KV tiles only,
  *   lse = ln(sum_j exp(s_j)),  out = sum_j exp(s_j - lse) V_j;
- * no key: out = 0, lse = -inf.  K_j, V_j are the cached values (code * scale); all
- * sums are fp32, and exp(s_j) V_j's weights are rounded to fp16 (11 bits).
+ * no key: out = 0, lse = -inf.  K_j, V_j are the cached values (code * scale); products
+ * with codes are exact, all sums are fp32, and the weights exp(s_j) vs_j of the value
+ * codes are rounded to fp16 (11 bits).
  *
  * q            device bf16, B rows of [Hq, D] contiguous elements, q_stride apart (at
  *              least Hq * D, a multiple of 8); 16-byte aligned.
@@ -561,8 +562,12 @@ bsattn_status bsattn_decode(const void *q, int64_t q_stride, int32_t B, int32_t 
  * bsattn_decode_shared_prefix -- bsattn_decode for a batch whose sequences all begin
  * with the same prefix: sequence b's keys are the prefix_len keys of the prefix, then
  * the seqlens[b] keys of its own page-table row (which meta and kv_valid_len, if
- * given, refer to; the prefix is attended whole).  The prefix's K and V are read once
- * for all sequences.
+ * given, refer to; the prefix is attended whole).  The prefix's K and V are read from
+ * HBM once for all sequences, and, where that is worth a kernel of its own, worked on
+ * once for all: many query rows then meet each key.  Scores keep the exactness that
+ * bsattn_decode describes, except those of int8 prefixes of 4096 keys and more and of
+ * caller-made scales that are not powers of two: there a key's scale is rounded to
+ * 11 bits, and its product with each code once more.
  *
  * prefix_table device int32 [ceil(prefix_len / page_size)]: the prefix's pages.
  * prefix_len   >= 0 (0: bsattn_decode).  table_cols may be 0: no sequence has keys of

@@ -56,14 +56,19 @@ class Pool:
         return t, torch.from_numpy(t).to(self.device)
 
     def host(self, name, table, h, positions):
-        return okv.gather(self.codes[name], self.scales[name], table, h, positions, self.dtype)
+        """64-bit rows of head h at positions; a page outside the cache yields no row (okv.gather, vectorised)."""
+        pos = np.asarray(positions, np.int64)
+        pg = np.asarray(table, np.int64)[pos // self.page] if len(pos) else pos
+        on = (pg >= 0) & (pg < len(self.codes[name]))
+        pg, row = pg[on], pos[on] % self.page
+        return okv.values(self.codes[name][pg, h, row], self.dtype) * self.scales[name][pg, h, row].astype(np.float64)[:, None]
 
 
 def pages_for(lens, page):
     return sum(-(-max(n, 0) // page) for n in lens)
 
 
-def expect(pool, q, G, parts, scale):
+def expect(pool, q, G, parts, scale, coarse=0.0):
     """Oracle (out, lse, out tolerance, lse tolerance) [B, Hq, ...]; parts(b, h): list of (table, positions).
 
     Scores: a dot product of D fp32 terms, accumulated in any order, is off by at most
@@ -72,7 +77,11 @@ def expect(pool, q, G, parts, scale):
     own size: ds = (D + 8) 2^-24 scale sum_d |q_d k_d|, largest over the keys.  A weight
     exp(s - m) is then off by 2 ds (numerator and sum) + 2^-20 (the exponentials' and
     sums' own rounding) relatively, by its rounding to fp16, 2^-11 of it, and absolutely
-    by 2^-32 of the largest weight times its value where it is too small for fp16."""
+    by 2^-32 of the largest weight times its value where it is too small for fp16.
+
+    coarse: relative error of every element of K and V that the call may make (prefixes
+    whose scales are rounded with the codes: 2 * 2^-11); a score is then off by coarse *
+    scale * |q| . |k| more, and a value by coarse of it."""
     B, Hq, D = q.shape
     out, lse = np.zeros((B, Hq, D)), np.full((B, Hq), -math.inf)
     to, tl = np.zeros((B, Hq, D)), np.zeros((B, Hq))
@@ -85,8 +94,8 @@ def expect(pool, q, G, parts, scale):
                 o, l, spread = okv.attend(x, k, v, scale)
                 out[b, h * G + g], lse[b, h * G + g] = o, l
                 if len(k):
-                    ds = (D + 8) * 2.0 ** -24 * scale * float(np.max(np.abs(k) @ np.abs(x)))
-                    to[b, h * G + g] = spread * (2.0 ** -11 + 2 * ds + 2.0 ** -20) + len(k) * 2.0 ** -32 * np.max(np.abs(v))
+                    ds = ((D + 8) * 2.0 ** -24 + coarse) * scale * float(np.max(np.abs(k) @ np.abs(x)))
+                    to[b, h * G + g] = spread * (2.0 ** -11 + 2 * ds + coarse + 2.0 ** -20) + len(k) * 2.0 ** -32 * np.max(np.abs(v))
                     tl[b, h * G + g] = ds + 2.0 ** -20 + abs(l) * 2.0 ** -22
     return out, lse, to, tl
 

@@ -4,17 +4,17 @@
 // prefix's keys, 4 D flop per row and key against 2 (D + 4) bytes per key: from about
 // 150 rows on the products bound it, not HBM.  The 8-bit codes are widened once per 256
 // rows, in shared memory:
-//   K' = fp16(code) fp16(ks 2^(6 - F)), F the largest binary exponent of a key scale in the
-//        tile: exact for power-of-two scales, otherwise off by two roundings to 11 bits.
-//        That is too coarse for the LSE of few keys, so int8 caches (whose scales are not
-//        powers of two) with prefixes below kFoldKeys take K' = fp16(code), exact, and the
-//        key's scale multiplies its scores in fp32 (kFold false; 1.6x the softmax's work);
+//   K' = fp16(code) 2^(f - F + 6), exact: f the binary exponent of the key's scale, F the
+//        largest in the tile; what is left of the scale, r in [1, 2), multiplies the
+//        key's scores in fp32, and only where some key of 32 has r > 1 (int8; the scales
+//        that e4m3 rows are given are powers of two);
 //   V' = fp16(code) fp16(vs 2^(6 - E)), E the largest binary exponent of a value scale
 //        so far (O is rescaled when it grows): exact for power-of-two scales, otherwise
 //        off by two roundings to 11 bits; a row keeps 10 bits down to 2^-30 of the largest;
 //   Q' = fp16(q 2^-e), e the row's largest binary exponent (as in bsattn_decode.cu).
-// With t_j the scores in true units and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 6) is rounded
-// to fp16 for P V', l sums it in fp32; out = O 2^(E - 6) / l, log2-LSE = m - 6 + log2 l.
+// With t_j the scores in true units and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 4)
+// is rounded to fp16 for P V', l sums it in fp32; out = O 2^(E - 6) / l, log2-LSE = m - 4 +
+// log2 l.  The reference m is moved only when some weight could pass 2^15.
 //
 // A segment is (KV head, 256 query rows): two 128-row tiles ("slots") that share each
 // K/V tile.  With 128 rows or fewer both slots hold the same rows and take the key tiles
@@ -41,30 +41,33 @@ namespace {
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
 // 96 registers per thread at launch; the control warpgroup's surplus and some of the
-// widening ones' go to the softmax: 128 * 32 + 2 * 128 * 144 + 2 * 128 * 80 = 61440 =
-// 640 * 96.
+// widening ones' go to the softmax: 128 * 48 + 2 * 128 * 144 + 2 * 128 * 72 = 61440 =
+// 640 * 96.  Int8 codes take more to widen, the e4m3 softmax keeps more loads in flight.
 constexpr int kLaunchRegs = 96;
-constexpr uint32_t kCtrlRegs = 32, kSoftmaxRegs = 144, kWidenRegs = 80;
-static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+constexpr uint32_t kCtrlRegs = 48;
+template <bool kInt8>
+constexpr uint32_t kSoftmaxRegs = kInt8 ? 144 : 152;
+template <bool kInt8>
+constexpr uint32_t kWidenRegs = kInt8 ? 72 : 64;
+static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs<true> + 256 * kWidenRegs<true> <= (uint32_t)kThreads * kLaunchRegs &&
+                  128 * kCtrlRegs + 256 * kSoftmaxRegs<false> + 256 * kWidenRegs<false> <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;  // 128 rows x 64 fp16: one 128-byte swizzle span
-// int8 prefixes from here on put key scales into K': the error of a score, 2^-11 of it
-// at most, averages out over the keys that the LSE sums.
-constexpr int kFoldKeys = 4096;
 constexpr int kMsgs = 4;                   // tiles whose key scales and masks are kept
 
 struct KeyMsg {
     uint32_t keep[4];  // keys that count, one bit each
     int32_t exp;       // E (biased) of the value factors
     int32_t key_exp;   // F (biased) of the key factors
-    int32_t pad[2];
+    uint8_t rest[4];   // whether some r of keys 32 q .. is not 1
+    int32_t pad;
 };
 
 template <int D>
 struct Cfg {
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + 2 * kTileBytes;
-    static constexpr uint32_t kScale = kV + 2 * kTileBytes;          // kMsgs x 128 key scales
+    static constexpr uint32_t kScale = kV + 2 * kTileBytes;          // kMsgs x 128 rests r of key scales
     static constexpr uint32_t kMsg = kScale + kMsgs * 512u;
     static constexpr uint32_t kBar = kMsg + kMsgs * (uint32_t)sizeof(KeyMsg);
     // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete
@@ -98,7 +101,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
 }
 
 // One slot: warps 4-7 (t = 0) or 8-11 (t = 1), one row per thread.
-template <int D, bool kFold>
+template <int D, bool kInt8>
 __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &w, Walk walk, uint32_t tmem, int t,
                                              uint32_t warp, uint32_t lane, uint32_t base, uint8_t *smem,
                                              volatile int *abort) {
@@ -170,21 +173,24 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             const bool masked = (kw.x & kw.y & kw.z & kw.w) != 0xffffffffu;
             const int exp_new = msg->exp;
             // what a score of S is worth in units of log2
-            const float ct = kFold ? c * ex2_approx((float)(msg->key_exp - 127 - 6)) : c;
-            // 32 loaded scores of columns 32 q .. (times their keys' scales, if those are not in
-            // K'), -inf where a key does not count
-            auto scores = [&](int q, const uint32_t (&v)[32], float (&s)[32]) {
+            const float ct = c * ex2_approx((float)(msg->key_exp - 127 - 6));
+            const uchar4 rest = *reinterpret_cast<const uchar4 *>(msg->rest);
+            // Int8 tiles take the general way, whose two passes are rolled: measured on 512 rows by
+            // 32768 keys, 8 heads, 91 us against 103 unrolled with loads ahead, the roles' loops
+            // sharing the instruction caches.  E4m3 tiles with power-of-two scales take the short
+            // one: 80 us with loads ahead against 97 rolled.
+            const bool plain = !kInt8 && !masked && !(rest.x | rest.y | rest.z | rest.w);
+            // 32 scores of columns 32 q .. times r; -inf where a key does not count
+            auto scores = [&](int q, float (&s)[32]) {
+                uint32_t v[32];
+                tmem_ld32(lane_addr + s_col + 32u * q, v);
+                tmem_wait_ld();
+                reg_fence(v);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    if constexpr (kFold) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) s[4 * x + y] = __uint_as_float(v[4 * x + y]);
-                    } else {
-                        const float4 f = ks[8 * q + x];
-                        fmul2(s[4 * x], s[4 * x + 1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
-                        fmul2(s[4 * x + 2], s[4 * x + 3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]),
-                              f.z, f.w);
-                    }
+                    const float4 f = ks[8 * q + x];
+                    fmul2(s[4 * x], s[4 * x + 1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                    fmul2(s[4 * x + 2], s[4 * x + 3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
                 }
                 if (masked) {
                     const uint32_t keep = q == 0 ? kw.x : q == 1 ? kw.y : q == 2 ? kw.z : kw.w;
@@ -193,10 +199,9 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                         if (!((keep >> x) & 1u)) s[x] = -INFINITY;
                 }
             };
-            // Two passes over S, the maximum and then P.  Where scores need no factor and no
-            // mask the first is the load's own reduction.
+            // The first pass, the maximum: the load's own reduction where scores need no factor and no mask.
             float m_new = m_run;
-            if (kFold && !masked) {
+            if (plain) {
                 float hm[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -206,16 +211,12 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) reg_fence(hm[q]);
-                m_new = fmaxf(m_new, fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3])) * ct);
+                m_new = fmaxf(m_run, fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3])) * ct);
             } else {
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t v[32];
-                    tmem_ld32(lane_addr + s_col + 32u * q, v);
-                    tmem_wait_ld();
-                    reg_fence(v);
                     float s[32];
-                    scores(q, v, s);
+                    scores(q, s);
                     float g0 = fmax3(s[0], s[1], s[2]), g1 = fmax3(s[3], s[4], s[5]);
 #pragma unroll
                     for (int x = 6; x < 30; x += 4) {
@@ -225,9 +226,9 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                     m_new = fmaxf(m_new, fmax3(g0, fmaxf(s[30], s[31]), g1) * ct);
                 }
             }
-            // O is rescaled when some row's maximum grew by more than 2^8 or E grew; otherwise
-            // the stale references serve (P stays below 2^14)
-            const bool grew = __any_sync(0xffffffffu, m_new - m_run > 8.f);
+            constexpr float kReach = 11.f;
+            const bool grew = done == 0 || __any_sync(0xffffffffu, m_new - m_run > kReach);
+            // O is rescaled when m moves or E grew
             float alpha = 1.f;
             if (grew) {
                 alpha = ex2_approx(m_run - m_new);
@@ -248,7 +249,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                 }
             }
             exp_run = exp_new;
-            const float nm = 6.f - m_run;
+            const float nm = 4.f - m_run;
             float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
             // 32 columns at a time, the next ones on their way; P over scores that have been
             // read.  The first 64 keys are handed over while the third part is worked on.
@@ -258,10 +259,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::bPR + 2 * t + half));
             };
-            uint32_t va[32], vb[32];
-            auto part = [&](int q, uint32_t (&v)[32]) {
-                float s[32];
-                scores(q, v, s);
+            auto part = [&](int q, float (&s)[32]) {
 #pragma unroll
                 for (int x = 0; x < 16; ++x) ffma2(s[2 * x], s[2 * x + 1], s[2 * x], s[2 * x + 1], ct, ct, nm, nm);
                 uint32_t pk[16];
@@ -274,24 +272,41 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                 }
                 tmem_st16(lane_addr + s_col + 16u * q, pk);
             };
-            tmem_ld32(lane_addr + s_col, va);
-            tmem_wait_ld();
-            reg_fence(va);
-            tmem_ld32(lane_addr + s_col + 32u, vb);
-            part(0, va);
-            tmem_wait_ld();
-            reg_fence(vb);
-            tmem_ld32(lane_addr + s_col + 64u, va);
-            part(1, vb);
-            tmem_wait_ld();
-            reg_fence(va);
-            tmem_ld32(lane_addr + s_col + 96u, vb);
-            part(2, va);
-            hand_over(0);
-            tmem_wait_ld();
-            reg_fence(vb);
-            part(3, vb);
-            hand_over(1);
+            auto plain_part = [&](int q, uint32_t (&v)[32]) {
+                float s[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(v[x]);
+                part(q, s);
+            };
+            if (plain) {
+                uint32_t va[32], vb[32];
+                tmem_ld32(lane_addr + s_col, va);
+                tmem_wait_ld();
+                reg_fence(va);
+                tmem_ld32(lane_addr + s_col + 32u, vb);
+                plain_part(0, va);
+                tmem_wait_ld();
+                reg_fence(vb);
+                tmem_ld32(lane_addr + s_col + 64u, va);
+                plain_part(1, vb);
+                tmem_wait_ld();
+                reg_fence(va);
+                tmem_ld32(lane_addr + s_col + 96u, vb);
+                plain_part(2, va);
+                hand_over(0);
+                tmem_wait_ld();
+                reg_fence(vb);
+                plain_part(3, vb);
+                hand_over(1);
+            } else {
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    float s[32];
+                    scores(q, s);
+                    part(q, s);
+                    if (q & 1) hand_over(q >> 1);
+                }
+            }
             const float l_tile = (la0 + lb0) + (la1 + lb1);
             l_run = l_run * alpha + l_tile;
             ++done;
@@ -341,7 +356,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             __syncwarp();
         }
         if (row_ok)
-            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - 6.f + lg2_approx(l_run);
+            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - 4.f + lg2_approx(l_run);
         tc_fence_before();
     }
 }
@@ -351,7 +366,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
 //
 // Lane: 8 codes of a row (16 bytes of fp16, one swizzle piece), D / 8 lanes to a row; a
 // tile's codes are loaded while the tile before it is widened.
-template <int D, bool kInt8, bool kFold>
+template <int D, bool kInt8>
 __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w, Walk walk, bool values, int warp,
                                            int lane, uint32_t base, uint8_t *smem, volatile int *abort) {
     using C = Cfg<D>;
@@ -385,7 +400,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         const int row = lane < 16 ? run0 : run1;
         scale = row >= 0 && warp * 32 + lane < n ? __ldg(scales + (long long)row + (lane & 15)) : 0.f;
         const bool on4 = row4 >= 0;
-        ks4 = on4 && kFold && !values ? __ldg(reinterpret_cast<const uint4 *>(p.c.ks + row4)) : make_uint4(0, 0, 0, 0);
+        ks4 = on4 && !values ? __ldg(reinterpret_cast<const uint4 *>(p.c.ks + row4)) : make_uint4(0, 0, 0, 0);
         vs4 = on4 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
         const uint8_t *a0 = codes + ((long long)run0 + sub_row) * D + piece * 8;
         const uint8_t *a1 = codes + ((long long)run1 + sub_row) * D + piece * 8;
@@ -439,11 +454,13 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         for (int k = 0; k < walk.n; ++k, ++it) {
             const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
             exp_run = max(exp_run, largest_exp(vs4));
-            const int exp = kFold && !values ? largest_exp(ks4) : exp_run;
+            const int exp = values ? exp_run : largest_exp(ks4);
             step();
             const int row4_2 = look_ahead();
-            float f32 = 1.f;   // scale 2^(6 - E), or 2^(6 - F)
-            if (kFold || values) f32 = scale * __uint_as_float((uint32_t)min(254, 260 - exp) << 23);
+            // V: vs 2^(6 - E); K: the power of two in ks, times 2^(6 - F)
+            const uint32_t bits = __float_as_uint(scale);
+            const float f32 = (values ? scale : __uint_as_float(bits & 0x7f800000u)) *
+                              __uint_as_float((uint32_t)min(254, 260 - exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
             const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF;
             if (!__all_sync(0xffffffffu, mbar_wait(bar(empty + (int)st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
@@ -465,10 +482,13 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             }
             if (!values) {
                 const uint32_t keep = __ballot_sync(0xffffffffu, (lane < 16 ? run0 : run1) >= 0 && warp * 32 + lane < n);
-                if (!kFold) reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] = scale;
+                reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] =
+                    __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+                const bool rest = __any_sync(0xffffffffu, (bits & 0x7fffffu) != 0u);
                 if (lane == 0) {
                     KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
                     msg->keep[warp] = keep;
+                    msg->rest[warp] = rest ? 1 : 0;
                     if (warp == 0) {
                         msg->exp = exp_run;
                         msg->key_exp = exp;
@@ -486,7 +506,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     }
 }
 
-template <int D, bool kInt8, bool kFold>
+template <int D, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
     bsattn_prefix_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w) {
     using C = Cfg<D>;
@@ -633,11 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
         regs_release<kCtrlRegs>();
     } else if (warp < 12) {
-        regs_claim<kSoftmaxRegs>();
-        softmax_role<D, kFold>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);
+        regs_claim<kSoftmaxRegs<kInt8>>();
+        softmax_role<D, kInt8>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);
     } else {
-        regs_release<kWidenRegs>();
-        widen_role<D, kInt8, kFold>(p, w, walk, warp >= 16, (int)(warp & 3u), (int)lane, base, smem, abort);
+        regs_release<kWidenRegs<kInt8>>();
+        widen_role<D, kInt8>(p, w, walk, warp >= 16, (int)(warp & 3u), (int)lane, base, smem, abort);
     }
     tc_fence_before();
     __syncthreads();
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool kInt8, bool kFold>
+template <int D, bool kInt8>
 cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
     using C = Cfg<D>;
     static int attr_set_for_device[64] = {0};
@@ -658,10 +678,10 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
     if (!attr_set_for_device[dev]) {
         // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, bsattn_prefix_kernel<D, kInt8, kFold>);
+        e = cudaFuncGetAttributes(&fa, bsattn_prefix_kernel<D, kInt8>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-        e = cudaFuncSetAttribute(bsattn_prefix_kernel<D, kInt8, kFold>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(bsattn_prefix_kernel<D, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)C::kAlloc);
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
@@ -676,19 +696,14 @@ cudaError_t launch(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)w.pre_cuts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kAlloc;
-    return cudaLaunchKernelEx(&cfg, bsattn_prefix_kernel<D, kInt8, kFold>, p, w);
+    return cudaLaunchKernelEx(&cfg, bsattn_prefix_kernel<D, kInt8>, p, w);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix(const DecodeParams &p, const Plan &w, cudaStream_t stream) {
-    const bool fold = !p.c.int8 || p.prefix_len >= kFoldKeys;
-    if (p.c.D == 128) {
-        if (!p.c.int8) return launch<128, false, true>(p, w, stream);
-        return fold ? launch<128, true, true>(p, w, stream) : launch<128, true, false>(p, w, stream);
-    }
-    if (!p.c.int8) return launch<64, false, true>(p, w, stream);
-    return fold ? launch<64, true, true>(p, w, stream) : launch<64, true, false>(p, w, stream);
+    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, w, stream) : launch<128, false>(p, w, stream);
+    return p.c.int8 ? launch<64, true>(p, w, stream) : launch<64, false>(p, w, stream);
 }
 
 }  // namespace bsattn

@@ -564,10 +564,8 @@ bsattn_status bsattn_decode(const void *q, int64_t q_stride, int32_t B, int32_t 
  * the seqlens[b] keys of its own page-table row (which meta and kv_valid_len, if
  * given, refer to; the prefix is attended whole).  The prefix's K and V are read from
  * HBM once for all sequences, and, where that is worth a kernel of its own, worked on
- * once for all: many query rows then meet each key.  Scores keep the exactness that
- * bsattn_decode describes, except those of int8 prefixes of 4096 keys and more and of
- * caller-made scales that are not powers of two: there a key's scale is rounded to
- * 11 bits, and its product with each code once more.
+ * once for all: many query rows then meet each key.  There, value scales that are not
+ * powers of two (int8) cost two more roundings to 11 bits per element of V.
  *
  * prefix_table device int32 [ceil(prefix_len / page_size)]: the prefix's pages.
  * prefix_len   >= 0 (0: bsattn_decode).  table_cols may be 0: no sequence has keys of

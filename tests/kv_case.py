@@ -79,9 +79,8 @@ def expect(pool, q, G, parts, scale, coarse=0.0):
     sums' own rounding) relatively, by its rounding to fp16, 2^-11 of it, and absolutely
     by 2^-32 of the largest weight times its value where it is too small for fp16.
 
-    coarse: relative error of every element of K and V that the call may make (prefixes
-    whose scales are rounded with the codes: 2 * 2^-11); a score is then off by coarse *
-    scale * |q| . |k| more, and a value by coarse of it."""
+    coarse: relative error of every element of V that the call may make (long prefixes
+    whose value scales are rounded with the codes: 2 * 2^-11)."""
     B, Hq, D = q.shape
     out, lse = np.zeros((B, Hq, D)), np.full((B, Hq), -math.inf)
     to, tl = np.zeros((B, Hq, D)), np.zeros((B, Hq))
@@ -94,7 +93,7 @@ def expect(pool, q, G, parts, scale, coarse=0.0):
                 o, l, spread = okv.attend(x, k, v, scale)
                 out[b, h * G + g], lse[b, h * G + g] = o, l
                 if len(k):
-                    ds = ((D + 8) * 2.0 ** -24 + coarse) * scale * float(np.max(np.abs(k) @ np.abs(x)))
+                    ds = (D + 8) * 2.0 ** -24 * scale * float(np.max(np.abs(k) @ np.abs(x)))
                     to[b, h * G + g] = spread * (2.0 ** -11 + 2 * ds + coarse + 2.0 ** -20) + len(k) * 2.0 ** -32 * np.max(np.abs(v))
                     tl[b, h * G + g] = ds + 2.0 ** -20 + abs(l) * 2.0 ** -22
     return out, lse, to, tl

@@ -150,12 +150,10 @@ def test_shared_prefix_long(dtype, H, G, D, page, prefix, lens):
     out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), err_flag=err,
                                         out_dtype=torch.float32)
     assert int(err) == 0
-    coarse = 2.0 ** -10 if dtype == "int8" and len(lens) * G > 16 else 0.0    # values always, scores from 4096 keys
-    ref = expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], range(lens[b]))], 1 / math.sqrt(D), coarse)
-    agree(out, lse, ref)
-    if prefix < 4096 or dtype == "e4m3":    # scores are exact there: the LSE is held to that
-        exact = expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], range(lens[b]))], 1 / math.sqrt(D))
-        assert np.all(np.abs(f64(lse) - exact[1]) <= exact[3])
+    # many rows: values whose scales are not powers of two carry two roundings to 11 bits more
+    coarse = 2.0 ** -10 if dtype == "int8" and len(lens) * G > 16 else 0.0
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], range(lens[b]))],
+                           1 / math.sqrt(D), coarse))
     again = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), out_dtype=torch.float32)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 

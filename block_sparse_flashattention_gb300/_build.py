@@ -1,16 +1,20 @@
-"""Compiles the CUDA sources into libbsattn.so (sm_103a) next to this file."""
+"""Compiles the CUDA sources into libbsattn.so (sm_103a) next to this file, and, beside
+it, the native form of the cache calls over torch tensors (_torch_calls.so)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsattn.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
@@ -38,9 +42,38 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def build_calls(force: bool = False) -> bool:
+    """Compiles csrc/torch_calls.cpp against the installed torch.  It only spares host time
+    (kv_cache.py marshals the same calls through ctypes without it), so that a machine
+    where it does not compile goes without: the reason is printed, False returned."""
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    inputs = [src, os.path.join(INCLUDE, "bsattn.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(f) <= os.path.getmtime(CALLS) for f in inputs):
+        return True
+    try:
+        import torch
+    except ImportError:
+        return False
+    root = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)))
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.sep in _nvcc() else "/usr/local/cuda"
+    tmp = f"{CALLS}.tmp.{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", tmp, "-I" + INCLUDE,
+           "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-L" + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"{src} was not compiled, the cache calls go through ctypes:\n{r.stderr}", file=sys.stderr)
+        return False
+    os.replace(tmp, CALLS)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (in parallel, one translation unit per process) and link."""
     if not force and up_to_date():
+        build_calls()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     nvcc = _nvcc()
@@ -56,8 +89,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(sources())) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
+        calls = ex.submit(build_calls, force)
         objs = list(ex.map(compile_one, sources()))
+        calls.result()
     tmp = f"{LIB}.tmp.{pid}"
     cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -30,11 +30,11 @@ def _check(status: int, where: str) -> None:
 
 
 # Bound by the first KVCache, so that importing the package does not import torch.
-torch = BF16 = F32 = I32 = _lib = _raw_stream = _current_device = None
+torch = BF16 = F32 = I32 = _lib = _raw_stream = _current_device = _calls = None
 
 
 def _bind() -> None:
-    global torch, BF16, F32, I32, _lib, _raw_stream, _current_device
+    global torch, BF16, F32, I32, _lib, _raw_stream, _current_device, _calls
     import torch as t
     BF16, F32, I32 = t.bfloat16, t.float32, t.int32
     # The current stream's handle: the raw form saves the stream object that the public
@@ -42,6 +42,16 @@ def _bind() -> None:
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
     _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     _lib = library()
+    # The ordinary calls in native code (csrc/torch_calls.cpp), where it was compiled for
+    # this torch: 9 us of host time for a decode call, against 17 here.
+    try:
+        from . import _torch_calls as calls
+        if calls.torch_version() == t.__version__.split("+")[0]:
+            calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                _lib.bsattn_kv_append, _lib.bsattn_kv_read, _lib.bsattn_decode, _lib.bsattn_decode_shared_prefix)))
+            _calls = calls
+    except ImportError:
+        pass
     torch = t
 
 
@@ -52,7 +62,7 @@ class KVCache:
     k_scale, v_scale: float32 [num_pages, H, page_size]; contiguous, one device."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "H", "page_size", "D", "dtype", "device", "index", "c", "ref",
-                 "scale")
+                 "scale", "at")
 
     def __init__(self, k, v, k_scale, v_scale):
         if torch is None:
@@ -75,7 +85,7 @@ class KVCache:
         self.c = bsattn_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                  self.num_pages, self.page_size, self.H, self.D,
                                  KV_INT8 if k.dtype == torch.int8 else KV_E4M3)
-        self.ref = ctypes.pointer(self.c)
+        self.ref, self.at = ctypes.pointer(self.c), ctypes.addressof(self.c)
 
 
 def alloc_kv_cache(num_pages: int, H: int, D: int, *, page_size: int = 128, dtype=None, device="cuda") -> KVCache:
@@ -155,6 +165,12 @@ def kv_append(k, v, cache: KVCache, page_table, seqlens, *, cu_seqlens=None, err
     cu_seqlens None: one new token per sequence; else int32 [B+1], the rows of each
     sequence's new tokens.  seqlens int32 [B]: the lengths after the append (0: a
     padding row); page_table int32 [B, pages]."""
+    if _calls is not None and stream is None and err_flag is None:
+        status = _calls.kv_append(cache.at, cache.index, k, v, page_table, seqlens, cu_seqlens)
+        if status is not None:
+            if status:
+                raise BsattnError(status, "bsattn_kv_append")
+            return cache
     if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
         return _elsewhere(cache, stream, lambda: kv_append(k, v, cache, page_table, seqlens, cu_seqlens=cu_seqlens,
                                                            err_flag=err_flag))
@@ -187,6 +203,12 @@ def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=Non
 
     total: rows to allocate when k and v are not given (cu_seqlens[-1], which lives on
     the device); rows outside every sequence are not written."""
+    if _calls is not None and stream is None and err_flag is None and k is None and v is None:
+        got = _calls.kv_read(cache.at, cache.index, page_table, cu_seqlens, total)
+        if got is not None:
+            if got.__class__ is tuple:
+                return got
+            raise BsattnError(got, "bsattn_kv_read")
     if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
         return _elsewhere(cache, stream, lambda: kv_read(cache, page_table, cu_seqlens, total=total, k=k, v=v,
                                                          err_flag=err_flag))
@@ -333,6 +355,14 @@ def decode(q, cache: KVCache, page_table, seqlens, *, meta=None, kv_valid_len=No
     B); kv_valid_len int32 [B, meta.num_n] as for ``forward``.  Returns (out [B, Hq, D]
     bf16 or out_dtype, lse fp32 [B, Hq]); a sequence without keys gets 0 and -inf.
     workspace: see alloc_decode_workspace; None allocates one for this call."""
+    if _calls is not None and workspace is not None and stream is None and out is None and lse is None and \
+            out_dtype is None and err_flag is None and kv_valid_len is None:
+        got = _calls.decode(cache.at, cache.index, q, page_table, seqlens,
+                            cache.scale if softmax_scale is None else softmax_scale, workspace, meta, None, 0)
+        if got is not None:
+            if got.__class__ is tuple:
+                return got
+            raise BsattnError(got, "bsattn_decode")
     return _decode(q, cache, None, 0, page_table, seqlens, meta, kv_valid_len, softmax_scale, out, out_dtype, lse,
                    workspace, err_flag, stream)
 
@@ -346,5 +376,13 @@ def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_
     be None when no sequence has keys of its own.  The prefix is read once for all."""
     if prefix_table is None:
         raise ValueError("prefix_table is needed (decode attends sequences without a prefix)")
+    if _calls is not None and workspace is not None and stream is None and out is None and lse is None and \
+            out_dtype is None and err_flag is None and kv_valid_len is None:
+        got = _calls.decode(cache.at, cache.index, q, page_table, seqlens,
+                            cache.scale if softmax_scale is None else softmax_scale, workspace, meta, prefix_table, prefix_len)
+        if got is not None:
+            if got.__class__ is tuple:
+                return got
+            raise BsattnError(got, "bsattn_decode_shared_prefix")
     return _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
                    out_dtype, lse, workspace, err_flag, stream)

@@ -484,3 +484,53 @@ def test_a_serving_run(dtype):
     kmax = float(kr.float().abs().max()) * float(q.float().abs().sum(-1).max())
     tol = 2 * ((D + 8) * 2.0 ** -24 * scale * kmax + 2.0 ** -20 + float(lse[0].abs().max()) * 2.0 ** -22)
     assert (dl[0] - lse[0]).abs().max() <= tol
+
+
+@pytest.mark.parametrize("listed", [False, True])
+def test_native_calls_equal_the_marshalled_ones(monkeypatch, listed):
+    """The native form of the calls and the ctypes form give the same bits, and refuse the same arguments."""
+    from block_sparse_flashattention_gb300 import kv_cache
+    H, G, D, page, lens, prefix = 2, 4, 128, 64, [500, 0, 77], 130
+    pool = Pool(90, pages_for(lens + [prefix], page), H, D, page, "e4m3")
+    if kv_cache._calls is None:
+        pytest.skip("torch_calls.cpp was not compiled for this torch")
+    hp = pool.take(-(-prefix // page))
+    _, table = pool.tables(lens)
+    n, q = _i32(lens), _q(91, 3, H * G, D)
+    k, v = _q(92, 3, H, D), _q(93, 3, H, D)
+    meta = lists(H, lens, lambda b, h: [0], mask_every=2) if listed else None
+    ws = bsa.alloc_decode_workspace(pool.cache, 3, H * G, prefix_len=prefix)
+    cu = _i32([0, 500, 500, 577])
+
+    def run():
+        c = bsa.KVCache(*(t.clone() for t in (pool.cache.k, pool.cache.v, pool.cache.k_scale, pool.cache.v_scale)))
+        bsa.kv_append(k, v, c, table, n)
+        return [*(t.view(torch.uint8) for t in (c.k, c.v, c.k_scale, c.v_scale)),
+                *bsa.kv_read(c, table, cu, total=577), *bsa.decode(q, c, table, n, meta=meta, workspace=ws),
+                *bsa.decode_shared_prefix(q, c, _i32(hp), prefix, table, n, meta=meta, workspace=ws, softmax_scale=0.3)]
+    bad = [lambda: bsa.kv_append(k.float(), v, pool.cache, table, n), lambda: bsa.kv_append(k, v[:2], pool.cache, table, n),
+           lambda: bsa.kv_append(k, v, pool.cache, table.long(), n), lambda: bsa.kv_append(k, v, pool.cache, table, n[:2]),
+           lambda: bsa.kv_append(k, v, pool.cache, table, n, cu_seqlens=n), lambda: bsa.kv_read(pool.cache, table, cu[:3], total=577),
+           lambda: bsa.kv_read(pool.cache, table, cu), lambda: bsa.decode(q.float(), pool.cache, table, n, workspace=ws),
+           lambda: bsa.decode(q, pool.cache, table[:2], n, workspace=ws), lambda: bsa.decode(q, pool.cache, table, n.cpu(), workspace=ws),
+           lambda: bsa.decode(q, pool.cache, table, n, workspace=ws.cpu()), lambda: bsa.decode(q, pool.cache, None, n, workspace=ws),
+           lambda: bsa.decode_shared_prefix(q, pool.cache, _i32(hp), 9999, table, n, workspace=ws)]
+    status = [lambda: bsa.decode(q[:, :5], pool.cache, table, n, workspace=ws),
+              lambda: bsa.decode(q, pool.cache, table, n, workspace=ws, softmax_scale=-1.0),
+              lambda: bsa.decode(q, pool.cache, table, n, workspace=ws[:256])]
+    got = run()
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in status:
+        with pytest.raises(bsa.BsattnError):
+            call()
+    monkeypatch.setattr(kv_cache, "_calls", None)
+    for a, b in zip(got, run()):
+        assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in status:
+        with pytest.raises(bsa.BsattnError):
+            call()

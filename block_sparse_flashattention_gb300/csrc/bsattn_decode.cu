@@ -463,8 +463,9 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     if (w.mode != kOwnKernel) grid_dependency_wait();
 
     // Where each worker's piece of the line begins.  Each thread sums the cost of a run
-    // of sequences (or, with lists, of (sequence, head) pairs); CTA c also writes the
-    // records of every gridDim-th of them: the workers its segments' parts lie with.
+    // of sequences (or, with lists, of (sequence, head) pairs); CTA c also checks every
+    // gridDim-th of them and writes the records of those without keys.  The record of any
+    // other segment, the workers its parts lie with, is written by the first of these.
     const int g_pre = w.sp ? (p.prefix_len + 15) / 16 : 0, lead = w.mode == kEach ? (p.prefix_len + 15) / 16 : 0;
     const long long line_pre = (long long)w.sp * (g_pre + kSegCost);
     const int units = p.has_lists ? p.B * p.c.H : p.B, per = (units + kThreads - 1) / kThreads;
@@ -501,7 +502,11 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
         piece_at[tid] = cuts ? total * worker / cuts : 0;
     }
     __syncthreads();
-    auto owner = [&](long long place) -> int { return (int)(((place + 1) * cuts - 1) / total); };
+    auto owner = [&](long long place) -> int {
+        const unsigned long long a = (unsigned long long)(place + 1) * (unsigned long long)cuts - 1u;
+        if (a <= 0xffffffffu) return (int)((unsigned)a / (unsigned)total);   // 64-bit division costs 10 times as much
+        return (int)(a / (unsigned long long)total);
+    };
     auto begins_at = [&](long long begin, long long len, int seg, long long seg_len) {
         // workers of this CTA whose pieces begin within [begin, begin + len): segments seg, seg + 1, ... of seg_len
         if (piece_at[kW] <= begin || piece_at[0] >= begin + len) return;
@@ -514,19 +519,12 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     };
     int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
     if (w.sp && tid == 0) begins_at(0, line_pre, 0, g_pre + kSegCost);
-    for (int x = (int)blockIdx.x * kThreads + tid; x < w.sp; x += (int)gridDim.x * kThreads) {
-        const long long a = (long long)x * (g_pre + kSegCost) + kSegCost;
-        rec[x] = make_int2(owner(a), owner(a + g_pre - 1));
-    }
     for (int x = u0; x < u1; ++x) {
         const int n = unit_groups(x, false);
         const long long len = n ? (long long)(n + kSegCost) * reps : 0;
         if (len) begins_at(at, len, w.sp + x * reps, n + kSegCost);
-        if (x % (int)gridDim.x == (int)blockIdx.x)
-            for (int r = 0; r < reps; ++r) {
-                const long long a = at + (long long)r * (n + kSegCost) + kSegCost;
-                rec[w.sp + x * reps + r] = n ? make_int2(owner(a), owner(a + n - 1)) : make_int2(0, -1);
-            }
+        else if (x % (int)gridDim.x == (int)blockIdx.x)
+            for (int r = 0; r < reps; ++r) rec[w.sp + x * reps + r] = make_int2(0, -1);
         at += len;
     }
     __syncthreads();
@@ -550,6 +548,7 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
             const long long first = begin + kSegCost;
             const int t0 = (int)max(0ll, min((long long)g, lo - first)), t1 = (int)max(0ll, min((long long)g, hi - first));
             if (t0 < t1) {
+                if (t0 == 0 && lane == 0) rec[seg] = make_int2((int)worker, t1 == g ? (int)worker : owner(first + g - 1));
                 k.groups(s, lead, n, lr, t0, t1);
                 k.finish(w, s, seg, (int)worker, t0 == 0 && t1 == g);
             }

@@ -451,7 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no CTA's piece is empty while a later one's is not: a segment's parts are consecutive
     const long long cuts = min((long long)gridDim.x, total), cta = blockIdx.x;
     const long long lo = cta < cuts ? total * cta / cuts : 0, hi = cta < cuts ? total * (cta + 1) / cuts : 0;
-    auto owner = [&](long long tile) -> int { return (int)(((tile + 1) * cuts - 1) / total); };
+    auto owner = [&](long long tile) -> int {
+        const unsigned long long a = (unsigned long long)(tile + 1) * (unsigned long long)cuts - 1u;
+        if (a <= 0xffffffffu) return (int)((unsigned)a / (unsigned)total);   // 64-bit division costs 10 times as much
+        return (int)(a / (unsigned long long)total);
+    };
     int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
     for (int x = u0; x < u1; ++x) {
         const bool mine = x % (int)gridDim.x == (int)blockIdx.x;

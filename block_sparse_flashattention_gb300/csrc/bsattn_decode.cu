@@ -562,10 +562,10 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
 
 // Joins the parts of one output row: out = sum_i o_i 2^(L_i - L), L = log2 sum_i 2^L_i.
 // One block per row, its warps share the parts; a row that the first kernel finished is
-// left alone.
-constexpr int kJoinWarps = 4;
-
-template <int D>
+// left alone.  Few rows have many parts each: blocks have 16 warps while four such blocks
+// per SM hold all rows, else 4 (us a call, 16 : 4 warps: 32 rows of 131072 keys 177 : 179.5,
+// 512 rows behind a prefix of 8192 keys 28.6 : 29.7; 2048 rows of 100 .. 4096 keys 64 : 56).
+template <int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) bsattn_decode_join_kernel(const __grid_constant__ DecodeParams p,
                                                                             const __grid_constant__ Plan w) {
     grid_launch_dependents();
@@ -728,8 +728,12 @@ cudaError_t launch_d(const DecodeParams &p, const Plan &w, int sms, cudaStream_t
     cfg.numAttrs = 1;
     cfg.stream = stream;
     cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hq));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D>, p, w);
+    if ((long long)p.B * p.Hq <= 4ll * sms) {
+        cfg.blockDim = dim3(16 * 32);
+        return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D, 16>, p, w);
+    }
+    cfg.blockDim = dim3(4 * 32);
+    return cudaLaunchKernelEx(&cfg, bsattn_decode_join_kernel<D, 4>, p, w);
 }
 
 }  // namespace

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) bsattn_decode_join_kernel(con
     } else if (w.mode == kOwnKernel) {
         const int blk = r / kBlockRows, sp = h * w.row_blocks + blk;
         const int nt = (p.prefix_len + kTile - 1) / kTile;
-        const int c0 = w.pre_owner((long long)sp * nt, nt), c1 = w.pre_owner((long long)(sp + 1) * nt - 1, nt);
+        const int c0 = w.pre_owner(sp, 0, nt), c1 = w.pre_owner(sp, nt - 1, nt);
         np = c1 - c0 + 1;
         pre_row = (long long)(sp + c0) * w.rows_p + (r - blk * kBlockRows);
         if (p.B * p.G - blk * kBlockRows <= kTile) {  // both slots hold parts of the row

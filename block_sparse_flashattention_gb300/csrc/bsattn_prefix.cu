@@ -25,9 +25,11 @@
 // Roles (640 threads, one CTA per SM, all of TMEM):
 //   warp 0        issues the MMAs: S_t = Q_t K'^T into TMEM, O_t += P_t V' with P in TMEM
 //   warp 1        owns the TMEM allocation
+//   warps 2, 3    fetch the codes of keys, of values: bulk copies into a raw tile each, on
+//                 their way from when the tile before has been read
 //   warps 4-7, 8-11   slot 0, slot 1: load the query rows, softmax, O rescale, part
-//   warps 12-15   load codes and scales of keys (the next tile's wait in registers) and
-//                 widen them into the K stages (128-byte swizzle)
+//   warps 12-15   widen the codes of keys from the raw tile into the K stages (128-byte
+//                 swizzle); the scales of the next tile wait in registers
 //   warps 16-19   the same for values, as they lie (MN-major)
 // TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P_t over S_t.
 #include "bsattn_internal.h"
@@ -67,15 +69,18 @@ template <int D>
 struct Cfg {
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + 2 * kTileBytes;
-    static constexpr uint32_t kScale = kV + 2 * kTileBytes;          // kMsgs x 128 rests r of key scales
+    static constexpr uint32_t kRaw = kV + 2 * kTileBytes;            // codes of a key and of a value tile
+    static constexpr uint32_t kRawBytes = kTile * D;
+    static constexpr uint32_t kScale = kRaw + 2 * kRawBytes;         // kMsgs x 128 rests r of key scales
     static constexpr uint32_t kMsg = kScale + kMsgs * 512u;
     static constexpr uint32_t kBar = kMsg + kMsgs * (uint32_t)sizeof(KeyMsg);
-    // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete
+    // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete;
+    // raw K / V tile full and empty
     static constexpr int bKF = 0, bKE = 2, bVF = 4, bVE = 6, bQF = 8, bSR = 10, bPR = 12, bOD = 16, bDrain = 18,
-                         kNumBars = 19;
+                         bRF = 19, bRE = 21, kNumBars = 23;
     static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
     static constexpr uint32_t kBytes = kMisc + 16;
-    static constexpr uint32_t kAlloc = kBytes + 1024;                // slack for 1024-byte alignment
+    static constexpr uint32_t kAlloc = kBytes;
     static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
@@ -86,7 +91,7 @@ struct Walk {
     int seg, off, n;  // segment, its first tile here, tiles here
     __device__ __forceinline__ bool next() {
         if (pos >= end) return false;
-        seg = (int)(pos / nt);
+        seg = (int)line_div(pos, nt);
         off = (int)(pos - (long long)seg * nt);
         n = (int)min((long long)(nt - off), end - pos);
         pos += n;
@@ -121,37 +126,42 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
         const bool split = rows <= kTile;
         const int row = split ? r : t * kTile + r;   // of the segment
         const bool row_ok = row < rows;
-        // ---- the query row: fp16 of q 2^-e into the slot's tile (K-major, swizzled)
-        float c;
+        // ---- the warp's query rows: fp16 of q 2^-e into the slot's tile (K-major, swizzled).
+        // D / 8 lanes load a row together, eight steps' loads at a time.
+        float c = 0.f;
         {
-            uint32_t x[D / 2];
+            constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kSteps = 32 / kRows;
+            const int piece = (int)lane % kRowLanes, sub = (int)lane / kRowLanes;
             const int m = row0 + row, b = row_ok ? m / p.G : 0;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + (long long)b * p.q_stride + (long long)(h * p.G + (row_ok ? m - b * p.G : 0)) * D);
-            uint32_t a = 0;
+            const long long mine = row_ok ? (long long)b * p.q_stride + (long long)(h * p.G + m - b * p.G) * D : -1;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kSteps; i0 += 8) {
+                uint4 x[8];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 y = row_ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                x[4 * i] = y.x;
-                x[4 * i + 1] = y.y;
-                x[4 * i + 2] = y.z;
-                x[4 * i + 3] = y.w;
-            }
+                for (int i = 0; i < 8; ++i) {
+                    const long long at = __shfl_sync(0xffffffffu, mine, (i0 + i) * kRows + sub);
+                    x[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.q + at) + piece) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-            for (int i = 0; i < D / 2; ++i) a = __vmaxu2(a, x[i] & 0x7fff7fffu);
-            a = max(a & 0xffffu, a >> 16);
-            float f;
-            row_scale(a, p.scale_log2, f, c);
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, a = 0;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                uint32_t y[4];
+                    for (int k = 0; k < 4; ++k) a = __vmaxu2(a, y[k] & 0x7fff7fffu);
+                    a = max(a & 0xffffu, a >> 16);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    y[k] = pack_f16x2(__uint_as_float(x[4 * i + k] << 16) * f,
-                                      __uint_as_float(x[4 * i + k] & 0xffff0000u) * f);
-                const uint32_t at = C::kQ + (uint32_t)t * C::kTileBytes + (uint32_t)(i >> 3) * kSub +
-                                    (uint32_t)r * 128u + (uint32_t)(((i & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4 *>(smem + at) = make_uint4(y[0], y[1], y[2], y[3]);
+                    for (int d = 1; d < kRowLanes; d <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+                    float f, back;
+                    row_scale(a, p.scale_log2, f, back);
+                    back = __shfl_sync(0xffffffffu, back, ((int)lane % kRows) * kRowLanes);
+                    if ((int)lane / kRows == i0 + i) c = back;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = pack_f16x2(__uint_as_float(y[k] << 16) * f, __uint_as_float(y[k] & 0xffff0000u) * f);
+                    const uint32_t rr = quarter * 32u + (uint32_t)((i0 + i) * kRows + sub);
+                    const uint32_t at = C::kQ + (uint32_t)t * C::kTileBytes + (uint32_t)(piece >> 3) * kSub + rr * 128u +
+                                        ((((uint32_t)piece & 7u) ^ (rr & 7u)) << 4);
+                    *reinterpret_cast<uint4 *>(smem + at) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
             }
         }
         fence_proxy_async_smem();
@@ -361,66 +371,80 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
     }
 }
 
+// Fetches the codes of K or V tiles, one warp each: a copy per 16 keys (no page is smaller),
+// none for keys past the prefix or on a page that is none.
+template <int D>
+__device__ __forceinline__ void fetch_role(const DecodeParams &p, const Plan &w, Walk walk, bool values, int lane,
+                                           uint32_t base, volatile int *abort) {
+    using C = Cfg<D>;
+    const uint32_t full = base + C::kBar + 8u * (uint32_t)(C::bRF + (values ? 1 : 0));
+    const uint32_t empty = base + C::kBar + 8u * (uint32_t)(C::bRE + (values ? 1 : 0));
+    const uint32_t raw = base + C::kRaw + (values ? C::kRawBytes : 0u);
+    const uint8_t *codes = values ? p.c.v : p.c.k;
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next()) {
+        const int h = walk.seg / w.row_blocks;
+        for (int k = 0; k < walk.n; ++k, ++it) {
+            const int key = (walk.off + k) * kTile + 16 * lane;
+            long long row = -1;
+            if (lane < 8 && key < p.prefix_len) {
+                const int page = __ldg(p.prefix_table + (key >> p.c.page_shift));
+                if (page >= 0 && page < p.c.num_pages)
+                    row = (((long long)page * p.c.H + h) << p.c.page_shift) + (key & ((1 << p.c.page_shift) - 1));
+                else
+                    raise(p, BSATTN_FLAG_BAD_INDEX);
+            }
+            const uint32_t on = __ballot_sync(0xffffffffu, row >= 0);
+            ok = __all_sync(0xffffffffu, mbar_wait(empty, (it & 1u) ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT));
+            if (!ok) break;
+            mbar_arrive_expect_tx_lead(lane == 0 ? 1u : 0u, full, (uint32_t)__popc(on) * 16u * D);
+            __syncwarp();
+            bulk_g2s_lead(row >= 0 ? 1u : 0u, raw + (uint32_t)lane * 16u * D, codes + row * D, 16u * D, full);
+        }
+    }
+    // nothing may be on its way into the tile when the CTA ends
+    if (it > 0) mbar_wait_drain(full, (it - 1u) & 1u);
+}
+
 // Widens the codes of K tiles (four warps, 32 keys each) or V tiles (four more); one code
 // for both, so that the warps share the instruction caches.
 //
-// Lane: 8 codes of a row (16 bytes of fp16, one swizzle piece), D / 8 lanes to a row; a
-// tile's codes are loaded while the tile before it is widened.
+// Lane: 16 codes of a row (two swizzle pieces of fp16), D / 16 lanes to a row.  A tile's
+// scales are loaded while the tile before it is widened.  The codes come through a raw tile:
+// loaded into registers instead, the lines on their way filled the load unit, and every
+// softmax warp stood still for some 1000 cycles a tile.
 template <int D, bool kInt8>
 __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w, Walk walk, bool values, int warp,
                                            int lane, uint32_t base, uint8_t *smem, volatile int *abort) {
     using C = Cfg<D>;
-    // row of a load instruction: 8 lanes with 8 codes each; a row of 128 codes takes two
-    constexpr int kSpans = D / 64, kSteps = 32 / 4;
+    constexpr int kRowLanes = D / 16, kRows = 32 / kRowLanes, kSteps = 32 / kRows;   // rows of a step, steps
     auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
-    const int piece = lane & 7, sub_row = lane >> 3;
+    const int col = lane % kRowLanes, sub_row = lane / kRowLanes;
     const int ps_shift = p.c.page_shift, n_keys = p.prefix_len;
-    const uint8_t *codes = values ? p.c.v : p.c.k;
     const float *scales = values ? p.c.vs : p.c.ks;
     // Cache row of this lane's keys 4 lane .. 4 lane + 3 of a tile (one page), or -1.
     auto look_up = [&](int tile, int h) -> int {
         const int key = tile * kTile + 4 * lane;
         if (key >= n_keys) return -1;
         const int page = __ldg(p.prefix_table + (key >> ps_shift));
-        if (page < 0 || page >= p.c.num_pages) {
-            if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
-            return -1;
-        }
+        if (page < 0 || page >= p.c.num_pages) return -1;
         return ((page * p.c.H + h) << ps_shift) + (key & ((1 << ps_shift) - 1));
     };
     // What is loaded of a tile one tile ahead.
-    int run0, run1, n;  // cache rows of the warp's keys 0 .. 15 and 16 .. 31 (or -1), keys of the tile
+    int n;              // keys of the tile
+    uint32_t keep;      // those of the warp's 32 keys that count
     float scale;        // of the warp's key `lane`
     uint4 ks4, vs4;     // scales of the tile's keys 4 lane ..
-    uint2 raw[kSteps][kSpans];
     auto load = [&](int row4, int tile) {
-        run0 = __shfl_sync(0xffffffffu, row4, warp * 8);
-        run1 = __shfl_sync(0xffffffffu, row4, warp * 8 + 4);
         n = min(kTile, n_keys - tile * kTile);
-        const int row = lane < 16 ? run0 : run1;
-        scale = row >= 0 && warp * 32 + lane < n ? __ldg(scales + (long long)row + (lane & 15)) : 0.f;
+        const int row = __shfl_sync(0xffffffffu, row4, warp * 8 + (lane >> 2));
+        const bool on = row >= 0 && warp * 32 + lane < n;
+        keep = __ballot_sync(0xffffffffu, on);
+        scale = on ? __ldg(scales + (long long)row + (lane & 3)) : 0.f;
         const bool on4 = row4 >= 0;
         ks4 = on4 && !values ? __ldg(reinterpret_cast<const uint4 *>(p.c.ks + row4)) : make_uint4(0, 0, 0, 0);
         vs4 = on4 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
-        const uint8_t *a0 = codes + ((long long)run0 + sub_row) * D + piece * 8;
-        const uint8_t *a1 = codes + ((long long)run1 + sub_row) * D + piece * 8;
-        if (run0 >= 0 && run1 >= 0 && warp * 32 + 32 <= n) {
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-                for (int x = 0; x < kSpans; ++x)
-                    raw[i][x] = __ldg(reinterpret_cast<const uint2 *>((i < 4 ? a0 : a1) + (i & 3) * 4 * D + x * 64));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const bool on = (i < 4 ? run0 : run1) >= 0 && warp * 32 + i * 4 + sub_row < n;
-#pragma unroll
-                for (int x = 0; x < kSpans; ++x) {
-                    raw[i][x] = make_uint2(0, 0);
-                    if (on) raw[i][x] = __ldg(reinterpret_cast<const uint2 *>((i < 4 ? a0 : a1) + (i & 3) * 4 * D + x * 64));
-                }
-            }
-        }
     };
     // Largest binary exponent (biased, at least 1) of a tile's scales; NaN and infinity do not count.
     auto largest_exp = [&](uint4 x) -> int {
@@ -431,8 +455,8 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             if (v[i] < 0x7f800000u && 4 * lane + i < n) top = max(top, v[i]);
         return (int)(__reduce_max_sync(0xffffffffu, top) >> 23);
     };
-    // `ahead` walks two tiles in front: its tile's page is being looked up while the tile
-    // before it is loaded and the one before that is widened.
+    // `ahead` walks two tiles in front: its tile's page is being looked up while the scales of
+    // the tile before it are loaded and the one before that is widened.
     Walk ahead = walk;
     int ak = 0;
     bool more2 = ahead.next();
@@ -448,6 +472,12 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     step();
     bool more1 = more2;
     int tile1 = ahead.off + ak, row4 = look_ahead();
+    const uint8_t *raw = smem + C::kRaw + (values ? C::kRawBytes : 0u) + (warp * 32 + sub_row) * D + col * 16;
+    // Eight lanes store 128 bytes at a time; where they share a row, half of them begin with
+    // their second piece: every bank once.
+    const bool swap = D == 128 && col >= 4;
+    const int first = 2 * (col & 3) + (swap ? 1 : 0), second = first ^ 1;
+    const uint32_t dst = (values ? C::kV : C::kK) + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 32 + sub_row) * 128u;
     uint32_t it = 0;
     while (walk.next()) {
         int exp_run = 1;            // E starts anew with a segment's sums
@@ -462,26 +492,33 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             const float f32 = (values ? scale : __uint_as_float(bits & 0x7f800000u)) *
                               __uint_as_float((uint32_t)min(254, 260 - exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
-            const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(empty + (int)st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
+            const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF, v = values ? 1 : 0;
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(bar(empty + (int)st), ph ^ 1u, abort, p.err, BSATTN_FLAG_TIMEOUT) &&
+                                mbar_wait(bar(C::bRF + v), it & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT)))
                 return;
-            uint8_t *tile = smem + (values ? C::kV : C::kK) + st * C::kTileBytes + (warp * 32 + sub_row) * 128;
-            const uint32_t swz[2] = {(uint32_t)((piece ^ sub_row) << 4), (uint32_t)((piece ^ (sub_row + 4)) << 4)};
+            uint8_t *tile = smem + dst + st * C::kTileBytes;
+            const bool whole = keep == 0xffffffffu;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const uint32_t f = __shfl_sync(0xffffffffu, factor, i * 4 + sub_row);
+                uint4 x = *reinterpret_cast<const uint4 *>(raw + i * kRows * D);
+                // what lies in the tile where no key was copied is of an earlier one
+                if (!whole && !((keep >> (i * kRows + sub_row)) & 1u)) x = make_uint4(0, 0, 0, 0);
+                const uint32_t f = __shfl_sync(0xffffffffu, factor, i * kRows + sub_row);
+                const uint32_t y[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
+                const int r7 = (i * kRows + sub_row) & 7;
 #pragma unroll
-                for (int x = 0; x < kSpans; ++x) {
+                for (int j = 0; j < 2; ++j) {
                     uint32_t o[4];
-                    codes_to_f16x2<kInt8>(raw[i][x].x, o[0], o[1]);
-                    codes_to_f16x2<kInt8>(raw[i][x].y, o[2], o[3]);
+                    codes_to_f16x2<kInt8>(y[2 * j], o[0], o[1]);
+                    codes_to_f16x2<kInt8>(y[2 * j + 1], o[2], o[3]);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[q]) : "r"(f));
-                    *reinterpret_cast<uint4 *>(tile + x * kSub + i * 512 + swz[i & 1]) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(tile + i * kRows * 128 + (((j ? second : first) ^ r7) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             if (!values) {
-                const uint32_t keep = __ballot_sync(0xffffffffu, (lane < 16 ? run0 : run1) >= 0 && warp * 32 + lane < n);
                 reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] =
                     __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
                 const bool rest = __any_sync(0xffffffffu, (bits & 0x7fffffu) != 0u);
@@ -497,7 +534,10 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(full + (int)st));
+            if (lane == 0) {
+                mbar_arrive(bar(full + (int)st));
+                mbar_arrive(bar(C::bRE + v));
+            }
             if (more1) load(row4, tile1);
             row4 = row4_2;
             more1 = more2;
@@ -510,10 +550,12 @@ template <int D, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
     bsattn_prefix_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Plan w) {
     using C = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {  // the swizzle counts from 1024-byte boundaries
+        if (threadIdx.x == 0) raise(p, BSATTN_FLAG_TIMEOUT);
+        return;
+    }
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(misc + 1);
     auto bar = [&](int i) -> uint32_t { return base + C::kBar + 8u * (uint32_t)i; };
@@ -531,10 +573,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(C::bOD + s), 1);
         }
         mbar_init(bar(C::bDrain), 1);
+        for (int v = 0; v < 2; ++v) {
+            mbar_init(bar(C::bRF + v), 1);       // the fetching warp's arrival and the bytes
+            mbar_init(bar(C::bRE + v), 4);       // one per widening warp
+        }
         misc[1] = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
+    Walk walk;
+    walk.nt = (p.prefix_len + kTile - 1) / kTile;
+    walk.pos = w.pre_first((int)blockIdx.x, walk.nt);
+    walk.end = w.pre_first((int)blockIdx.x + 1, walk.nt);
     if (warp == 1) {
         tmem_alloc(base + C::kMisc, kTmemCols);
         tmem_relinquish();
@@ -547,11 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // does not wait for what this grid writes, may start once that has completed.
     grid_dependency_wait();
     grid_launch_dependents();
-    Walk walk;
-    walk.nt = (p.prefix_len + kTile - 1) / kTile;
-    walk.pos = w.pre_first((int)blockIdx.x, walk.nt);
-    walk.end = w.pre_first((int)blockIdx.x + 1, walk.nt);
-
     if (warp == 0) {
         regs_release<kCtrlRegs>();
         // ---------------------------------------------------- MMA issuer --
@@ -652,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(bar(C::bDrain), 0);
     } else if (warp < 4) {
         regs_release<kCtrlRegs>();
+        if (warp >= 2) fetch_role<D>(p, w, walk, warp == 3, (int)lane, base, abort);
     } else if (warp < 12) {
         regs_claim<kSoftmaxRegs<kInt8>>();
         softmax_role<D, kInt8>(p, w, walk, tmem, warp >= 8 ? 1 : 0, warp, lane, base, smem, abort);

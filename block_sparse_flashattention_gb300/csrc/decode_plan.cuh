@@ -23,6 +23,17 @@ enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2, kEach = 3 };
 // 14.2 : 18.9, 41 MB 18.2 : 20.1, 68 MB 17.9 : 18.8, 135 MB 28.7 : 20.4, 270 MB 42 : 31.
 constexpr long long kEachBytes = 76ll << 20;
 
+// What the prefix kernel pays for a segment, in tiles: query rows, the first tiles' latency,
+// the part.  512 rows of 8 heads, 32768 keys: CTAs with tiles of two segments took 178000
+// cycles of 1.95 GHz, those with as many of one 157000.
+constexpr int kPreCost = 3;
+
+// Quotient of numbers that mostly fit 32 bits, where a division costs a tenth.
+__host__ __device__ inline long long line_div(long long a, long long b) {
+    if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+    return a / b;
+}
+
 // Segments: of the prefix, one per KV head (kInLine) or (KV head, block of 256 query
 // rows); of the sequences' own keys, (sequence, KV head).  A line of keys is cut over
 // workers (warps or CTAs), and part `segment + worker` holds what a worker computed of a
@@ -36,15 +47,21 @@ struct Plan {
     int rows_p;                            // rows a prefix part has room for
     int sp, ss;                            // prefix and own segments of the decode kernel's line
     int pre_cuts;                          // CTAs of the prefix kernel
+    int pre_cost;                          // tiles that a segment costs it besides its own
     size_t rec, pre_o, pre_l, suf_o, suf_l, total;  // byte offsets: records, parts, size
 
-    // First tile of CTA `cta`'s piece of the prefix kernel's line.
+    // The prefix kernel's line: of each segment pre_cost places, then its nt tiles.  First
+    // tile, counted over all segments, of CTA `cta`'s piece.
     __host__ __device__ long long pre_first(int cta, int nt) const {
-        return (long long)pre_segs * nt * cta / pre_cuts;
+        const long long place = line_div((long long)pre_segs * (nt + pre_cost) * cta, pre_cuts);
+        const long long seg = line_div(place, nt + pre_cost);
+        const long long off = place - seg * (nt + pre_cost) - pre_cost;
+        return seg * nt + (off > 0 ? off : 0);
     }
-    // The CTA whose piece holds tile `tile` of that line.
-    __host__ __device__ int pre_owner(long long tile, int nt) const {
-        return (int)(((tile + 1) * pre_cuts - 1) / ((long long)pre_segs * nt));
+    // The CTA whose piece holds tile `off` of segment `seg`.
+    __host__ __device__ int pre_owner(int seg, int off, int nt) const {
+        const long long place = (long long)seg * (nt + pre_cost) + pre_cost + off;
+        return (int)line_div((place + 1) * pre_cuts - 1, (long long)pre_segs * (nt + pre_cost));
     }
 };
 
@@ -65,6 +82,8 @@ inline Plan make_plan(int B, int H, int G, int D, int prefix_len, int sms) {
     const long long tiles = (long long)w.pre_segs * ((prefix_len + kTile - 1) / kTile);
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
     w.pre_cuts = (int)(tiles < most ? tiles : most);
+    // every piece keeps tiles of its own
+    w.pre_cost = w.pre_cuts > 0 && tiles / w.pre_cuts > 2 * kPreCost ? kPreCost : 0;
     const size_t workers = w.streaming ? kMaxCtas * kStreamWarps : kMaxCtas;
     const size_t np = w.mode == kOwnKernel ? (size_t)(w.pre_segs + kMaxCtas) * w.rows_p
                     : w.mode == kInLine    ? ((size_t)w.sp + workers) * w.rows_p : 0;

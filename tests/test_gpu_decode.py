@@ -188,6 +188,64 @@ def test_long_prefix_with_faults_and_odd_scales(B, G, dtype):
     agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix))], 1 / math.sqrt(D)))
 
 
+@pytest.mark.parametrize("dtype,D", [("e4m3", 64), ("int8", 128)])
+def test_long_prefix_many_tiles_per_block(dtype, D):
+    """Two blocks of query rows and two heads over 313 tiles: pieces of eight tiles and more, some of which hold
+    the end of one block's line and the beginning of the next."""
+    H, G, page, prefix, B = 2, 2, 128, 40000, 150
+    pool = Pool(126, pages_for([prefix], page), H, D, page, dtype)
+    hp = pool.take(-(-prefix // page))
+    q = _q(127, B, H * G, D)
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, None, _i32([0] * B), out_dtype=torch.float32)
+    some = [0, 63, 64, 127, 128, 149]
+    coarse = 2.0 ** -10 if dtype == "int8" else 0.0
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, range(prefix))], 1 / math.sqrt(D), coarse))
+
+
+@pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
+    ("e4m3", 8, 1, 128, 5, 8000),      # prefix in the streaming line
+    ("int8", 2, 2, 128, 20, 8000),     # in its own kernel
+    ("e4m3", 1, 20, 64, 9, 3000),      # the same, more query rows a head than a streaming warp holds
+])
+@pytest.mark.parametrize("kind", ["varlen", "batched"])
+def test_long_prefix_with_lists_and_fused_rows(dtype, H, G, D, B, prefix, kind):
+    page, lens = 64, [(137 * i) % 400 for i in range(B)]
+    pool = Pool(128, pages_for(lens + [prefix], page), H, D, page, dtype)
+    hp = pool.take(-(-prefix // page))
+    ht, table = pool.tables(lens)
+    q = _q(129, B, H * G + 3 * H, D)[:, 2 * H:2 * H + H * G]     # rows of a fused projection
+    sel = lambda b, h: [t for t in range(-(-lens[b] // 128)) if (t + b + h) % 3]  # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), err_flag=err,
+                                        meta=lists(H, lens, sel, kind=kind, mask_every=2), out_dtype=torch.float32)
+    assert int(err) == 0
+    keys = lambda b, h: [p for t in sel(b, h) for p in range(128 * t, min(lens[b], 128 * t + 128))]  # noqa: E731
+    coarse = 2.0 ** -10 if dtype == "int8" else 0.0
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(hp, range(prefix)), (ht[b], keys(b, h))], 1 / math.sqrt(D), coarse))
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,G", [(4, 2), (20, 1), (150, 2), (3, 20)])
+def test_nan_rows_of_a_prefix_reach_their_head_only(dtype, B, G):
+    H, D, page, prefix = 10, 128, 128, 9000
+    pool = Pool(130, pages_for([prefix], page), H, D, page, dtype)
+    hp = pool.take(-(-prefix // page))
+    q = _q(131, B, H * G, D)
+    run = lambda: bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, None, _i32([0] * B), out_dtype=torch.float32)  # noqa: E731
+    clean, clean_lse = run()
+    at = (hp[4000 // page], 3, 4000 % page)
+    heads = torch.arange(H * G, device="cuda") // G == 3
+    pool.cache.v[at] = torch.zeros(D, device="cuda").to(pool.cache.v.dtype)    # as a row with NaN or infinity is kept
+    pool.cache.v_scale[at] = float("nan")
+    out, lse = run()
+    assert out[:, heads].isnan().all() and torch.equal(out[:, ~heads], clean[:, ~heads]) and torch.equal(lse, clean_lse)
+    pool.cache.k[at] = torch.zeros(D, device="cuda").to(pool.cache.k.dtype)
+    pool.cache.k_scale[at] = float("nan")
+    out, lse = run()
+    assert out[:, heads].isnan().all() and lse[:, heads].isnan().all()
+    assert torch.equal(out[:, ~heads], clean[:, ~heads]) and torch.equal(lse[:, ~heads], clean_lse[:, ~heads])
+
+
 def test_prefix_equals_private_copies():
     """A shared prefix gives what the same keys at the head of every sequence's own table give."""
     H, G, D, page, prefix, lens = 2, 4, 128, 16, 160, [37, 1, 300]

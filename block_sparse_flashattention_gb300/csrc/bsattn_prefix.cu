@@ -185,10 +185,10 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             // what a score of S is worth in units of log2
             const float ct = c * ex2_approx((float)(msg->key_exp - 127 - 6));
             const uchar4 rest = *reinterpret_cast<const uchar4 *>(msg->rest);
-            // Int8 tiles take the general way, whose two passes are rolled: measured on 512 rows by
-            // 32768 keys, 8 heads, 91 us against 103 unrolled with loads ahead, the roles' loops
-            // sharing the instruction caches.  E4m3 tiles with power-of-two scales take the short
-            // one: 80 us with loads ahead against 97 rolled.
+            // Int8 tiles take the general way, whose two passes are rolled: 512 rows by 32768 keys,
+            // 8 heads, own keys of one token, 94 us a call against 107 with the passes unrolled
+            // (the roles' loops share the instruction caches).  E4m3 tiles with power-of-two scales
+            // take the short one, its second pass with loads ahead: 78 us against 96.
             const bool plain = !kInt8 && !masked && !(rest.x | rest.y | rest.z | rest.w);
             // 32 scores of columns 32 q .. times r; -inf where a key does not count
             auto scores = [&](int q, float (&s)[32]) {
@@ -261,8 +261,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             exp_run = exp_new;
             const float nm = 4.f - m_run;
             float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
-            // 32 columns at a time, the next ones on their way; P over scores that have been
-            // read.  The first 64 keys are handed over while the third part is worked on.
+            // 32 columns at a time, P over scores that have been read; 64 keys are handed over at a time.
             auto hand_over = [&](int half) {
                 tmem_wait_st();
                 tc_fence_before();
@@ -291,23 +290,18 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             if (plain) {
                 uint32_t va[32], vb[32];
                 tmem_ld32(lane_addr + s_col, va);
-                tmem_wait_ld();
-                reg_fence(va);
-                tmem_ld32(lane_addr + s_col + 32u, vb);
-                plain_part(0, va);
-                tmem_wait_ld();
-                reg_fence(vb);
-                tmem_ld32(lane_addr + s_col + 64u, va);
-                plain_part(1, vb);
-                tmem_wait_ld();
-                reg_fence(va);
-                tmem_ld32(lane_addr + s_col + 96u, vb);
-                plain_part(2, va);
-                hand_over(0);
-                tmem_wait_ld();
-                reg_fence(vb);
-                plain_part(3, vb);
-                hand_over(1);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    tmem_wait_ld();
+                    reg_fence(va);
+                    tmem_ld32(lane_addr + s_col + 64u * i + 32u, vb);
+                    plain_part(2 * i, va);
+                    tmem_wait_ld();
+                    reg_fence(vb);
+                    if (i == 0) tmem_ld32(lane_addr + s_col + 64u, va);
+                    plain_part(2 * i + 1, vb);
+                    hand_over(i);
+                }
             } else {
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
@@ -499,7 +493,8 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
                 return;
             uint8_t *tile = smem + dst + st * C::kTileBytes;
             const bool whole = keep == 0xffffffffu;
-#pragma unroll
+            // two steps at a time: 94 us as above, 96 with all eight unrolled
+#pragma unroll 2
             for (int i = 0; i < kSteps; ++i) {
                 uint4 x = *reinterpret_cast<const uint4 *>(raw + i * kRows * D);
                 // what lies in the tile where no key was copied is of an earlier one

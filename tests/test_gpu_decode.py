@@ -479,6 +479,47 @@ def test_captured_steps_share_a_workspace():
         assert torch.equal(n, n2) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_captured_fork_and_join():
+    """Appends on a side stream of a capture, joined before the decodes; both decodes depend on more than their
+    stream's last kernel, one of them through the prefix's own kernel.  Replays see new inputs."""
+    H, G, D, page, B, prefix = 8, 2, 128, 64, 16, 5000
+    lens = [1 + 37 * i for i in range(B)]
+    pool = Pool(132, pages_for(lens + [prefix], page), H, D, page, "int8")
+    hp = _i32(pool.take(-(-prefix // page)))
+    _, table = pool.tables(lens)
+    twin = bsa.KVCache(*(t.clone() for t in (pool.cache.k, pool.cache.v, pool.cache.k_scale, pool.cache.v_scale)))
+    n, q, k, v = _i32(lens), _q(133, B, H * G, D), _q(134, B, H, D), _q(135, B, H, D)
+    ws = [bsa.alloc_decode_workspace(pool.cache, B, H * G, prefix_len=prefix) for _ in range(2)]
+
+    def step(cache, side):
+        main = torch.cuda.current_stream()
+        if side is not None:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                bsa.kv_append(k, v, cache, table, n)
+            twice = q * 2
+            main.wait_stream(side)
+        else:
+            bsa.kv_append(k, v, cache, table, n)
+            twice = q * 2
+        a = bsa.decode_shared_prefix(twice, cache, hp, prefix, table, n, workspace=ws[0])
+        b = bsa.decode(twice, cache, table, n, workspace=ws[1])
+        c = bsa.decode_shared_prefix(twice, cache, hp, prefix, table, n, workspace=ws[0])
+        return a + b + c
+    step(pool.cache, None)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        res = step(pool.cache, side)
+    for i in range(4):
+        q.copy_(_q(140 + i, B, H * G, D))
+        k.copy_(_q(150 + i, B, H, D))
+        v.copy_(_q(160 + i, B, H, D))
+        g.replay()
+        got = [t.clone() for t in res]
+        for x, y in zip(got, step(twin, None)):
+            assert torch.equal(x, y)
+
+
 def test_other_streams_have_their_own_allocations():
     H, G, D, page, lens = 2, 4, 128, 128, [2000, 500]
     pool = Pool(46, pages_for(lens, page), H, D, page, "e4m3")

@@ -15,7 +15,12 @@
 // fp16 (11 bits) is a number relative to the largest contribution, whatever the scales
 // are, and 2^7 of headroom keeps full precision down to 2^-21 of that.
 //
-// Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.
+// Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.  Measured
+// (D = 128): 131072 keys x 32 heads (e4m3) 177 us, 6.3 TB/s of 6.7; 64 sequences of 100 ..
+// 4096 keys x 8 heads, 4 queries a head (int8) 56 us, 5.0 TB/s: 5 us until the first codes
+// arrive, 6 to 8 us from the first warp that is done to the last (the SMs do not reach HBM
+// equally fast, and pieces handed out as warps come free cost more than they save), 3 us for
+// the join.  2 sequences of 1024 keys x 4 heads: 8.9 us, the two launches' latencies.
 //
 // Work split.  Every warp is a worker of its own.  A segment is one (sequence, KV head),
 // or one KV head of the prefix while at most 16 query rows a head meet it (more take
@@ -24,9 +29,9 @@
 // one, and the line is cut evenly over the warps of the device: every warp streams the
 // same number of bytes whatever the lengths.  A warp holds the query rows and the sums in
 // registers and keeps a ring of its own in shared memory full with asynchronous copies;
-// nothing in its loop waits for another warp.  A segment within one warp's piece is finished there; the parts of the others (fp32 output
-// and LSE) go to the workspace, and a second kernel, a programmatic dependent of the
-// first, joins them.
+// nothing in its loop waits for another warp.  A segment within one warp's piece is finished
+// there; the parts of the others (fp32 output and LSE) go to the workspace, and a second
+// kernel, a programmatic dependent of the first, joins them.
 //
 // Fragments without a transpose.  In S = Q K^T (m16n8k16) the contraction index may be
 // permuted alike on both sides, so lane 4g + t takes the D / 4 consecutive codes d =
@@ -44,7 +49,9 @@ namespace bsattn {
 
 namespace {
 
-constexpr int kSegCost = 2;   // groups of 16 keys that starting and ending a segment costs
+// Groups of 16 keys that starting and ending a segment costs: 128 sequences of 1 .. 400 keys,
+// 8 heads: 25.5 us a call with 0, 20.5 with 2, 21.0 with 4.
+constexpr int kSegCost = 2;
 constexpr int kMinPiece = 2;  // places that make a worker of their own worth its part in the join (1, 4, 8 measured
                               // slower on short calls)
 

@@ -9,7 +9,11 @@ namespace bsattn {
 
 constexpr int kMaxCtas = 320;      // CTAs whose parts the workspace has room for
 constexpr int kStreamWarps = 8;    // warps of a streaming CTA, each a worker of its own
-constexpr int kStreamRows = 16;    // query rows a streaming worker holds
+// Query rows a streaming worker holds.  Up to there it beats the other kernel that could take
+// the rows (us a call, e4m3, D = 128): against the block kernel 25 : 39 (16 sequences of 8192
+// keys, 2 heads, G = 16), 37 : 60 (4 heads, G = 8); a prefix of 32768 keys, 8 heads, in the
+// streaming line against the prefix kernel 20 : 33 (2 rows a head), 26 : 34 (16 rows).
+constexpr int kStreamRows = 16;
 constexpr int kBlockRows = 256;    // query rows of a segment in the prefix kernel
 
 // How the keys of a shared prefix are met.  kEach: they are the first keys of every
@@ -25,7 +29,8 @@ constexpr long long kEachBytes = 76ll << 20;
 
 // What the prefix kernel pays for a segment, in tiles: query rows, the first tiles' latency,
 // the part.  512 rows of 8 heads, 32768 keys: CTAs with tiles of two segments took 178000
-// cycles of 1.95 GHz, those with as many of one 157000.
+// cycles of 1.95 GHz, those with as many of one 157000.  A call with own keys (e4m3, int8):
+// 120, 128 us without this weight, 111, 125 with it.
 constexpr int kPreCost = 3;
 
 // Quotient of numbers that mostly fit 32 bits, where a division costs a tenth.

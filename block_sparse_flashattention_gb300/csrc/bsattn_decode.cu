@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     auto unit_groups = [&](int x, bool check) -> int {
         if (!p.has_lists) return lead + (seq_keys(p, x, check) + 15) / 16;
         const int b = x / p.c.H, h = x - b * p.c.H;
-        const ListRow r = list_row(p, b, h, seq_keys(p, b, check && h == 0), check);
+        int n;
+        const ListRow r = list_row(p, b, h, n, check);
         return lead + 8 * (r.full + r.mask);
     };
     const int reps = p.has_lists ? 1 : p.c.H;  // segments of a unit, of equal length
@@ -543,12 +544,14 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
         int seg = start_seg[warp];
         for (long long begin = start_at[warp]; begin < hi; ++seg) {
             const Seg s = segment(p, w, seg);
-            const int n = s.prefix ? p.prefix_len : seq_keys(p, s.b, false);
+            int n = p.prefix_len, g;
             ListRow lr = {};
-            int g = (n + 15) / 16;
             if (p.has_lists && !s.prefix) {
                 lr = list_row(p, s.b, s.h, n, false);
                 g = 8 * (lr.full + lr.mask);
+            } else {
+                if (!s.prefix) n = seq_keys(p, s.b, false);
+                g = (n + 15) / 16;
             }
             if (!s.prefix) g += lead;
             if (g == 0) continue;

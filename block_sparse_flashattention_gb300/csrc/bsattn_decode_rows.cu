@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto unit_tiles = [&](int x, bool check) -> int {
         if (!p.has_lists) return (seq_keys(p, x, check) + kTile - 1) / kTile;
         const int b = x / p.c.H, h = x - b * p.c.H;
-        const ListRow r = list_row(p, b, h, seq_keys(p, b, check && h == 0), check);
+        int n;
+        const ListRow r = list_row(p, b, h, n, check);
         return r.full + r.mask;
     };
     const int reps = p.has_lists ? 1 : p.c.H;  // segments of a unit, of equal length

@@ -46,21 +46,23 @@ struct ListRow {
     long long at;        // first index entry
 };
 
-__device__ __forceinline__ ListRow list_row(const DecodeParams &p, int b, int h, int n, bool check) {
+// The lists of (sequence b, head h), and the sequence's keys n.  All loads go out at once.
+__device__ __forceinline__ ListRow list_row(const DecodeParams &p, int b, int h, int &n, bool check) {
     ListRow r;
+    const long long cnt_at = p.lists_varlen ? (long long)h * p.B + b : (long long)b * p.c.H + h;
+    const int f = __ldg(p.full_cnt + cnt_at), m = __ldg(p.mask_cnt + cnt_at);
+    const int off = p.lists_varlen ? __ldg(p.cu_off + b) : 0;
+    n = seq_keys(p, b, check && h == 0);
     r.full = r.mask = 0;
     r.nn = p.lists_varlen ? (n + kTile - 1) / kTile : p.list_n;
-    const long long cnt_at = p.lists_varlen ? (long long)h * p.B + b : (long long)b * p.c.H + h;
     r.at = cnt_at * p.list_n;
     if (p.lists_varlen) {
-        const int off = __ldg(p.cu_off + b);
         r.at = (long long)h * p.total_n + off;
         if (off < 0 || (long long)off + r.nn > p.total_n || (p.vl && r.nn > p.list_n)) {
             if (check) raise(p, BSATTN_FLAG_BAD_SEQLENS);
             return r;
         }
     }
-    const int f = __ldg(p.full_cnt + cnt_at), m = __ldg(p.mask_cnt + cnt_at);
     r.full = min(max(f, 0), r.nn);
     r.mask = min(max(m, 0), r.nn);
     if (check && (r.full != f || r.mask != m)) raise(p, BSATTN_FLAG_BAD_COUNT);

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     using R = Ring<D, kCols>;
     constexpr int kW = R::kWarps, kThreads = kW * 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long warp_sum[kW], piece_at[kW + 1], start_at[kW];
+    __shared__ long long warp_sum[kW], run_at[kThreads], piece[kW][2], start_at[kW], line[2];
     __shared__ int start_seg[kW];
     const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
     grid_launch_dependents();  // the joining kernel may take its place; it waits for this grid
@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     // of sequences (or, with lists, of (sequence, head) pairs); CTA c also checks every
     // gridDim-th of them and writes the records of those without keys.  The record of any
     // other segment, the workers its parts lie with, is written by the first of these.
+    // Each warp then looks for the run, and in it the segment, that its piece begins in.
     const int g_pre = w.sp ? (p.prefix_len + 15) / 16 : 0, lead = w.mode == kEach ? (p.prefix_len + 15) / 16 : 0;
     const long long line_pre = (long long)w.sp * (g_pre + kSegCost);
     const int units = p.has_lists ? p.B * p.c.H : p.B, per = (units + kThreads - 1) / kThreads;
@@ -503,46 +504,71 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
         if (i < warp) at += warp_sum[i];
         total += warp_sum[i];
     }
+    run_at[tid] = at;
+    int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
+    for (int x = u0; x < u1; ++x)
+        if (x % (int)gridDim.x == (int)blockIdx.x && unit_groups(x, false) == 0)
+            for (int r = 0; r < reps; ++r) rec[w.sp + x * reps + r] = make_int2(0, -1);
+    __syncthreads();
     // pieces of kMinPiece places or a few less: a segment's parts lie with consecutive workers
     const long long cuts = min((long long)gridDim.x * kW, (total + kMinPiece - 1) / kMinPiece);
-    if (tid <= kW) {  // where the pieces of this CTA's workers begin
-        const long long worker = min((long long)blockIdx.x * kW + tid, cuts);
-        piece_at[tid] = cuts ? total * worker / cuts : 0;
-    }
-    __syncthreads();
-    auto owner = [&](long long place) -> int {
-        const unsigned long long a = (unsigned long long)(place + 1) * (unsigned long long)cuts - 1u;
-        if (a <= 0xffffffffu) return (int)((unsigned)a / (unsigned)total);   // 64-bit division costs 10 times as much
-        return (int)(a / (unsigned long long)total);
-    };
-    auto begins_at = [&](long long begin, long long len, int seg, long long seg_len) {
-        // workers of this CTA whose pieces begin within [begin, begin + len): segments seg, seg + 1, ... of seg_len
-        if (piece_at[kW] <= begin || piece_at[0] >= begin + len) return;
-        for (int x = 0; x < kW; ++x)
-            if (piece_at[x] >= begin && piece_at[x] < begin + len) {
-                const int k = (int)((piece_at[x] - begin) / seg_len);
-                start_seg[x] = seg + k;
-                start_at[x] = begin + k * seg_len;
+    if (const long long worker = (long long)blockIdx.x * kW + warp; worker < cuts) {
+        const long long lo = line_div(total * worker, cuts);
+        int seg;
+        long long begin;   // where it begins
+        if (lo < line_pre) {
+            seg = (int)line_div(lo, g_pre + kSegCost);
+            begin = (long long)seg * (g_pre + kSegCost);
+        } else {
+            int run = -1;   // the last run that begins at or before lo
+#pragma unroll
+            for (int i = 0; i < kThreads; i += 32) run += __popc(__ballot_sync(0xffffffffu, run_at[i + lane] <= lo));
+            begin = run_at[run];
+            const int run_end = min(units, (run + 1) * per);
+            for (int x0 = run * per;; x0 += 32) {   // 32 of its units at a time
+                const int n = x0 + lane < run_end ? unit_groups(x0 + lane, false) : 0;
+                const long long len = n ? (long long)(n + kSegCost) * reps : 0;
+                long long end = len;
+                if (per > 1) {
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const long long y = __shfl_up_sync(0xffffffffu, end, d);
+                        if (lane >= d) end += y;
+                    }
+                }
+                end += begin;
+                const unsigned behind = __ballot_sync(0xffffffffu, end > lo);
+                if (behind == 0u && x0 + 32 < run_end) {
+                    begin = __shfl_sync(0xffffffffu, end, 31);
+                    continue;
+                }
+                const int hit = behind ? __ffs(behind) - 1 : 31, un = __shfl_sync(0xffffffffu, n, hit) + kSegCost;
+                begin = __shfl_sync(0xffffffffu, end - len, hit);
+                const int k = (int)line_div(lo - begin, un);
+                begin += (long long)k * un;
+                seg = w.sp + (x0 + hit) * reps + k;
+                break;
             }
-    };
-    int2 *rec = reinterpret_cast<int2 *>(p.ws + w.rec);
-    if (w.sp && tid == 0) begins_at(0, line_pre, 0, g_pre + kSegCost);
-    for (int x = u0; x < u1; ++x) {
-        const int n = unit_groups(x, false);
-        const long long len = n ? (long long)(n + kSegCost) * reps : 0;
-        if (len) begins_at(at, len, w.sp + x * reps, n + kSegCost);
-        else if (x % (int)gridDim.x == (int)blockIdx.x)
-            for (int r = 0; r < reps; ++r) rec[w.sp + x * reps + r] = make_int2(0, -1);
-        at += len;
+        }
+        if (lane == 0) {
+            piece[warp][0] = lo;
+            piece[warp][1] = line_div(total * (worker + 1), cuts);
+            start_at[warp] = begin;
+            start_seg[warp] = seg;
+        }
     }
+    if (tid == 0) line[0] = total, line[1] = cuts;
     __syncthreads();
-    const long long worker = (long long)blockIdx.x * kW + warp;
-    if (worker < cuts) {
-        const long long lo = piece_at[warp], hi = piece_at[warp + 1];
-        Worker<D, kInt8, kCols> k{p, lane, lane >> 2, lane & 3};
-        k.ring = smem_u32(smem) + (uint32_t)warp * R::kStages * R::kStage;
+    // what is needed between segments waits in shared memory: a segment's groups take every register
+    auto owner = [&](long long place) -> int {
+        const volatile long long *l = line;
+        return (int)line_div((place + 1) * l[1] - 1, l[0]);
+    };
+    if ((int)blockIdx.x * kW + warp < line[1]) {
+        const int worker = (int)blockIdx.x * kW + warp;
+        const volatile long long *pc = piece[warp];
         int seg = start_seg[warp];
-        for (long long begin = start_at[warp]; begin < hi; ++seg) {
+        for (long long begin = start_at[warp]; begin < pc[1]; ++seg) {
             const Seg s = segment(p, w, seg);
             int n = p.prefix_len, g;
             ListRow lr = {};
@@ -556,11 +582,13 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
             if (!s.prefix) g += lead;
             if (g == 0) continue;
             const long long first = begin + kSegCost;
-            const int t0 = (int)max(0ll, min((long long)g, lo - first)), t1 = (int)max(0ll, min((long long)g, hi - first));
+            const int t0 = (int)max(0ll, min((long long)g, pc[0] - first)), t1 = (int)max(0ll, min((long long)g, pc[1] - first));
             if (t0 < t1) {
-                if (t0 == 0 && lane == 0) rec[seg] = make_int2((int)worker, t1 == g ? (int)worker : owner(first + g - 1));
+                if (t0 == 0 && lane == 0) rec[seg] = make_int2(worker, t1 == g ? worker : owner(first + g - 1));
+                Worker<D, kInt8, kCols> k{p, lane, lane >> 2, lane & 3};
+                k.ring = smem_u32(smem) + (uint32_t)warp * R::kStages * R::kStage;
                 k.groups(s, lead, n, lr, t0, t1);
-                k.finish(w, s, seg, (int)worker, t0 == 0 && t1 == g);
+                k.finish(w, s, seg, worker, t0 == 0 && t1 == g);
             }
             begin = first + g;
         }

@@ -101,6 +101,14 @@ struct Ring {
     static constexpr uint32_t kBytes = kWarps * kStages * kStage;
 };
 
+// The segment that a warp works on; in shared memory, where looking groups up and finishing
+// find it, since the loop over groups needs every register.
+struct SegKeys {
+    Seg s;
+    ListRow lists;
+    int n, lead;   // keys, groups of the shared prefix before them
+};
+
 // One warp's state: kCols groups of 8 query rows.
 template <int D, bool kInt8, int kCols>
 struct Worker {
@@ -330,24 +338,21 @@ struct Worker {
 
     // Starts a segment of n keys, behind `lead` groups of the shared prefix, and works on
     // its groups t0 .. t1.
-    __device__ __forceinline__ void groups(const Seg &s, int lead, int n, const ListRow &lr, int t0, int t1) {
-        const bool listed = p.has_lists && !s.prefix;
-        const int32_t *own = s.prefix ? p.prefix_table : p.table + (long long)s.b * p.table_stride;
+    __device__ __forceinline__ void groups(const SegKeys *seg_keys, int t0, int t1) {
+        const Seg &s = seg_keys->s;
         // cache row of group i's first key (-1: nothing to read) and how many of its keys count, one group per lane
         auto look_up = [&](int i, int &row, int &nv) {
             row = -1;
             nv = 0;
             if (i >= t1) return;
-            const int32_t *table = own;
-            int keys = n, lim = 16;
-            if (i < lead) {                      // the shared prefix's groups
-                table = p.prefix_table;
-                keys = p.prefix_len;
-            } else {
-                i -= lead;
-            }
+            const ListRow &lr = seg_keys->lists;
+            const int lead = seg_keys->lead, n = seg_keys->n;
+            const bool own = !s.prefix && i >= lead;   // not a group of the shared prefix
+            const int32_t *table = own ? p.table + (long long)s.b * p.table_stride : p.prefix_table;
+            int keys = own ? n : p.prefix_len, lim = 16;
+            if (own) i -= lead;
             int key = i * 16;
-            if (listed && table == own) {
+            if (p.has_lists && own) {
                 const int e = i >> 3;
                 const bool masked = e >= lr.full;
                 const int tile = __ldg((masked ? p.mask_idx + (e - lr.full) : p.full_idx + e) + lr.at);
@@ -410,7 +415,8 @@ struct Worker {
     }
 
     // Writes the rows of a segment (or of the part of it that this worker has).
-    __device__ __forceinline__ void finish(const Plan &w, const Seg &s, int seg, int worker, bool complete) {
+    __device__ __forceinline__ void finish(const Plan &w, const SegKeys *seg_keys, int seg, int worker, bool complete) {
+        const Seg &s = seg_keys->s;
 #pragma unroll
         for (int n = 0; n < kCols; ++n) {
             l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
@@ -465,6 +471,7 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long warp_sum[kW], run_at[kThreads], piece[kW][2], start_at[kW], line[2];
     __shared__ int start_seg[kW];
+    __shared__ SegKeys seg_keys[kW];
     const int warp = (int)warp_id(), lane = (int)lane_id(), tid = threadIdx.x;
     grid_launch_dependents();  // the joining kernel may take its place; it waits for this grid
     // Beside the prefix kernel (which has waited) this one needs nothing that it writes.
@@ -588,8 +595,11 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
                 if (t0 == 0 && lane == 0) rec[seg] = make_int2(worker, t1 == g ? worker : owner(first + g - 1));
                 Worker<D, kInt8, kCols> k{p, lane, lane >> 2, lane & 3};
                 k.ring = smem_u32(smem) + (uint32_t)warp * R::kStages * R::kStage;
-                k.groups(s, lead, n, lr, t0, t1);
-                k.finish(w, s, seg, worker, t0 == 0 && t1 == g);
+                __syncwarp();
+                if (lane == 0) seg_keys[warp] = SegKeys{s, lr, n, lead};
+                __syncwarp();
+                k.groups(&seg_keys[warp], t0, t1);
+                k.finish(w, &seg_keys[warp], seg, worker, t0 == 0 && t1 == g);
             }
             begin = first + g;
         }

@@ -17,11 +17,11 @@
 //
 // Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.  Measured
 // (D = 128): 131072 keys x 32 heads (e4m3) 175 us, 6.3 TB/s of 6.7; 64 sequences of 100 ..
-// 4096 keys x 8 heads, 4 queries a head (int8) 57 us, 5.0 TB/s: 5 us until the first codes
+// 4096 keys x 8 heads, 4 queries a head (int8) 56 us, 5.1 TB/s: 5 us until the first codes
 // arrive (the look-up of the pieces 2, of the pages 1), 6 to 8 us from the first warp that is
 // done to the last (the SMs do not reach HBM equally fast, and pieces handed out as warps come
 // free cost more than they save), 3 us for the join.  2 sequences of 1024 keys x 4 heads:
-// 8.1 us, the latencies of the two launches.
+// 8.2 us, the latencies of the two launches.
 //
 // Work split.  Every warp is a worker of its own.  A segment is one (sequence, KV head),
 // or one KV head of the prefix while at most 16 query rows a head meet it (more take

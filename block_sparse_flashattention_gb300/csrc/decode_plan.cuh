@@ -10,8 +10,8 @@ namespace bsattn {
 constexpr int kMaxCtas = 320;      // CTAs whose parts the workspace has room for
 constexpr int kStreamWarps = 8;    // warps of a streaming CTA, each a worker of its own
 // Query rows a streaming worker holds.  Up to there it beats the other kernel that could take
-// the rows (us a call, e4m3, D = 128): against the block kernel 25 : 39 (16 sequences of 8192
-// keys, 2 heads, G = 16), 37 : 60 (4 heads, G = 8); a prefix of 32768 keys, 8 heads, in the
+// the rows (us a call, e4m3, D = 128): against the block kernel 24 : 39 (16 sequences of 8192
+// keys, 2 heads, G = 16), 36 : 60 (4 heads, G = 8); a prefix of 32768 keys, 8 heads, in the
 // streaming line against the prefix kernel 20 : 33 (2 rows a head), 26 : 34 (16 rows).
 constexpr int kStreamRows = 16;
 constexpr int kBlockRows = 256;    // query rows of a segment in the prefix kernel

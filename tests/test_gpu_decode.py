@@ -246,6 +246,44 @@ def test_nan_rows_of_a_prefix_reach_their_head_only(dtype, B, G):
     assert torch.equal(out[:, ~heads], clean[:, ~heads]) and torch.equal(lse[:, ~heads], clean_lse[:, ~heads])
 
 
+@pytest.mark.parametrize("listed", [False, True])
+def test_many_sequences(listed):
+    """More sequences than a block has threads, most of them short or empty; many blocks of query rows."""
+    B, H, G, D, page, prefix = 3000, 2, 2, 64, 16, 500
+    lens = [(7 * i) % 4 if i % 500 else 300 for i in range(B)]
+    pool = Pool(136, pages_for(lens + [prefix], page), H, D, page, "e4m3")
+    hp = pool.take(-(-prefix // page))
+    ht, table = pool.tables(lens)
+    q = _q(137, B, H * G, D)
+    meta = lists(H, lens, lambda b, h: range(0, -(-lens[b] // 128), 2)) if listed else None
+    keys = lambda b: [p for p in range(lens[b]) if not listed or p // 128 % 2 == 0]  # noqa: E731
+    some = sorted({0, 1, 2, 3, 31, 32, 499, 500, 501, 1023, 1024, 1500, 2047, 2500, 2998, 2999})
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), meta=meta, err_flag=err, out_dtype=torch.float32)
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(ht[some[b]], keys(some[b]))], 1 / math.sqrt(D)))
+    empty = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert not out[empty].any() and torch.isneginf(lse[empty]).all() and lse[~empty].isfinite().all()
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, table, _i32(lens), meta=meta, err_flag=err,
+                                        out_dtype=torch.float32)
+    assert int(err) == 0 and lse.isfinite().all()
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, range(prefix)), (ht[some[b]], keys(some[b]))],
+                                       1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("G", [1, 24])
+def test_one_long_sequence_among_many(G):
+    """A sequence that takes most of the line, empty ones before and behind it."""
+    H, D, page = 1, 64, 64
+    lens = [0] * 300 + [20000] + [0, 1] * 200
+    pool = Pool(138, pages_for(lens, page), H, D, page, "int8")
+    ht, table = pool.tables(lens)
+    q = _q(139, len(lens), H * G, D)
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    some = [0, 299, 300, 301, 302, 303, 699, 700]
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(ht[some[b]], range(lens[some[b]]))], 1 / math.sqrt(D)))
+    assert lse[torch.tensor([n > 0 for n in lens], device="cuda")].isfinite().all()
+
+
 def test_prefix_equals_private_copies():
     """A shared prefix gives what the same keys at the head of every sequence's own table give."""
     H, G, D, page, prefix, lens = 2, 4, 128, 16, 160, [37, 1, 300]

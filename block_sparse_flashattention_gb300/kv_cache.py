@@ -43,7 +43,7 @@ def _bind() -> None:
     _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     _lib = library()
     # The ordinary calls in native code (csrc/torch_calls.cpp), where it was compiled for
-    # this torch: 9 us of host time for a decode call, against 17 here.
+    # this torch: 8 us of host time for a decode call, against 17 here.
     try:
         from . import _torch_calls as calls
         if calls.torch_version() == t.__version__.split("+")[0]:

@@ -97,7 +97,7 @@ struct Ring {
     static constexpr uint32_t kCodes = 16u * D;
     static constexpr uint32_t kStage = 2u * kCodes + 128u;
     // ~200 KB in flight per SM (HBM needs 44 KB at 6.7 TB/s and ~1 us).  131072 keys x 32 heads
-    // with 5, 6, 7, 8 warps a CTA (5, 4, 3, 3 stages): 184, 176, 184, 173 us.
+    // with 5, 6, 7, 8 warps a CTA (4, 4, 3, 3 stages): 184, 176, 184, 173 us.
     static constexpr int kStages = (int)(101376u * (2 / kCtas) / (kWarps * kStage));
     static constexpr uint32_t kBytes = kWarps * kStages * kStage;
 };

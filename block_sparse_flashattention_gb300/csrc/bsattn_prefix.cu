@@ -81,8 +81,8 @@ struct Cfg {
     static constexpr uint32_t kScale = kRaw + 2 * kRawBytes;         // kMsgs x 128 rests r of key scales
     static constexpr uint32_t kMsg = kScale + kMsgs * 512u;
     static constexpr uint32_t kBar = kMsg + kMsgs * (uint32_t)sizeof(KeyMsg);
-    // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete;
-    // raw K / V tile full and empty
+    // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete
+    // (once a segment, also for a slot without tiles); raw K / V tile full and empty
     static constexpr int bKF = 0, bKE = 2, bVF = 4, bVE = 6, bQF = 8, bSR = 10, bPR = 12, bOD = 16, bDrain = 18,
                          bRF = 19, bRE = 21, kNumBars = 23;
     static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
@@ -325,13 +325,13 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
         if (!ok) break;
         tile0 += (uint32_t)walk.n;
         // ---- the part: rows of 128-byte blocks go through the slot's query tile (no S of
-        // this segment is outstanding), so that every store writes whole row pieces
-        if (done > 0) {
-            ok = mbar_wait(bar(C::bOD + t), od & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            ++od;
-            tc_fence_after();
-        }
+        // this segment is outstanding), so that every store writes whole row pieces.  A slot
+        // without tiles waits too: its warps would otherwise arrive for the next segment's
+        // query rows before the issuing warp, or each other, are through with this one's.
+        ok = mbar_wait(bar(C::bOD + t), od & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        ++od;
+        tc_fence_after();
         const bool empty = done == 0 || l_run == 0.f;   // NaN is not empty
         const float inv = empty ? 0.f : ex2_approx((float)(exp_run - 127 - 6)) / l_run;
         const long long part_row = ((long long)walk.seg + blockIdx.x) * w.rows_p + t * kTile;
@@ -647,6 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool split = p.B * p.G - row0 <= kTile;
             if (!wait(C::bQF, seg & 1u) || !wait(C::bQF + 1, seg & 1u)) break;
             tc_fence_after();
+            // slot 1 has no tile and no O of its own to wait for
+            mbar_arrive_lead(split && walk.n == 1 ? lead : 0u, bar(C::bOD + 1));
             for (int k = 0; ok && k < walk.n; ++k) {
                 const uint32_t tile = it + (uint32_t)k;
                 if (!wait(C::bKF + (int)(tile & 1u), (tile >> 1) & 1u)) break;

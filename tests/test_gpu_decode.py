@@ -202,6 +202,50 @@ def test_long_prefix_many_tiles_per_block(dtype, D):
     agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, range(prefix))], 1 / math.sqrt(D), coarse))
 
 
+class _Heads:
+    """Some heads of a pool, as expect() asks for rows."""
+
+    def __init__(self, pool, heads):
+        self.pool, self.heads = pool, heads
+
+    def host(self, name, table, h, positions):
+        return self.pool.host(name, table, self.heads[h], positions)
+
+
+def _some_heads(pool, q, G, heads, parts, scale, coarse=0.0):
+    """(columns of the query heads of KV heads `heads`, expect() for them)."""
+    cols = [h * G + g for h in heads for g in range(G)]
+    return cols, expect(_Heads(pool, heads), f64(q[:, cols]), G, parts, scale, coarse)
+
+
+@pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
+    ("int8", 600, 20, 64, 2, 100),     # one tile a segment, several segments a block
+    ("e4m3", 600, 20, 64, 6, 128),
+    ("e4m3", 32, 1, 128, 128, 640),    # pieces of one tile, some of two segments
+    ("int8", 90, 18, 64, 3, 300),      # three tiles a segment: pieces with the last tile of one, the first of the next
+])
+def test_long_prefix_with_one_tile_of_a_segment_in_a_block(dtype, H, G, D, B, prefix):
+    """At most 128 query rows a head and one tile of a segment in a block: one of the two slots has no key there,
+    in one segment after the other.  The workspace holds NaN before each call: no part may be left out."""
+    page = 64
+    pool = Pool(170, pages_for([prefix], page), H, D, page, dtype)
+    hp = pool.take(-(-prefix // page))
+    q = _q(171, B, H * G, D)
+    ws = bsa.alloc_decode_workspace(pool.cache, B, H * G, prefix_len=prefix)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = None
+    for _ in range(8):
+        ws.fill_(255)
+        got = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), prefix, None, _i32([0] * B), workspace=ws, err_flag=err,
+                                       out_dtype=torch.float32)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    assert int(err) == 0
+    cols, ref = _some_heads(pool, q, G, sorted({0, 1, 2, H // 3, H // 2, H - 2, H - 1}), lambda b, h: [(hp, range(prefix))],
+                            1 / math.sqrt(D), 2.0 ** -10 if dtype == "int8" else 0.0)
+    agree(first[0][:, cols], first[1][:, cols], ref)
+
+
 @pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
     ("e4m3", 8, 1, 128, 5, 8000),      # prefix in the streaming line
     ("int8", 2, 2, 128, 20, 8000),     # in its own kernel

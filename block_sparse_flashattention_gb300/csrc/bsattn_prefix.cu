@@ -64,6 +64,13 @@ static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs<true> + 256 * kWidenRegs<true
 constexpr uint32_t kSub = kTile * 64 * 2;  // 128 rows x 64 fp16: one 128-byte swizzle span
 constexpr int kMsgs = 4;                   // tiles whose key scales and masks are kept
 
+// The factors' exponents E and F are at least this (biased): 2^(6 - E) and its inverse are then
+// normal numbers, also for the smallest scales, those of rows of zeros.
+constexpr int kLeastExp = 7;
+
+// 2^(e - 6) of a biased exponent e in [kLeastExp, 254].
+__device__ __forceinline__ float scale_down(int e) { return __uint_as_float((uint32_t)(e - 6) << 23); }
+
 struct KeyMsg {
     uint32_t keep[4];  // keys that count, one bit each
     int32_t exp;       // E (biased) of the value factors
@@ -189,8 +196,8 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             const uint4 kw = *reinterpret_cast<const uint4 *>(msg->keep);
             const bool masked = (kw.x & kw.y & kw.z & kw.w) != 0xffffffffu;
             const int exp_new = msg->exp;
-            // what a score of S is worth in units of log2
-            const float ct = c * ex2_approx((float)(msg->key_exp - 127 - 6));
+            // what a score of S is worth in units of log2; above 0: a masked key's -inf stays -inf
+            const float ct = fmaxf(c * scale_down(msg->key_exp), 0x1p-126f);
             const uchar4 rest = *reinterpret_cast<const uchar4 *>(msg->rest);
             // Int8 tiles take the general way, whose two passes are rolled: 512 rows by 32768 keys,
             // 8 heads, own keys of one token, 94 us a call against 107 with the passes unrolled
@@ -333,7 +340,8 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
         ++od;
         tc_fence_after();
         const bool empty = done == 0 || l_run == 0.f;   // NaN is not empty
-        const float inv = empty ? 0.f : ex2_approx((float)(exp_run - 127 - 6)) / l_run;
+        // l and the values' scale one after the other: their quotient may be below fp32's range, the result not
+        const float inv = empty ? 0.f : 1.f / l_run, unit = done == 0 ? 0.f : scale_down(exp_run);
         const long long part_row = ((long long)walk.seg + blockIdx.x) * w.rows_p + t * kTile;
         float *po = reinterpret_cast<float *>(p.ws + w.pre_o) + part_row * D;
         uint4 *scr = reinterpret_cast<uint4 *>(smem + C::kQ + (uint32_t)t * C::kTileBytes + quarter * 4096u);
@@ -353,10 +361,10 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 scr[lane * 8u + ((uint32_t)i ^ (lane & 7u))] =
-                    make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * inv),
-                               __float_as_uint(__uint_as_float(v[4 * i + 1]) * inv),
-                               __float_as_uint(__uint_as_float(v[4 * i + 2]) * inv),
-                               __float_as_uint(__uint_as_float(v[4 * i + 3]) * inv));
+                    make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * inv * unit),
+                               __float_as_uint(__uint_as_float(v[4 * i + 1]) * inv * unit),
+                               __float_as_uint(__uint_as_float(v[4 * i + 2]) * inv * unit),
+                               __float_as_uint(__uint_as_float(v[4 * i + 3]) * inv * unit));
             __syncwarp();
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -447,10 +455,10 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         ks4 = on4 && !values ? __ldg(reinterpret_cast<const uint4 *>(p.c.ks + row4)) : make_uint4(0, 0, 0, 0);
         vs4 = on4 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
     };
-    // Largest binary exponent (biased, at least 1) of a tile's scales; NaN and infinity do not count.
+    // Largest binary exponent (biased, at least kLeastExp) of a tile's scales; NaN and infinity do not count.
     auto largest_exp = [&](uint4 x) -> int {
         const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-        uint32_t top = 1u << 23;
+        uint32_t top = (uint32_t)kLeastExp << 23;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (v[i] < 0x7f800000u && 4 * lane + i < n) top = max(top, v[i]);
@@ -481,7 +489,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     const uint32_t dst = (values ? C::kV : C::kK) + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 32 + sub_row) * 128u;
     uint32_t it = 0;
     while (walk.next()) {
-        int exp_run = 1;            // E starts anew with a segment's sums
+        int exp_run = kLeastExp;    // E starts anew with a segment's sums
         for (int k = 0; k < walk.n; ++k, ++it) {
             const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
             exp_run = max(exp_run, largest_exp(vs4));
@@ -491,7 +499,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             // V: vs 2^(6 - E); K: the power of two in ks, times 2^(6 - F)
             const uint32_t bits = __float_as_uint(scale);
             const float f32 = (values ? scale : __uint_as_float(bits & 0x7f800000u)) *
-                              __uint_as_float((uint32_t)min(254, 260 - exp) << 23);
+                              __uint_as_float((uint32_t)(260 - exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
             const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF, v = values ? 1 : 0;
             if (!__all_sync(0xffffffffu,

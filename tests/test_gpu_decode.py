@@ -246,6 +246,87 @@ def test_long_prefix_with_one_tile_of_a_segment_in_a_block(dtype, H, G, D, B, pr
     agree(first[0][:, cols], first[1][:, cols], ref)
 
 
+OWN_KERNEL = [(120, 1, 2, 1500), (3, 20, 3, 300), (60, 5, 2, 2700)]   # B, G, H, keys: rows in both slots alike, in both halves
+
+
+def _own_kernel(seed, B, G, H, n, page, dtype, spread=0.3, more=2):
+    """A pool of heads of 128 for a prefix of about n keys that has a kernel of its own, and its pages."""
+    assert G > 16 or B * H * n * 2 * 132 > 76 << 20
+    pool = Pool(seed, pages_for([n], page) + more, H, 128, page, dtype, spread=spread)
+    return pool, pool.take(-(-n // page))
+
+
+def _set_row(pool, name, page, row, scale, zero=True):
+    """Row `row` of a page: zeros (or its codes), with this scale, in the cache and in its host copy."""
+    pool.scales[name][page, :, row] = scale
+    getattr(pool.cache, name + "_scale")[page, :, row] = scale
+    if zero:
+        pool.codes[name][page, :, row] = 0
+        getattr(pool.cache, name).view(torch.uint8)[page, :, row] = 0
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("page", [128, 32])
+@pytest.mark.parametrize("B,G,H,n", OWN_KERNEL)
+def test_a_tile_of_a_long_prefix_without_a_key(B, G, H, n, page, dtype):
+    """Every page of a tile bad (with pages of 128: one entry): its keys are left out and flagged, whether they
+    come first, amid others or are all there are; the sequences' own keys are attended all the same."""
+    pool, hp = _own_kernel(172, B, G, H, n, page, dtype, more=B)
+    lens = [i % 3 for i in range(B)]
+    ht, table = pool.tables(lens)
+    q = _q(173, B, H * G, 128)
+    per, coarse = 128 // page, 2.0 ** -10 if dtype == "int8" else 0.0
+    some = [0, 1, 2, B - 1]
+    for tiles in ([1], [0], range(-(-n // 128))):
+        bad = list(hp)
+        for t in tiles:
+            for i in range(t * per, min((t + 1) * per, len(bad))):
+                bad[i] = -1 if i % 2 else 10 ** 6
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(bad), n, table, _i32(lens), err_flag=err, out_dtype=torch.float32)
+        assert int(err) == bsa.FLAG_BAD_INDEX
+        agree(out[some], lse[some], expect(pool, f64(q[some]), G,
+                                           lambda b, h: [(bad, range(n)), (ht[some[b]], range(lens[some[b]]))], 1 / math.sqrt(128), coarse))
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("scale", [2.0 ** -126, 0.0])           # as rows of zeros are appended, as a new cache holds them
+@pytest.mark.parametrize("B,G,H,n", OWN_KERNEL + [(2, 20, 2, 1)])
+def test_zero_keys_in_the_last_tile_of_a_long_prefix(B, G, H, n, scale, dtype):
+    n = (n - 1) // 128 * 128 + 1
+    pool, hp = _own_kernel(174, B, G, H, n, 128, dtype)
+    for name in ("k", "v"):
+        _set_row(pool, name, hp[-1], 0, scale)
+    q = _q(175, B, H * G, 128)
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), n, None, _i32([0] * B), out_dtype=torch.float32)
+    some = [0, 1, B - 1]
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, range(n))], 1 / math.sqrt(128),
+                                       2.0 ** -10 if dtype == "int8" else 0.0))
+
+
+@pytest.mark.parametrize("B,G,H,n", OWN_KERNEL)
+def test_a_long_prefix_in_a_new_cache(B, G, H, n):
+    """A zero-filled cache, as a warm-up call meets it: every score is 0, every value too."""
+    cache = bsa.alloc_kv_cache(-(-n // 128), H, 128)
+    out, lse = bsa.decode_shared_prefix(_q(176, B, H * G, 128), cache, _i32(list(range(cache.num_pages))), n, None,
+                                        _i32([0] * B), out_dtype=torch.float32)
+    assert not out.any() and (lse - math.log(n)).abs().max() <= math.log(n) * 2.0 ** -22 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("B,G,H,n", OWN_KERNEL)
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+def test_the_smallest_scales_of_a_long_prefix(B, G, H, n, dtype):
+    """Keys and values whose scales are fp32's smallest normal number, queries so large that the scores differ."""
+    pool, hp = _own_kernel(177, B, G, H, n, 128, dtype)
+    for name in ("k", "v"):
+        pool.scales[name][:] = 2.0 ** -126
+        getattr(pool.cache, name + "_scale").fill_(2.0 ** -126)
+    q = _q(178, B, H * G, 128, size=2.0 ** (126 - 6))
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), n, None, _i32([0] * B), out_dtype=torch.float32)
+    some = [0, 1, B - 1]
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, range(n))], 1 / math.sqrt(128)))
+
+
 @pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
     ("e4m3", 8, 1, 128, 5, 8000),      # prefix in the streaming line
     ("int8", 2, 2, 128, 20, 8000),     # in its own kernel

@@ -496,9 +496,11 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             const int exp = values ? exp_run : largest_exp(ks4);
             step();
             const int row4_2 = look_ahead();
-            // V: vs 2^(6 - E); K: the power of two in ks, times 2^(6 - F)
+            // V: vs 2^(6 - E); K: the power of two in ks, times 2^(6 - F), but NaN where ks is: an
+            // infinity, the power of two in a NaN, could give a score that drops the key
             const uint32_t bits = __float_as_uint(scale);
-            const float f32 = (values ? scale : __uint_as_float(bits & 0x7f800000u)) *
+            const bool number = (bits & 0x7fffffffu) < 0x7f800000u;
+            const float f32 = (values ? scale : __uint_as_float(number ? bits & 0x7f800000u : 0x7fc00000u)) *
                               __uint_as_float((uint32_t)(260 - exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
             const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF, v = values ? 1 : 0;

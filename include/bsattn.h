@@ -446,7 +446,7 @@ bsattn_status bsattn_bwd_workspace_size(const bsattn_meta *meta, size_t *bytes);
  *   k_scale, v_scale  device fp32, [num_pages, H, page_size], 16-byte aligned
  * Position p of sequence b is row p % page_size of page page_table[b][p / page_size].
  * A row's value is code * scale.  A scale is what bsattn_kv_append writes, or any
- * value >= 0 of the caller's; a NaN scale makes its row NaN.
+ * finite value >= 0 of the caller's; a NaN scale makes its row NaN, whatever its codes.
  * page_size in {16, 32, 64, 128}; D in {64, 128} (else BSATTN_ERR_UNSUPPORTED);
  * num_pages * H * page_size < 2^31.
  */

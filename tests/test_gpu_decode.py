@@ -327,6 +327,25 @@ def test_the_smallest_scales_of_a_long_prefix(B, G, H, n, dtype):
     agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, range(n))], 1 / math.sqrt(128)))
 
 
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,G,H,n", OWN_KERNEL + [(4, 2, 3, 300), (2, 12, 3, 300)])
+def test_a_nan_key_scale_is_not_dropped(B, G, H, n, dtype):
+    """A row whose key scale is NaN is NaN whatever its codes are, also where all of them and the queries have one sign
+    each, so that a score of infinite size would be -inf, the score of a key that does not count."""
+    pool = Pool(179, pages_for([n], 64), H, 128, 64, dtype)
+    hp = pool.take(-(-n // 64))
+    at = (hp[1], 1, 9)
+    pool.cache.k.view(torch.uint8)[at] = 0x7E if dtype == "e4m3" else 0x7F     # the largest code
+    pool.cache.k_scale[at] = float("nan")
+    q = -_q(180, B, H * G, 128).abs()
+    nan = torch.arange(H * G, device="cuda") // G == 1
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), n, None, _i32([0] * B), out_dtype=torch.float32)
+    assert out[:, nan].isnan().all() and lse[:, nan].isnan().all()
+    assert out[:, ~nan].isfinite().all() and lse[:, ~nan].isfinite().all()
+    o2, l2 = bsa.decode(q, pool.cache, _i32([hp] * B), _i32([n] * B), out_dtype=torch.float32)
+    assert o2[:, nan].isnan().all() and l2[:, nan].isnan().all() and l2[:, ~nan].isfinite().all()
+
+
 @pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
     ("e4m3", 8, 1, 128, 5, 8000),      # prefix in the streaming line
     ("int8", 2, 2, 128, 20, 8000),     # in its own kernel

@@ -214,10 +214,11 @@ __global__ void __launch_bounds__(kWarps * 32) bsattn_kv_read_kernel(const __gri
         }
 }
 
-// One warp per token and 8 heads, and at least one thread.
+// One warp per token and 8 heads, and at least one block: with an error word the offsets
+// are checked also where there is no row.
 unsigned blocks_for(long long total, int H) {
     const long long warps = total * ((H + kHeadsPerWarp - 1) / kHeadsPerWarp);
-    return (unsigned)((warps + kWarps - 1) / kWarps);
+    return (unsigned)(warps > 0 ? (warps + kWarps - 1) / kWarps : 1);
 }
 
 // Launches as a programmatic dependent of what precedes on the stream: the launch

@@ -132,12 +132,12 @@ bsattn_status bsattn_kv_append(const void *k, const void *v, int64_t k_stride, i
     bsattn_status st = check_cache(cache);
     if (st != BSATTN_OK) return st;
     if (B <= 0 || total < 0 || (!cu_seqlens && total != B)) return BSATTN_ERR_INVALID_ARG;
-    if (!k || !v || !seqlens) return BSATTN_ERR_INVALID_ARG;
+    if (!seqlens || (total > 0 && (!k || !v))) return BSATTN_ERR_INVALID_ARG;
     if (misaligned(k, 16) || misaligned(v, 16)) return BSATTN_ERR_INVALID_ARG;
     const int64_t row = (int64_t)cache->H * cache->D;
     if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return BSATTN_ERR_INVALID_ARG;
     if ((st = check_table(page_table, table_stride, table_cols, cache->page_size, false)) != BSATTN_OK) return st;
-    if (total == 0) return BSATTN_OK;
+    if (total == 0 && !err_flag) return BSATTN_OK;  // else the offsets are still checked
     bsattn::AppendParams p = {};
     p.c = view(cache);
     p.k = static_cast<const uint16_t *>(k);
@@ -162,10 +162,10 @@ bsattn_status bsattn_kv_read(const bsattn_kv_cache *cache, const int32_t *page_t
                              int32_t *err_flag, void *stream) {
     bsattn_status st = check_cache(cache);
     if (st != BSATTN_OK) return st;
-    if (B <= 0 || total < 0 || !cu_seqlens || !k || !v) return BSATTN_ERR_INVALID_ARG;
+    if (B <= 0 || total < 0 || !cu_seqlens || (total > 0 && (!k || !v))) return BSATTN_ERR_INVALID_ARG;
     if (misaligned(k, 16) || misaligned(v, 16)) return BSATTN_ERR_INVALID_ARG;
     if ((st = check_table(page_table, table_stride, table_cols, cache->page_size, false)) != BSATTN_OK) return st;
-    if (total == 0) return BSATTN_OK;
+    if (total == 0 && !err_flag) return BSATTN_OK;  // else the offsets are still checked
     bsattn::ReadParams p = {};
     p.c = view(cache);
     p.table = page_table;

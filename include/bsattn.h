@@ -480,7 +480,7 @@ typedef struct {
  *              elements from token to token (at least H * D and a multiple of 8, so
  *              that the K or V part of a fused projection can be given as it is);
  *              16-byte aligned.
- * total        packed rows of k and v.
+ * total        packed rows of k and v (0: k and v may be NULL).
  * cu_seqlens   device int32 [B+1], or NULL: one new token per sequence (total == B).
  * page_table   device int32, B rows of table_cols entries, table_stride apart.
  * seqlens      device int32 [B].  seqlens[b] <= 0: the sequence is padding, its rows
@@ -507,8 +507,8 @@ bsattn_status bsattn_kv_append(const void *k, const void *v, int64_t k_stride, i
  * read back exactly.
  *
  * k, v         device bf16 [total, H, D], contiguous, 16-byte aligned (written).
- * total        rows of k and v; rows outside every sequence's range are left as
- *              they were.
+ * total        rows of k and v (0: they may be NULL); rows outside every sequence's
+ *              range are left as they were.
  * A page outside [0, num_pages): its rows read as 0, BSATTN_FLAG_BAD_INDEX.  A
  * sequence whose offsets leave [0, total] or decrease, or that is longer than its
  * table row: none of its rows is written, BSATTN_FLAG_BAD_SEQLENS.

@@ -216,3 +216,29 @@ def test_wide_strides_and_other_stream():
     for name in ("k", "v", "k_scale", "v_scale"):
         assert torch.equal(getattr(cache, name).view(torch.uint8), getattr(plain, name).view(torch.uint8))
     assert not torch.equal(cache.k.view(torch.uint8), _empty(8, H, D, page, "e4m3").k.view(torch.uint8))
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_calls_without_a_row(native, monkeypatch):
+    """No sequence has a new token, no row is read back: nothing happens; offsets that promise rows are flagged."""
+    from block_sparse_flashattention_gb300 import kv_cache
+    cache = _empty(2, 2, 64, 16, "e4m3")
+    if not native:
+        monkeypatch.setattr(kv_cache, "_calls", None)
+    before = [t.view(torch.uint8).clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    table, n, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0], [1], [0]], [3, 0, 16], [0, 0, 0, 0]))
+    none = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for e in (None, err):
+        assert bsa.kv_append(none, none, cache, table, n, cu_seqlens=cu, err_flag=e) is cache
+        for kw in (dict(total=0), dict(k=none.clone(), v=none.clone())):
+            k, v = bsa.kv_read(cache, table, cu, err_flag=e, **kw)
+            assert k.shape == v.shape == none.shape
+    assert int(err) == 0
+    assert all(torch.equal(a, t.view(torch.uint8)) for a, t in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    bad = torch.tensor([0, 0, 1, 1], dtype=torch.int32, device="cuda")
+    for call in (lambda: bsa.kv_append(none, none, cache, table, n, cu_seqlens=bad, err_flag=err),
+                 lambda: bsa.kv_read(cache, table, bad, total=0, err_flag=err)):
+        err.zero_()
+        call()
+        assert int(err) == bsa.FLAG_BAD_SEQLENS

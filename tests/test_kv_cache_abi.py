@@ -79,6 +79,17 @@ def test_append_of_nothing():
     assert _append(total=0, cu_seqlens=FAKE) == bsa.BSATTN_OK
 
 
+def test_nothing_has_no_address():
+    """An empty tensor's address is null; the other arguments are checked all the same."""
+    none = dict(total=0, k=None, v=None)
+    assert _append(cu_seqlens=FAKE, **none) == bsa.BSATTN_OK and _read(**none) == bsa.BSATTN_OK
+    for bad in (dict(B=0), dict(seqlens=None), dict(table_cols=0), dict(k_stride=255)):
+        assert _append(**{**none, "cu_seqlens": FAKE, **bad}) == INV
+    for bad in (dict(B=0), dict(cu_seqlens=None), dict(page_table=None)):
+        assert _read(**{**none, **bad}) == INV
+    assert _append(**none) == INV                  # B rows are due without offsets
+
+
 @pytest.mark.parametrize("kw", [
     dict(B=0), dict(total=-1), dict(cu_seqlens=None), dict(k=None), dict(v=None), dict(k=FAKE + 8), dict(v=FAKE + 2),
     dict(page_table=None), dict(table_cols=0), dict(table_stride=0)])

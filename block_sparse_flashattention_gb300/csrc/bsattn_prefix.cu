@@ -6,8 +6,9 @@
 // rows, in shared memory:
 //   K' = fp16(code) 2^(f - F + 6), exact: f the binary exponent of the key's scale, F the
 //        largest in the tile; what is left of the scale, r in [1, 2), multiplies the
-//        key's scores in fp32, and only where some key of 32 has r > 1 (int8; the scales
-//        that e4m3 rows are given are powers of two);
+//        key's scores in fp32, and only where some key of 32 has r != 1 (int8; the scales
+//        that e4m3 rows are given are powers of two).  Where f < F - 14 it is
+//        K' = fp16(code) 2^6 and r times 2^(f - F) instead;
 //   V' = fp16(code) fp16(vs 2^(6 - E)), E the largest binary exponent of a value scale
 //        so far (O is rescaled when it grows): exact for power-of-two scales, otherwise
 //        off by two roundings to 11 bits; a row keeps 10 bits down to 2^-30 of the largest;
@@ -67,6 +68,10 @@ constexpr int kMsgs = 4;                   // tiles whose key scales and masks a
 // The factors' exponents E and F are at least this (biased): 2^(6 - E) and its inverse are then
 // normal numbers, also for the smallest scales, those of rows of zeros.
 constexpr int kLeastExp = 7;
+
+// Binary exponents by which a scale may lie below the largest and share its factor: codes
+// (multiples of 2^-9 in e4m3, of 1 in int8) times 2^(6 - kNear) are exact in fp16.
+constexpr int kNear = 14;
 
 // 2^(e - 6) of a biased exponent e in [kLeastExp, 254].
 __device__ __forceinline__ float scale_down(int e) { return __uint_as_float((uint32_t)(e - 6) << 23); }
@@ -497,11 +502,13 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             step();
             const int row4_2 = look_ahead();
             // V: vs 2^(6 - E); K: the power of two in ks, times 2^(6 - F), but NaN where ks is: an
-            // infinity, the power of two in a NaN, could give a score that drops the key
+            // infinity, the power of two in a NaN, could give a score that drops the key.  A key
+            // far below the largest keeps its own exponent, and the difference goes into r.
             const uint32_t bits = __float_as_uint(scale);
             const bool number = (bits & 0x7fffffffu) < 0x7f800000u;
+            const int own = max((int)(bits >> 23 & 255u), kLeastExp), base_exp = !values && exp - own > kNear ? own : exp;
             const float f32 = (values ? scale : __uint_as_float(number ? bits & 0x7f800000u : 0x7fc00000u)) *
-                              __uint_as_float((uint32_t)(260 - exp) << 23);
+                              __uint_as_float((uint32_t)(260 - base_exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
             const int empty = values ? C::bVE : C::bKE, full = values ? C::bVF : C::bKF, v = values ? 1 : 0;
             if (!__all_sync(0xffffffffu,
@@ -531,9 +538,10 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
                 }
             }
             if (!values) {
+                const int below = min(exp - base_exp, 126);
                 reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] =
-                    __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-                const bool rest = __any_sync(0xffffffffu, (bits & 0x7fffffu) != 0u);
+                    __uint_as_float((bits & 0x7fffffu) | (uint32_t)(127 - below) << 23);
+                const bool rest = __any_sync(0xffffffffu, (bits & 0x7fffffu) != 0u || below > 0);
                 if (lane == 0) {
                     KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
                     msg->keep[warp] = keep;

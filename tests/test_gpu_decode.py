@@ -346,6 +346,22 @@ def test_a_nan_key_scale_is_not_dropped(B, G, H, n, dtype):
     assert o2[:, nan].isnan().all() and l2[:, nan].isnan().all() and l2[:, ~nan].isfinite().all()
 
 
+@pytest.mark.parametrize("B,G,H,n", OWN_KERNEL)
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("far", [15, 34, 80])
+def test_a_huge_key_leaves_the_others_their_scores(B, G, H, n, dtype, far):
+    """One key's scale is 2^far times its neighbours', and its score so low that it has no weight: the scores of the
+    keys in its tile are as exact as without it."""
+    pool, hp = _own_kernel(181, B, G, H, n, 128, dtype)
+    pool.cache.k.view(torch.uint8)[hp[1], :, 9] = 0xFE if dtype == "e4m3" else 0x81     # -448, -127
+    pool.cache.k_scale[hp[1], :, 9] = 2.0 ** (far - 8)      # the neighbours' are about 2^-8 (e4m3) and 2^-6
+    q = _q(182, B, H * G, 128).abs()
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), n, None, _i32([0] * B), out_dtype=torch.float32)
+    some = [0, 1, B - 1]
+    agree(out[some], lse[some], expect(pool, f64(q[some]), G, lambda b, h: [(hp, [j for j in range(n) if j != 128 + 9])],
+                                       1 / math.sqrt(128), 2.0 ** -10 if dtype == "int8" else 0.0))
+
+
 @pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
     ("e4m3", 8, 1, 128, 5, 8000),      # prefix in the streaming line
     ("int8", 2, 2, 128, 20, 8000),     # in its own kernel

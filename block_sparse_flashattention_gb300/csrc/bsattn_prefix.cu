@@ -11,11 +11,16 @@
 //        K' = fp16(code) 2^6 and r times 2^(f - F) instead;
 //   V' = fp16(code) fp16(vs 2^(6 - E)), E the largest binary exponent of a value scale
 //        so far (O is rescaled when it grows): exact for power-of-two scales, otherwise
-//        off by two roundings to 11 bits; a row keeps 10 bits down to 2^-30 of the largest;
+//        off by two roundings to 11 bits;
 //   Q' = fp16(q 2^-e), e the row's largest binary exponent (as in bsattn_decode.cu).
-// With t_j the scores in true units and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 4)
-// is rounded to fp16 for P V', l sums it in fp32; out = O 2^(E - 6) / l, log2-LSE = m - 4 +
+// With t_j the scores in true units and c = softmax_scale log2(e) 2^e: p_j = 2^(c t_j - m + 7)
+// is rounded to fp16 for P V', l sums it in fp32; out = O 2^(E - 6) / l, log2-LSE = m - 7 +
 // log2 l.  The reference m is moved only when some weight could pass 2^15.
+//
+// A weight below 2^-32 of the largest is 0 in fp16, which is enough while the value scales lie
+// within 2^12 of each other.  From the first tile on where they do not, the weights of P V'
+// carry them as in bsattn_decode.cu: V' = fp16(code) fp16(vs 2^(6 - f)), p_j = 2^(c t_j + f - E -
+// u + 7) with a reference u of their own, out = O 2^(u - m + E - 6) / l.
 //
 // A segment is (KV head, 256 query rows): two 128-row tiles ("slots") that share each
 // K/V tile.  With 128 rows or fewer both slots hold the same rows and take the key tiles
@@ -69,9 +74,13 @@ constexpr int kMsgs = 4;                   // tiles whose key scales and masks a
 // normal numbers, also for the smallest scales, those of rows of zeros.
 constexpr int kLeastExp = 7;
 
-// Binary exponents by which a scale may lie below the largest and share its factor: codes
-// (multiples of 2^-9 in e4m3, of 1 in int8) times 2^(6 - kNear) are exact in fp16.
-constexpr int kNear = 14;
+// Binary exponents by which a scale may lie below the largest and share its factor.  Keys:
+// codes (multiples of 2^-9 in e4m3, of 1 in int8) times 2^(6 - 14) are exact in fp16.  Values:
+// so far below E, and so much may E grow within a segment, before the weights carry the scales.
+constexpr int kNearKeys = 14, kNearValues = 8, kGrowth = 4;
+
+// log2 of the largest weight when the reference moves, and how far it may grow before it does again.
+constexpr float kLift = 7.f, kReach = 8.f;
 
 // 2^(e - 6) of a biased exponent e in [kLeastExp, 254].
 __device__ __forceinline__ float scale_down(int e) { return __uint_as_float((uint32_t)(e - 6) << 23); }
@@ -81,8 +90,9 @@ struct KeyMsg {
     int32_t exp;       // E (biased) of the value factors
     int32_t key_exp;   // F (biased) of the key factors
     uint8_t rest[4];   // whether some r of keys 32 q .. is not 1
-    int32_t pad;
+    int32_t wide;      // value scales are far apart: the weights of P V' carry them
 };
+constexpr uint32_t kZeroRow = 255;  // in place of a key's E - f: its values count as 0
 
 template <int D>
 struct Cfg {
@@ -92,7 +102,8 @@ struct Cfg {
     static constexpr uint32_t kRawBytes = kTile * D;
     static constexpr uint32_t kScale = kRaw + 2 * kRawBytes;         // kMsgs x 128 rests r of key scales
     static constexpr uint32_t kMsg = kScale + kMsgs * 512u;
-    static constexpr uint32_t kBar = kMsg + kMsgs * (uint32_t)sizeof(KeyMsg);
+    static constexpr uint32_t kDown = kMsg + kMsgs * (uint32_t)sizeof(KeyMsg);  // kMsgs x 128 bytes: E - f, if wide
+    static constexpr uint32_t kBar = kDown + kMsgs * 128u;
     // K / V stage full and empty, per slot: query rows there, S ready, two halves of P ready, O complete
     // (once a segment, also for a slot without tiles); raw K / V tile full and empty
     static constexpr int bKF = 0, bKE = 2, bVF = 4, bVE = 6, bQF = 8, bSR = 10, bPR = 12, bOD = 16, bDrain = 18,
@@ -188,8 +199,9 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::bQF + t));
         // ---- the slot's tiles
-        float m_run = kNoKey, l_run = 0.f;
+        float m_run = kNoKey, l_run = 0.f, u_run = kNoKey;   // u_run: m_run unless wide
         int exp_run = 0, done = 0;
+        bool wide = false;
         for (int k = split ? t : 0; ok && k < walk.n; k += split ? 2 : 1) {
             ok = mbar_wait(bar(C::bSR + t), sc & 1u, abort, p.err, BSATTN_FLAG_TIMEOUT);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -200,15 +212,16 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             const float4 *ks = reinterpret_cast<const float4 *>(smem + C::kScale + slot * 512u);
             const uint4 kw = *reinterpret_cast<const uint4 *>(msg->keep);
             const bool masked = (kw.x & kw.y & kw.z & kw.w) != 0xffffffffu;
-            const int exp_new = msg->exp;
+            const int4 info = *reinterpret_cast<const int4 *>(&msg->exp);   // exp, key_exp, rest, wide
+            const int exp_new = info.x;
             // what a score of S is worth in units of log2; above 0: a masked key's -inf stays -inf
-            const float ct = fmaxf(c * scale_down(msg->key_exp), 0x1p-126f);
-            const uchar4 rest = *reinterpret_cast<const uchar4 *>(msg->rest);
+            const float ct = fmaxf(c * scale_down(info.y), 0x1p-126f);
             // Int8 tiles take the general way, whose two passes are rolled: 512 rows by 32768 keys,
             // 8 heads, own keys of one token, 94 us a call against 107 with the passes unrolled
             // (the roles' loops share the instruction caches).  E4m3 tiles with power-of-two scales
             // take the short one, its second pass with loads ahead: 78 us against 96.
-            const bool plain = !kInt8 && !masked && !(rest.x | rest.y | rest.z | rest.w);
+            wide = info.w != 0;
+            const bool plain = !kInt8 && !masked && !wide && info.z == 0;
             // 32 scores of columns 32 q .. times r; -inf where a key does not count
             auto scores = [&](int q, float (&s)[32]) {
                 uint32_t v[32];
@@ -255,17 +268,50 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                     m_new = fmaxf(m_new, fmax3(g0, fmaxf(s[30], s[31]), g1) * ct);
                 }
             }
-            constexpr float kReach = 11.f;
             const bool grew = done == 0 || __any_sync(0xffffffffu, m_new - m_run > kReach);
-            // O is rescaled when m moves or E grew
+            // O is rescaled when m moves or E grew; if wide, when u moves
             float alpha = 1.f;
             if (grew) {
                 alpha = ex2_approx(m_run - m_new);
                 m_run = m_new;
             }
-            if (done > 0 && (grew || exp_new != exp_run)) {
+            float alpha_o = alpha * ex2_approx((float)(exp_run - exp_new));
+            bool rescale = grew || exp_new != exp_run;
+            const uint32_t *down = reinterpret_cast<const uint32_t *>(smem + C::kDown + slot * 128u);
+            // 8 scores of columns 8 c .. in units of log2 and their keys' E - f, infinite for rows of zeros
+            // (small loops: they are rare, and the usual ones share the instruction caches with them)
+            auto wide_scores = [&](int c, float (&z)[8], float (&d)[8]) {
+                uint32_t v[8];
+                tmem_ld8(lane_addr + s_col + 8u * c, v);
+                tmem_wait_ld();
+                reg_fence(v);
+                const uint32_t keep = (c < 8 ? c < 4 ? kw.x : kw.y : c < 12 ? kw.z : kw.w) >> (8 * (c & 3));
+                const float *r = reinterpret_cast<const float *>(ks) + 8 * c;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    z[x] = (keep >> x) & 1u ? __uint_as_float(v[x]) * r[x] * ct : -INFINITY;
+                    const uint32_t byte = (down[2 * c + (x >> 2)] >> (8 * (x & 3))) & 255u;
+                    d[x] = byte == kZeroRow ? INFINITY : (float)byte;
+                }
+            };
+            if (__builtin_expect(wide, 0)) {
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 16; ++c) {
+                    float z[8], d[8];
+                    wide_scores(c, z, d);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) top = fmaxf(top, z[x] - d[x]);
+                }
+                const float kept = u_run + (float)(exp_run - exp_new);   // O as it is, in units of E
+                rescale = __any_sync(0xffffffffu, done == 0 || top - kept > kReach);
+                u_run = rescale ? fmaxf(kept, top) : kept;
+                alpha_o = ex2_approx(kept - u_run);
+            } else {
+                u_run = m_run;
+            }
+            if (done > 0 && rescale) {
                 // S of this tile was issued after the slot's previous P V: O is up to date
-                const float alpha_o = alpha * ex2_approx((float)(exp_run - exp_new));
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t v[32];
@@ -278,7 +324,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                 }
             }
             exp_run = exp_new;
-            const float nm = 4.f - m_run;
+            const float nm = kLift - m_run;
             float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
             // 32 columns at a time, P over scores that have been read; 64 keys are handed over at a time.
             auto hand_over = [&](int half) {
@@ -321,13 +367,29 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
                     plain_part(2 * i + 1, vb);
                     hand_over(i);
                 }
-            } else {
+            } else if (__builtin_expect(!wide, 1)) {
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     float s[32];
                     scores(q, s);
                     part(q, s);
                     if (q & 1) hand_over(q >> 1);
+                }
+            } else {
+                const float nu = kLift - u_run;
+#pragma unroll 1
+                for (int c = 0; c < 16; ++c) {
+                    float z[8], d[8];
+                    uint32_t pk[4];
+                    wide_scores(c, z, d);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        la0 += ex2_approx(z[2 * x] + nm);
+                        la1 += ex2_approx(z[2 * x + 1] + nm);
+                        pk[x] = pack_f16x2(ex2_approx(z[2 * x] + nu - d[2 * x]), ex2_approx(z[2 * x + 1] + nu - d[2 * x + 1]));
+                    }
+                    tmem_st4(lane_addr + s_col + 4u * c, pk);
+                    if ((c & 7) == 7) hand_over(c >> 3);
                 }
             }
             const float l_tile = (la0 + lb0) + (la1 + lb1);
@@ -346,7 +408,8 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
         tc_fence_after();
         const bool empty = done == 0 || l_run == 0.f;   // NaN is not empty
         // l and the values' scale one after the other: their quotient may be below fp32's range, the result not
-        const float inv = empty ? 0.f : 1.f / l_run, unit = done == 0 ? 0.f : scale_down(exp_run);
+        const float inv = empty ? 0.f : 1.f / l_run;
+        const float unit = done == 0 ? 0.f : wide ? ex2_approx(u_run - m_run + (float)(exp_run - 127 - 6)) : scale_down(exp_run);
         const long long part_row = ((long long)walk.seg + blockIdx.x) * w.rows_p + t * kTile;
         float *po = reinterpret_cast<float *>(p.ws + w.pre_o) + part_row * D;
         uint4 *scr = reinterpret_cast<uint4 *>(smem + C::kQ + (uint32_t)t * C::kTileBytes + quarter * 4096u);
@@ -380,7 +443,7 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             __syncwarp();
         }
         if (row_ok)
-            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - 4.f + lg2_approx(l_run);
+            reinterpret_cast<float *>(p.ws + w.pre_l)[part_row + r] = empty ? -INFINITY : m_run - kLift + lg2_approx(l_run);
         tc_fence_before();
     }
 }
@@ -459,6 +522,13 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         const bool on4 = row4 >= 0;
         ks4 = on4 && !values ? __ldg(reinterpret_cast<const uint4 *>(p.c.ks + row4)) : make_uint4(0, 0, 0, 0);
         vs4 = on4 ? __ldg(reinterpret_cast<const uint4 *>(p.c.vs + row4)) : make_uint4(0, 0, 0, 0);
+        if (n < kTile) {   // behind the last key
+            auto cut = [&](uint32_t &x, int i) {
+                if (4 * lane + i >= n) x = 0u;
+            };
+            cut(ks4.x, 0), cut(ks4.y, 1), cut(ks4.z, 2), cut(ks4.w, 3);
+            cut(vs4.x, 0), cut(vs4.y, 1), cut(vs4.z, 2), cut(vs4.w, 3);
+        }
     };
     // Largest binary exponent (biased, at least kLeastExp) of a tile's scales; NaN and infinity do not count.
     auto largest_exp = [&](uint4 x) -> int {
@@ -466,8 +536,30 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
         uint32_t top = (uint32_t)kLeastExp << 23;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (v[i] < 0x7f800000u && 4 * lane + i < n) top = max(top, v[i]);
+            if (v[i] < 0x7f800000u) top = max(top, v[i]);
         return (int)(__reduce_max_sync(0xffffffffu, top) >> 23);
+    };
+    // A scale of 0, or the smallest, which rows of zeros have.
+    auto zero_row = [](uint32_t bits) -> bool { return (bits & 0x7fffffffu) <= 1u << 23; };
+    // E - f of this lane's four values, kZeroRow for rows of zeros; one byte each.
+    auto far_bytes = [&](int exp) -> uint32_t {
+        const uint32_t v[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+        uint32_t out = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = max(exp - max((int)(v[i] >> 23 & 255u), kLeastExp), 0);
+            out |= (zero_row(v[i]) ? kZeroRow : (uint32_t)d) << (8 * i);
+        }
+        return out;
+    };
+    // Whether one of the tile's values that are not rows of zeros lies more than 2^kNearValues below E.
+    auto any_far = [&](int exp) -> bool {
+        const uint32_t v[4] = {vs4.x, vs4.y, vs4.z, vs4.w}, least = (1u << 23) + 1u;
+        const uint32_t near = (uint32_t)max(exp - kNearValues, 1) << 23;
+        bool far = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) far |= v[i] - least < near - least;   // in [least, near)
+        return __any_sync(0xffffffffu, far && near > least);
     };
     // `ahead` walks two tiles in front: its tile's page is being looked up while the scales of
     // the tile before it are loaded and the one before that is widened.
@@ -494,10 +586,14 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
     const uint32_t dst = (values ? C::kV : C::kK) + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 32 + sub_row) * 128u;
     uint32_t it = 0;
     while (walk.next()) {
-        int exp_run = kLeastExp;    // E starts anew with a segment's sums
+        int exp_run = kLeastExp, exp_first = 0;   // E starts anew with a segment's sums
+        bool wide = false;
         for (int k = 0; k < walk.n; ++k, ++it) {
             const uint32_t st = it & 1u, ph = (it >> 1) & 1u;
             exp_run = max(exp_run, largest_exp(vs4));
+            if (exp_first <= kLeastExp) exp_first = exp_run;   // tiles of zeros do not count
+            // what no tile had far below its E lies within 2^(kNearValues + kGrowth) of the present E
+            wide = wide || exp_run - exp_first > kGrowth || any_far(exp_run);
             const int exp = values ? exp_run : largest_exp(ks4);
             step();
             const int row4_2 = look_ahead();
@@ -506,7 +602,8 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
             // far below the largest keeps its own exponent, and the difference goes into r.
             const uint32_t bits = __float_as_uint(scale);
             const bool number = (bits & 0x7fffffffu) < 0x7f800000u;
-            const int own = max((int)(bits >> 23 & 255u), kLeastExp), base_exp = !values && exp - own > kNear ? own : exp;
+            const int own = max((int)(bits >> 23 & 255u), kLeastExp);
+            const int base_exp = (values ? wide && !zero_row(bits) : exp - own > kNearKeys) ? own : exp;
             const float f32 = (values ? scale : __uint_as_float(number ? bits & 0x7f800000u : 0x7fc00000u)) *
                               __uint_as_float((uint32_t)(260 - base_exp) << 23);
             const uint32_t factor = pack_f16x2(f32, f32);
@@ -542,6 +639,8 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
                 reinterpret_cast<float *>(smem + C::kScale + (it % kMsgs) * 512u)[warp * 32 + lane] =
                     __uint_as_float((bits & 0x7fffffu) | (uint32_t)(127 - below) << 23);
                 const bool rest = __any_sync(0xffffffffu, (bits & 0x7fffffu) != 0u || below > 0);
+                if (wide && warp == 0)
+                    reinterpret_cast<uint32_t *>(smem + C::kDown + (it % kMsgs) * 128u)[lane] = far_bytes(exp_run);
                 if (lane == 0) {
                     KeyMsg *msg = reinterpret_cast<KeyMsg *>(smem + C::kMsg) + it % kMsgs;
                     msg->keep[warp] = keep;
@@ -549,6 +648,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
                     if (warp == 0) {
                         msg->exp = exp_run;
                         msg->key_exp = exp;
+                        msg->wide = wide ? 1 : 0;
                     }
                 }
             }

@@ -362,6 +362,81 @@ def test_a_huge_key_leaves_the_others_their_scores(B, G, H, n, dtype, far):
                                        1 / math.sqrt(128), 2.0 ** -10 if dtype == "int8" else 0.0))
 
 
+def _agree_far(out, lse, pool, q, G, keys, coarse):
+    """Against the oracle, relative to what the keys contribute, not to the largest value.  The weights of P V carry the
+    value scales where these lie far apart: a weight is rounded by 2^-11 of itself, or by 2^-25 where the largest is 2^7
+    or more, and multiplies at most 2^7 largest codes, the one of the largest contribution at least 2^5 (codes and
+    factors vary by 2 each): 2^-30 of the largest contribution, 2^-28 where the scales of tiles that are not far apart
+    differ by 2^2 at most.  Scores: as in expect()."""
+    B, Hq, D = q.shape
+    scale = 1 / math.sqrt(D)
+    got, gl, x = f64(out), f64(lse), f64(q)
+    for h in range(Hq // G):
+        k, v = pool.host("k", keys, h, range(len(keys) * pool.page)), pool.host("v", keys, h, range(len(keys) * pool.page))
+        for b in range(B):
+            for g in range(G):
+                i = h * G + g
+                o, l, spread = okv.attend(x[b, i], k, v, scale)
+                s = scale * (k @ x[b, i])
+                ds = (D + 8) * 2.0 ** -24 * scale * float(np.max(np.abs(k) @ np.abs(x[b, i])))
+                top = float(np.max(np.exp(s - l) * np.max(np.abs(v), 1)))
+                tol = spread * (2.0 ** -11 + 2 * ds + coarse + 2.0 ** -20) + len(k) * 2.0 ** -28 * top
+                assert np.all(np.abs(got[b, i] - o) <= tol), (b, i, np.max(np.abs(got[b, i] - o) / tol))
+                assert abs(gl[b, i] - l) <= ds + 2.0 ** -20 + abs(l) * 2.0 ** -22
+
+
+def _scaled(pool, name, factor):
+    """Multiplies scales (broadcast over heads) by factor [pages, rows], in the cache and in its host copy."""
+    pool.scales[name] = (pool.scales[name] * factor[:, None]).astype(np.float32)
+    getattr(pool.cache, name + "_scale").copy_(torch.from_numpy(pool.scales[name]))
+
+
+@pytest.mark.parametrize("B,G,H,n", [(120, 1, 2, 1536), (3, 20, 3, 384), (60, 5, 2, 2688), (3, 20, 60, 1536), (75, 4, 40, 1024)])
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("far,first", [(13, 0), (26, 0), (26, 1), (60, 0), (60, 1), (40, 2)])
+def test_value_scales_far_apart_in_a_long_prefix(B, G, H, n, dtype, far, first):
+    """Half of the values are 2^far smaller than the others, and one key there has 2^far the weight of one among the
+    others, so that both contribute alike, whichever half comes first (2: every other key)."""
+    pool, hp = _own_kernel(183, B, G, H, n, 128, dtype, spread=0.0, more=0)
+    small = np.zeros((len(hp), 128), bool).reshape(-1)
+    small[::2] = first == 2
+    if first < 2:
+        small[:n // 2] = first == 0
+        small[n // 2:] = first == 1
+    _scaled(pool, "v", np.where(small, 2.0 ** -far * 1.3, 1.0).reshape(-1, 128)[np.argsort(hp)])
+    pair = [int(np.flatnonzero(small)[len(small) // 4 - 3]), int(np.flatnonzero(~small)[len(small) // 4 - 3])]
+    _scaled(pool, "k", np.full((len(hp), 128), 2.0 ** -10))
+    q = _q(184, B, H * G, 128).abs()
+    some = sorted({0, 1, B - 1})
+    for j, s in zip(pair, (20 + far, 20)):               # scores of about s ln 2: q . k = 1.2 x 128 code scale
+        x = s * math.log(2) * math.sqrt(128) / (1.2 * 128)
+        code, value = (0x7E, 448.0) if dtype == "e4m3" else (0x7F, 127.0)
+        pg, row = hp[j // 128], j % 128
+        pool.codes["k"][pg, :, row] = code
+        pool.cache.k.view(torch.uint8)[pg, :, row] = code
+        _set_row(pool, "k", pg, row, float(np.float32(x / value)), zero=False)
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(hp), n, None, _i32([0] * B), out_dtype=torch.float32)
+    _agree_far(out[some], lse[some], pool, q[some], G, hp, 2.0 ** -10)
+
+
+@pytest.mark.parametrize("B,G,H,n", [(120, 1, 2, 1536), (3, 20, 3, 384), (60, 5, 2, 2688)])
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+def test_value_scales_of_all_sizes_in_a_long_prefix(B, G, H, n, dtype):
+    """Value scales of every size from 2^-60 to 2^60 and 0, some rows of zeros, one tile of bad pages; queries so large
+    that the weights differ as much."""
+    pool, hp = _own_kernel(185, B, G, H, n, 128, dtype, spread=0.0, more=0)
+    rng = np.random.default_rng(186)
+    _scaled(pool, "v", 2.0 ** rng.uniform(-60, 60, (len(hp), 128)))
+    for row, scale in ((5, 0.0), (70, 2.0 ** -126), (127, 0.0)):
+        _set_row(pool, "v", hp[2], row, scale)
+    pages = list(hp)
+    pages[1] = -1
+    q = _q(187, B, H * G, 128, size=12.0)
+    some = sorted({0, 1, B - 1})
+    out, lse = bsa.decode_shared_prefix(q, pool.cache, _i32(pages), n, None, _i32([0] * B), out_dtype=torch.float32)
+    _agree_far(out[some], lse[some], pool, q[some], G, pages, 2.0 ** -10)
+
+
 @pytest.mark.parametrize("dtype,H,G,D,B,prefix", [
     ("e4m3", 8, 1, 128, 5, 8000),      # prefix in the streaming line
     ("int8", 2, 2, 128, 20, 8000),     # in its own kernel

@@ -109,7 +109,11 @@ def _elsewhere(cache, stream, call):
         if stream is None:
             return call()
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=cache.device)
+            # the default stream's handle is 0, which ExternalStream takes for a stream of torch's pool
+            stream = torch.cuda.ExternalStream(stream, device=cache.device) if stream else \
+                torch.cuda.default_stream(cache.device)
+        elif stream.device != cache.device:
+            raise ValueError("stream must be of the cache's device")
         with torch.cuda.stream(stream):
             return call()
 

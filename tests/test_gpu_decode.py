@@ -808,6 +808,27 @@ def test_other_streams_have_their_own_allocations():
         assert torch.equal(o, want[0]) and torch.equal(l, want[1])
 
 
+def test_the_default_streams_handle_is_the_default_stream():
+    """Its handle is 0 (what current_stream().cuda_stream gives): the calls run behind what is queued there, with
+    their outputs allocated there."""
+    from block_sparse_flashattention_gb300 import kv_cache
+    H, G, D, page, lens = 2, 4, 128, 128, [2000, 500]
+    pool = Pool(46, pages_for(lens, page), H, D, page, "e4m3")
+    _, table = pool.tables(lens)
+    x, n = _q(47, 2, H * G, D), _i32(lens)
+    want = bsa.decode(x, pool.cache, table, n)
+    seen = kv_cache._elsewhere(pool.cache, 0, torch.cuda.current_stream)
+    assert seen == torch.cuda.default_stream() and seen.cuda_stream == 0
+    big, q = torch.ones((8192, 8192), dtype=torch.bfloat16, device="cuda"), torch.zeros_like(x)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        big = big @ big * 2.0 ** -13
+    q += x * big[0, 0]                                    # queued behind the products; 1 times x
+    out, lse = bsa.decode(q, pool.cache, table, n, stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("dtype", ["e4m3", "int8"])
 def test_a_serving_run(dtype):
     """Prompts appended, steps of append + decode, then the cached context read back for the block-sparse forward:

@@ -424,19 +424,20 @@ struct Worker {
             l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
             const bool empty = l[n] == 0.f;
             // no key with a value scale above 0: O is 0, whatever the quotient of the references
-            const float own_inv = empty || u[n] == kNoKey ? 0.f : ex2_approx(u[n] - m[n] - 7.f) / l[n];
+            const float2 own_inv = empty || u[n] == kNoKey ? make_float2(0.f, 0.f) : quotient(u[n] - m[n] - 7.f, l[n]);
             const float own_lse = empty ? -INFINITY : m[n] + lg2_approx(l[n]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float inv = __shfl_sync(0xffffffffu, own_inv, 8 * t + 4 * e);
+                const float inv = __shfl_sync(0xffffffffu, own_inv.x, 8 * t + 4 * e);
+                const float rest = __shfl_sync(0xffffffffu, own_inv.y, 8 * t + 4 * e);
                 const float lse2 = __shfl_sync(0xffffffffu, own_lse, 8 * t + 4 * e);
                 const int r = 8 * n + 2 * t + e;
                 if (r >= s.rows) continue;
                 float y[D / 8];                  // elements (D / 8) g ..
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
-                    y[2 * i] = o[i][n][e] * inv;
-                    y[2 * i + 1] = o[i][n][2 + e] * inv;
+                    y[2 * i] = o[i][n][e] * inv * rest;
+                    y[2 * i + 1] = o[i][n][2 + e] * inv * rest;
                 }
                 RowOut at;
                 if (!s.prefix && complete && w.direct) at = RowOut{0, (long long)s.b * p.Hq + s.h * p.G + r};

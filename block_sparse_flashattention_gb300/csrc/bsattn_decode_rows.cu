@@ -335,7 +335,7 @@ struct Consumer {
                 for (int k = 0; k < key_groups; ++k) ll += st[k].z * ex2_approx(st[k].x - bm);
                 const bool empty = ll == 0.f;
                 // no key with a value scale above 0: O is 0, whatever the quotient of the references
-                const float inv = empty || bu == kNoKey ? 0.f : ex2_approx(bu - bm - 7.f) / ll;
+                const float2 inv = empty || bu == kNoKey ? make_float2(0.f, 0.f) : quotient(bu - bm - 7.f, ll);
                 const float lse2 = empty ? -INFINITY : bm + lg2_approx(ll);
                 if (row_tile * 16 + r < s.rows) {
                     const RowOut at = row_out(s, seg, complete, row_tile * 16 + r);
@@ -347,7 +347,7 @@ struct Consumer {
                             y0 = fmaf(f, x[0], y0);
                             y1 = fmaf(f, x[64], y1);
                         }
-                        store_pair(at, g * (D / 8) + 2 * i, y0 * inv, y1 * inv);
+                        store_pair(at, g * (D / 8) + 2 * i, y0 * inv.x * inv.y, y1 * inv.x * inv.y);
                     }
                     if (key_group == 0 && g == 0) store_lse(p, w, at, lse2);
                 }

@@ -75,6 +75,12 @@ __device__ __forceinline__ float lg2_approx(float x) {
     return y;
 }
 
+// 2^x / l as two factors: with the smallest value scales it may be below fp32's range, while
+// what it multiplies is large enough for the product to be within.
+__device__ __forceinline__ float2 quotient(float x, float l) {
+    return make_float2(ex2_approx(fmaxf(x, -100.f)) / l, ex2_approx(fminf(x + 100.f, 0.f)));
+}
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
     asm volatile(

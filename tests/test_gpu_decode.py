@@ -663,6 +663,21 @@ def test_scales_of_all_sizes(G):
     agree(out, lse, expect(pool, f64(meta_q), G, lambda b, h: [(ht[b], range(lens[b]))], 1 / math.sqrt(D)))
 
 
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("G,D", [(1, 128), (12, 64), (20, 128), (100, 64)])
+def test_the_smallest_scales(G, D, dtype):
+    """Keys and values whose scales are fp32's smallest normal number, queries so large that the scores differ."""
+    H, page, lens = 2, 32, [500, 1, 70]
+    pool = Pool(188, pages_for(lens, page), H, D, page, dtype)
+    ht, table = pool.tables(lens)
+    for name in ("k", "v"):
+        pool.scales[name][:] = 2.0 ** -126
+        getattr(pool.cache, name + "_scale").fill_(2.0 ** -126)
+    q = _q(189, 3, H * G, D, size=2.0 ** (126 - 6))
+    out, lse = bsa.decode(q, pool.cache, table, _i32(lens), out_dtype=torch.float32)
+    agree(out, lse, expect(pool, f64(q), G, lambda b, h: [(ht[b], range(lens[b]))], 1 / math.sqrt(D)))
+
+
 def test_queries_of_all_sizes():
     """Queries far below and above fp16's range, zeros, strided rows."""
     H, G, D, page, lens = 1, 6, 128, 128, [200]

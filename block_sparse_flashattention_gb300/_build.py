@@ -16,6 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsattn.so")
 CALLS = os.path.join(PKG, "_torch_calls.so")
 OBJDIR = os.path.join(ROOT, "_build")
+CALLS_TORCH = os.path.join(OBJDIR, "torch_calls.version")   # the torch that CALLS was compiled against
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -42,18 +43,26 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def calls_up_to_date(torch_version: str) -> bool:
+    """Whether CALLS is newer than its sources and was compiled against this torch."""
+    if not os.path.exists(CALLS) or not os.path.exists(CALLS_TORCH):
+        return False
+    inputs = [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(INCLUDE, "bsattn.h"), os.path.abspath(__file__)]
+    with open(CALLS_TORCH) as f:
+        return f.read() == torch_version and all(os.path.getmtime(x) <= os.path.getmtime(CALLS) for x in inputs)
+
+
 def build_calls(force: bool = False) -> bool:
     """Compiles csrc/torch_calls.cpp against the installed torch.  It only spares host time
     (kv_cache.py marshals the same calls through ctypes without it), so that a machine
     where it does not compile goes without: the reason is printed, False returned."""
     src = os.path.join(CSRC, "torch_calls.cpp")
-    inputs = [src, os.path.join(INCLUDE, "bsattn.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(f) <= os.path.getmtime(CALLS) for f in inputs):
-        return True
     try:
         import torch
     except ImportError:
         return False
+    if not force and calls_up_to_date(torch.__version__):
+        return True
     root = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)))
     cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.sep in _nvcc() else "/usr/local/cuda"
     tmp = f"{CALLS}.tmp.{os.getpid()}"
@@ -67,6 +76,9 @@ def build_calls(force: bool = False) -> bool:
         print(f"{src} was not compiled, the cache calls go through ctypes:\n{r.stderr}", file=sys.stderr)
         return False
     os.replace(tmp, CALLS)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(CALLS_TORCH, "w") as f:
+        f.write(torch.__version__)
     return True
 
 

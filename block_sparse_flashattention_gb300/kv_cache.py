@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import warnings
 
 from ._binding import (BSATTN_OK, KV_E4M3, KV_INT8, OUT_BF16, OUT_F32, BsattnError, bsattn_decode_workspace_size,
                        bsattn_kv_cache, library)
@@ -50,6 +51,9 @@ def _bind() -> None:
             calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 _lib.bsattn_kv_append, _lib.bsattn_kv_read, _lib.bsattn_decode, _lib.bsattn_decode_shared_prefix)))
             _calls = calls
+        else:
+            warnings.warn(f"the native cache calls were compiled for torch {calls.torch_version()}, not {t.__version__}: "
+                          "they are marshalled through ctypes until the package is built again", stacklevel=3)
     except ImportError:
         pass
     torch = t

@@ -147,6 +147,39 @@ def test_workspace_size():
             bsa.bsattn_decode_workspace_size(_cache(), **{**dict(B=3, Hq=4, prefix_len=0), **kw})
 
 
+# -------------------------------------------------------- the native calls --
+
+def test_native_calls_are_compiled_anew_for_another_torch(monkeypatch, tmp_path):
+    if not _build.build_calls():
+        pytest.skip("torch_calls.cpp does not compile here")
+    assert _build.calls_up_to_date(torch.__version__) and not _build.calls_up_to_date("0.1")
+    stamp = tmp_path / "version"
+    stamp.write_text("0.1")
+    monkeypatch.setattr(_build, "CALLS_TORCH", str(stamp))
+    ran = []
+
+    class Failed:
+        returncode, stderr = 1, "not run"
+    monkeypatch.setattr(_build.subprocess, "run", lambda cmd, **kw: ran.append(cmd) or Failed)
+    assert not _build.build_calls() and len(ran) == 1 and ran[0][0] == "g++"
+    stamp.write_text(torch.__version__)
+    assert _build.build_calls() and len(ran) == 1
+
+
+def test_native_calls_of_another_torch_are_left_with_a_warning(monkeypatch):
+    import sys
+    import types
+    from block_sparse_flashattention_gb300 import kv_cache
+    other = types.ModuleType("other")
+    other.torch_version = lambda: "0.1"
+    monkeypatch.setitem(sys.modules, "block_sparse_flashattention_gb300._torch_calls", other)
+    monkeypatch.setattr(bsa, "_torch_calls", other, raising=False)
+    monkeypatch.setattr(kv_cache, "_calls", None)
+    with pytest.warns(UserWarning, match="compiled for torch 0.1"):
+        kv_cache._bind()
+    assert kv_cache._calls is None
+
+
 # ------------------------------------------------------ the torch wrappers --
 
 def _cpu_cache(**kw):

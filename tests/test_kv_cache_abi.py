@@ -174,7 +174,8 @@ def test_native_calls_of_another_torch_are_left_with_a_warning(monkeypatch):
     other.torch_version = lambda: "0.1"
     monkeypatch.setitem(sys.modules, "block_sparse_flashattention_gb300._torch_calls", other)
     monkeypatch.setattr(bsa, "_torch_calls", other, raising=False)
-    monkeypatch.setattr(kv_cache, "_calls", None)
+    for name in ("_calls", "torch"):                # as they were when this is over: bound later, or bound already
+        monkeypatch.setattr(kv_cache, name, None if name == "_calls" else kv_cache.torch)
     with pytest.warns(UserWarning, match="compiled for torch 0.1"):
         kv_cache._bind()
     assert kv_cache._calls is None

@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 
 import block_sparse_flashattention_gb300 as bsa  # noqa: E402
 from oracle import kv_cache as okv  # noqa: E402
-from tests.kv_case import Pool, agree, bf16, expect, f64, lists, pages_for  # noqa: E402
+from tests.kv_case import DT, Pool, agree, bf16, expect, f64, lists, pages_for  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -842,6 +842,35 @@ def test_the_default_streams_handle_is_the_default_stream():
     out, lse = bsa.decode(q, pool.cache, table, n, stream=torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype,G,B", [("e4m3", 2, 3), ("int8", 20, 3), ("e4m3", 4, 40)])
+def test_codes_past_32_bits_of_bytes(dtype, G, B):
+    """A cache with more than 2^31 bytes of codes gives the bits of a small one with the same rows, wherever its pages
+    lie: appended, read back, decoded, behind a prefix (by its own kernel: G = 20, B = 40)."""
+    H, D, page, prefix = 8, 128, 128, 1200
+    lens = [1 + (61 * i) % 300 for i in range(B)]
+    need = pages_for(lens + [prefix], page)
+    small = bsa.alloc_kv_cache(need, H, D, dtype=DT[dtype])
+    large = bsa.alloc_kv_cache((5 << 29) // (H * page * D), H, D, dtype=DT[dtype])
+    rng = np.random.default_rng(190)
+    at = torch.from_numpy(np.concatenate([[large.num_pages - 1 - i for i in range(need // 2)],
+                                          rng.permutation(large.num_pages - need)[:need - need // 2]]).astype(np.int32)).cuda()
+    table, k = torch.zeros((B + 1, -(-prefix // page)), dtype=torch.int32), 0
+    for b, n in enumerate(lens + [prefix]):
+        table[b, :-(-n // page)] = torch.arange(k, k - (-n // page), dtype=torch.int32)
+        k -= -n // page
+    table = table.cuda()
+    total = sum(lens) + prefix
+    x, q = [_q(191 + i, total, H, D) for i in range(2)], _q(193, B, H * G, D)
+    n, cu = _i32(lens + [prefix]), _i32(np.concatenate([[0], np.cumsum(lens + [prefix])]).tolist())
+    got = []
+    for cache, t in ((small, table), (large, at[table.long()])):
+        bsa.kv_append(*x, cache, t, n, cu_seqlens=cu)
+        got.append([*bsa.kv_read(cache, t, cu, total=total), *bsa.decode(q, cache, t[:B], n[:B]),
+                    *bsa.decode_shared_prefix(q, cache, t[B].contiguous(), prefix, t[:B], n[:B])])
+    for a, b in zip(*got):
+        assert a.isfinite().all() and torch.equal(a, b)
 
 
 @pytest.mark.parametrize("dtype", ["e4m3", "int8"])

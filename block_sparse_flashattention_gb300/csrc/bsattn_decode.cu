@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(Ring<D, kCols>::kWarps * 32, Ring<D, kCols>::k
         const int worker = (int)blockIdx.x * kW + warp;
         const volatile long long *pc = piece[warp];
         int seg = start_seg[warp];
-        for (long long begin = start_at[warp]; begin < pc[1]; ++seg) {
+        // (the segments end where the line does, unless a length is changed while the kernel runs)
+        for (long long begin = start_at[warp]; begin < pc[1] && seg < w.sp + w.ss; ++seg) {
             const Seg s = segment(p, w, seg);
             int n = p.prefix_len, g;
             ListRow lr = {};

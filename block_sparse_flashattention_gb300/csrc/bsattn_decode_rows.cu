@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(bar(2 * C::kStages), kConsumers);
         misc->abort = 0;
+        misc->start_seg = w.ss;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -497,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A window of 32 segments, one per lane; x counts tiles from the window's first.
         int seg0 = misc->start_seg;
         long long x = misc->start_off, pos = lo;
-        while (ok && pos < hi) {
+        // (the segments end where the line does, unless a length is changed while the kernel runs)
+        while (ok && pos < hi && seg0 < w.ss) {
             const int ws = seg0 + lane;
             int n = 0, nt = 0;
             ListRow r = {};

@@ -18,9 +18,11 @@
 // log2 l.  The reference m is moved only when some weight could pass 2^15.
 //
 // A weight below 2^-32 of the largest is 0 in fp16, which is enough while the value scales lie
-// within 2^12 of each other.  From the first tile on where they do not, the weights of P V'
+// within 2^13 of each other.  From the first tile on where they do not, the weights of P V'
 // carry them as in bsattn_decode.cu: V' = fp16(code) fp16(vs 2^(6 - f)), p_j = 2^(c t_j + f - E -
-// u + 7) with a reference u of their own, out = O 2^(u - m + E - 6) / l.
+// u + 7) with a reference u of their own, out = O 2^(u - m + E - 6) / l.  A call where every
+// tile does so takes 1.5 to 1.8 (64 and 128 rows) or 2.4 to 2.7 times (512) as long; the limit
+// leaves out a first token whose values are 2^8 smaller than the others', as models learn it.
 //
 // A segment is (KV head, 256 query rows): two 128-row tiles ("slots") that share each
 // K/V tile.  With 128 rows or fewer both slots hold the same rows and take the key tiles
@@ -29,7 +31,7 @@
 // SMs; each part (fp32 output and LSE per slot row) goes to the workspace for the join.
 //
 // Measured (8 heads, D = 128, 32768 prefix keys, own keys of one token; us a call, launches and
-// join within): 512 rows a head e4m3 78, int8 94 (the products alone take 35 at 1958 TFLOP/s);
+// join within): 512 rows a head e4m3 77, int8 92 (the products alone take 35 at 1958 TFLOP/s);
 // 128 rows int8 46.  A 128-key tile of 256 rows takes 5000 to 5500 cycles, 2048 of them in the
 // tensor pipe: each slot's chain of S, softmax (3000 to 3800 cycles, the schedulers shared
 // with the widening warps) and P V bounds it.  The first S is there 15000 cycles after the
@@ -77,7 +79,7 @@ constexpr int kLeastExp = 7;
 // Binary exponents by which a scale may lie below the largest and share its factor.  Keys:
 // codes (multiples of 2^-9 in e4m3, of 1 in int8) times 2^(6 - 14) are exact in fp16.  Values:
 // so far below E, and so much may E grow within a segment, before the weights carry the scales.
-constexpr int kNearKeys = 14, kNearValues = 8, kGrowth = 4;
+constexpr int kNearKeys = 14, kNearValues = 10, kGrowth = 3;
 
 // log2 of the largest weight when the reference moves, and how far it may grow before it does again.
 constexpr float kLift = 7.f, kReach = 8.f;

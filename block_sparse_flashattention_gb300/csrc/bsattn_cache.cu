@@ -13,11 +13,11 @@
 // is found once, D / 8 lanes hold a row (16 bytes of bf16 or 8 of codes each), and all
 // loads of the 8 K and 8 V rows go out before the first is used.
 //
-// Measured, against 6.7 TB/s of a plain copy: 61440 tokens x 24 heads x 128 (int8) appended
-// in 184 us, 6.2 TB/s; the same (e4m3) read in 167 us, 6.8 TB/s; 8 sequences of 100 .. 4096
-// tokens, 16 heads, appended in 37 us, 6.0 TB/s, read (D = 64, pages of 16) in 16.4 us, in
-// part from L2.  One token each for 8 sequences: 3.2 us, the launch and three dependent
-// loads (offsets, page, rows).
+// Measured, each call on other memory than the one before, against 6.7 TB/s of a plain copy:
+// 61440 tokens x 24 heads x 128 (int8) appended in 184 us, 6.2 TB/s; the same (e4m3) read in
+// 168 us, 6.8 TB/s; 8 sequences of 100 .. 4096 tokens, 16 heads, appended in 39.6 us, 5.7 TB/s,
+// read (D = 64, pages of 16) in 19.1 us.  One token each for 8 sequences: 3.3 us, the launch
+// and three dependent loads (offsets, page, rows).
 #include "bsattn_internal.h"
 #include "kv_codes.cuh"
 #include "sm100_ptx.cuh"

@@ -16,12 +16,14 @@
 // are, and 2^7 of headroom keeps full precision down to 2^-21 of that.
 //
 // Bound by HBM: 2 (D + 4) bytes per key and KV head, 4 D flop per query on it.  Measured
-// (D = 128): 131072 keys x 32 heads (e4m3) 175 us, 6.3 TB/s of 6.7; 64 sequences of 100 ..
-// 4096 keys x 8 heads, 4 queries a head (int8) 56 us, 5.1 TB/s: 5 us until the first codes
+// (D = 128, each call on other memory than the one before): 131072 keys x 32 heads (e4m3)
+// 177 us, 6.2 TB/s of 6.7; 64 sequences of 100 .. 4096 keys x 8 heads, 4 queries a head (int8)
+// 57.5 us, 4.9 TB/s: 5 us until the first codes
 // arrive (the look-up of the pieces 2, of the pages 1), 6 to 8 us from the first warp that is
 // done to the last (the SMs do not reach HBM equally fast, and pieces handed out as warps come
 // free cost more than they save), 3 us for the join.  2 sequences of 1024 keys x 4 heads:
-// 8.2 us, the latencies of the two launches.
+// 8.6 to 9.7 us, the latencies of the two launches.  Times beside the rules below are of calls
+// in a graph over the same memory, which for small ones lies in L2.
 //
 // Work split.  Every warp is a worker of its own.  A segment is one (sequence, KV head),
 // or one KV head of the prefix while at most 16 query rows a head meet it (more take

@@ -11,8 +11,8 @@
 // bsattn_decode.cu.  With the swizzled rows none of the 16-byte shared-memory loads meets
 // a bank twice (the 8-byte loads of V at D = 64 do, two ways).
 //
-// Bound by the issue of mma.sync and of the widening before it, not by HBM (us a call, e4m3,
-// D = 128): 16 sequences of 8192 keys, 2 heads, G = 17 or 32: 39 us, 1.8 TB/s, G = 128: 104 us;
+// Bound by the issue of mma.sync and of the widening before it, not by HBM (us a call in a
+// graph over the same memory, e4m3, D = 128): 16 sequences of 8192 keys, 2 heads, G = 17 or 32: 39 us, 1.8 TB/s, G = 128: 104 us;
 // 2 sequences of 65536 keys, 8 heads, G = 32: 103 us, 2.7 TB/s, G = 128: 314 us, 219 TFLOP/s.
 //
 // 288 threads: warp 8 looks up lists and pages, 32 at a time, and keeps the ring full;

@@ -30,8 +30,8 @@
 // products of the other.  The line of all segments' 128-key tiles is cut evenly over the
 // SMs; each part (fp32 output and LSE per slot row) goes to the workspace for the join.
 //
-// Measured (8 heads, D = 128, 32768 prefix keys, own keys of one token; us a call, launches and
-// join within): 512 rows a head e4m3 77, int8 92 (the products alone take 35 at 1958 TFLOP/s);
+// Measured (8 heads, D = 128, 32768 prefix keys, own keys of one token; us a call in a
+// graph, launches and join within): 512 rows a head e4m3 77, int8 94 (the products alone take 35 at 1958 TFLOP/s);
 // 128 rows int8 46.  A 128-key tile of 256 rows takes 5000 to 5500 cycles, 2048 of them in the
 // tensor pipe: each slot's chain of S, softmax (3000 to 3800 cycles, the schedulers shared
 // with the widening warps) and P V bounds it.  The first S is there 15000 cycles after the
@@ -219,9 +219,9 @@ __device__ __forceinline__ void softmax_role(const DecodeParams &p, const Plan &
             // what a score of S is worth in units of log2; above 0: a masked key's -inf stays -inf
             const float ct = fmaxf(c * scale_down(info.y), 0x1p-126f);
             // Int8 tiles take the general way, whose two passes are rolled: 512 rows by 32768 keys,
-            // 8 heads, own keys of one token, 94 us a call against 107 with the passes unrolled
+            // 8 heads, own keys of one token, 94 us a call against 102 with the passes unrolled
             // (the roles' loops share the instruction caches).  E4m3 tiles with power-of-two scales
-            // take the short one, its second pass with loads ahead: 78 us against 96.
+            // take the short one, its second pass with loads ahead: 77 us against 95.
             wide = info.w != 0;
             const bool plain = !kInt8 && !masked && !wide && info.z == 0;
             // 32 scores of columns 32 q .. times r; -inf where a key does not count
@@ -616,7 +616,7 @@ __device__ __forceinline__ void widen_role(const DecodeParams &p, const Plan &w,
                 return;
             uint8_t *tile = smem + dst + st * C::kTileBytes;
             const bool whole = keep == 0xffffffffu;
-            // two steps at a time: 94 us as above, 96 with all eight unrolled
+            // two steps at a time: 94 us as above, 95 with all eight unrolled
 #pragma unroll 2
             for (int i = 0; i < kSteps; ++i) {
                 uint4 x = *reinterpret_cast<const uint4 *>(raw + i * kRows * D);

@@ -23,8 +23,13 @@ constexpr int kBlockRows = 256;    // query rows of a segment in the prefix kern
 enum PrefixMode { kNoPrefix = 0, kInLine = 1, kOwnKernel = 2, kEach = 3 };
 
 // Cache bytes that all sequences together may read of the prefix under kEach.  Measured
-// (e4m3, D = 128, own keys of 1 to 200, us a call, kEach against the prefix kernel): 17 MB
-// 14.2 : 18.9, 41 MB 18.2 : 20.1, 68 MB 17.9 : 18.8, 135 MB 28.7 : 20.4, 270 MB 42 : 31.
+// (own keys of 100 tokens, us a call, kEach against the prefix kernel; int8 within 1.5 us):
+//                                            17 MB        41 MB        68 MB        135 MB
+//   32 sequences, 8 heads, G = 1, D = 128     11.3 : 14.9  14.4 : 15.5  17.8 : 16.2  26.5 : 19.4
+//   G = 4                                     12.1 : 15.8  15.4 : 16.5  18.8 : 17.4  27.4 : 22.6
+//   G = 16                                    19.3 : 21.7  22.5 : 28.1  26.0 : 29.7  34.9 : 30.3
+//   64 sequences, 4 heads, G = 8, D = 64      12.6 : 14.5  16.3 : 16.0  20.3 : 20.3  29.2 : 21.0
+//   128 sequences, 8 heads, G = 4, D = 128    19.1 : 29.8  21.6 : 30.0  25.3 : 30.3  33.8 : 30.6
 constexpr long long kEachBytes = 76ll << 20;
 
 // What the prefix kernel pays for a segment, in tiles: query rows, the first tiles' latency,

@@ -1,8 +1,7 @@
 """The paged 8-bit K/V cache and the attention of single query tokens over it.
 
 ``kv_append`` quantises new K and V rows into a cache's pages, ``kv_read`` reads
-them back as packed bf16 rows (what ``forward`` takes, for a prefill that follows
-cached context), ``decode`` attends one query token per sequence over them, and
+them back as packed bf16 rows (what ``forward`` takes), ``decode`` attends one query token per sequence over them, and
 ``decode_shared_prefix`` does so for a batch behind one common prefix.  These are
 calls of the C functions of the same names (bsattn_*, include/bsattn.h, where the
 formats and faults are described) with torch checks and allocations around them.
@@ -11,8 +10,10 @@ formats and faults are described) with torch checks and allocations around them.
     bsa.kv_append(k, v, cache, page_table, seqlens)             # k, v [B, H, D]: a token each
     out, lse = bsa.decode(q, cache, page_table, seqlens)        # q [B, Hq, D]
 
-Work is queued on ``stream`` (the current stream of the cache's device when None);
-outputs and workspaces that a call allocates belong to that stream.  Device faults
+Work is queued on ``stream`` (a torch stream or its handle; the current stream of the
+cache's device when None); outputs and workspaces that a call allocates belong to that
+stream, and tensors that come from another one are the caller's to keep until the work is
+done.  Device faults
 (a page outside the cache, lengths that do not fit) set FLAG_* bits in ``err_flag``.
 """
 from __future__ import annotations
@@ -210,7 +211,12 @@ def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=Non
     b's positions 0, 1, ... in rows cu_seqlens[b] .. cu_seqlens[b+1] (int32 [B+1]).
 
     total: rows to allocate when k and v are not given (cu_seqlens[-1], which lives on
-    the device); rows outside every sequence are not written."""
+    the device); rows outside every sequence are not written.
+
+    A causal prefill of new tokens over cached context: ``forward`` counts query positions
+    from 0 in every sequence, so give it query rows for the context's positions too (of any
+    content) and list nothing for their Q tiles; repeat k and v along their heads
+    (repeat_interleave) where query heads are grouped."""
     if _calls is not None and stream is None and err_flag is None and k is None and v is None:
         got = _calls.kv_read(cache.at, cache.index, page_table, cu_seqlens, total)
         if got is not None:
@@ -381,7 +387,8 @@ def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_
     """``decode`` for a batch whose sequences all begin with one prefix of prefix_len
     cached tokens, in the pages prefix_table (int32 [pages]); page_table and seqlens
     (and meta, kv_valid_len) describe what each sequence has after it.  page_table may
-    be None when no sequence has keys of its own.  The prefix is read once for all."""
+    be None when no sequence has keys of its own.  The prefix is read from HBM once for all;
+    a long one is also worked on once for all."""
     if prefix_table is None:
         raise ValueError("prefix_table is needed (decode attends sequences without a prefix)")
     if _calls is not None and workspace is not None and stream is None and out is None and lse is None and \

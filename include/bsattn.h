@@ -504,7 +504,10 @@ bsattn_status bsattn_kv_append(const void *k, const void *v, int64_t k_stride, i
  * bsattn_fwd takes: rows cu_seqlens[b] .. cu_seqlens[b+1] of k and v receive
  * positions 0, 1, ... of sequence b, each element code * scale in fp32, rounded to
  * bf16 (to nearest even).  Rows with a power-of-two scale, as e4m3 rows have, are
- * read back exactly.
+ * read back exactly.  For a causal prefill of new tokens over cached context: bsattn_fwd
+ * counts query positions from 0 in every sequence, so q takes rows for the context's
+ * positions too (of any content), whose Q tiles list nothing; and it has one KV head per
+ * query head, so that K and V of grouped heads are repeated first.
  *
  * k, v         device bf16 [total, H, D], contiguous, 16-byte aligned (written).
  * total        rows of k and v (0: they may be NULL); rows outside every sequence's

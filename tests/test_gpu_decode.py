@@ -923,6 +923,36 @@ def test_a_serving_run(dtype):
     assert (dl[0] - lse[0]).abs().max() <= tol
 
 
+def test_new_tokens_over_cached_context():
+    """What kv_read's documentation says of a causal prefill over cached context: query rows for the context's positions
+    too, whose Q tiles list nothing, and K and V repeated for grouped heads."""
+    H, G, D, page, context, new = 2, 2, 64, 32, [300, 128], [90, 200]
+    lens = [a + b for a, b in zip(context, new)]
+    pool = Pool(196, pages_for(lens, page), H, D, page, "e4m3")
+    ht, table = pool.tables(lens)
+    cu = _i32(np.concatenate([[0], np.cumsum(lens)]).tolist())
+    k, v = (x.repeat_interleave(G, 1) for x in bsa.kv_read(pool.cache, table, cu, total=sum(lens)))
+    q = _q(197, sum(lens), H * G, D)
+    nb = [-(-n // 128) for n in lens]
+    meta = bsa.alloc_meta(2, H * G, varlen=True, total_m_blocks=sum(nb), total_n_blocks=sum(n * n for n in nb), max_num_n=max(nb))
+    block_map = torch.cat([torch.ones((H * G, n, n), dtype=torch.uint8).index_fill_(1, torch.arange(c // 128), 0).flatten(1)
+                           for n, c in zip(nb, context)], 1).cuda()
+    args = dict(cu_seqlens_q=cu, cu_seqlens_k=cu, kind=bsa.MASK_CAUSAL)
+    bsa.build_meta(block_map, meta, seqlen_q=sum(lens), seqlen_k=sum(lens), **args)
+    out, lse = bsa.forward(q, k, v, meta, out_dtype=torch.float32, **args)
+    x = f64(q)
+    for b, n in enumerate(lens):
+        at = int(cu[b])
+        assert not out[at:at + context[b] // 128 * 128].any()           # the context's tiles were left out
+        for i in sorted({context[b], context[b] + 1, n - 50, n - 1}):
+            for h in range(H * G):
+                o, l, _ = okv.attend(x[at + i, h], pool.host("k", ht[b], h // G, range(i + 1)),
+                                     pool.host("v", ht[b], h // G, range(i + 1)), 1 / math.sqrt(D))
+                # a weight is rounded to bf16, by at most 2^-8 of itself, and the weights sum to 1
+                assert np.all(np.abs(f64(out[at + i, h]) - o) <= 2.0 ** -8 * np.max(np.abs(pool.host("v", ht[b], h // G, range(i + 1)))))
+                assert abs(float(lse[h, at + i]) - l) <= 1e-4
+
+
 @pytest.mark.parametrize("listed", [False, True])
 def test_native_calls_equal_the_marshalled_ones(monkeypatch, listed):
     """The native form of the calls and the ctypes form give the same bits, and refuse the same arguments."""

@@ -568,7 +568,9 @@ bsattn_status bsattn_decode(const void *q, int64_t q_stride, int32_t B, int32_t 
  * given, refer to; the prefix is attended whole).  The prefix's K and V are read from
  * HBM once for all sequences, and, where that is worth a kernel of its own, worked on
  * once for all: many query rows then meet each key.  There, value scales that are not
- * powers of two (int8) cost two more roundings to 11 bits per element of V.
+ * powers of two (int8) cost two more roundings to 11 bits per element of V, and while the
+ * value scales lie within 2^13 of each other (rows of zeros aside) a key with less than
+ * 2^-32 of the largest weight may count as 0.
  *
  * prefix_table device int32 [ceil(prefix_len / page_size)]: the prefix's pages.
  * prefix_len   >= 0 (0: bsattn_decode).  table_cols may be 0: no sequence has keys of

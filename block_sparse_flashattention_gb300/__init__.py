@@ -7,7 +7,8 @@ is the Python face of that C ABI: ``bsattn_build_meta``, ``bsattn_fwd``,
 ``bsattn_bwd`` and the rest carry the C names and only marshal arguments;
 ``alloc_meta``, ``build_meta``, ``forward`` and ``backward`` add torch
 allocation of the outputs around them, and so do, for serving, ``alloc_kv_cache``,
-``kv_append``, ``kv_read``, ``decode`` and ``decode_shared_prefix`` (kv_cache.py).
+``kv_append``, ``kv_read``, ``decode``, ``decode_shared_prefix``, ``prefill``, ``kv_weigh`` and
+``kv_evict`` (kv_cache.py).
 PyTorch provides device memory and streams only.
 """
 from __future__ import annotations
@@ -21,20 +22,22 @@ from ._binding import (BSATTN_ERR_CAPACITY, BSATTN_ERR_CUDA, BSATTN_ERR_INVALID_
                        MASK_CAUSAL, MASK_DOCUMENT, MASK_NONE, MASK_PREFIX, MASK_SLIDING_WINDOW,
                        OUT_BF16, OUT_F32,
                        bsattn_decode, bsattn_decode_shared_prefix, bsattn_decode_workspace_size,
-                       bsattn_kv_append, bsattn_kv_cache, bsattn_kv_read,
+                       bsattn_kv_append, bsattn_kv_cache, bsattn_kv_evict, bsattn_kv_read, bsattn_kv_weigh,
+                       bsattn_prefill, bsattn_prefill_workspace_size,
                        BsattnError, MaskParams, Meta, bsattn_abi_version, bsattn_build_meta,
                        bsattn_build_meta_bitmask, bsattn_build_meta_blocks, bsattn_build_meta_bsr,
                        bsattn_fwd_proxy, bsattn_kv_summaries, bsattn_bwd, bsattn_bwd_workspace_size,
                        bsattn_fwd, bsattn_fwd_static_scratch, bsattn_fwd_workspace_size,
                        bsattn_testing_set_wait_limit, library, status_string)
 
-from .kv_cache import (KVCache, alloc_decode_workspace, alloc_kv_cache, decode, decode_shared_prefix,
-                       kv_append, kv_read)
+from .kv_cache import (KVCache, alloc_decode_workspace, alloc_kv_cache, alloc_kv_weights, alloc_prefill_workspace,
+                       decode, decode_shared_prefix, kv_append, kv_evict, kv_read, kv_weigh, prefill)
 
 TILE = 128
 
 __all__ = ["KVCache", "alloc_kv_cache", "alloc_decode_workspace", "kv_append", "kv_read", "decode",
-           "decode_shared_prefix", "bsattn_kv_append", "bsattn_kv_read", "bsattn_decode",
+           "decode_shared_prefix", "prefill", "alloc_prefill_workspace", "kv_weigh", "kv_evict", "alloc_kv_weights",
+           "bsattn_prefill", "bsattn_prefill_workspace_size", "bsattn_kv_weigh", "bsattn_kv_evict", "bsattn_kv_append", "bsattn_kv_read", "bsattn_decode",
            "bsattn_decode_shared_prefix", "bsattn_decode_workspace_size", "bsattn_kv_cache", "KV_E4M3", "KV_INT8",
            "bsattn_bwd", "bsattn_bwd_workspace_size", "backward", "bsattn_fwd_proxy", "bsattn_kv_summaries", "bsattn_build_meta", "bsattn_build_meta_bitmask", "bsattn_build_meta_blocks", "bsattn_build_meta_bsr", "bsattn_fwd", "bsattn_fwd_static_scratch", "bsattn_fwd_workspace_size", "bsattn_abi_version", "bsattn_testing_set_wait_limit",
            "alloc_meta", "alloc_workspace", "build_meta",

@@ -131,6 +131,17 @@ def library() -> ctypes.CDLL:
         lib.bsattn_decode_shared_prefix.restype = ctypes.c_int
         lib.bsattn_decode_workspace_size.argtypes = [cache, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
         lib.bsattn_decode_workspace_size.restype = ctypes.c_int
+        mask = ctypes.POINTER(bsattn_mask_params)
+        lib.bsattn_prefill.argtypes = [vp, i64, i32, i32, i32, vp, cache, vp, i32, i32, vp, i64, ctypes.c_int, mask,
+                                       ctypes.c_float, vp, ctypes.c_int, vp, vp, ctypes.c_size_t, vp, vp]
+        lib.bsattn_prefill.restype = ctypes.c_int
+        lib.bsattn_prefill_workspace_size.argtypes = [cache, i32, i32, i32, i64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.bsattn_prefill_workspace_size.restype = ctypes.c_int
+        lib.bsattn_kv_weigh.argtypes = [vp, i64, vp, i32, i32, i32, vp, cache, vp, i32, vp, i32, i32, vp, ctypes.c_int,
+                                        mask, ctypes.c_float, vp, vp]
+        lib.bsattn_kv_weigh.restype = ctypes.c_int
+        lib.bsattn_kv_evict.argtypes = [cache, vp, vp, i32, i32, vp, i32, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp]
+        lib.bsattn_kv_evict.restype = ctypes.c_int
         lib.bsattn_status_string.argtypes = [ctypes.c_int]
         lib.bsattn_status_string.restype = ctypes.c_char_p
         lib.bsattn_abi_version.argtypes = []
@@ -403,6 +414,49 @@ def bsattn_decode_workspace_size(cache: bsattn_kv_cache, B: int, Hq: int, prefix
     if st != BSATTN_OK:
         raise BsattnError(st, "bsattn_decode_workspace_size")
     return int(n.value)
+
+
+def bsattn_prefill(q, q_stride: int, total: int, B: int, Hq: int, cu_seqlens, cache: bsattn_kv_cache, page_table,
+                   table_stride: int, table_cols: int, seqlens, keys: int, kind: int,
+                   mask_params: Optional[MaskParams], softmax_scale: float, out, out_dtype: int, lse, workspace,
+                   workspace_bytes: int = 0, err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    mp = mask_params.to_c() if mask_params is not None else None
+    if workspace is not None and not isinstance(workspace, int) and workspace_bytes == 0:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return library().bsattn_prefill(
+        _ptr(q), q_stride, total, B, Hq, _ptr(cu_seqlens), cache, _ptr(page_table), table_stride, table_cols,
+        _ptr(seqlens), keys, kind, ctypes.byref(mp) if mp is not None else None, softmax_scale, _ptr(out), out_dtype,
+        _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(err_flag), _stream(stream))
+
+
+def bsattn_prefill_workspace_size(cache: bsattn_kv_cache, total: int, B: int, Hq: int, keys: int) -> int:
+    """Bytes of workspace a prefill call with these sizes needs."""
+    n = ctypes.c_size_t(0)
+    st = library().bsattn_prefill_workspace_size(cache, total, B, Hq, keys, ctypes.byref(n))
+    if st != BSATTN_OK:
+        raise BsattnError(st, "bsattn_prefill_workspace_size")
+    return int(n.value)
+
+
+def bsattn_kv_weigh(q, q_stride: int, lse, total: int, B: int, Hq: int, cu_seqlens, cache: bsattn_kv_cache, weights,
+                    accumulate: int, page_table, table_stride: int, table_cols: int, seqlens, kind: int,
+                    mask_params: Optional[MaskParams], softmax_scale: float, err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    mp = mask_params.to_c() if mask_params is not None else None
+    return library().bsattn_kv_weigh(
+        _ptr(q), q_stride, _ptr(lse), total, B, Hq, _ptr(cu_seqlens), cache, _ptr(weights), accumulate,
+        _ptr(page_table), table_stride, table_cols, _ptr(seqlens), kind, ctypes.byref(mp) if mp is not None else None,
+        softmax_scale, _ptr(err_flag), _stream(stream))
+
+
+def bsattn_kv_evict(cache: bsattn_kv_cache, weights, page_table, table_stride: int, table_cols: int, seqlens, B: int,
+                    keep: int, recent: int, sinks: int, out_table, out_stride: int, out_cols: int, kept, lens,
+                    err_flag=None, stream=None) -> int:
+    """Forwards to the C function of the same name; returns its status code."""
+    return library().bsattn_kv_evict(
+        cache, _ptr(weights), _ptr(page_table), table_stride, table_cols, _ptr(seqlens), B, keep, recent, sinks,
+        _ptr(out_table), out_stride, out_cols, _ptr(kept), _ptr(lens), _ptr(err_flag), _stream(stream))
 
 
 def bsattn_abi_version() -> int:

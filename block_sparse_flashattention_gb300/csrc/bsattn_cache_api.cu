@@ -1,6 +1,6 @@
-// C-ABI entry points of the paged 8-bit K/V cache and the attention of single
-// query tokens over it: host-side validation and launches.  Nothing here
-// allocates device memory or synchronises with the device.
+// C-ABI entry points of the paged 8-bit K/V cache, the attention of single query tokens and
+// of chunks over it, the weights of its keys and their eviction: host-side validation and
+// launches.  Nothing here allocates device memory or synchronises with the device.
 #include <cmath>
 #include <cstdint>
 
@@ -120,6 +120,59 @@ bsattn_status decode_impl(const void *q, int64_t q_stride, int32_t B, int32_t Hq
     return e == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
+// The mask kinds that positions in a cache define (document ids belong to packed rows).
+bsattn_status check_kind(bsattn_mask_kind kind, const bsattn_mask_params *mp) {
+    switch (kind) {
+    case BSATTN_MASK_NONE:
+    case BSATTN_MASK_CAUSAL: return BSATTN_OK;
+    case BSATTN_MASK_SLIDING_WINDOW:
+        return mp && mp->window_left >= 0 && mp->sink_tokens >= 0 ? BSATTN_OK : BSATTN_ERR_INVALID_ARG;
+    case BSATTN_MASK_PREFIX: return mp && mp->prefix_len >= 0 ? BSATTN_OK : BSATTN_ERR_INVALID_ARG;
+    case BSATTN_MASK_DOCUMENT: return BSATTN_ERR_UNSUPPORTED;
+    }
+    return BSATTN_ERR_INVALID_ARG;
+}
+
+// What bsattn_prefill and bsattn_kv_weigh have in common; fills *p.
+bsattn_status chunk_params(const void *q, int64_t q_stride, int32_t total, int32_t B, int32_t Hq,
+                           const int32_t *cu_seqlens, const bsattn_kv_cache *cache, const int32_t *page_table,
+                           int32_t table_stride, int32_t table_cols, const int32_t *seqlens,
+                           bsattn_mask_kind kind, const bsattn_mask_params *mp, float softmax_scale,
+                           int32_t *err_flag, bsattn::ChunkParams *p) {
+    bsattn_status st = check_cache(cache);
+    if (st != BSATTN_OK) return st;
+    if (B <= 0 || total < 0 || (!cu_seqlens && total != B) || Hq <= 0 || Hq % cache->H) return BSATTN_ERR_INVALID_ARG;
+    if (Hq / cache->H > 128) return BSATTN_ERR_UNSUPPORTED;
+    // B * H and total * Hq number segments and rows in 32 bits
+    if ((long long)B * cache->H > INT32_MAX / 2 || (long long)total * Hq > INT32_MAX) return BSATTN_ERR_INVALID_ARG;
+    if (!seqlens || (total > 0 && !q) || misaligned(q, 16)) return BSATTN_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)Hq * cache->D || q_stride % 8) return BSATTN_ERR_INVALID_ARG;
+    if ((st = check_table(page_table, table_stride, table_cols, cache->page_size, false)) != BSATTN_OK) return st;
+    if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return BSATTN_ERR_INVALID_ARG;
+    if ((st = check_kind(kind, mp)) != BSATTN_OK) return st;
+    p->c = view(cache);
+    p->q = static_cast<const uint16_t *>(q);
+    p->q_stride = q_stride;
+    p->total = total;
+    p->B = B;
+    p->Hq = Hq;
+    p->G = Hq / cache->H;
+    p->cu = cu_seqlens;
+    p->table = page_table;
+    p->table_stride = table_stride;
+    p->table_cols = table_cols;
+    p->seqlens = seqlens;
+    p->kind = kind;
+    if (mp) {
+        p->window_left = mp->window_left;
+        p->sink_tokens = mp->sink_tokens;
+        p->prefix_len = mp->prefix_len;
+    }
+    p->scale_log2 = (float)((double)softmax_scale * 1.4426950408889634074);
+    p->err = err_flag;
+    return BSATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +269,106 @@ bsattn_status bsattn_decode_shared_prefix(const void *q, int64_t q_stride, int32
     return decode_impl(q, q_stride, B, Hq, cache, prefix_table, prefix_len, page_table, table_stride,
                        table_cols, seqlens, meta, kv_valid_len, softmax_scale, out, out_dtype, lse, workspace,
                        workspace_bytes, err_flag, stream);
+}
+
+bsattn_status bsattn_prefill_workspace_size(const bsattn_kv_cache *cache, int32_t total, int32_t B, int32_t Hq,
+                                            int64_t keys, size_t *bytes) {
+    if (!bytes) return BSATTN_ERR_INVALID_ARG;
+    *bytes = 0;
+    bsattn_status st = check_cache_shape(cache);
+    if (st != BSATTN_OK) return st;
+    if (B <= 0 || total < 0 || Hq <= 0 || Hq % cache->H || keys < 0) return BSATTN_ERR_INVALID_ARG;
+    if (Hq / cache->H > 128) return BSATTN_ERR_UNSUPPORTED;
+    if ((long long)B * cache->H > INT32_MAX / 2 || (long long)total * Hq > INT32_MAX || keys > INT64_MAX / (1 << 24))
+        return BSATTN_ERR_INVALID_ARG;
+    *bytes = bsattn::prefill_workspace_bytes(total, B, cache->H, Hq / cache->H, cache->D, keys);
+    return BSATTN_OK;
+}
+
+bsattn_status bsattn_prefill(const void *q, int64_t q_stride, int32_t total, int32_t B, int32_t Hq,
+                             const int32_t *cu_seqlens, const bsattn_kv_cache *cache,
+                             const int32_t *page_table, int32_t table_stride, int32_t table_cols,
+                             const int32_t *seqlens, int64_t keys, bsattn_mask_kind kind,
+                             const bsattn_mask_params *mp, float softmax_scale, void *out,
+                             bsattn_out_dtype out_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                             int32_t *err_flag, void *stream) {
+    bsattn::ChunkParams p = {};
+    bsattn_status st = chunk_params(q, q_stride, total, B, Hq, cu_seqlens, cache, page_table, table_stride, table_cols,
+                                    seqlens, kind, mp, softmax_scale, err_flag, &p);
+    if (st != BSATTN_OK) return st;
+    if (out_dtype != BSATTN_OUT_BF16 && out_dtype != BSATTN_OUT_F32) return BSATTN_ERR_INVALID_ARG;
+    if ((total > 0 && (!out || !lse)) || misaligned(out, 16)) return BSATTN_ERR_INVALID_ARG;
+    if (!workspace || misaligned(workspace, 256)) return BSATTN_ERR_INVALID_ARG;
+    size_t need = 0;
+    if ((st = bsattn_prefill_workspace_size(cache, total, B, Hq, keys, &need)) != BSATTN_OK) return st;
+    if (workspace_bytes < need) return BSATTN_ERR_INVALID_ARG;
+    if (total == 0 && !err_flag) return BSATTN_OK;  // else the offsets are still checked
+    p.out = out;
+    p.out_f32 = out_dtype == BSATTN_OUT_F32 ? 1 : 0;
+    p.lse = lse;
+    p.ws = static_cast<uint8_t *>(workspace);
+    p.keys = keys;
+    const cudaError_t e = bsattn::launch_prefill(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+bsattn_status bsattn_kv_weigh(const void *q, int64_t q_stride, const float *lse, int32_t total, int32_t B, int32_t Hq,
+                              const int32_t *cu_seqlens, const bsattn_kv_cache *cache, float *weights,
+                              int32_t accumulate, const int32_t *page_table, int32_t table_stride,
+                              int32_t table_cols, const int32_t *seqlens, bsattn_mask_kind kind,
+                              const bsattn_mask_params *mp, float softmax_scale, int32_t *err_flag, void *stream) {
+    bsattn::ChunkParams p = {};
+    bsattn_status st = chunk_params(q, q_stride, total, B, Hq, cu_seqlens, cache, page_table, table_stride, table_cols,
+                                    seqlens, kind, mp, softmax_scale, err_flag, &p);
+    if (st != BSATTN_OK) return st;
+    if ((total > 0 && !lse) || !weights || misaligned(weights, 16)) return BSATTN_ERR_INVALID_ARG;
+    p.lse = const_cast<float *>(lse);
+    p.weights = weights;
+    p.accumulate = accumulate ? 1 : 0;
+    const cudaError_t e = bsattn::launch_weigh(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
+}
+
+bsattn_status bsattn_kv_evict(const bsattn_kv_cache *cache, float *weights, const int32_t *page_table,
+                              int32_t table_stride, int32_t table_cols, const int32_t *seqlens, int32_t B,
+                              int32_t keep, int32_t recent, int32_t sinks, const int32_t *out_table,
+                              int32_t out_stride, int32_t out_cols, int32_t *kept, int32_t *lens,
+                              int32_t *err_flag, void *stream) {
+    bsattn_status st = check_cache(cache);
+    if (st != BSATTN_OK) return st;
+    if (B <= 0 || keep <= 0 || recent < 0 || sinks < 0 || sinks > keep || recent > keep - sinks)
+        return BSATTN_ERR_INVALID_ARG;
+    if (!weights || misaligned(weights, 16) || !seqlens || !kept || !lens) return BSATTN_ERR_INVALID_ARG;
+    if ((long long)B * cache->H > INT32_MAX / 2 || keep > INT32_MAX - kTile) return BSATTN_ERR_INVALID_ARG;
+    if ((st = check_table(page_table, table_stride, table_cols, cache->page_size, false)) != BSATTN_OK) return st;
+    bsattn::EvictParams p = {};
+    if (out_table) {
+        if ((st = check_table(out_table, out_stride, out_cols, cache->page_size, false)) != BSATTN_OK) return st;
+        // room for every key that may be kept
+        if (out_cols < table_cols && (long long)out_cols * cache->page_size < keep) return BSATTN_ERR_INVALID_ARG;
+        p.out_table = out_table;
+        p.out_stride = out_stride;
+        p.out_cols = out_cols;
+    } else {
+        p.out_table = page_table;
+        p.out_stride = table_stride;
+        p.out_cols = table_cols;
+    }
+    p.c = view(cache);
+    p.weights = weights;
+    p.table = page_table;
+    p.table_stride = table_stride;
+    p.table_cols = table_cols;
+    p.seqlens = seqlens;
+    p.B = B;
+    p.keep = keep;
+    p.recent = recent;
+    p.sinks = sinks;
+    p.kept = kept;
+    p.lens = lens;
+    p.err = err_flag;
+    const cudaError_t e = bsattn::launch_evict(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BSATTN_OK : BSATTN_ERR_CUDA;
 }
 
 }  // extern "C"

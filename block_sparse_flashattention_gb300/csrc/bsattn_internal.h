@@ -180,6 +180,46 @@ struct DecodeParams {
     uint8_t *ws;
 };
 
+// Queries of each sequence's newest tokens over the cache: attention (out, lse written) or the
+// keys' weights (lse given, weights written).
+struct ChunkParams {
+    CacheView c;
+    const uint16_t *q;             // bf16 [total, Hq, D], q_stride elements between tokens
+    long long q_stride;
+    int total, B, Hq, G;           // G = Hq / H query heads per KV head
+    const int32_t *cu;             // [B + 1], or null: one token per sequence
+    const int32_t *table;
+    int table_stride, table_cols;
+    const int32_t *seqlens;
+    int kind, window_left, sink_tokens, prefix_len;
+    float scale_log2;              // softmax_scale * log2(e)
+    void *out;                     // [total, Hq, D], bf16 or fp32 (out_f32)
+    int out_f32;
+    float *lse;                    // [total, Hq]
+    float *weights;                // [num_pages, H, page_size]
+    int accumulate;
+    int32_t *err;
+    uint8_t *ws;
+    long long keys;                // cached keys that the workspace has room for
+};
+
+struct EvictParams {
+    CacheView c;
+    float *weights;
+    const int32_t *table, *out_table;  // the same: rows move within their pages
+    int table_stride, table_cols, out_stride, out_cols;
+    const int32_t *seqlens;
+    int B, keep, recent, sinks;
+    int32_t *kept;                 // [B, H, keep]
+    int32_t *lens;                 // [B]
+    int32_t *err;
+};
+
+cudaError_t launch_prefill(const ChunkParams &p, cudaStream_t stream);
+size_t prefill_workspace_bytes(int total, int B, int H, int G, int D, long long keys);
+cudaError_t launch_weigh(const ChunkParams &p, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_read(const ReadParams &p, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams &p, cudaStream_t stream);

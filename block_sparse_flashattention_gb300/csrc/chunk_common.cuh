@@ -1,0 +1,67 @@
+// Device code that the kernels for chunks of new tokens share (bsattn_prefill, bsattn_kv_weigh):
+// a sequence's numbers and what a query may meet.
+#pragma once
+
+#include "bsattn_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace bsattn {
+
+// A sequence: its queries are the packed rows first .. first + m - 1, at the positions
+// n - m .. n - 1 of its n keys.  m = 0: nothing is to be done (no token, or faulty numbers).
+struct Chunk {
+    int first, m, n;
+};
+
+// `check`: flag what is faulty: offsets that leave the packed rows or decrease, more new
+// tokens than keys, more keys than the page table's row holds.  A sequence of length 0 or less
+// has no key (n = 0): its queries, if it has any, meet nothing.
+__device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b, bool check) {
+    Chunk s;
+    int end;
+    if (p.cu) {
+        s.first = __ldg(p.cu + b);
+        end = __ldg(p.cu + b + 1);
+    } else {
+        s.first = b;
+        end = b + 1;
+    }
+    const int n = __ldg(p.seqlens + b);
+    s.n = max(n, 0);
+    s.m = 0;
+    const bool rows_ok = s.first >= 0 && end >= s.first && end <= p.total;
+    if (!rows_ok || (n > 0 && (end - s.first > n || n > (p.table_cols << p.c.page_shift)))) {
+        if (check && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
+        return s;
+    }
+    s.m = end - s.first;
+    return s;
+}
+
+// The keys that the query at position i of a sequence of n keys meets: j < hb or la <= j < ha.
+struct Met {
+    int hb, la, ha;
+};
+
+__device__ __forceinline__ Met met(const ChunkParams &p, int i, int n) {
+    Met r = {0, 0, n};
+    if (p.kind == BSATTN_MASK_CAUSAL) {
+        r.ha = min(n, i + 1);
+    } else if (p.kind == BSATTN_MASK_SLIDING_WINDOW) {
+        r.ha = min(n, i + 1);
+        r.la = i + 1 <= p.window_left ? 0 : i + 1 - p.window_left;
+        r.hb = min(r.ha, p.sink_tokens);
+    } else if (p.kind == BSATTN_MASK_PREFIX) {
+        r.ha = min(n, max(p.prefix_len, i + 1));
+    }
+    return r;
+}
+
+// Cache row of position j of sequence b, head h (the first of its page's, plus j mod page), or -1.
+__device__ __forceinline__ long long cache_row(const CacheView &c, const int32_t *table_row, int h, int j) {
+    const int page = __ldg(table_row + (j >> c.page_shift));
+    if (page < 0 || page >= c.num_pages) return -1;
+    return (((long long)page * c.H + h) << c.page_shift) + (j & ((1 << c.page_shift) - 1));
+}
+
+}  // namespace bsattn

@@ -1,14 +1,20 @@
-"""The paged 8-bit K/V cache and the attention of single query tokens over it.
+"""The paged 8-bit K/V cache, the attention of single query tokens and of chunks over it, and its eviction.
 
 ``kv_append`` quantises new K and V rows into a cache's pages, ``kv_read`` reads
 them back as packed bf16 rows (what ``forward`` takes), ``decode`` attends one query token per sequence over them, and
-``decode_shared_prefix`` does so for a batch behind one common prefix.  These are
-calls of the C functions of the same names (bsattn_*, include/bsattn.h, where the
+``decode_shared_prefix`` does so for a batch behind one common prefix, and ``prefill`` for
+chunks of new tokens; ``kv_weigh`` sums the weight that queries give to every key, and
+``kv_evict`` keeps the keys of most weight.  These are calls of the C functions of the same names (bsattn_*, include/bsattn.h, where the
 formats and faults are described) with torch checks and allocations around them.
 
     cache = bsa.alloc_kv_cache(num_pages, H, D)                 # e4m3, pages of 128
     bsa.kv_append(k, v, cache, page_table, seqlens)             # k, v [B, H, D]: a token each
     out, lse = bsa.decode(q, cache, page_table, seqlens)        # q [B, Hq, D]
+
+    bsa.kv_append(k, v, cache, page_table, seqlens, cu_seqlens=cu)          # k, v [total, H, D]: a chunk each
+    out, lse = bsa.prefill(q, cache, page_table, seqlens, cu, keys=keys)    # q [total, Hq, D], keys: sum of seqlens
+    bsa.kv_weigh(q, lse, cache, weights, page_table, seqlens, cu_seqlens=cu)
+    kept, seqlens = bsa.kv_evict(cache, weights, page_table, seqlens, 1024, recent=128)
 
 Work is queued on ``stream`` (a torch stream or its handle; the current stream of the
 cache's device when None); outputs and workspaces that a call allocates belong to that
@@ -22,8 +28,8 @@ import ctypes
 import math
 import warnings
 
-from ._binding import (BSATTN_OK, KV_E4M3, KV_INT8, OUT_BF16, OUT_F32, BsattnError, bsattn_decode_workspace_size,
-                       bsattn_kv_cache, library)
+from ._binding import (BSATTN_OK, KV_E4M3, KV_INT8, MASK_CAUSAL, OUT_BF16, OUT_F32, BsattnError,
+                       bsattn_decode_workspace_size, bsattn_kv_cache, bsattn_prefill_workspace_size, library)
 
 
 def _check(status: int, where: str) -> None:
@@ -162,7 +168,7 @@ def _rows(t, name, H, D, device):
     if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or t.device != device:
         raise ValueError(f"{name} must be a torch.bfloat16 tensor [tokens, {H}, {D}] on the cache's device")
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and H > 1):
+    if t.numel() and (s2 != 1 or (s1 != D and H > 1)):   # strides of an empty tensor say nothing
         raise ValueError(f"{name}'s heads and elements must be contiguous")
     return s0 if t.shape[0] > 1 else H * D
 
@@ -401,3 +407,165 @@ def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_
             raise BsattnError(got, "bsattn_decode_shared_prefix")
     return _decode(q, cache, prefix_table, prefix_len, page_table, seqlens, meta, kv_valid_len, softmax_scale, out,
                    out_dtype, lse, workspace, err_flag, stream)
+
+
+def alloc_prefill_workspace(cache: KVCache, total: int, B: int, Hq: int, keys: int):
+    """Workspace of a ``prefill`` call for `total` query tokens of B sequences, Hq query heads and
+    up to `keys` cached keys of all sequences together.  It can be kept from call to call; two
+    calls that may run at the same time need one each."""
+    return torch.empty(bsattn_prefill_workspace_size(cache.ref, total, B, Hq, keys), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def alloc_kv_weights(cache: KVCache):
+    """Weights of a cache's keys for ``kv_weigh`` and ``kv_evict``: float32 zeros [num_pages, H, page_size]."""
+    return torch.zeros((cache.num_pages, cache.H, cache.page_size), dtype=F32, device=cache.device)
+
+
+def _chunk_checks(q, cache, page_table, seqlens, cu_seqlens):
+    """(token stride of q, row stride of page_table, its columns) of a call with queries of new tokens."""
+    dev = cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, Hq, D]")
+    qs = _rows(q, "q", q.shape[1], cache.D, dev)
+    B = page_table.shape[0]
+    stride, cols = _table(page_table, "page_table", B, dev)
+    _ints(seqlens, "seqlens", 1, dev)
+    if seqlens.shape[0] != B:
+        raise ValueError("seqlens must have one entry per sequence")
+    if cu_seqlens is not None:
+        _ints(cu_seqlens, "cu_seqlens", 1, dev)
+        if cu_seqlens.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must have B + 1 entries")
+    elif q.shape[0] != B:
+        raise ValueError("q must have one token per sequence where no cu_seqlens are given")
+    return qs, stride, cols
+
+
+def _weights(weights, cache):
+    if weights.dtype != F32 or tuple(weights.shape) != tuple(cache.k_scale.shape) or weights.device != cache.device or \
+            not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 [num_pages, H, page_size] tensor on the cache's device")
+
+
+def prefill(q, cache: KVCache, page_table, seqlens, cu_seqlens, *, keys=None, kind: int = MASK_CAUSAL,
+            mask_params=None, softmax_scale=None, out=None, out_dtype=None, lse=None, workspace=None, err_flag=None,
+            stream=None):
+    """Attention of chunks of new tokens over the cache: the packed rows cu_seqlens[b] ..
+    cu_seqlens[b+1] of q (bf16 [total, Hq, D]; tokens may be any multiple of 8 elements apart; Hq
+    a multiple of the cache's heads) are the queries of sequence b's newest tokens, whose K and V
+    ``kv_append`` has written: they have the positions seqlens[b] - n .. seqlens[b] - 1.
+
+    kind, mask_params: which cached keys a query meets, by its position (MASK_NONE, MASK_CAUSAL,
+    MASK_SLIDING_WINDOW, MASK_PREFIX as for ``forward``).  keys: the sum of seqlens (or more), which
+    lives on the device; None: what page_table has room for, which may ask for a large workspace.
+    Returns (out [total, Hq, D] bf16 or out_dtype, lse fp32 [total, Hq]); a query without keys gets
+    0 and -inf, rows outside every sequence are not written.  workspace: see
+    alloc_prefill_workspace; None allocates one for this call."""
+    if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
+        return _elsewhere(cache, stream, lambda: prefill(
+            q, cache, page_table, seqlens, cu_seqlens, keys=keys, kind=kind, mask_params=mask_params,
+            softmax_scale=softmax_scale, out=out, out_dtype=out_dtype, lse=lse, workspace=workspace, err_flag=err_flag))
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is needed (decode attends one token per sequence)")
+    qs, stride, cols = _chunk_checks(q, cache, page_table, seqlens, cu_seqlens)
+    dev, B, (total, Hq, _) = cache.device, page_table.shape[0], q.shape
+    _err(err_flag, dev)
+    if out_dtype not in (None, BF16, F32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    if out is not None and (out.dtype not in (BF16, F32) or (out_dtype is not None and out.dtype != out_dtype) or
+                            out.shape != q.shape or out.device != dev or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous [total, Hq, D] tensor of out_dtype on the cache's device")
+    if lse is not None and (lse.dtype != F32 or tuple(lse.shape) != (total, Hq) or lse.device != dev or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [total, Hq] tensor on the cache's device")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    if keys is None:
+        keys = B * cols * cache.page_size
+    _on_gpu(cache)
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or BF16, device=dev)
+    if lse is None:
+        lse = torch.empty((total, Hq), dtype=F32, device=dev)
+    if workspace is None:
+        workspace = alloc_prefill_workspace(cache, total, B, Hq, keys)
+    _check(_lib.bsattn_prefill(q.data_ptr(), qs, total, B, Hq, cu_seqlens.data_ptr(), cache.ref,
+                               page_table.data_ptr(), stride, cols, seqlens.data_ptr(), keys, kind,
+                               None if mask_params is None else ctypes.byref(mask_params.to_c()),
+                               cache.scale if softmax_scale is None else softmax_scale, out.data_ptr(),
+                               OUT_BF16 if out.dtype is BF16 else OUT_F32, lse.data_ptr(), workspace.data_ptr(),
+                               workspace.nbytes, None if err_flag is None else err_flag.data_ptr(),
+                               _raw_stream(cache.index)), "bsattn_prefill")
+    return out, lse
+
+
+def kv_weigh(q, lse, cache: KVCache, weights, page_table, seqlens, *, cu_seqlens=None, accumulate: bool = True,
+             kind: int = MASK_CAUSAL, mask_params=None, softmax_scale=None, err_flag=None, stream=None):
+    """Adds to weights (float32 [num_pages, H, page_size], see alloc_kv_weights), for every cached key
+    of every sequence and KV head, the attention weight exp(s - lse) that the given queries give to
+    it, summed over them and over the query heads of the KV head, and returns weights.
+
+    q, lse: queries and the lse that ``decode`` (cu_seqlens None: one token per sequence, q [B, Hq, D])
+    or ``prefill`` (with cu_seqlens) returned for them; fewer of a sequence's newest tokens do too, so
+    that the last ones of a prompt say what it needs.  kind, mask_params, softmax_scale as in that call
+    (a single newest token meets every key under MASK_CAUSAL).  accumulate False: the weights of the
+    sequences' keys are set instead, to 0 where no query meets a key.  A page's weights are the
+    caller's to set to 0 when it is handed out."""
+    if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
+        return _elsewhere(cache, stream, lambda: kv_weigh(
+            q, lse, cache, weights, page_table, seqlens, cu_seqlens=cu_seqlens, accumulate=accumulate, kind=kind,
+            mask_params=mask_params, softmax_scale=softmax_scale, err_flag=err_flag))
+    qs, stride, cols = _chunk_checks(q, cache, page_table, seqlens, cu_seqlens)
+    dev, B, (total, Hq, _) = cache.device, page_table.shape[0], q.shape
+    if lse.dtype != F32 or tuple(lse.shape) != (total, Hq) or lse.device != dev or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [tokens, Hq] tensor on the cache's device")
+    _weights(weights, cache)
+    _err(err_flag, dev)
+    _on_gpu(cache)
+    _check(_lib.bsattn_kv_weigh(q.data_ptr(), qs, lse.data_ptr(), total, B, Hq,
+                                None if cu_seqlens is None else cu_seqlens.data_ptr(), cache.ref, weights.data_ptr(),
+                                1 if accumulate else 0, page_table.data_ptr(), stride, cols, seqlens.data_ptr(), kind,
+                                None if mask_params is None else ctypes.byref(mask_params.to_c()),
+                                cache.scale if softmax_scale is None else softmax_scale,
+                                None if err_flag is None else err_flag.data_ptr(), _raw_stream(cache.index)),
+           "bsattn_kv_weigh")
+    return weights
+
+
+def kv_evict(cache: KVCache, weights, page_table, seqlens, keep: int, *, recent: int = 0, sinks: int = 0,
+             out_table=None, err_flag=None, stream=None):
+    """Bounds every sequence of more than `keep` keys to `keep`: per KV head its first `sinks` and its
+    newest `recent` keys stay, and of the others those of largest weight (equal ones: the first;
+    NaN counts as the largest).  Their rows (codes, scales, weights) move, in the order of their
+    positions, to the positions 0, 1, ... of the sequence.
+
+    out_table None: within the sequence's own pages; the weights of the positions given up become 0.
+    The pages that are moved must not be another sequence's too.  Else int32 [B, pages]: to these
+    other pages, for every sequence, short ones whole; page_table's pages are only read, so that
+    several sequences may share them.  Returns (kept int32 [B, H, keep]: the positions that stay, -1
+    behind the last; lens int32 [B]: the keys that the sequences have now)."""
+    if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
+        return _elsewhere(cache, stream, lambda: kv_evict(cache, weights, page_table, seqlens, keep, recent=recent,
+                                                          sinks=sinks, out_table=out_table, err_flag=err_flag))
+    dev, B = cache.device, page_table.shape[0]
+    _weights(weights, cache)
+    stride, cols = _table(page_table, "page_table", B, dev)
+    _ints(seqlens, "seqlens", 1, dev)
+    if seqlens.shape[0] != B:
+        raise ValueError("seqlens must have one entry per sequence")
+    out_stride = out_cols = 0
+    if out_table is not None:
+        out_stride, out_cols = _table(out_table, "out_table", B, dev)
+    if keep <= 0 or recent < 0 or sinks < 0 or recent + sinks > keep:
+        raise ValueError("keep must be positive and hold recent and sinks")
+    _err(err_flag, dev)
+    _on_gpu(cache)
+    kept = torch.empty((B, cache.H, keep), dtype=I32, device=dev)
+    lens = torch.empty((B,), dtype=I32, device=dev)
+    _check(_lib.bsattn_kv_evict(cache.ref, weights.data_ptr(), page_table.data_ptr(), stride, cols,
+                                seqlens.data_ptr(), B, keep, recent, sinks,
+                                None if out_table is None else out_table.data_ptr(), out_stride, out_cols,
+                                kept.data_ptr(), lens.data_ptr(), None if err_flag is None else err_flag.data_ptr(),
+                                _raw_stream(cache.index)), "bsattn_kv_evict")
+    return kept, lens

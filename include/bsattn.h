@@ -2,8 +2,9 @@
  * bsattn -- block-sparse attention for NVIDIA GB300 (sm_103a): metadata from a
  * block map (byte map, bitmask, BSR or coarse blocks), the forward (exact, or
  * with proxy compensation), and the backward of the exact forward; for serving, a
- * paged 8-bit K/V cache (append, read back) and the attention of single query
- * tokens over it, alone or behind a prefix that the batch shares.
+ * paged 8-bit K/V cache (append, read back), the attention of single query
+ * tokens over it, alone or behind a prefix that the batch shares, and of chunks of
+ * new tokens, the weights that queries give to its keys, and eviction by weight.
  *
  * C ABI.  Every pointer argument is caller-owned memory; the library allocates
  * nothing and keeps no state between calls.  Device pointers must be CUDA
@@ -593,6 +594,111 @@ bsattn_status bsattn_decode_shared_prefix(const void *q, int64_t q_stride, int32
  */
 bsattn_status bsattn_decode_workspace_size(const bsattn_kv_cache *cache, int32_t B, int32_t Hq,
                                            int32_t prefix_len, size_t *bytes);
+
+/*
+ * bsattn_prefill -- attention of a chunk of new tokens per sequence over a paged 8-bit cache.
+ * Sequence b's queries are the packed rows cu_seqlens[b] .. cu_seqlens[b+1] of q (n of them);
+ * they have the positions i = seqlens[b] - n .. seqlens[b] - 1 of the sequence's seqlens[b]
+ * cached keys, their own (written by bsattn_kv_append) among them.  For query head hq and its
+ * KV head h = hq / (Hq / H), over the keys j < seqlens[b] that mask_mod(i, j) leaves (all of
+ * them for BSATTN_MASK_NONE; see bsattn_mask_kind):
+ *   s_j = softmax_scale * q . K_j,  lse = ln(sum_j exp(s_j)),  out = sum_j exp(s_j - lse) V_j;
+ * no key: out = 0, lse = -inf.  K_j, V_j are the cached values (code * scale); products with
+ * codes are exact and all sums are fp32; the weights times what a value's scale has besides a
+ * power of two are rounded to fp16 (11 bits), or, among keys whose value scales are more than
+ * 2^8 apart, to bf16 (8 bits).
+ *
+ * q            device bf16, `total` rows of [Hq, D] contiguous elements, q_stride apart (at
+ *              least Hq * D, a multiple of 8); 16-byte aligned.
+ * Hq           query heads, a multiple of cache->H with Hq / H <= 128 (else
+ *              BSATTN_ERR_UNSUPPORTED).
+ * total        packed rows of q (0: q, out and lse may be NULL).
+ * cu_seqlens   device int32 [B+1].
+ * page_table, table_stride, table_cols   as for bsattn_kv_append.
+ * seqlens      device int32 [B]; <= 0: no key.
+ * keys         the sum of all seqlens (of those above 0), or more: the workspace has room for a
+ *              copy of so many keys.  Sequences that have no room left are not written,
+ *              BSATTN_FLAG_BAD_SEQLENS.
+ * kind, mp     BSATTN_MASK_NONE, _CAUSAL, _SLIDING_WINDOW or _PREFIX; BSATTN_MASK_DOCUMENT ->
+ *              BSATTN_ERR_UNSUPPORTED (its ids belong to packed keys).
+ * A sequence whose offsets leave [0, total] or decrease, that has more new tokens than
+ * seqlens[b] (above 0), or that outgrows its table row: none of its rows is written,
+ * BSATTN_FLAG_BAD_SEQLENS.  A page outside [0, num_pages): its keys are left out,
+ * BSATTN_FLAG_BAD_INDEX.  Rows outside every sequence's range are left as they were.
+ * out          device, [total, Hq, D] contiguous, 16-byte aligned, out_dtype.
+ * lse          device fp32 [total, Hq].
+ * workspace    device, 256-byte aligned, at least bsattn_prefill_workspace_size bytes; needs no
+ *              zeroing and carries nothing from call to call.  Two calls that may run
+ *              concurrently must not share one.
+ */
+bsattn_status bsattn_prefill(const void *q, int64_t q_stride, int32_t total, int32_t B, int32_t Hq,
+                             const int32_t *cu_seqlens, const bsattn_kv_cache *cache,
+                             const int32_t *page_table, int32_t table_stride, int32_t table_cols,
+                             const int32_t *seqlens, int64_t keys, bsattn_mask_kind kind,
+                             const bsattn_mask_params *mp, float softmax_scale, void *out,
+                             bsattn_out_dtype out_dtype, float *lse, void *workspace,
+                             size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * bsattn_prefill_workspace_size -- bytes of workspace that bsattn_prefill needs for `total` query
+ * tokens of B sequences, Hq query heads, `keys` cached keys and a cache of this shape (its pointers
+ * are not looked at).
+ */
+bsattn_status bsattn_prefill_workspace_size(const bsattn_kv_cache *cache, int32_t total, int32_t B,
+                                            int32_t Hq, int64_t keys, size_t *bytes);
+
+/*
+ * bsattn_kv_weigh -- the attention weight that queries give to cached keys: for every sequence b,
+ * KV head h and key j < seqlens[b],
+ *   weights[place of j] += sum over its queries i and the query heads hq of h of exp(s_ij - lse_i),
+ * where s_ij as for bsattn_prefill, over the keys that mask_mod leaves.  With the queries and lse of
+ * every step the sums are the keys' accumulated weights; with those of a prompt's last tokens
+ * alone, what these ask for.
+ *
+ * weights      device fp32 [num_pages, H, page_size], 16-byte aligned: one per cached row, at the
+ *              place of its scales.  accumulate == 0: the weights of the sequences' keys are set
+ *              instead of added to, to 0 where no query meets a key.  A place that two sequences
+ *              share (a common prefix) receives the sum of both where they are added, in no set
+ *              order; where they are set, one of the two.  Other places are left as they were.
+ * lse          device fp32 [total, Hq], as bsattn_prefill or bsattn_decode wrote it.  -inf: the
+ *              query gives no weight.
+ * cu_seqlens   device int32 [B+1], or NULL: one query token per sequence (total == B), the newest.
+ * A sequence without query tokens, or with faulty numbers (flagged as by bsattn_prefill), is left as
+ * it was.  Other arguments as for bsattn_prefill.
+ */
+bsattn_status bsattn_kv_weigh(const void *q, int64_t q_stride, const float *lse, int32_t total, int32_t B,
+                              int32_t Hq, const int32_t *cu_seqlens, const bsattn_kv_cache *cache,
+                              float *weights, int32_t accumulate, const int32_t *page_table,
+                              int32_t table_stride, int32_t table_cols, const int32_t *seqlens,
+                              bsattn_mask_kind kind, const bsattn_mask_params *mp, float softmax_scale,
+                              int32_t *err_flag, void *stream);
+
+/*
+ * bsattn_kv_evict -- bounds sequences to `keep` keys, by weight.  Of a sequence of n > keep keys
+ * there stay, per KV head, the positions below `sinks`, the `recent` last ones, and of the others
+ * those of largest weight (of equal ones the lowest positions; NaN counts as the largest, a page
+ * outside the cache as less than any weight).  Of a shorter one all stay.  The i-th that stays, in
+ * ascending order, is moved to position i of the sequence's row of out_table: codes, scales, weight.
+ *
+ * weights      as for bsattn_kv_weigh.
+ * keep         > 0; recent, sinks >= 0, together at most keep.
+ * out_table    device int32, B rows of out_cols entries, out_stride apart: the pages to move to,
+ *              room for min(keep, table_cols * page_size) keys.  None of the pages it names may be in
+ *              page_table's rows or named twice; page_table's pages are only read.  NULL, or
+ *              page_table itself: rows move within their sequence's own pages, and the weights at the
+ *              positions min(n, keep) .. n - 1 become 0.  Then no page that is moved may be
+ *              another sequence's too.
+ * kept         device int32 [B, H, keep]: the positions that stay, ascending, then -1.
+ * lens         device int32 [B]: min(seqlens[b], keep), 0 for seqlens[b] <= 0.
+ * A row read from a page outside [0, num_pages) moves as zeros; one that would go to such a page is
+ * not moved; both BSATTN_FLAG_BAD_INDEX.  A sequence that outgrows its row of page_table is not
+ * moved: lens 0, kept -1, BSATTN_FLAG_BAD_SEQLENS.  All else in the cache is left as it was.
+ */
+bsattn_status bsattn_kv_evict(const bsattn_kv_cache *cache, float *weights, const int32_t *page_table,
+                              int32_t table_stride, int32_t table_cols, const int32_t *seqlens, int32_t B,
+                              int32_t keep, int32_t recent, int32_t sinks, const int32_t *out_table,
+                              int32_t out_stride, int32_t out_cols, int32_t *kept, int32_t *lens,
+                              int32_t *err_flag, void *stream);
 
 /*
  * bsattn_testing_set_wait_limit -- testing hook, not for production use; the

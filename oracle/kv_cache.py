@@ -78,3 +78,53 @@ def gather(codes: np.ndarray, scales: np.ndarray, table, h: int, positions, dtyp
         if 0 <= pg < codes.shape[0]:
             rows.append(values(codes[pg, h, p % page], dtype) * float(scales[pg, h, p % page]))
     return np.array(rows).reshape(-1, codes.shape[3])
+
+
+def chunk_mask(n: int, m: int, kind: int, window: int = 0, sinks: int = 0, prefix: int = 0) -> np.ndarray:
+    """[m, n]: whether the query at position n - m + t meets key j (kinds numbered as in the C ABI:
+    0 all keys, 1 causal, 2 sliding window with sink tokens, 4 prefix)."""
+    i, j = np.arange(n - m, n)[:, None], np.arange(n)[None]
+    if kind == 0:
+        return np.ones((m, n), bool)
+    if kind == 1:
+        return j <= i
+    if kind == 2:
+        return (j <= i) & ((i - j < window) | (j < sinks))
+    if kind == 4:
+        return (j < prefix) | (j <= i)
+    raise ValueError(kind)
+
+
+def attend_rows(q: np.ndarray, k: np.ndarray, v: np.ndarray, mask: np.ndarray, scale: float):
+    """``attend`` of every row of q [r, D] over the keys its row of mask [r, n] names: (out, lse, spread)."""
+    out = np.zeros((len(q), v.shape[1]))
+    lse, spread = np.full(len(q), -math.inf), np.zeros_like(out)
+    for r in range(len(q)):
+        out[r], lse[r], spread[r] = attend(q[r], k[mask[r]], v[mask[r]], scale)
+    return out, lse, spread
+
+
+def weigh(q: np.ndarray, lse: np.ndarray, k: np.ndarray, mask: np.ndarray, scale: float) -> np.ndarray:
+    """[n]: the weight that the rows of q [r, D], with their lse [r], give to keys k [n, D]."""
+    w = np.zeros(len(k))
+    for r in range(len(q)):
+        if lse[r] != -math.inf:
+            w[mask[r]] += np.exp(scale * (k[mask[r]] @ q[r]) - lse[r])
+    return w
+
+
+def evict(weights: np.ndarray, keep: int, recent: int, sinks: int) -> np.ndarray:
+    """The ascending positions that stay of keys with these weights [n]; a weight None stands for a key that
+    cannot be read."""
+    n = len(weights)
+    if n <= keep:
+        return np.arange(n)
+    first = [j for j in range(n) if j < sinks or j >= n - recent]
+
+    def rank(j):
+        w = weights[j]
+        if w is None:
+            return (2, 0.0, j)
+        return (0, 0.0, j) if math.isnan(w) else (1, -float(w), j)
+    rest = sorted((j for j in range(n) if sinks <= j < n - recent), key=rank)
+    return np.array(sorted(first + rest[:keep - len(first)]))

@@ -230,6 +230,10 @@ bsattn_status check_meta_desc(const bsattn_meta *m);
 int current_device_sms();          // 0 on failure
 // Tensor map of [rows, D] codes, box_rows x D per copy (128- or 64-byte swizzle).
 bool encode_code_rows(CUtensorMap *map, const void *ptr, long long rows, int D, int box_rows);
+// Tensor map of query rows [total, Hq, D] bf16, `stride` elements from token to token: `tokens` tokens x
+// `heads` heads x 64 elements per copy (128-byte swizzle).
+bool encode_query_rows(CUtensorMap *map, const void *ptr, int total, int Hq, int D, long long stride, int tokens,
+                       int heads);
 
 cudaError_t launch_meta(const MetaParams &p, cudaStream_t stream);
 cudaError_t launch_kv_summary(const void *k, const void *v, int B, int S, int H, int D, void *k_sum,

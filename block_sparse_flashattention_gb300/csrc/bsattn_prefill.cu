@@ -1,4 +1,37 @@
-// Attention of a chunk of new tokens over a paged 8-bit K/V cache.
+// Attention of chunks of new tokens over a paged 8-bit K/V cache: four launches.
+//
+// Of a KV head's queries, (token, query head) pairs are rows of one attention over the
+// sequence's keys: 4 D flop per row and key, so that from some hundred rows on the products bound
+// it.  The codes are widened once per call, into the workspace, and the attention reads tiles that
+// lie there as its shared memory wants them (bulk copies, no tensor map):
+//   K' = bf16(code 2^e), exact: e the binary exponent of the key's scale; what is left of the
+//        scale, r in [1, 2), multiplies the key's scores in fp32, and only in tiles where some
+//        r != 1 (int8; the scales that e4m3 rows are given are powers of two);
+//   V' = fp16(code 2^(f - E + 6)), exact: f the exponent of the value's scale, E (a multiple of 4)
+//        the tile's largest; what is left, u in [1, 2), multiplies the weight before it is
+//        rounded, again only where some u != 1.  Where scales of a tile are more than 2^14 apart
+//        its V' and its weights are bf16 instead, which has the exponents for them and 8 bits.
+// With z_j the scores in units of log2: p_j = 2^(z_j - m + 7) u_j is rounded to fp16 (11 bits)
+// for P V', l sums 2^(z_j - m + 7) in fp32; out = O 2^(E - 6) / l, lse = ln 2 (m - 7 + log2 l).  The
+// reference m is moved only when some weight could pass 2^14 (the output is then rescaled), and
+// O is rescaled to another E only where it is larger or more than 2^8 smaller.
+//
+// Work.  A segment is (sequence, KV head, block of 2 x floor(128 / G) tokens): two 128-row
+// tiles ("slots") that share each K/V tile.  It visits the key tiles that its rows meet: all up to
+// its last position, or the sink tiles and those from the window's first on.  A plan kernel numbers
+// the tiles of all segments along one line (each segment also counts kSegCost places for what
+// starting and ending one costs), which is cut into equal pieces, so many per CTA that the keys
+// of those which the CTAs work on at a time fit L2.  What a piece
+// computes of a segment that it does not hold whole goes to the workspace (fp32 output and LSE);
+// the last launch joins these parts in a fixed order.
+//
+// Roles of the attention kernel (384 threads, one CTA per SM, all of TMEM):
+//   warp 0      copies: query tiles (TMA), K and V tiles with their scales (bulk)
+//   warp 1      issues the MMAs: S_t = Q_t K'^T into TMEM, O_t += P_t V' with P in TMEM
+//   warp 2      owns the TMEM allocation
+//   warp 3      finds the segments of the CTA's pieces, one ahead of the others
+//   warps 4-7, 8-11   slot 0, slot 1: softmax, O rescale, output
+// TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P_t over S_t.
 #include "chunk_common.cuh"
 #include "kv_codes.cuh"
 
@@ -6,97 +39,1070 @@ namespace bsattn {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+// 168 registers per thread at launch: 128 * 120 + 2 * 128 * 192 = 64512 = 384 * 168.
+constexpr int kLaunchRegs = 168;
+constexpr uint32_t kCtrlRegs = 120, kSoftmaxRegs = 192;
+static_assert(128 * kCtrlRegs + 2 * 128 * kSoftmaxRegs <= (uint32_t)kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 elements: one 128-byte swizzle span
+constexpr int kMaxCtas = 160;
+constexpr int kSegCost = 2;
+constexpr int kLeastPiece = 4;              // places of a piece: each makes parts for the join
+constexpr int kDescs = 2;                   // segments found ahead
+constexpr int kPlanThreads = 1024, kWidenThreads = 256, kJoinThreads = 256;
+constexpr int kJoinRows = 32;               // rows of a part that a block of the join takes
 
-// One warp per query row, 32 keys at a time: each lane scores a key, then all lanes sum the
-// values' columns.
-template <int D, bool kInt8>
-__global__ void __launch_bounds__(kWarps * 32) bsattn_prefill_kernel(const __grid_constant__ ChunkParams p) {
-    __shared__ float sq[kWarps][D];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int t = blockIdx.x, hq = blockIdx.y * kWarps + warp;
-    int b = -1;
-    Chunk s = {};
-    for (int x = 0; x < p.B; ++x) {
-        s = chunk_of(p, x, t == 0 && hq == 0 && lane == 0);
-        if (t >= s.first && t < s.first + s.m) { b = x; break; }
-    }
-    if (t == 0 && hq == 0)
-        for (int x = max(b, 0); x < p.B; ++x) chunk_of(p, x, lane == 0);
-    if (b < 0 || hq >= p.Hq) return;
-    const int h = hq / p.G;
-    for (int d = lane; d < D; d += 32)
-        sq[warp][d] = __uint_as_float((uint32_t)p.q[(long long)t * p.q_stride + (long long)hq * D + d] << 16);
-    __syncwarp();
-    const Met r = s.n > 0 ? met(p, s.n - s.m + t - s.first, s.n) : Met{0, 0, 0};
-    const int32_t *table = p.table + (long long)b * p.table_stride;
-    float m = -INFINITY, l = 0.f, o[D / 32] = {};
-    for (int j0 = 0; j0 < r.ha; j0 += 32) {
-        const int j = j0 + lane;
-        const bool in = j < r.hb || (j >= r.la && j < r.ha);
-        if (!__any_sync(0xffffffffu, in)) continue;
-        const long long row = in ? cache_row(p.c, table, h, j) : -1;
-        if (in && row < 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
-        float z = -INFINITY;
-        if (row >= 0) {
-            float acc = 0.f;
-            for (int d = 0; d < D; d += 4) {
-                float y[4];
-                const uint32_t x = *reinterpret_cast<const uint32_t *>(p.c.k + row * D + d);
-                if (kInt8) unpack_int8(x, y);
-                else unpack_e4m3(x, y);
-                for (int i = 0; i < 4; ++i) acc += sq[warp][d + i] * y[i];
-            }
-            z = acc * p.c.ks[row] * p.scale_log2;
-        }
-        float top = z;
-        bool nan = z != z;
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float m_new = fmaxf(m, top);
-        if (m_new == -INFINITY && !__any_sync(0xffffffffu, nan)) continue;
-        const float ref = m_new == -INFINITY ? 0.f : m_new, alpha = exp2f(m - ref), w = row >= 0 ? exp2f(z - ref) : 0.f;
-        float sum = w;
-        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l = l * alpha + sum;
-        for (int c = 0; c < D / 32; ++c) o[c] *= alpha;
-        m = m_new;
-        const float wv = row >= 0 ? w * p.c.vs[row] : 0.f;
-        for (int x = 0; x < 32; ++x) {
-            const long long at = __shfl_sync(0xffffffffu, row, x);
-            const float f = __shfl_sync(0xffffffffu, wv, x);
-            if (at < 0) continue;
-            for (int c = 0; c < D / 32; ++c) {
-                float y[4];
-                const uint32_t code = p.c.v[at * D + c * 32 + lane];
-                if (kInt8) unpack_int8(code, y);
-                else unpack_e4m3(code, y);
-                o[c] += f * y[0];
-            }
-        }
-    }
-    const bool empty = l == 0.f;
-    const long long at = (long long)t * p.Hq + hq;
-    for (int c = 0; c < D / 32; ++c) {
-        const float v = empty ? 0.f : o[c] / l;
-        if (p.out_f32) static_cast<float *>(p.out)[at * D + c * 32 + lane] = v;
-        else static_cast<uint16_t *>(p.out)[at * D + c * 32 + lane] = (uint16_t)pack_bf16x2(v, 0.f);
-    }
-    if (lane == 0) p.lse[at] = empty ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+// Binary exponents (biased) that go into K', and those that go into V' (2^(E - 6) and its inverse are then
+// normal numbers); what lies outside stays in r and u.
+constexpr int kLeastKey = 27, kMostKey = 227, kLeastValue = 7, kMostValue = 227;
+constexpr int kNear = 14;
+constexpr float kLift = 7.f, kReach = 7.f;
+constexpr float kNoKey = -0x1p100f;         // reference before the first key
+
+// Flags of a tile: some r, some u is not 1; bf16 values; some values are not numbers.
+constexpr uint32_t kRestK = 1u, kRestV = 2u, kFar = 4u, kOdd = 8u;
+
+// What goes with a tile: r and u of its keys, the keys that count, E (biased), flags, and the keys whose
+// values are not numbers (NaN or infinite scales, NaN codes).  V' of those is 0, since a NaN times the
+// weight 0 of a query that does not meet the key would be NaN; a query that does is told by its mask.
+struct TileHead {
+    float r[kTile], u[kTile];
+    uint32_t keep[4];
+    int32_t exp;
+    uint32_t flags;
+    int32_t pad[2];
+    uint32_t odd[4];
+};
+static_assert(sizeof(TileHead) % 16 == 0, "copied in pieces of 16 bytes");
+
+// A sequence as the plan kernel leaves it.
+struct SeqPlan {
+    int32_t first, m, n;     // as in Chunk
+    int32_t tile0;           // its first tile in the workspace
+    int32_t sinks, near;     // tiles that some query meets: below sinks, and from near to end
+    int32_t end;
+    int32_t block0, blocks;  // its row blocks (of every head)
+    int32_t pass;            // places of all of a head's blocks in the line
+    long long base;          // first place
+};
+
+struct PlanTotals {
+    long long places;
+    int32_t tiles;
+    int32_t pieces;          // of the line; at most as many as the layout has room for
+};
+
+// A segment, or the part of it that lies in one piece of the line.
+struct SegDesc {
+    int32_t b, h;            // b < 0: no more
+    int32_t token, tokens;   // first packed row, rows' tokens
+    int32_t pos, n;          // position of the first token, keys of the sequence
+    int32_t sinks, near;     // tiles visited: 0 .. sinks - 1, then near, near + 1, ...
+    int32_t count[2];        // how many of them slot t meets
+    int32_t k0, k1;          // those of this piece
+    int32_t tile0;           // where the sequence's tiles lie in the workspace, one after the other:
+    int32_t seq_sinks, seq_near;  // those below seq_sinks, and from seq_near on
+    int32_t part;            // -1: the rows go to the output
+    int32_t pad;
+};
+
+// A segment that is cut: its rows and how many parts there are.
+struct CutInfo {
+    int32_t token, tokens, h, parts;
+};
+
+struct Layout {
+    int tokens;              // of a slot: floor(128 / G)
+    int pieces, ctas;
+    long long tiles;         // of a head that the workspace has room for
+    long long blocks;
+    size_t seq, block_place, totals, cuts, part_o, part_l, k, v, head, total;
+};
+
+// Widened bytes that the CTAs work on at a time: of 129 MB of L2, less what else passes through.
+constexpr long long kPhaseBytes = 64ll << 20;
+
+inline Layout make_layout(int total, int B, int H, int G, int D, long long keys, int ctas) {
+    Layout w = {};
+    w.tokens = kTile / G;
+    w.ctas = ctas;
+    w.tiles = keys / kTile + B;
+    w.blocks = (long long)total / (2 * w.tokens) + B;
+    const long long bytes = w.tiles * H * kTile * D * 4;
+    const long long phases = (bytes + kPhaseBytes - 1) / kPhaseBytes;
+    w.pieces = ctas * (int)(phases < 1 ? 1 : phases > 64 ? 64 : phases);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255u) & ~(size_t)255u;
+        return here;
+    };
+    w.seq = take((size_t)B * sizeof(SeqPlan));
+    w.block_place = take((size_t)w.blocks * 4u);
+    w.totals = take(sizeof(PlanTotals));
+    w.cuts = take((size_t)w.pieces * sizeof(CutInfo));
+    w.part_l = take((size_t)w.pieces * 2 * 256 * 4);
+    w.part_o = take((size_t)w.pieces * 2 * 256 * D * 4);
+    w.head = take((size_t)w.tiles * H * sizeof(TileHead));
+    w.k = take((size_t)w.tiles * H * kTile * D * 2);
+    w.v = take((size_t)w.tiles * H * kTile * D * 2);
+    w.total = at;
+    return w;
 }
 
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^d of an integer d, 0 below 2^-126.
+__device__ __forceinline__ float pow2(int d) { return d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(d, 127)) << 23); }
+
+// Tiles that queries at positions i0 .. i1 of a sequence of n keys visit: 0 .. sinks - 1 and near .. end - 1.
+struct Visit {
+    int sinks, near, end;
+    __device__ __forceinline__ int count() const { return sinks + end - near; }
+};
+
+__device__ __forceinline__ Visit visit(const ChunkParams &p, int n, int i0, int i1) {
+    Visit v;
+    const int ha = met(p, i1, n).ha;
+    v.end = (ha + kTile - 1) / kTile;
+    v.sinks = v.near = 0;
+    if (p.kind == BSATTN_MASK_SLIDING_WINDOW) {
+        v.near = min(met(p, i0, n).la / kTile, v.end);
+        v.sinks = min((int)(((long long)p.sink_tokens + kTile - 1) / kTile), v.near);
+    }
+    return v;
+}
+
+// ------------------------------------------------------------------- plan --
+
+// Sum over the block's threads before this one; *all: over all of them.
+__device__ __forceinline__ long long block_scan(long long x, long long *all, long long *warps) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    long long s = x;
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = s;
+    __syncthreads();
+    long long before = 0, sum = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += warps[w];
+        sum += warps[w];
+    }
+    *all = sum;
+    return before + s - x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const __grid_constant__ ChunkParams p,
+                                                                           const __grid_constant__ Layout w) {
+    __shared__ long long warps[kPlanThreads / 32];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    SeqPlan *seq = reinterpret_cast<SeqPlan *>(p.ws + w.seq);
+    int32_t *place = reinterpret_cast<int32_t *>(p.ws + w.block_place);
+    const int step = 2 * w.tokens, tid = threadIdx.x, lane = tid % 32;
+    long long tiles = 0, blocks = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        SeqPlan s = {};
+        if (b < p.B) {
+            const Chunk c = chunk_of(p, b, true);
+            s.first = c.first, s.m = c.m, s.n = c.n;
+            s.blocks = (c.m + step - 1) / step;
+            if (c.m > 0 && c.n > 0) {
+                const Visit v = visit(p, c.n, c.n - c.m, c.n - 1);
+                s.sinks = v.sinks, s.near = v.near, s.end = v.end;
+            }
+        }
+        long long sum;
+        s.tile0 = (int)min(tiles + block_scan(s.sinks + s.end - s.near, &sum, warps), (long long)INT32_MAX);
+        if (s.m > 0 && (long long)s.tile0 + s.sinks + s.end - s.near > w.tiles) {
+            // no room for its keys
+            if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
+            s.m = s.blocks = s.sinks = s.near = s.end = 0;
+        }
+        tiles += sum;
+        s.block0 = (int)(blocks + block_scan(s.blocks, &sum, warps));
+        blocks += sum;
+        if (b < p.B) seq[b] = s;
+    }
+    __syncthreads();
+    // places of the row blocks within a head's pass over them: a warp per sequence
+    for (int b = tid / 32; b < p.B; b += kPlanThreads / 32) {
+        const SeqPlan s = seq[b];
+        int sum = 0;
+        for (int r0 = 0; r0 < s.blocks; r0 += 32) {
+            const int r = r0 + lane;
+            int x = 0;
+            if (r < s.blocks) {
+                x = kSegCost;
+                if (s.n > 0) x += visit(p, s.n, s.n - s.m + r * step, s.n - s.m + min((r + 1) * step, s.m) - 1).count();
+            }
+            int y = x;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int z = __shfl_up_sync(0xffffffffu, y, d);
+                if (lane >= d) y += z;
+            }
+            if (r < s.blocks) place[s.block0 + r] = sum + y - x;
+            sum += __shfl_sync(0xffffffffu, y, 31);
+        }
+        if (lane == 0) seq[b].pass = sum;
+    }
+    __syncthreads();
+    long long places = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        long long sum;
+        const long long before = block_scan(b < p.B ? (long long)seq[b].pass * p.c.H : 0, &sum, warps);
+        if (b < p.B) seq[b].base = places + before;
+        places += sum;
+    }
+    if (tid == 0) {
+        PlanTotals t = {};
+        t.places = places;
+        t.tiles = (int)min(tiles, w.tiles);
+        t.pieces = (int)max(1ll, min((long long)w.pieces, places / kLeastPiece));
+        *reinterpret_cast<PlanTotals *>(p.ws + w.totals) = t;
+    }
+}
+
+// ------------------------------------------------------------------ widen --
+
+// One tile of one head per turn: rows of K and V in pieces of 16 codes, D / 16 lanes to a row.
 template <int D, bool kInt8>
+__global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(const __grid_constant__ ChunkParams p,
+                                                                             const __grid_constant__ Layout w) {
+    constexpr int kRowLanes = D / 16, kRows = kWidenThreads / kRowLanes, kSteps = kTile / kRows;
+    __shared__ int s_row[kTile];                 // cache row of each key, -1: none
+    __shared__ float s_k[kTile];                 // 2^e
+    __shared__ int s_f[kTile];                   // f (biased)
+    __shared__ int s_top[4], s_far[4];
+    __shared__ uint32_t s_keep[4], s_rest[4], s_odd[4];
+    __shared__ int s_nan[kTile];                 // the key's value is not a number
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const SeqPlan *seq = reinterpret_cast<const SeqPlan *>(p.ws + w.seq);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const long long items = (long long)reinterpret_cast<const PlanTotals *>(p.ws + w.totals)->tiles * p.c.H;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int slot = (int)(it / p.c.H), h = (int)(it - (long long)slot * p.c.H);
+        // the last sequence whose tiles begin at or before this one
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (seq[mid].tile0 <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        const SeqPlan s = seq[lo];
+        int tile = slot - s.tile0;
+        if (tile >= s.sinks) tile += s.near - s.sinks;
+        if (tile >= s.end) continue;             // a sequence that has no room
+        __syncthreads();
+        float ks = 1.f, vs = 1.f;
+        int f = 0;
+        if (tid < kTile) {
+            const int j = tile * kTile + tid;
+            const long long row = j < s.n ? cache_row(p.c, p.table + (long long)lo * p.table_stride, h, j) : -1;
+            if (j < s.n && row < 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+            if (row >= 0) ks = p.c.ks[row], vs = p.c.vs[row];
+            s_row[tid] = (int)row;
+            const uint32_t kb = __float_as_uint(ks) & 0x7fffffffu, vb = __float_as_uint(vs) & 0x7fffffffu;
+            const int e = kb < 0x7f800000u ? min(max((int)(kb >> 23), kLeastKey), kMostKey) : 127;
+            s_k[tid] = pow2(e - 127);
+            ks *= pow2(127 - e);
+            const bool number = vb < 0x7f800000u;
+            // rows of zeros have the smallest scale; they, NaN and infinity do not count for E (f = E, then)
+            f = row >= 0 && number && vb > 1u << 23 ? min(max((int)(vb >> 23), kLeastValue), kMostValue) : 0;
+            s_nan[tid] = number ? 0 : 1;
+            const int top = __reduce_max_sync(0xffffffffu, max(f, kLeastValue));
+            if (lane == 0) s_top[warp] = top;
+            const uint32_t keep = __ballot_sync(0xffffffffu, row >= 0);
+            const int least = __reduce_min_sync(0xffffffffu, f > 0 ? f : 1000);
+            if (lane == 0) s_keep[warp] = keep, s_far[warp] = least;
+        }
+        __syncthreads();
+        const int exp = (max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3])) + 3) & ~3;
+        const bool far = exp - min(min(s_far[0], s_far[1]), min(s_far[2], s_far[3])) > kNear;
+        if (tid < kTile) s_f[tid] = f = f > 0 ? f : exp;
+        const long long at = (long long)h * w.tiles + slot;
+        TileHead *head = reinterpret_cast<TileHead *>(p.ws + w.head) + at;
+        const int piece = tid % kRowLanes, sub = tid / kRowLanes;
+        uint4 x[2][kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const long long row = s_row[i * kRows + sub];
+            x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+            if (row >= 0) {
+                x[0][i] = __ldg(reinterpret_cast<const uint4 *>(p.c.k + row * D) + piece);
+                x[1][i] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + row * D) + piece);
+            }
+        }
+        if (!kInt8) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const uint32_t y[4] = {x[1][i].x, x[1][i].y, x[1][i].z, x[1][i].w};
+                uint32_t nan = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) nan |= ((y[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                if (nan) s_nan[i * kRows + sub] = 1;
+            }
+        }
+        __syncthreads();
+        if (tid < kTile) {
+            const bool odd = s_nan[tid] != 0;
+            vs = odd || s_row[tid] < 0 ? 1.f : vs * pow2(127 - f);
+            head->r[tid] = ks;
+            head->u[tid] = vs;
+            const uint32_t rest = (__any_sync(0xffffffffu, ks != 1.f) ? kRestK : 0u) | (__any_sync(0xffffffffu, vs != 1.f) ? kRestV : 0u);
+            const uint32_t odds = __ballot_sync(0xffffffffu, odd);
+            if (lane == 0) s_rest[warp] = rest | (odds ? kOdd : 0u), s_odd[warp] = odds;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            *reinterpret_cast<uint4 *>(head->keep) = make_uint4(s_keep[0], s_keep[1], s_keep[2], s_keep[3]);
+            *reinterpret_cast<uint4 *>(head->odd) = make_uint4(s_odd[0], s_odd[1], s_odd[2], s_odd[3]);
+            head->exp = exp;
+            head->flags = s_rest[0] | s_rest[1] | s_rest[2] | s_rest[3] | (far ? kFar : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = i * kRows + sub;
+            const float kf = s_k[r], vf = pow2(s_f[r] - exp + 6);
+            if (s_nan[r]) x[1][i] = make_uint4(0, 0, 0, 0);
+            const uint32_t vh = pack_f16x2(vf, vf);
+#pragma unroll
+            for (int values = 0; values < 2; ++values) {
+                const uint32_t y[4] = {x[values][i].x, x[values][i].y, x[values][i].z, x[values][i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t c2[2];
+                    codes_to_f16x2<kInt8>(y[q], c2[0], c2[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (values && !far) {
+                            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * q + k]) : "r"(c2[k]), "r"(vh));
+                        } else {
+                            float a, c;
+                            asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+                                : "=f"(a), "=f"(c)
+                                : "r"(c2[k]));
+                            const float f32 = values ? vf : kf;
+                            o[2 * q + k] = pack_bf16x2(a * f32, c * f32);
+                        }
+                    }
+                }
+                uint8_t *dst = p.ws + (values ? w.v : w.k) + at * (kTile * D * 2) + (size_t)(piece >> 2) * kSub + r * 128;
+                const int c0 = 2 * (piece & 3);
+                *reinterpret_cast<uint4 *>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------- attention --
+
+template <int D>
+struct Cfg {
+    static constexpr uint32_t kTileBytes = kTile * D * 2;
+    static constexpr uint32_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + 2 * kTileBytes;
+    static constexpr uint32_t kHead = kV + 2 * kTileBytes;
+    static constexpr uint32_t kEpi = kHead + 2 * (uint32_t)sizeof(TileHead);   // 2 KB per softmax warp
+    static constexpr uint32_t kDesc = kEpi + 8u * 2048u;
+    static constexpr uint32_t kBar = kDesc + kDescs * (uint32_t)sizeof(SegDesc);
+    // K / V stage full and empty, per slot: query tile full and empty, S ready, two halves of P
+    // ready, O complete; descriptor full and empty
+    static constexpr int bKF = 0, bKE = 2, bVF = 4, bVE = 6, bQF = 8, bQE = 10, bSR = 12, bPR = 14, bOD = 18, bUF = 20,
+                         bUE = bUF + kDescs, bDrain = bUE + kDescs, kNumBars = bDrain + 1;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;                     // [0] tmem base, [1] abort
+    static constexpr uint32_t kBytes = kMisc + 16;
+    static constexpr uint32_t kAlloc = kBytes + 1024;                          // slack for 1024-byte alignment
+    static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > 32 ? 32 : hi;
+    if (hi <= lo) return 0u;
+    return (hi >= 32 ? 0xffffffffu : ((1u << hi) - 1u)) & ~((1u << lo) - 1u);
+}
+
+// Waiting for one of the CTA's barriers; false where the CTA gives up.
+struct Waiter {
+    uint32_t bars;
+    volatile int *abort;
+    int *err;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
+    __device__ __forceinline__ bool operator()(int i, uint32_t phase) const {
+        return mbar_wait(bar(i), phase & 1u, abort, err, BSATTN_FLAG_TIMEOUT);
+    }
+};
+
+// Reads the next segment's descriptor (the whole warp), and gives its place back.
+template <int D>
+__device__ __forceinline__ bool next_desc(const Waiter &wait, const uint8_t *smem, uint32_t &count, SegDesc &d) {
+    using C = Cfg<D>;
+    const int slot = (int)(count % kDescs);
+    if (!__all_sync(0xffffffffu, wait(C::bUF + slot, count / kDescs))) return false;
+    d = reinterpret_cast<const SegDesc *>(smem + C::kDesc)[slot];
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(wait.bar(C::bUE + slot));
+    ++count;
+    return d.b >= 0;
+}
+
+// Finds the segments of the CTA's pieces and writes their descriptors.
+template <int D>
+__device__ __forceinline__ void schedule_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint8_t *smem) {
+    using C = Cfg<D>;
+    const SeqPlan *seq = reinterpret_cast<const SeqPlan *>(p.ws + w.seq);
+    const int32_t *place = reinterpret_cast<const int32_t *>(p.ws + w.block_place);
+    CutInfo *cuts = reinterpret_cast<CutInfo *>(p.ws + w.cuts);
+    const PlanTotals totals = *reinterpret_cast<const PlanTotals *>(p.ws + w.totals);
+    const long long line = totals.places;
+    const int step = 2 * w.tokens, pieces = totals.pieces;
+    uint32_t count = 0;
+    bool ok = true;
+    for (int piece = blockIdx.x; piece < w.pieces; piece += w.ctas) cuts[piece] = CutInfo{};   // also of pieces not come to
+    auto emit = [&](const SegDesc &d) -> bool {
+        const int slot = (int)(count % kDescs);
+        if (!(ok = wait(C::bUE + slot, (count / kDescs) ^ 1u))) return false;
+        reinterpret_cast<SegDesc *>(smem + C::kDesc)[slot] = d;
+        mbar_arrive(wait.bar(C::bUF + slot));
+        ++count;
+        return true;
+    };
+    for (int piece = blockIdx.x; ok && piece < pieces; piece += w.ctas) {
+        const long long from = line * piece / pieces, to = line * (piece + 1) / pieces;
+        CutInfo cut = {};
+        if (from < to) {
+            int b = 0, hi = p.B - 1;             // the last sequence that begins at or before `from`
+            while (b < hi) {
+                const int mid = (b + hi + 1) / 2;
+                if (seq[mid].base <= from) b = mid;
+                else hi = mid - 1;
+            }
+            SeqPlan s = seq[b];
+            int h = s.pass > 0 ? (int)((from - s.base) / s.pass) : 0;
+            int r = 0;
+            if (s.pass > 0) {
+                const int off = (int)(from - s.base - (long long)h * s.pass);
+                int top = s.blocks - 1;
+                while (r < top) {
+                    const int mid = (r + top + 1) / 2;
+                    if (place[s.block0 + mid] <= off) r = mid;
+                    else top = mid - 1;
+                }
+            }
+            while (ok) {
+                if (r >= s.blocks) {
+                    r = 0;
+                    if (++h >= p.c.H || s.blocks == 0) {
+                        h = 0;
+                        if (++b >= p.B) break;
+                        s = seq[b];
+                        continue;
+                    }
+                }
+                const long long begin = s.base + (long long)h * s.pass + place[s.block0 + r];
+                if (begin >= to) break;
+                SegDesc d = {};
+                d.b = b, d.h = h, d.n = s.n;
+                d.token = s.first + r * step, d.tokens = min(step, s.m - r * step);
+                d.pos = s.n - s.m + r * step;
+                d.part = -1;
+                int tiles = 0;
+                if (s.n > 0) {
+                    const Visit v = visit(p, s.n, d.pos, d.pos + d.tokens - 1);
+                    d.sinks = v.sinks, d.near = v.near;
+                    tiles = v.count();
+                    // slot 0 meets no tile past its own last position
+                    const int mine = (met(p, d.pos + min(w.tokens, d.tokens) - 1, s.n).ha + kTile - 1) / kTile;
+                    d.count[0] = v.sinks + max(mine - v.near, 0);
+                    d.count[1] = d.tokens > w.tokens ? tiles : 0;
+                    d.tile0 = s.tile0, d.seq_sinks = s.sinks, d.seq_near = s.near;
+                }
+                const long long first = begin + kSegCost;   // place of its first tile
+                d.k0 = (int)max(from - first, 0ll);
+                d.k1 = (int)min(to - first, (long long)tiles);
+                if (tiles == 0 ? begin >= from : d.k1 > d.k0) {
+                    if (tiles == 0) d.k0 = d.k1 = 0;
+                    else if (d.k0 > 0 || d.k1 < tiles) {
+                        d.part = 2 * piece + (d.k0 > 0 ? 0 : 1);
+                        if (d.k0 == 0) {
+                            // the piece that holds the last tile: place x is in piece ((x + 1) pieces - 1) / line
+                            const int last = (int)(((first + tiles) * pieces - 1) / line);
+                            cut.token = d.token, cut.tokens = d.tokens, cut.h = h, cut.parts = last - piece + 1;
+                        }
+                    }
+                    if (!emit(d)) break;
+                }
+                ++r;
+            }
+        }
+        cuts[piece] = cut;
+    }
+    if (!ok) return;
+    SegDesc stop = {};
+    stop.b = -1;
+    emit(stop);
+}
+
+// One slot: warps 4-7 (t = 0) or 8-11 (t = 1), one row per thread.
+template <int D>
+__device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint32_t tmem,
+                                             int t, uint32_t warp, uint32_t lane, uint8_t *smem) {
+    using C = Cfg<D>;
+    const uint32_t quarter = warp & 3u;
+    const int row = (int)(quarter * 32 + lane), token_of = row / p.G, head_of = row - token_of * p.G;
+    const uint32_t lane_addr = tmem + ((quarter * 32u) << 16);
+    const uint32_t s_col = (uint32_t)t * 128u, o_col = 256u + (uint32_t)t * D;
+    const float sl2 = p.scale_log2;
+    uint32_t descs = 0, sc = 0, od = 0, tile0 = 0;   // descriptors; phases of S and O; tiles of earlier segments
+    bool ok = true;
+    SegDesc d;
+    while (ok && next_desc<D>(wait, smem, descs, d)) {
+        const int tok = t * w.tokens + token_of;     // of the segment
+        const bool row_ok = token_of < w.tokens && tok < d.tokens;
+        const int end = min(d.k1, d.count[t]);
+        // keys that the row meets: below hb, or from la to ha - 1
+        const Met own = d.n > 0 ? met(p, d.pos + min(tok, d.tokens - 1), d.n) : Met{0, 0, 0};
+        // what every row of the slot meets: the first row's end, the last one's window
+        const int slot_first = d.pos + min(t * w.tokens, d.tokens - 1), slot_last = d.pos + min((t + 1) * w.tokens, d.tokens) - 1;
+        const Met low = met(p, slot_first, d.n), high = met(p, slot_last, d.n);
+        float m_run = kNoKey, l_run = 0.f;
+        int exp_run = 0;
+        bool nan = false;                            // the row meets a value that is not a number
+        for (int k = d.k0; k < end; ++k) {
+            const uint32_t it = tile0 + (uint32_t)(k - d.k0), st = it & 1u;
+            // S first: a slot that left tiles out may be more than a phase ahead of the V stages, of which S
+            // says that they have come to this tile
+            ok = wait(C::bSR + t, sc) && wait(C::bVF + (int)st, it >> 1);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            ++sc;
+            tc_fence_after();
+            const TileHead *head = reinterpret_cast<const TileHead *>(smem + C::kHead) + st;
+            const int4 info = *reinterpret_cast<const int4 *>(&head->exp);
+            const uint4 kw = *reinterpret_cast<const uint4 *>(head->keep);
+            const int j0 = (k < d.sinks ? k : k - d.sinks + d.near) * kTile;
+            float s[128], hm[4];
+            {
+                uint32_t v0[32], v1[32], v2[32], v3[32];
+                tmem_ld32_max(lane_addr + s_col + 0, v0, hm[0]);
+                tmem_ld32_max(lane_addr + s_col + 32, v1, hm[1]);
+                tmem_ld32_max(lane_addr + s_col + 64, v2, hm[2]);
+                tmem_ld32_max(lane_addr + s_col + 96, v3, hm[3]);
+                tmem_wait_ld();
+                reg_fence(v0), reg_fence(v1), reg_fence(v2), reg_fence(v3);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) reg_fence(hm[x]);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    s[x] = __uint_as_float(v0[x]);
+                    s[32 + x] = __uint_as_float(v1[x]);
+                    s[64 + x] = __uint_as_float(v2[x]);
+                    s[96 + x] = __uint_as_float(v3[x]);
+                }
+            }
+            auto group_max = [&](int g) {
+                float a = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
+#pragma unroll
+                for (int x = 3; x < 31; x += 2) a = fmax3(a, s[32 * g + x], s[32 * g + x + 1]);
+                hm[g] = fmaxf(a, s[32 * g + 31]);
+            };
+            const bool rest = ((uint32_t)info.y & kRestK) != 0;
+            if (rest) {
+                const float4 *r = reinterpret_cast<const float4 *>(head->r);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float4 f = r[x];
+                    fmul2(s[4 * x], s[4 * x + 1], s[4 * x], s[4 * x + 1], f.x, f.y);
+                    fmul2(s[4 * x + 2], s[4 * x + 3], s[4 * x + 2], s[4 * x + 3], f.z, f.w);
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) group_max(g);
+            }
+            // a tile that every row of the slot meets whole needs no mask
+            const bool whole = (kw.x & kw.y & kw.z & kw.w) == 0xffffffffu && j0 + kTile <= low.ha &&
+                               (high.la <= j0 || high.hb >= j0 + kTile);
+            if (!whole) {
+                const uint32_t keep[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int c = j0 + 32 * g;
+                    const uint32_t bits = keep[g] & (span_bits(own.la - c, own.ha - c) | span_bits(0, own.hb - c));
+                    if (bits == 0xffffffffu) continue;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (!((bits >> x) & 1u)) s[32 * g + x] = -INFINITY;
+                    group_max(g);
+                }
+            }
+            const float m_new = fmaxf(m_run, fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3])) * sl2);
+            const bool begun = k > d.k0;
+            const bool grew = !begun || __any_sync(0xffffffffu, m_new - m_run > kReach);
+            float alpha = 1.f;
+            if (grew) {
+                alpha = ex2_approx(m_run - m_new);
+                m_run = m_new;
+            }
+            // the tile's E against that of O: a little smaller, and the weights make up for it
+            const int below = exp_run - info.x;
+            int shift = 0;
+            if (!begun) exp_run = info.x;
+            else if (below < 0 || below > 8) shift = min(below, 60), exp_run -= shift;
+            const float unit = pow2(info.x - exp_run);
+            const bool rescale = begun && (grew || shift != 0);
+            const float nm = kLift - m_run;
+            float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
+            auto publish = [&](int half) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(wait.bar(C::bPR + 2 * t + half));
+            };
+            const bool weighted = ((uint32_t)info.y & kRestV) != 0 || unit != 1.f, far = ((uint32_t)info.y & kFar) != 0;
+            if (__builtin_expect(((uint32_t)info.y & kOdd) != 0, 0)) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int c = j0 + 32 * g;
+                    nan |= (head->odd[g] & (span_bits(own.la - c, own.ha - c) | span_bits(0, own.hb - c))) != 0u;
+                }
+            }
+            auto half = [&](int c) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    float x0, x1;
+                    ffma2(x0, x1, s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1], sl2, sl2, nm, nm);
+                    x0 = ex2_approx(x0);
+                    x1 = ex2_approx(x1);
+                    if (x & 1) fadd2(lb0, lb1, lb0, lb1, x0, x1);
+                    else fadd2(la0, la1, la0, la1, x0, x1);
+                    s[c * 64 + 2 * x] = x0;
+                    s[c * 64 + 2 * x + 1] = x1;
+                }
+                if (weighted) {
+                    const float4 *u = reinterpret_cast<const float4 *>(head->u) + 16 * c;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        float4 f = u[x];
+                        fmul2(f.x, f.y, f.x, f.y, unit, unit);
+                        fmul2(f.z, f.w, f.z, f.w, unit, unit);
+                        float *y = s + c * 64 + 4 * x;
+                        fmul2(y[0], y[1], y[0], y[1], f.x, f.y);
+                        fmul2(y[2], y[3], y[2], y[3], f.z, f.w);
+                    }
+                }
+                if (__builtin_expect(far, 0)) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) pk[x] = pack_f16x2(s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1]);
+                }
+                tmem_st32(lane_addr + s_col + c * 32, pk);
+            };
+            half(0);
+            if (rescale) {
+                // S of this tile was issued after the slot's previous P V: O is up to date
+                const float f = alpha * pow2(shift);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_addr + o_col + c * 32, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+                    tmem_st32(lane_addr + o_col + c * 32, v);
+                }
+            }
+            publish(0);
+            half(1);
+            publish(1);
+            l_run = l_run * alpha + ((la0 + lb0) + (la1 + lb1));
+        }
+        if (!ok) break;
+        tile0 += (uint32_t)(d.k1 - d.k0);
+        const bool any = end > d.k0;
+        if (any) {
+            ok = wait(C::bOD + t, od);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            ++od;
+            tc_fence_after();
+        }
+        const bool empty = !any || l_run == 0.f;     // NaN is not empty
+        const float inv = empty ? 0.f : nan ? __uint_as_float(0x7fc00000u) : 1.f / l_run;
+        const float scale = any ? pow2(exp_run - 127 - 6) : 0.f;
+        // A block of 64 bytes of every row goes through the warp's scratch (16-byte pieces at piece ^
+        // (row / 2 mod 4)) and comes back with lane 4 g + j holding piece j of row 8 i + g: each store
+        // writes 8 whole pieces of 64 bytes.
+        const bool part = d.part >= 0;
+        const long long out_row = part ? ((long long)d.part * 2 + t) * kTile + row
+                                       : (long long)(d.token + tok) * p.Hq + d.h * p.G + head_of;
+        const bool half_words = !part && !p.out_f32;
+        const long long row_bytes = D * (half_words ? 2 : 4);
+        const long long dst = row_ok ? out_row * row_bytes : -1;
+        uint8_t *out = part ? p.ws + w.part_o : static_cast<uint8_t *>(p.out);
+        uint4 *scr = reinterpret_cast<uint4 *>(smem + C::kEpi + (warp - 4u) * 2048u);
+        const int gl = (int)(lane & 3u), rl = (int)(lane >> 2);
+        auto store = [&](uint32_t (&x)[16], int block) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                scr[lane * 4u + ((uint32_t)i ^ ((lane >> 1) & 3u))] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = 8 * i + rl;
+                const uint4 y = scr[rr * 4 + (gl ^ ((rr >> 1) & 3))];
+                const long long at = __shfl_sync(0xffffffffu, dst, rr);
+                if (at >= 0) *reinterpret_cast<uint4 *>(out + at + block * 64 + gl * 16) = y;
+            }
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            if (any) {
+                tmem_ld32(lane_addr + o_col + c * 32, v);
+                tmem_wait_ld();
+                reg_fence(v);
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = empty ? 0u : __float_as_uint(__uint_as_float(v[x]) * inv * scale);
+            uint32_t y[16];
+            if (half_words) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) y[x] = pack_bf16x2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
+                store(y, c);
+            } else {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) y[x] = v[16 * hf + x];
+                    store(y, 2 * c + hf);
+                }
+            }
+        }
+        if (row_ok) {
+            const float lse2 = empty ? -INFINITY : m_run - kLift + lg2_approx(l_run);
+            if (part) reinterpret_cast<float *>(p.ws + w.part_l)[out_row] = lse2;
+            else p.lse[out_row] = empty ? -INFINITY : (m_run - kLift) * 0.69314718055994530942f + logf(l_run);
+        }
+        tc_fence_before();
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    bsattn_prefill_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Layout w,
+                          const __grid_constant__ CUtensorMap tq) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    const uint32_t warp = warp_id(), lane = lane_id();
+    Waiter wait;
+    wait.bars = base + C::kBar;
+    wait.abort = reinterpret_cast<volatile int *>(misc + 1);
+    wait.err = p.err;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(wait.bar(C::bKF + s), 1);
+            mbar_init(wait.bar(C::bKE + s), 1);
+            mbar_init(wait.bar(C::bVF + s), 1);
+            mbar_init(wait.bar(C::bVE + s), 1);
+            mbar_init(wait.bar(C::bQF + s), 1);
+            mbar_init(wait.bar(C::bQE + s), 1);
+            mbar_init(wait.bar(C::bSR + s), 1);
+            mbar_init(wait.bar(C::bPR + 2 * s), 4);
+            mbar_init(wait.bar(C::bPR + 2 * s + 1), 4);
+            mbar_init(wait.bar(C::bOD + s), 1);
+        }
+        for (int s = 0; s < kDescs; ++s) {
+            mbar_init(wait.bar(C::bUF + s), 1);
+            mbar_init(wait.bar(C::bUE + s), 10);   // copying warp, issuing warp, eight softmax warps
+        }
+        mbar_init(wait.bar(C::bDrain), 1);
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    // rows of a query tile that no token fills stay 0
+    for (uint32_t i = threadIdx.x; i < 2 * C::kTileBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(smem + C::kQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 2) {
+        tmem_alloc(base + C::kMisc, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (warp == 0) {
+        regs_release<kCtrlRegs>();
+        // ------------------------------------------------------- copies --
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        if (lane == 0) tma_prefetch_desc(&tq);
+        uint32_t descs = 0, kc = 0, vc = 0, qc[2] = {0, 0};
+        const uint32_t q_bytes = (uint32_t)(p.G * w.tokens) * D * 2u;
+        bool ok = true;
+        SegDesc d;
+        while (ok && next_desc<D>(wait, smem, descs, d)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!ok || min(d.k1, d.count[t]) <= d.k0) continue;
+                if (!(ok = __all_sync(0xffffffffu, wait(C::bQE + t, qc[t] ^ 1u)))) break;
+                mbar_arrive_expect_tx_lead(lead, wait.bar(C::bQF + t), q_bytes);
+                __syncwarp();
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_3d_lead(lead, base + C::kQ + t * C::kTileBytes + x * kSub, &tq, wait.bar(C::bQF + t), x * 64,
+                                     d.h * p.G, d.token + t * w.tokens);
+                ++qc[t];
+            }
+            for (int k = d.k0; ok && k < d.k1; ++k) {
+                const int tile = k < d.sinks ? k : k - d.sinks + d.near;
+                const int slot = d.tile0 + (tile < d.seq_sinks ? tile : tile - d.seq_near + d.seq_sinks);
+                const long long at = (long long)d.h * w.tiles + slot;
+                const int ks = (int)(kc & 1u), vs = (int)(vc & 1u);
+                if (!(ok = __all_sync(0xffffffffu, wait(C::bKE + ks, (kc >> 1) ^ 1u)))) break;
+                mbar_arrive_expect_tx_lead(lead, wait.bar(C::bKF + ks), C::kTileBytes);
+                bulk_g2s_lead(lead, base + C::kK + ks * C::kTileBytes, p.ws + w.k + at * C::kTileBytes, C::kTileBytes,
+                              wait.bar(C::bKF + ks));
+                ++kc;
+                if (!(ok = __all_sync(0xffffffffu, wait(C::bVE + vs, (vc >> 1) ^ 1u)))) break;
+                mbar_arrive_expect_tx_lead(lead, wait.bar(C::bVF + vs), C::kTileBytes + (uint32_t)sizeof(TileHead));
+                bulk_g2s_lead(lead, base + C::kHead + vs * (uint32_t)sizeof(TileHead),
+                              p.ws + w.head + at * (long long)sizeof(TileHead), (uint32_t)sizeof(TileHead), wait.bar(C::bVF + vs));
+                bulk_g2s_lead(lead, base + C::kV + vs * C::kTileBytes, p.ws + w.v + at * C::kTileBytes, C::kTileBytes,
+                              wait.bar(C::bVF + vs));
+                ++vc;
+            }
+        }
+        // nothing may be on its way into shared memory when the CTA ends
+        for (uint32_t s = 0; s < 2; ++s) {
+            if (kc > s) mbar_wait_drain(wait.bar(C::bKF + (int)s), ((kc - 1 - s) >> 1) & 1u);
+            if (vc > s) mbar_wait_drain(wait.bar(C::bVF + (int)s), ((vc - 1 - s) >> 1) & 1u);
+            if (qc[s] > 0) mbar_wait_drain(wait.bar(C::bQF + (int)s), (qc[s] - 1) & 1u);
+        }
+    } else if (warp == 1) {
+        regs_release<kCtrlRegs>();
+        // ---------------------------------------------------- MMA issuer --
+        // The whole warp runs in step; lane 0 issues.
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
+        constexpr uint32_t idesc_pv16 = idesc_bf16_f32(128, D, true);
+        constexpr uint32_t idesc_pv = idesc_pv16 & ~((1u << 7) | (1u << 10));   // fp16 A and B
+        const uint64_t desc_q = smem_desc_sw128(base + C::kQ, 16, 1024);
+        const uint64_t desc_k = smem_desc_sw128(base + C::kK, 16, 1024);
+        const uint64_t desc_v = smem_desc_sw128(base + C::kV, kSub, 1024);
+        constexpr uint64_t kTileUnits = C::kTileBytes >> 4, kSubUnits = kSub >> 4;
+        uint32_t descs = 0, tile0 = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+        bool ok = true;
+        auto ready = [&](int b, uint32_t phase) -> bool {
+            ok = ok && wait(b, phase);
+            return ok;
+        };
+        auto score = [&](int t, uint32_t it) {
+            const uint64_t qd = desc_q + (uint64_t)t * kTileUnits, kd = desc_k + (uint64_t)(it & 1u) * kTileUnits;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)((kk >> 2) * kSubUnits + (kk & 3) * 2);
+                mma_ss_lead(lead, tmem + t * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_lead(lead, wait.bar(C::bSR + t));
+        };
+        auto output = [&](int t, uint32_t it, bool first) -> bool {
+            if (!ready(C::bVF + (int)(it & 1u), it >> 1)) return false;
+            const TileHead *head = reinterpret_cast<const TileHead *>(smem + C::kHead) + (it & 1u);
+            const uint32_t idesc = (head->flags & kFar) ? idesc_pv16 : idesc_pv;
+            const uint64_t vd = desc_v + (uint64_t)(it & 1u) * kTileUnits;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!ready(C::bPR + 2 * t + half, pc[t])) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                    mma_ts_lead(lead, tmem + 256 + t * D, tmem + t * 128 + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)), idesc,
+                                kk > 0 || !first ? 1u : 0u);
+            }
+            ++pc[t];
+            return true;
+        };
+        SegDesc d;
+        while (ok && next_desc<D>(wait, smem, descs, d)) {
+            const int end[2] = {min(d.k1, d.count[0]), min(d.k1, d.count[1])};
+            for (int t = 0; t < 2; ++t)
+                if (end[t] > d.k0) {
+                    ready(C::bQF + t, qc[t]);
+                    ++qc[t];
+                }
+            if (!ok) break;
+            tc_fence_after();
+            for (int k = d.k0; ok && k <= d.k1; ++k) {
+                const uint32_t it = tile0 + (uint32_t)(k - d.k0);
+                if (k < d.k1) {
+                    if (!ready(C::bKF + (int)(it & 1u), it >> 1)) break;
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (k > d.k0 && k - 1 < end[t]) {
+                        if (!output(t, it - 1, k - 1 == d.k0)) break;
+                        if (k == end[t]) mma_commit_lead(lead, wait.bar(C::bOD + t));
+                    }
+                    if (k < end[t]) {
+                        score(t, it);
+                        if (k == end[t] - 1) mma_commit_lead(lead, wait.bar(C::bQE + t));
+                    }
+                }
+                if (!ok) break;
+                if (k > d.k0) mma_commit_lead(lead, wait.bar(C::bVE + (int)((it - 1) & 1u)));
+                if (k < d.k1) mma_commit_lead(lead, wait.bar(C::bKE + (int)(it & 1u)));
+            }
+            tile0 += (uint32_t)(d.k1 - d.k0);
+        }
+        // Wait until every tcgen05 operation issued above has completed.
+        mma_commit_lead(lead, wait.bar(C::bDrain));
+        mbar_wait_drain(wait.bar(C::bDrain), 0);
+    } else if (warp < 4) {
+        regs_release<kCtrlRegs>();
+        if (warp == 3 && lane == 0) schedule_role<D>(p, w, wait, smem);
+        __syncwarp();
+    } else {
+        regs_claim<kSoftmaxRegs>();
+        softmax_role<D>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------- join --
+
+// Block (x, y): kJoinRows rows of the segment that begins in piece x and ends in a later one; D / 4
+// lanes to a row.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) bsattn_prefill_join_kernel(const __grid_constant__ ChunkParams p,
+                                                                           const __grid_constant__ Layout w) {
+    grid_dependency_wait();
+    const int piece = blockIdx.x;
+    const CutInfo cut = reinterpret_cast<const CutInfo *>(p.ws + w.cuts)[piece];
+    if (cut.parts == 0) return;
+    constexpr int kLanes = D / 4, kStep = kJoinThreads / kLanes;
+    const int lane = threadIdx.x % kLanes;
+    const float *part_l = reinterpret_cast<const float *>(p.ws + w.part_l);
+    const float4 *part_o = reinterpret_cast<const float4 *>(p.ws + w.part_o);
+    for (int i = threadIdx.x / kLanes; i < kJoinRows; i += kStep) {
+        const int r = blockIdx.y * kJoinRows + i, t = r / kTile, row = r % kTile;
+        const int token_of = row / p.G, tok = t * w.tokens + token_of;
+        if (token_of >= w.tokens || tok >= cut.tokens) continue;
+        auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
+        float m = -INFINITY;
+        bool nan = false;
+        for (int x = 0; x < cut.parts; ++x) {
+            const float l = part_l[at(x)];
+            nan |= l != l;
+            m = fmaxf(m, l);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        if (m != -INFINITY || nan)
+            for (int x = 0; x < cut.parts; ++x) {
+                const float l = part_l[at(x)];
+                if (l == -INFINITY) continue;
+                const float f = ex2_approx(l - m);
+                const float4 y = part_o[at(x) * kLanes + lane];
+                sum += f;
+                o.x += f * y.x, o.y += f * y.y, o.z += f * y.z, o.w += f * y.w;
+            }
+        const bool empty = sum == 0.f;
+        const float inv = empty ? 0.f : 1.f / sum;
+        o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+        const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
+        if (p.out_f32) reinterpret_cast<float4 *>(p.out)[out * kLanes + lane] = o;
+        else reinterpret_cast<uint2 *>(p.out)[out * kLanes + lane] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
+    }
+}
+
+cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t smem, void **args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <int D>
 cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
-    bsattn_prefill_kernel<D, kInt8><<<dim3(p.total > 0 ? p.total : 1, (p.Hq + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    using C = Cfg<D>;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, bsattn_prefill_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(bsattn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    const int sms = current_device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const Layout w = make_layout(p.total, p.B, p.c.H, p.G, D, p.keys, sms < kMaxCtas ? sms : kMaxCtas);
+    CUtensorMap tq = {};
+    if (p.total > 0 && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
+    void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w), &tq};
+    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_plan_kernel), dim3(1), kPlanThreads, 0, args, stream);
+    if (e != cudaSuccess || p.total == 0) return e;
+    const long long items = w.tiles * p.c.H;
+    const unsigned blocks = (unsigned)(items < sms * 8ll ? items : sms * 8ll);
+    e = launch_dependent(p.c.int8 ? reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, true>)
+                                  : reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, false>),
+                         dim3(blocks), kWidenThreads, 0, args, stream);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_kernel<D>), dim3((unsigned)w.ctas), kThreads, C::kAlloc, args, stream);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_join_kernel<D>),
+                            dim3((unsigned)w.pieces, 2 * kTile / kJoinRows), kJoinThreads, 0, args, stream);
 }
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int, int, int, int, int, long long) { return 256; }
+size_t prefill_workspace_bytes(int total, int B, int H, int G, int D, long long keys) {
+    return make_layout(total, B, H, G, D, keys, kMaxCtas).total;
+}
 
 cudaError_t launch_prefill(const ChunkParams &p, cudaStream_t stream) {
-    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
-    return p.c.int8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+    return p.c.D == 128 ? launch<128>(p, stream) : launch<64>(p, stream);
 }
 
 }  // namespace bsattn

@@ -7,14 +7,13 @@
 //   K' = bf16(code 2^e), exact: e the binary exponent of the key's scale; what is left of the
 //        scale, r in [1, 2), multiplies the key's scores in fp32, and only in tiles where some
 //        r != 1 (int8; the scales that e4m3 rows are given are powers of two);
-//   V' = fp16(code 2^(f - E + 6)), exact: f the exponent of the value's scale, E (a multiple of 4)
-//        the tile's largest; what is left, u in [1, 2), multiplies the weight before it is
-//        rounded, again only where some u != 1.  Where scales of a tile are more than 2^14 apart
-//        its V' and its weights are bf16 instead, which has the exponents for them and 8 bits.
-// With z_j the scores in units of log2: p_j = 2^(z_j - m + 7) u_j is rounded to fp16 (11 bits)
-// for P V', l sums 2^(z_j - m + 7) in fp32; out = O 2^(E - 6) / l, lse = ln 2 (m - 7 + log2 l).  The
-// reference m is moved only when some weight could pass 2^14 (the output is then rescaled), and
-// O is rescaled to another E only where it is larger or more than 2^8 smaller.
+//   V' = fp16(code vs 2^(6 - E)), E (a multiple of 4) the largest binary exponent of the tile's value
+//        scales vs: exact where vs is a power of two (e4m3), else rounded to 11 bits (a value 2^28 below
+//        the tile's largest may count as 0).
+// With z_j the scores in units of log2: p_j = 2^(z_j - m + 7) is rounded to fp16 (11 bits) for P V',
+// l sums it in fp32; out = O 2^(E - 6) / l, lse = ln 2 (m - 7 + log2 l).  The reference m is moved
+// only when some weight could pass 2^15 (the output is then rescaled), and O is rescaled to
+// another E only where it is larger or more than 2^8 smaller.
 //
 // Work.  A segment is (sequence, KV head, block of 2 x floor(128 / G) tokens): two 128-row
 // tiles ("slots") that share each K/V tile.  It visits the key tiles that its rows meet: all up to
@@ -32,7 +31,7 @@
 //   warp 3      finds the segments of the CTA's pieces, one ahead of the others
 //   warps 4-7, 8-11   slot 0, slot 1: softmax, O rescale, output
 // TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P_t over S_t.
-#include "chunk_common.cuh"
+#include "prefill_plan.cuh"
 #include "kv_codes.cuh"
 
 namespace bsattn {
@@ -47,137 +46,14 @@ constexpr uint32_t kCtrlRegs = 120, kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 2 * 128 * kSoftmaxRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 elements: one 128-byte swizzle span
-constexpr int kMaxCtas = 160;
-constexpr int kSegCost = 2;
-constexpr int kLeastPiece = 4;              // places of a piece: each makes parts for the join
-constexpr int kDescs = 2;                   // segments found ahead
 constexpr int kPlanThreads = 1024, kWidenThreads = 256, kJoinThreads = 256;
 constexpr int kJoinRows = 32;               // rows of a part that a block of the join takes
 
-// Binary exponents (biased) that go into K', and those that go into V' (2^(E - 6) and its inverse are then
-// normal numbers); what lies outside stays in r and u.
-constexpr int kLeastKey = 27, kMostKey = 227, kLeastValue = 7, kMostValue = 227;
-constexpr int kNear = 14;
-constexpr float kLift = 7.f, kReach = 7.f;
-constexpr float kNoKey = -0x1p100f;         // reference before the first key
+// Binary exponents (biased) that go into K' (what lies outside stays in r), and those that E is taken from
+// (2^(E - 6) and its inverse are then normal numbers).
+constexpr int kLeastKey = 27, kMostKey = 227, kLeastValue = 7, kMostValue = 254;
+constexpr float kLift = 7.f, kReach = 8.f;
 
-// Flags of a tile: some r, some u is not 1; bf16 values; some values are not numbers.
-constexpr uint32_t kRestK = 1u, kRestV = 2u, kFar = 4u, kOdd = 8u;
-
-// What goes with a tile: r and u of its keys, the keys that count, E (biased), flags, and the keys whose
-// values are not numbers (NaN or infinite scales, NaN codes).  V' of those is 0, since a NaN times the
-// weight 0 of a query that does not meet the key would be NaN; a query that does is told by its mask.
-struct TileHead {
-    float r[kTile], u[kTile];
-    uint32_t keep[4];
-    int32_t exp;
-    uint32_t flags;
-    int32_t pad[2];
-    uint32_t odd[4];
-};
-static_assert(sizeof(TileHead) % 16 == 0, "copied in pieces of 16 bytes");
-
-// A sequence as the plan kernel leaves it.
-struct SeqPlan {
-    int32_t first, m, n;     // as in Chunk
-    int32_t tile0;           // its first tile in the workspace
-    int32_t sinks, near;     // tiles that some query meets: below sinks, and from near to end
-    int32_t end;
-    int32_t block0, blocks;  // its row blocks (of every head)
-    int32_t pass;            // places of all of a head's blocks in the line
-    long long base;          // first place
-};
-
-struct PlanTotals {
-    long long places;
-    int32_t tiles;
-    int32_t pieces;          // of the line; at most as many as the layout has room for
-};
-
-// A segment, or the part of it that lies in one piece of the line.
-struct SegDesc {
-    int32_t b, h;            // b < 0: no more
-    int32_t token, tokens;   // first packed row, rows' tokens
-    int32_t pos, n;          // position of the first token, keys of the sequence
-    int32_t sinks, near;     // tiles visited: 0 .. sinks - 1, then near, near + 1, ...
-    int32_t count[2];        // how many of them slot t meets
-    int32_t k0, k1;          // those of this piece
-    int32_t tile0;           // where the sequence's tiles lie in the workspace, one after the other:
-    int32_t seq_sinks, seq_near;  // those below seq_sinks, and from seq_near on
-    int32_t part;            // -1: the rows go to the output
-    int32_t pad;
-};
-
-// A segment that is cut: its rows and how many parts there are.
-struct CutInfo {
-    int32_t token, tokens, h, parts;
-};
-
-struct Layout {
-    int tokens;              // of a slot: floor(128 / G)
-    int pieces, ctas;
-    long long tiles;         // of a head that the workspace has room for
-    long long blocks;
-    size_t seq, block_place, totals, cuts, part_o, part_l, k, v, head, total;
-};
-
-// Widened bytes that the CTAs work on at a time: of 129 MB of L2, less what else passes through.
-constexpr long long kPhaseBytes = 64ll << 20;
-
-inline Layout make_layout(int total, int B, int H, int G, int D, long long keys, int ctas) {
-    Layout w = {};
-    w.tokens = kTile / G;
-    w.ctas = ctas;
-    w.tiles = keys / kTile + B;
-    w.blocks = (long long)total / (2 * w.tokens) + B;
-    const long long bytes = w.tiles * H * kTile * D * 4;
-    const long long phases = (bytes + kPhaseBytes - 1) / kPhaseBytes;
-    w.pieces = ctas * (int)(phases < 1 ? 1 : phases > 64 ? 64 : phases);
-    size_t at = 0;
-    auto take = [&](size_t n) {
-        const size_t here = at;
-        at += (n + 255u) & ~(size_t)255u;
-        return here;
-    };
-    w.seq = take((size_t)B * sizeof(SeqPlan));
-    w.block_place = take((size_t)w.blocks * 4u);
-    w.totals = take(sizeof(PlanTotals));
-    w.cuts = take((size_t)w.pieces * sizeof(CutInfo));
-    w.part_l = take((size_t)w.pieces * 2 * 256 * 4);
-    w.part_o = take((size_t)w.pieces * 2 * 256 * D * 4);
-    w.head = take((size_t)w.tiles * H * sizeof(TileHead));
-    w.k = take((size_t)w.tiles * H * kTile * D * 2);
-    w.v = take((size_t)w.tiles * H * kTile * D * 2);
-    w.total = at;
-    return w;
-}
-
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 2^d of an integer d, 0 below 2^-126.
-__device__ __forceinline__ float pow2(int d) { return d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + min(d, 127)) << 23); }
-
-// Tiles that queries at positions i0 .. i1 of a sequence of n keys visit: 0 .. sinks - 1 and near .. end - 1.
-struct Visit {
-    int sinks, near, end;
-    __device__ __forceinline__ int count() const { return sinks + end - near; }
-};
-
-__device__ __forceinline__ Visit visit(const ChunkParams &p, int n, int i0, int i1) {
-    Visit v;
-    const int ha = met(p, i1, n).ha;
-    v.end = (ha + kTile - 1) / kTile;
-    v.sinks = v.near = 0;
-    if (p.kind == BSATTN_MASK_SLIDING_WINDOW) {
-        v.near = min(met(p, i0, n).la / kTile, v.end);
-        v.sinks = min((int)(((long long)p.sink_tokens + kTile - 1) / kTile), v.near);
-    }
-    return v;
-}
 
 // ------------------------------------------------------------------- plan --
 
@@ -208,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
     grid_dependency_wait();
     SeqPlan *seq = reinterpret_cast<SeqPlan *>(p.ws + w.seq);
     int32_t *place = reinterpret_cast<int32_t *>(p.ws + w.block_place);
-    const int step = 2 * w.tokens, tid = threadIdx.x, lane = tid % 32;
+    const int step = w.step, tid = threadIdx.x, lane = tid % 32;
     long long tiles = 0, blocks = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
@@ -224,7 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
         }
         long long sum;
         s.tile0 = (int)min(tiles + block_scan(s.sinks + s.end - s.near, &sum, warps), (long long)INT32_MAX);
-        if (s.m > 0 && (long long)s.tile0 + s.sinks + s.end - s.near > w.tiles) {
+        if (!w.few && s.m > 0 && (long long)s.tile0 + s.sinks + s.end - s.near > w.tiles) {
             // no room for its keys
             if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
             s.m = s.blocks = s.sinks = s.near = s.end = 0;
@@ -269,7 +145,9 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
         PlanTotals t = {};
         t.places = places;
         t.tiles = (int)min(tiles, w.tiles);
-        t.pieces = (int)max(1ll, min((long long)w.pieces, places / kLeastPiece));
+        // so many phases that the keys of one fit L2
+        const long long phases = w.few ? 1 : (t.tiles * (long long)p.c.H * (kTile * 4 * p.c.D) + kPhaseBytes - 1) / kPhaseBytes;
+        t.pieces = (int)max(1ll, min(min((long long)w.pieces, w.ctas * max(phases, 1ll)), places / kLeastPiece));
         *reinterpret_cast<PlanTotals *>(p.ws + w.totals) = t;
     }
 }
@@ -283,8 +161,8 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
     constexpr int kRowLanes = D / 16, kRows = kWidenThreads / kRowLanes, kSteps = kTile / kRows;
     __shared__ int s_row[kTile];                 // cache row of each key, -1: none
     __shared__ float s_k[kTile];                 // 2^e
-    __shared__ int s_f[kTile];                   // f (biased)
-    __shared__ int s_top[4], s_far[4];
+    __shared__ float s_v[kTile];                 // vs 2^(6 - E)
+    __shared__ int s_top[4];
     __shared__ uint32_t s_keep[4], s_rest[4], s_odd[4];
     __shared__ int s_nan[kTile];                 // the key's value is not a number
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -319,19 +197,17 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
             s_k[tid] = pow2(e - 127);
             ks *= pow2(127 - e);
             const bool number = vb < 0x7f800000u;
-            // rows of zeros have the smallest scale; they, NaN and infinity do not count for E (f = E, then)
+            // rows of zeros have the smallest scale; they, NaN and infinity do not count for E
             f = row >= 0 && number && vb > 1u << 23 ? min(max((int)(vb >> 23), kLeastValue), kMostValue) : 0;
             s_nan[tid] = number ? 0 : 1;
             const int top = __reduce_max_sync(0xffffffffu, max(f, kLeastValue));
             if (lane == 0) s_top[warp] = top;
             const uint32_t keep = __ballot_sync(0xffffffffu, row >= 0);
-            const int least = __reduce_min_sync(0xffffffffu, f > 0 ? f : 1000);
-            if (lane == 0) s_keep[warp] = keep, s_far[warp] = least;
+            if (lane == 0) s_keep[warp] = keep;
         }
         __syncthreads();
         const int exp = (max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3])) + 3) & ~3;
-        const bool far = exp - min(min(s_far[0], s_far[1]), min(s_far[2], s_far[3])) > kNear;
-        if (tid < kTile) s_f[tid] = f = f > 0 ? f : exp;
+        if (tid < kTile) s_v[tid] = vs * pow2(133 - exp);
         const long long at = (long long)h * w.tiles + slot;
         TileHead *head = reinterpret_cast<TileHead *>(p.ws + w.head) + at;
         const int piece = tid % kRowLanes, sub = tid / kRowLanes;
@@ -358,10 +234,8 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
         __syncthreads();
         if (tid < kTile) {
             const bool odd = s_nan[tid] != 0;
-            vs = odd || s_row[tid] < 0 ? 1.f : vs * pow2(127 - f);
             head->r[tid] = ks;
-            head->u[tid] = vs;
-            const uint32_t rest = (__any_sync(0xffffffffu, ks != 1.f) ? kRestK : 0u) | (__any_sync(0xffffffffu, vs != 1.f) ? kRestV : 0u);
+            const uint32_t rest = __any_sync(0xffffffffu, ks != 1.f) ? kRest : 0u;
             const uint32_t odds = __ballot_sync(0xffffffffu, odd);
             if (lane == 0) s_rest[warp] = rest | (odds ? kOdd : 0u), s_odd[warp] = odds;
         }
@@ -370,14 +244,14 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
             *reinterpret_cast<uint4 *>(head->keep) = make_uint4(s_keep[0], s_keep[1], s_keep[2], s_keep[3]);
             *reinterpret_cast<uint4 *>(head->odd) = make_uint4(s_odd[0], s_odd[1], s_odd[2], s_odd[3]);
             head->exp = exp;
-            head->flags = s_rest[0] | s_rest[1] | s_rest[2] | s_rest[3] | (far ? kFar : 0u);
+            head->flags = s_rest[0] | s_rest[1] | s_rest[2] | s_rest[3];
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = i * kRows + sub;
-            const float kf = s_k[r], vf = pow2(s_f[r] - exp + 6);
-            if (s_nan[r]) x[1][i] = make_uint4(0, 0, 0, 0);
-            const uint32_t vh = pack_f16x2(vf, vf);
+            const bool nan = s_nan[r] != 0;
+            const float kf = s_k[r], vf = nan ? 0.f : s_v[r];
+            if (nan) x[1][i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int values = 0; values < 2; ++values) {
                 const uint32_t y[4] = {x[values][i].x, x[values][i].y, x[values][i].z, x[values][i].w};
@@ -388,16 +262,12 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
                     codes_to_f16x2<kInt8>(y[q], c2[0], c2[1]);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        if (values && !far) {
-                            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * q + k]) : "r"(c2[k]), "r"(vh));
-                        } else {
-                            float a, c;
-                            asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
-                                : "=f"(a), "=f"(c)
-                                : "r"(c2[k]));
-                            const float f32 = values ? vf : kf;
-                            o[2 * q + k] = pack_bf16x2(a * f32, c * f32);
-                        }
+                        float a, c;
+                        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+                            : "=f"(a), "=f"(c)
+                            : "r"(c2[k]));
+                        const float f32 = values ? vf : kf;
+                        o[2 * q + k] = values ? pack_f16x2(a * f32, c * f32) : pack_bf16x2(a * f32, c * f32);
                     }
                 }
                 uint8_t *dst = p.ws + (values ? w.v : w.k) + at * (kTile * D * 2) + (size_t)(piece >> 2) * kSub + r * 128;
@@ -416,8 +286,7 @@ struct Cfg {
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + 2 * kTileBytes;
     static constexpr uint32_t kHead = kV + 2 * kTileBytes;
-    static constexpr uint32_t kEpi = kHead + 2 * (uint32_t)sizeof(TileHead);   // 2 KB per softmax warp
-    static constexpr uint32_t kDesc = kEpi + 8u * 2048u;
+    static constexpr uint32_t kDesc = kHead + 2 * (uint32_t)sizeof(TileHead);
     static constexpr uint32_t kBar = kDesc + kDescs * (uint32_t)sizeof(SegDesc);
     // K / V stage full and empty, per slot: query tile full and empty, S ready, two halves of P
     // ready, O complete; descriptor full and empty
@@ -429,132 +298,16 @@ struct Cfg {
     static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > 32 ? 32 : hi;
-    if (hi <= lo) return 0u;
-    return (hi >= 32 ? 0xffffffffu : ((1u << hi) - 1u)) & ~((1u << lo) - 1u);
-}
-
-// Waiting for one of the CTA's barriers; false where the CTA gives up.
-struct Waiter {
-    uint32_t bars;
-    volatile int *abort;
-    int *err;
-    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
-    __device__ __forceinline__ bool operator()(int i, uint32_t phase) const {
-        return mbar_wait(bar(i), phase & 1u, abort, err, BSATTN_FLAG_TIMEOUT);
+// 32 bytes; `whole`: the address is a multiple of 32.
+__device__ __forceinline__ void store32(uint8_t *dst, const uint32_t *v, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
-};
-
-// Reads the next segment's descriptor (the whole warp), and gives its place back.
-template <int D>
-__device__ __forceinline__ bool next_desc(const Waiter &wait, const uint8_t *smem, uint32_t &count, SegDesc &d) {
-    using C = Cfg<D>;
-    const int slot = (int)(count % kDescs);
-    if (!__all_sync(0xffffffffu, wait(C::bUF + slot, count / kDescs))) return false;
-    d = reinterpret_cast<const SegDesc *>(smem + C::kDesc)[slot];
-    __syncwarp();
-    if (lane_id() == 0) mbar_arrive(wait.bar(C::bUE + slot));
-    ++count;
-    return d.b >= 0;
-}
-
-// Finds the segments of the CTA's pieces and writes their descriptors.
-template <int D>
-__device__ __forceinline__ void schedule_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint8_t *smem) {
-    using C = Cfg<D>;
-    const SeqPlan *seq = reinterpret_cast<const SeqPlan *>(p.ws + w.seq);
-    const int32_t *place = reinterpret_cast<const int32_t *>(p.ws + w.block_place);
-    CutInfo *cuts = reinterpret_cast<CutInfo *>(p.ws + w.cuts);
-    const PlanTotals totals = *reinterpret_cast<const PlanTotals *>(p.ws + w.totals);
-    const long long line = totals.places;
-    const int step = 2 * w.tokens, pieces = totals.pieces;
-    uint32_t count = 0;
-    bool ok = true;
-    for (int piece = blockIdx.x; piece < w.pieces; piece += w.ctas) cuts[piece] = CutInfo{};   // also of pieces not come to
-    auto emit = [&](const SegDesc &d) -> bool {
-        const int slot = (int)(count % kDescs);
-        if (!(ok = wait(C::bUE + slot, (count / kDescs) ^ 1u))) return false;
-        reinterpret_cast<SegDesc *>(smem + C::kDesc)[slot] = d;
-        mbar_arrive(wait.bar(C::bUF + slot));
-        ++count;
-        return true;
-    };
-    for (int piece = blockIdx.x; ok && piece < pieces; piece += w.ctas) {
-        const long long from = line * piece / pieces, to = line * (piece + 1) / pieces;
-        CutInfo cut = {};
-        if (from < to) {
-            int b = 0, hi = p.B - 1;             // the last sequence that begins at or before `from`
-            while (b < hi) {
-                const int mid = (b + hi + 1) / 2;
-                if (seq[mid].base <= from) b = mid;
-                else hi = mid - 1;
-            }
-            SeqPlan s = seq[b];
-            int h = s.pass > 0 ? (int)((from - s.base) / s.pass) : 0;
-            int r = 0;
-            if (s.pass > 0) {
-                const int off = (int)(from - s.base - (long long)h * s.pass);
-                int top = s.blocks - 1;
-                while (r < top) {
-                    const int mid = (r + top + 1) / 2;
-                    if (place[s.block0 + mid] <= off) r = mid;
-                    else top = mid - 1;
-                }
-            }
-            while (ok) {
-                if (r >= s.blocks) {
-                    r = 0;
-                    if (++h >= p.c.H || s.blocks == 0) {
-                        h = 0;
-                        if (++b >= p.B) break;
-                        s = seq[b];
-                        continue;
-                    }
-                }
-                const long long begin = s.base + (long long)h * s.pass + place[s.block0 + r];
-                if (begin >= to) break;
-                SegDesc d = {};
-                d.b = b, d.h = h, d.n = s.n;
-                d.token = s.first + r * step, d.tokens = min(step, s.m - r * step);
-                d.pos = s.n - s.m + r * step;
-                d.part = -1;
-                int tiles = 0;
-                if (s.n > 0) {
-                    const Visit v = visit(p, s.n, d.pos, d.pos + d.tokens - 1);
-                    d.sinks = v.sinks, d.near = v.near;
-                    tiles = v.count();
-                    // slot 0 meets no tile past its own last position
-                    const int mine = (met(p, d.pos + min(w.tokens, d.tokens) - 1, s.n).ha + kTile - 1) / kTile;
-                    d.count[0] = v.sinks + max(mine - v.near, 0);
-                    d.count[1] = d.tokens > w.tokens ? tiles : 0;
-                    d.tile0 = s.tile0, d.seq_sinks = s.sinks, d.seq_near = s.near;
-                }
-                const long long first = begin + kSegCost;   // place of its first tile
-                d.k0 = (int)max(from - first, 0ll);
-                d.k1 = (int)min(to - first, (long long)tiles);
-                if (tiles == 0 ? begin >= from : d.k1 > d.k0) {
-                    if (tiles == 0) d.k0 = d.k1 = 0;
-                    else if (d.k0 > 0 || d.k1 < tiles) {
-                        d.part = 2 * piece + (d.k0 > 0 ? 0 : 1);
-                        if (d.k0 == 0) {
-                            // the piece that holds the last tile: place x is in piece ((x + 1) pieces - 1) / line
-                            const int last = (int)(((first + tiles) * pieces - 1) / line);
-                            cut.token = d.token, cut.tokens = d.tokens, cut.h = h, cut.parts = last - piece + 1;
-                        }
-                    }
-                    if (!emit(d)) break;
-                }
-                ++r;
-            }
-        }
-        cuts[piece] = cut;
-    }
-    if (!ok) return;
-    SegDesc stop = {};
-    stop.b = -1;
-    emit(stop);
 }
 
 // One slot: warps 4-7 (t = 0) or 8-11 (t = 1), one row per thread.
@@ -570,7 +323,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
     uint32_t descs = 0, sc = 0, od = 0, tile0 = 0;   // descriptors; phases of S and O; tiles of earlier segments
     bool ok = true;
     SegDesc d;
-    while (ok && next_desc<D>(wait, smem, descs, d)) {
+    while (ok && next_desc<C>(wait, smem, descs, d)) {
         const int tok = t * w.tokens + token_of;     // of the segment
         const bool row_ok = token_of < w.tokens && tok < d.tokens;
         const int end = min(d.k1, d.count[t]);
@@ -619,7 +372,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                 for (int x = 3; x < 31; x += 2) a = fmax3(a, s[32 * g + x], s[32 * g + x + 1]);
                 hm[g] = fmaxf(a, s[32 * g + 31]);
             };
-            const bool rest = ((uint32_t)info.y & kRestK) != 0;
+            const bool rest = ((uint32_t)info.y & kRest) != 0;
             if (rest) {
                 const float4 *r = reinterpret_cast<const float4 *>(head->r);
 #pragma unroll
@@ -670,7 +423,6 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(wait.bar(C::bPR + 2 * t + half));
             };
-            const bool weighted = ((uint32_t)info.y & kRestV) != 0 || unit != 1.f, far = ((uint32_t)info.y & kFar) != 0;
             if (__builtin_expect(((uint32_t)info.y & kOdd) != 0, 0)) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -678,37 +430,26 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                     nan |= (head->odd[g] & (span_bits(own.la - c, own.ha - c) | span_bits(0, own.hb - c))) != 0u;
                 }
             }
+            const bool usual = unit == 1.f;
             auto half = [&](int c) {
                 uint32_t pk[32];
+                if (__builtin_expect(usual, 1)) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float x0, x1;
-                    ffma2(x0, x1, s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1], sl2, sl2, nm, nm);
-                    x0 = ex2_approx(x0);
-                    x1 = ex2_approx(x1);
-                    if (x & 1) fadd2(lb0, lb1, lb0, lb1, x0, x1);
-                    else fadd2(la0, la1, la0, la1, x0, x1);
-                    s[c * 64 + 2 * x] = x0;
-                    s[c * 64 + 2 * x + 1] = x1;
-                }
-                if (weighted) {
-                    const float4 *u = reinterpret_cast<const float4 *>(head->u) + 16 * c;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        float4 f = u[x];
-                        fmul2(f.x, f.y, f.x, f.y, unit, unit);
-                        fmul2(f.z, f.w, f.z, f.w, unit, unit);
-                        float *y = s + c * 64 + 4 * x;
-                        fmul2(y[0], y[1], y[0], y[1], f.x, f.y);
-                        fmul2(y[2], y[3], y[2], y[3], f.z, f.w);
+                    for (int x = 0; x < 32; ++x) {
+                        float x0, x1;
+                        ffma2(x0, x1, s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1], sl2, sl2, nm, nm);
+                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
+                        else fadd2(la0, la1, la0, la1, p0, p1);
+                        pk[x] = pack_f16x2(p0, p1);
                     }
-                }
-                if (__builtin_expect(far, 0)) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1]);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) pk[x] = pack_f16x2(s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1]);
+                    for (int x = 0; x < 32; ++x) {
+                        const float p0 = ex2_approx(fmaf(s[c * 64 + 2 * x], sl2, nm)), p1 = ex2_approx(fmaf(s[c * 64 + 2 * x + 1], sl2, nm));
+                        la0 += p0, la1 += p1;
+                        pk[x] = pack_f16x2(p0 * unit, p1 * unit);
+                    }
                 }
                 tmem_st32(lane_addr + s_col + c * 32, pk);
             };
@@ -744,32 +485,13 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
         const bool empty = !any || l_run == 0.f;     // NaN is not empty
         const float inv = empty ? 0.f : nan ? __uint_as_float(0x7fc00000u) : 1.f / l_run;
         const float scale = any ? pow2(exp_run - 127 - 6) : 0.f;
-        // A block of 64 bytes of every row goes through the warp's scratch (16-byte pieces at piece ^
-        // (row / 2 mod 4)) and comes back with lane 4 g + j holding piece j of row 8 i + g: each store
-        // writes 8 whole pieces of 64 bytes.
+        // Each lane writes its row, whole sectors of 32 bytes at a time.
         const bool part = d.part >= 0;
         const long long out_row = part ? ((long long)d.part * 2 + t) * kTile + row
                                        : (long long)(d.token + tok) * p.Hq + d.h * p.G + head_of;
         const bool half_words = !part && !p.out_f32;
-        const long long row_bytes = D * (half_words ? 2 : 4);
-        const long long dst = row_ok ? out_row * row_bytes : -1;
-        uint8_t *out = part ? p.ws + w.part_o : static_cast<uint8_t *>(p.out);
-        uint4 *scr = reinterpret_cast<uint4 *>(smem + C::kEpi + (warp - 4u) * 2048u);
-        const int gl = (int)(lane & 3u), rl = (int)(lane >> 2);
-        auto store = [&](uint32_t (&x)[16], int block) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                scr[lane * 4u + ((uint32_t)i ^ ((lane >> 1) & 3u))] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rr = 8 * i + rl;
-                const uint4 y = scr[rr * 4 + (gl ^ ((rr >> 1) & 3))];
-                const long long at = __shfl_sync(0xffffffffu, dst, rr);
-                if (at >= 0) *reinterpret_cast<uint4 *>(out + at + block * 64 + gl * 16) = y;
-            }
-            __syncwarp();
-        };
+        uint8_t *dst = (part ? p.ws + w.part_o : static_cast<uint8_t *>(p.out)) + out_row * (D * (half_words ? 2 : 4));
+        const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -780,19 +502,16 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
             }
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = empty ? 0u : __float_as_uint(__uint_as_float(v[x]) * inv * scale);
-            uint32_t y[16];
-            if (half_words) {
+            if (row_ok && half_words) {
 #pragma unroll
-                for (int x = 0; x < 16; ++x) y[x] = pack_bf16x2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
-                store(y, c);
-            } else {
+                for (int x = 0; x < 16; ++x) v[x] = pack_bf16x2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
+                store32(dst + c * 64, v, sectors);
+                store32(dst + c * 64 + 32, v + 8, sectors);
+            } else if (row_ok) {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) y[x] = v[16 * hf + x];
-                    store(y, 2 * c + hf);
-                }
+                for (int x = 0; x < 4; ++x) store32(dst + c * 128 + 32 * x, v + 8 * x, sectors);
             }
+            __syncwarp();
         }
         if (row_ok) {
             const float lse2 = empty ? -INFINITY : m_run - kLift + lg2_approx(l_run);
@@ -862,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_bytes = (uint32_t)(p.G * w.tokens) * D * 2u;
         bool ok = true;
         SegDesc d;
-        while (ok && next_desc<D>(wait, smem, descs, d)) {
+        while (ok && next_desc<C>(wait, smem, descs, d)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (!ok || min(d.k1, d.count[t]) <= d.k0) continue;
@@ -905,8 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp runs in step; lane 0 issues.
         const uint32_t lead = lane == 0 ? 1u : 0u;
         constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
-        constexpr uint32_t idesc_pv16 = idesc_bf16_f32(128, D, true);
-        constexpr uint32_t idesc_pv = idesc_pv16 & ~((1u << 7) | (1u << 10));   // fp16 A and B
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true) & ~((1u << 7) | (1u << 10));   // fp16 A and B
         const uint64_t desc_q = smem_desc_sw128(base + C::kQ, 16, 1024);
         const uint64_t desc_k = smem_desc_sw128(base + C::kK, 16, 1024);
         const uint64_t desc_v = smem_desc_sw128(base + C::kV, kSub, 1024);
@@ -928,8 +646,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto output = [&](int t, uint32_t it, bool first) -> bool {
             if (!ready(C::bVF + (int)(it & 1u), it >> 1)) return false;
-            const TileHead *head = reinterpret_cast<const TileHead *>(smem + C::kHead) + (it & 1u);
-            const uint32_t idesc = (head->flags & kFar) ? idesc_pv16 : idesc_pv;
             const uint64_t vd = desc_v + (uint64_t)(it & 1u) * kTileUnits;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -937,14 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                    mma_ts_lead(lead, tmem + 256 + t * D, tmem + t * 128 + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)), idesc,
+                    mma_ts_lead(lead, tmem + 256 + t * D, tmem + t * 128 + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)), idesc_pv,
                                 kk > 0 || !first ? 1u : 0u);
             }
             ++pc[t];
             return true;
         };
         SegDesc d;
-        while (ok && next_desc<D>(wait, smem, descs, d)) {
+        while (ok && next_desc<C>(wait, smem, descs, d)) {
             const int end[2] = {min(d.k1, d.count[0]), min(d.k1, d.count[1])};
             for (int t = 0; t < 2; ++t)
                 if (end[t] > d.k0) {
@@ -981,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(wait.bar(C::bDrain), 0);
     } else if (warp < 4) {
         regs_release<kCtrlRegs>();
-        if (warp == 3 && lane == 0) schedule_role<D>(p, w, wait, smem);
+        if (warp == 3 && lane == 0) schedule_role<C>(p, w, wait, smem);
         __syncwarp();
     } else {
         regs_claim<kSoftmaxRegs>();
@@ -1043,20 +759,6 @@ __global__ void __launch_bounds__(kJoinThreads) bsattn_prefill_join_kernel(const
     }
 }
 
-cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t smem, void **args, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelExC(&cfg, kernel, args);
-}
-
 template <int D>
 cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     using C = Cfg<D>;
@@ -1079,10 +781,16 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     const Layout w = make_layout(p.total, p.B, p.c.H, p.G, D, p.keys, sms < kMaxCtas ? sms : kMaxCtas);
     CUtensorMap tq = {};
-    if (p.total > 0 && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
+    if (p.total > 0 && !w.few && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
     void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w), &tq};
     e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_plan_kernel), dim3(1), kPlanThreads, 0, args, stream);
     if (e != cudaSuccess || p.total == 0) return e;
+    const unsigned join_rows = (w.few ? kTile : 2 * kTile) / kJoinRows;
+    const auto join = reinterpret_cast<const void *>(bsattn_prefill_join_kernel<D>);
+    if (w.few) {
+        e = launch_prefill_rows(p, w, stream);
+        return e != cudaSuccess ? e : launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinThreads, 0, args, stream);
+    }
     const long long items = w.tiles * p.c.H;
     const unsigned blocks = (unsigned)(items < sms * 8ll ? items : sms * 8ll);
     e = launch_dependent(p.c.int8 ? reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, true>)
@@ -1091,11 +799,24 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_kernel<D>), dim3((unsigned)w.ctas), kThreads, C::kAlloc, args, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_join_kernel<D>),
-                            dim3((unsigned)w.pieces, 2 * kTile / kJoinRows), kJoinThreads, 0, args, stream);
+    return launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinThreads, 0, args, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t smem, void **args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
 
 size_t prefill_workspace_bytes(int total, int B, int H, int G, int D, long long keys) {
     return make_layout(total, B, H, G, D, keys, kMaxCtas).total;

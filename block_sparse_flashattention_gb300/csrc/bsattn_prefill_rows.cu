@@ -1,0 +1,717 @@
+// Attention of chunks of few new tokens over a paged 8-bit K/V cache: up to 128 query rows of a KV head
+// share each key, which is widened in shared memory on its way (more rows: bsattn_prefill.cu, whose line of
+// work and parts this kernel shares).
+//
+// With few rows HBM bounds it: 2 (D + 4) bytes per key and KV head.  So the keys lie on the tensor cores' 128
+// rows and the queries on their columns, of which there are 16 to 128:
+//   S^T = K' Q'^T,  O^T += V'^T P^T,
+//   K' = fp16(code), V' = fp16(code), exact, no scale in either; Q' = fp16(q 2^-e) with the row's largest
+//   binary exponent e (exact for every element down to 2^-14 of the largest).
+// A thread has one key of the tile: its scales are two registers, z_r = S_r c_r ks (c_r = softmax_scale
+// log2(e) 2^e of row r) and p_r = 2^(z_r - m_r + 7); p_r vs 2^-E is rounded to fp16 (11 bits) for V'^T P^T,
+// and the thread sums p_r of its keys by itself, in fp32.  Only at a segment's end are sums joined over the
+// threads.  The reference m_r (per query row, kept by all) and E (the largest binary exponent of a value scale so
+// far, a multiple of 4) are moved only when some weight could pass 2^14 or some scale passes E: the threads
+// vote on every tile, and the maxima over the keys, which cost a pass of their own, are taken then.
+//
+// Up to 64 rows two groups of threads take the tiles in turn, each with sums of its own, joined at the end: while
+// one group's weights are formed, the other's products run.  With more, each group has 64 of the rows.
+//
+// Roles (640 threads, one CTA per SM):
+//   warp 0        issues the MMAs
+//   warp 1        owns the TMEM allocation; finds the segments of the CTA's piece of the line
+//   warps 2, 3    fetch the codes of keys, of values: bulk copies of 16 keys into a ring of raw tiles
+//   warps 4-7, 8-11   group 0, group 1: query rows, weights, output
+//   warps 12-15   widen the codes of keys (128-byte swizzle, a tile's rows K-major)
+//   warps 16-19   the same for values, as they lie (MN-major)
+// TMEM: S^T of group g [64 g, 64 g + 64), O^T of group g [128 + 64 g, 192 + 64 g).
+#include <type_traits>
+
+#include "kv_codes.cuh"
+#include "prefill_plan.cuh"
+
+namespace bsattn {
+
+namespace {
+
+constexpr int kThreads = 640;
+constexpr uint32_t kTmemCols = 256;
+// 96 registers per thread at launch: 128 * 48 + 2 * 128 * 160 + 2 * 128 * 56 = 61440 = 640 * 96.
+constexpr int kLaunchRegs = 96;
+constexpr uint32_t kCtrlRegs = 48, kGroupRegs = 160, kWidenRegs = 56;
+static_assert(128 * kCtrlRegs + 256 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 fp16: one 128-byte swizzle span
+constexpr int kCols = 64;                   // query rows of a group
+constexpr float kLift = 7.f, kReach = 7.f;
+
+template <int D>
+struct Cfg {
+    static constexpr uint32_t kTileBytes = kTile * D * 2, kRawBytes = kTile * D;
+    static constexpr uint32_t kQ = 0, kK = kQ + kTileBytes, kV = kK + kTileBytes, kP = kV + 2 * kTileBytes;
+    static constexpr uint32_t kRaw = kP + 2 * kSub;                  // K0, K1, V0, V1
+    static constexpr uint32_t kStat = kRaw + 4 * kRawBytes;          // see Stat
+    static constexpr uint32_t kStatBytes = 128 * 4 * 2 + 2 * kCols * 4 * 2 + 128 + 2 * 128 + 64;
+    static constexpr uint32_t kDesc = (kStat + kStatBytes + 15u) & ~15u;
+    static constexpr uint32_t kBar = kDesc + kDescs * (uint32_t)sizeof(SegDesc);
+    // K' full and empty, V' stages full and empty, query rows there, per group: S ready, P ready, O complete;
+    // raw K / V stages full and empty (2 v + stage); descriptor full and empty
+    static constexpr int bKF = 0, bKE = 1, bVF = 2, bVE = 4, bQF = 6, bSR = 7, bPR = 9, bOD = 11, bRF = 13, bRE = 17, bUF = 21,
+                         bUE = bUF + kDescs, bDrain = bUE + kDescs, kNumBars = bDrain + 1;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort, [2..3] raw V tiles' groups
+    static constexpr uint32_t kAlloc = kMisc + 32;
+    static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+
+// Numbers of the segment's rows, in shared memory.
+struct Stat {
+    float c[128];            // c_r, 0 of rows that are none
+    int32_t out[128];        // row of the output or the parts, -1: none
+    float nm[2][kCols];      // 7 - m_r of the groups' rows, -inf of rows that are none
+    float alpha[2][kCols];   // what sums are multiplied by when m moves; at the end what O is
+    uint8_t bad[128];        // the row meets a value that is not a number
+    uint8_t odd[2][128];     // keys of the V' stages that have a NaN code
+    int32_t exp[2], any[2], pad[12];
+};
+static_assert(sizeof(Stat) == Cfg<64>::kStatBytes, "stat area");
+
+// Threads of a group, or of both, meet; whether `x` holds for one of them.
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\tbarrier.cta.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(x ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool any_of_both(bool x) { return any_of(1, 256, x); }
+__device__ __forceinline__ bool any_of_group(int g, bool x) { return any_of(2 + g, 128, x); }
+__device__ __forceinline__ void group_sync(int g) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + g) : "memory"); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Largest of a float over the warp, NaN left out.
+__device__ __forceinline__ float warp_max(float x) {
+    const int b = x == x ? __float_as_int(x) : (int)0xff800000;
+    const int y = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+    return __int_as_float(y ^ ((y >> 31) & 0x7fffffff));
+}
+
+// Key tile k of a segment's visiting list.
+__device__ __forceinline__ int tile_of(const SegDesc &d, int k) { return k < d.sinks ? k : k - d.sinks + d.near; }
+
+// One group: 128 threads, one key of a tile each.
+template <int D, bool kInt8>
+__device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint32_t tmem, int g,
+                                           uint32_t warp, uint32_t lane, uint8_t *smem) {
+    using C = Cfg<D>;
+    Stat *st = reinterpret_cast<Stat *>(smem + C::kStat);
+    const uint32_t quarter = warp & 3u;
+    const int key = (int)(quarter * 32 + lane), sw = (int)warp - 4;
+    const uint32_t s_addr = tmem + ((quarter * 32u) << 16) + (uint32_t)g * kCols, o_addr = s_addr + 2 * kCols;
+    uint8_t *pbuf = smem + C::kP + (uint32_t)g * kSub;
+    float *red = reinterpret_cast<float *>(pbuf);     // [4][64] while no weights are in the buffer, then 4 exponents
+    auto sums = [&](int of) -> float * { return reinterpret_cast<float *>(smem + C::kP + (uint32_t)of * kSub) + 5 * kCols; };
+    uint32_t descs = 0, sc = 0, od = 0, tile0 = 0;
+    SegDesc d;
+    while (true) {
+        const bool got = next_desc<C>(wait, smem, descs, d);
+        if (any_of_both(!got)) break;
+        const int rows = d.tokens * p.G;
+        const bool turns = rows <= kCols;
+        const int row0 = turns ? 0 : kCols * g, cols = turns ? rows : min(max(rows - row0, 0), kCols);
+        const int chunks = (cols + 15) / 16;
+        // ---- query rows: fp16 of q 2^-e (K-major, swizzled), D / 8 lanes to a row
+        if (16 * sw < rows) {
+            constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kSteps = 16 / kRows;
+            const int piece = (int)lane % kRowLanes, sub = (int)lane / kRowLanes;
+            uint4 x[kSteps];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int r = 16 * sw + i * kRows + sub, tok = r / p.G;
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (r < rows)
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (long long)(d.token + tok) * p.q_stride +
+                                                                 (long long)(d.h * p.G + r - tok * p.G) * D) + piece);
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int r = 16 * sw + i * kRows + sub;
+                uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, a = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a = __vmaxu2(a, y[k] & 0x7fff7fffu);
+                a = max(a & 0xffffu, a >> 16);
+#pragma unroll
+                for (int s = 1; s < kRowLanes; s <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, s));
+                // zero rows and rows that are not finite stay as they are
+                const int e = a == 0 || a >= 0x7f80u ? 127 : min(max((int)(a >> 7), 1), 253);
+                const float f = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[k] = pack_f16x2(__uint_as_float(y[k] << 16) * f, __uint_as_float(y[k] & 0xffff0000u) * f);
+                const uint32_t at = C::kQ + (uint32_t)(piece >> 3) * kSub + (uint32_t)r * 128u + ((((uint32_t)piece & 7u) ^ ((uint32_t)r & 7u)) << 4);
+                *reinterpret_cast<uint4 *>(smem + at) = make_uint4(y[0], y[1], y[2], y[3]);
+                if (piece == 0) {
+                    const int tok = r / p.G;
+                    st->c[r] = r < rows ? p.scale_log2 * __uint_as_float((uint32_t)e << 23) : 0.f;
+                    st->out[r] = r >= rows ? -1 : d.part >= 0 ? d.part * 2 * kTile + r : (d.token + tok) * p.Hq + d.h * p.G + r - tok * p.G;
+                }
+            }
+        }
+        if (key < kCols) {
+            st->nm[g][key] = key < cols ? kLift - kNoKey : -INFINITY;
+            st->bad[kCols * g + key] = 0;
+        }
+        fence_proxy_async_smem();
+        any_of_both(false);
+        if (lane == 0) mbar_arrive(wait.bar(C::bQF));
+        // ---- the group's tiles
+        float l[kCols];
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) l[x] = 0.f;
+        int exp_run = 0;
+        bool ok = true, begun = false;
+        const int step = turns ? 2 : 1, k_first = turns ? d.k0 + g : d.k0;
+        const int32_t *table = p.table + (long long)d.b * p.table_stride;
+        // scales of the thread's key in the next tile; row -1: no such key
+        long long row_next = -1;
+        float ks_next = 0.f, vs_next = 0.f;
+        auto look = [&](int k) {
+            const int j = tile_of(d, k) * kTile + key;
+            row_next = k < d.k1 && j < d.n ? cache_row(p.c, table, d.h, j) : -1;
+            if (row_next >= 0) ks_next = __ldg(p.c.ks + row_next), vs_next = __ldg(p.c.vs + row_next);
+        };
+        look(k_first);
+        for (int k = k_first; k < d.k1; k += step) {
+            const uint32_t it = tile0 + (uint32_t)(k - d.k0), stage = it & 1u;
+            const bool there = row_next >= 0;
+            const float ks = there ? ks_next : 0.f;
+            float vs = there ? vs_next : 0.f;
+            const int j = tile_of(d, k) * kTile + key;
+            look(k + step);
+            // rows that meet the key: lo <= r < hi
+            int lo = 0, hi = 0;
+            if (there) {
+                hi = rows;
+                if (p.kind == BSATTN_MASK_CAUSAL || p.kind == BSATTN_MASK_SLIDING_WINDOW || (p.kind == BSATTN_MASK_PREFIX && j >= p.prefix_len))
+                    lo = min(max(j - d.pos, 0), d.tokens) * p.G;
+                if (p.kind == BSATTN_MASK_SLIDING_WINDOW && j >= p.sink_tokens)
+                    hi = (int)min(max((long long)j + p.window_left - d.pos, 0ll), (long long)d.tokens) * p.G;
+            }
+            lo -= row0, hi -= row0;
+            const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < cols);
+            const uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
+            const int vexp = vb < 0x7f800000u && vb > 1u << 23 ? (int)(vb >> 23) : 0;
+            ok = __all_sync(0xffffffffu, wait(C::bSR + g, sc) && (kInt8 || wait(C::bVF + (int)stage, it >> 1)));
+            ++sc;
+            tc_fence_after();
+            if (there && (vb >= 0x7f800000u || (!kInt8 && ok && st->odd[stage][key]))) {
+                vs = 0.f;
+                for (int r = max(lo, 0); r < min(hi, cols); ++r) st->bad[kCols * g + r] = 1;
+            }
+            float a[kCols];
+            auto weights = [&](bool with_m) -> float {
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= chunks) break;
+                    uint32_t v[16];
+                    tmem_ld16(s_addr + 16u * c, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+                    const float4 *cr = reinterpret_cast<const float4 *>(st->c + row0 + 16 * c), *nm = reinterpret_cast<const float4 *>(st->nm[g] + 16 * c);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 f = cr[x];
+                        const float4 n = with_m ? nm[x] : make_float4(0.f, 0.f, 0.f, 0.f);
+                        float *y = a + 16 * c + 4 * x;
+                        fmul2(y[0], y[1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                        fmul2(y[2], y[3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
+                        ffma2(y[0], y[1], y[0], y[1], ks, ks, n.x, n.y);
+                        ffma2(y[2], y[3], y[2], y[3], ks, ks, n.z, n.w);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (16 * c + x < lo || 16 * c + x >= hi) a[16 * c + x] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) top = fmax3(top, a[16 * c + x], a[16 * c + x + 1]);
+                }
+                return top;
+            };
+            const float top = ok ? weights(true) : 0.f;
+            bool move = !begun || any_of_group(g, !ok || top > kLift + kReach || vexp > exp_run);
+            if (__builtin_expect(move, 0)) {
+                if (any_of_group(g, !ok)) {
+                    ok = false;
+                    break;
+                }
+                // maxima of the scores over the keys, and of the value scales' exponents
+                weights(false);
+                int *rexp = reinterpret_cast<int *>(red + 4 * kCols);
+#pragma unroll
+                for (int x = 0; x < kCols; ++x) {
+                    if (x >= 16 * chunks) break;
+                    const float m = warp_max(a[x]);
+                    if (lane == 0) red[quarter * kCols + x] = m;
+                }
+                const int we = __reduce_max_sync(0xffffffffu, vexp);
+                if (lane == 0) rexp[quarter] = we;
+                group_sync(g);
+                if (key < kCols) {
+                    float alpha = 1.f;
+                    if (key < cols) {
+                        const float old = kLift - st->nm[g][key];
+                        const float m = fmaxf(old, fmaxf(fmaxf(red[key], red[kCols + key]), fmaxf(red[2 * kCols + key], red[3 * kCols + key])));
+                        alpha = ex2_approx(old - m);
+                        st->nm[g][key] = kLift - m;
+                    }
+                    st->alpha[g][key] = alpha;
+                }
+                const int e = min((max(max(max(rexp[0], rexp[1]), max(rexp[2], rexp[3])), 8) + 3) & ~3, 252);
+                const float drop = !begun ? 0.f : pow2(exp_run - max(exp_run, e));
+                exp_run = max(exp_run, e);
+                group_sync(g);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= chunks) break;
+                    float f[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        f[x] = st->alpha[g][16 * c + x];
+                        l[16 * c + x] *= f[x];
+                    }
+                    if (begun) {
+                        // S of this tile was issued after the group's previous V P: O is up to date
+                        uint32_t v[16];
+                        tmem_ld16(o_addr + 16u * c, v);
+                        tmem_wait_ld();
+                        reg_fence(v);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * (f[x] * drop));
+                        tmem_st16(o_addr + 16u * c, v);
+                    }
+                }
+                tmem_wait_st();
+                weights(true);
+            }
+            begun = true;
+            const float wv = vs * pow2(127 - exp_run);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c >= chunks) break;
+                uint32_t pk[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int i = 16 * c + 2 * x;
+                    float p0 = ex2_approx(a[i]), p1 = ex2_approx(a[i + 1]);
+                    fadd2(l[i], l[i + 1], l[i], l[i + 1], p0, p1);
+                    fmul2(p0, p1, p0, p1, wv, wv);
+                    pk[x] = pack_f16x2(p0, p1);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    *reinterpret_cast<uint4 *>(pbuf + key * 128 + (((2 * c + x) ^ (key & 7)) << 4)) =
+                        make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wait.bar(C::bPR + g));
+        }
+        tile0 += (uint32_t)(d.k1 - d.k0);
+        if (ok && begun) {
+            ok = wait(C::bOD + g, od);
+            ++od;
+            tc_fence_after();
+        }
+        // ---- sums over the keys: 62 exchanges leave each lane two rows' sums over the warp
+        {
+            auto fold = [&](auto n_, int d_) {
+                constexpr int n = decltype(n_)::value;
+                const bool upper = (lane & (uint32_t)d_) != 0;
+#pragma unroll
+                for (int x = 0; x < n; ++x) {
+                    const float other = __shfl_xor_sync(0xffffffffu, upper ? l[x] : l[n + x], d_);
+                    l[x] = (upper ? l[n + x] : l[x]) + other;
+                }
+            };
+            fold(std::integral_constant<int, 32>{}, 16);
+            fold(std::integral_constant<int, 16>{}, 8);
+            fold(std::integral_constant<int, 8>{}, 4);
+            fold(std::integral_constant<int, 4>{}, 2);
+            fold(std::integral_constant<int, 2>{}, 1);
+        }
+        red[quarter * kCols + 2 * lane] = l[0];
+        red[quarter * kCols + 2 * lane + 1] = l[1];
+        group_sync(g);
+        if (key < kCols) sums(g)[key] = (red[key] + red[kCols + key]) + (red[2 * kCols + key] + red[3 * kCols + key]);
+        if (key == 0) st->exp[g] = exp_run, st->any[g] = begun ? 1 : 0;
+        if (any_of_both(!ok)) break;
+        // ---- a row's weight of either group's O, its LSE
+        {
+            const int r = g * kTile + key;      // of 256 threads, the first 128 have a row each
+            if (r < (turns ? kCols : 2 * kCols)) {
+                const int g0 = turns ? 0 : r / kCols, c = turns ? r : r % kCols;
+                const float m0 = kLift - st->nm[g0][c], l0 = sums(g0)[c];
+                const float m1 = turns ? kLift - st->nm[1][c] : kNoKey, l1 = turns ? sums(1)[c] : 0.f;
+                const float m = fmaxf(m0, m1), f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
+                const float sum = l0 * f0 + l1 * f1;
+                const bool empty = sum == 0.f;       // NaN is not empty
+                const bool bad = st->bad[kCols * g0 + c] || (turns && st->bad[kCols + c]);
+                const float inv = empty ? 0.f : bad ? __uint_as_float(0x7fc00000u) : 1.f / sum;
+                st->alpha[g0][c] = f0 * inv;
+                if (turns) st->alpha[1][c] = f1 * inv;
+                const int out = r < rows ? st->out[r] : -1;
+                if (out >= 0) {
+                    if (d.part >= 0) reinterpret_cast<float *>(p.ws + w.part_l)[out] = empty ? -INFINITY : m - kLift + lg2_approx(sum);
+                    else p.lse[out] = empty ? -INFINITY : (m - kLift) * 0.69314718055994530942f + logf(sum);
+                }
+            }
+        }
+        any_of_both(false);
+        // ---- output: lanes are columns of V, a warp writes 32 of them of one row at a time
+        {
+            const bool f32 = d.part >= 0 || p.out_f32;
+            uint8_t *out = d.part >= 0 ? p.ws + w.part_o : static_cast<uint8_t *>(p.out);
+            const bool any0 = st->any[turns ? 0 : g] != 0, any1 = turns && st->any[1] != 0;
+            const float u0 = pow2(st->exp[turns ? 0 : g] - 127), u1 = pow2(st->exp[1] - 127);
+            const uint32_t o0 = tmem + ((quarter * 32u) << 16) + 2 * kCols + (turns ? 0 : (uint32_t)g * kCols), o1 = o0 + kCols;
+            const int c0 = turns ? 2 * g : 0, c1 = turns ? 2 * g + 2 : 4;     // chunks of 16 rows
+#pragma unroll 1
+            for (int c = c0; c < c1 && 16 * c < cols; ++c) {
+                float v[16];
+                uint32_t x0[16], x1[16];
+                tmem_ld16(o0 + 16u * c, x0);
+                if (any1) tmem_ld16(o1 + 16u * c, x1);
+                tmem_wait_ld();
+                reg_fence(x0);
+                if (any1) reg_fence(x1);
+                const float *f0 = st->alpha[turns ? 0 : g] + 16 * c, *f1 = st->alpha[1] + 16 * c;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    v[x] = any0 ? __uint_as_float(x0[x]) * f0[x] * u0 : 0.f * f0[x];
+                    if (any1) v[x] += __uint_as_float(x1[x]) * f1[x] * u1;
+                }
+                if (key < D) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const int at = row0 + 16 * c + x < rows ? st->out[row0 + 16 * c + x] : -1;
+                        if (at < 0) continue;
+                        if (f32) reinterpret_cast<float *>(out)[(long long)at * D + key] = v[x];
+                        else reinterpret_cast<uint16_t *>(out)[(long long)at * D + key] = (uint16_t)pack_bf16x2(v[x], 0.f);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+    }
+}
+
+// Fetches the codes of K or V tiles, a warp each: a copy per 16 keys (no page is smaller), none for keys
+// past the sequence's last or on a page that is none.
+template <int D>
+__device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &wait, bool values, int lane, uint32_t base, uint8_t *smem) {
+    using C = Cfg<D>;
+    const int v = values ? 2 : 0;
+    const uint8_t *codes = values ? p.c.v : p.c.k;
+    uint32_t *groups = reinterpret_cast<uint32_t *>(smem + C::kMisc) + 2;
+    uint32_t descs = 0, it = 0;
+    bool ok = true;
+    SegDesc d;
+    while (ok && next_desc<C>(wait, smem, descs, d)) {
+        const int32_t *table = p.table + (long long)d.b * p.table_stride;
+        for (int k = d.k0; k < d.k1; ++k, ++it) {
+            const int key = tile_of(d, k) * kTile + 16 * lane, stage = (int)(it & 1u);
+            long long row = -1;
+            if (lane < 8 && key < d.n) {
+                row = cache_row(p.c, table, d.h, key);
+                if (row < 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+            }
+            const uint32_t on = __ballot_sync(0xffffffffu, row >= 0);
+            ok = __all_sync(0xffffffffu, wait(C::bRE + v + stage, (it >> 1) ^ 1u));
+            if (!ok) break;
+            if (values && lane == 0) groups[stage] = on;
+            mbar_arrive_expect_tx_lead(lane == 0 ? 1u : 0u, wait.bar(C::bRF + v + stage), (uint32_t)__popc(on) * 16u * D);
+            __syncwarp();
+            bulk_g2s_lead(row >= 0 ? 1u : 0u, base + C::kRaw + (uint32_t)(v + stage) * C::kRawBytes + (uint32_t)lane * 16u * D,
+                          codes + row * D, 16u * D, wait.bar(C::bRF + v + stage));
+        }
+    }
+    // nothing may be on its way into a tile when the CTA ends
+    for (uint32_t s = 0; s < 2; ++s)
+        if (it > s) mbar_wait_drain(wait.bar(C::bRF + v + (int)s), ((it - 1 - s) >> 1) & 1u);
+}
+
+// Widens the codes of K tiles (four warps, 32 keys each) or V tiles (four more).  Lane: 16 codes of a row, two
+// swizzle pieces of fp16; D / 16 lanes to a row.  Rows of V that are no key, or have a NaN code, become 0:
+// a weight of 0 must leave nothing of them.
+template <int D, bool kInt8>
+__device__ __forceinline__ void widen_role(const Waiter &wait, bool values, int warp, int lane, uint8_t *smem) {
+    using C = Cfg<D>;
+    constexpr int kRowLanes = D / 16, kRows = 32 / kRowLanes, kSteps = 32 / kRows;
+    const int v = values ? 2 : 0, col = lane % kRowLanes, sub_row = lane / kRowLanes;
+    Stat *st = reinterpret_cast<Stat *>(smem + C::kStat);
+    const uint32_t *groups = reinterpret_cast<const uint32_t *>(smem + C::kMisc) + 2;
+    // Eight lanes store 128 bytes at a time; where they share a row, half of them begin with their second
+    // piece: every bank once.
+    const bool swap = D == 128 && col >= 4;
+    const int first = 2 * (col & 3) + (swap ? 1 : 0), second = first ^ 1;
+    const uint32_t dst = (values ? C::kV : C::kK) + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 32 + sub_row) * 128u;
+    uint32_t descs = 0, it = 0;
+    SegDesc d;
+    while (next_desc<C>(wait, smem, descs, d)) {
+        for (int k = d.k0; k < d.k1; ++k, ++it) {
+            const uint32_t stage = it & 1u;
+            const bool ok = values ? wait(C::bVE + (int)stage, (it >> 1) ^ 1u) : wait(C::bKE, it ^ 1u);
+            if (!__all_sync(0xffffffffu, ok && wait(C::bRF + v + (int)stage, it >> 1))) return;
+            const uint8_t *raw = smem + C::kRaw + (uint32_t)(v + (int)stage) * C::kRawBytes + (warp * 32 + sub_row) * D + col * 16;
+            uint8_t *tile = smem + dst + (values ? stage * C::kTileBytes : 0u);
+            const uint32_t on = values ? groups[stage] >> (2 * warp) : 3u;
+            const int left = d.n - tile_of(d, k) * kTile - warp * 32;
+#pragma unroll 2
+            for (int i = 0; i < kSteps; ++i) {
+                const int r = i * kRows + sub_row;
+                uint4 x = *reinterpret_cast<const uint4 *>(raw + i * kRows * D);
+                if (values) {
+                    bool none = r >= left || !((on >> (r >> 4)) & 1u);
+                    if (!kInt8) {
+                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) nan |= ((y[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        const uint32_t b = __ballot_sync(0xffffffffu, nan != 0u) >> (sub_row * kRowLanes);
+                        const bool odd = (b & ((1u << kRowLanes) - 1u)) != 0u;
+                        if (col == 0) st->odd[stage][warp * 32 + r] = odd ? 1 : 0;
+                        none |= odd;
+                    }
+                    if (none) x = make_uint4(0, 0, 0, 0);
+                }
+                const uint32_t y[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
+                const int r7 = r & 7;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t o[4];
+                    codes_to_f16x2<kInt8>(y[2 * q], o[0], o[1]);
+                    codes_to_f16x2<kInt8>(y[2 * q + 1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(tile + i * kRows * 128 + (((q ? second : first) ^ r7) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(wait.bar(values ? C::bVF + (int)stage : C::bKF));
+                mbar_arrive(wait.bar(C::bRE + v + (int)stage));
+            }
+        }
+    }
+}
+
+template <int D, bool kInt8>
+__global__ void __launch_bounds__(kThreads, 1)
+    bsattn_prefill_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Layout w) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {  // the swizzle counts from 1024-byte boundaries
+        if (threadIdx.x == 0 && p.err) atomicOr(p.err, BSATTN_FLAG_TIMEOUT);
+        return;
+    }
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    const uint32_t warp = warp_id(), lane = lane_id();
+    Waiter wait;
+    wait.bars = base + C::kBar;
+    wait.abort = reinterpret_cast<volatile int *>(misc + 1);
+    wait.err = p.err;
+    if (threadIdx.x == 0) {
+        mbar_init(wait.bar(C::bKF), 4);          // one arrival per widening warp
+        mbar_init(wait.bar(C::bKE), 1);
+        mbar_init(wait.bar(C::bQF), 8);          // one per warp of the groups
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(wait.bar(C::bVF + s), 4);
+            mbar_init(wait.bar(C::bVE + s), 1);
+            mbar_init(wait.bar(C::bSR + s), 1);
+            mbar_init(wait.bar(C::bPR + s), 4);
+            mbar_init(wait.bar(C::bOD + s), 1);
+        }
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(wait.bar(C::bRF + s), 1);  // the fetching warp's arrival and the bytes
+            mbar_init(wait.bar(C::bRE + s), 4);
+        }
+        for (int s = 0; s < kDescs; ++s) {
+            mbar_init(wait.bar(C::bUF + s), 1);
+            mbar_init(wait.bar(C::bUE + s), 19); // issuing, fetching, group and widening warps
+        }
+        mbar_init(wait.bar(C::bDrain), 1);
+        misc[1] = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(base + C::kMisc, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (warp == 0) {
+        regs_release<kCtrlRegs>();
+        // ---------------------------------------------------- MMA issuer --
+        // The whole warp runs in step; lane 0 issues.
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        // kind::f16, fp16 A and B, fp32 D; M = 128; N below
+        constexpr uint32_t idesc_s = (1u << 4) | (static_cast<uint32_t>(128 >> 4) << 24);
+        constexpr uint32_t idesc_o = idesc_s | (1u << 15) | (1u << 16);   // A and B MN-major
+        const uint64_t desc_q = smem_desc_sw128(base + C::kQ, 16, 1024);
+        const uint64_t desc_k = smem_desc_sw128(base + C::kK, 16, 1024);
+        const uint64_t desc_v = smem_desc_sw128(base + C::kV, kSub, 1024);
+        const uint64_t desc_p = smem_desc_sw128(base + C::kP, kSub, 1024);
+        constexpr uint64_t kTileUnits = C::kTileBytes >> 4, kSubUnits = kSub >> 4;
+        uint32_t descs = 0, tile0 = 0, segs = 0, pc[2] = {0, 0};
+        bool ok = true;
+        auto ready = [&](int b, uint32_t phase) -> bool {
+            ok = ok && wait(b, phase);
+            return ok;
+        };
+        SegDesc d;
+        while (ok && next_desc<C>(wait, smem, descs, d)) {
+            const int rows = d.tokens * p.G, n = d.k1 - d.k0;
+            const bool turns = rows <= kCols;
+            const uint32_t cols[2] = {(uint32_t)(min(rows, kCols) + 15) & ~15u, (uint32_t)((turns ? rows : rows - kCols) + 15) & ~15u};
+            auto score = [&](int g) {
+                const uint64_t qd = desc_q + (turns ? 0u : (uint64_t)g * (kCols * 128 >> 4));
+                const uint32_t idesc = idesc_s | ((cols[g] >> 3) << 17);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = (uint64_t)((kk >> 2) * kSubUnits + (kk & 3) * 2);
+                    mma_ss_lead(lead, tmem + g * kCols, desc_k + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+                }
+                mma_commit_lead(lead, wait.bar(C::bSR + g));
+            };
+            auto output = [&](int g, uint32_t it, bool first) -> bool {
+                if (!ready(C::bVF + (int)(it & 1u), it >> 1) || !ready(C::bPR + g, pc[g])) return false;
+                ++pc[g];
+                tc_fence_after();
+                const uint64_t vd = desc_v + (uint64_t)(it & 1u) * kTileUnits, pd = desc_p + (uint64_t)g * kSubUnits;
+                const uint32_t idesc = idesc_o | ((cols[g] >> 3) << 17);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_ss_lead(lead, tmem + 2 * kCols + g * kCols, vd + (uint64_t)(kk * (2048 >> 4)),
+                                pd + (uint64_t)(kk * (2048 >> 4)), idesc, kk > 0 || !first ? 1u : 0u);
+                return true;
+            };
+            if (!ready(C::bQF, segs)) break;
+            ++segs;
+            tc_fence_after();
+            for (int k = 0; ok && k < n; ++k) {
+                const uint32_t it = tile0 + (uint32_t)k;
+                if (!ready(C::bKF, it)) break;
+                tc_fence_after();
+                if (turns) {
+                    const int g = k & 1;
+                    if (k >= 2) {
+                        if (!output(g, it - 2, k < 4)) break;
+                        mma_commit_lead(lead, wait.bar(C::bVE + (int)(it & 1u)));
+                    }
+                    score(g);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (k > 0 && !output(g, it - 1, k == 1)) break;
+                        score(g);
+                    }
+                    if (!ok) break;
+                    if (k > 0) mma_commit_lead(lead, wait.bar(C::bVE + (int)((it - 1) & 1u)));
+                }
+                mma_commit_lead(lead, wait.bar(C::bKE));
+            }
+            if (!ok) break;
+            const uint32_t last = tile0 + (uint32_t)n - 1;
+            if (turns) {
+                for (int k = max(n - 2, 0); k < n; ++k) {
+                    const uint32_t it = tile0 + (uint32_t)k;
+                    if (!output(k & 1, it, k < 2)) break;
+                    mma_commit_lead(lead, wait.bar(C::bVE + (int)(it & 1u)));
+                    mma_commit_lead(lead, wait.bar(C::bOD + (k & 1)));
+                }
+            } else if (n > 0) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!output(g, last, n == 1)) break;
+                    mma_commit_lead(lead, wait.bar(C::bOD + g));
+                }
+                if (ok) mma_commit_lead(lead, wait.bar(C::bVE + (int)(last & 1u)));
+            }
+            tile0 += (uint32_t)n;
+        }
+        // Wait until every tcgen05 operation issued above has completed.
+        mma_commit_lead(lead, wait.bar(C::bDrain));
+        mbar_wait_drain(wait.bar(C::bDrain), 0);
+    } else if (warp < 4) {
+        regs_release<kCtrlRegs>();
+        if (warp == 1) {
+            if (lane == 0) schedule_role<C>(p, w, wait, smem);
+            __syncwarp();
+        } else {
+            fetch_role<D>(p, wait, warp == 3, (int)lane, base, smem);
+        }
+    } else if (warp < 12) {
+        regs_claim<kGroupRegs>();
+        group_role<D, kInt8>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
+    } else {
+        regs_release<kWidenRegs>();
+        widen_role<D, kInt8>(wait, warp >= 16, (int)(warp & 3u), (int)lane, smem);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool kInt8>
+cudaError_t launch(const ChunkParams &p, const Layout &w, cudaStream_t stream) {
+    using C = Cfg<D>;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, bsattn_prefill_rows_kernel<D, kInt8>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(bsattn_prefill_rows_kernel<D, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w)};
+    return launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_rows_kernel<D, kInt8>), dim3((unsigned)w.ctas), kThreads,
+                            C::kAlloc, args, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_rows(const ChunkParams &p, const Layout &w, cudaStream_t stream) {
+    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, w, stream) : launch<128, false>(p, w, stream);
+    return p.c.int8 ? launch<64, true>(p, w, stream) : launch<64, false>(p, w, stream);
+}
+
+}  // namespace bsattn

@@ -604,9 +604,9 @@ bsattn_status bsattn_decode_workspace_size(const bsattn_kv_cache *cache, int32_t
  * them for BSATTN_MASK_NONE; see bsattn_mask_kind):
  *   s_j = softmax_scale * q . K_j,  lse = ln(sum_j exp(s_j)),  out = sum_j exp(s_j - lse) V_j;
  * no key: out = 0, lse = -inf.  K_j, V_j are the cached values (code * scale); products with
- * codes are exact and all sums are fp32; the weights times what a value's scale has besides a
- * power of two are rounded to fp16 (11 bits), or, among keys whose value scales are more than
- * 2^8 apart, to bf16 (8 bits).
+ * codes are exact in the scores and all sums are fp32; weights are rounded to fp16 (11 bits), and so
+ * are values whose scale is not a power of two (int8).  What a key contributes may count as 0 where
+ * it is 2^-27 of the largest value or less.
  *
  * q            device bf16, `total` rows of [Hq, D] contiguous elements, q_stride apart (at
  *              least Hq * D, a multiple of 8); 16-byte aligned.

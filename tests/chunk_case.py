@@ -43,15 +43,17 @@ class Chunks:
         return (q.reshape(m * G, self.D), self.pool.host("k", self.host_table[b], h, pos),
                 self.pool.host("v", self.host_table[b], h, pos), np.repeat(mask[:, ok], G, axis=0), ok)
 
-    def expect(self, coarse=2.0 ** -11):
+    def expect(self, coarse=None):
         """Oracle (out, lse, out tolerance, lse tolerance) [total, Hq, ...].
 
         Scores: a dot product of D fp32 terms in any order is off by at most D 2^-24 of sum |q k|;
         scales, the maximum's subtraction and the exponential's argument add 8 such steps: ds = (D + 8)
         2^-24 scale sum_d |q_d k_d|, largest over the keys.  A weight is then off by 2 ds + 2^-20
-        relatively, by its rounding (`coarse`: to fp16 2^-11, to bf16 2^-8), and absolutely by at most
-        2^-32 of the largest weight where it is too small for fp16, times at most 2^5 where the values
+        relatively, by its rounding to fp16, 2^-11, and by the value's where its scale is not a power of two
+        (int8), 2^-11 more (`coarse`: what both come to where it is not that), and absolutely by at most 2^-32 of the largest weight where it is too small for fp16, times at most 2^5 where the values
         of its tile are smaller than those of another."""
+        if coarse is None:
+            coarse = 2.0 ** -10 if self.pool.dtype == "int8" else 2.0 ** -11
         total, Hq = self.q.shape[:2]
         out, lse = np.zeros((total, Hq, self.D)), np.full((total, Hq), -math.inf)
         to, tl = np.zeros_like(out), np.zeros_like(lse)

@@ -46,8 +46,8 @@ constexpr uint32_t kCtrlRegs = 120, kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 2 * 128 * kSoftmaxRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 elements: one 128-byte swizzle span
-constexpr int kPlanThreads = 1024, kWidenThreads = 256, kJoinThreads = 256;
-constexpr int kJoinRows = 32;               // rows of a part that a block of the join takes
+constexpr int kPlanThreads = 1024, kWidenThreads = 256;
+constexpr int kJoinRows = 8;                // rows of a part that a block of the join takes
 
 // Binary exponents (biased) that go into K' (what lies outside stays in r), and those that E is taken from
 // (2^(E - 6) and its inverse are then normal numbers).
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
         }
         long long sum;
         s.tile0 = (int)min(tiles + block_scan(s.sinks + s.end - s.near, &sum, warps), (long long)INT32_MAX);
-        if (!w.few && s.m > 0 && (long long)s.tile0 + s.sinks + s.end - s.near > w.tiles) {
+        if (s.m > 0 && (long long)s.tile0 + s.sinks + s.end - s.near > w.tiles) {
             // no room for its keys
             if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
             s.m = s.blocks = s.sinks = s.near = s.end = 0;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
         t.places = places;
         t.tiles = (int)min(tiles, w.tiles);
         // so many phases that the keys of one fit L2
-        const long long phases = w.few ? 1 : (t.tiles * (long long)p.c.H * (kTile * 4 * p.c.D) + kPhaseBytes - 1) / kPhaseBytes;
+        const long long phases = (t.tiles * (long long)p.c.H * (kTile * 4 * p.c.D) + kPhaseBytes - 1) / kPhaseBytes;
         t.pieces = (int)max(1ll, min(min((long long)w.pieces, w.ctas * max(phases, 1ll)), places / kLeastPiece));
         *reinterpret_cast<PlanTotals *>(p.ws + w.totals) = t;
     }
@@ -713,50 +713,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- join --
 
-// Block (x, y): kJoinRows rows of the segment that begins in piece x and ends in a later one; D / 4
-// lanes to a row.
+// Block (x, y): kJoinRows rows of the segment that begins in piece x and ends in a later one, a warp each.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) bsattn_prefill_join_kernel(const __grid_constant__ ChunkParams p,
-                                                                           const __grid_constant__ Layout w) {
+__global__ void __launch_bounds__(kJoinRows * 32) bsattn_prefill_join_kernel(const __grid_constant__ ChunkParams p,
+                                                                             const __grid_constant__ Layout w) {
+    grid_launch_dependents();
+    const int r = blockIdx.y * kJoinRows + (int)(threadIdx.x / 32), lane = (int)(threadIdx.x % 32), piece = blockIdx.x;
+    const int t = r / kTile, row = r % kTile, token_of = row / p.G, tok = t * w.tokens + token_of;
     grid_dependency_wait();
-    const int piece = blockIdx.x;
     const CutInfo cut = reinterpret_cast<const CutInfo *>(p.ws + w.cuts)[piece];
-    if (cut.parts == 0) return;
-    constexpr int kLanes = D / 4, kStep = kJoinThreads / kLanes;
-    const int lane = threadIdx.x % kLanes;
+    if (cut.parts == 0 || token_of >= w.tokens || tok >= cut.tokens) return;
     const float *part_l = reinterpret_cast<const float *>(p.ws + w.part_l);
-    const float4 *part_o = reinterpret_cast<const float4 *>(p.ws + w.part_o);
-    for (int i = threadIdx.x / kLanes; i < kJoinRows; i += kStep) {
-        const int r = blockIdx.y * kJoinRows + i, t = r / kTile, row = r % kTile;
-        const int token_of = row / p.G, tok = t * w.tokens + token_of;
-        if (token_of >= w.tokens || tok >= cut.tokens) continue;
-        auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
-        float m = -INFINITY;
-        bool nan = false;
-        for (int x = 0; x < cut.parts; ++x) {
-            const float l = part_l[at(x)];
-            nan |= l != l;
-            m = fmaxf(m, l);
-        }
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        if (m != -INFINITY || nan)
-            for (int x = 0; x < cut.parts; ++x) {
-                const float l = part_l[at(x)];
-                if (l == -INFINITY) continue;
-                const float f = ex2_approx(l - m);
-                const float4 y = part_o[at(x) * kLanes + lane];
-                sum += f;
-                o.x += f * y.x, o.y += f * y.y, o.z += f * y.z, o.w += f * y.w;
+    const float *part_o = reinterpret_cast<const float *>(p.ws + w.part_o);
+    auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
+    float m = -INFINITY, sum = 0.f, o[D / 32] = {};
+    for (int x0 = 0; x0 < cut.parts; x0 += 32) {
+        const float l = x0 + lane < cut.parts ? part_l[at(x0 + lane)] : -INFINITY;
+        float top = l;
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float m_new = fmaxf(m, top);
+        const float f = l == -INFINITY ? 0.f : ex2_approx(l - m_new), drop = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+        m = m_new;
+        sum *= drop;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] *= drop;
+        const int n = min(32, cut.parts - x0);
+#pragma unroll 4
+        for (int x = 0; x < n; ++x) {
+            const float fx = __shfl_sync(0xffffffffu, f, x);
+            if (fx == 0.f) continue;             // no key, or next to nothing
+            const float *y = part_o + at(x0 + x) * D + lane * (D / 32);
+            sum += fx;
+            if constexpr (D == 128) {
+                const float4 v = *reinterpret_cast<const float4 *>(y);
+                o[0] += fx * v.x, o[1] += fx * v.y, o[2] += fx * v.z, o[3] += fx * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(y);
+                o[0] += fx * v.x, o[1] += fx * v.y;
             }
-        const bool empty = sum == 0.f;
-        const float inv = empty ? 0.f : 1.f / sum;
-        o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-        const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
-        if (p.out_f32) reinterpret_cast<float4 *>(p.out)[out * kLanes + lane] = o;
-        else reinterpret_cast<uint2 *>(p.out)[out * kLanes + lane] = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-        if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
+        }
     }
+    const bool empty = sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+    const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
+    if (p.out_f32) {
+        float *dst = static_cast<float *>(p.out) + out * D + lane * (D / 32);
+#pragma unroll
+        for (int c = 0; c < D / 32; c += 2) reinterpret_cast<float2 *>(dst)[c / 2] = make_float2(o[c] * inv, o[c + 1] * inv);
+    } else {
+        uint32_t *dst = static_cast<uint32_t *>(p.out) + (out * D + lane * (D / 32)) / 2;
+#pragma unroll
+        for (int c = 0; c < D / 32; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+    }
+    if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
 }
 
 template <int D>
@@ -783,14 +792,14 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     CUtensorMap tq = {};
     if (p.total > 0 && !w.few && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
     void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w), &tq};
-    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_plan_kernel), dim3(1), kPlanThreads, 0, args, stream);
-    if (e != cudaSuccess || p.total == 0) return e;
-    const unsigned join_rows = (w.few ? kTile : 2 * kTile) / kJoinRows;
     const auto join = reinterpret_cast<const void *>(bsattn_prefill_join_kernel<D>);
+    const unsigned join_rows = (unsigned)((w.few ? w.few : 2 * kTile) / kJoinRows);
     if (w.few) {
         e = launch_prefill_rows(p, w, stream);
-        return e != cudaSuccess ? e : launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinThreads, 0, args, stream);
+        return e != cudaSuccess || p.total == 0 ? e : launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinRows * 32, 0, args, stream);
     }
+    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_plan_kernel), dim3(1), kPlanThreads, 0, args, stream);
+    if (e != cudaSuccess || p.total == 0) return e;
     const long long items = w.tiles * p.c.H;
     const unsigned blocks = (unsigned)(items < sms * 8ll ? items : sms * 8ll);
     e = launch_dependent(p.c.int8 ? reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, true>)
@@ -799,7 +808,7 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_kernel<D>), dim3((unsigned)w.ctas), kThreads, C::kAlloc, args, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinThreads, 0, args, stream);
+    return launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinRows * 32, 0, args, stream);
 }
 
 }  // namespace

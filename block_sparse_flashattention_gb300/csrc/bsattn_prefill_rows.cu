@@ -25,8 +25,6 @@
 //   warps 12-15   widen the codes of keys (128-byte swizzle, a tile's rows K-major)
 //   warps 16-19   the same for values, as they lie (MN-major)
 // TMEM: S^T of group g [64 g, 64 g + 64), O^T of group g [128 + 64 g, 192 + 64 g).
-#include <type_traits>
-
 #include "kv_codes.cuh"
 #include "prefill_plan.cuh"
 
@@ -42,24 +40,25 @@ constexpr uint32_t kCtrlRegs = 48, kGroupRegs = 160, kWidenRegs = 56;
 static_assert(128 * kCtrlRegs + 256 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 fp16: one 128-byte swizzle span
-constexpr int kCols = 64;                   // query rows of a group
 constexpr float kLift = 7.f, kReach = 7.f;
 
-template <int D>
+// kRows: query rows of a segment at most.
+template <int D, int kRows>
 struct Cfg {
+    static constexpr int kCols = kRows < 64 ? kRows : 64;            // of a group
     static constexpr uint32_t kTileBytes = kTile * D * 2, kRawBytes = kTile * D;
     static constexpr uint32_t kQ = 0, kK = kQ + kTileBytes, kV = kK + kTileBytes, kP = kV + 2 * kTileBytes;
     static constexpr uint32_t kRaw = kP + 2 * kSub;                  // K0, K1, V0, V1
     static constexpr uint32_t kStat = kRaw + 4 * kRawBytes;          // see Stat
-    static constexpr uint32_t kStatBytes = 128 * 4 * 2 + 2 * kCols * 4 * 2 + 128 + 2 * 128 + 64;
+    static constexpr uint32_t kStatBytes = 128 * 4 * 2 + 2 * 64 * 4 * 2 + 64 * 4 + 128 + 2 * 16 + 2 * 8 + 8 + 16 + 16;
     static constexpr uint32_t kDesc = (kStat + kStatBytes + 15u) & ~15u;
     static constexpr uint32_t kBar = kDesc + kDescs * (uint32_t)sizeof(SegDesc);
     // K' full and empty, V' stages full and empty, query rows there, per group: S ready, P ready, O complete;
     // raw K / V stages full and empty (2 v + stage); descriptor full and empty
     static constexpr int bKF = 0, bKE = 1, bVF = 2, bVE = 4, bQF = 6, bSR = 7, bPR = 9, bOD = 11, bRF = 13, bRE = 17, bUF = 21,
                          bUE = bUF + kDescs, bDrain = bUE + kDescs, kNumBars = bDrain + 1;
-    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort, [2..3] raw V tiles' groups
-    static constexpr uint32_t kAlloc = kMisc + 32;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
+    static constexpr uint32_t kAlloc = kMisc + 16;
     static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
@@ -67,13 +66,18 @@ struct Cfg {
 struct Stat {
     float c[128];            // c_r, 0 of rows that are none
     int32_t out[128];        // row of the output or the parts, -1: none
-    float nm[2][kCols];      // 7 - m_r of the groups' rows, -inf of rows that are none
-    float alpha[2][kCols];   // what sums are multiplied by when m moves; at the end what O is
+    float nm[2][64];         // 7 - m_r of the groups' rows, -inf of rows that are none
+    float alpha[2][64];      // what sums are multiplied by when m moves; at the end what O is
+    float zero[64];
     uint8_t bad[128];        // the row meets a value that is not a number
-    uint8_t odd[2][128];     // keys of the V' stages that have a NaN code
-    int32_t exp[2], any[2], pad[12];
+    uint32_t odd[2][4];      // keys of the V' stages that have a NaN code
+    int32_t exp[2], any[2];
+    uint32_t groups[2];      // 16-key groups of the raw V tiles that are there
+    int32_t b, h, r;         // where the CTA's piece of the line begins
+    int32_t pieces;
+    long long begin, line;   // place at which that segment begins; places in all
 };
-static_assert(sizeof(Stat) == Cfg<64>::kStatBytes, "stat area");
+static_assert(sizeof(Stat) <= Cfg<64, 16>::kStatBytes, "stat area");
 
 // Threads of a group, or of both, meet; whether `x` holds for one of them.
 __device__ __forceinline__ bool any_of(int id, int threads, bool x) {
@@ -105,38 +109,191 @@ __device__ __forceinline__ float warp_max(float x) {
     return __int_as_float(y ^ ((y >> 31) & 0x7fffffff));
 }
 
+// Of 2 n sums of each of two lanes, `d` apart, either keeps the n of its own rows.
+template <int n, int kCols>
+__device__ __forceinline__ void fold(float (&l)[kCols], uint32_t lane, int d) {
+    const bool upper = (lane & (uint32_t)d) != 0;
+#pragma unroll
+    for (int x = 0; x < n; ++x) {
+        const float other = __shfl_xor_sync(0xffffffffu, upper ? l[x] : l[n + x], d);
+        l[x] = (upper ? l[n + x] : l[x]) + other;
+    }
+}
+
 // Key tile k of a segment's visiting list.
 __device__ __forceinline__ int tile_of(const SegDesc &d, int k) { return k < d.sinks ? k : k - d.sinks + d.near; }
 
+// The line of work of this kernel is numbered by every CTA for itself (lengths are on the device): places of
+// one head's pass over a sequence's segments.
+constexpr int kRowsCost = 4;                // places that starting and ending a segment costs
+
+__device__ __forceinline__ int segment_tiles(const ChunkParams &p, const Layout &w, const Chunk &c, int r) {
+    if (c.n <= 0) return 0;
+    return visit(p, c.n, c.n - c.m + r * w.step, c.n - c.m + min((r + 1) * w.step, c.m) - 1).count();
+}
+
+__device__ __forceinline__ long long pass_places(const ChunkParams &p, const Layout &w, const Chunk &c) {
+    long long sum = 0;
+    for (int r = 0; r * (long long)w.step < c.m; ++r) sum += kRowsCost + segment_tiles(p, w, c, r);
+    return sum;
+}
+
+// Numbers the line and finds where the CTA's piece begins; all threads.
+template <class C>
+__device__ __forceinline__ void find_piece(const ChunkParams &p, const Layout &w, uint8_t *smem) {
+    Stat *st = reinterpret_cast<Stat *>(smem + C::kStat);
+    long long *warps = reinterpret_cast<long long *>(smem + C::kK);   // no tile is there yet
+    const int tid = (int)threadIdx.x, lane = tid % 32, warp = tid / 32;
+    auto scan = [&](long long x, long long &all) -> long long {       // sum over the threads before this one
+        long long s = x;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        __syncthreads();
+        if (lane == 31) warps[warp] = s;
+        __syncthreads();
+        long long before = 0;
+        all = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += warps[i];
+            all += warps[i];
+        }
+        return before + s - x;
+    };
+    Chunk c = {};
+    long long line = 0, pass = 0, before = 0, all;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        c = Chunk{};
+        if (b0 + tid < p.B) c = chunk_of(p, b0 + tid, blockIdx.x == 0);
+        pass = pass_places(p, w, c);
+        before = line + scan(pass * p.c.H, all);
+        line += all;
+    }
+    const int pieces = (int)max(1ll, min((long long)w.ctas, line / kLeastPiece)), piece = (int)blockIdx.x;
+    const long long from = line * piece / pieces;
+    if (tid == 0) st->pieces = pieces, st->line = line, st->b = p.B;
+    __syncthreads();
+    if (piece >= pieces || from >= line) return;
+    // more sequences than threads: once more from the first
+    long long sum = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        if (p.B > kThreads) {
+            c = Chunk{};
+            if (b0 + tid < p.B) c = chunk_of(p, b0 + tid, false);
+            pass = pass_places(p, w, c);
+            before = sum + scan(pass * p.c.H, all);
+            sum += all;
+        }
+        if (from >= before && from < before + pass * p.c.H) {
+            const int h = (int)((from - before) / pass);
+            long long at = before + h * pass;
+            int r = 0;
+            for (int len; at + (len = kRowsCost + segment_tiles(p, w, c, r)) <= from; ++r) at += len;
+            st->b = b0 + tid, st->h = h, st->r = r, st->begin = at;
+        }
+    }
+}
+
+// Finds the segments of the CTA's piece and writes their descriptors.
+template <class C>
+__device__ __forceinline__ void segment_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint8_t *smem) {
+    const Stat *st = reinterpret_cast<const Stat *>(smem + C::kStat);
+    CutInfo *cut = reinterpret_cast<CutInfo *>(p.ws + w.cuts) + blockIdx.x;
+    *cut = CutInfo{};
+    uint32_t count = 0;
+    auto emit = [&](const SegDesc &d) -> bool {
+        const int slot = (int)(count % kDescs);
+        if (!wait(C::bUE + slot, (count / kDescs) ^ 1u)) return false;
+        reinterpret_cast<SegDesc *>(smem + C::kDesc)[slot] = d;
+        mbar_arrive(wait.bar(C::bUF + slot));
+        ++count;
+        return true;
+    };
+    const long long line = st->line;
+    const int pieces = st->pieces, piece = (int)blockIdx.x;
+    int b = st->b, h = st->h, r = st->r;
+    if (b < p.B) {
+        const long long from = line * piece / pieces, to = line * (piece + 1) / pieces;
+        long long begin = st->begin;
+        Chunk s = chunk_of(p, b, false);
+        while (begin < to) {
+            if (r * (long long)w.step >= s.m) {
+                r = 0;
+                if (s.m == 0 || ++h >= p.c.H) {
+                    h = 0;
+                    if (++b >= p.B) break;
+                    s = chunk_of(p, b, false);
+                }
+                continue;
+            }
+            SegDesc d = {};
+            d.b = b, d.h = h, d.n = s.n;
+            d.token = s.first + r * w.step, d.tokens = min(w.step, s.m - r * w.step);
+            d.pos = s.n - s.m + r * w.step;
+            d.part = -1;
+            int tiles = 0;
+            if (s.n > 0) {
+                const Visit v = visit(p, s.n, d.pos, d.pos + d.tokens - 1);
+                d.sinks = v.sinks, d.near = v.near;
+                tiles = v.count();
+            }
+            const long long first = begin + kRowsCost;   // place of its first tile
+            d.k0 = (int)max(from - first, 0ll);
+            d.k1 = (int)min(to - first, (long long)tiles);
+            if (tiles == 0 ? begin >= from : d.k1 > d.k0) {
+                if (tiles == 0) d.k0 = d.k1 = 0;
+                else if (d.k0 > 0 || d.k1 < tiles) {
+                    d.part = 2 * piece + (d.k0 > 0 ? 0 : 1);
+                    if (d.k0 == 0) {
+                        // the piece that holds the last tile: place x is in piece ((x + 1) pieces - 1) / line
+                        const int last = (int)(((first + tiles) * pieces - 1) / line);
+                        CutInfo x;
+                        x.token = d.token, x.tokens = d.tokens, x.h = h, x.parts = last - piece + 1;
+                        *cut = x;
+                    }
+                }
+                if (!emit(d)) return;
+            }
+            begin = first + tiles;
+            ++r;
+        }
+    }
+    SegDesc stop = {};
+    stop.b = -1;
+    emit(stop);
+}
+
 // One group: 128 threads, one key of a tile each.
-template <int D, bool kInt8>
+template <int D, int kRows, bool kInt8>
 __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint32_t tmem, int g,
                                            uint32_t warp, uint32_t lane, uint8_t *smem) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kRows>;
+    constexpr int kCols = C::kCols, kChunks = kCols / 16;
     Stat *st = reinterpret_cast<Stat *>(smem + C::kStat);
     const uint32_t quarter = warp & 3u;
     const int key = (int)(quarter * 32 + lane), sw = (int)warp - 4;
-    const uint32_t s_addr = tmem + ((quarter * 32u) << 16) + (uint32_t)g * kCols, o_addr = s_addr + 2 * kCols;
+    const uint32_t s_addr = tmem + ((quarter * 32u) << 16) + (uint32_t)g * 64u, o_addr = s_addr + 128u;
     uint8_t *pbuf = smem + C::kP + (uint32_t)g * kSub;
-    float *red = reinterpret_cast<float *>(pbuf);     // [4][64] while no weights are in the buffer, then 4 exponents
-    auto sums = [&](int of) -> float * { return reinterpret_cast<float *>(smem + C::kP + (uint32_t)of * kSub) + 5 * kCols; };
+    float *red = reinterpret_cast<float *>(pbuf);     // [4][64] while no weights are in the buffer, then 4 exponents, sums
+    auto sums = [&](int of) -> float * { return reinterpret_cast<float *>(smem + C::kP + (uint32_t)of * kSub) + 5 * 64; };
     uint32_t descs = 0, sc = 0, od = 0, tile0 = 0;
     SegDesc d;
     while (true) {
         const bool got = next_desc<C>(wait, smem, descs, d);
         if (any_of_both(!got)) break;
         const int rows = d.tokens * p.G;
-        const bool turns = rows <= kCols;
-        const int row0 = turns ? 0 : kCols * g, cols = turns ? rows : min(max(rows - row0, 0), kCols);
+        const bool turns = kRows <= 64 || rows <= 64;
+        const int row0 = turns ? 0 : 64 * g, cols = turns ? rows : min(max(rows - row0, 0), kCols);
         const int chunks = (cols + 15) / 16;
         // ---- query rows: fp16 of q 2^-e (K-major, swizzled), D / 8 lanes to a row
         if (16 * sw < rows) {
-            constexpr int kRowLanes = D / 8, kRows = 32 / kRowLanes, kSteps = 16 / kRows;
+            constexpr int kRowLanes = D / 8, kAtOnce = 32 / kRowLanes, kSteps = 16 / kAtOnce;
             const int piece = (int)lane % kRowLanes, sub = (int)lane / kRowLanes;
             uint4 x[kSteps];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * sw + i * kRows + sub, tok = r / p.G;
+                const int r = 16 * sw + i * kAtOnce + sub, tok = r / p.G;
                 x[i] = make_uint4(0, 0, 0, 0);
                 if (r < rows)
                     x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (long long)(d.token + tok) * p.q_stride +
@@ -144,7 +301,7 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
             }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * sw + i * kRows + sub;
+                const int r = 16 * sw + i * kAtOnce + sub;
                 uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, a = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) a = __vmaxu2(a, y[k] & 0x7fff7fffu);
@@ -168,7 +325,7 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
         }
         if (key < kCols) {
             st->nm[g][key] = key < cols ? kLift - kNoKey : -INFINITY;
-            st->bad[kCols * g + key] = 0;
+            st->bad[64 * g + key] = 0;
         }
         fence_proxy_async_smem();
         any_of_both(false);
@@ -210,59 +367,64 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
             const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < cols);
             const uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
             const int vexp = vb < 0x7f800000u && vb > 1u << 23 ? (int)(vb >> 23) : 0;
+            bool fresh = false;                  // m has just been moved
             ok = __all_sync(0xffffffffu, wait(C::bSR + g, sc) && (kInt8 || wait(C::bVF + (int)stage, it >> 1)));
             ++sc;
             tc_fence_after();
-            if (there && (vb >= 0x7f800000u || (!kInt8 && ok && st->odd[stage][key]))) {
+            if (there && (vb >= 0x7f800000u || (!kInt8 && ok && ((st->odd[stage][quarter] >> lane) & 1u)))) {
                 vs = 0.f;
-                for (int r = max(lo, 0); r < min(hi, cols); ++r) st->bad[kCols * g + r] = 1;
+                for (int r = max(lo, 0); r < min(hi, cols); ++r) st->bad[64 * g + r] = 1;
             }
+            // The scores less m (a, in units of log2, 7 for the largest).  Where the threads vote to move m,
+            // they are formed again without it, their maxima taken, and formed once more.
             float a[kCols];
-            auto weights = [&](bool with_m) -> float {
+            bool raw = !begun;
+            if (raw && any_of_group(g, !ok)) ok = false;
+            while (ok || begun) {
                 float top = -INFINITY;
+                if (ok) {
+                    const float4 *cr = reinterpret_cast<const float4 *>(st->c + row0);
+                    const float4 *nm = reinterpret_cast<const float4 *>(raw ? st->zero : st->nm[g]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c >= chunks) break;
-                    uint32_t v[16];
-                    tmem_ld16(s_addr + 16u * c, v);
-                    tmem_wait_ld();
-                    reg_fence(v);
-                    const float4 *cr = reinterpret_cast<const float4 *>(st->c + row0 + 16 * c), *nm = reinterpret_cast<const float4 *>(st->nm[g] + 16 * c);
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (kChunks > 1 && c >= chunks) break;
+                        uint32_t v[16];
+                        tmem_ld16(s_addr + 16u * c, v);
+                        tmem_wait_ld();
+                        reg_fence(v);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 f = cr[x];
-                        const float4 n = with_m ? nm[x] : make_float4(0.f, 0.f, 0.f, 0.f);
-                        float *y = a + 16 * c + 4 * x;
-                        fmul2(y[0], y[1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
-                        fmul2(y[2], y[3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
-                        ffma2(y[0], y[1], y[0], y[1], ks, ks, n.x, n.y);
-                        ffma2(y[2], y[3], y[2], y[3], ks, ks, n.z, n.w);
+                        for (int x = 0; x < 4; ++x) {
+                            const float4 f = cr[4 * c + x], n = nm[4 * c + x];
+                            float *y = a + 16 * c + 4 * x;
+                            fmul2(y[0], y[1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                            fmul2(y[2], y[3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
+                            ffma2(y[0], y[1], y[0], y[1], ks, ks, n.x, n.y);
+                            ffma2(y[2], y[3], y[2], y[3], ks, ks, n.z, n.w);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                if (16 * c + x < lo || 16 * c + x >= hi) a[16 * c + x] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) top = fmax3(top, a[16 * c + x], a[16 * c + x + 1]);
                     }
-                    if (masked) {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            if (16 * c + x < lo || 16 * c + x >= hi) a[16 * c + x] = -INFINITY;
+                }
+                if (!raw) {
+                    if (fresh || !any_of_group(g, !ok || top > kLift + kReach || vexp > exp_run)) break;
+                    if (any_of_group(g, !ok)) {
+                        ok = false;
+                        break;
                     }
-#pragma unroll
-                    for (int x = 0; x < 16; x += 2) top = fmax3(top, a[16 * c + x], a[16 * c + x + 1]);
+                    raw = true;
+                    continue;
                 }
-                return top;
-            };
-            const float top = ok ? weights(true) : 0.f;
-            bool move = !begun || any_of_group(g, !ok || top > kLift + kReach || vexp > exp_run);
-            if (__builtin_expect(move, 0)) {
-                if (any_of_group(g, !ok)) {
-                    ok = false;
-                    break;
-                }
-                // maxima of the scores over the keys, and of the value scales' exponents
-                weights(false);
-                int *rexp = reinterpret_cast<int *>(red + 4 * kCols);
+                int *rexp = reinterpret_cast<int *>(red + 256);
 #pragma unroll
                 for (int x = 0; x < kCols; ++x) {
-                    if (x >= 16 * chunks) break;
+                    if (kChunks > 1 && x >= 16 * chunks) break;
                     const float m = warp_max(a[x]);
-                    if (lane == 0) red[quarter * kCols + x] = m;
+                    if (lane == 0) red[quarter * 64 + x] = m;
                 }
                 const int we = __reduce_max_sync(0xffffffffu, vexp);
                 if (lane == 0) rexp[quarter] = we;
@@ -271,44 +433,44 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
                     float alpha = 1.f;
                     if (key < cols) {
                         const float old = kLift - st->nm[g][key];
-                        const float m = fmaxf(old, fmaxf(fmaxf(red[key], red[kCols + key]), fmaxf(red[2 * kCols + key], red[3 * kCols + key])));
+                        const float m = fmaxf(old, fmaxf(fmaxf(red[key], red[64 + key]), fmaxf(red[128 + key], red[192 + key])));
                         alpha = ex2_approx(old - m);
                         st->nm[g][key] = kLift - m;
                     }
                     st->alpha[g][key] = alpha;
                 }
                 const int e = min((max(max(max(rexp[0], rexp[1]), max(rexp[2], rexp[3])), 8) + 3) & ~3, 252);
-                const float drop = !begun ? 0.f : pow2(exp_run - max(exp_run, e));
+                const float drop = pow2(exp_run - max(exp_run, e));
                 exp_run = max(exp_run, e);
                 group_sync(g);
+                if (begun) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c >= chunks) break;
-                    float f[16];
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        f[x] = st->alpha[g][16 * c + x];
-                        l[16 * c + x] *= f[x];
-                    }
-                    if (begun) {
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (kChunks > 1 && c >= chunks) break;
                         // S of this tile was issued after the group's previous V P: O is up to date
                         uint32_t v[16];
                         tmem_ld16(o_addr + 16u * c, v);
                         tmem_wait_ld();
                         reg_fence(v);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * (f[x] * drop));
+                        for (int x = 0; x < 16; ++x) {
+                            const float f = st->alpha[g][16 * c + x];
+                            l[16 * c + x] *= f;
+                            v[x] = __float_as_uint(__uint_as_float(v[x]) * (f * drop));
+                        }
                         tmem_st16(o_addr + 16u * c, v);
                     }
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
-                weights(true);
+                raw = false;
+                fresh = true;
             }
+            if (!ok) break;
             begun = true;
             const float wv = vs * pow2(127 - exp_run);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c >= chunks) break;
+            for (int c = 0; c < kChunks; ++c) {
+                if (kChunks > 1 && c >= chunks) break;
                 uint32_t pk[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
@@ -334,40 +496,31 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
             ++od;
             tc_fence_after();
         }
-        // ---- sums over the keys: 62 exchanges leave each lane two rows' sums over the warp
-        {
-            auto fold = [&](auto n_, int d_) {
-                constexpr int n = decltype(n_)::value;
-                const bool upper = (lane & (uint32_t)d_) != 0;
-#pragma unroll
-                for (int x = 0; x < n; ++x) {
-                    const float other = __shfl_xor_sync(0xffffffffu, upper ? l[x] : l[n + x], d_);
-                    l[x] = (upper ? l[n + x] : l[x]) + other;
-                }
-            };
-            fold(std::integral_constant<int, 32>{}, 16);
-            fold(std::integral_constant<int, 16>{}, 8);
-            fold(std::integral_constant<int, 8>{}, 4);
-            fold(std::integral_constant<int, 4>{}, 2);
-            fold(std::integral_constant<int, 2>{}, 1);
+        // ---- sums over the keys: each exchange halves the rows that a lane has sums of
+        if constexpr (kCols == 64) fold<32>(l, lane, 16), fold<16>(l, lane, 8), fold<8>(l, lane, 4), fold<4>(l, lane, 2), fold<2>(l, lane, 1);
+        else if constexpr (kCols == 32) fold<16>(l, lane, 16), fold<8>(l, lane, 8), fold<4>(l, lane, 4), fold<2>(l, lane, 2), fold<1>(l, lane, 1);
+        else fold<8>(l, lane, 16), fold<4>(l, lane, 8), fold<2>(l, lane, 4), fold<1>(l, lane, 2), l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+        if constexpr (kCols == 64) {
+            red[quarter * 64 + 2 * lane] = l[0];
+            red[quarter * 64 + 2 * lane + 1] = l[1];
+        } else {
+            red[quarter * 64 + lane * kCols / 32] = l[0];
         }
-        red[quarter * kCols + 2 * lane] = l[0];
-        red[quarter * kCols + 2 * lane + 1] = l[1];
         group_sync(g);
-        if (key < kCols) sums(g)[key] = (red[key] + red[kCols + key]) + (red[2 * kCols + key] + red[3 * kCols + key]);
+        if (key < kCols) sums(g)[key] = (red[key] + red[64 + key]) + (red[128 + key] + red[192 + key]);
         if (key == 0) st->exp[g] = exp_run, st->any[g] = begun ? 1 : 0;
         if (any_of_both(!ok)) break;
         // ---- a row's weight of either group's O, its LSE
         {
             const int r = g * kTile + key;      // of 256 threads, the first 128 have a row each
-            if (r < (turns ? kCols : 2 * kCols)) {
-                const int g0 = turns ? 0 : r / kCols, c = turns ? r : r % kCols;
+            if (r < (turns ? kCols : 128)) {
+                const int g0 = turns ? 0 : r / 64, c = turns ? r : r % 64;
                 const float m0 = kLift - st->nm[g0][c], l0 = sums(g0)[c];
                 const float m1 = turns ? kLift - st->nm[1][c] : kNoKey, l1 = turns ? sums(1)[c] : 0.f;
                 const float m = fmaxf(m0, m1), f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
                 const float sum = l0 * f0 + l1 * f1;
                 const bool empty = sum == 0.f;       // NaN is not empty
-                const bool bad = st->bad[kCols * g0 + c] || (turns && st->bad[kCols + c]);
+                const bool bad = st->bad[64 * g0 + c] || (turns && st->bad[64 + c]);
                 const float inv = empty ? 0.f : bad ? __uint_as_float(0x7fc00000u) : 1.f / sum;
                 st->alpha[g0][c] = f0 * inv;
                 if (turns) st->alpha[1][c] = f1 * inv;
@@ -385,10 +538,11 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
             uint8_t *out = d.part >= 0 ? p.ws + w.part_o : static_cast<uint8_t *>(p.out);
             const bool any0 = st->any[turns ? 0 : g] != 0, any1 = turns && st->any[1] != 0;
             const float u0 = pow2(st->exp[turns ? 0 : g] - 127), u1 = pow2(st->exp[1] - 127);
-            const uint32_t o0 = tmem + ((quarter * 32u) << 16) + 2 * kCols + (turns ? 0 : (uint32_t)g * kCols), o1 = o0 + kCols;
-            const int c0 = turns ? 2 * g : 0, c1 = turns ? 2 * g + 2 : 4;     // chunks of 16 rows
+            const uint32_t o0 = tmem + ((quarter * 32u) << 16) + 128u + (turns ? 0 : (uint32_t)g * 64u), o1 = o0 + 64u;
+            // chunks of 16 rows: each group's own, or, in turns, every other
+            const int c0 = turns ? g : 0, dc = turns ? 2 : 1;
 #pragma unroll 1
-            for (int c = c0; c < c1 && 16 * c < cols; ++c) {
+            for (int c = c0; 16 * c < cols; c += dc) {
                 float v[16];
                 uint32_t x0[16], x1[16];
                 tmem_ld16(o0 + 16u * c, x0);
@@ -420,12 +574,12 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
 
 // Fetches the codes of K or V tiles, a warp each: a copy per 16 keys (no page is smaller), none for keys
 // past the sequence's last or on a page that is none.
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &wait, bool values, int lane, uint32_t base, uint8_t *smem) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kRows>;
     const int v = values ? 2 : 0;
     const uint8_t *codes = values ? p.c.v : p.c.k;
-    uint32_t *groups = reinterpret_cast<uint32_t *>(smem + C::kMisc) + 2;
+    uint32_t *groups = reinterpret_cast<Stat *>(smem + C::kStat)->groups;
     uint32_t descs = 0, it = 0;
     bool ok = true;
     SegDesc d;
@@ -456,13 +610,13 @@ __device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &w
 // Widens the codes of K tiles (four warps, 32 keys each) or V tiles (four more).  Lane: 16 codes of a row, two
 // swizzle pieces of fp16; D / 16 lanes to a row.  Rows of V that are no key, or have a NaN code, become 0:
 // a weight of 0 must leave nothing of them.
-template <int D, bool kInt8>
+template <int D, int kRows, bool kInt8>
 __device__ __forceinline__ void widen_role(const Waiter &wait, bool values, int warp, int lane, uint8_t *smem) {
-    using C = Cfg<D>;
-    constexpr int kRowLanes = D / 16, kRows = 32 / kRowLanes, kSteps = 32 / kRows;
+    using C = Cfg<D, kRows>;
+    constexpr int kRowLanes = D / 16, kAtOnce = 32 / kRowLanes, kSteps = 32 / kAtOnce;
     const int v = values ? 2 : 0, col = lane % kRowLanes, sub_row = lane / kRowLanes;
     Stat *st = reinterpret_cast<Stat *>(smem + C::kStat);
-    const uint32_t *groups = reinterpret_cast<const uint32_t *>(smem + C::kMisc) + 2;
+    const uint32_t *groups = st->groups;
     // Eight lanes store 128 bytes at a time; where they share a row, half of them begin with their second
     // piece: every bank once.
     const bool swap = D == 128 && col >= 4;
@@ -479,10 +633,11 @@ __device__ __forceinline__ void widen_role(const Waiter &wait, bool values, int 
             uint8_t *tile = smem + dst + (values ? stage * C::kTileBytes : 0u);
             const uint32_t on = values ? groups[stage] >> (2 * warp) : 3u;
             const int left = d.n - tile_of(d, k) * kTile - warp * 32;
+            uint32_t odd = 0;                        // rows that have a NaN code
 #pragma unroll 2
             for (int i = 0; i < kSteps; ++i) {
-                const int r = i * kRows + sub_row;
-                uint4 x = *reinterpret_cast<const uint4 *>(raw + i * kRows * D);
+                const int r = i * kAtOnce + sub_row;
+                uint4 x = *reinterpret_cast<const uint4 *>(raw + i * kAtOnce * D);
                 if (values) {
                     bool none = r >= left || !((on >> (r >> 4)) & 1u);
                     if (!kInt8) {
@@ -490,10 +645,12 @@ __device__ __forceinline__ void widen_role(const Waiter &wait, bool values, int 
                         uint32_t nan = 0;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) nan |= ((y[q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                        const uint32_t b = __ballot_sync(0xffffffffu, nan != 0u) >> (sub_row * kRowLanes);
-                        const bool odd = (b & ((1u << kRowLanes) - 1u)) != 0u;
-                        if (col == 0) st->odd[stage][warp * 32 + r] = odd ? 1 : 0;
-                        none |= odd;
+                        const uint32_t b = __ballot_sync(0xffffffffu, nan != 0u);
+                        // one bit per row of the step
+#pragma unroll
+                        for (int q = 0; q < kAtOnce; ++q)
+                            if ((b >> (q * kRowLanes)) & ((1u << kRowLanes) - 1u)) odd |= 1u << (i * kAtOnce + q);
+                        none |= ((odd >> r) & 1u) != 0u;
                     }
                     if (none) x = make_uint4(0, 0, 0, 0);
                 }
@@ -504,10 +661,11 @@ __device__ __forceinline__ void widen_role(const Waiter &wait, bool values, int 
                     uint32_t o[4];
                     codes_to_f16x2<kInt8>(y[2 * q], o[0], o[1]);
                     codes_to_f16x2<kInt8>(y[2 * q + 1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(tile + i * kRows * 128 + (((q ? second : first) ^ r7) << 4)) =
+                    *reinterpret_cast<uint4 *>(tile + i * kAtOnce * 128 + (((q ? second : first) ^ r7) << 4)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
+            if (!kInt8 && values && lane == 0) st->odd[stage][warp] = odd;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -518,10 +676,10 @@ __device__ __forceinline__ void widen_role(const Waiter &wait, bool values, int 
     }
 }
 
-template <int D, bool kInt8>
+template <int D, int kRows, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
     bsattn_prefill_rows_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Layout w) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kRows>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) {  // the swizzle counts from 1024-byte boundaries
@@ -558,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
         fence_proxy_async_smem();
     }
+    if (threadIdx.x < 64) reinterpret_cast<Stat *>(smem + C::kStat)->zero[threadIdx.x] = 0.f;
     if (warp == 1) {
         tmem_alloc(base + C::kMisc, kTmemCols);
         tmem_relinquish();
@@ -568,6 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = misc[0];
     grid_launch_dependents();
     grid_dependency_wait();
+    find_piece<C>(p, w, smem);
+    __syncthreads();
     if (warp == 0) {
         regs_release<kCtrlRegs>();
         // ---------------------------------------------------- MMA issuer --
@@ -590,15 +751,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         SegDesc d;
         while (ok && next_desc<C>(wait, smem, descs, d)) {
             const int rows = d.tokens * p.G, n = d.k1 - d.k0;
-            const bool turns = rows <= kCols;
-            const uint32_t cols[2] = {(uint32_t)(min(rows, kCols) + 15) & ~15u, (uint32_t)((turns ? rows : rows - kCols) + 15) & ~15u};
+            const bool turns = kRows <= 64 || rows <= 64;
+            const uint32_t cols[2] = {(uint32_t)(min(rows, 64) + 15) & ~15u, (uint32_t)((turns ? rows : rows - 64) + 15) & ~15u};
             auto score = [&](int g) {
-                const uint64_t qd = desc_q + (turns ? 0u : (uint64_t)g * (kCols * 128 >> 4));
+                const uint64_t qd = desc_q + (turns ? 0u : (uint64_t)g * (64 * 128 >> 4));
                 const uint32_t idesc = idesc_s | ((cols[g] >> 3) << 17);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t off = (uint64_t)((kk >> 2) * kSubUnits + (kk & 3) * 2);
-                    mma_ss_lead(lead, tmem + g * kCols, desc_k + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+                    mma_ss_lead(lead, tmem + g * 64, desc_k + off, qd + off, idesc, kk > 0 ? 1u : 0u);
                 }
                 mma_commit_lead(lead, wait.bar(C::bSR + g));
             };
@@ -610,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t idesc = idesc_o | ((cols[g] >> 3) << 17);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    mma_ss_lead(lead, tmem + 2 * kCols + g * kCols, vd + (uint64_t)(kk * (2048 >> 4)),
+                    mma_ss_lead(lead, tmem + 128 + g * 64, vd + (uint64_t)(kk * (2048 >> 4)),
                                 pd + (uint64_t)(kk * (2048 >> 4)), idesc, kk > 0 || !first ? 1u : 0u);
                 return true;
             };
@@ -664,17 +825,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
         regs_release<kCtrlRegs>();
         if (warp == 1) {
-            if (lane == 0) schedule_role<C>(p, w, wait, smem);
+            if (lane == 0) segment_role<C>(p, w, wait, smem);
             __syncwarp();
         } else {
-            fetch_role<D>(p, wait, warp == 3, (int)lane, base, smem);
+            fetch_role<D, kRows>(p, wait, warp == 3, (int)lane, base, smem);
         }
     } else if (warp < 12) {
         regs_claim<kGroupRegs>();
-        group_role<D, kInt8>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
+        group_role<D, kRows, kInt8>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
     } else {
         regs_release<kWidenRegs>();
-        widen_role<D, kInt8>(wait, warp >= 16, (int)(warp & 3u), (int)lane, smem);
+        widen_role<D, kRows, kInt8>(wait, warp >= 16, (int)(warp & 3u), (int)lane, smem);
     }
     tc_fence_before();
     __syncthreads();
@@ -684,9 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool kInt8>
+template <int D, int kRows, bool kInt8>
 cudaError_t launch(const ChunkParams &p, const Layout &w, cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, kRows>;
     static int attr_set_for_device[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -695,23 +856,33 @@ cudaError_t launch(const ChunkParams &p, const Layout &w, cudaStream_t stream) {
     if (!attr_set_for_device[dev]) {
         // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, bsattn_prefill_rows_kernel<D, kInt8>);
+        e = cudaFuncGetAttributes(&fa, bsattn_prefill_rows_kernel<D, kRows, kInt8>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-        e = cudaFuncSetAttribute(bsattn_prefill_rows_kernel<D, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
+        e = cudaFuncSetAttribute(bsattn_prefill_rows_kernel<D, kRows, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
     void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w)};
-    return launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_rows_kernel<D, kInt8>), dim3((unsigned)w.ctas), kThreads,
+    return launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_rows_kernel<D, kRows, kInt8>), dim3((unsigned)w.ctas), kThreads,
                             C::kAlloc, args, stream);
+}
+
+template <int D, bool kInt8>
+cudaError_t launch_of(const ChunkParams &p, const Layout &w, cudaStream_t stream) {
+    switch (w.few) {
+    case 16: return launch<D, 16, kInt8>(p, w, stream);
+    case 32: return launch<D, 32, kInt8>(p, w, stream);
+    case 64: return launch<D, 64, kInt8>(p, w, stream);
+    default: return launch<D, 128, kInt8>(p, w, stream);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_rows(const ChunkParams &p, const Layout &w, cudaStream_t stream) {
-    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, w, stream) : launch<128, false>(p, w, stream);
-    return p.c.int8 ? launch<64, true>(p, w, stream) : launch<64, false>(p, w, stream);
+    if (p.c.D == 128) return p.c.int8 ? launch_of<128, true>(p, w, stream) : launch_of<128, false>(p, w, stream);
+    return p.c.int8 ? launch_of<64, true>(p, w, stream) : launch_of<64, false>(p, w, stream);
 }
 
 }  // namespace bsattn

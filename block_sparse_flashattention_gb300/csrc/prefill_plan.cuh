@@ -65,7 +65,7 @@ struct CutInfo {
 };
 
 struct Layout {
-    int few;                 // which kernel: see few_rows
+    int few;                 // rows of a segment, 0: two slots of 128 (see segment_rows)
     int tokens, step;        // of a slot: floor(128 / G); of a segment
     int pieces, ctas;
     long long tiles;         // of a head that the workspace has room for
@@ -74,10 +74,15 @@ struct Layout {
 };
 
 // Which kernel takes a call: with few query rows a KV head (per sequence, on the average) the one that
-// widens codes in shared memory, once per block of 128 rows; else the one that has them widened into the
-// workspace first.
-constexpr long long kFewRows = 128;
-inline int few_rows(int total, int B, int G) { return (long long)total * G <= kFewRows * B ? 1 : 0; }
+// widens codes in shared memory, for segments of up to 16, 32, 64 or 128 rows; else (0) the one that has them
+// widened into the workspace first.
+constexpr int kFewRows = 128;
+inline int segment_rows(int total, int B, int G) {
+    const long long mean = ((long long)total * G + B - 1) / B;
+    for (int rows = 16; rows <= kFewRows; rows *= 2)
+        if (mean <= rows && G <= rows) return rows;
+    return 0;
+}
 
 // Widened bytes that the CTAs work on at a time: of 129 MB of L2, less what else passes through.
 constexpr long long kPhaseBytes = 64ll << 20;
@@ -85,8 +90,8 @@ constexpr long long kPhaseBytes = 64ll << 20;
 inline Layout make_layout(int total, int B, int H, int G, int D, long long keys, int ctas) {
     Layout w = {};
     w.tokens = kTile / G;
-    w.few = few_rows(total, B, G);
-    w.step = w.few ? w.tokens : 2 * w.tokens;
+    w.few = segment_rows(total, B, G);
+    w.step = w.few ? w.few / G : 2 * w.tokens;
     w.ctas = ctas;
     w.tiles = w.few ? 0 : keys / kTile + B;   // the other kernel widens in shared memory
     w.blocks = (long long)total / w.step + B;

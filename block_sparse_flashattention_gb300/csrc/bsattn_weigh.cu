@@ -1,71 +1,691 @@
-// Attention weight of cached keys, summed over the queries of the newest tokens.
-#include "chunk_common.cuh"
+// Attention weight of cached keys, summed over the queries of the newest tokens: weight_j += sum_i exp(s_ij - lse_i).
+//
+// The lse is known, so that the softmax needs no pass of its own, and V is not read: D + 4 bytes per key and
+// KV head, 2 D flop and an exponential per query row on it.  From some 100 rows on the exponentials and the
+// products bound it, below that HBM.
+//
+// Keys lie on the tensor cores' 128 rows and queries on their columns: S^T = K' Q^T with K' = bf16(code), exact,
+// and Q as it is.  A thread has one key, so that the sum over the queries stays in its registers: weight = sum_r
+// 2^(S_r c - lse_r log2(e)), c = ks softmax_scale log2(e).  The sum is fp32 within a block of 128 rows, and
+// compensated from block to block: thousands of rows cost no more accuracy than one block does.
+//
+// A unit is 256 keys of a (sequence, KV head): two tiles, one for each of two groups of 128 threads, whose blocks of
+// query rows are loaded once for both.  Units are handed out along a line on which each counts its blocks and
+// kUnitCost; every CTA numbers the line for itself (lengths are on the device).  A unit is not split: its weights
+// have one writer, and their sums one order.
+//
+// Roles (640 threads, one CTA per SM, all of TMEM):
+//   warp 0        issues the MMAs
+//   warp 1        owns the TMEM allocation; finds the CTA's units
+//   warp 2        fetches the codes of keys: bulk copies of 16 keys into raw tiles
+//   warp 3        query blocks (TMA) and their lse
+//   warps 4-7, 8-11   group 0, group 1: sums
+//   warps 12-15, 16-19   widen the codes of group 0's and group 1's tile (128-byte swizzle)
+// TMEM: S^T of group g and buffer i: [256 g + 128 i, 256 g + 128 i + 128).
 #include "kv_codes.cuh"
+#include "prefill_plan.cuh"
 
 namespace bsattn {
 
 namespace {
 
-constexpr int kThreads = 128, kRows = 32;
+constexpr int kThreads = 640;
+constexpr uint32_t kTmemCols = 512;
+// 96 registers per thread at launch: 128 * 48 + 2 * 128 * 152 + 2 * 128 * 64 = 61440 = 640 * 96.
+constexpr int kLaunchRegs = 96;
+constexpr uint32_t kCtrlRegs = 48, kGroupRegs = 152, kWidenRegs = 64;
+static_assert(128 * kCtrlRegs + 256 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 bf16: one 128-byte swizzle span
+constexpr int kUnitKeys = 2 * kTile;
+constexpr int kUnitCost = 2;                // blocks that a unit's own work is worth
+constexpr int kSeqChunk = 2048;             // sequences whose places fit shared memory at a time
+constexpr int kUnits = 2;                   // units found ahead
 
-// One thread per key, 32 query rows at a time in shared memory.
-template <int D, bool kInt8>
-__global__ void __launch_bounds__(kThreads) bsattn_weigh_kernel(const __grid_constant__ ChunkParams p) {
-    __shared__ float sq[kRows][D], sl[kRows];
-    const int b = blockIdx.y, h = blockIdx.z;
-    const Chunk s = chunk_of(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-    const int32_t *table = p.table + (long long)b * p.table_stride;
-    const int rows = s.m * p.G;
-    if (rows == 0) return;
-    for (int j0 = blockIdx.x * kThreads; j0 < s.n; j0 += gridDim.x * kThreads) {
-        const int j = j0 + threadIdx.x;
-        const long long row = j < s.n ? cache_row(p.c, table, h, j) : -1;
-        if (j < s.n && row < 0 && h == 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
-        float k[D], w = 0.f;
-        for (int d = 0; d < D; d += 4) {
-            float y[4] = {};
-            if (row >= 0) {
-                const uint32_t x = *reinterpret_cast<const uint32_t *>(p.c.k + row * D + d);
-                if (kInt8) unpack_int8(x, y);
-                else unpack_e4m3(x, y);
-            }
-            for (int i = 0; i < 4; ++i) k[d + i] = y[i];
+// Rows of a query block: tokens of all of a KV head's query heads.
+struct Blocks {
+    int tokens;              // of a block
+    int cols;                // columns of the products: rows, up to a multiple of 32
+};
+
+struct Unit {
+    int32_t b, h;            // b < 0: no more
+    int32_t key0, n;         // first key, keys of the sequence
+    int32_t first, m;        // the sequence's queries
+    int32_t q0, q1;          // blocks that some of the keys are met by
+};
+
+// kFew: blocks of up to 64 rows, where HBM bounds the kernel: some 100 KB of codes on their way, one unit widened.  Else
+// the next unit is widened while the many blocks of one are worked on.
+template <int D, bool kFew>
+struct Cfg {
+    static constexpr int kStages = kFew ? 1 : 2, kRaws = kFew ? (D == 128 ? 3 : 6) : 1;
+    static constexpr uint32_t kTileBytes = kTile * D * 2, kRawBytes = kTile * D;
+    static constexpr uint32_t kBlockBytes = kFew ? kTileBytes / 2 : kTileBytes;
+    static constexpr uint32_t kBlockSub = kFew ? kSub / 2 : kSub;    // 64 columns of a block
+    static constexpr uint32_t kQ = 0, kK = kQ + 2 * kBlockBytes;     // two blocks; [stages][2 groups]
+    static constexpr uint32_t kRaw = kK + kStages * 2 * kTileBytes;  // [raws][2 groups]
+    static constexpr uint32_t kScale = kRaw + kRaws * 2 * kRawBytes; // key scales of the raw tiles
+    static constexpr uint32_t kLse = kScale + kRaws * 1024;          // -lse log2(e) of the two blocks' rows
+    static constexpr uint32_t kOn = kLse + 2 * 512;                  // raw tiles' 16-key groups that are there
+    static constexpr uint32_t kOdd = kOn + 32;                       // keys that have a NaN code, of four units
+    static constexpr uint32_t kUnit = kOdd + 4 * 32;
+    static constexpr uint32_t kBar = kUnit + kUnits * (uint32_t)sizeof(Unit);
+    // K' full (2 stage + group) and empty (stage), query blocks full and empty, S full and empty (2 group + buffer), raw
+    // units full and empty, units full and empty
+    static constexpr int bKF = 0, bKE = 4, bQF = 6, bQE = 8, bSF = 10, bSE = 14, bRF = 18, bRE = 24, bUF = 30, bUE = bUF + kUnits,
+                         bDrain = bUE + kUnits, kNumBars = bDrain + 1;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // tmem base, abort; see Start
+    static constexpr uint32_t kAlloc = kMisc + 64;
+    static_assert(kAlloc <= 227u * 1024u, "shared memory");
+};
+
+// Where the CTA's piece of the line begins.
+struct Start {
+    uint32_t tmem;
+    int32_t abort;
+    int32_t b, h, u, pieces;
+    long long begin, line;
+};
+
+// Blocks that meet a key of j0 .. j1 (below n): a range.
+struct Range {
+    int q0, q1;
+};
+
+__device__ __forceinline__ Range blocks_of(const ChunkParams &p, const Blocks &w, const Chunk &c, int j0, int j1) {
+    const int nb = (c.m + w.tokens - 1) / w.tokens, pos = c.n - c.m;
+    Range r = {0, nb};
+    if (p.kind == BSATTN_MASK_CAUSAL || p.kind == BSATTN_MASK_SLIDING_WINDOW || (p.kind == BSATTN_MASK_PREFIX && j0 >= p.prefix_len))
+        r.q0 = min(max(j0 - pos, 0) / w.tokens, nb);
+    if (p.kind == BSATTN_MASK_SLIDING_WINDOW && j0 >= p.sink_tokens) {
+        const long long t = (long long)j1 + p.window_left - pos;     // tokens below t meet the last key
+        r.q1 = t <= 0 ? 0 : (int)min((t + w.tokens - 1) / w.tokens, (long long)nb);
+    }
+    r.q1 = max(r.q1, r.q0);
+    return r;
+}
+
+__device__ __forceinline__ Range unit_blocks(const ChunkParams &p, const Blocks &w, const Chunk &c, int u) {
+    return blocks_of(p, w, c, u * kUnitKeys, min((u + 1) * kUnitKeys, c.n) - 1);
+}
+
+__device__ __forceinline__ int unit_count(const Chunk &c) { return c.m > 0 ? (c.n + kUnitKeys - 1) / kUnitKeys : 0; }
+
+// Places of one head's units of a sequence, by a warp: a lane counts every 32nd unit.
+__device__ __forceinline__ long long pass_places(const ChunkParams &p, const Blocks &w, const Chunk &c, int lane) {
+    long long sum = 0;
+    for (int u = lane; u < unit_count(c); u += 32) {
+        const Range r = unit_blocks(p, w, c, u);
+        sum += kUnitCost + r.q1 - r.q0;
+    }
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return sum;
+}
+
+// Numbers the line and finds where the CTA's piece begins; all threads.
+__device__ __forceinline__ void find_piece(const ChunkParams &p, const Blocks &w, Start *st, long long *pass) {
+    const int tid = (int)threadIdx.x, lane = tid % 32, warp = tid / 32;
+    long long *warps = pass + kSeqChunk;
+    // of a chunk of sequences: each one's places before it (of all heads), and those of all
+    auto number = [&](int b0, bool check, long long before) -> long long {
+        const int n = min(kSeqChunk, p.B - b0);
+        __syncthreads();
+        for (int i = warp; i < n; i += kThreads / 32) {
+            const Chunk c = chunk_of(p, b0 + i, check && lane == 0);
+            const long long x = pass_places(p, w, c, lane);
+            if (lane == 0) pass[i] = x * p.c.H;
         }
-        const float f = row >= 0 ? p.c.ks[row] * p.scale_log2 : 0.f;
-        for (int r0 = 0; r0 < rows; r0 += kRows) {
-            __syncthreads();
-            for (int x = threadIdx.x; x < kRows * D; x += kThreads) {
-                const int r = r0 + x / D, t = s.first + r / p.G, hq = h * p.G + r % p.G;
-                sq[x / D][x % D] = r < rows ? __uint_as_float((uint32_t)p.q[(long long)t * p.q_stride + (long long)hq * D + x % D] << 16) : 0.f;
-                if (x % D == 0) {
-                    const float lse = r < rows ? p.lse[(long long)t * p.Hq + hq] : -INFINITY;
-                    sl[x / D] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+        __syncthreads();
+        // a thread sums consecutive sequences
+        const int per = (n + kThreads - 1) / kThreads, lo = min(tid * per, n), hi = min(lo + per, n);
+        long long s = 0;
+        for (int i = lo; i < hi; ++i) s += pass[i];
+        const long long own = s;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        if (lane == 31) warps[warp] = s;
+        __syncthreads();
+        long long all = 0, at = before + s - own;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) at += warps[i];
+            all += warps[i];
+        }
+        for (int i = lo; i < hi; ++i) {
+            const long long x = pass[i];
+            pass[i] = at;
+            at += x;
+        }
+        __syncthreads();
+        return before + all;
+    };
+    long long line = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kSeqChunk) line = number(b0, blockIdx.x == 0, line);
+    const int pieces = (int)max(1ll, min((long long)gridDim.x, line / kUnitCost)), piece = (int)blockIdx.x;
+    if (tid == 0) st->b = p.B, st->pieces = pieces, st->line = line;
+    if (piece >= pieces || line == 0) return;
+    const long long from = line * piece / pieces;
+    long long at = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kSeqChunk) {
+        const long long end = p.B > kSeqChunk ? number(b0, false, at) : line;
+        const int n = min(kSeqChunk, p.B - b0);
+        if (from >= at && from < end) {
+            // the last sequence that begins at or before `from`
+            int i = 0, hi = n - 1;
+            while (i < hi) {
+                const int mid = (i + hi + 1) / 2;
+                if (pass[mid] <= from) i = mid;
+                else hi = mid - 1;
+            }
+            if (warp == 0) {
+                const Chunk c = chunk_of(p, b0 + i, false);
+                const long long places = pass_places(p, w, c, lane);
+                if (places > 0) {
+                    const int h = (int)((from - pass[i]) / places);
+                    long long begin = pass[i] + h * places;
+                    // the first unit that begins at or behind `from`
+                    int u = 0;
+                    for (bool found = false; !found && u < unit_count(c);) {
+                        long long x = 0;
+                        if (u + lane < unit_count(c)) {
+                            const Range r = unit_blocks(p, w, c, u + lane);
+                            x = kUnitCost + r.q1 - r.q0;
+                        }
+                        long long s = x;
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const long long y = __shfl_up_sync(0xffffffffu, s, d);
+                            if (lane >= d) s += y;
+                        }
+                        const uint32_t hit = __ballot_sync(0xffffffffu, u + lane < unit_count(c) && begin + s - x >= from);
+                        if (hit) {
+                            const int k = __ffs(hit) - 1;
+                            begin += __shfl_sync(0xffffffffu, s - x, k);
+                            u += k;
+                            found = true;
+                        } else {
+                            begin += __shfl_sync(0xffffffffu, s, 31);
+                            u = min(u + 32, unit_count(c));
+                        }
+                    }
+                    if (lane == 0) st->b = b0 + i, st->h = h, st->u = u, st->begin = begin;
                 }
             }
-            __syncthreads();
-            for (int r = 0; r < kRows && r0 + r < rows; ++r) {
-                const Met e = met(p, s.n - s.m + (r0 + r) / p.G, s.n);
-                if (!(j < e.hb || (j >= e.la && j < e.ha)) || row < 0) continue;
-                float acc = 0.f;
-                for (int d = 0; d < D; ++d) acc += sq[r][d] * k[d];
-                w += exp2f(acc * f - sl[r]);
-            }
         }
-        if (row >= 0) p.weights[row] = p.accumulate ? p.weights[row] + w : w;
+        at = end;
     }
 }
 
-template <int D, bool kInt8>
-cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
-    bsattn_weigh_kernel<D, kInt8><<<dim3(256, p.B, p.c.H), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+template <class C>
+__device__ __forceinline__ bool next_unit(const Waiter &wait, const uint8_t *smem, uint32_t &count, Unit &x) {
+    const int slot = (int)(count % kUnits);
+    if (!__all_sync(0xffffffffu, wait(C::bUF + slot, count / kUnits))) return false;
+    x = reinterpret_cast<const Unit *>(smem + C::kUnit)[slot];
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(wait.bar(C::bUE + slot));
+    ++count;
+    return x.b >= 0;
+}
+
+// Finds the units that begin in the CTA's piece.
+template <class C>
+__device__ __forceinline__ void unit_role(const ChunkParams &p, const Blocks &w, const Waiter &wait, uint8_t *smem, const Start &st) {
+    uint32_t count = 0;
+    auto emit = [&](const Unit &x) -> bool {
+        const int slot = (int)(count % kUnits);
+        if (!wait(C::bUE + slot, (count / kUnits) ^ 1u)) return false;
+        reinterpret_cast<Unit *>(smem + C::kUnit)[slot] = x;
+        mbar_arrive(wait.bar(C::bUF + slot));
+        ++count;
+        return true;
+    };
+    int b = st.b, h = st.h, u = st.u;
+    if (b < p.B) {
+        const long long to = st.line * ((long long)blockIdx.x + 1) / st.pieces;
+        long long begin = st.begin;
+        Chunk c = chunk_of(p, b, false);
+        int units = unit_count(c);
+        while (begin < to) {
+            if (u >= units) {
+                u = 0;
+                if (units == 0 || ++h >= p.c.H) {
+                    h = 0;
+                    if (++b >= p.B) break;
+                    c = chunk_of(p, b, false);
+                    units = unit_count(c);
+                }
+                continue;
+            }
+            const Range r = unit_blocks(p, w, c, u);
+            // where weights are added to, keys that no query meets need nothing
+            if (r.q1 > r.q0 || !p.accumulate) {
+                Unit x;
+                x.b = b, x.h = h, x.key0 = u * kUnitKeys, x.n = c.n;
+                x.first = c.first, x.m = c.m, x.q0 = r.q0, x.q1 = r.q1;
+                if (!emit(x)) return;
+            }
+            begin += kUnitCost + r.q1 - r.q0;
+            ++u;
+        }
+    }
+    Unit stop = {};
+    stop.b = -1;
+    emit(stop);
+}
+
+// One group: 128 threads, a key each.
+template <int D, bool kFew>
+__device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w, const Waiter &wait, uint32_t tmem, int g, uint32_t warp,
+                                           uint32_t lane, uint8_t *smem) {
+    using C = Cfg<D, kFew>;
+    const uint32_t quarter = warp & 3u;
+    const int key = (int)(quarter * 32 + lane) + g * kTile;
+    const uint32_t s_addr = tmem + ((quarter * 32u) << 16) + (uint32_t)g * 256u;
+    uint32_t units = 0, ut = 0, it = 0;          // units, those with blocks, blocks so far
+    Unit x;
+    while (next_unit<C>(wait, smem, units, x)) {
+        const int j = x.key0 + key;
+        const long long row = j < x.n ? cache_row(p.c, p.table + (long long)x.b * p.table_stride, x.h, j) : -1;
+        float c = 0.f;
+        bool there = false;
+        // tokens that meet the key: lo <= t < hi
+        const int pos = x.n - x.m;
+        int lo = 0, hi = 0;
+        bool ok = true;
+        if (x.q1 > x.q0) {
+            const uint32_t raw = ut % C::kRaws;
+            ok = __all_sync(0xffffffffu, wait(C::bRF + (int)raw, ut / C::kRaws));
+            if (!ok) break;
+            const uint32_t on = reinterpret_cast<const uint32_t *>(smem + C::kOn)[raw];
+            there = j < x.n && ((on >> (key >> 4)) & 1u);
+            c = reinterpret_cast<const float *>(smem + C::kScale + raw * 1024u)[key] * p.scale_log2;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wait.bar(C::bRE + (int)raw));
+        }
+        if (there) {
+            hi = x.m;
+            if (p.kind == BSATTN_MASK_CAUSAL || p.kind == BSATTN_MASK_SLIDING_WINDOW || (p.kind == BSATTN_MASK_PREFIX && j >= p.prefix_len))
+                lo = max(j - pos, 0);
+            if (p.kind == BSATTN_MASK_SLIDING_WINDOW && j >= p.sink_tokens)
+                hi = (int)min(max((long long)j + p.window_left - pos, 0ll), (long long)x.m);
+        }
+        float sum = 0.f, lost = 0.f;             // compensated
+        for (int q = x.q0; q < x.q1; ++q, ++it) {
+            const uint32_t buf = it & 1u;
+            ok = __all_sync(0xffffffffu, wait(C::bSF + 2 * g + (int)buf, it >> 1) && wait(C::bQF + (int)buf, it >> 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (q == x.q0 && ((reinterpret_cast<const uint32_t *>(smem + C::kOdd)[8 * (ut & 3u) + 4 * g + quarter] >> lane) & 1u))
+                c = __uint_as_float(0x7fc00000u);
+            // of the block: columns that meet the key; of none behind the sequence's last token
+            const int t0 = q * w.tokens, tokens = min(w.tokens, x.m - t0);
+            const int from = min(max(lo - t0, 0), tokens) * p.G, to = min(max(hi - t0, 0), tokens) * p.G;
+            const bool masked = __any_sync(0xffffffffu, from > 0 || to < w.tokens * p.G);
+            const float4 *nl = reinterpret_cast<const float4 *>(smem + C::kLse + buf * 512u);
+            const uint32_t at = s_addr + buf * 128u;
+            float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+            auto chunk = [&](int cc, uint32_t (&v)[32]) {
+                float y[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 n = nl[8 * cc + i];
+                    ffma2(y[4 * i], y[4 * i + 1], __uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), c, c, n.x, n.y);
+                    ffma2(y[4 * i + 2], y[4 * i + 3], __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]), c, c, n.z, n.w);
+                }
+                if (masked) {
+                    const int f = from - 32 * cc, t = to - 32 * cc;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < f || i >= t) y[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    fadd2(a0, a1, a0, a1, ex2_approx(y[i]), ex2_approx(y[i + 1]));
+                    fadd2(b0, b1, b0, b1, ex2_approx(y[i + 2]), ex2_approx(y[i + 3]));
+                }
+            };
+            uint32_t va[32], vb[32];
+            const int chunks = w.cols / 32;
+            tmem_ld32(at, va);
+#pragma unroll 1
+            for (int cc = 0; cc < chunks; cc += 2) {
+                tmem_wait_ld();
+                reg_fence(va);
+                if (cc + 1 < chunks) tmem_ld32(at + 32u * (cc + 1), vb);
+                chunk(cc, va);
+                if (cc + 1 >= chunks) break;
+                tmem_wait_ld();
+                reg_fence(vb);
+                if (cc + 2 < chunks) tmem_ld32(at + 32u * (cc + 2), va);
+                chunk(cc + 1, vb);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(wait.bar(C::bSE + 2 * g + (int)buf));
+                mbar_arrive(wait.bar(C::bQE + (int)buf));
+            }
+            const float add = ((a0 + b0) + (a1 + b1)) - lost, next = sum + add;
+            lost = (next - sum) - add;
+            sum = next;
+        }
+        if (!ok) break;
+        if (x.q1 > x.q0) ++ut;
+        if (row >= 0) {
+            if (!p.accumulate) p.weights[row] = sum;
+            else if (hi > lo) atomicAdd(p.weights + row, sum);
+        }
+    }
+}
+
+// Fetches the codes and scales of a unit's two tiles: copies of 16 keys (no page is smaller), none for keys past
+// the last or on a page that is none.
+template <int D, bool kFew>
+__device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &wait, int lane, uint32_t base, uint8_t *smem) {
+    using C = Cfg<D, kFew>;
+    uint32_t units = 0, it = 0;
+    bool ok = true;
+    Unit x;
+    while (ok && next_unit<C>(wait, smem, units, x)) {
+        const int32_t *table = p.table + (long long)x.b * p.table_stride;
+        const int key = x.key0 + 16 * lane;
+        long long row = -1;
+        if (lane < 16 && key < x.n) {
+            row = cache_row(p.c, table, x.h, key);
+            if (row < 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+        }
+        if (x.q1 == x.q0) continue;              // no query meets them
+        const uint32_t on = __ballot_sync(0xffffffffu, row >= 0), raw = it % C::kRaws;
+        if (!(ok = __all_sync(0xffffffffu, wait(C::bRE + (int)raw, (it / C::kRaws) ^ 1u)))) break;
+        if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::kOn)[raw] = on;
+        const uint32_t full = wait.bar(C::bRF + (int)raw), lead = row >= 0 ? 1u : 0u;
+        mbar_arrive_expect_tx_lead(lane == 0 ? 1u : 0u, full, (uint32_t)__popc(on) * (16u * D + 64u));
+        __syncwarp();
+        bulk_g2s_lead(lead, base + C::kRaw + raw * 2u * C::kRawBytes + (uint32_t)lane * 16u * D, p.c.k + row * D, 16u * D, full);
+        bulk_g2s_lead(lead, base + C::kScale + raw * 1024u + (uint32_t)lane * 64u, p.c.ks + row, 64u, full);
+        ++it;
+    }
+    // nothing may be on its way into a tile when the CTA ends
+    for (uint32_t s = 0; s < (uint32_t)C::kRaws; ++s)
+        if (it > s) mbar_wait_drain(wait.bar(C::bRF + (int)s), ((it - 1 - s) / C::kRaws) & 1u);
+}
+
+// Two e4m3 or int8 codes (16-bit halves of `x`, the code in the high byte) as bf16.  e4m3: its exponent and
+// mantissa moved to bf16's are the value times 2^-120.  int8, whose low 7 bits l and sign s make 128 + l (bits
+// 0x4300 | l) less 128 or, where s, 256.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t code_to_bf16x2(uint32_t x) {
+    uint32_t r;
+    if constexpr (kInt8) {
+        const uint32_t y = x >> 8;               // codes in the low bytes
+        const uint32_t a = (y & 0x007f007fu) | 0x43004300u, b = (y & 0x00800080u) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+        const uint32_t a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7b807b80u));   // 2^120
+    }
+    return r;
+}
+
+// Widens the codes of a group's tile (four warps, 32 keys each).  Lane: 16 codes of a row, two swizzle pieces; D / 16
+// lanes to a row.  What no copy has filled is left: such keys are masked.
+template <int D, bool kFew, bool kInt8>
+__device__ __forceinline__ void widen_role(const Waiter &wait, int g, int warp, int lane, uint8_t *smem) {
+    using C = Cfg<D, kFew>;
+    constexpr int kRowLanes = D / 16, kAtOnce = 32 / kRowLanes, kSteps = 32 / kAtOnce;
+    const int col = lane % kRowLanes, sub_row = lane / kRowLanes;
+    // Eight lanes store 128 bytes at a time; where they share a row, half of them begin with their second
+    // piece: every bank once.
+    const bool swap = D == 128 && col >= 4;
+    const int first = 2 * (col & 3) + (swap ? 1 : 0), second = first ^ 1;
+    const uint8_t *raw = smem + C::kRaw + (uint32_t)g * C::kRawBytes + (warp * 32 + sub_row) * D + col * 16;
+    uint8_t *dst = smem + C::kK + (uint32_t)g * C::kTileBytes + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 32 + sub_row) * 128u;
+    uint32_t units = 0, it = 0;
+    Unit x;
+    while (next_unit<C>(wait, smem, units, x)) {
+        if (x.q1 == x.q0) continue;
+        const uint32_t stage = it % C::kStages, rs = it % C::kRaws;
+        if (!__all_sync(0xffffffffu, wait(C::bKE + (int)stage, (it / C::kStages) ^ 1u) && wait(C::bRF + (int)rs, it / C::kRaws))) return;
+        const uint8_t *from = raw + rs * 2u * C::kRawBytes;
+        uint8_t *tile = dst + stage * 2u * C::kTileBytes;
+        uint32_t odd = 0;                        // rows that have a NaN code
+#pragma unroll 2
+        for (int i = 0; i < kSteps; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * kAtOnce * D);
+            const uint32_t y[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z, swap ? v.y : v.w};
+            const int r7 = (i * kAtOnce + sub_row) & 7;
+            if (!kInt8) {
+                uint32_t nan = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) nan |= (y[q] & 0x7f7f7f7fu) + 0x01010101u;
+                const uint32_t b = __ballot_sync(0xffffffffu, (nan & 0x80808080u) != 0u);
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q)
+                    if ((b >> (q * kRowLanes)) & ((1u << kRowLanes) - 1u)) odd |= 1u << (i * kAtOnce + q);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    o[2 * k] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x1404));
+                    o[2 * k + 1] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x3424));
+                }
+                *reinterpret_cast<uint4 *>(tile + i * kAtOnce * 128 + (((q ? second : first) ^ r7) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::kOdd)[8 * (it & 3u) + 4 * g + warp] = odd;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(wait.bar(C::bKF + 2 * (int)stage + g));
+            mbar_arrive(wait.bar(C::bRE + (int)rs));
+        }
+        ++it;
+    }
+}
+
+template <int D, bool kFew, bool kInt8>
+__global__ void __launch_bounds__(kThreads, 1)
+    bsattn_weigh_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Blocks w, const __grid_constant__ CUtensorMap tq) {
+    using C = Cfg<D, kFew>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {  // the swizzle counts from 1024-byte boundaries
+        if (threadIdx.x == 0 && p.err) atomicOr(p.err, BSATTN_FLAG_TIMEOUT);
+        return;
+    }
+    Start *st = reinterpret_cast<Start *>(smem + C::kMisc);
+    const uint32_t warp = warp_id(), lane = lane_id();
+    Waiter wait;
+    wait.bars = base + C::kBar;
+    wait.abort = &st->abort;
+    wait.err = p.err;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(wait.bar(C::bKF + s), 4);      // one arrival per widening warp
+            mbar_init(wait.bar(C::bSF + s), 1);
+            mbar_init(wait.bar(C::bSE + s), 4);      // one per warp of the group
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(wait.bar(C::bKE + s), 1);
+            mbar_init(wait.bar(C::bQF + s), 1);
+            mbar_init(wait.bar(C::bQE + s), 9);      // the products' completion, one per warp of the groups
+        }
+        for (int s = 0; s < C::kRaws; ++s) {
+            mbar_init(wait.bar(C::bRF + s), 1);
+            mbar_init(wait.bar(C::bRE + s), 16);     // widening and group warps
+        }
+        for (int s = 0; s < kUnits; ++s) {
+            mbar_init(wait.bar(C::bUF + s), 1);
+            mbar_init(wait.bar(C::bUE + s), 19);     // issuing, fetching, query, group and widening warps
+        }
+        mbar_init(wait.bar(C::bDrain), 1);
+        st->abort = 0;
+        fence_barrier_init();
+    }
+    // rows of a block that no copy fills stay 0
+    for (uint32_t i = threadIdx.x; i < 2 * C::kBlockBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(smem + C::kQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 1) {
+        tmem_alloc(base + C::kMisc, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = st->tmem;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    find_piece(p, w, st, reinterpret_cast<long long *>(smem + C::kK));
+    __syncthreads();
+    if (warp == 0) {
+        regs_release<kCtrlRegs>();
+        // ---------------------------------------------------- MMA issuer --
+        // The whole warp runs in step; lane 0 issues.
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        const uint32_t idesc = idesc_bf16_f32(128, w.cols, false);
+        const uint64_t desc_q = smem_desc_sw128(base + C::kQ, 16, 1024);
+        const uint64_t desc_k = smem_desc_sw128(base + C::kK, 16, 1024);
+        constexpr uint64_t kTileUnits = C::kTileBytes >> 4, kBlockUnits = C::kBlockBytes >> 4;
+        uint32_t units = 0, kt = 0, it = 0;
+        bool ok = true;
+        auto ready = [&](int b, uint32_t phase) -> bool {
+            ok = ok && wait(b, phase);
+            return ok;
+        };
+        Unit x;
+        while (ok && next_unit<C>(wait, smem, units, x)) {
+            if (x.q1 == x.q0) continue;
+            const uint32_t stage = kt % C::kStages;
+            for (int q = x.q0; ok && q < x.q1; ++q, ++it) {
+                const uint32_t buf = it & 1u;
+                if (!ready(C::bQF + (int)buf, it >> 1)) break;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (q == x.q0 && !ready(C::bKF + 2 * (int)stage + g, kt / C::kStages)) break;
+                    if (!ready(C::bSE + 2 * g + (int)buf, (it >> 1) ^ 1u)) break;
+                    tc_fence_after();
+                    const uint64_t kd = desc_k + (uint64_t)(2 * stage + g) * kTileUnits, qd = desc_q + (uint64_t)buf * kBlockUnits;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t in = (uint64_t)((kk & 3) * 2);
+                        mma_ss_lead(lead, tmem + g * 256 + buf * 128, kd + (uint64_t)(kk >> 2) * (kSub >> 4) + in,
+                                    qd + (uint64_t)(kk >> 2) * (C::kBlockSub >> 4) + in, idesc, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_lead(lead, wait.bar(C::bSF + 2 * g + (int)buf));
+                }
+                if (!ok) break;
+                mma_commit_lead(lead, wait.bar(C::bQE + (int)buf));
+            }
+            if (!ok) break;
+            mma_commit_lead(lead, wait.bar(C::bKE + (int)stage));
+            ++kt;
+        }
+        // Wait until every tcgen05 operation issued above has completed.
+        mma_commit_lead(lead, wait.bar(C::bDrain));
+        mbar_wait_drain(wait.bar(C::bDrain), 0);
+    } else if (warp == 1) {
+        regs_release<kCtrlRegs>();
+        if (lane == 0) unit_role<C>(p, w, wait, smem, *st);
+        __syncwarp();
+    } else if (warp == 2) {
+        regs_release<kCtrlRegs>();
+        fetch_role<D, kFew>(p, wait, (int)lane, base, smem);
+    } else if (warp == 3) {
+        regs_release<kCtrlRegs>();
+        // ------------------------------------------------- query blocks --
+        if (lane == 0) tma_prefetch_desc(&tq);
+        const uint32_t bytes = (uint32_t)(p.G * w.tokens) * D * 2u;
+        uint32_t units = 0, it = 0;
+        bool ok = true;
+        Unit x;
+        while (ok && next_unit<C>(wait, smem, units, x)) {
+            for (int q = x.q0; q < x.q1; ++q, ++it) {
+                const uint32_t buf = it & 1u;
+                const int t0 = q * w.tokens, rows = min(w.tokens, x.m - t0) * p.G;
+                float nl[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 32 * i + (int)lane, tok = r / p.G;
+                    nl[i] = r < rows ? __ldg(p.lse + (long long)(x.first + t0 + tok) * p.Hq + x.h * p.G + r - tok * p.G) : INFINITY;
+                }
+                if (!(ok = __all_sync(0xffffffffu, wait(C::bQE + (int)buf, (it >> 1) ^ 1u)))) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)     // -inf: a query without keys
+                    reinterpret_cast<float *>(smem + C::kLse + buf * 512u)[32 * i + lane] = nl[i] == -INFINITY ? -INFINITY : nl[i] * -1.44269504088896340736f;
+                __syncwarp();
+                const uint32_t full = wait.bar(C::bQF + (int)buf), lead = lane == 0 ? 1u : 0u;
+                mbar_arrive_expect_tx_lead(lead, full, bytes);
+                __syncwarp();
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d_lead(lead, base + C::kQ + buf * C::kBlockBytes + c * C::kBlockSub, &tq, full, c * 64, x.h * p.G, x.first + t0);
+            }
+        }
+        // nothing may be on its way into shared memory when the CTA ends
+        for (uint32_t s = 0; s < 2; ++s)
+            if (it > s) mbar_wait_drain(wait.bar(C::bQF + (int)s), ((it - 1 - s) >> 1) & 1u);
+    } else if (warp < 12) {
+        regs_claim<kGroupRegs>();
+        group_role<D, kFew>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
+    } else {
+        regs_release<kWidenRegs>();
+        widen_role<D, kFew, kInt8>(wait, warp >= 16 ? 1 : 0, (int)(warp & 3u), (int)lane, smem);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool kFew, bool kInt8>
+cudaError_t launch(const ChunkParams &p, const Blocks &w, cudaStream_t stream) {
+    using C = Cfg<D, kFew>;
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, bsattn_weigh_kernel<D, kFew, kInt8>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(bsattn_weigh_kernel<D, kFew, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    const int sms = current_device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    CUtensorMap tq = {};
+    if (p.total > 0 && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
+    void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Blocks *>(&w), &tq};
+    return launch_dependent(reinterpret_cast<const void *>(bsattn_weigh_kernel<D, kFew, kInt8>), dim3((unsigned)sms), kThreads,
+                            C::kAlloc, args, stream);
+}
+
+template <int D, bool kFew>
+cudaError_t launch_of(const ChunkParams &p, const Blocks &w, cudaStream_t stream) {
+    return p.c.int8 ? launch<D, kFew, true>(p, w, stream) : launch<D, kFew, false>(p, w, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_weigh(const ChunkParams &p, cudaStream_t stream) {
-    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
-    return p.c.int8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+    // Rows of a block: what the sequences have on the average, so that a decoding step's products are 32
+    // columns wide.
+    const long long mean = ((long long)p.total + p.B - 1) / p.B;
+    Blocks w;
+    w.tokens = (int)(mean < kTile / p.G ? (mean > 0 ? mean : 1) : kTile / p.G);
+    w.cols = (w.tokens * p.G + 31) & ~31;
+    if (p.c.D == 128) return w.cols <= 64 ? launch_of<128, true>(p, w, stream) : launch_of<128, false>(p, w, stream);
+    return w.cols <= 64 ? launch_of<64, true>(p, w, stream) : launch_of<64, false>(p, w, stream);
 }
 
 }  // namespace bsattn

@@ -20,7 +20,7 @@
 //   warp 2        fetches the codes of keys: bulk copies of 16 keys into raw tiles
 //   warp 3        query blocks (TMA) and their lse
 //   warps 4-7, 8-11   group 0, group 1: sums
-//   warps 12-15, 16-19   widen the codes of group 0's and group 1's tile (128-byte swizzle)
+//   warps 12-19   widen the codes (128-byte swizzle)
 // TMEM: S^T of group g and buffer i: [256 g + 128 i, 256 g + 128 i + 128).
 #include "kv_codes.cuh"
 #include "prefill_plan.cuh"
@@ -31,9 +31,9 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
-// 96 registers per thread at launch: 128 * 48 + 2 * 128 * 152 + 2 * 128 * 64 = 61440 = 640 * 96.
+// 96 registers per thread at launch, 61440 in all: 128 * 88 + 2 * 128 * 136 + 2 * 128 * 56 = 60416.
 constexpr int kLaunchRegs = 96;
-constexpr uint32_t kCtrlRegs = 48, kGroupRegs = 152, kWidenRegs = 64;
+constexpr uint32_t kCtrlRegs = 88, kGroupRegs = 136, kWidenRegs = 56;
 static_assert(128 * kCtrlRegs + 256 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 bf16: one 128-byte swizzle span
@@ -55,37 +55,37 @@ struct Unit {
     int32_t q0, q1;          // blocks that some of the keys are met by
 };
 
-// kFew: blocks of up to 64 rows, where HBM bounds the kernel: some 100 KB of codes on their way, one unit widened.  Else
-// the next unit is widened while the many blocks of one are worked on.
+// kFew: blocks of up to 64 rows, where HBM bounds the kernel: two units' codes on their way.  Else more blocks of
+// queries are.  Three tiles are widened at a time: the two of a unit, and the next one's first.
 template <int D, bool kFew>
 struct Cfg {
-    static constexpr int kStages = kFew ? 1 : 2, kRaws = kFew ? (D == 128 ? 3 : 6) : 1;
+    static constexpr int kTiles = 3, kBlocks = kFew ? 2 : 3, kRaws = kFew ? (D == 128 ? 2 : 4) : 1;
     static constexpr uint32_t kTileBytes = kTile * D * 2, kRawBytes = kTile * D;
     static constexpr uint32_t kBlockBytes = kFew ? kTileBytes / 2 : kTileBytes;
     static constexpr uint32_t kBlockSub = kFew ? kSub / 2 : kSub;    // 64 columns of a block
-    static constexpr uint32_t kQ = 0, kK = kQ + 2 * kBlockBytes;     // two blocks; [stages][2 groups]
-    static constexpr uint32_t kRaw = kK + kStages * 2 * kTileBytes;  // [raws][2 groups]
+    static constexpr uint32_t kQ = 0, kK = kQ + kBlocks * kBlockBytes;
+    static constexpr uint32_t kRaw = kK + kTiles * kTileBytes;       // [raws][2 groups]
     static constexpr uint32_t kScale = kRaw + kRaws * 2 * kRawBytes; // key scales of the raw tiles
-    static constexpr uint32_t kLse = kScale + kRaws * 1024;          // -lse log2(e) of the two blocks' rows
-    static constexpr uint32_t kOn = kLse + 2 * 512;                  // raw tiles' 16-key groups that are there
-    static constexpr uint32_t kOdd = kOn + 32;                       // keys that have a NaN code, of four units
+    static constexpr uint32_t kLse = kScale + kRaws * 1024;          // -lse log2(e) of the blocks' rows
+    static constexpr uint32_t kRow = kLse + kBlocks * 512;           // cache rows of the raw tiles' 16-key groups, -1: none
+    static constexpr uint32_t kOdd = kRow + kRaws * 64;              // keys that have a NaN code, of four units
     static constexpr uint32_t kUnit = kOdd + 4 * 32;
     static constexpr uint32_t kBar = kUnit + kUnits * (uint32_t)sizeof(Unit);
-    // K' full (2 stage + group) and empty (stage), query blocks full and empty, S full and empty (2 group + buffer), raw
-    // units full and empty, units full and empty
-    static constexpr int bKF = 0, bKE = 4, bQF = 6, bQE = 8, bSF = 10, bSE = 14, bRF = 18, bRE = 24, bUF = 30, bUE = bUF + kUnits,
-                         bDrain = bUE + kUnits, kNumBars = bDrain + 1;
-    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // tmem base, abort; see Start
-    static constexpr uint32_t kAlloc = kMisc + 64;
+    // K' tiles full and empty, query blocks full and empty, S full and empty (2 group + buffer), raw units full and
+    // empty, units full and empty
+    static constexpr int bKF = 0, bKE = bKF + kTiles, bQF = bKE + kTiles, bQE = bQF + kBlocks, bSF = bQE + kBlocks, bSE = bSF + 4,
+                         bRF = bSE + 4, bRE = bRF + kRaws, bUF = bRE + kRaws, bUE = bUF + kUnits, bDrain = bUE + kUnits,
+                         kNumBars = bDrain + 1;
+    static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
+    static constexpr uint32_t kAlloc = kMisc + 8;
     static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
 // Where the CTA's piece of the line begins.
 struct Start {
-    uint32_t tmem;
-    int32_t abort;
     int32_t b, h, u, pieces;
     long long begin, line;
+    Chunk c;                 // of sequence b
 };
 
 // Blocks that meet a key of j0 .. j1 (below n): a range.
@@ -112,15 +112,55 @@ __device__ __forceinline__ Range unit_blocks(const ChunkParams &p, const Blocks 
 
 __device__ __forceinline__ int unit_count(const Chunk &c) { return c.m > 0 ? (c.n + kUnitKeys - 1) / kUnitKeys : 0; }
 
+// Places of a unit in the line.  Of few blocks each counts, whether the unit's keys meet it or not.
+__device__ __forceinline__ bool plain_places(const Blocks &w, const Chunk &c) { return c.m <= 2 * w.tokens; }
+
+__device__ __forceinline__ int unit_places(const ChunkParams &p, const Blocks &w, const Chunk &c, int u) {
+    if (plain_places(w, c)) return kUnitCost + (c.m + w.tokens - 1) / w.tokens;
+    const Range r = unit_blocks(p, w, c, u);
+    return kUnitCost + r.q1 - r.q0;
+}
+
 // Places of one head's units of a sequence, by a warp: a lane counts every 32nd unit.
 __device__ __forceinline__ long long pass_places(const ChunkParams &p, const Blocks &w, const Chunk &c, int lane) {
+    if (plain_places(w, c)) return (long long)unit_count(c) * unit_places(p, w, c, 0);
     long long sum = 0;
-    for (int u = lane; u < unit_count(c); u += 32) {
-        const Range r = unit_blocks(p, w, c, u);
-        sum += kUnitCost + r.q1 - r.q0;
-    }
+    for (int u = lane; u < unit_count(c); u += 32) sum += unit_places(p, w, c, u);
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     return sum;
+}
+
+// The first unit of a sequence (st.c) that begins at or behind place `from`; the sequence begins at `begin`, each head
+// has `places`.  A whole warp; fills h, u, begin.
+__device__ __forceinline__ void first_unit(const ChunkParams &p, const Blocks &w, long long from, long long begin, long long places,
+                                           int lane, Start &st) {
+    const Chunk &c = st.c;
+    st.h = (int)((from - begin) / places);
+    st.begin = begin + st.h * places;
+    st.u = 0;
+    if (plain_places(w, c)) {
+        const int x = unit_places(p, w, c, 0);
+        st.u = min((int)((from - st.begin + x - 1) / x), unit_count(c));
+        st.begin += (long long)st.u * x;
+        return;
+    }
+    while (st.u < unit_count(c)) {
+        const long long x = st.u + lane < unit_count(c) ? unit_places(p, w, c, st.u + lane) : 0;
+        long long s = x;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, st.u + lane < unit_count(c) && st.begin + s - x >= from);
+        if (hit) {
+            const int k = __ffs(hit) - 1;
+            st.begin += __shfl_sync(0xffffffffu, s - x, k);
+            st.u += k;
+            return;
+        }
+        st.begin += __shfl_sync(0xffffffffu, s, 31);
+        st.u = min(st.u + 32, unit_count(c));
+    }
 }
 
 // Numbers the line and finds where the CTA's piece begins; all threads.
@@ -131,10 +171,21 @@ __device__ __forceinline__ void find_piece(const ChunkParams &p, const Blocks &w
     auto number = [&](int b0, bool check, long long before) -> long long {
         const int n = min(kSeqChunk, p.B - b0);
         __syncthreads();
-        for (int i = warp; i < n; i += kThreads / 32) {
-            const Chunk c = chunk_of(p, b0 + i, check && lane == 0);
-            const long long x = pass_places(p, w, c, lane);
-            if (lane == 0) pass[i] = x * p.c.H;
+        // a thread per sequence; a warp for those whose units differ
+        for (int i0 = warp * 32; i0 < n; i0 += kThreads) {
+            Chunk c = {};
+            if (i0 + lane < n) c = chunk_of(p, b0 + i0 + lane, check);
+            const bool plain = plain_places(w, c);
+            if (i0 + lane < n && plain) pass[i0 + lane] = (long long)unit_count(c) * unit_places(p, w, c, 0) * p.c.H;
+            for (uint32_t left = __ballot_sync(0xffffffffu, !plain); left; left &= left - 1) {
+                const int x = __ffs(left) - 1;
+                Chunk y;
+                y.first = __shfl_sync(0xffffffffu, c.first, x);
+                y.m = __shfl_sync(0xffffffffu, c.m, x);
+                y.n = __shfl_sync(0xffffffffu, c.n, x);
+                const long long places = pass_places(p, w, y, lane);
+                if (lane == 0) pass[i0 + x] = places * p.c.H;
+            }
         }
         __syncthreads();
         // a thread sums consecutive sequences
@@ -183,38 +234,70 @@ __device__ __forceinline__ void find_piece(const ChunkParams &p, const Blocks &w
                 const Chunk c = chunk_of(p, b0 + i, false);
                 const long long places = pass_places(p, w, c, lane);
                 if (places > 0) {
-                    const int h = (int)((from - pass[i]) / places);
-                    long long begin = pass[i] + h * places;
-                    // the first unit that begins at or behind `from`
-                    int u = 0;
-                    for (bool found = false; !found && u < unit_count(c);) {
-                        long long x = 0;
-                        if (u + lane < unit_count(c)) {
-                            const Range r = unit_blocks(p, w, c, u + lane);
-                            x = kUnitCost + r.q1 - r.q0;
-                        }
-                        long long s = x;
-                        for (int d = 1; d < 32; d <<= 1) {
-                            const long long y = __shfl_up_sync(0xffffffffu, s, d);
-                            if (lane >= d) s += y;
-                        }
-                        const uint32_t hit = __ballot_sync(0xffffffffu, u + lane < unit_count(c) && begin + s - x >= from);
-                        if (hit) {
-                            const int k = __ffs(hit) - 1;
-                            begin += __shfl_sync(0xffffffffu, s - x, k);
-                            u += k;
-                            found = true;
-                        } else {
-                            begin += __shfl_sync(0xffffffffu, s, 31);
-                            u = min(u + 32, unit_count(c));
-                        }
-                    }
-                    if (lane == 0) st->b = b0 + i, st->h = h, st->u = u, st->begin = begin;
+                    Start x = {};
+                    x.c = c;
+                    first_unit(p, w, from, pass[i], places, lane, x);
+                    if (lane == 0) st->b = b0 + i, st->h = x.h, st->u = x.u, st->begin = x.begin, st->c = c;
                 }
             }
         }
         at = end;
     }
+}
+
+// The same by one warp, without a barrier, of up to 32 kLaneSeqs sequences.
+constexpr int kLaneSeqs = 4;
+
+__device__ __forceinline__ Start find_piece_warp(const ChunkParams &p, const Blocks &w, int lane) {
+    Chunk c[kLaneSeqs];
+    long long pass[kLaneSeqs], before[kLaneSeqs], line = 0;
+#pragma unroll
+    for (int k = 0; k < kLaneSeqs; ++k) {
+        c[k] = Chunk{};
+        if (32 * k + lane < p.B) c[k] = chunk_of(p, 32 * k + lane, blockIdx.x == 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kLaneSeqs; ++k) {
+        if (32 * k >= p.B) break;
+        const bool plain = plain_places(w, c[k]);
+        pass[k] = plain ? (long long)unit_count(c[k]) * unit_places(p, w, c[k], 0) : 0;
+        for (uint32_t left = __ballot_sync(0xffffffffu, !plain); left; left &= left - 1) {
+            const int x = __ffs(left) - 1;
+            Chunk y;
+            y.first = __shfl_sync(0xffffffffu, c[k].first, x);
+            y.m = __shfl_sync(0xffffffffu, c[k].m, x);
+            y.n = __shfl_sync(0xffffffffu, c[k].n, x);
+            const long long places = pass_places(p, w, y, lane);
+            if (lane == x) pass[k] = places;
+        }
+        long long s = pass[k] * p.c.H;
+        const long long own = s;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        before[k] = line + s - own;
+        line += __shfl_sync(0xffffffffu, s, 31);
+    }
+    Start st = {};
+    st.line = line;
+    st.pieces = (int)max(1ll, min((long long)gridDim.x, line / kUnitCost));
+    st.b = p.B;
+    if ((int)blockIdx.x >= st.pieces) return st;
+    const long long from = line * (int)blockIdx.x / st.pieces;
+#pragma unroll
+    for (int k = 0; k < kLaneSeqs; ++k) {
+        if (32 * k >= p.B) break;
+        const uint32_t hit = __ballot_sync(0xffffffffu, from >= before[k] && from < before[k] + pass[k] * p.c.H);
+        if (!hit) continue;
+        const int x = __ffs(hit) - 1;
+        st.b = 32 * k + x;
+        st.c.first = __shfl_sync(0xffffffffu, c[k].first, x);
+        st.c.m = __shfl_sync(0xffffffffu, c[k].m, x);
+        st.c.n = __shfl_sync(0xffffffffu, c[k].n, x);
+        first_unit(p, w, from, __shfl_sync(0xffffffffu, before[k], x), __shfl_sync(0xffffffffu, pass[k], x), lane, st);
+    }
+    return st;
 }
 
 template <class C>
@@ -244,7 +327,7 @@ __device__ __forceinline__ void unit_role(const ChunkParams &p, const Blocks &w,
     if (b < p.B) {
         const long long to = st.line * ((long long)blockIdx.x + 1) / st.pieces;
         long long begin = st.begin;
-        Chunk c = chunk_of(p, b, false);
+        Chunk c = st.c;
         int units = unit_count(c);
         while (begin < to) {
             if (u >= units) {
@@ -265,7 +348,7 @@ __device__ __forceinline__ void unit_role(const ChunkParams &p, const Blocks &w,
                 x.first = c.first, x.m = c.m, x.q0 = r.q0, x.q1 = r.q1;
                 if (!emit(x)) return;
             }
-            begin += kUnitCost + r.q1 - r.q0;
+            begin += unit_places(p, w, c, u);
             ++u;
         }
     }
@@ -286,9 +369,8 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
     Unit x;
     while (next_unit<C>(wait, smem, units, x)) {
         const int j = x.key0 + key;
-        const long long row = j < x.n ? cache_row(p.c, p.table + (long long)x.b * p.table_stride, x.h, j) : -1;
+        int row = -1;
         float c = 0.f;
-        bool there = false;
         // tokens that meet the key: lo <= t < hi
         const int pos = x.n - x.m;
         int lo = 0, hi = 0;
@@ -297,13 +379,15 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
             const uint32_t raw = ut % C::kRaws;
             ok = __all_sync(0xffffffffu, wait(C::bRF + (int)raw, ut / C::kRaws));
             if (!ok) break;
-            const uint32_t on = reinterpret_cast<const uint32_t *>(smem + C::kOn)[raw];
-            there = j < x.n && ((on >> (key >> 4)) & 1u);
+            row = reinterpret_cast<const int *>(smem + C::kRow + raw * 64u)[key >> 4];
+            row = j < x.n && row >= 0 ? row + (key & 15) : -1;
             c = reinterpret_cast<const float *>(smem + C::kScale + raw * 1024u)[key] * p.scale_log2;
             __syncwarp();
             if (lane == 0) mbar_arrive(wait.bar(C::bRE + (int)raw));
+        } else if (j < x.n) {
+            row = (int)cache_row(p.c, p.table + (long long)x.b * p.table_stride, x.h, j);
         }
-        if (there) {
+        if (row >= 0) {
             hi = x.m;
             if (p.kind == BSATTN_MASK_CAUSAL || p.kind == BSATTN_MASK_SLIDING_WINDOW || (p.kind == BSATTN_MASK_PREFIX && j >= p.prefix_len))
                 lo = max(j - pos, 0);
@@ -312,17 +396,17 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
         }
         float sum = 0.f, lost = 0.f;             // compensated
         for (int q = x.q0; q < x.q1; ++q, ++it) {
-            const uint32_t buf = it & 1u;
-            ok = __all_sync(0xffffffffu, wait(C::bSF + 2 * g + (int)buf, it >> 1) && wait(C::bQF + (int)buf, it >> 1));
+            const uint32_t buf = it & 1u, blk = it % C::kBlocks;
+            ok = __all_sync(0xffffffffu, wait(C::bSF + 2 * g + (int)buf, it >> 1) && wait(C::bQF + (int)blk, it / C::kBlocks));
             if (!ok) break;
             tc_fence_after();
-            if (q == x.q0 && ((reinterpret_cast<const uint32_t *>(smem + C::kOdd)[8 * (ut & 3u) + 4 * g + quarter] >> lane) & 1u))
+            if (q == x.q0 && ((reinterpret_cast<const uint16_t *>(smem + C::kOdd)[16 * (ut & 3u) + 8 * g + 2 * quarter + (lane >> 4)] >> (lane & 15u)) & 1u))
                 c = __uint_as_float(0x7fc00000u);
             // of the block: columns that meet the key; of none behind the sequence's last token
             const int t0 = q * w.tokens, tokens = min(w.tokens, x.m - t0);
             const int from = min(max(lo - t0, 0), tokens) * p.G, to = min(max(hi - t0, 0), tokens) * p.G;
             const bool masked = __any_sync(0xffffffffu, from > 0 || to < w.tokens * p.G);
-            const float4 *nl = reinterpret_cast<const float4 *>(smem + C::kLse + buf * 512u);
+            const float4 *nl = reinterpret_cast<const float4 *>(smem + C::kLse + blk * 512u);
             const uint32_t at = s_addr + buf * 128u;
             float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
             auto chunk = [&](int cc, uint32_t (&v)[32]) {
@@ -364,7 +448,7 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(wait.bar(C::bSE + 2 * g + (int)buf));
-                mbar_arrive(wait.bar(C::bQE + (int)buf));
+                mbar_arrive(wait.bar(C::bQE + (int)blk));
             }
             const float add = ((a0 + b0) + (a1 + b1)) - lost, next = sum + add;
             lost = (next - sum) - add;
@@ -398,7 +482,8 @@ __device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &w
         if (x.q1 == x.q0) continue;              // no query meets them
         const uint32_t on = __ballot_sync(0xffffffffu, row >= 0), raw = it % C::kRaws;
         if (!(ok = __all_sync(0xffffffffu, wait(C::bRE + (int)raw, (it / C::kRaws) ^ 1u)))) break;
-        if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::kOn)[raw] = on;
+        if (lane < 16) reinterpret_cast<int *>(smem + C::kRow + raw * 64u)[lane] = (int)row;
+        __syncwarp();
         const uint32_t full = wait.bar(C::bRF + (int)raw), lead = row >= 0 ? 1u : 0u;
         mbar_arrive_expect_tx_lead(lane == 0 ? 1u : 0u, full, (uint32_t)__popc(on) * (16u * D + 64u));
         __syncwarp();
@@ -428,61 +513,69 @@ __device__ __forceinline__ uint32_t code_to_bf16x2(uint32_t x) {
     return r;
 }
 
-// Widens the codes of a group's tile (four warps, 32 keys each).  Lane: 16 codes of a row, two swizzle pieces; D / 16
+// Widens the codes of tiles, eight warps each, 16 keys a warp.  Lane: 16 codes of a row, two swizzle pieces; D / 16
 // lanes to a row.  What no copy has filled is left: such keys are masked.
 template <int D, bool kFew, bool kInt8>
-__device__ __forceinline__ void widen_role(const Waiter &wait, int g, int warp, int lane, uint8_t *smem) {
+__device__ __forceinline__ void widen_role(const Waiter &wait, int warp, int lane, uint8_t *smem) {
     using C = Cfg<D, kFew>;
-    constexpr int kRowLanes = D / 16, kAtOnce = 32 / kRowLanes, kSteps = 32 / kAtOnce;
+    constexpr int kRowLanes = D / 16, kAtOnce = 32 / kRowLanes, kSteps = 16 / kAtOnce;
     const int col = lane % kRowLanes, sub_row = lane / kRowLanes;
     // Eight lanes store 128 bytes at a time; where they share a row, half of them begin with their second
     // piece: every bank once.
     const bool swap = D == 128 && col >= 4;
     const int first = 2 * (col & 3) + (swap ? 1 : 0), second = first ^ 1;
-    const uint8_t *raw = smem + C::kRaw + (uint32_t)g * C::kRawBytes + (warp * 32 + sub_row) * D + col * 16;
-    uint8_t *dst = smem + C::kK + (uint32_t)g * C::kTileBytes + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 32 + sub_row) * 128u;
+    const uint8_t *raw = smem + C::kRaw + (warp * 16 + sub_row) * D + col * 16;
+    uint8_t *dst = smem + C::kK + (uint32_t)(col >> 2) * kSub + (uint32_t)(warp * 16 + sub_row) * 128u;
     uint32_t units = 0, it = 0;
     Unit x;
     while (next_unit<C>(wait, smem, units, x)) {
         if (x.q1 == x.q0) continue;
-        const uint32_t stage = it % C::kStages, rs = it % C::kRaws;
-        if (!__all_sync(0xffffffffu, wait(C::bKE + (int)stage, (it / C::kStages) ^ 1u) && wait(C::bRF + (int)rs, it / C::kRaws))) return;
-        const uint8_t *from = raw + rs * 2u * C::kRawBytes;
-        uint8_t *tile = dst + stage * 2u * C::kTileBytes;
-        uint32_t odd = 0;                        // rows that have a NaN code
-#pragma unroll 2
-        for (int i = 0; i < kSteps; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(from + i * kAtOnce * D);
-            const uint32_t y[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z, swap ? v.y : v.w};
-            const int r7 = (i * kAtOnce + sub_row) & 7;
-            if (!kInt8) {
-                uint32_t nan = 0;
+        const uint32_t rs = it % C::kRaws;
+        bool ok = wait(C::bRF + (int)rs, it / C::kRaws);
+#pragma unroll 1
+        for (uint32_t g = 0; g < 2; ++g) {
+            const uint32_t tile = 2 * it + g, stage = tile % C::kTiles;
+            const uint8_t *from = raw + (rs * 2u + g) * C::kRawBytes;
+            uint4 v[kSteps];
+            if (!__all_sync(0xffffffffu, ok)) return;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) nan |= (y[q] & 0x7f7f7f7fu) + 0x01010101u;
-                const uint32_t b = __ballot_sync(0xffffffffu, (nan & 0x80808080u) != 0u);
+            for (int i = 0; i < kSteps; ++i) v[i] = *reinterpret_cast<const uint4 *>(from + i * kAtOnce * D);
+            if (!__all_sync(0xffffffffu, wait(C::bKE + (int)stage, (tile / C::kTiles) ^ 1u))) return;
+            uint8_t *to = dst + stage * C::kTileBytes;
+            uint32_t odd = 0;                        // rows that have a NaN code
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q)
-                    if ((b >> (q * kRowLanes)) & ((1u << kRowLanes) - 1u)) odd |= 1u << (i * kAtOnce + q);
-            }
+            for (int i = 0; i < kSteps; ++i) {
+                const uint32_t y[4] = {swap ? v[i].z : v[i].x, swap ? v[i].w : v[i].y, swap ? v[i].x : v[i].z, swap ? v[i].y : v[i].w};
+                const int r7 = (i * kAtOnce + sub_row) & 7;
+                if (!kInt8) {
+                    uint32_t nan = 0;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t o[4];
+                    for (int q = 0; q < 4; ++q) nan |= (y[q] & 0x7f7f7f7fu) + 0x01010101u;
+                    const uint32_t b = __ballot_sync(0xffffffffu, (nan & 0x80808080u) != 0u);
+                    if (b) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    o[2 * k] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x1404));
-                    o[2 * k + 1] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x3424));
+                        for (int q = 0; q < kAtOnce; ++q)
+                            if ((b >> (q * kRowLanes)) & ((1u << kRowLanes) - 1u)) odd |= 1u << (i * kAtOnce + q);
+                    }
                 }
-                *reinterpret_cast<uint4 *>(tile + i * kAtOnce * 128 + (((q ? second : first) ^ r7) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        o[2 * k] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x1404));
+                        o[2 * k + 1] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x3424));
+                    }
+                    *reinterpret_cast<uint4 *>(to + i * kAtOnce * 128 + (((q ? second : first) ^ r7) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
+            if (lane == 0) reinterpret_cast<uint16_t *>(smem + C::kOdd)[16 * (it & 3u) + 8 * g + warp] = (uint16_t)odd;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wait.bar(C::bKF + (int)stage));
         }
-        if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::kOdd)[8 * (it & 3u) + 4 * g + warp] = odd;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(wait.bar(C::bKF + 2 * (int)stage + g));
-            mbar_arrive(wait.bar(C::bRE + (int)rs));
-        }
+        if (lane == 0) mbar_arrive(wait.bar(C::bRE + (int)rs));
         ++it;
     }
 }
@@ -497,20 +590,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0 && p.err) atomicOr(p.err, BSATTN_FLAG_TIMEOUT);
         return;
     }
-    Start *st = reinterpret_cast<Start *>(smem + C::kMisc);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    Start *st = reinterpret_cast<Start *>(smem + C::kLse);   // read before the first lse is written
     const uint32_t warp = warp_id(), lane = lane_id();
     Waiter wait;
     wait.bars = base + C::kBar;
-    wait.abort = &st->abort;
+    wait.abort = reinterpret_cast<volatile int *>(misc + 1);
     wait.err = p.err;
     if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kTiles; ++s) {
+            mbar_init(wait.bar(C::bKF + s), 8);      // one arrival per widening warp
+            mbar_init(wait.bar(C::bKE + s), 1);
+        }
         for (int s = 0; s < 4; ++s) {
-            mbar_init(wait.bar(C::bKF + s), 4);      // one arrival per widening warp
             mbar_init(wait.bar(C::bSF + s), 1);
             mbar_init(wait.bar(C::bSE + s), 4);      // one per warp of the group
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(wait.bar(C::bKE + s), 1);
+        for (int s = 0; s < C::kBlocks; ++s) {
             mbar_init(wait.bar(C::bQF + s), 1);
             mbar_init(wait.bar(C::bQE + s), 9);      // the products' completion, one per warp of the groups
         }
@@ -523,11 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(wait.bar(C::bUE + s), 19);     // issuing, fetching, query, group and widening warps
         }
         mbar_init(wait.bar(C::bDrain), 1);
-        st->abort = 0;
+        misc[1] = 0;
         fence_barrier_init();
     }
     // rows of a block that no copy fills stay 0
-    for (uint32_t i = threadIdx.x; i < 2 * C::kBlockBytes / 16; i += kThreads)
+    for (uint32_t i = threadIdx.x; i < C::kBlocks * C::kBlockBytes / 16; i += kThreads)
         reinterpret_cast<uint4 *>(smem + C::kQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (warp == 1) {
@@ -537,11 +633,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = st->tmem;
+    const uint32_t tmem = misc[0];
     grid_launch_dependents();
     grid_dependency_wait();
-    find_piece(p, w, st, reinterpret_cast<long long *>(smem + C::kK));
-    __syncthreads();
+    const bool alone = p.B <= 32 * kLaneSeqs;    // one warp numbers the line, while the others take their places
+    if (!alone) {
+        find_piece(p, w, st, reinterpret_cast<long long *>(smem + C::kK));
+        __syncthreads();
+    }
     if (warp == 0) {
         regs_release<kCtrlRegs>();
         // ---------------------------------------------------- MMA issuer --
@@ -551,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t desc_q = smem_desc_sw128(base + C::kQ, 16, 1024);
         const uint64_t desc_k = smem_desc_sw128(base + C::kK, 16, 1024);
         constexpr uint64_t kTileUnits = C::kTileBytes >> 4, kBlockUnits = C::kBlockBytes >> 4;
-        uint32_t units = 0, kt = 0, it = 0;
+        uint32_t units = 0, kt = 0, it = 0;      // units; tiles, blocks so far
         bool ok = true;
         auto ready = [&](int b, uint32_t phase) -> bool {
             ok = ok && wait(b, phase);
@@ -560,16 +659,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit x;
         while (ok && next_unit<C>(wait, smem, units, x)) {
             if (x.q1 == x.q0) continue;
-            const uint32_t stage = kt % C::kStages;
             for (int q = x.q0; ok && q < x.q1; ++q, ++it) {
-                const uint32_t buf = it & 1u;
-                if (!ready(C::bQF + (int)buf, it >> 1)) break;
+                const uint32_t buf = it & 1u, blk = it % C::kBlocks;
+                if (!ready(C::bQF + (int)blk, it / C::kBlocks)) break;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    if (q == x.q0 && !ready(C::bKF + 2 * (int)stage + g, kt / C::kStages)) break;
+                    const uint32_t tile = kt + (uint32_t)g, stage = tile % C::kTiles;
+                    if (q == x.q0 && !ready(C::bKF + (int)stage, tile / C::kTiles)) break;
                     if (!ready(C::bSE + 2 * g + (int)buf, (it >> 1) ^ 1u)) break;
                     tc_fence_after();
-                    const uint64_t kd = desc_k + (uint64_t)(2 * stage + g) * kTileUnits, qd = desc_q + (uint64_t)buf * kBlockUnits;
+                    const uint64_t kd = desc_k + (uint64_t)stage * kTileUnits, qd = desc_q + (uint64_t)blk * kBlockUnits;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t in = (uint64_t)((kk & 3) * 2);
@@ -577,20 +676,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     qd + (uint64_t)(kk >> 2) * (C::kBlockSub >> 4) + in, idesc, kk > 0 ? 1u : 0u);
                     }
                     mma_commit_lead(lead, wait.bar(C::bSF + 2 * g + (int)buf));
+                    if (q == x.q1 - 1) mma_commit_lead(lead, wait.bar(C::bKE + (int)stage));
                 }
                 if (!ok) break;
-                mma_commit_lead(lead, wait.bar(C::bQE + (int)buf));
+                mma_commit_lead(lead, wait.bar(C::bQE + (int)blk));
             }
-            if (!ok) break;
-            mma_commit_lead(lead, wait.bar(C::bKE + (int)stage));
-            ++kt;
+            kt += 2;
         }
         // Wait until every tcgen05 operation issued above has completed.
         mma_commit_lead(lead, wait.bar(C::bDrain));
         mbar_wait_drain(wait.bar(C::bDrain), 0);
     } else if (warp == 1) {
         regs_release<kCtrlRegs>();
-        if (lane == 0) unit_role<C>(p, w, wait, smem, *st);
+        const Start from = alone ? find_piece_warp(p, w, (int)lane) : *st;
+        if (lane == 0) unit_role<C>(p, w, wait, smem, from);
         __syncwarp();
     } else if (warp == 2) {
         regs_release<kCtrlRegs>();
@@ -602,38 +701,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = (uint32_t)(p.G * w.tokens) * D * 2u;
         uint32_t units = 0, it = 0;
         bool ok = true;
-        Unit x;
-        while (ok && next_unit<C>(wait, smem, units, x)) {
-            for (int q = x.q0; q < x.q1; ++q, ++it) {
-                const uint32_t buf = it & 1u;
-                const int t0 = q * w.tokens, rows = min(w.tokens, x.m - t0) * p.G;
-                float nl[4];
+        // lse of the lane's four rows of a block, loaded while the block before waits for its place
+        int at[4], tok[4];
+        float nl[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 32 * i + (int)lane, tok = r / p.G;
-                    nl[i] = r < rows ? __ldg(p.lse + (long long)(x.first + t0 + tok) * p.Hq + x.h * p.G + r - tok * p.G) : INFINITY;
-                }
-                if (!(ok = __all_sync(0xffffffffu, wait(C::bQE + (int)buf, (it >> 1) ^ 1u)))) break;
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + (int)lane;
+            tok[i] = r / p.G;
+            at[i] = tok[i] * p.Hq + r - tok[i] * p.G;
+        }
+        Unit x = {};
+        auto load = [&](int q) {
+            const float *lse = p.lse + (long long)(x.first + q * w.tokens) * p.Hq + x.h * p.G;
+            const int tokens = min(w.tokens, x.m - q * w.tokens);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nl[i] = tok[i] < tokens ? __ldg(lse + at[i]) : INFINITY;
+        };
+        while (ok && next_unit<C>(wait, smem, units, x)) {
+            if (x.q0 < x.q1) load(x.q0);
+            for (int q = x.q0; q < x.q1; ++q, ++it) {
+                const uint32_t blk = it % C::kBlocks;
+                if (!(ok = __all_sync(0xffffffffu, wait(C::bQE + (int)blk, (it / C::kBlocks) ^ 1u)))) break;
+                const uint32_t full = wait.bar(C::bQF + (int)blk), lead = lane == 0 ? 1u : 0u;
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d_lead(lead, base + C::kQ + blk * C::kBlockBytes + c * C::kBlockSub, &tq, full, c * 64, x.h * p.G,
+                                     x.first + q * w.tokens);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)     // -inf: a query without keys
-                    reinterpret_cast<float *>(smem + C::kLse + buf * 512u)[32 * i + lane] = nl[i] == -INFINITY ? -INFINITY : nl[i] * -1.44269504088896340736f;
+                    reinterpret_cast<float *>(smem + C::kLse + blk * 512u)[32 * i + lane] = nl[i] == -INFINITY ? -INFINITY : nl[i] * -1.44269504088896340736f;
                 __syncwarp();
-                const uint32_t full = wait.bar(C::bQF + (int)buf), lead = lane == 0 ? 1u : 0u;
                 mbar_arrive_expect_tx_lead(lead, full, bytes);
-                __syncwarp();
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d_lead(lead, base + C::kQ + buf * C::kBlockBytes + c * C::kBlockSub, &tq, full, c * 64, x.h * p.G, x.first + t0);
+                if (q + 1 < x.q1) load(q + 1);
             }
         }
         // nothing may be on its way into shared memory when the CTA ends
-        for (uint32_t s = 0; s < 2; ++s)
-            if (it > s) mbar_wait_drain(wait.bar(C::bQF + (int)s), ((it - 1 - s) >> 1) & 1u);
+        for (uint32_t s = 0; s < (uint32_t)C::kBlocks; ++s)
+            if (it > s) mbar_wait_drain(wait.bar(C::bQF + (int)s), ((it - 1 - s) / C::kBlocks) & 1u);
     } else if (warp < 12) {
         regs_claim<kGroupRegs>();
         group_role<D, kFew>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
     } else {
         regs_release<kWidenRegs>();
-        widen_role<D, kFew, kInt8>(wait, warp >= 16 ? 1 : 0, (int)(warp & 3u), (int)lane, smem);
+        widen_role<D, kFew, kInt8>(wait, (int)warp - 12, (int)lane, smem);
     }
     tc_fence_before();
     __syncthreads();

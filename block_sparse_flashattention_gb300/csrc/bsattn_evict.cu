@@ -3,14 +3,15 @@
 // (equal weights: the lower positions).  What stays is moved, in order, to the places 0, 1, ... of
 // the sequence's row of out_table.
 //
-// Two kernels.  bsattn_evict_select_kernel, a CTA per (sequence, head), finds the weight w* of
-// the last key that stays by a radix selection (weights as ordered 32-bit integers, four digits of
-// 8 bits, the highest first, a histogram of the digit among the keys that agree so far), then
-// writes the positions of all keys above w* and of the first ones equal to it: every warp
-// counts its piece of the positions, a scan over the warps gives each its place in the list.
-// bsattn_evict_move_kernel moves rows.  To other pages every row is independent; within
-// its own pages row i comes from position kept[i] >= i, so one CTA per (sequence, head)
-// goes through the rows in ascending blocks, each read whole before it is written.
+// Two kernels.  bsattn_evict_select_kernel, a cluster of 1 to 8 CTAs per (sequence, head), finds the weight w* of
+// the last key that stays by a radix selection: weights as ordered 32-bit integers, three digits of 11, 11 and
+// 10 bits, the highest first, a histogram of the digit among the keys that agree so far.  Each CTA reads its
+// piece of the positions once and keeps it in shared memory; histograms are summed through distributed shared
+// memory.  Then the positions of all keys above w* and of the first ones equal to it are written: every warp counts its
+// piece, and the counts before it, of the CTA's warps and of the CTAs before, give it its place in the list.
+// bsattn_evict_move_kernel moves rows.  To other pages every row is independent; within its own pages row i comes
+// from position kept[i] >= i, so one CTA per (sequence, head) goes through the rows in ascending blocks, each read
+// whole before it is written.
 #include "bsattn_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -18,8 +19,9 @@ namespace bsattn {
 
 namespace {
 
-constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
-constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32, kBins = 2048;
+constexpr int kMostKeys = 40960;             // of a CTA that shared memory holds; more are read again for every digit
+constexpr int kMoveThreads = 256;
 constexpr uint32_t kForced = 0xffffffffu;
 
 // Weights as integers in the same order: NaN above all, -0 equal to 0.  kForced is none of them
@@ -51,87 +53,162 @@ __device__ __forceinline__ long long row_at(const CacheView &c, const int32_t *t
     return (((long long)page * c.H + h) << c.page_shift) + (j & ((1 << c.page_shift) - 1));
 }
 
-__global__ void __launch_bounds__(kSelectThreads) bsattn_evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ uint32_t hist[256], s_digit, s_left;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A word of another CTA of the cluster.
+__device__ __forceinline__ uint32_t peer_word(const uint32_t *mine, uint32_t rank) {
+    uint32_t at, x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+
+__device__ __forceinline__ uint4 peer_words(const uint32_t *mine, uint32_t rank) {
+    uint32_t at;
+    uint4 x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+    return x;
+}
+
+// ranks: CTAs of a cluster; room: keys that `keys` holds.
+__global__ void __launch_bounds__(kSelectThreads, 3) bsattn_evict_select_kernel(const __grid_constant__ EvictParams p, int ranks, int room) {
+    extern __shared__ uint32_t keys[];
+    __shared__ __align__(16) uint32_t hist[2][kBins];
+    __shared__ uint32_t s_digit, s_left, s_warps[kSelectWarps], s_count[2];
     __shared__ int above[kSelectWarps], equal[kSelectWarps];
-    const int b = blockIdx.x / p.c.H, h = blockIdx.x - b * p.c.H, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const Evicted s = sequence(p, b, h == 0 && tid == 0);
-    if (h == 0 && tid == 0) p.lens[b] = s.m;
+    const int rank = (int)blockIdx.x % ranks, seg = (int)blockIdx.x / ranks;
+    const int b = seg / p.c.H, h = seg - b * p.c.H, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const Evicted s = sequence(p, b, h == 0 && rank == 0 && tid == 0);
+    if (h == 0 && rank == 0 && tid == 0) p.lens[b] = s.m;
     const int32_t *table = p.table + (long long)b * p.table_stride;
     int32_t *kept = p.kept + ((long long)b * p.c.H + h) * p.keep;
-    for (int i = s.m + tid; i < p.keep; i += kSelectThreads) kept[i] = -1;
+    const int all = rank * kSelectThreads + tid, step = ranks * kSelectThreads;
+    for (int i = s.m + all; i < p.keep; i += step) kept[i] = -1;
     if (s.n <= p.keep) {
-        for (int i = tid; i < s.m; i += kSelectThreads) kept[i] = i;
+        for (int i = all; i < s.m; i += step) kept[i] = i;
         return;
     }
-    auto key = [&](int j) -> uint32_t {
-        if (j < p.sinks || j >= s.n - p.recent) return kForced;
+    // the CTA's positions first .. first + n - 1
+    const int per = ((s.n + ranks - 1) / ranks + 31) & ~31;
+    const int first = (int)min((long long)rank * per, (long long)s.n), n = min(per, s.n - first);
+    auto kept_anyway = [&](int j) -> bool { return j < p.sinks || j >= s.n - p.recent; };
+    auto load = [&](int i) -> uint32_t {
+        const int j = first + i;
+        if (kept_anyway(j)) return kForced;
         const long long row = row_at(p.c, table, h, j);
         return row < 0 ? 0u : ordered(p.weights[row]);
     };
-    // the digits of w*: `left` keys are still to be found among those that agree with `prefix`
-    uint32_t prefix = 0, left = (uint32_t)p.keep;
+    const int held = min(n, room);
+    for (int i0 = tid; i0 < held; i0 += 8 * kSelectThreads) {
+        long long row[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) row[k] = i0 + k * kSelectThreads < held ? row_at(p.c, table, h, first + i0 + k * kSelectThreads) : -1;
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = row[k] >= 0 ? __ldg(p.weights + row[k]) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kSelectThreads;
+            if (i < held) keys[i] = kept_anyway(first + i) ? kForced : row[k] < 0 ? 0u : ordered(x[k]);
+        }
+    }
+    auto key = [&](int i) -> uint32_t { return i < held ? keys[i] : load(i); };
+    for (int i = tid; i < kBins; i += kSelectThreads) hist[0][i] = 0;
+    __syncthreads();
+    // the digits of w*: `left` keys are still to be found among those that agree with it so far
+    uint32_t star = 0, left = (uint32_t)p.keep;
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        uint32_t *mine = hist[pass & 1];
+#pragma unroll 4
+        for (int i = tid; i < n; i += kSelectThreads) {
+            const uint32_t k = key(i);
+            if (pass == 0 || ((k ^ star) >> (shift + bits)) == 0u) atomicAdd(&mine[(k >> shift) & ((1u << bits) - 1u)], 1u);
+        }
+        if (ranks > 1) cluster_sync();
+        else __syncthreads();
+        // a thread: four digits, the highest first; `more`: keys of larger ones
+        constexpr int kOwn = 4;
+        static_assert(kOwn * kSelectThreads == kBins, "digits of a thread");
+        const int top = kBins - kOwn * (tid + 1);
+        uint4 x[8];
+        x[0] = *reinterpret_cast<const uint4 *>(mine + top);
+        if (ranks > 1) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x[r] = r < ranks ? peer_words(mine + top, (uint32_t)r) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 1; r < 8; ++r) x[0].x += x[r].x, x[0].y += x[r].y, x[0].z += x[r].z, x[0].w += x[r].w;
+        }
+        const uint32_t c[kOwn] = {x[0].w, x[0].z, x[0].y, x[0].x}, sum = (c[0] + c[1]) + (c[2] + c[3]);
+        uint32_t more = sum;
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, more, d);
+            if (lane >= d) more += y;
+        }
+        if (lane == 31) s_warps[warp] = more;
+        // the other histogram, read in the pass before the last barrier, is free
+        for (int i = tid; i < kBins; i += kSelectThreads) hist[(pass & 1) ^ 1][i] = 0;
         __syncthreads();
-        for (int j = tid; j < s.n; j += kSelectThreads) {
-            const uint32_t k = key(j);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        more -= sum;
+        for (int w = 0; w < warp; ++w) more += s_warps[w];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (more < left && left <= more + c[i]) {
+                s_digit = (uint32_t)(kBins - 1 - kOwn * tid - i);
+                s_left = left - more;
+            }
+            more += c[i];
         }
         __syncthreads();
-        if (warp == 0) {
-            // lane: 8 digits, the highest first; `more`: keys of larger digits
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
-            uint32_t more = sum;
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, more, d);
-                if (lane >= d) more += x;
-            }
-            more -= sum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (more < left && left <= more + c[i]) {
-                    s_digit = 255u - 8u * lane - i;
-                    s_left = left - more;
-                }
-                more += c[i];
-            }
-        }
-        __syncthreads();
-        prefix |= s_digit << shift;
+        star |= s_digit << shift;
         left = s_left;
         __syncthreads();
     }
     // warps' pieces of the positions
-    const int per = ((s.n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
-    const int lo = min(s.n, warp * per), hi = min(s.n, lo + per);
+    const int piece = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+    const int lo = min(n, warp * piece), hi = min(n, lo + piece);
     int na = 0, ne = 0;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const uint32_t k = j0 + lane < hi ? key(j0 + lane) : 0u;
-        const bool in = j0 + lane < hi;
-        na += __popc(__ballot_sync(0xffffffffu, in && k > prefix));
-        ne += __popc(__ballot_sync(0xffffffffu, in && k == prefix));
+#pragma unroll 4
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const bool in = i0 + lane < hi;
+        const uint32_t k = in ? key(i0 + lane) : 0u;
+        na += __popc(__ballot_sync(0xffffffffu, in && k > star));
+        ne += __popc(__ballot_sync(0xffffffffu, in && k == star));
     }
     if (lane == 0) above[warp] = na, equal[warp] = ne;
     __syncthreads();
-    int out = 0, before = 0;   // places taken, equal keys, both before this warp's piece
-    for (int w = 0; w < warp; ++w) {
-        out += above[w] + min(equal[w], max((int)left - before, 0));
-        before += equal[w];
+    if (tid == 0) {
+        uint32_t a = 0, e = 0;
+        for (int w = 0; w < kSelectWarps; ++w) a += (uint32_t)above[w], e += (uint32_t)equal[w];
+        s_count[0] = a, s_count[1] = e;
     }
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const bool in = j0 + lane < hi;
-        const uint32_t k = in ? key(j0 + lane) : 0u;
-        const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix), below = (1u << lane) - 1u;
-        const bool stays = in && (k > prefix || (k == prefix && before + __popc(eq & below) < (int)left));
+    if (ranks > 1) cluster_sync();
+    // keys above w*, equal ones, before this warp's piece; the first `left` equal ones stay
+    int out = 0, before = 0;
+    for (int r = 0; r < rank; ++r) {
+        out += (int)peer_word(&s_count[0], (uint32_t)r);
+        before += (int)peer_word(&s_count[1], (uint32_t)r);
+    }
+    for (int w = 0; w < warp; ++w) out += above[w], before += equal[w];
+    out += min(before, (int)left);
+#pragma unroll 4
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const bool in = i0 + lane < hi;
+        const uint32_t k = in ? key(i0 + lane) : 0u;
+        const uint32_t eq = __ballot_sync(0xffffffffu, in && k == star), below = (1u << lane) - 1u;
+        const bool stays = in && (k > star || (k == star && before + __popc(eq & below) < (int)left));
         const uint32_t st = __ballot_sync(0xffffffffu, stays);
-        if (stays) kept[out + __popc(st & below)] = j0 + lane;
+        if (stays) kept[out + __popc(st & below)] = first + i0 + lane;
         out += __popc(st);
         before += __popc(eq);
     }
+    if (ranks > 1) cluster_sync();   // no CTA ends while another reads its counts
 }
 
 // One row: codes of K and V (16 bytes a lane), scales and weight.  D / 16 lanes to a row.
@@ -162,10 +239,12 @@ template <int D, bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads) bsattn_evict_move_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kLanes = D / 16, kRows = kMoveThreads / kLanes;
     const int b = blockIdx.x / p.c.H, h = blockIdx.x - b * p.c.H, tid = threadIdx.x;
-    const Evicted s = sequence(p, b, false);
     const int32_t *table = p.table + (long long)b * p.table_stride, *out = p.out_table + (long long)b * p.out_stride;
     const int32_t *kept = p.kept + ((long long)b * p.c.H + h) * p.keep;
     const int piece = tid % kLanes;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const Evicted s = sequence(p, b, false);
     for (int i0 = blockIdx.y * kRows; i0 < s.m; i0 += gridDim.y * kRows) {
         const int i = i0 + tid / kLanes;
         const int from = i < s.m ? kept[i] : -1;
@@ -188,24 +267,62 @@ __global__ void __launch_bounds__(kMoveThreads) bsattn_evict_move_kernel(const _
         }
 }
 
+cudaError_t launch_ex(const void *kernel, dim3 grid, int threads, size_t smem, int cluster, void **args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.stream = stream;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
 template <int D>
-void launch_move(const EvictParams &p, cudaStream_t stream) {
+cudaError_t launch_move(const EvictParams &p, cudaStream_t stream) {
     constexpr int kRows = kMoveThreads / (D / 16);
+    void *args[] = {const_cast<EvictParams *>(&p)};
+    const unsigned segs = (unsigned)(p.B * p.c.H);
     if (p.table == p.out_table)
-        bsattn_evict_move_kernel<D, true><<<p.B * p.c.H, kMoveThreads, 0, stream>>>(p);
-    else
-        bsattn_evict_move_kernel<D, false><<<dim3(p.B * p.c.H, min((p.keep + kRows - 1) / kRows, 1024)), kMoveThreads, 0, stream>>>(p);
+        return launch_ex(reinterpret_cast<const void *>(bsattn_evict_move_kernel<D, true>), dim3(segs), kMoveThreads, 0, 1, args, stream);
+    const long long room = min((long long)p.keep, (long long)p.table_cols << p.c.page_shift);
+    const unsigned blocks = (unsigned)min((room + kRows - 1) / kRows, 1024ll);
+    return launch_ex(reinterpret_cast<const void *>(bsattn_evict_move_kernel<D, false>), dim3(segs, blocks), kMoveThreads, 0, 1, args, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream) {
-    bsattn_evict_select_kernel<<<p.B * p.c.H, kSelectThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    static int attr_set_for_device[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (p.c.D == 128) launch_move<128>(p, stream);
-    else launch_move<64>(p, stream);
-    return cudaGetLastError();
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set_for_device[dev]) {
+        e = cudaFuncSetAttribute(bsattn_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
+        if (e != cudaSuccess) return e;
+        attr_set_for_device[dev] = 1;
+    }
+    const int sms = current_device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // Clusters while they fill no more than two CTAs per SM and leave each CTA some thousand of the keys that
+    // the table has room for.
+    const long long segs = (long long)p.B * p.c.H, most = (long long)p.table_cols << p.c.page_shift;
+    int ranks = 1;
+    while (ranks < 8 && segs * ranks <= sms && most / ranks > 4096) ranks *= 2;
+    int room = (int)min((most + ranks - 1) / ranks + 32, (long long)kMostKeys);
+    void *args[] = {const_cast<EvictParams *>(&p), &ranks, &room};
+    if (segs * ranks > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_ex(reinterpret_cast<const void *>(bsattn_evict_select_kernel), dim3((unsigned)(segs * ranks)), kSelectThreads,
+                  (size_t)room * 4, ranks, args, stream);
+    if (e != cudaSuccess) return e;
+    return p.c.D == 128 ? launch_move<128>(p, stream) : launch_move<64>(p, stream);
 }
 
 }  // namespace bsattn

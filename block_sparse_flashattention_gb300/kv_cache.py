@@ -56,7 +56,8 @@ def _bind() -> None:
         from . import _torch_calls as calls
         if calls.torch_version() == t.__version__.split("+")[0]:
             calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                _lib.bsattn_kv_append, _lib.bsattn_kv_read, _lib.bsattn_decode, _lib.bsattn_decode_shared_prefix)))
+                _lib.bsattn_kv_append, _lib.bsattn_kv_read, _lib.bsattn_decode, _lib.bsattn_decode_shared_prefix,
+                _lib.bsattn_prefill, _lib.bsattn_kv_weigh, _lib.bsattn_kv_evict)))
             _calls = calls
         else:
             warnings.warn(f"the native cache calls were compiled for torch {calls.torch_version()}, not {t.__version__}: "
@@ -462,6 +463,14 @@ def prefill(q, cache: KVCache, page_table, seqlens, cu_seqlens, *, keys=None, ki
     Returns (out [total, Hq, D] bf16 or out_dtype, lse fp32 [total, Hq]); a query without keys gets
     0 and -inf, rows outside every sequence are not written.  workspace: see
     alloc_prefill_workspace; None allocates one for this call."""
+    if _calls is not None and workspace is not None and keys is not None and stream is None and out is None and \
+            lse is None and out_dtype is None and err_flag is None:
+        got = _calls.prefill(cache.at, cache.index, q, page_table, seqlens, cu_seqlens, keys, kind, mask_params,
+                             cache.scale if softmax_scale is None else softmax_scale, workspace)
+        if got is not None:
+            if got.__class__ is tuple:
+                return got
+            raise BsattnError(got, "bsattn_prefill")
     if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
         return _elsewhere(cache, stream, lambda: prefill(
             q, cache, page_table, seqlens, cu_seqlens, keys=keys, kind=kind, mask_params=mask_params,
@@ -512,6 +521,13 @@ def kv_weigh(q, lse, cache: KVCache, weights, page_table, seqlens, *, cu_seqlens
     (a single newest token meets every key under MASK_CAUSAL).  accumulate False: the weights of the
     sequences' keys are set instead, to 0 where no query meets a key.  A page's weights are the
     caller's to set to 0 when it is handed out."""
+    if _calls is not None and stream is None and err_flag is None:
+        status = _calls.kv_weigh(cache.at, cache.index, q, lse, weights, page_table, seqlens, cu_seqlens, accumulate,
+                                 kind, mask_params, cache.scale if softmax_scale is None else softmax_scale)
+        if status is not None:
+            if status:
+                raise BsattnError(status, "bsattn_kv_weigh")
+            return weights
     if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
         return _elsewhere(cache, stream, lambda: kv_weigh(
             q, lse, cache, weights, page_table, seqlens, cu_seqlens=cu_seqlens, accumulate=accumulate, kind=kind,
@@ -545,6 +561,12 @@ def kv_evict(cache: KVCache, weights, page_table, seqlens, keep: int, *, recent:
     other pages, for every sequence, short ones whole; page_table's pages are only read, so that
     several sequences may share them.  Returns (kept int32 [B, H, keep]: the positions that stay, -1
     behind the last; lens int32 [B]: the keys that the sequences have now)."""
+    if _calls is not None and stream is None and err_flag is None:
+        got = _calls.kv_evict(cache.at, cache.index, weights, page_table, seqlens, keep, recent, sinks, out_table)
+        if got is not None:
+            if got.__class__ is tuple:
+                return got
+            raise BsattnError(got, "bsattn_kv_evict")
     if stream is not None or (cache.index >= 0 and cache.index != _current_device()):
         return _elsewhere(cache, stream, lambda: kv_evict(cache, weights, page_table, seqlens, keep, recent=recent,
                                                           sinks=sinks, out_table=out_table, err_flag=err_flag))

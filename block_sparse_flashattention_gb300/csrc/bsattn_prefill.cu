@@ -713,59 +713,64 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- join --
 
-// Block (x, y): kJoinRows rows of the segment that begins in piece x and ends in a later one, a warp each.
+// Block (x, y): kJoinRows rows of the segment that begins in piece x (x + gridDim.x, ..) and ends in a later one, a
+// warp each.
 template <int D>
 __global__ void __launch_bounds__(kJoinRows * 32) bsattn_prefill_join_kernel(const __grid_constant__ ChunkParams p,
                                                                              const __grid_constant__ Layout w) {
     grid_launch_dependents();
-    const int r = blockIdx.y * kJoinRows + (int)(threadIdx.x / 32), lane = (int)(threadIdx.x % 32), piece = blockIdx.x;
+    const int r = blockIdx.y * kJoinRows + (int)(threadIdx.x / 32), lane = (int)(threadIdx.x % 32);
     const int t = r / kTile, row = r % kTile, token_of = row / p.G, tok = t * w.tokens + token_of;
     grid_dependency_wait();
-    const CutInfo cut = reinterpret_cast<const CutInfo *>(p.ws + w.cuts)[piece];
-    if (cut.parts == 0 || token_of >= w.tokens || tok >= cut.tokens) return;
+    if (token_of >= w.tokens) return;
+    const int pieces = w.few ? w.pieces : reinterpret_cast<const PlanTotals *>(p.ws + w.totals)->pieces;
     const float *part_l = reinterpret_cast<const float *>(p.ws + w.part_l);
     const float *part_o = reinterpret_cast<const float *>(p.ws + w.part_o);
-    auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
-    float m = -INFINITY, sum = 0.f, o[D / 32] = {};
-    for (int x0 = 0; x0 < cut.parts; x0 += 32) {
-        const float l = x0 + lane < cut.parts ? part_l[at(x0 + lane)] : -INFINITY;
-        float top = l;
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float m_new = fmaxf(m, top);
-        const float f = l == -INFINITY ? 0.f : ex2_approx(l - m_new), drop = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-        m = m_new;
-        sum *= drop;
+    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+        const CutInfo cut = reinterpret_cast<const CutInfo *>(p.ws + w.cuts)[piece];
+        if (cut.parts == 0 || tok >= cut.tokens) continue;
+        auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
+        float m = -INFINITY, sum = 0.f, o[D / 32] = {};
+        for (int x0 = 0; x0 < cut.parts; x0 += 32) {
+            const float l = x0 + lane < cut.parts ? part_l[at(x0 + lane)] : -INFINITY;
+            float top = l;
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float m_new = fmaxf(m, top);
+            const float f = l == -INFINITY ? 0.f : ex2_approx(l - m_new), drop = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+            m = m_new;
+            sum *= drop;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) o[c] *= drop;
-        const int n = min(32, cut.parts - x0);
+            for (int c = 0; c < D / 32; ++c) o[c] *= drop;
+            const int n = min(32, cut.parts - x0);
 #pragma unroll 4
-        for (int x = 0; x < n; ++x) {
-            const float fx = __shfl_sync(0xffffffffu, f, x);
-            if (fx == 0.f) continue;             // no key, or next to nothing
-            const float *y = part_o + at(x0 + x) * D + lane * (D / 32);
-            sum += fx;
-            if constexpr (D == 128) {
-                const float4 v = *reinterpret_cast<const float4 *>(y);
-                o[0] += fx * v.x, o[1] += fx * v.y, o[2] += fx * v.z, o[3] += fx * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(y);
-                o[0] += fx * v.x, o[1] += fx * v.y;
+            for (int x = 0; x < n; ++x) {
+                const float fx = __shfl_sync(0xffffffffu, f, x);
+                if (fx == 0.f) continue;             // no key, or next to nothing
+                const float *y = part_o + at(x0 + x) * D + lane * (D / 32);
+                sum += fx;
+                if constexpr (D == 128) {
+                    const float4 v = *reinterpret_cast<const float4 *>(y);
+                    o[0] += fx * v.x, o[1] += fx * v.y, o[2] += fx * v.z, o[3] += fx * v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(y);
+                    o[0] += fx * v.x, o[1] += fx * v.y;
+                }
             }
         }
-    }
-    const bool empty = sum == 0.f;
-    const float inv = empty ? 0.f : 1.f / sum;
-    const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
-    if (p.out_f32) {
-        float *dst = static_cast<float *>(p.out) + out * D + lane * (D / 32);
+        const bool empty = sum == 0.f;
+        const float inv = empty ? 0.f : 1.f / sum;
+        const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
+        if (p.out_f32) {
+            float *dst = static_cast<float *>(p.out) + out * D + lane * (D / 32);
 #pragma unroll
-        for (int c = 0; c < D / 32; c += 2) reinterpret_cast<float2 *>(dst)[c / 2] = make_float2(o[c] * inv, o[c + 1] * inv);
-    } else {
-        uint32_t *dst = static_cast<uint32_t *>(p.out) + (out * D + lane * (D / 32)) / 2;
+            for (int c = 0; c < D / 32; c += 2) reinterpret_cast<float2 *>(dst)[c / 2] = make_float2(o[c] * inv, o[c + 1] * inv);
+        } else {
+            uint32_t *dst = static_cast<uint32_t *>(p.out) + (out * D + lane * (D / 32)) / 2;
 #pragma unroll
-        for (int c = 0; c < D / 32; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+            for (int c = 0; c < D / 32; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+        }
+        if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
     }
-    if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
 }
 
 template <int D>
@@ -808,7 +813,7 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_kernel<D>), dim3((unsigned)w.ctas), kThreads, C::kAlloc, args, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinRows * 32, 0, args, stream);
+    return launch_dependent(join, dim3((unsigned)(2 * w.ctas), join_rows), kJoinRows * 32, 0, args, stream);
 }
 
 }  // namespace

@@ -46,8 +46,7 @@ constexpr uint32_t kCtrlRegs = 120, kSoftmaxRegs = 192;
 static_assert(128 * kCtrlRegs + 2 * 128 * kSoftmaxRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 elements: one 128-byte swizzle span
-constexpr int kPlanThreads = 1024, kWidenThreads = 256;
-constexpr int kJoinRows = 8;                // rows of a part that a block of the join takes
+constexpr int kPlanThreads = 1024, kWidenThreads = 256, kJoinThreads = 256;
 
 // Binary exponents (biased) that go into K' (what lies outside stays in r), and those that E is taken from
 // (2^(E - 6) and its inverse are then normal numbers).
@@ -145,8 +144,11 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
         PlanTotals t = {};
         t.places = places;
         t.tiles = (int)min(tiles, w.tiles);
-        // so many phases that the keys of one fit L2
-        const long long phases = (t.tiles * (long long)p.c.H * (kTile * 4 * p.c.D) + kPhaseBytes - 1) / kPhaseBytes;
+        // Phases only where tiles are visited so often that reading them again from HBM would bound the call: a
+        // prompt's chunk of 2048 tokens x 4 heads behind 61440 (32 visits a tile) takes 1716 us with phases of 64 MB, 1778
+        // with one; 16 ragged chunks (4 visits) 269 and 240, a window of 4096 (9 visits) 366 and 329 us: each phase has
+        // parts to be joined.
+        const long long phases = places < kPhaseVisits * t.tiles * p.c.H ? 1 : (t.tiles * (long long)p.c.H * (kTile * 4 * p.c.D) + kPhaseBytes - 1) / kPhaseBytes;
         t.pieces = (int)max(1ll, min(min((long long)w.pieces, w.ctas * max(phases, 1ll)), places / kLeastPiece));
         *reinterpret_cast<PlanTotals *>(p.ws + w.totals) = t;
     }
@@ -311,7 +313,7 @@ __device__ __forceinline__ void store32(uint8_t *dst, const uint32_t *v, bool wh
 }
 
 // One slot: warps 4-7 (t = 0) or 8-11 (t = 1), one row per thread.
-template <int D>
+template <int D, bool kInt8>
 __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint32_t tmem,
                                              int t, uint32_t warp, uint32_t lane, uint8_t *smem) {
     using C = Cfg<D>;
@@ -347,60 +349,122 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
             const int4 info = *reinterpret_cast<const int4 *>(&head->exp);
             const uint4 kw = *reinterpret_cast<const uint4 *>(head->keep);
             const int j0 = (k < d.sinks ? k : k - d.sinks + d.near) * kTile;
-            float s[128], hm[4];
-            {
-                uint32_t v0[32], v1[32], v2[32], v3[32];
-                tmem_ld32_max(lane_addr + s_col + 0, v0, hm[0]);
-                tmem_ld32_max(lane_addr + s_col + 32, v1, hm[1]);
-                tmem_ld32_max(lane_addr + s_col + 64, v2, hm[2]);
-                tmem_ld32_max(lane_addr + s_col + 96, v3, hm[3]);
-                tmem_wait_ld();
-                reg_fence(v0), reg_fence(v1), reg_fence(v2), reg_fence(v3);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) reg_fence(hm[x]);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    s[x] = __uint_as_float(v0[x]);
-                    s[32 + x] = __uint_as_float(v1[x]);
-                    s[64 + x] = __uint_as_float(v2[x]);
-                    s[96 + x] = __uint_as_float(v3[x]);
-                }
-            }
-            auto group_max = [&](int g) {
-                float a = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
-#pragma unroll
-                for (int x = 3; x < 31; x += 2) a = fmax3(a, s[32 * g + x], s[32 * g + x + 1]);
-                hm[g] = fmaxf(a, s[32 * g + 31]);
-            };
             const bool rest = ((uint32_t)info.y & kRest) != 0;
-            if (rest) {
-                const float4 *r = reinterpret_cast<const float4 *>(head->r);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const float4 f = r[x];
-                    fmul2(s[4 * x], s[4 * x + 1], s[4 * x], s[4 * x + 1], f.x, f.y);
-                    fmul2(s[4 * x + 2], s[4 * x + 3], s[4 * x + 2], s[4 * x + 3], f.z, f.w);
-                }
-#pragma unroll
-                for (int g = 0; g < 4; ++g) group_max(g);
-            }
             // a tile that every row of the slot meets whole needs no mask
-            const bool whole = (kw.x & kw.y & kw.z & kw.w) == 0xffffffffu && j0 + kTile <= low.ha &&
-                               (high.la <= j0 || high.hb >= j0 + kTile);
-            if (!whole) {
-                const uint32_t keep[4] = {kw.x, kw.y, kw.z, kw.w};
+            const bool masked = (kw.x & kw.y & kw.z & kw.w) != 0xffffffffu || j0 + kTile > low.ha ||
+                                (high.la > j0 && high.hb < j0 + kTile);
+            const bool plain = !rest && !masked;
+            // columns of 32 g .. that the row meets
+            auto meets = [&](int g) -> uint32_t {
+                const int c = j0 + 32 * g;
+                return span_bits(own.la - c, own.ha - c) | span_bits(0, own.hb - c);
+            };
+            float top = -INFINITY, s[kInt8 ? 128 : 1], hm[4];
+            // 32 scores of columns 32 g .. times r, -inf where the row does not meet the key
+            auto scores = [&](int g, float (&y)[32]) {
+                uint32_t v[32];
+                tmem_ld32(lane_addr + s_col + 32u * g, v);
+                tmem_wait_ld();
+                reg_fence(v);
+                if (rest) {
+                    const float4 *r = reinterpret_cast<const float4 *>(head->r) + 8 * g;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int c = j0 + 32 * g;
-                    const uint32_t bits = keep[g] & (span_bits(own.la - c, own.ha - c) | span_bits(0, own.hb - c));
-                    if (bits == 0xffffffffu) continue;
+                    for (int x = 0; x < 8; ++x) {
+                        const float4 f = r[x];
+                        fmul2(y[4 * x], y[4 * x + 1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                        fmul2(y[4 * x + 2], y[4 * x + 3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) y[x] = __uint_as_float(v[x]);
+                }
+                if (masked) {
+                    const uint32_t bits = (g == 0 ? kw.x : g == 1 ? kw.y : g == 2 ? kw.z : kw.w) & meets(g);
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
-                        if (!((bits >> x) & 1u)) s[32 * g + x] = -INFINITY;
-                    group_max(g);
+                        if (!((bits >> x) & 1u)) y[x] = -INFINITY;
+                }
+            };
+            if constexpr (kInt8) {
+                // Almost every tile's scores take factors: they stay in registers between the passes.
+                {
+                    uint32_t v0[32], v1[32], v2[32], v3[32];
+                    tmem_ld32_max(lane_addr + s_col + 0, v0, hm[0]);
+                    tmem_ld32_max(lane_addr + s_col + 32, v1, hm[1]);
+                    tmem_ld32_max(lane_addr + s_col + 64, v2, hm[2]);
+                    tmem_ld32_max(lane_addr + s_col + 96, v3, hm[3]);
+                    tmem_wait_ld();
+                    reg_fence(v0), reg_fence(v1), reg_fence(v2), reg_fence(v3);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) reg_fence(hm[x]);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        s[x] = __uint_as_float(v0[x]);
+                        s[32 + x] = __uint_as_float(v1[x]);
+                        s[64 + x] = __uint_as_float(v2[x]);
+                        s[96 + x] = __uint_as_float(v3[x]);
+                    }
+                }
+                auto group_max = [&](int g) {
+                    float a = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
+#pragma unroll
+                    for (int x = 3; x < 31; x += 2) a = fmax3(a, s[32 * g + x], s[32 * g + x + 1]);
+                    hm[g] = fmaxf(a, s[32 * g + 31]);
+                };
+                if (rest) {
+                    const float4 *r = reinterpret_cast<const float4 *>(head->r);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float4 f = r[x];
+                        fmul2(s[4 * x], s[4 * x + 1], s[4 * x], s[4 * x + 1], f.x, f.y);
+                        fmul2(s[4 * x + 2], s[4 * x + 3], s[4 * x + 2], s[4 * x + 3], f.z, f.w);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) group_max(g);
+                }
+                if (masked) {
+                    const uint32_t keep[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t bits = keep[g] & meets(g);
+                        if (bits == 0xffffffffu) continue;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!((bits >> x) & 1u)) s[32 * g + x] = -INFINITY;
+                        group_max(g);
+                    }
+                }
+                top = fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3]));
+            } else {
+                // First pass, the maximum: the load's own reduction where scores need no factor and no mask.  The loops of
+                // the passes are small (the roles share the instruction caches).
+                if (plain) {
+                    float hm[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t v[32];
+                        tmem_ld32_max(lane_addr + s_col + 32u * g, v, hm[g]);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) reg_fence(hm[g]);
+                    top = fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3]));
+                } else {
+#pragma unroll 1
+                    for (int g = 0; g < 4; ++g) {
+                        float y[32];
+                        scores(g, y);
+                        float t0 = fmax3(y[0], y[1], y[2]), t1 = fmax3(y[3], y[4], y[5]);
+#pragma unroll
+                        for (int x = 6; x < 30; x += 4) {
+                            t0 = fmax3(t0, y[x], y[x + 1]);
+                            t1 = fmax3(t1, y[x + 2], y[x + 3]);
+                        }
+                        top = fmaxf(top, fmax3(t0, fmaxf(y[30], y[31]), t1));
+                    }
                 }
             }
-            const float m_new = fmaxf(m_run, fmax3(hm[0], hm[1], fmaxf(hm[2], hm[3])) * sl2);
+            const float m_new = fmaxf(m_run, top * sl2);
             const bool begun = k > d.k0;
             const bool grew = !begun || __any_sync(0xffffffffu, m_new - m_run > kReach);
             float alpha = 1.f;
@@ -417,44 +481,8 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
             const bool rescale = begun && (grew || shift != 0);
             const float nm = kLift - m_run;
             float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
-            auto publish = [&](int half) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(wait.bar(C::bPR + 2 * t + half));
-            };
-            if (__builtin_expect(((uint32_t)info.y & kOdd) != 0, 0)) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int c = j0 + 32 * g;
-                    nan |= (head->odd[g] & (span_bits(own.la - c, own.ha - c) | span_bits(0, own.hb - c))) != 0u;
-                }
-            }
-            const bool usual = unit == 1.f;
-            auto half = [&](int c) {
-                uint32_t pk[32];
-                if (__builtin_expect(usual, 1)) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        float x0, x1;
-                        ffma2(x0, x1, s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1], sl2, sl2, nm, nm);
-                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                        if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
-                        else fadd2(la0, la1, la0, la1, p0, p1);
-                        pk[x] = pack_f16x2(p0, p1);
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float p0 = ex2_approx(fmaf(s[c * 64 + 2 * x], sl2, nm)), p1 = ex2_approx(fmaf(s[c * 64 + 2 * x + 1], sl2, nm));
-                        la0 += p0, la1 += p1;
-                        pk[x] = pack_f16x2(p0 * unit, p1 * unit);
-                    }
-                }
-                tmem_st32(lane_addr + s_col + c * 32, pk);
-            };
-            half(0);
-            if (rescale) {
+            auto rescale_output = [&] {
+                if (!rescale) return;
                 // S of this tile was issued after the slot's previous P V: O is up to date
                 const float f = alpha * pow2(shift);
 #pragma unroll
@@ -467,10 +495,97 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                     for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
                     tmem_st32(lane_addr + o_col + c * 32, v);
                 }
+            };
+            if (__builtin_expect(((uint32_t)info.y & kOdd) != 0, 0)) {
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) nan |= (head->odd[g] & meets(g)) != 0u;
             }
-            publish(0);
-            half(1);
-            publish(1);
+            // Second pass: 32 columns at a time, P over scores that have been read; 64 keys are handed over at a time.
+            auto hand_over = [&](int half) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(wait.bar(C::bPR + 2 * t + half));
+            };
+            auto part = [&](int g, float (&y)[32]) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) ffma2(y[2 * x], y[2 * x + 1], y[2 * x], y[2 * x + 1], sl2, sl2, nm, nm);
+                uint32_t pk[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    float p0 = ex2_approx(y[2 * x]), p1 = ex2_approx(y[2 * x + 1]);
+                    if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
+                    else fadd2(la0, la1, la0, la1, p0, p1);
+                    pk[x] = pack_f16x2(p0, p1);
+                }
+                if (__builtin_expect(unit != 1.f, 0)) {   // a power of two below 1
+                    const uint32_t u2 = pack_f16x2(unit, unit);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(pk[x]) : "r"(u2));
+                }
+                tmem_st16(lane_addr + s_col + 16u * g, pk);
+            };
+            if constexpr (kInt8) {
+                auto half = [&](int c) {
+                    uint32_t pk[32];
+                    if (__builtin_expect(unit == 1.f, 1)) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            float x0, x1;
+                            ffma2(x0, x1, s[c * 64 + 2 * x], s[c * 64 + 2 * x + 1], sl2, sl2, nm, nm);
+                            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                            if (x & 1) fadd2(lb0, lb1, lb0, lb1, p0, p1);
+                            else fadd2(la0, la1, la0, la1, p0, p1);
+                            pk[x] = pack_f16x2(p0, p1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            const float p0 = ex2_approx(fmaf(s[c * 64 + 2 * x], sl2, nm)), p1 = ex2_approx(fmaf(s[c * 64 + 2 * x + 1], sl2, nm));
+                            la0 += p0, la1 += p1;
+                            pk[x] = pack_f16x2(p0 * unit, p1 * unit);
+                        }
+                    }
+                    tmem_st32(lane_addr + s_col + c * 32, pk);
+                };
+                half(0);
+                rescale_output();
+                hand_over(0);
+                half(1);
+                hand_over(1);
+            } else {
+                rescale_output();
+                if (plain) {
+                    auto plain_part = [&](int g, uint32_t (&v)[32]) {
+                        float y[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) y[x] = __uint_as_float(v[x]);
+                        part(g, y);
+                    };
+                    uint32_t va[32], vb[32];
+                    tmem_ld32(lane_addr + s_col, va);
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        tmem_wait_ld();
+                        reg_fence(va);
+                        tmem_ld32(lane_addr + s_col + 64u * i + 32u, vb);
+                        plain_part(2 * i, va);
+                        tmem_wait_ld();
+                        reg_fence(vb);
+                        if (i == 0) tmem_ld32(lane_addr + s_col + 64u, va);
+                        plain_part(2 * i + 1, vb);
+                        hand_over(i);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int g = 0; g < 4; ++g) {
+                        float y[32];
+                        scores(g, y);
+                        part(g, y);
+                        if (g & 1) hand_over(g >> 1);
+                    }
+                }
+            }
             l_run = l_run * alpha + ((la0 + lb0) + (la1 + lb1));
         }
         if (!ok) break;
@@ -522,7 +637,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
     }
 }
 
-template <int D>
+template <int D, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
     bsattn_prefill_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Layout w,
                           const __grid_constant__ CUtensorMap tq) {
@@ -701,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         regs_claim<kSoftmaxRegs>();
-        softmax_role<D>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
+        softmax_role<D, kInt8>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
     }
     tc_fence_before();
     __syncthreads();
@@ -713,67 +828,69 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- join --
 
-// Block (x, y): kJoinRows rows of the segment that begins in piece x (x + gridDim.x, ..) and ends in a later one, a
-// warp each.
+// Blocks x, x + gridDim.x, ..: the segment that begins in that piece and ends in a later one; its rows are dealt out to the
+// warps of the blocks (x, 0), (x, 1), ..
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * 32) bsattn_prefill_join_kernel(const __grid_constant__ ChunkParams p,
-                                                                             const __grid_constant__ Layout w) {
+__global__ void __launch_bounds__(kJoinThreads) bsattn_prefill_join_kernel(const __grid_constant__ ChunkParams p,
+                                                                           const __grid_constant__ Layout w) {
+    constexpr int kWarps = kJoinThreads / 32;
     grid_launch_dependents();
-    const int r = blockIdx.y * kJoinRows + (int)(threadIdx.x / 32), lane = (int)(threadIdx.x % 32);
-    const int t = r / kTile, row = r % kTile, token_of = row / p.G, tok = t * w.tokens + token_of;
-    grid_dependency_wait();
-    if (token_of >= w.tokens) return;
-    const int pieces = w.few ? w.pieces : reinterpret_cast<const PlanTotals *>(p.ws + w.totals)->pieces;
+    const int lane = (int)(threadIdx.x % 32), rows = w.few ? w.few : 2 * kTile;
     const float *part_l = reinterpret_cast<const float *>(p.ws + w.part_l);
     const float *part_o = reinterpret_cast<const float *>(p.ws + w.part_o);
-    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+    grid_dependency_wait();
+    for (int piece = blockIdx.x; piece < w.pieces; piece += gridDim.x) {
         const CutInfo cut = reinterpret_cast<const CutInfo *>(p.ws + w.cuts)[piece];
-        if (cut.parts == 0 || tok >= cut.tokens) continue;
-        auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
-        float m = -INFINITY, sum = 0.f, o[D / 32] = {};
-        for (int x0 = 0; x0 < cut.parts; x0 += 32) {
-            const float l = x0 + lane < cut.parts ? part_l[at(x0 + lane)] : -INFINITY;
-            float top = l;
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float m_new = fmaxf(m, top);
-            const float f = l == -INFINITY ? 0.f : ex2_approx(l - m_new), drop = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-            m = m_new;
-            sum *= drop;
+        if (cut.parts == 0) continue;
+        for (int r = (int)(blockIdx.y * kWarps + threadIdx.x / 32); r < rows; r += (int)gridDim.y * kWarps) {
+            const int t = r / kTile, row = r % kTile, token_of = row / p.G, tok = t * w.tokens + token_of;
+            if (token_of >= w.tokens || tok >= cut.tokens) continue;
+            auto at = [&](int x) -> long long { return ((long long)(x == 0 ? 2 * piece + 1 : 2 * (piece + x)) * 2 + t) * kTile + row; };
+            float m = -INFINITY, sum = 0.f, o[D / 32] = {};
+            for (int x0 = 0; x0 < cut.parts; x0 += 32) {
+                const float l = x0 + lane < cut.parts ? part_l[at(x0 + lane)] : -INFINITY;
+                float top = l;
+                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float m_new = fmaxf(m, top);
+                const float f = l == -INFINITY ? 0.f : ex2_approx(l - m_new), drop = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+                m = m_new;
+                sum *= drop;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] *= drop;
-            const int n = min(32, cut.parts - x0);
+                for (int c = 0; c < D / 32; ++c) o[c] *= drop;
+                const int n = min(32, cut.parts - x0);
 #pragma unroll 4
-            for (int x = 0; x < n; ++x) {
-                const float fx = __shfl_sync(0xffffffffu, f, x);
-                if (fx == 0.f) continue;             // no key, or next to nothing
-                const float *y = part_o + at(x0 + x) * D + lane * (D / 32);
-                sum += fx;
-                if constexpr (D == 128) {
-                    const float4 v = *reinterpret_cast<const float4 *>(y);
-                    o[0] += fx * v.x, o[1] += fx * v.y, o[2] += fx * v.z, o[3] += fx * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(y);
-                    o[0] += fx * v.x, o[1] += fx * v.y;
+                for (int x = 0; x < n; ++x) {
+                    const float fx = __shfl_sync(0xffffffffu, f, x);
+                    if (fx == 0.f) continue;             // no key, or next to nothing
+                    const float *y = part_o + at(x0 + x) * D + lane * (D / 32);
+                    sum += fx;
+                    if constexpr (D == 128) {
+                        const float4 v = *reinterpret_cast<const float4 *>(y);
+                        o[0] += fx * v.x, o[1] += fx * v.y, o[2] += fx * v.z, o[3] += fx * v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2 *>(y);
+                        o[0] += fx * v.x, o[1] += fx * v.y;
+                    }
                 }
             }
-        }
-        const bool empty = sum == 0.f;
-        const float inv = empty ? 0.f : 1.f / sum;
-        const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
-        if (p.out_f32) {
-            float *dst = static_cast<float *>(p.out) + out * D + lane * (D / 32);
+            const bool empty = sum == 0.f;
+            const float inv = empty ? 0.f : 1.f / sum;
+            const long long out = (long long)(cut.token + tok) * p.Hq + cut.h * p.G + row - token_of * p.G;
+            if (p.out_f32) {
+                float *dst = static_cast<float *>(p.out) + out * D + lane * (D / 32);
 #pragma unroll
-            for (int c = 0; c < D / 32; c += 2) reinterpret_cast<float2 *>(dst)[c / 2] = make_float2(o[c] * inv, o[c + 1] * inv);
-        } else {
-            uint32_t *dst = static_cast<uint32_t *>(p.out) + (out * D + lane * (D / 32)) / 2;
+                for (int c = 0; c < D / 32; c += 2) reinterpret_cast<float2 *>(dst)[c / 2] = make_float2(o[c] * inv, o[c + 1] * inv);
+            } else {
+                uint32_t *dst = static_cast<uint32_t *>(p.out) + (out * D + lane * (D / 32)) / 2;
 #pragma unroll
-            for (int c = 0; c < D / 32; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+                for (int c = 0; c < D / 32; c += 2) dst[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+            }
+            if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
         }
-        if (lane == 0) p.lse[out] = empty ? -INFINITY : m * 0.69314718055994530942f + logf(sum);
     }
 }
 
-template <int D>
+template <int D, bool kInt8>
 cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     using C = Cfg<D>;
     static int attr_set_for_device[64] = {0};
@@ -784,10 +901,10 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     if (!attr_set_for_device[dev]) {
         // the register split inside the kernel assumes exactly kLaunchRegs per thread at launch
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, bsattn_prefill_kernel<D>);
+        e = cudaFuncGetAttributes(&fa, bsattn_prefill_kernel<D, kInt8>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-        e = cudaFuncSetAttribute(bsattn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
+        e = cudaFuncSetAttribute(bsattn_prefill_kernel<D, kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kAlloc);
         if (e != cudaSuccess) return e;
         attr_set_for_device[dev] = 1;
     }
@@ -798,22 +915,19 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     if (p.total > 0 && !w.few && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
     void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w), &tq};
     const auto join = reinterpret_cast<const void *>(bsattn_prefill_join_kernel<D>);
-    const unsigned join_rows = (unsigned)((w.few ? w.few : 2 * kTile) / kJoinRows);
     if (w.few) {
         e = launch_prefill_rows(p, w, stream);
-        return e != cudaSuccess || p.total == 0 ? e : launch_dependent(join, dim3((unsigned)w.pieces, join_rows), kJoinRows * 32, 0, args, stream);
+        return e != cudaSuccess || p.total == 0 ? e : launch_dependent(join, dim3((unsigned)w.pieces, (unsigned)(w.few * 32 / kJoinThreads)), kJoinThreads, 0, args, stream);
     }
     e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_plan_kernel), dim3(1), kPlanThreads, 0, args, stream);
     if (e != cudaSuccess || p.total == 0) return e;
     const long long items = w.tiles * p.c.H;
     const unsigned blocks = (unsigned)(items < sms * 8ll ? items : sms * 8ll);
-    e = launch_dependent(p.c.int8 ? reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, true>)
-                                  : reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, false>),
-                         dim3(blocks), kWidenThreads, 0, args, stream);
+    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_widen_kernel<D, kInt8>), dim3(blocks), kWidenThreads, 0, args, stream);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_kernel<D>), dim3((unsigned)w.ctas), kThreads, C::kAlloc, args, stream);
+    e = launch_dependent(reinterpret_cast<const void *>(bsattn_prefill_kernel<D, kInt8>), dim3((unsigned)w.ctas), kThreads, C::kAlloc, args, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(join, dim3((unsigned)(2 * w.ctas), join_rows), kJoinRows * 32, 0, args, stream);
+    return launch_dependent(join, dim3((unsigned)(w.pieces < 1024 ? w.pieces : 1024), 8), kJoinThreads, 0, args, stream);
 }
 
 }  // namespace
@@ -837,7 +951,8 @@ size_t prefill_workspace_bytes(int total, int B, int H, int G, int D, long long 
 }
 
 cudaError_t launch_prefill(const ChunkParams &p, cudaStream_t stream) {
-    return p.c.D == 128 ? launch<128>(p, stream) : launch<64>(p, stream);
+    if (p.c.D == 128) return p.c.int8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+    return p.c.int8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
 }
 
 }  // namespace bsattn

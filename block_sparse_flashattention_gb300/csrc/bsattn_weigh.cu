@@ -14,13 +14,13 @@
 // kUnitCost; every CTA numbers the line for itself (lengths are on the device).  A unit is not split: its weights
 // have one writer, and their sums one order.
 //
-// Roles (640 threads, one CTA per SM, all of TMEM):
+// Roles (896 threads, one CTA per SM, all of TMEM):
 //   warp 0        issues the MMAs
 //   warp 1        owns the TMEM allocation; finds the CTA's units
 //   warp 2        fetches the codes of keys: bulk copies of 16 keys into raw tiles
 //   warp 3        query blocks (TMA) and their lse
-//   warps 4-7, 8-11   group 0, group 1: sums
-//   warps 12-19   widen the codes (128-byte swizzle)
+//   warps 4-7, 8-11, 12-15, 16-19   first halves of group 0 and 1, second halves: sums
+//   warps 20-27   widen the codes (128-byte swizzle)
 // TMEM: S^T of group g and buffer i: [256 g + 128 i, 256 g + 128 i + 128).
 #include "kv_codes.cuh"
 #include "prefill_plan.cuh"
@@ -29,13 +29,14 @@ namespace bsattn {
 
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
 constexpr uint32_t kTmemCols = 512;
-// 96 registers per thread at launch, 61440 in all: 128 * 88 + 2 * 128 * 136 + 2 * 128 * 56 = 60416.
-constexpr int kLaunchRegs = 96;
-constexpr uint32_t kCtrlRegs = 88, kGroupRegs = 136, kWidenRegs = 56;
-static_assert(128 * kCtrlRegs + 256 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+// 72 registers per thread at launch: 128 * 72 + 4 * 128 * 80 + 2 * 128 * 56 = 64512 = 896 * 72.
+constexpr int kLaunchRegs = 72;
+constexpr uint32_t kCtrlRegs = 72, kGroupRegs = 80, kWidenRegs = 56;
+static_assert(128 * kCtrlRegs + 512 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
+constexpr int kSums = 4;                    // units whose half sums wait to be joined
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 bf16: one 128-byte swizzle span
 constexpr int kUnitKeys = 2 * kTile;
 constexpr int kUnitCost = 2;                // blocks that a unit's own work is worth
@@ -56,10 +57,10 @@ struct Unit {
 };
 
 // kFew: blocks of up to 64 rows, where HBM bounds the kernel: two units' codes on their way.  Else more blocks of
-// queries are.  Three tiles are widened at a time: the two of a unit, and the next one's first.
+// queries are, and the widened tiles are the two of a unit alone (with few, the next one's first is a third).
 template <int D, bool kFew>
 struct Cfg {
-    static constexpr int kTiles = 3, kBlocks = kFew ? 2 : 3, kRaws = kFew ? (D == 128 ? 2 : 4) : 1;
+    static constexpr int kTiles = kFew ? 3 : 2, kBlocks = kFew ? 2 : 3, kRaws = kFew ? (D == 128 ? 2 : 4) : 1;
     static constexpr uint32_t kTileBytes = kTile * D * 2, kRawBytes = kTile * D;
     static constexpr uint32_t kBlockBytes = kFew ? kTileBytes / 2 : kTileBytes;
     static constexpr uint32_t kBlockSub = kFew ? kSub / 2 : kSub;    // 64 columns of a block
@@ -69,13 +70,14 @@ struct Cfg {
     static constexpr uint32_t kLse = kScale + kRaws * 1024;          // -lse log2(e) of the blocks' rows
     static constexpr uint32_t kRow = kLse + kBlocks * 512;           // cache rows of the raw tiles' 16-key groups, -1: none
     static constexpr uint32_t kOdd = kRow + kRaws * 64;              // keys that have a NaN code, of four units
-    static constexpr uint32_t kUnit = kOdd + 4 * 32;
+    static constexpr uint32_t kSum = kOdd + 4 * 32;                  // sums of the groups' second halves
+    static constexpr uint32_t kUnit = kSum + kSums * 1024;
     static constexpr uint32_t kBar = kUnit + kUnits * (uint32_t)sizeof(Unit);
     // K' tiles full and empty, query blocks full and empty, S full and empty (2 group + buffer), raw units full and
-    // empty, units full and empty
+    // empty, half sums there (2 of a unit: per group), units full and empty
     static constexpr int bKF = 0, bKE = bKF + kTiles, bQF = bKE + kTiles, bQE = bQF + kBlocks, bSF = bQE + kBlocks, bSE = bSF + 4,
-                         bRF = bSE + 4, bRE = bRF + kRaws, bUF = bRE + kRaws, bUE = bUF + kUnits, bDrain = bUE + kUnits,
-                         kNumBars = bDrain + 1;
+                         bRF = bSE + 4, bRE = bRF + kRaws, bHF = bRE + kRaws, bUF = bHF + 2 * kSums, bUE = bUF + kUnits,
+                         bDrain = bUE + kUnits, kNumBars = bDrain + 1;
     static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
     static constexpr uint32_t kAlloc = kMisc + 8;
     static_assert(kAlloc <= 227u * 1024u, "shared memory");
@@ -357,10 +359,11 @@ __device__ __forceinline__ void unit_role(const ChunkParams &p, const Blocks &w,
     emit(stop);
 }
 
-// One group: 128 threads, a key each.
+// One half of a group: 128 threads, a key each, every other block (two buffers of S: one of either half's).  Four
+// warps a scheduler hide the exponentials' and loads' latencies that two do not.
 template <int D, bool kFew>
-__device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w, const Waiter &wait, uint32_t tmem, int g, uint32_t warp,
-                                           uint32_t lane, uint8_t *smem) {
+__device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w, const Waiter &wait, uint32_t tmem, int g, int half,
+                                           uint32_t warp, uint32_t lane, uint8_t *smem) {
     using C = Cfg<D, kFew>;
     const uint32_t quarter = warp & 3u;
     const int key = (int)(quarter * 32 + lane) + g * kTile;
@@ -395,13 +398,16 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
                 hi = (int)min(max((long long)j + p.window_left - pos, 0ll), (long long)x.m);
         }
         float sum = 0.f, lost = 0.f;             // compensated
+        bool first = true;
         for (int q = x.q0; q < x.q1; ++q, ++it) {
             const uint32_t buf = it & 1u, blk = it % C::kBlocks;
+            if ((int)buf != half) continue;
             ok = __all_sync(0xffffffffu, wait(C::bSF + 2 * g + (int)buf, it >> 1) && wait(C::bQF + (int)blk, it / C::kBlocks));
             if (!ok) break;
             tc_fence_after();
-            if (q == x.q0 && ((reinterpret_cast<const uint16_t *>(smem + C::kOdd)[16 * (ut & 3u) + 8 * g + 2 * quarter + (lane >> 4)] >> (lane & 15u)) & 1u))
+            if (first && ((reinterpret_cast<const uint16_t *>(smem + C::kOdd)[16 * (ut & 3u) + 8 * g + 2 * quarter + (lane >> 4)] >> (lane & 15u)) & 1u))
                 c = __uint_as_float(0x7fc00000u);
+            first = false;
             // of the block: columns that meet the key; of none behind the sequence's last token
             const int t0 = q * w.tokens, tokens = min(w.tokens, x.m - t0);
             const int from = min(max(lo - t0, 0), tokens) * p.G, to = min(max(hi - t0, 0), tokens) * p.G;
@@ -409,39 +415,40 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
             const float4 *nl = reinterpret_cast<const float4 *>(smem + C::kLse + blk * 512u);
             const uint32_t at = s_addr + buf * 128u;
             float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
-            auto chunk = [&](int cc, uint32_t (&v)[32]) {
-                float y[32];
+            auto chunk = [&](int cc, uint32_t (&v)[16]) {
+                float y[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 n = nl[8 * cc + i];
+                for (int i = 0; i < 4; ++i) {
+                    const float4 n = nl[4 * cc + i];
                     ffma2(y[4 * i], y[4 * i + 1], __uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), c, c, n.x, n.y);
                     ffma2(y[4 * i + 2], y[4 * i + 3], __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]), c, c, n.z, n.w);
                 }
                 if (masked) {
-                    const int f = from - 32 * cc, t = to - 32 * cc;
+                    const int f = from - 16 * cc, t = to - 16 * cc;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < 16; ++i)
                         if (i < f || i >= t) y[i] = -INFINITY;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    fadd2(a0, a1, a0, a1, ex2_approx(y[i]), ex2_approx(y[i + 1]));
-                    fadd2(b0, b1, b0, b1, ex2_approx(y[i + 2]), ex2_approx(y[i + 3]));
+                for (int i = 0; i < 16; ++i) y[i] = ex2_approx(y[i]);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    fadd2(a0, a1, a0, a1, y[i], y[i + 1]);
+                    fadd2(b0, b1, b0, b1, y[i + 2], y[i + 3]);
                 }
             };
-            uint32_t va[32], vb[32];
-            const int chunks = w.cols / 32;
-            tmem_ld32(at, va);
+            uint32_t va[16], vb[16];
+            const int chunks = w.cols / 16;     // even
+            tmem_ld16(at, va);
 #pragma unroll 1
             for (int cc = 0; cc < chunks; cc += 2) {
                 tmem_wait_ld();
                 reg_fence(va);
-                if (cc + 1 < chunks) tmem_ld32(at + 32u * (cc + 1), vb);
+                tmem_ld16(at + 16u * (cc + 1), vb);
                 chunk(cc, va);
-                if (cc + 1 >= chunks) break;
                 tmem_wait_ld();
                 reg_fence(vb);
-                if (cc + 2 < chunks) tmem_ld32(at + 32u * (cc + 2), va);
+                if (cc + 2 < chunks) tmem_ld16(at + 16u * (cc + 2), va);
                 chunk(cc + 1, vb);
             }
             tc_fence_before();
@@ -455,8 +462,22 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
             sum = next;
         }
         if (!ok) break;
-        if (x.q1 > x.q0) ++ut;
-        if (row >= 0) {
+        if (x.q1 > x.q0) {
+            // the second half's sum goes to the first, which has the weight written; by the blocks' barriers it is at
+            // most two units ahead
+            const uint32_t at = ut % kSums, full = C::bHF + 2 * at + (uint32_t)g;
+            float *sums = reinterpret_cast<float *>(smem + C::kSum + at * 1024u);
+            if (half == 1) {
+                sums[key] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(wait.bar((int)full));
+            } else {
+                if (!__all_sync(0xffffffffu, wait((int)full, ut / kSums))) break;
+                sum += sums[key];
+            }
+            ++ut;
+        }
+        if (row >= 0 && half == 0) {
             if (!p.accumulate) p.weights[row] = sum;
             else if (hi > lo) atomicAdd(p.weights + row, sum);
         }
@@ -604,19 +625,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(wait.bar(C::bSF + s), 1);
-            mbar_init(wait.bar(C::bSE + s), 4);      // one per warp of the group
+            mbar_init(wait.bar(C::bSE + s), 4);      // one per warp of the group's half
         }
         for (int s = 0; s < C::kBlocks; ++s) {
             mbar_init(wait.bar(C::bQF + s), 1);
-            mbar_init(wait.bar(C::bQE + s), 9);      // the products' completion, one per warp of the groups
+            mbar_init(wait.bar(C::bQE + s), 9);      // the products' completion, one per warp that reads the block's lse
         }
         for (int s = 0; s < C::kRaws; ++s) {
             mbar_init(wait.bar(C::bRF + s), 1);
-            mbar_init(wait.bar(C::bRE + s), 16);     // widening and group warps
+            mbar_init(wait.bar(C::bRE + s), 24);     // widening and group warps
         }
+        for (int s = 0; s < 2 * kSums; ++s) mbar_init(wait.bar(C::bHF + s), 4);
         for (int s = 0; s < kUnits; ++s) {
             mbar_init(wait.bar(C::bUF + s), 1);
-            mbar_init(wait.bar(C::bUE + s), 19);     // issuing, fetching, query, group and widening warps
+            mbar_init(wait.bar(C::bUE + s), 27);     // issuing, fetching, query, group and widening warps
         }
         mbar_init(wait.bar(C::bDrain), 1);
         misc[1] = 0;
@@ -642,7 +664,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
     if (warp == 0) {
-        regs_release<kCtrlRegs>();
         // ---------------------------------------------------- MMA issuer --
         // The whole warp runs in step; lane 0 issues.
         const uint32_t lead = lane == 0 ? 1u : 0u;
@@ -687,15 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_lead(lead, wait.bar(C::bDrain));
         mbar_wait_drain(wait.bar(C::bDrain), 0);
     } else if (warp == 1) {
-        regs_release<kCtrlRegs>();
         const Start from = alone ? find_piece_warp(p, w, (int)lane) : *st;
         if (lane == 0) unit_role<C>(p, w, wait, smem, from);
         __syncwarp();
     } else if (warp == 2) {
-        regs_release<kCtrlRegs>();
         fetch_role<D, kFew>(p, wait, (int)lane, base, smem);
     } else if (warp == 3) {
-        regs_release<kCtrlRegs>();
         // ------------------------------------------------- query blocks --
         if (lane == 0) tma_prefetch_desc(&tq);
         const uint32_t bytes = (uint32_t)(p.G * w.tokens) * D * 2u;
@@ -737,12 +755,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // nothing may be on its way into shared memory when the CTA ends
         for (uint32_t s = 0; s < (uint32_t)C::kBlocks; ++s)
             if (it > s) mbar_wait_drain(wait.bar(C::bQF + (int)s), ((it - 1 - s) / C::kBlocks) & 1u);
-    } else if (warp < 12) {
+    } else if (warp < 20) {
         regs_claim<kGroupRegs>();
-        group_role<D, kFew>(p, w, wait, tmem, warp >= 8 ? 1 : 0, warp, lane, smem);
+        group_role<D, kFew>(p, w, wait, tmem, (int)(warp >> 2 & 1u) ^ 1, (int)(warp - 4) >> 3, warp, lane, smem);
     } else {
         regs_release<kWidenRegs>();
-        widen_role<D, kFew, kInt8>(wait, (int)warp - 12, (int)lane, smem);
+        widen_role<D, kFew, kInt8>(wait, (int)warp - 20, (int)lane, smem);
     }
     tc_fence_before();
     __syncthreads();

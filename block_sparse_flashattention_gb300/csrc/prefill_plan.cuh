@@ -86,6 +86,7 @@ inline int segment_rows(int total, int B, int G) {
 
 // Widened bytes that the CTAs work on at a time: of 129 MB of L2, less what else passes through.
 constexpr long long kPhaseBytes = 64ll << 20;
+constexpr int kPhaseVisits = 16;
 
 inline Layout make_layout(int total, int B, int H, int G, int D, long long keys, int ctas) {
     Layout w = {};

@@ -910,7 +910,7 @@ cudaError_t launch(const ChunkParams &p, cudaStream_t stream) {
     }
     const int sms = current_device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const Layout w = make_layout(p.total, p.B, p.c.H, p.G, D, p.keys, sms < kMaxCtas ? sms : kMaxCtas);
+    const Layout w = make_layout(p.total, p.B, p.c.H, p.G, D, p.keys, sms < kPrefillCtas ? sms : kPrefillCtas);
     CUtensorMap tq = {};
     if (p.total > 0 && !w.few && !encode_query_rows(&tq, p.q, p.total, p.Hq, D, p.q_stride, w.tokens, p.G)) return cudaErrorInvalidValue;
     void *args[] = {const_cast<ChunkParams *>(&p), const_cast<Layout *>(&w), &tq};
@@ -947,7 +947,7 @@ cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t 
 }
 
 size_t prefill_workspace_bytes(int total, int B, int H, int G, int D, long long keys) {
-    return make_layout(total, B, H, G, D, keys, kMaxCtas).total;
+    return make_layout(total, B, H, G, D, keys, kPrefillCtas).total;
 }
 
 cudaError_t launch_prefill(const ChunkParams &p, cudaStream_t stream) {

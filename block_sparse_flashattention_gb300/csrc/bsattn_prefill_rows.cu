@@ -10,8 +10,8 @@
 // A thread has one key of the tile: its scales are two registers, z_r = S_r c_r ks (c_r = softmax_scale
 // log2(e) 2^e of row r) and p_r = 2^(z_r - m_r + 7); p_r vs 2^-E is rounded to fp16 (11 bits) for V'^T P^T,
 // and the thread sums p_r of its keys by itself, in fp32.  Only at a segment's end are sums joined over the
-// threads.  The reference m_r (per query row, kept by all) and E (the largest binary exponent of a value scale so
-// far, a multiple of 4) are moved only when some weight could pass 2^14 or some scale passes E: the threads
+// threads.  The reference m_r (per query row, kept by all) and E (2^2 above the largest binary exponent of a value
+// scale so far, rounded up to a multiple of 4) are moved only when some weight could pass 2^14 or some scale passes E: the threads
 // vote on every tile, and the maxima over the keys, which cost a pass of their own, are taken then.
 //
 // Up to 64 rows two groups of threads take the tiles in turn, each with sums of its own, joined at the end: while
@@ -34,13 +34,14 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 256;
-// 96 registers per thread at launch: 128 * 48 + 2 * 128 * 160 + 2 * 128 * 56 = 61440 = 640 * 96.
+// 96 registers per thread at launch: 128 * 80 + 2 * 128 * 144 + 2 * 128 * 56 = 61440 = 640 * 96.
 constexpr int kLaunchRegs = 96;
-constexpr uint32_t kCtrlRegs = 48, kGroupRegs = 160, kWidenRegs = 56;
+constexpr uint32_t kCtrlRegs = 80, kGroupRegs = 144, kWidenRegs = 56;
 static_assert(128 * kCtrlRegs + 256 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 fp16: one 128-byte swizzle span
 constexpr float kLift = 7.f, kReach = 7.f;
+constexpr int kRoom = 2;                    // binary exponents of value scales up to which E stays
 
 // kRows: query rows of a segment at most.
 template <int D, int kRows>
@@ -161,8 +162,8 @@ __device__ __forceinline__ void find_piece(const ChunkParams &p, const Layout &w
         before = line + scan(pass * p.c.H, all);
         line += all;
     }
-    const int pieces = (int)max(1ll, min((long long)w.ctas, line / kLeastPiece)), piece = (int)blockIdx.x;
-    const long long from = line * piece / pieces;
+    const int pieces = (int)max(1ll, min((long long)w.ctas, line_div(line, kLeastPiece))), piece = (int)blockIdx.x;
+    const long long from = line_div(line * piece, pieces);
     if (tid == 0) st->pieces = pieces, st->line = line, st->b = p.B;
     __syncthreads();
     if (piece >= pieces || from >= line) return;
@@ -177,7 +178,7 @@ __device__ __forceinline__ void find_piece(const ChunkParams &p, const Layout &w
             sum += all;
         }
         if (from >= before && from < before + pass * p.c.H) {
-            const int h = (int)((from - before) / pass);
+            const int h = (int)line_div(from - before, pass);
             long long at = before + h * pass;
             int r = 0;
             for (int len; at + (len = kRowsCost + segment_tiles(p, w, c, r)) <= from; ++r) at += len;
@@ -186,10 +187,66 @@ __device__ __forceinline__ void find_piece(const ChunkParams &p, const Layout &w
     }
 }
 
+// The same by one warp, without a barrier, of up to 32 kLaneSeqs sequences.
+struct Start {
+    int b, h, r, pieces;
+    long long begin, line;
+    Chunk c;                 // of sequence b
+};
+constexpr int kLaneSeqs = 4;
+
+__device__ __forceinline__ Start find_piece_warp(const ChunkParams &p, const Layout &w, int lane) {
+    Chunk c[kLaneSeqs];
+    long long pass[kLaneSeqs], before[kLaneSeqs];
+    Start st = {};
+#pragma unroll
+    for (int k = 0; k < kLaneSeqs; ++k) {
+        c[k] = Chunk{};
+        if (32 * k + lane < p.B) c[k] = chunk_of(p, 32 * k + lane, blockIdx.x == 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kLaneSeqs; ++k) {
+        if (32 * k >= p.B) break;
+        pass[k] = pass_places(p, w, c[k]);
+        long long s = pass[k] * p.c.H;
+        const long long own = s;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        before[k] = st.line + s - own;
+        st.line += __shfl_sync(0xffffffffu, s, 31);
+    }
+    st.pieces = (int)max(1ll, min((long long)w.ctas, line_div(st.line, kLeastPiece)));
+    st.b = p.B;
+    const long long from = line_div(st.line * (int)blockIdx.x, st.pieces);
+    if ((int)blockIdx.x >= st.pieces) return st;
+#pragma unroll
+    for (int k = 0; k < kLaneSeqs; ++k) {
+        if (32 * k >= p.B) break;
+        const bool here = from >= before[k] && from < before[k] + pass[k] * p.c.H;
+        const uint32_t hit = __ballot_sync(0xffffffffu, here);
+        if (!hit) continue;
+        if (here) {
+            st.h = (int)line_div(from - before[k], pass[k]);
+            st.begin = before[k] + st.h * pass[k];
+            for (int len; st.begin + (len = kRowsCost + segment_tiles(p, w, c[k], st.r)) <= from; ++st.r) st.begin += len;
+        }
+        const int x = __ffs(hit) - 1;
+        st.b = 32 * k + x;
+        st.h = __shfl_sync(0xffffffffu, st.h, x);
+        st.r = __shfl_sync(0xffffffffu, st.r, x);
+        st.begin = __shfl_sync(0xffffffffu, st.begin, x);
+        st.c.first = __shfl_sync(0xffffffffu, c[k].first, x);
+        st.c.m = __shfl_sync(0xffffffffu, c[k].m, x);
+        st.c.n = __shfl_sync(0xffffffffu, c[k].n, x);
+    }
+    return st;
+}
+
 // Finds the segments of the CTA's piece and writes their descriptors.
 template <class C>
-__device__ __forceinline__ void segment_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint8_t *smem) {
-    const Stat *st = reinterpret_cast<const Stat *>(smem + C::kStat);
+__device__ __forceinline__ void segment_role(const ChunkParams &p, const Layout &w, const Waiter &wait, uint8_t *smem, const Start &st) {
     CutInfo *cut = reinterpret_cast<CutInfo *>(p.ws + w.cuts) + blockIdx.x;
     *cut = CutInfo{};
     uint32_t count = 0;
@@ -201,13 +258,13 @@ __device__ __forceinline__ void segment_role(const ChunkParams &p, const Layout 
         ++count;
         return true;
     };
-    const long long line = st->line;
-    const int pieces = st->pieces, piece = (int)blockIdx.x;
-    int b = st->b, h = st->h, r = st->r;
+    const long long line = st.line;
+    const int pieces = st.pieces, piece = (int)blockIdx.x;
+    int b = st.b, h = st.h, r = st.r;
     if (b < p.B) {
-        const long long from = line * piece / pieces, to = line * (piece + 1) / pieces;
-        long long begin = st->begin;
-        Chunk s = chunk_of(p, b, false);
+        const long long from = line_div(line * piece, pieces), to = line_div(line * (piece + 1), pieces);
+        long long begin = st.begin;
+        Chunk s = st.c;
         while (begin < to) {
             if (r * (long long)w.step >= s.m) {
                 r = 0;
@@ -238,7 +295,7 @@ __device__ __forceinline__ void segment_role(const ChunkParams &p, const Layout 
                     d.part = 2 * piece + (d.k0 > 0 ? 0 : 1);
                     if (d.k0 == 0) {
                         // the piece that holds the last tile: place x is in piece ((x + 1) pieces - 1) / line
-                        const int last = (int)(((first + tiles) * pieces - 1) / line);
+                        const int last = (int)line_div((first + tiles) * pieces - 1, line);
                         CutInfo x;
                         x.token = d.token, x.tokens = d.tokens, x.h = h, x.parts = last - piece + 1;
                         *cut = x;
@@ -277,14 +334,15 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
         const bool turns = kRows <= 64 || rows <= 64;
         const int row0 = turns ? 0 : 64 * g, cols = turns ? rows : min(max(rows - row0, 0), kCols);
         const int chunks = (cols + 15) / 16;
-        // ---- query rows: fp16 of q 2^-e (K-major, swizzled), D / 8 lanes to a row
-        if (16 * sw < rows) {
-            constexpr int kRowLanes = D / 8, kAtOnce = 32 / kRowLanes, kSteps = 16 / kAtOnce;
+        // ---- query rows: fp16 of q 2^-e (K-major, swizzled), D / 8 lanes to a row, the rows dealt out to all warps
+        constexpr int kOwn = kRows / 8;
+        if (kOwn * sw < ((rows + 15) & ~15)) {
+            constexpr int kRowLanes = D / 8, kAtOnce = 32 / kRowLanes < kOwn ? 32 / kRowLanes : kOwn, kSteps = kOwn / kAtOnce;
             const int piece = (int)lane % kRowLanes, sub = (int)lane / kRowLanes;
             uint4 x[kSteps];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * sw + i * kAtOnce + sub, tok = r / p.G;
+                const int r = kOwn * sw + i * kAtOnce + min(sub, kAtOnce - 1), tok = r / p.G;
                 x[i] = make_uint4(0, 0, 0, 0);
                 if (r < rows)
                     x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (long long)(d.token + tok) * p.q_stride +
@@ -292,7 +350,7 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
             }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
-                const int r = 16 * sw + i * kAtOnce + sub;
+                const int r = kOwn * sw + i * kAtOnce + min(sub, kAtOnce - 1);
                 uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, a = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) a = __vmaxu2(a, y[k] & 0x7fff7fffu);
@@ -358,7 +416,6 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
             const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < cols);
             const uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
             const int vexp = vb < 0x7f800000u && vb > 1u << 23 ? (int)(vb >> 23) : 0;
-            bool fresh = false;                  // m has just been moved
             ok = __all_sync(0xffffffffu, wait(C::bSR + g, sc) && (kInt8 || wait(C::bVF + (int)stage, it >> 1)));
             ++sc;
             tc_fence_after();
@@ -366,56 +423,58 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
                 vs = 0.f;
                 for (int r = max(lo, 0); r < min(hi, cols); ++r) st->bad[64 * g + r] = 1;
             }
-            // The scores less m (a, in units of log2, 7 for the largest).  Where the threads vote to move m,
-            // they are formed again without it, their maxima taken, and formed once more.
-            float a[kCols];
-            bool raw = !begun;
-            if (raw && any_of_group(g, !ok)) ok = false;
-            while (ok || begun) {
+            // scores of columns 16 c .. less m, in units of log2: 7 for the largest (nm zero: the scores)
+            auto scores = [&](int c, const float *nm, float (&y)[16]) {
+                uint32_t v[16];
+                tmem_ld16(s_addr + 16u * c, v);
+                tmem_wait_ld();
+                reg_fence(v);
+                const float4 *cr = reinterpret_cast<const float4 *>(st->c + row0 + 16 * c), *less = reinterpret_cast<const float4 *>(nm + 16 * c);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float4 f = cr[x], n = less[x];
+                    float *z = y + 4 * x;
+                    fmul2(z[0], z[1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
+                    fmul2(z[2], z[3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
+                    ffma2(z[0], z[1], z[0], z[1], ks, ks, n.x, n.y);
+                    ffma2(z[2], z[3], z[2], z[3], ks, ks, n.z, n.w);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        if (16 * c + x < lo || 16 * c + x >= hi) y[x] = -INFINITY;
+                }
+            };
+            // Does m, or E, have to move?  All threads of the group decide as one.
+            bool move = !begun;
+            if (begun) {
                 float top = -INFINITY;
                 if (ok) {
-                    const float4 *cr = reinterpret_cast<const float4 *>(st->c + row0);
-                    const float4 *nm = reinterpret_cast<const float4 *>(raw ? st->zero : st->nm[g]);
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        float y[16];
+                        scores(c, st->nm[g], y);
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (kChunks > 1 && c >= chunks) break;
-                        uint32_t v[16];
-                        tmem_ld16(s_addr + 16u * c, v);
-                        tmem_wait_ld();
-                        reg_fence(v);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float4 f = cr[4 * c + x], n = nm[4 * c + x];
-                            float *y = a + 16 * c + 4 * x;
-                            fmul2(y[0], y[1], __uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), f.x, f.y);
-                            fmul2(y[2], y[3], __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]), f.z, f.w);
-                            ffma2(y[0], y[1], y[0], y[1], ks, ks, n.x, n.y);
-                            ffma2(y[2], y[3], y[2], y[3], ks, ks, n.z, n.w);
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int x = 0; x < 16; ++x)
-                                if (16 * c + x < lo || 16 * c + x >= hi) a[16 * c + x] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int x = 0; x < 16; x += 2) top = fmax3(top, a[16 * c + x], a[16 * c + x + 1]);
+                        for (int x = 0; x < 16; x += 2) top = fmax3(top, y[x], y[x + 1]);
                     }
                 }
-                if (!raw) {
-                    if (fresh || !any_of_group(g, !ok || top > kLift + kReach || vexp > exp_run)) break;
-                    if (any_of_group(g, !ok)) {
-                        ok = false;
-                        break;
-                    }
-                    raw = true;
-                    continue;
+                move = any_of_group(g, !ok || top > kLift + kReach || vexp > exp_run);
+            }
+            if (move) {
+                if (any_of_group(g, !ok)) {
+                    ok = false;
+                    break;
                 }
                 int *rexp = reinterpret_cast<int *>(red + 256);
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    float y[16];
+                    scores(c, st->zero, y);
 #pragma unroll
-                for (int x = 0; x < kCols; ++x) {
-                    if (kChunks > 1 && x >= 16 * chunks) break;
-                    const float m = warp_max(a[x]);
-                    if (lane == 0) red[quarter * 64 + x] = m;
+                    for (int x = 0; x < 16; ++x) {
+                        const float m = warp_max(y[x]);
+                        if (lane == 0) red[quarter * 64 + 16 * c + x] = m;
+                    }
                 }
                 const int we = __reduce_max_sync(0xffffffffu, vexp);
                 if (lane == 0) rexp[quarter] = we;
@@ -430,7 +489,8 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
                     }
                     st->alpha[g][key] = alpha;
                 }
-                const int e = min((max(max(max(rexp[0], rexp[1]), max(rexp[2], rexp[3])), 8) + 3) & ~3, 252);
+                // with room for a scale or two that are larger
+                const int e = min(((max(max(max(rexp[0], rexp[1]), max(rexp[2], rexp[3])), 8) + 3) & ~3) + kRoom, 252);
                 const float drop = pow2(exp_run - max(exp_run, e));
                 exp_run = max(exp_run, e);
                 group_sync(g);
@@ -453,20 +513,19 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
                     }
                     tmem_wait_st();
                 }
-                raw = false;
-                fresh = true;
             }
-            if (!ok) break;
             begun = true;
             const float wv = vs * pow2(127 - exp_run);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if (kChunks > 1 && c >= chunks) break;
+                float y[16];
+                scores(c, st->nm[g], y);
                 uint32_t pk[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const int i = 16 * c + 2 * x;
-                    float p0 = ex2_approx(a[i]), p1 = ex2_approx(a[i + 1]);
+                    float p0 = ex2_approx(y[2 * x]), p1 = ex2_approx(y[2 * x + 1]);
                     fadd2(l[i], l[i + 1], l[i], l[i + 1], p0, p1);
                     fmul2(p0, p1, p0, p1, wv, wv);
                     pk[x] = pack_f16x2(p0, p1);
@@ -718,8 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = misc[0];
     grid_launch_dependents();
     grid_dependency_wait();
-    find_piece<C>(p, w, smem);
-    __syncthreads();
+    const bool alone = p.B <= 32 * kLaneSeqs;    // one warp numbers the line, while the others take their places
+    if (!alone) {
+        find_piece<C>(p, w, smem);
+        __syncthreads();
+    }
     if (warp == 0) {
         regs_release<kCtrlRegs>();
         // ---------------------------------------------------- MMA issuer --
@@ -816,7 +878,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
         regs_release<kCtrlRegs>();
         if (warp == 1) {
-            if (lane == 0) segment_role<C>(p, w, wait, smem);
+            Start from;
+            if (alone) {
+                from = find_piece_warp(p, w, (int)lane);
+            } else {
+                const Stat *st = reinterpret_cast<const Stat *>(smem + C::kStat);
+                from.b = st->b, from.h = st->h, from.r = st->r, from.pieces = st->pieces, from.begin = st->begin, from.line = st->line;
+                if (from.b < p.B) from.c = chunk_of(p, from.b, false);
+            }
+            if (lane == 0) segment_role<C>(p, w, wait, smem, from);
             __syncwarp();
         } else {
             fetch_role<D, kRows>(p, wait, warp == 3, (int)lane, base, smem);

@@ -137,12 +137,12 @@ __device__ __forceinline__ long long pass_places(const ChunkParams &p, const Blo
 __device__ __forceinline__ void first_unit(const ChunkParams &p, const Blocks &w, long long from, long long begin, long long places,
                                            int lane, Start &st) {
     const Chunk &c = st.c;
-    st.h = (int)((from - begin) / places);
+    st.h = (int)line_div(from - begin, places);
     st.begin = begin + st.h * places;
     st.u = 0;
     if (plain_places(w, c)) {
         const int x = unit_places(p, w, c, 0);
-        st.u = min((int)((from - st.begin + x - 1) / x), unit_count(c));
+        st.u = min((int)line_div(from - st.begin + x - 1, x), unit_count(c));
         st.begin += (long long)st.u * x;
         return;
     }
@@ -216,10 +216,10 @@ __device__ __forceinline__ void find_piece(const ChunkParams &p, const Blocks &w
     };
     long long line = 0;
     for (int b0 = 0; b0 < p.B; b0 += kSeqChunk) line = number(b0, blockIdx.x == 0, line);
-    const int pieces = (int)max(1ll, min((long long)gridDim.x, line / kUnitCost)), piece = (int)blockIdx.x;
+    const int pieces = (int)max(1ll, min((long long)gridDim.x, line_div(line, kUnitCost))), piece = (int)blockIdx.x;
     if (tid == 0) st->b = p.B, st->pieces = pieces, st->line = line;
     if (piece >= pieces || line == 0) return;
-    const long long from = line * piece / pieces;
+    const long long from = line_div(line * piece, pieces);
     long long at = 0;
     for (int b0 = 0; b0 < p.B; b0 += kSeqChunk) {
         const long long end = p.B > kSeqChunk ? number(b0, false, at) : line;
@@ -283,10 +283,10 @@ __device__ __forceinline__ Start find_piece_warp(const ChunkParams &p, const Blo
     }
     Start st = {};
     st.line = line;
-    st.pieces = (int)max(1ll, min((long long)gridDim.x, line / kUnitCost));
+    st.pieces = (int)max(1ll, min((long long)gridDim.x, line_div(line, kUnitCost)));
     st.b = p.B;
     if ((int)blockIdx.x >= st.pieces) return st;
-    const long long from = line * (int)blockIdx.x / st.pieces;
+    const long long from = line_div(line * (int)blockIdx.x, st.pieces);
 #pragma unroll
     for (int k = 0; k < kLaneSeqs; ++k) {
         if (32 * k >= p.B) break;
@@ -327,7 +327,7 @@ __device__ __forceinline__ void unit_role(const ChunkParams &p, const Blocks &w,
     };
     int b = st.b, h = st.h, u = st.u;
     if (b < p.B) {
-        const long long to = st.line * ((long long)blockIdx.x + 1) / st.pieces;
+        const long long to = line_div(st.line * ((long long)blockIdx.x + 1), st.pieces);
         long long begin = st.begin;
         Chunk c = st.c;
         int units = unit_count(c);

@@ -3,10 +3,11 @@
 #pragma once
 
 #include "chunk_common.cuh"
+#include "decode_plan.cuh"
 
 namespace bsattn {
 
-constexpr int kMaxCtas = 160;
+constexpr int kPrefillCtas = 160;
 constexpr int kSegCost = 2;                 // places of the line that starting and ending a segment costs
 constexpr int kLeastPiece = 4;              // places of a piece: each makes parts for the join
 constexpr int kDescs = 2;                   // segments found ahead
@@ -196,7 +197,7 @@ __device__ __forceinline__ void schedule_role(const ChunkParams &p, const Layout
         return true;
     };
     for (int piece = blockIdx.x; ok && piece < pieces; piece += w.ctas) {
-        const long long from = line * piece / pieces, to = line * (piece + 1) / pieces;
+        const long long from = line_div(line * piece, pieces), to = line_div(line * (piece + 1), pieces);
         CutInfo cut = {};
         if (from < to) {
             int b = 0, hi = p.B - 1;             // the last sequence that begins at or before `from`
@@ -206,7 +207,7 @@ __device__ __forceinline__ void schedule_role(const ChunkParams &p, const Layout
                 else hi = mid - 1;
             }
             SeqPlan s = seq[b];
-            int h = s.pass > 0 ? (int)((from - s.base) / s.pass) : 0;
+            int h = s.pass > 0 ? (int)line_div(from - s.base, s.pass) : 0;
             int r = 0;
             if (s.pass > 0) {
                 const int off = (int)(from - s.base - (long long)h * s.pass);
@@ -254,7 +255,7 @@ __device__ __forceinline__ void schedule_role(const ChunkParams &p, const Layout
                         d.part = 2 * piece + (d.k0 > 0 ? 0 : 1);
                         if (d.k0 == 0) {
                             // the piece that holds the last tile: place x is in piece ((x + 1) pieces - 1) / line
-                            const int last = (int)(((first + tiles) * pieces - 1) / line);
+                            const int last = (int)line_div((first + tiles) * pieces - 1, line);
                             cut.token = d.token, cut.tokens = d.tokens, cut.h = h, cut.parts = last - piece + 1;
                         }
                     }

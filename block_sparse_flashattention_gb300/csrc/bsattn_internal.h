@@ -215,9 +215,12 @@ struct EvictParams {
     int32_t *err;
 };
 
+// A launch that may begin before the one ahead of it in the stream has ended (it waits where it says so).
+cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t smem, void **args, cudaStream_t stream);
 cudaError_t launch_prefill(const ChunkParams &p, cudaStream_t stream);
 size_t prefill_workspace_bytes(int total, int B, int H, int G, int D, long long keys);
 cudaError_t launch_weigh(const ChunkParams &p, cudaStream_t stream);
+cudaError_t launch_weigh_step(const ChunkParams &p, int rows, cudaStream_t stream);   // of up to 32 rows
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);

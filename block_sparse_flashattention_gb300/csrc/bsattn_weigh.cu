@@ -42,6 +42,9 @@ constexpr int kUnitKeys = 2 * kTile;
 constexpr int kUnitCost = 2;                // blocks that a unit's own work is worth
 constexpr int kSeqChunk = 2048;             // sequences whose places fit shared memory at a time
 constexpr int kUnits = 2;                   // units found ahead
+// Mean query rows of a KV head up to which bsattn_weigh_step.cu is the faster one.  32 sequences of 4096 keys, 8 heads,
+// D = 128, us a call there and here: 4 rows 44, 80, 16 rows 49, 80, 32 rows 60, 80; D = 64: 33, 62, 40, 62, 50, 62.
+constexpr int kStepRows = 32;
 
 // Rows of a query block: tokens of all of a KV head's query heads.
 struct Blocks {
@@ -517,23 +520,6 @@ __device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &w
         if (it > s) mbar_wait_drain(wait.bar(C::bRF + (int)s), ((it - 1 - s) / C::kRaws) & 1u);
 }
 
-// Two e4m3 or int8 codes (16-bit halves of `x`, the code in the high byte) as bf16.  e4m3: its exponent and
-// mantissa moved to bf16's are the value times 2^-120.  int8, whose low 7 bits l and sign s make 128 + l (bits
-// 0x4300 | l) less 128 or, where s, 256.
-template <bool kInt8>
-__device__ __forceinline__ uint32_t code_to_bf16x2(uint32_t x) {
-    uint32_t r;
-    if constexpr (kInt8) {
-        const uint32_t y = x >> 8;               // codes in the low bytes
-        const uint32_t a = (y & 0x007f007fu) | 0x43004300u, b = (y & 0x00800080u) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    } else {
-        const uint32_t a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7b807b80u));   // 2^120
-    }
-    return r;
-}
-
 // Widens the codes of tiles, eight warps each, 16 keys a warp.  Lane: 16 codes of a row, two swizzle pieces; D / 16
 // lanes to a row.  What no copy has filled is left: such keys are masked.
 template <int D, bool kFew, bool kInt8>
@@ -808,6 +794,8 @@ cudaError_t launch_weigh(const ChunkParams &p, cudaStream_t stream) {
     // Rows of a block: what the sequences have on the average, so that a decoding step's products are 32
     // columns wide.
     const long long mean = ((long long)p.total + p.B - 1) / p.B;
+    const long long rows = (mean > 0 ? mean : 1) * p.G;
+    if (rows <= kStepRows) return launch_weigh_step(p, (int)rows, stream);
     Blocks w;
     w.tokens = (int)(mean < kTile / p.G ? (mean > 0 ? mean : 1) : kTile / p.G);
     w.cols = (w.tokens * p.G + 31) & ~31;

@@ -64,6 +64,23 @@ __device__ __forceinline__ long long cache_row(const CacheView &c, const int32_t
     return (((long long)page * c.H + h) << c.page_shift) + (j & ((1 << c.page_shift) - 1));
 }
 
+// Two e4m3 or int8 codes (16-bit halves of `x`, the code in the high byte) as bf16.  e4m3: its exponent and
+// mantissa moved to bf16's are the value times 2^-120.  int8, whose low 7 bits l and sign s make 128 + l (bits
+// 0x4300 | l) less 128 or, where s, 256.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t code_to_bf16x2(uint32_t x) {
+    uint32_t r;
+    if constexpr (kInt8) {
+        const uint32_t y = x >> 8;               // codes in the low bytes
+        const uint32_t a = (y & 0x007f007fu) | 0x43004300u, b = (y & 0x00800080u) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+        const uint32_t a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7b807b80u));   // 2^120
+    }
+    return r;
+}
+
 // 16 consecutive 32-bit columns of this thread's TMEM lane -> registers.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

@@ -273,6 +273,5 @@ __device__ __forceinline__ void schedule_role(const ChunkParams &p, const Layout
 }
 
 cudaError_t launch_prefill_rows(const ChunkParams &p, const Layout &w, cudaStream_t stream);
-cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t smem, void **args, cudaStream_t stream);
 
 }  // namespace bsattn

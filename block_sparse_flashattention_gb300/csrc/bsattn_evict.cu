@@ -9,9 +9,14 @@
 // piece of the positions once and keeps it in shared memory; histograms are summed through distributed shared
 // memory.  Then the positions of all keys above w* and of the first ones equal to it are written: every warp counts its
 // piece, and the counts before it, of the CTA's warps and of the CTAs before, give it its place in the list.
-// bsattn_evict_move_kernel moves rows.  To other pages every row is independent; within its own pages row i comes
-// from position kept[i] >= i, so one CTA per (sequence, head) goes through the rows in ascending blocks, each read
-// whole before it is written.
+// bsattn_evict_move_kernel moves rows to other pages, each independent of the others; bsattn_evict_close_kernel
+// moves them within their pages, in waves.
+//
+// HBM bounds it: 4 bytes per key, and 2 (2 D + 12) per row that is moved.  int8, D = 128, us a call, to other pages /
+// within the pages: a sequence of 131072 keys, 32 heads, keeping 32768 (536 MB of rows): 156 (select 50, move 93: 5.8
+// TB/s), 193; 8 heads: 74, 134; 64 sequences of 4096, 8 heads, keeping 1024 (268 MB): 83, 89; 8 of 32768 keeping 8192:
+// 85, 101.  With one CTA per (sequence, head) instead of clusters, the selection made it 625, 556, 83, 119, and the
+// rows within the pages 1412, 1176, 97, 394.
 #include "bsattn_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -21,7 +26,7 @@ namespace {
 
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32, kBins = 2048;
 constexpr int kMostKeys = 40960;             // of a CTA that shared memory holds; more are read again for every digit
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kCloseThreads = 512, kCloseRows = 4;   // rows that a thread has on their way
 constexpr uint32_t kForced = 0xffffffffu;
 
 // Weights as integers in the same order: NaN above all, -0 equal to 0.  kForced is none of them
@@ -235,7 +240,15 @@ __device__ __forceinline__ void store_row(const EvictParams &p, long long row, i
     if (piece == 0) p.c.ks[row] = x.ks, p.c.vs[row] = x.vs, p.weights[row] = x.w;
 }
 
-template <int D, bool kInPlace>
+// What goes from position `from` to place i.
+__device__ __forceinline__ void places(const EvictParams &p, const int32_t *table, const int32_t *out, int h, int from, int i,
+                                       long long &row, long long &to) {
+    row = row_at(p.c, table, h, from);
+    to = row_at(p.c, out, h, i);
+    if ((row < 0 || to < 0) && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+}
+
+template <int D>
 __global__ void __launch_bounds__(kMoveThreads) bsattn_evict_move_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kLanes = D / 16, kRows = kMoveThreads / kLanes;
     const int b = blockIdx.x / p.c.H, h = blockIdx.x - b * p.c.H, tid = threadIdx.x;
@@ -245,26 +258,58 @@ __global__ void __launch_bounds__(kMoveThreads) bsattn_evict_move_kernel(const _
     grid_launch_dependents();
     grid_dependency_wait();
     const Evicted s = sequence(p, b, false);
-    for (int i0 = blockIdx.y * kRows; i0 < s.m; i0 += gridDim.y * kRows) {
-        const int i = i0 + tid / kLanes;
-        const int from = i < s.m ? kept[i] : -1;
-        const bool move = from >= 0 && !(kInPlace && from == i);
-        Moved x;
-        long long to = -1;
-        if (move) {
-            const long long row = row_at(p.c, table, h, from);
-            to = row_at(p.c, out, h, i);
-            if ((row < 0 || to < 0) && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
-            x = load_row<D>(p, row, piece);
-        }
-        if (kInPlace) __syncthreads();
-        if (move) store_row<D>(p, to, piece, x);
+    for (int i = blockIdx.y * kRows + tid / kLanes; i < s.m; i += gridDim.y * kRows) {
+        const int from = kept[i];
+        if (from < 0) continue;
+        long long row, to;
+        places(p, table, out, h, from, i, row, to);
+        store_row<D>(p, to, piece, load_row<D>(p, row, piece));
     }
-    if (kInPlace)   // the places given up: their next keys' weights start at 0
-        for (int j = s.m + tid; j < s.n; j += kMoveThreads) {
-            const long long row = row_at(p.c, out, h, j);
-            if (row >= 0) p.weights[row] = 0.f;
+}
+
+// Within the pages: a cluster's CTAs read a wave of rows, meet, and write it.  Row i comes from kept[i] >= i, so what
+// a wave writes lies before all that later waves read.  512 threads of 4 rows each: with 2 rows the first of the cases
+// above is 221 us, with 256 threads of 8 rows 210.
+template <int D>
+__global__ void __launch_bounds__(kCloseThreads) bsattn_evict_close_kernel(const __grid_constant__ EvictParams p, int ranks) {
+    constexpr int kLanes = D / 16, kRows = kCloseThreads / kLanes;
+    const int seg = blockIdx.x / ranks, rank = blockIdx.x - seg * ranks;
+    const int b = seg / p.c.H, h = seg - b * p.c.H, tid = threadIdx.x;
+    const int32_t *table = p.table + (long long)b * p.table_stride;
+    const int32_t *kept = p.kept + ((long long)b * p.c.H + h) * p.keep;
+    const int piece = tid % kLanes;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const Evicted s = sequence(p, b, false);
+    const auto meet = [&] {
+        if (ranks > 1) cluster_sync();
+        else __syncthreads();
+    };
+    for (int i0 = 0; i0 < s.m; i0 += ranks * kRows * kCloseRows) {
+        Moved x[kCloseRows];
+        long long to[kCloseRows];
+        int from[kCloseRows];
+        const int i1 = i0 + rank * kRows * kCloseRows + tid / kLanes;
+#pragma unroll
+        for (int u = 0; u < kCloseRows; ++u) from[u] = i1 + u * kRows < s.m ? kept[i1 + u * kRows] : -1;
+#pragma unroll
+        for (int u = 0; u < kCloseRows; ++u) {
+            const int i = i1 + u * kRows;
+            to[u] = -1;
+            if (from[u] < 0 || from[u] == i) continue;
+            long long row;
+            places(p, table, table, h, from[u], i, row, to[u]);
+            x[u] = load_row<D>(p, row, piece);
         }
+        meet();
+#pragma unroll
+        for (int u = 0; u < kCloseRows; ++u) store_row<D>(p, to[u], piece, x[u]);
+    }
+    // the places given up: their next keys' weights start at 0
+    for (int j = s.m + rank * kCloseThreads + tid; j < s.n; j += ranks * kCloseThreads) {
+        const long long row = row_at(p.c, table, h, j);
+        if (row >= 0) p.weights[row] = 0.f;
+    }
 }
 
 cudaError_t launch_ex(const void *kernel, dim3 grid, int threads, size_t smem, int cluster, void **args, cudaStream_t stream) {
@@ -285,15 +330,20 @@ cudaError_t launch_ex(const void *kernel, dim3 grid, int threads, size_t smem, i
 }
 
 template <int D>
-cudaError_t launch_move(const EvictParams &p, cudaStream_t stream) {
+cudaError_t launch_move(const EvictParams &p, int sms, cudaStream_t stream) {
     constexpr int kRows = kMoveThreads / (D / 16);
     void *args[] = {const_cast<EvictParams *>(&p)};
     const unsigned segs = (unsigned)(p.B * p.c.H);
-    if (p.table == p.out_table)
-        return launch_ex(reinterpret_cast<const void *>(bsattn_evict_move_kernel<D, true>), dim3(segs), kMoveThreads, 0, 1, args, stream);
+    if (p.table == p.out_table) {
+        int close_ranks = 1;
+        while (close_ranks < 8 && (long long)segs * close_ranks <= sms && p.keep / close_ranks > 2 * (kCloseThreads / (D / 16)) * kCloseRows) close_ranks *= 2;
+        void *close_args[] = {const_cast<EvictParams *>(&p), &close_ranks};
+        return launch_ex(reinterpret_cast<const void *>(bsattn_evict_close_kernel<D>), dim3(segs * close_ranks), kCloseThreads, 0,
+                         close_ranks, close_args, stream);
+    }
     const long long room = min((long long)p.keep, (long long)p.table_cols << p.c.page_shift);
     const unsigned blocks = (unsigned)min((room + kRows - 1) / kRows, 1024ll);
-    return launch_ex(reinterpret_cast<const void *>(bsattn_evict_move_kernel<D, false>), dim3(segs, blocks), kMoveThreads, 0, 1, args, stream);
+    return launch_ex(reinterpret_cast<const void *>(bsattn_evict_move_kernel<D>), dim3(segs, blocks), kMoveThreads, 0, 1, args, stream);
 }
 
 }  // namespace
@@ -322,7 +372,7 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream) {
     e = launch_ex(reinterpret_cast<const void *>(bsattn_evict_select_kernel), dim3((unsigned)(segs * ranks)), kSelectThreads,
                   (size_t)room * 4, ranks, args, stream);
     if (e != cudaSuccess) return e;
-    return p.c.D == 128 ? launch_move<128>(p, stream) : launch_move<64>(p, stream);
+    return p.c.D == 128 ? launch_move<128>(p, sms, stream) : launch_move<64>(p, sms, stream);
 }
 
 }  // namespace bsattn

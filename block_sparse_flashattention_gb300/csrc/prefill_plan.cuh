@@ -76,11 +76,18 @@ struct Layout {
 
 // Which kernel takes a call: with few query rows a KV head (per sequence, on the average) the one that
 // widens codes in shared memory, for segments of up to 16, 32, 64 or 128 rows; else (0) the one that has them
-// widened into the workspace first.
-constexpr int kFewRows = 128;
-inline int segment_rows(int total, int B, int G) {
+// widened into the workspace first.  8 heads, e4m3, us a call there and here:
+//   rows                                   16        32        64        96       128
+//   D = 128, 16 sequences of 4096 keys   71, 172   78, 172  102, 176  142, 176  148, 178
+//   D = 128, 64 of 1000                  86, 178  101, 180  140, 182  201, 184  207, 186
+//   D = 64, 16 of 4096                   57, 122   63, 124   85, 129  124, 129  127, 131
+//   D = 64, 64 of 1000                   75, 131   88, 131  120, 133  179, 135  183, 138
+// Above 64 rows a segment's own cost counts: there, only where a CTA gets two at most.
+constexpr int kFewRows = 128, kFewSegs = 2 * kPrefillCtas;
+inline int segment_rows(int total, int B, int H, int G) {
     const long long mean = ((long long)total * G + B - 1) / B;
-    for (int rows = 16; rows <= kFewRows; rows *= 2)
+    const int most = (long long)B * H <= kFewSegs ? kFewRows : kFewRows / 2;
+    for (int rows = 16; rows <= most; rows *= 2)
         if (mean <= rows && G <= rows) return rows;
     return 0;
 }
@@ -92,7 +99,7 @@ constexpr int kPhaseVisits = 16;
 inline Layout make_layout(int total, int B, int H, int G, int D, long long keys, int ctas) {
     Layout w = {};
     w.tokens = kTile / G;
-    w.few = segment_rows(total, B, G);
+    w.few = segment_rows(total, B, H, G);
     w.step = w.few ? w.few / G : 2 * w.tokens;
     w.ctas = ctas;
     w.tiles = w.few ? 0 : keys / kTile + B;   // the other kernel widens in shared memory

@@ -2,12 +2,17 @@
 //
 // The lse is known, so that the softmax needs no pass of its own, and V is not read: D + 4 bytes per key and
 // KV head, 2 D flop and an exponential per query row on it.  From some 100 rows on the exponentials and the
-// products bound it, below that HBM.
+// products bound it, below that, in theory, HBM.  Calls of up to 32 rows a KV head are bsattn_weigh_step.cu's.
 //
 // Keys lie on the tensor cores' 128 rows and queries on their columns: S^T = K' Q^T with K' = bf16(code), exact,
 // and Q as it is.  A thread has one key, so that the sum over the queries stays in its registers: weight = sum_r
 // 2^(S_r c - lse_r log2(e)), c = ks softmax_scale log2(e).  The sum is fp32 within a block of 128 rows, and
 // compensated from block to block: thousands of rows cost no more accuracy than one block does.
+//
+// Measured: 2048 tokens on 33792 keys, 8 heads, G = 4, int8, D = 128: 466 us, 1.18 PFLOP/s, where the products would take
+// 281 and the exponentials 232; 64 tokens on 61440 keys, 24 heads, e4m3: 90 us, 2.2 TB/s.  There neither more units
+// on their way (3 instead of 2: 93 us) nor query blocks that stay from unit to unit (102, where it was 102) made a
+// difference; copies of a page instead of 16 keys did (95, 90), and fewer instructions for widening (102, 95).
 //
 // A unit is 256 keys of a (sequence, KV head): two tiles, one for each of two groups of 128 threads, whose blocks of
 // query rows are loaded once for both.  Units are handed out along a line on which each counts its blocks and
@@ -17,10 +22,11 @@
 // Roles (896 threads, one CTA per SM, all of TMEM):
 //   warp 0        issues the MMAs
 //   warp 1        owns the TMEM allocation; finds the CTA's units
-//   warp 2        fetches the codes of keys: bulk copies of 16 keys into raw tiles
+//   warp 2        fetches the codes of keys: bulk copies into raw tiles
 //   warp 3        query blocks (TMA) and their lse
 //   warps 4-7, 8-11, 12-15, 16-19   first halves of group 0 and 1, second halves: sums
 //   warps 20-27   widen the codes (128-byte swizzle)
+// Of few rows (kFew) a group has one half, and 16 warps widen.
 // TMEM: S^T of group g and buffer i: [256 g + 128 i, 256 g + 128 i + 128).
 #include "kv_codes.cuh"
 #include "prefill_plan.cuh"
@@ -34,12 +40,13 @@ constexpr uint32_t kTmemCols = 512;
 // 72 registers per thread at launch: 128 * 72 + 4 * 128 * 80 + 2 * 128 * 56 = 64512 = 896 * 72.
 constexpr int kLaunchRegs = 72;
 constexpr uint32_t kCtrlRegs = 72, kGroupRegs = 80, kWidenRegs = 56;
-static_assert(128 * kCtrlRegs + 512 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
+static_assert(128 * kCtrlRegs + 512 * kGroupRegs + 256 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs &&
+                  128 * kCtrlRegs + 256 * kGroupRegs + 512 * kWidenRegs <= (uint32_t)kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr int kSums = 4;                    // units whose half sums wait to be joined
 constexpr uint32_t kSub = kTile * 64 * 2;   // 128 rows x 64 bf16: one 128-byte swizzle span
 constexpr int kUnitKeys = 2 * kTile;
-constexpr int kUnitCost = 2;                // blocks that a unit's own work is worth
+constexpr int kUnitCost = 2;                // blocks that a unit's own work is worth (1, 2 and 4 measured alike)
 constexpr int kSeqChunk = 2048;             // sequences whose places fit shared memory at a time
 constexpr int kUnits = 2;                   // units found ahead
 // Mean query rows of a KV head up to which bsattn_weigh_step.cu is the faster one.  32 sequences of 4096 keys, 8 heads,
@@ -59,11 +66,14 @@ struct Unit {
     int32_t q0, q1;          // blocks that some of the keys are met by
 };
 
-// kFew: blocks of up to 64 rows, where HBM bounds the kernel: two units' codes on their way.  Else more blocks of
-// queries are, and the widened tiles are the two of a unit alone (with few, the next one's first is a third).
+// kFew: blocks of up to 64 rows.  Codes and their widening are what the kernel waits for: two units' codes on their
+// way, and the next unit's first tile widened ahead.  Else more blocks of queries are, and the widened tiles are the two
+// of a unit alone.  16 sequences of 4096 keys, 8 heads, 64 rows, us a call with this and without: D = 128, e4m3 44, 56;
+// D = 64, int8 35, 48.
 template <int D, bool kFew>
 struct Cfg {
     static constexpr int kTiles = kFew ? 3 : 2, kBlocks = kFew ? 2 : 3, kRaws = kFew ? (D == 128 ? 2 : 4) : 1;
+    static constexpr int kHalves = kFew ? 1 : 2, kGroupWarps = 8 * kHalves, kWidenWarps = 24 - kGroupWarps;
     static constexpr uint32_t kTileBytes = kTile * D * 2, kRawBytes = kTile * D;
     static constexpr uint32_t kBlockBytes = kFew ? kTileBytes / 2 : kTileBytes;
     static constexpr uint32_t kBlockSub = kFew ? kSub / 2 : kSub;    // 64 columns of a block
@@ -72,8 +82,8 @@ struct Cfg {
     static constexpr uint32_t kScale = kRaw + kRaws * 2 * kRawBytes; // key scales of the raw tiles
     static constexpr uint32_t kLse = kScale + kRaws * 1024;          // -lse log2(e) of the blocks' rows
     static constexpr uint32_t kRow = kLse + kBlocks * 512;           // cache rows of the raw tiles' 16-key groups, -1: none
-    static constexpr uint32_t kOdd = kRow + kRaws * 64;              // keys that have a NaN code, of four units
-    static constexpr uint32_t kSum = kOdd + 4 * 32;                  // sums of the groups' second halves
+    static constexpr uint32_t kOdd = kRow + kRaws * 64;              // keys that have a NaN code, of kSums units
+    static constexpr uint32_t kSum = kOdd + kSums * 32;                  // sums of the groups' second halves
     static constexpr uint32_t kUnit = kSum + kSums * 1024;
     static constexpr uint32_t kBar = kUnit + kUnits * (uint32_t)sizeof(Unit);
     // K' tiles full and empty, query blocks full and empty, S full and empty (2 group + buffer), raw units full and
@@ -83,6 +93,7 @@ struct Cfg {
                          bDrain = bUE + kUnits, kNumBars = bDrain + 1;
     static constexpr uint32_t kMisc = kBar + kNumBars * 8;           // [0] tmem base, [1] abort
     static constexpr uint32_t kAlloc = kMisc + 8;
+    static_assert(kUnits < kSums, "sums and odd keys of the units under way");
     static_assert(kAlloc <= 227u * 1024u, "shared memory");
 };
 
@@ -404,11 +415,11 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
         bool first = true;
         for (int q = x.q0; q < x.q1; ++q, ++it) {
             const uint32_t buf = it & 1u, blk = it % C::kBlocks;
-            if ((int)buf != half) continue;
+            if (C::kHalves == 2 && (int)buf != half) continue;
             ok = __all_sync(0xffffffffu, wait(C::bSF + 2 * g + (int)buf, it >> 1) && wait(C::bQF + (int)blk, it / C::kBlocks));
             if (!ok) break;
             tc_fence_after();
-            if (first && ((reinterpret_cast<const uint16_t *>(smem + C::kOdd)[16 * (ut & 3u) + 8 * g + 2 * quarter + (lane >> 4)] >> (lane & 15u)) & 1u))
+            if (first && ((reinterpret_cast<const uint16_t *>(smem + C::kOdd)[16 * (ut % kSums) + 8 * g + 2 * quarter + (lane >> 4)] >> (lane & 15u)) & 1u))
                 c = __uint_as_float(0x7fc00000u);
             first = false;
             // of the block: columns that meet the key; of none behind the sequence's last token
@@ -466,17 +477,19 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
         }
         if (!ok) break;
         if (x.q1 > x.q0) {
-            // the second half's sum goes to the first, which has the weight written; by the blocks' barriers it is at
-            // most two units ahead
-            const uint32_t at = ut % kSums, full = C::bHF + 2 * at + (uint32_t)g;
-            float *sums = reinterpret_cast<float *>(smem + C::kSum + at * 1024u);
-            if (half == 1) {
-                sums[key] = sum;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(wait.bar((int)full));
-            } else {
-                if (!__all_sync(0xffffffffu, wait((int)full, ut / kSums))) break;
-                sum += sums[key];
+            if constexpr (C::kHalves == 2) {
+                // the second half's sum goes to the first, which has the weight written; it is at most kUnits units
+                // ahead
+                const uint32_t at = ut % kSums, full = C::bHF + 2 * at + (uint32_t)g;
+                float *sums = reinterpret_cast<float *>(smem + C::kSum + at * 1024u);
+                if (half == 1) {
+                    sums[key] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(wait.bar((int)full));
+                } else {
+                    if (!__all_sync(0xffffffffu, wait((int)full, ut / kSums))) break;
+                    sum += sums[key];
+                }
             }
             ++ut;
         }
@@ -487,32 +500,34 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Blocks &w
     }
 }
 
-// Fetches the codes and scales of a unit's two tiles: copies of 16 keys (no page is smaller), none for keys past
-// the last or on a page that is none.
+// Fetches the codes and scales of a unit's two tiles: a copy per page or tile, none for keys past the last or on a
+// page that is none.
 template <int D, bool kFew>
 __device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &wait, int lane, uint32_t base, uint8_t *smem) {
     using C = Cfg<D, kFew>;
     uint32_t units = 0, it = 0;
     bool ok = true;
+    const int shift = min(p.c.page_shift, 7);    // keys of a copy
     Unit x;
     while (ok && next_unit<C>(wait, smem, units, x)) {
         const int32_t *table = p.table + (long long)x.b * p.table_stride;
-        const int key = x.key0 + 16 * lane;
+        const int key = x.key0 + (lane << shift);
         long long row = -1;
-        if (lane < 16 && key < x.n) {
+        if (lane < kUnitKeys >> shift && key < x.n) {
             row = cache_row(p.c, table, x.h, key);
             if (row < 0 && p.err) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
         }
         if (x.q1 == x.q0) continue;              // no query meets them
         const uint32_t on = __ballot_sync(0xffffffffu, row >= 0), raw = it % C::kRaws;
         if (!(ok = __all_sync(0xffffffffu, wait(C::bRE + (int)raw, (it / C::kRaws) ^ 1u)))) break;
-        if (lane < 16) reinterpret_cast<int *>(smem + C::kRow + raw * 64u)[lane] = (int)row;
+        const int whole = __shfl_sync(0xffffffffu, (int)row, (16 * lane & (kUnitKeys - 1)) >> shift);
+        if (lane < 16) reinterpret_cast<int *>(smem + C::kRow + raw * 64u)[lane] = whole < 0 ? -1 : whole + (16 * lane & ((1 << shift) - 1));
         __syncwarp();
         const uint32_t full = wait.bar(C::bRF + (int)raw), lead = row >= 0 ? 1u : 0u;
-        mbar_arrive_expect_tx_lead(lane == 0 ? 1u : 0u, full, (uint32_t)__popc(on) * (16u * D + 64u));
+        mbar_arrive_expect_tx_lead(lane == 0 ? 1u : 0u, full, ((uint32_t)__popc(on) * (D + 4u)) << shift);
         __syncwarp();
-        bulk_g2s_lead(lead, base + C::kRaw + raw * 2u * C::kRawBytes + (uint32_t)lane * 16u * D, p.c.k + row * D, 16u * D, full);
-        bulk_g2s_lead(lead, base + C::kScale + raw * 1024u + (uint32_t)lane * 64u, p.c.ks + row, 64u, full);
+        bulk_g2s_lead(lead, base + C::kRaw + raw * 2u * C::kRawBytes + ((uint32_t)lane * D << shift), p.c.k + row * D, (uint32_t)D << shift, full);
+        bulk_g2s_lead(lead, base + C::kScale + raw * 1024u + ((uint32_t)lane * 4u << shift), p.c.ks + row, 4u << shift, full);
         ++it;
     }
     // nothing may be on its way into a tile when the CTA ends
@@ -523,10 +538,11 @@ __device__ __forceinline__ void fetch_role(const ChunkParams &p, const Waiter &w
 // Widens the codes of tiles, eight warps each, 16 keys a warp.  Lane: 16 codes of a row, two swizzle pieces; D / 16
 // lanes to a row.  What no copy has filled is left: such keys are masked.
 template <int D, bool kFew, bool kInt8>
-__device__ __forceinline__ void widen_role(const Waiter &wait, int warp, int lane, uint8_t *smem) {
+__device__ __forceinline__ void widen_role(const Waiter &wait, int widener, int lane, uint8_t *smem) {
     using C = Cfg<D, kFew>;
     constexpr int kRowLanes = D / 16, kAtOnce = 32 / kRowLanes, kSteps = 16 / kAtOnce;
-    const int col = lane % kRowLanes, sub_row = lane / kRowLanes;
+    constexpr uint32_t kEach = 2 * 8 / C::kWidenWarps;    // tiles of a unit that a warp works on
+    const int warp = widener & 7, col = lane % kRowLanes, sub_row = lane / kRowLanes;
     // Eight lanes store 128 bytes at a time; where they share a row, half of them begin with their second
     // piece: every bank once.
     const bool swap = D == 128 && col >= 4;
@@ -540,8 +556,8 @@ __device__ __forceinline__ void widen_role(const Waiter &wait, int warp, int lan
         const uint32_t rs = it % C::kRaws;
         bool ok = wait(C::bRF + (int)rs, it / C::kRaws);
 #pragma unroll 1
-        for (uint32_t g = 0; g < 2; ++g) {
-            const uint32_t tile = 2 * it + g, stage = tile % C::kTiles;
+        for (uint32_t n = 0; n < kEach; ++n) {
+            const uint32_t g = kEach == 2 ? n : (uint32_t)widener >> 3, tile = 2 * it + g, stage = tile % C::kTiles;
             const uint8_t *from = raw + (rs * 2u + g) * C::kRawBytes;
             uint4 v[kSteps];
             if (!__all_sync(0xffffffffu, ok)) return;
@@ -570,14 +586,14 @@ __device__ __forceinline__ void widen_role(const Waiter &wait, int warp, int lan
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        o[2 * k] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x1404));
-                        o[2 * k + 1] = code_to_bf16x2<kInt8>(__byte_perm(y[2 * q + k], 0u, 0x3424));
+                        o[2 * k] = codes_to_bf16x2<kInt8, false>(y[2 * q + k]);
+                        o[2 * k + 1] = codes_to_bf16x2<kInt8, true>(y[2 * q + k]);
                     }
                     *reinterpret_cast<uint4 *>(to + i * kAtOnce * 128 + (((q ? second : first) ^ r7) << 4)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            if (lane == 0) reinterpret_cast<uint16_t *>(smem + C::kOdd)[16 * (it & 3u) + 8 * g + warp] = (uint16_t)odd;
+            if (lane == 0) reinterpret_cast<uint16_t *>(smem + C::kOdd)[16 * (it % kSums) + 8 * g + warp] = (uint16_t)odd;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(wait.bar(C::bKF + (int)stage));
@@ -741,12 +757,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // nothing may be on its way into shared memory when the CTA ends
         for (uint32_t s = 0; s < (uint32_t)C::kBlocks; ++s)
             if (it > s) mbar_wait_drain(wait.bar(C::bQF + (int)s), ((it - 1 - s) / C::kBlocks) & 1u);
-    } else if (warp < 20) {
+    } else if (warp < 4 + C::kGroupWarps) {
         regs_claim<kGroupRegs>();
         group_role<D, kFew>(p, w, wait, tmem, (int)(warp >> 2 & 1u) ^ 1, (int)(warp - 4) >> 3, warp, lane, smem);
     } else {
         regs_release<kWidenRegs>();
-        widen_role<D, kFew, kInt8>(wait, (int)warp - 20, (int)lane, smem);
+        widen_role<D, kFew, kInt8>(wait, (int)warp - 4 - C::kGroupWarps, (int)lane, smem);
     }
     tc_fence_before();
     __syncthreads();

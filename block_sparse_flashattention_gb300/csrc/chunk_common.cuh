@@ -64,19 +64,19 @@ __device__ __forceinline__ long long cache_row(const CacheView &c, const int32_t
     return (((long long)page * c.H + h) << c.page_shift) + (j & ((1 << c.page_shift) - 1));
 }
 
-// Two e4m3 or int8 codes (16-bit halves of `x`, the code in the high byte) as bf16.  e4m3: its exponent and
-// mantissa moved to bf16's are the value times 2^-120.  int8, whose low 7 bits l and sign s make 128 + l (bits
+// Codes 0 and 1 (or 2 and 3) of four as bf16, exact.  e4m3: under a sign-extended byte shifted by 4 its exponent and
+// mantissa lie where bf16 has its lowest, the value times 2^-120.  int8, whose low 7 bits l and sign s make 128 + l (bits
 // 0x4300 | l) less 128 or, where s, 256.
-template <bool kInt8>
-__device__ __forceinline__ uint32_t code_to_bf16x2(uint32_t x) {
+template <bool kInt8, bool kUpper>
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x) {
     uint32_t r;
     if constexpr (kInt8) {
-        const uint32_t y = x >> 8;               // codes in the low bytes
-        const uint32_t a = (y & 0x007f007fu) | 0x43004300u, b = (y & 0x00800080u) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        const uint32_t y = __byte_perm(x, 0x43434343u, kUpper ? 0x4342 : 0x4140);
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y & 0xff7fff7fu), "r"(y & 0xff80ff80u));
     } else {
-        const uint32_t a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7b807b80u));   // 2^120
+        uint32_t y;
+        asm("prmt.b32 %0, %1, %1, %2;" : "=r"(y) : "r"(x), "n"(kUpper ? 0xb3a2 : 0x9180));   // 8 + i: the sign of byte i
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((y << 4) & 0x87f087f0u), "r"(0x7b807b80u));   // 2^120
     }
     return r;
 }

@@ -344,6 +344,7 @@ bsattn_status bsattn_kv_evict(const bsattn_kv_cache *cache, float *weights, cons
     bsattn::EvictParams p = {};
     if (out_table) {
         if ((st = check_table(out_table, out_stride, out_cols, cache->page_size, false)) != BSATTN_OK) return st;
+        if (out_table == page_table && B > 1 && out_stride != table_stride) return BSATTN_ERR_INVALID_ARG;
         // room for every key that may be kept
         if (out_cols < table_cols && (long long)out_cols * cache->page_size < keep) return BSATTN_ERR_INVALID_ARG;
         p.out_table = out_table;

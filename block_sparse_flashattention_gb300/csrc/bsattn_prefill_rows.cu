@@ -17,6 +17,12 @@
 // Up to 64 rows two groups of threads take the tiles in turn, each with sums of its own, joined at the end: while
 // one group's weights are formed, the other's products run.  With more, each group has 64 of the rows.
 //
+// Measured (us a call, cold L2): 8 sequences of 100 to 4096 keys with drafts of 4 tokens, 8 heads x 4, e4m3, D = 128: 29
+// (35 MB: 5.3 at the copy's rate), of which the join 6.5; 16 sequences of 4096 keys, 8 heads (142 MB: 21): 16 rows 71,
+// 32 78, 64 102, 128 148.  Before a CTA's first product lie 6000 cycles for its piece of the line, 1300 for query rows,
+// 3000 to 5000 for the first codes; then a tile takes some 3000, of which HBM's latency behind a ring of two is the
+// largest part.  Copies of a page in place of 16 keys made no difference.
+//
 // Roles (640 threads, one CTA per SM):
 //   warp 0        issues the MMAs
 //   warp 1        owns the TMEM allocation; finds the segments of the CTA's piece of the line
@@ -117,7 +123,9 @@ __device__ __forceinline__ int tile_of(const SegDesc &d, int k) { return k < d.s
 
 // The line of work of this kernel is numbered by every CTA for itself (lengths are on the device): places of
 // one head's pass over a sequence's segments.
-constexpr int kRowsCost = 4;                // places that starting and ending a segment costs
+// Places that starting and ending a segment costs.  Drafts of 4 tokens, 8 sequences, us a call: 30.1 with 1, 29.4 with 2,
+// 29.0 with 3, 30.6 with 4, 32.2 with 8; 64 sequences of 1000 keys, 8 heads, 64 rows: 153 with 1, 150 with 2, 141 with 4.
+constexpr int kRowsCost = 3;
 
 __device__ __forceinline__ int segment_tiles(const ChunkParams &p, const Layout &w, const Chunk &c, int r) {
     if (c.n <= 0) return 0;

@@ -8,7 +8,9 @@
 namespace bsattn {
 
 constexpr int kPrefillCtas = 160;
-constexpr int kSegCost = 2;                 // places of the line that starting and ending a segment costs
+// Places of the line that starting and ending a segment costs.  Prompts of 100 to 4096 tokens, 16 heads, D = 64, us a
+// call: 225 with 1, 217 with 2, 223 with 4; 16 sequences with 1 to 512 new tokens: 245, 244, 247.
+constexpr int kSegCost = 2;
 constexpr int kLeastPiece = 4;              // places of a piece: each makes parts for the join
 constexpr int kDescs = 2;                   // segments found ahead
 constexpr float kNoKey = -0x1p100f;         // reference before the first key
@@ -92,7 +94,9 @@ inline int segment_rows(int total, int B, int H, int G) {
     return 0;
 }
 
-// Widened bytes that the CTAs work on at a time: of 129 MB of L2, less what else passes through.
+// Widened bytes that the CTAs work on at a time: of 129 MB of L2, less what else passes through.  2048 tokens on
+// 63488 keys, 8 heads x 4, us a call: 1736 with 64 MB, 1760 with 128, 1768 without phases; 4096 tokens in a window of
+// 4096, 32 heads: 341, 336, 332.
 constexpr long long kPhaseBytes = 64ll << 20;
 constexpr int kPhaseVisits = 16;
 

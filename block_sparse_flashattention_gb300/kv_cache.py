@@ -1,11 +1,12 @@
 """The paged 8-bit K/V cache, the attention of single query tokens and of chunks over it, and its eviction.
 
 ``kv_append`` quantises new K and V rows into a cache's pages, ``kv_read`` reads
-them back as packed bf16 rows (what ``forward`` takes), ``decode`` attends one query token per sequence over them, and
-``decode_shared_prefix`` does so for a batch behind one common prefix, and ``prefill`` for
-chunks of new tokens; ``kv_weigh`` sums the weight that queries give to every key, and
-``kv_evict`` keeps the keys of most weight.  These are calls of the C functions of the same names (bsattn_*, include/bsattn.h, where the
-formats and faults are described) with torch checks and allocations around them.
+them back as packed bf16 rows (what ``forward`` takes).  ``decode`` attends one query token per
+sequence over them, ``decode_shared_prefix`` does so for a batch behind one common prefix, and
+``prefill`` for chunks of new tokens.  ``kv_weigh`` sums the weight that queries give to every key,
+and ``kv_evict`` keeps the keys of most weight.  These are calls of the C functions of the same
+names (bsattn_*, include/bsattn.h, where the formats and faults are described) with torch checks
+and allocations around them.
 
     cache = bsa.alloc_kv_cache(num_pages, H, D)                 # e4m3, pages of 128
     bsa.kv_append(k, v, cache, page_table, seqlens)             # k, v [B, H, D]: a token each
@@ -220,7 +221,8 @@ def kv_read(cache: KVCache, page_table, cu_seqlens, *, total=None, k=None, v=Non
     total: rows to allocate when k and v are not given (cu_seqlens[-1], which lives on
     the device); rows outside every sequence are not written.
 
-    A causal prefill of new tokens over cached context: ``forward`` counts query positions
+    New tokens over cached context are ``prefill``'s; where they are to meet listed tiles alone,
+    ``forward`` takes the rows read back.  It counts query positions
     from 0 in every sequence, so give it query rows for the context's positions too (of any
     content) and list nothing for their Q tiles; repeat k and v along their heads
     (repeat_interleave) where query heads are grouped."""
@@ -411,7 +413,7 @@ def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_
 
 
 def alloc_prefill_workspace(cache: KVCache, total: int, B: int, Hq: int, keys: int):
-    """Workspace of a ``prefill`` call for `total` query tokens of B sequences, Hq query heads and
+    """Workspace of a ``prefill`` call for up to `total` query tokens of B sequences, Hq query heads and
     up to `keys` cached keys of all sequences together.  It can be kept from call to call; two
     calls that may run at the same time need one each."""
     return torch.empty(bsattn_prefill_workspace_size(cache.ref, total, B, Hq, keys), dtype=torch.uint8,
@@ -559,7 +561,7 @@ def kv_evict(cache: KVCache, weights, page_table, seqlens, keep: int, *, recent:
     out_table None: within the sequence's own pages; the weights of the positions given up become 0.
     The pages that are moved must not be another sequence's too.  Else int32 [B, pages]: to these
     other pages, for every sequence, short ones whole; page_table's pages are only read, so that
-    several sequences may share them.  Returns (kept int32 [B, H, keep]: the positions that stay, -1
+    several sequences may share them, and none of them may be in out_table, nor a page there twice.  Returns (kept int32 [B, H, keep]: the positions that stay, -1
     behind the last; lens int32 [B]: the keys that the sequences have now)."""
     if _calls is not None and stream is None and err_flag is None:
         got = _calls.kv_evict(cache.at, cache.index, weights, page_table, seqlens, keep, recent, sinks, out_table)

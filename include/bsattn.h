@@ -505,7 +505,8 @@ bsattn_status bsattn_kv_append(const void *k, const void *v, int64_t k_stride, i
  * bsattn_fwd takes: rows cu_seqlens[b] .. cu_seqlens[b+1] of k and v receive
  * positions 0, 1, ... of sequence b, each element code * scale in fp32, rounded to
  * bf16 (to nearest even).  Rows with a power-of-two scale, as e4m3 rows have, are
- * read back exactly.  For a causal prefill of new tokens over cached context: bsattn_fwd
+ * read back exactly.  New tokens over cached context are bsattn_prefill's; where they are to meet
+ * listed tiles alone, bsattn_fwd takes the rows read back.  It
  * counts query positions from 0 in every sequence, so q takes rows for the context's
  * positions too (of any content), whose Q tiles list nothing; and it has one KV head per
  * query head, so that K and V of grouped heads are repeated first.
@@ -617,8 +618,8 @@ bsattn_status bsattn_decode_workspace_size(const bsattn_kv_cache *cache, int32_t
  * page_table, table_stride, table_cols   as for bsattn_kv_append.
  * seqlens      device int32 [B]; <= 0: no key.
  * keys         the sum of all seqlens (of those above 0), or more: the workspace has room for a
- *              copy of so many keys.  Sequences that have no room left are not written,
- *              BSATTN_FLAG_BAD_SEQLENS.
+ *              copy of so many keys, which calls of many query rows make.  There, sequences that
+ *              have no room left are not written, BSATTN_FLAG_BAD_SEQLENS.
  * kind, mp     BSATTN_MASK_NONE, _CAUSAL, _SLIDING_WINDOW or _PREFIX; BSATTN_MASK_DOCUMENT ->
  *              BSATTN_ERR_UNSUPPORTED (its ids belong to packed keys).
  * A sequence whose offsets leave [0, total] or decrease, that has more new tokens than
@@ -640,9 +641,9 @@ bsattn_status bsattn_prefill(const void *q, int64_t q_stride, int32_t total, int
                              size_t workspace_bytes, int32_t *err_flag, void *stream);
 
 /*
- * bsattn_prefill_workspace_size -- bytes of workspace that bsattn_prefill needs for `total` query
- * tokens of B sequences, Hq query heads, `keys` cached keys and a cache of this shape (its pointers
- * are not looked at).
+ * bsattn_prefill_workspace_size -- bytes of workspace that bsattn_prefill needs for up to `total` query
+ * tokens of B sequences, Hq query heads, up to `keys` cached keys and a cache of this shape (its pointers
+ * are not looked at).  For fewer sequences more may be needed.
  */
 bsattn_status bsattn_prefill_workspace_size(const bsattn_kv_cache *cache, int32_t total, int32_t B,
                                             int32_t Hq, int64_t keys, size_t *bytes);
@@ -683,7 +684,8 @@ bsattn_status bsattn_kv_weigh(const void *q, int64_t q_stride, const float *lse,
  * weights      as for bsattn_kv_weigh.
  * keep         > 0; recent, sinks >= 0, together at most keep.
  * out_table    device int32, B rows of out_cols entries, out_stride apart: the pages to move to,
- *              room for min(keep, table_cols * page_size) keys.  None of the pages it names may be in
+ *              room for min(keep, table_cols * page_size) keys (page_table itself: out_stride ==
+ *              table_stride).  None of the pages it names may be in
  *              page_table's rows or named twice; page_table's pages are only read.  NULL, or
  *              page_table itself: rows move within their sequence's own pages, and the weights at the
  *              positions min(n, keep) .. n - 1 become 0.  Then no page that is moved may be

@@ -144,3 +144,19 @@ def test_evict_checks_tensors(kw):
     a.pop("q"), a.pop("cu_seqlens")
     with pytest.raises(ValueError):
         bsa.kv_evict(**{**a, "weights": torch.zeros(4, 2, 16), "keep": 10, **kw})
+
+
+@pytest.mark.parametrize("H,G,D,B", [(1, 1, 64, 1), (8, 4, 128, 8), (32, 1, 64, 300), (2, 64, 128, 5), (4, 7, 64, 64), (8, 128, 128, 3)])
+def test_a_workspace_serves_fewer_tokens_and_keys(H, G, D, B):
+    """Bytes never fall with the tokens or keys of a call."""
+    cache = _cache(H=H, D=D)
+    last = 0
+    for total in sorted({*range(0, 70), *(B * k + d for k in (1, 2, 4, 8, 16, 32, 64, 128) for d in (-1, 0, 1)),
+                         *(B * k // G + d for k in (16, 32, 64, 128) for d in (0, 1)), 1000, 5000, 20000}):
+        n = [bsa.bsattn_prefill_workspace_size(cache, total, B, H * G, keys) for keys in (0, 300, 40000)]
+        assert n == sorted(n) and n[1] >= last
+        last = n[1]
+
+
+def test_evict_the_same_table_by_other_strides():
+    assert _evict(out_table=FAKE, out_stride=3, out_cols=2) == INV

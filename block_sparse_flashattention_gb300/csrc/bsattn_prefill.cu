@@ -112,7 +112,13 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
             s.m = s.blocks = s.sinks = s.near = s.end = 0;
         }
         tiles += sum;
-        s.block0 = (int)(blocks + block_scan(s.blocks, &sum, warps));
+        const long long block0 = blocks + block_scan(s.blocks, &sum, warps);
+        s.block0 = (int)min(block0, (long long)INT32_MAX);
+        if (s.blocks > 0 && block0 + s.blocks > w.blocks) {
+            // offsets that decrease in between: more rows than there are
+            if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
+            s.m = s.blocks = s.sinks = s.near = s.end = 0;
+        }
         blocks += sum;
         if (b < p.B) seq[b] = s;
     }
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
     // places of the row blocks within a head's pass over them: a warp per sequence
     for (int b = tid / 32; b < p.B; b += kPlanThreads / 32) {
         const SeqPlan s = seq[b];
-        int sum = 0;
+        long long sum = 0;
         for (int r0 = 0; r0 < s.blocks; r0 += 32) {
             const int r = r0 + lane;
             int x = 0;
@@ -133,10 +139,16 @@ __global__ void __launch_bounds__(kPlanThreads) bsattn_prefill_plan_kernel(const
                 const int z = __shfl_up_sync(0xffffffffu, y, d);
                 if (lane >= d) y += z;
             }
-            if (r < s.blocks) place[s.block0 + r] = sum + y - x;
+            if (r < s.blocks) place[s.block0 + r] = (int)min(sum + y - x, (long long)INT32_MAX);
             sum += __shfl_sync(0xffffffffu, y, 31);
         }
-        if (lane == 0) seq[b].pass = sum;
+        if (lane == 0 && sum > INT32_MAX) {
+            // a head's pass is numbered in 32 bits
+            if (p.err) atomicOr(p.err, BSATTN_FLAG_BAD_SEQLENS);
+            seq[b].m = seq[b].blocks = 0;
+            sum = 0;
+        }
+        if (lane == 0) seq[b].pass = (int)sum;
     }
     __syncthreads();
     long long places = 0;

@@ -623,8 +623,9 @@ bsattn_status bsattn_decode_workspace_size(const bsattn_kv_cache *cache, int32_t
  * kind, mp     BSATTN_MASK_NONE, _CAUSAL, _SLIDING_WINDOW or _PREFIX; BSATTN_MASK_DOCUMENT ->
  *              BSATTN_ERR_UNSUPPORTED (its ids belong to packed keys).
  * A sequence whose offsets leave [0, total] or decrease, that has more new tokens than
- * seqlens[b] (above 0), or that outgrows its table row: none of its rows is written,
- * BSATTN_FLAG_BAD_SEQLENS.  A page outside [0, num_pages): its keys are left out,
+ * seqlens[b] (above 0), that outgrows its table row, or whose rows of a KV head (tokens times query
+ * heads) times keys pass 2^45: none of its rows is written, BSATTN_FLAG_BAD_SEQLENS.  Behind offsets that decrease, others may be left out
+ * with the same flag, or write the same rows.  A page outside [0, num_pages): its keys are left out,
  * BSATTN_FLAG_BAD_INDEX.  Rows outside every sequence's range are left as they were.
  * out          device, [total, Hq, D] contiguous, 16-byte aligned, out_dtype.
  * lse          device fp32 [total, Hq].

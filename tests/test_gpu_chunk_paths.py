@@ -296,3 +296,21 @@ def test_replayed_with_other_lengths(m):
         ref = c.expect()
         agree(out[:end], lse[:end], tuple(x[:end] for x in ref))
         _near(w, c.expect_weights(lse))
+
+
+@pytest.mark.parametrize("m", [2, 100, 300])
+def test_offsets_that_go_back_and_forth(m):
+    """Sequences that claim the same rows over and over: flagged, and nothing outside the workspace is written."""
+    B = 64
+    c = Chunks(40, "e4m3", 1, 2, 64, 16, [320] * B, [m] + [0] * (B - 1))
+    cu = i32([0 if b % 2 == 0 else m for b in range(B + 1)])
+    n = bsa.bsattn_prefill_workspace_size(c.pool.cache.ref, m, B, 2, 320 * B)
+    buf = torch.full((n + (1 << 20),), 77, dtype=torch.uint8, device="cuda")
+    wide = torch.full((m + 8, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    err = i32([0])
+    bsa.prefill(c.q, c.pool.cache, c.table, c.seqlens, cu, keys=320 * B, workspace=buf[:n], out=wide[:m], err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == bsa.FLAG_BAD_SEQLENS
+    assert (buf[n:] == 77).all() and (wide[m:] == 5).all()
+    w, err = _weigh(c, torch.zeros(m, 2, device="cuda"), cu_seqlens=cu)
+    assert err == bsa.FLAG_BAD_SEQLENS

@@ -107,7 +107,7 @@ def test_rows_of_no_sequence_stay():
 def test_faulty_sequences_are_left_and_flagged():
     c = Chunks(45, "int8", 2, 2, 128, 32, [200, 100, 64, 90], [30, 40, 64, 10])
     base_o, base_l, _ = _run(c, out_dtype=torch.float32)
-    first = c.first
+    first, ref = c.first, c.expect()
     for lens, cu in [([200, 39, 64, 90], None),                             # more new tokens than keys
                      ([200, c.table.shape[1] * 32 + 1, 64, 90], None),      # outgrows the table
                      (c.lens, [0, 30, 20, 134, 144]),                       # offsets decrease
@@ -124,7 +124,9 @@ def test_faulty_sequences_are_left_and_flagged():
             same = off[b] == first[b] and off[b + 1] == first[b + 1]
             r = slice(first[b], first[b + 1])
             if good and same:
-                assert torch.equal(out[r], base_o[r]) and torch.equal(lse[r], base_l[r])
+                # What the others are worth moves the places where this sequence's keys are divided, and with
+                # them the order of its sums: each division is within the tolerance that any order has.
+                agree(out[r], lse[r], tuple(x[r] for x in ref))
             elif not good and cu is None:
                 assert (out[r] == 7).all() and (lse[r] == 7).all()
 

@@ -692,7 +692,7 @@ bsattn_status bsattn_kv_weigh(const void *q, int64_t q_stride, const float *lse,
  *              positions min(n, keep) .. n - 1 become 0.  Then no page that is moved may be
  *              another sequence's too.
  * kept         device int32 [B, H, keep]: the positions that stay, ascending, then -1.
- * lens         device int32 [B]: min(seqlens[b], keep), 0 for seqlens[b] <= 0.
+ * lens         device int32 [B], not seqlens itself: min(seqlens[b], keep), 0 for seqlens[b] <= 0.
  * A row read from a page outside [0, num_pages) moves as zeros; one that would go to such a page is
  * not moved; both BSATTN_FLAG_BAD_INDEX.  A sequence that outgrows its row of page_table is not
  * moved: lens 0, kept -1, BSATTN_FLAG_BAD_SEQLENS.  All else in the cache is left as it was.

@@ -17,8 +17,8 @@
 // Up to 64 rows two groups of threads take the tiles in turn, each with sums of its own, joined at the end: while
 // one group's weights are formed, the other's products run.  With more, each group has 64 of the rows.
 //
-// Measured (us a call, cold L2): 8 sequences of 100 to 4096 keys with drafts of 4 tokens, 8 heads x 4, e4m3, D = 128: 29
-// (35 MB: 5.3 at the copy's rate), of which the join 6.5; 16 sequences of 4096 keys, 8 heads (142 MB: 21): 16 rows 71,
+// Measured (us a call, cold L2): 8 sequences of 100 to 4096 keys with drafts of 4 tokens, 8 heads x 4, e4m3, D = 128: 28
+// (35 MB: 5.3 at the copy's rate), of which the join 5.5; 16 sequences of 4096 keys, 8 heads (142 MB: 21): 16 rows 71,
 // 32 78, 64 102, 128 148.  Before a CTA's first product lie 6000 cycles for its piece of the line, 1300 for query rows,
 // 3000 to 5000 for the first codes; then a tile takes some 3000, of which HBM's latency behind a ring of two is the
 // largest part.  Copies of a page in place of 16 keys made no difference.

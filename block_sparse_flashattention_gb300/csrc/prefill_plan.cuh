@@ -11,7 +11,10 @@ constexpr int kPrefillCtas = 160;
 // Places of the line that starting and ending a segment costs.  Prompts of 100 to 4096 tokens, 16 heads, D = 64, us a
 // call: 225 with 1, 217 with 2, 223 with 4; 16 sequences with 1 to 512 new tokens: 245, 244, 247.
 constexpr int kSegCost = 2;
-constexpr int kLeastPiece = 4;              // places of a piece: each makes parts for the join
+// Places of a piece: each makes parts for the join, but where the line is short CTAs are free.  5 sequences of 10 to 243
+// keys with 7 or 8 new tokens, 3 heads x 6, us a call: 18.7 with 1, 20.1 with 2, 29.1 with 4; 2 of 6 keys, 20 heads: 12.9,
+// 11.4, 11.4.
+constexpr int kLeastPiece = 2;
 constexpr int kDescs = 2;                   // segments found ahead
 constexpr float kNoKey = -0x1p100f;         // reference before the first key
 

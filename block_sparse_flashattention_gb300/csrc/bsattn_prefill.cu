@@ -13,7 +13,7 @@
 // With z_j the scores in units of log2: p_j = 2^(z_j - m + 7) is rounded to fp16 (11 bits) for P V',
 // l sums it in fp32; out = O 2^(E - 6) / l, lse = ln 2 (m - 7 + log2 l).  The reference m is moved
 // only when some weight could pass 2^15 (the output is then rescaled), and O is rescaled to
-// another E only where it is larger or more than 2^8 smaller.
+// another E only where it is larger or more than 2^8 smaller, then no further than O stays below 2^100.
 //
 // Work.  A segment is (sequence, KV head, block of 2 x floor(128 / G) tokens): two 128-row
 // tiles ("slots") that share each K/V tile.  It visits the key tiles that its rows meet: all up to
@@ -59,7 +59,8 @@ constexpr int kPlanThreads = 1024, kWidenThreads = 256, kJoinThreads = 256;
 // (2^(E - 6) and its inverse are then normal numbers).
 constexpr int kLeastKey = 27, kMostKey = 227, kLeastValue = 7, kMostValue = 254;
 constexpr float kLift = 7.f, kReach = 8.f;
-
+// Binary exponent below which O stays where another E moves it up: 2^24 tiles of 2^38 each may still be added.
+constexpr int kMostO = 100;
 
 // ------------------------------------------------------------------- plan --
 
@@ -491,19 +492,45 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                 alpha = ex2_approx(m_run - m_new);
                 m_run = m_new;
             }
-            // the tile's E against that of O: a little smaller, and the weights make up for it
-            const int below = exp_run - info.x;
-            int shift = 0;
+            // The tile's E against that of O: a little smaller, and the weights make up for it (unit), else O moves.  Down
+            // only as far as O stays below 2^kMostO (tiles without values, whose E is the lowest, may follow one another): where
+            // that is not all the way, the tile's values are so far below what O holds that their weights' lost bits
+            // are too.
+            float f = alpha, unit = 1.f;
+            bool rescale = begun && grew, scaled = false;   // the same for the whole warp
             if (!begun) exp_run = info.x;
-            else if (below < 0 || below > 8) shift = min(below, 60), exp_run -= shift;
-            const float unit = pow2(info.x - exp_run);
-            const bool rescale = begun && (grew || shift != 0);
+            if (__builtin_expect(__any_sync(0xffffffffu, exp_run != info.x), 0)) {
+                const int below = exp_run - info.x;
+                if (__any_sync(0xffffffffu, below < 0 || below > 8)) {
+                    int room = below;
+                    if (__any_sync(0xffffffffu, below > 8)) {
+                        // S of this tile was issued after the slot's previous P V: O is up to date
+                        float top_o = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c) {
+                            uint32_t v[8];
+                            tmem_ld8(lane_addr + o_col + 8u * c, v);
+                            tmem_wait_ld();
+                            reg_fence(v);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) top_o = fmaxf(top_o, fabsf(__uint_as_float(v[x])));
+                        }
+                        top_o *= alpha;
+                        // below 2^-27 it counts as 0 beside what weighs most
+                        if (!(top_o < 0x1p-27f)) room = max(127 + kMostO - (int)(__float_as_uint(top_o) >> 23), 0);
+                    }
+                    const int shift = below > 8 ? min(below, room) : min(below, 0);
+                    exp_run -= shift;
+                    f *= pow2(shift);
+                    rescale = begun;
+                }
+                unit = pow2(info.x - exp_run);
+                scaled = __any_sync(0xffffffffu, unit != 1.f);
+            }
             const float nm = kLift - m_run;
             float la0 = 0.f, la1 = 0.f, lb0 = 0.f, lb1 = 0.f;
             auto rescale_output = [&] {
                 if (!rescale) return;
-                // S of this tile was issued after the slot's previous P V: O is up to date
-                const float f = alpha * pow2(shift);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
@@ -537,7 +564,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                     else fadd2(la0, la1, la0, la1, p0, p1);
                     pk[x] = pack_f16x2(p0, p1);
                 }
-                if (__builtin_expect(unit != 1.f, 0)) {   // a power of two below 1
+                if (__builtin_expect(scaled, 0)) {   // by powers of two
                     const uint32_t u2 = pack_f16x2(unit, unit);
 #pragma unroll
                     for (int x = 0; x < 16; ++x) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(pk[x]) : "r"(u2));
@@ -547,7 +574,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
             if constexpr (kInt8) {
                 auto half = [&](int c) {
                     uint32_t pk[32];
-                    if (__builtin_expect(unit == 1.f, 1)) {
+                    if (__builtin_expect(!scaled, 1)) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x) {
                             float x0, x1;

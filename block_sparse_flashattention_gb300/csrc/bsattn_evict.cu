@@ -92,10 +92,11 @@ __global__ void __launch_bounds__(kSelectThreads, 3) bsattn_evict_select_kernel(
     if (h == 0 && rank == 0 && tid == 0) p.lens[b] = s.m;
     const int32_t *table = p.table + (long long)b * p.table_stride;
     int32_t *kept = p.kept + ((long long)b * p.c.H + h) * p.keep;
-    const int all = rank * kSelectThreads + tid, step = ranks * kSelectThreads;
-    for (int i = s.m + all; i < p.keep; i += step) kept[i] = -1;
+    // Positions are counted without sign: a step past the last of them stays below 2^32, not below 2^31.
+    const unsigned all = rank * kSelectThreads + tid, step = ranks * kSelectThreads;
+    for (unsigned i = s.m + all; i < (unsigned)p.keep; i += step) kept[i] = -1;
     if (s.n <= p.keep) {
-        for (int i = all; i < s.m; i += step) kept[i] = i;
+        for (unsigned i = all; i < (unsigned)s.m; i += step) kept[i] = (int)i;
         return;
     }
     // the CTA's positions first .. first + n - 1
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(kSelectThreads, 3) bsattn_evict_select_kernel(
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         uint32_t *mine = hist[pass & 1];
 #pragma unroll 4
-        for (int i = tid; i < n; i += kSelectThreads) {
-            const uint32_t k = key(i);
+        for (unsigned i = tid; i < (unsigned)n; i += kSelectThreads) {
+            const uint32_t k = key((int)i);
             if (pass == 0 || ((k ^ star) >> (shift + bits)) == 0u) atomicAdd(&mine[(k >> shift) & ((1u << bits) - 1u)], 1u);
         }
         if (ranks > 1) cluster_sync();
@@ -258,11 +259,11 @@ __global__ void __launch_bounds__(kMoveThreads) bsattn_evict_move_kernel(const _
     grid_launch_dependents();
     grid_dependency_wait();
     const Evicted s = sequence(p, b, false);
-    for (int i = blockIdx.y * kRows + tid / kLanes; i < s.m; i += gridDim.y * kRows) {
+    for (unsigned i = blockIdx.y * kRows + tid / kLanes; i < (unsigned)s.m; i += gridDim.y * kRows) {
         const int from = kept[i];
         if (from < 0) continue;
         long long row, to;
-        places(p, table, out, h, from, i, row, to);
+        places(p, table, out, h, from, (int)i, row, to);
         store_row<D>(p, to, piece, load_row<D>(p, row, piece));
     }
 }
@@ -285,16 +286,16 @@ __global__ void __launch_bounds__(kCloseThreads) bsattn_evict_close_kernel(const
         if (ranks > 1) cluster_sync();
         else __syncthreads();
     };
-    for (int i0 = 0; i0 < s.m; i0 += ranks * kRows * kCloseRows) {
+    for (unsigned i0 = 0; i0 < (unsigned)s.m; i0 += ranks * kRows * kCloseRows) {
         Moved x[kCloseRows];
         long long to[kCloseRows];
         int from[kCloseRows];
-        const int i1 = i0 + rank * kRows * kCloseRows + tid / kLanes;
+        const unsigned i1 = i0 + rank * kRows * kCloseRows + tid / kLanes;
 #pragma unroll
-        for (int u = 0; u < kCloseRows; ++u) from[u] = i1 + u * kRows < s.m ? kept[i1 + u * kRows] : -1;
+        for (int u = 0; u < kCloseRows; ++u) from[u] = i1 + u * kRows < (unsigned)s.m ? kept[i1 + u * kRows] : -1;
 #pragma unroll
         for (int u = 0; u < kCloseRows; ++u) {
-            const int i = i1 + u * kRows;
+            const int i = (int)(i1 + u * kRows);
             to[u] = -1;
             if (from[u] < 0 || from[u] == i) continue;
             long long row;
@@ -306,8 +307,8 @@ __global__ void __launch_bounds__(kCloseThreads) bsattn_evict_close_kernel(const
         for (int u = 0; u < kCloseRows; ++u) store_row<D>(p, to[u], piece, x[u]);
     }
     // the places given up: their next keys' weights start at 0
-    for (int j = s.m + rank * kCloseThreads + tid; j < s.n; j += ranks * kCloseThreads) {
-        const long long row = row_at(p.c, table, h, j);
+    for (unsigned j = s.m + rank * kCloseThreads + tid; j < (unsigned)s.n; j += ranks * kCloseThreads) {
+        const long long row = row_at(p.c, table, h, (int)j);
         if (row >= 0) p.weights[row] = 0.f;
     }
 }

@@ -306,6 +306,12 @@ __global__ void __launch_bounds__(kCloseThreads) bsattn_evict_close_kernel(const
 #pragma unroll
         for (int u = 0; u < kCloseRows; ++u) store_row<D>(p, to[u], piece, x[u]);
     }
+    // Rows that do not move are the first ones (kept ascends): of each page that has any, its own first one is.
+    if (p.err) {
+        for (unsigned i = (unsigned)(rank * kCloseThreads + tid) << p.c.page_shift; i < (unsigned)s.m;
+             i += (unsigned)(ranks * kCloseThreads) << p.c.page_shift)
+            if (kept[i] == (int)i && row_at(p.c, table, h, (int)i) < 0) atomicOr(p.err, BSATTN_FLAG_BAD_INDEX);
+    }
     // the places given up: their next keys' weights start at 0
     for (unsigned j = s.m + rank * kCloseThreads + tid; j < (unsigned)s.n; j += ranks * kCloseThreads) {
         const long long row = row_at(p.c, table, h, (int)j);

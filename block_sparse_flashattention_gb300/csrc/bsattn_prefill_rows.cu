@@ -589,7 +589,10 @@ __device__ __forceinline__ void group_role(const ChunkParams &p, const Layout &w
                 }
             }
         }
+        // Either group is about to read what the other has waited for.
+        tc_fence_before();
         any_of_both(false);
+        tc_fence_after();
         // ---- output: lanes are columns of V, a warp writes 32 of them of one row at a time
         {
             const bool f32 = d.part >= 0 || p.out_f32;

@@ -322,6 +322,7 @@ bsattn_status bsattn_kv_weigh(const void *q, int64_t q_stride, const float *lse,
                                     seqlens, kind, mp, softmax_scale, err_flag, &p);
     if (st != BSATTN_OK) return st;
     if ((total > 0 && !lse) || !weights || misaligned(weights, 16)) return BSATTN_ERR_INVALID_ARG;
+    if (total == 0 && !err_flag) return BSATTN_OK;  // else the offsets are still checked
     p.lse = const_cast<float *>(lse);
     p.weights = weights;
     p.accumulate = accumulate ? 1 : 0;

@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch_role<D, kFew>(p, wait, (int)lane, base, smem);
     } else if (warp == 3) {
         // ------------------------------------------------- query blocks --
-        if (lane == 0) tma_prefetch_desc(&tq);
+        if (lane == 0 && p.total > 0) tma_prefetch_desc(&tq);   // of no rows there is no map
         const uint32_t bytes = (uint32_t)(p.G * w.tokens) * D * 2u;
         uint32_t units = 0, it = 0;
         bool ok = true;

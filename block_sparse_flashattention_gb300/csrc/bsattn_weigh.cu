@@ -123,10 +123,10 @@ __device__ __forceinline__ Range blocks_of(const ChunkParams &p, const Blocks &w
 }
 
 __device__ __forceinline__ Range unit_blocks(const ChunkParams &p, const Blocks &w, const Chunk &c, int u) {
-    return blocks_of(p, w, c, u * kUnitKeys, min((u + 1) * kUnitKeys, c.n) - 1);
+    return blocks_of(p, w, c, u * kUnitKeys, min(u * kUnitKeys, c.n - kUnitKeys) + kUnitKeys - 1);   // below 2^31
 }
 
-__device__ __forceinline__ int unit_count(const Chunk &c) { return c.m > 0 ? (c.n + kUnitKeys - 1) / kUnitKeys : 0; }
+__device__ __forceinline__ int unit_count(const Chunk &c) { return c.m > 0 && c.n > 0 ? (c.n - 1) / kUnitKeys + 1 : 0; }
 
 // Places of a unit in the line.  Of few blocks each counts, whether the unit's keys meet it or not.
 __device__ __forceinline__ bool plain_places(const Blocks &w, const Chunk &c) { return c.m <= 2 * w.tokens; }

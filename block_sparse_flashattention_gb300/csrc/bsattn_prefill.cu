@@ -57,7 +57,7 @@ constexpr int kPlanThreads = 1024, kWidenThreads = 256, kJoinThreads = 256;
 
 // Binary exponents (biased) that go into K' (what lies outside stays in r), and those that E is taken from
 // (2^(E - 6) and its inverse are then normal numbers).
-constexpr int kLeastKey = 27, kMostKey = 227, kLeastValue = 7, kMostValue = 254;
+constexpr int kLeastKey = 27, kMostKey = 227, kLeastValue = 7, kMostValue = 254, kLeastExp = (kLeastValue + 3) & ~3;
 constexpr float kLift = 7.f, kReach = 8.f;
 // Binary exponent below which O stays where another E moves it up: 2^24 tiles of 2^38 each may still be added.
 constexpr int kMostO = 100;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
             if (lane == 0) s_keep[warp] = keep;
         }
         __syncthreads();
-        const int exp = (max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3])) + 3) & ~3;
+        const int exp = (max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3])) + 3) & ~3;   // kLeastExp: maybe no value at all
         if (tid < kTile) s_v[tid] = vs * pow2(133 - exp);
         const long long at = (long long)h * w.tiles + slot;
         TileHead *head = reinterpret_cast<TileHead *>(p.ws + w.head) + at;
@@ -254,6 +254,16 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
             }
         }
         __syncthreads();
+        bool none = false;                       // no value that is not 0
+        if (exp <= kLeastExp) {
+            uint32_t some = 0;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int r = i * kRows + sub;
+                if (s_v[r] != 0.f && s_nan[r] == 0) some |= (x[1][i].x | x[1][i].y | x[1][i].z | x[1][i].w) & (kInt8 ? 0xffffffffu : 0x7f7f7f7fu);
+            }
+            none = !__syncthreads_or(some != 0u);
+        }
         if (tid < kTile) {
             const bool odd = s_nan[tid] != 0;
             head->r[tid] = ks;
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kWidenThreads) bsattn_prefill_widen_kernel(con
         if (tid == 0) {
             *reinterpret_cast<uint4 *>(head->keep) = make_uint4(s_keep[0], s_keep[1], s_keep[2], s_keep[3]);
             *reinterpret_cast<uint4 *>(head->odd) = make_uint4(s_odd[0], s_odd[1], s_odd[2], s_odd[3]);
-            head->exp = exp;
+            head->exp = none ? 0 : exp;
             head->flags = s_rest[0] | s_rest[1] | s_rest[2] | s_rest[3];
         }
 #pragma unroll
@@ -492,15 +502,15 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                 alpha = ex2_approx(m_run - m_new);
                 m_run = m_new;
             }
-            // The tile's E against that of O: a little smaller, and the weights make up for it (unit), else O moves.  Down
-            // only as far as O stays below 2^kMostO (tiles without values, whose E is the lowest, may follow one another): where
-            // that is not all the way, the tile's values are so far below what O holds that their weights' lost bits
-            // are too.
+            // The tile's E (a tile without values: O's) against that of O: a little smaller, and the weights make up for it
+            // (unit), else O moves.  Down only as far as O stays below 2^kMostO: where that is not all the way, the
+            // tile's values are so far below what O holds that their weights' lost bits are too.
+            const int exp = info.x != 0 ? info.x : exp_run;
             float f = alpha, unit = 1.f;
             bool rescale = begun && grew, scaled = false;   // the same for the whole warp
-            if (!begun) exp_run = info.x;
-            if (__builtin_expect(__any_sync(0xffffffffu, exp_run != info.x), 0)) {
-                const int below = exp_run - info.x;
+            if (!begun) exp_run = exp;
+            if (__builtin_expect(__any_sync(0xffffffffu, exp_run != exp), 0)) {
+                const int below = exp_run - exp;
                 if (__any_sync(0xffffffffu, below < 0 || below > 8)) {
                     int room = below;
                     if (__any_sync(0xffffffffu, below > 8)) {
@@ -522,9 +532,9 @@ __device__ __forceinline__ void softmax_role(const ChunkParams &p, const Layout 
                     const int shift = below > 8 ? min(below, room) : min(below, 0);
                     exp_run -= shift;
                     f *= pow2(shift);
-                    rescale = begun;
+                    rescale |= __any_sync(0xffffffffu, shift != 0);
                 }
-                unit = pow2(info.x - exp_run);
+                unit = pow2(exp - exp_run);
                 scaled = __any_sync(0xffffffffu, unit != 1.f);
             }
             const float nm = kLift - m_run;

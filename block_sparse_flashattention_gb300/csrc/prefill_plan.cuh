@@ -21,7 +21,7 @@ constexpr float kNoKey = -0x1p100f;         // reference before the first key
 // Flags of a tile: some r is not 1; some values are not numbers.
 constexpr uint32_t kRest = 1u, kOdd = 2u;
 
-// What goes with a tile: r of its keys, the keys that count, E (biased), flags, and the keys whose
+// What goes with a tile: r of its keys, the keys that count, E (biased; 0: no value), flags, and the keys whose
 // values are not numbers (NaN or infinite scales, NaN codes).  V' of those is 0, since a NaN times the
 // weight 0 of a query that does not meet the key would be NaN; a query that does is told by its mask.
 struct TileHead {

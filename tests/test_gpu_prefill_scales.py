@@ -130,3 +130,26 @@ def test_largest_scales():
         out, lse, err = _run(c, out_dtype=torch.float32)
         assert err == 0 and math.isfinite(float(lse.sum()))
         agree(out, lse, c.expect(COARSE))
+
+
+@pytest.mark.parametrize("tiny", [list(range(12)), [3, 4, 5], [0, 1, 2, 3], [9, 10, 11], [1, 3, 5, 7, 9, 11]])
+@pytest.mark.parametrize("m", [FEW, MANY])
+@pytest.mark.parametrize("dtype,D", [("e4m3", 128), ("int8", 64)])
+def test_smallest_scales(dtype, D, m, tiny):
+    """The scale of rows of zeros, 2^-126, under codes that are not 0, alone and among ordinary tiles."""
+    c = Chunks(87, dtype, 1, 1, D, 64, [12 * TILE], [m])
+    for t in tiny:
+        for j in range(t * TILE, (t + 1) * TILE):
+            c.pool.scales["v"][c.host_table[0][j // 64], :, j % 64] = 2.0 ** -126
+    c.pool.cache.v_scale.copy_(torch.from_numpy(c.pool.scales["v"]))
+    _check(c)
+
+
+def test_zero_scales_under_codes():
+    """A scale of 0 makes a value 0 whatever its code is."""
+    for dtype in ("e4m3", "int8"):
+        c = Chunks(88, dtype, 1, 2, 64, 64, [12 * TILE], [MANY])
+        for j in range(4 * TILE, 9 * TILE):
+            c.pool.scales["v"][c.host_table[0][j // 64], :, j % 64] = 0
+        c.pool.cache.v_scale.copy_(torch.from_numpy(c.pool.scales["v"]))
+        _check(c)

@@ -25,9 +25,9 @@
 // the last launch joins these parts in a fixed order.
 //
 // Measured (us a call, cold L2; of it the plan 8, widening 27 to 83, the join 13 to 48; products at 1955 TFLOP/s in
-// brackets): 2048 tokens on 63488 keys, 8 heads x 4, int8, D = 128: 1727 (1072), 1.21 PFLOP/s; 4096 tokens, window of 4096
-// behind 512 sinks, 32 heads, e4m3: 339 (158); prompts of 100 to 4096 tokens, 16 heads, e4m3, D = 64: 216 (53); 16
-// sequences with 1 to 512 new tokens, 8 heads x 4, int8: 243 (75).  Within a segment the chain of one tile's softmax
+// brackets): 2048 tokens on 63488 keys, 8 heads x 4, int8, D = 128: 1720 (1072), 1.22 PFLOP/s; 4096 tokens, window of 4096
+// behind 512 sinks, 32 heads, e4m3: 340 (158); prompts of 100 to 4096 tokens, 16 heads, e4m3, D = 64: 218 (53); 16
+// sequences with 1 to 512 new tokens, 8 heads x 4, int8: 245 (75).  Within a segment the chain of one tile's softmax
 // bounds it, 3600 cycles of which 2048 are the products'; short segments add some 10000 cycles each for their
 // description, query rows, output and the slots' unequal tiles.
 //

@@ -123,8 +123,8 @@ __device__ __forceinline__ int tile_of(const SegDesc &d, int k) { return k < d.s
 
 // The line of work of this kernel is numbered by every CTA for itself (lengths are on the device): places of
 // one head's pass over a sequence's segments.
-// Places that starting and ending a segment costs.  Drafts of 4 tokens, 8 sequences, us a call: 30.1 with 1, 29.4 with 2,
-// 29.0 with 3, 30.6 with 4, 32.2 with 8; 64 sequences of 1000 keys, 8 heads, 64 rows: 153 with 1, 150 with 2, 141 with 4.
+// Places that starting and ending a segment costs.  Drafts of 4 tokens, 8 sequences, us a call: 29.3 with 1, 28.3 with 2,
+// 28.1 with 3, 29.5 with 4; 64 sequences of 1000 keys, 8 heads, 64 rows, e4m3: 150, 148, 140, 138.
 constexpr int kRowsCost = 3;
 
 __device__ __forceinline__ int segment_tiles(const ChunkParams &p, const Layout &w, const Chunk &c, int r) {

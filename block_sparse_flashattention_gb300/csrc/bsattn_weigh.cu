@@ -9,8 +9,8 @@
 // 2^(S_r c - lse_r log2(e)), c = ks softmax_scale log2(e).  The sum is fp32 within a block of 128 rows, and
 // compensated from block to block: thousands of rows cost no more accuracy than one block does.
 //
-// Measured: 2048 tokens on 33792 keys, 8 heads, G = 4, int8, D = 128: 466 us, 1.18 PFLOP/s, where the products would take
-// 281 and the exponentials 232; 64 tokens on 61440 keys, 24 heads, e4m3: 90 us, 2.2 TB/s.  There neither more units
+// Measured: 2048 tokens on 33792 keys, 8 heads, G = 4, int8, D = 128: 469 us, 1.17 PFLOP/s, where the products would take
+// 281 and the exponentials 232; 64 tokens on 61440 keys, 24 heads, e4m3: 91 us, 2.2 TB/s.  There neither more units
 // on their way (3 instead of 2: 93 us) nor query blocks that stay from unit to unit (102, where it was 102) made a
 // difference; copies of a page instead of 16 keys did (95, 90), and fewer instructions for widening (102, 95).
 //
@@ -51,6 +51,8 @@ constexpr int kSeqChunk = 2048;             // sequences whose places fit shared
 constexpr int kUnits = 2;                   // units found ahead
 // Mean query rows of a KV head up to which bsattn_weigh_step.cu is the faster one.  32 sequences of 4096 keys, 8 heads,
 // D = 128, us a call there and here: 4 rows 44, 80, 16 rows 49, 80, 32 rows 60, 80; D = 64: 33, 62, 40, 62, 50, 62.
+// The mean says nothing of a chunk among single tokens: 127 tokens and a chunk of 400, 4096 keys each, 8 heads x 4 (mean
+// 16 rows), take 691 us there, 396 here, and 149 as two calls, each with its own kernel.
 constexpr int kStepRows = 32;
 
 // Rows of a query block: tokens of all of a KV head's query heads.

@@ -88,6 +88,9 @@ struct Layout {
 //   D = 64, 16 of 4096                   57, 122   63, 124   85, 129  124, 129  127, 131
 //   D = 64, 64 of 1000                   75, 131   88, 131  120, 133  179, 135  183, 138
 // Above 64 rows a segment's own cost counts: there, only where a CTA gets two at most.
+// The mean says nothing of a chunk among single tokens: 255 tokens and a chunk of 2048, 4096 keys each, int8 (mean 36
+// rows), take 1417 there and 2309 here, as two calls 737 + 135; 31 tokens and a chunk of 1024, 16384 keys each (mean
+// 132), 1269 here, as two calls 351 + 264.
 constexpr int kFewRows = 128, kFewSegs = 2 * kPrefillCtas;
 inline int segment_rows(int total, int B, int H, int G) {
     const long long mean = ((long long)total * G + B - 1) / B;

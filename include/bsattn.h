@@ -607,7 +607,9 @@ bsattn_status bsattn_decode_workspace_size(const bsattn_kv_cache *cache, int32_t
  * no key: out = 0, lse = -inf.  K_j, V_j are the cached values (code * scale); products with
  * codes are exact in the scores and all sums are fp32; weights are rounded to fp16 (11 bits), and so
  * are values whose scale is not a power of two (int8).  What a key contributes may count as 0 where
- * it is 2^-27 of the largest value or less.
+ * it is 2^-27 of the largest value or less (of any key of the sequence, whether the query meets it or
+ * not).  Calls of few query rows round an element of q that is below 2^-14 of its row's largest one to
+ * a multiple of 2^-24 of that one's power of two.
  *
  * q            device bf16, `total` rows of [Hq, D] contiguous elements, q_stride apart (at
  *              least Hq * D, a multiple of 8); 16-byte aligned.
@@ -653,7 +655,8 @@ bsattn_status bsattn_prefill_workspace_size(const bsattn_kv_cache *cache, int32_
  * bsattn_kv_weigh -- the attention weight that queries give to cached keys: for every sequence b,
  * KV head h and key j < seqlens[b],
  *   weights[place of j] += sum over its queries i and the query heads hq of h of exp(s_ij - lse_i),
- * where s_ij as for bsattn_prefill, over the keys that mask_mod leaves.  With the queries and lse of
+ * where s_ij as for bsattn_prefill, over the keys that mask_mod leaves (calls of few query rows: elements
+ * of q keep their bits down to 2^-29 of their row's largest).  With the queries and lse of
  * every step the sums are the keys' accumulated weights; with those of a prompt's last tokens
  * alone, what these ask for.
  *
@@ -663,7 +666,7 @@ bsattn_status bsattn_prefill_workspace_size(const bsattn_kv_cache *cache, int32_
  *              share (a common prefix) receives the sum of both where they are added, in no set
  *              order; where they are set, one of the two.  Other places are left as they were.
  * lse          device fp32 [total, Hq], as bsattn_prefill or bsattn_decode wrote it.  -inf: the
- *              query gives no weight.
+ *              query gives no weight, whatever it and the keys hold.
  * cu_seqlens   device int32 [B+1], or NULL: one query token per sequence (total == B), the newest.
  * A sequence without query tokens, or with faulty numbers (flagged as by bsattn_prefill), is left as
  * it was.  Other arguments as for bsattn_prefill.
@@ -690,7 +693,7 @@ bsattn_status bsattn_kv_weigh(const void *q, int64_t q_stride, const float *lse,
  *              page_table's rows or named twice; page_table's pages are only read.  NULL, or
  *              page_table itself: rows move within their sequence's own pages, and the weights at the
  *              positions min(n, keep) .. n - 1 become 0.  Then no page that is moved may be
- *              another sequence's too.
+ *              another sequence's too, or be named twice in its own row.
  * kept         device int32 [B, H, keep]: the positions that stay, ascending, then -1.
  * lens         device int32 [B], not seqlens itself: min(seqlens[b], keep), 0 for seqlens[b] <= 0.
  * A row read from a page outside [0, num_pages) moves as zeros; one that would go to such a page is

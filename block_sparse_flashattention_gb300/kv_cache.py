@@ -414,8 +414,9 @@ def decode_shared_prefix(q, cache: KVCache, prefix_table, prefix_len: int, page_
 
 def alloc_prefill_workspace(cache: KVCache, total: int, B: int, Hq: int, keys: int):
     """Workspace of a ``prefill`` call for up to `total` query tokens of B sequences, Hq query heads and
-    up to `keys` cached keys of all sequences together.  It can be kept from call to call; two
-    calls that may run at the same time need one each."""
+    up to `keys` cached keys of all sequences together (of fewer sequences a call may need more: pad the
+    batch with sequences of length 0, or ask again).  It can be kept from call to call; two calls that
+    may run at the same time need one each."""
     return torch.empty(bsattn_prefill_workspace_size(cache.ref, total, B, Hq, keys), dtype=torch.uint8,
                        device=cache.device)
 
